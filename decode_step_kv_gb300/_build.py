@@ -1,7 +1,7 @@
 """Build the CUDA library in-tree: decode_step_kv_gb300/_build/libfa_decode.so.
 
-One translation unit, one -gencode (sm_103a), static CUDA runtime.  Used by
-``__graft_entry__.build()`` and by the binding on first use.
+A few translation units compiled side by side, one -gencode (sm_103a), static
+CUDA runtime.  Used by ``__graft_entry__.build()`` and by the binding on first use.
 """
 from __future__ import annotations
 
@@ -11,8 +11,9 @@ import subprocess
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
-SRC = os.path.join(HERE, "csrc", "fa_decode.cu")
-HDR = os.path.join(ROOT, "include", "fa_decode.h")
+CSRC = os.path.join(HERE, "csrc")
+SRCS = [os.path.join(CSRC, f) for f in ("fa_decode.cu", "fa_int4.cu", "fa_evict.cu")]
+HDRS = [os.path.join(ROOT, "include", "fa_decode.h"), os.path.join(CSRC, "fa_common.cuh")]
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libfa_decode.so")
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
@@ -29,7 +30,7 @@ def _stale() -> bool:
     if not os.path.exists(LIB):
         return True
     t = os.path.getmtime(LIB)
-    return any(os.path.getmtime(f) > t for f in (SRC, HDR, __file__))
+    return any(os.path.getmtime(f) > t for f in (*SRCS, *HDRS, __file__))
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -37,15 +38,31 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return LIB
     os.makedirs(OUT_DIR, exist_ok=True)
     tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [nvcc(), ARCH, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",
-           "-shared", "-o", tmp, SRC]
-    if verbose:
-        cmd.insert(2, "-Xptxas=-v")
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if res.returncode != 0:
-        raise RuntimeError(f"nvcc failed ({res.returncode}):\n{res.stderr}")
-    if verbose:
-        print(res.stderr)
+    objs, running = [], []
+    for src in SRCS:
+        obj = os.path.join(OUT_DIR, os.path.basename(src) + f".{os.getpid()}.o")
+        cmd = [nvcc(), ARCH, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2", "-c",
+               "-o", obj, src]
+        if verbose:
+            cmd.insert(2, "-Xptxas=-v")
+        objs.append(obj)
+        running.append(subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.PIPE,
+                                        text=True))
+    done = [p.communicate() for p in running]
+    try:
+        for p, (_, err) in zip(running, done):
+            if p.returncode != 0:
+                raise RuntimeError(f"nvcc failed ({p.returncode}):\n{err}")
+            if verbose:
+                print(err)
+        res = subprocess.run([nvcc(), ARCH, "-shared", "-Xcompiler", "-fPIC", "-o", tmp, *objs],
+                             capture_output=True, text=True)
+        if res.returncode != 0:
+            raise RuntimeError(f"nvcc link failed ({res.returncode}):\n{res.stderr}")
+    finally:
+        for obj in objs:
+            if os.path.exists(obj):
+                os.remove(obj)
     os.replace(tmp, LIB)
     return LIB
 

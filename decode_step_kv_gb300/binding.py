@@ -83,6 +83,25 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
             lib.fa_append_kv_slots.restype = i32
             lib.fa_append_kv.argtypes = [P, P, P, P, P, P, P, i32, i32, i32, i32, i32, i32, P]
             lib.fa_append_kv.restype = i32
+            lib.fa_append_kv_int4.argtypes = [P, P, P, P, P, P, P, P, P, i32, i32, i32, i32, i32,
+                                              i32, i32, P]
+            lib.fa_append_kv_int4.restype = i32
+            lib.fa_gather_kv_int4.argtypes = [P, P, P, P, P, P, P, P, P, i32, i32, i32, i32, i32,
+                                              i32, i32, P]
+            lib.fa_gather_kv_int4.restype = i32
+            lib.fa_decode_int4.argtypes = [P, P, P, P, P, P, P, i32, i32, i32, i32, f32, P, P, P,
+                                           i32, i32, i32, i32, P, sz, P]
+            lib.fa_decode_int4.restype = i32
+            lib.fa_decode_int4_workspace_size.argtypes = [i32] * 8
+            lib.fa_decode_int4_workspace_size.restype = sz
+            lib.fa_decode_weights.argtypes = [P, P, P, P, P, P, i32, i32, i32, i32, f32, P, P, P,
+                                              i32, i32, i32, i32, P, sz, P]
+            lib.fa_decode_weights.restype = i32
+            lib.fa_decode_weights_workspace_size.argtypes = [i32] * 7
+            lib.fa_decode_weights_workspace_size.restype = sz
+            lib.fa_evict_kv.argtypes = [P, P, P, P, P, P, P, P, P, i32, i32, i32, i32, i32, i32,
+                                        i32, i32, i32, P]
+            lib.fa_evict_kv.restype = i32
             lib.fa_gather_kv_debug.argtypes = [P, i32, P, i32, i32, i32, i32, i32, i32, P, P]
             lib.fa_gather_kv_debug.restype = i32
             lib.fa_decode_device_status.argtypes = [ctypes.POINTER(ctypes.c_uint), P]
@@ -331,6 +350,191 @@ def fa_append_kv(k_new, v_new, k_cache, v_cache, v_scales, block_table, position
                              int(n_kv_heads), int(head_dim), int(page_size),
                              int(max_blocks_per_seq), int(num_blocks), _stream(stream))
     _check(rc)
+
+
+def _take(name, t, dtype, shape=None):
+    """Device pointer (None for None) of a contiguous tensor of `dtype` on the
+    current device, of `shape` where one is given."""
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} must be on the current CUDA device, got {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _cache_dims(name, k, block_table, batch):
+    """(kv heads, page_size, max_blocks_per_seq, num_blocks, row shape) of a cache
+    [num_blocks, Hkv, page, ...] (paged) or [batch, Hkv, capacity, ...]."""
+    if k.dim() != 4:
+        raise ValueError(f"{name}: caches are [blocks or batch, kv heads, page or capacity, row]")
+    if block_table is None:
+        if k.shape[0] != batch:
+            raise ValueError(f"{name}: a contiguous cache holds {k.shape[0]} sequences, "
+                             f"the call has {batch}")
+        return k.shape[1], 16, k.shape[2], 0, tuple(k.shape[:3])
+    if block_table.dim() != 2 or block_table.shape[0] != batch:
+        raise ValueError(f"{name}: block_table must be [batch, max_blocks_per_seq]")
+    return k.shape[1], k.shape[2], block_table.shape[1], k.shape[0], tuple(k.shape[:3])
+
+
+def _stream_ptr(stream):
+    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+
+
+def _bytes(workspace):
+    return 0 if workspace is None else workspace.numel() * workspace.element_size()
+
+
+def _int4_cache(name, k_codes, k_scales, v_codes, v_scales, block_table, batch):
+    """Pointers and sizes of a 4-bit cache: (pointers, table, kv heads, page,
+    max_blocks, num_blocks, rows, head_dim)."""
+    hkv, page, blocks, total, rows = _cache_dims(name, k_codes, block_table, batch)
+    half = k_codes.shape[3]
+    ptrs = (_take("k_codes", k_codes, torch.uint8),
+            _take("k_scales", k_scales, torch.float16, (*rows, half // 16)),
+            _take("v_codes", v_codes, torch.uint8, (*rows, half)),
+            _take("v_scales", v_scales, torch.float16, (*rows, half // 16)))
+    return (ptrs, _take("block_table", block_table, torch.int32), hkv, page, blocks, total, rows,
+            2 * half)
+
+
+def fa_append_kv_int4(k_new, v_new, k_codes, k_scales, v_codes, v_scales, block_table, positions,
+                      *, n_new=None, stream=None):
+    """Write rows k_new / v_new [B, T, Hkv, D] fp32 into a 4-bit cache, sequence b's
+    row i at token positions[b] + i; `n_new` [B] int32: only the first n_new[b] rows.
+
+    codes: uint8 [blocks, Hkv, page, D/2] with a block_table, or [B, Hkv, capacity, D/2];
+    scales: fp16 [..., D/32] beside them."""
+    B, T = k_new.shape[:2]
+    c, bt, hkv, page, blocks, total, _, D = _int4_cache("fa_append_kv_int4", k_codes, k_scales,
+                                                        v_codes, v_scales, block_table, B)
+    new = (B, T, hkv, D)
+    _check(load().fa_append_kv_int4(
+        _take("k_new", k_new, torch.float32, new), _take("v_new", v_new, torch.float32, new), *c,
+        bt, _take("positions", positions, torch.int32, (B,)),
+        _take("n_new", n_new, torch.int32, (B,)), B, T, hkv, D, page, blocks, total,
+        _stream_ptr(stream)))
+
+
+def fa_gather_kv_int4(k_codes, k_scales, v_codes, v_scales, block_table, positions, k_out, v_out,
+                      *, n_rows=None, stream=None):
+    """Rows positions[b] + i of a 4-bit cache as fp16 k_out / v_out [B, T, Hkv, D];
+    `n_rows` [B] int32: only the first n_rows[b] of them."""
+    B, T = k_out.shape[:2]
+    c, bt, hkv, page, blocks, total, _, D = _int4_cache("fa_gather_kv_int4", k_codes, k_scales,
+                                                        v_codes, v_scales, block_table, B)
+    to = (B, T, hkv, D)
+    _check(load().fa_gather_kv_int4(
+        *c, bt, _take("positions", positions, torch.int32, (B,)),
+        _take("n_rows", n_rows, torch.int32, (B,)), _take("k_out", k_out, torch.float16, to),
+        _take("v_out", v_out, torch.float16, to), B, T, hkv, D, page, blocks, total,
+        _stream_ptr(stream)))
+
+
+def _queries(name, q, out, n_q_heads, head_dim):
+    """(batch, queries, q pointer, out pointer) of q and out, [B, Hq, D] or [B, Tq, Hq, D]."""
+    if q.dim() not in (3, 4) or tuple(q.shape[-2:]) != (n_q_heads, head_dim):
+        raise ValueError(f"{name}: q must be [B, Hq, D] or [B, Tq, Hq, D]")
+    return (q.shape[0], 1 if q.dim() == 3 else q.shape[1], _take("q", q, torch.float16),
+            _take("out", out, torch.float16, q.shape))
+
+
+def fa_decode_int4(q, k_codes, k_scales, v_codes, v_scales, block_table, seq_lens, n_q_heads,
+                   n_kv_heads, head_dim, scale, window, out, *, acc=None, workspace=None,
+                   stream=None):
+    """Decode attention over a 4-bit cache: q, out fp16 [B, Hq, D] (one query per
+    sequence) or [B, Tq, Hq, D] (each sequence's last Tq tokens, causal).  `acc`
+    (fp32, one value per cache row) also gets every key's softmax weight added, as in
+    ``fa_decode_weights``.  The workspace is ``alloc_workspace_int4``'s."""
+    B, tq, qp, op = _queries("fa_decode_int4", q, out, n_q_heads, head_dim)
+    c, bt, hkv, page, blocks, total, rows, D = _int4_cache("fa_decode_int4", k_codes, k_scales,
+                                                           v_codes, v_scales, block_table, B)
+    if hkv != n_kv_heads or D != head_dim:
+        raise ValueError(f"fa_decode_int4: the cache holds {hkv} heads of {D}")
+    _check(load().fa_decode_int4(
+        qp, *c, bt, _take("seq_lens", seq_lens, torch.int32, (B,)), tq, n_q_heads, hkv, D, scale,
+        _take("window", window, torch.int32, (B,)), op, _take("acc", acc, torch.float32, rows), B,
+        page, blocks, total, _ptr(workspace), _bytes(workspace), _stream_ptr(stream)))
+
+
+def fa_decode_int4_workspace_size(batch, n_queries, n_q_heads, n_kv_heads, head_dim, max_kv_len,
+                                  with_weights=False, num_sms=0) -> int:
+    return int(load().fa_decode_int4_workspace_size(batch, n_queries, n_q_heads, n_kv_heads,
+                                                    head_dim, max_kv_len, int(with_weights),
+                                                    num_sms))
+
+
+def alloc_workspace_int4(batch, n_queries, n_q_heads, n_kv_heads, head_dim, max_kv_len, *,
+                         weights=False, device="cuda"):
+    """Device scratch for fa_decode_int4 (weights=True: for calls with acc too)."""
+    n = fa_decode_int4_workspace_size(batch, n_queries, n_q_heads, n_kv_heads, head_dim,
+                                      max_kv_len, weights)
+    return torch.empty(max(n, 16), dtype=torch.uint8, device=device)
+
+
+def fa_decode_weights(q, k_cache, v_cache, v_scales, block_table, seq_lens, n_q_heads, n_kv_heads,
+                      head_dim, scale, window, out, acc, *, workspace=None, stream=None):
+    """``fa_decode_multi`` (q fp16 [B, Hq, D] or [B, Tq, Hq, D]) with fp16 out, which also
+    adds every key's softmax weight, summed over the queries and the query heads of its
+    KV head, to `acc` (fp32, one value per cache row: the cache's shape without D).
+    The workspace is ``alloc_workspace_weights``'s."""
+    hkv, page, blocks, total, rows = _cache_dims("fa_decode_weights", k_cache, block_table,
+                                                 q.shape[0])
+    B, tq, qp, op = _queries("fa_decode_weights", q, out, n_q_heads, head_dim)
+    if hkv != n_kv_heads:
+        raise ValueError(f"fa_decode_weights: the cache holds {hkv} heads")
+    row = (*rows, head_dim)
+    _check(load().fa_decode_weights(
+        qp, _take("k_cache", k_cache, torch.float16, row),
+        _take("v_cache", v_cache, torch.float16 if v_scales is None else torch.int8, row),
+        _take("v_scales", v_scales, torch.float16, (*rows, head_dim // 32)),
+        _take("block_table", block_table, torch.int32),
+        _take("seq_lens", seq_lens, torch.int32, (B,)), tq, n_q_heads, hkv, head_dim, scale,
+        _take("window", window, torch.int32, (B,)), op, _take("acc", acc, torch.float32, rows), B,
+        page, blocks, total, _ptr(workspace), _bytes(workspace), _stream_ptr(stream)))
+
+
+def fa_decode_weights_workspace_size(batch, n_queries, n_q_heads, n_kv_heads, head_dim, max_kv_len,
+                                     num_sms=0) -> int:
+    return int(load().fa_decode_weights_workspace_size(batch, n_queries, n_q_heads, n_kv_heads,
+                                                       head_dim, max_kv_len, num_sms))
+
+
+def alloc_workspace_weights(batch, n_queries, n_q_heads, n_kv_heads, head_dim, max_kv_len, *,
+                            device="cuda"):
+    """Device scratch for fa_decode_weights."""
+    n = fa_decode_weights_workspace_size(batch, n_queries, n_q_heads, n_kv_heads, head_dim,
+                                         max_kv_len)
+    return torch.empty(max(n, 16), dtype=torch.uint8, device=device)
+
+
+def fa_evict_kv(k_cache, v_cache, acc, block_table, seq_lens, new_lens, *, budget, n_sink,
+                n_recent, kept, k_scales=None, v_scales=None, stream=None):
+    """Cut every sequence to `budget` tokens per KV head, in place: the first n_sink, the
+    last n_recent, and the largest `acc` totals between them (ties: lowest index), moved in
+    order to the front.  fp16 caches; with v_scales, int8 V; with both scales, 4-bit K and V
+    (uint8 codes).  Writes new_lens [B] and kept [B, Hkv, budget] (int32)."""
+    B = seq_lens.shape[0]
+    hkv, page, blocks, total, rows = _cache_dims("fa_evict_kv", k_cache, block_table, B)
+    int4 = k_scales is not None
+    D = k_cache.shape[3] * (2 if int4 else 1)
+    scales = (*rows, D // 32)
+    _check(load().fa_evict_kv(
+        _take("k_cache", k_cache, torch.uint8 if int4 else torch.float16),
+        _take("v_cache", v_cache, torch.uint8 if int4 else torch.float16 if v_scales is None
+              else torch.int8, k_cache.shape),
+        _take("k_scales", k_scales, torch.float16, scales),
+        _take("v_scales", v_scales, torch.float16, scales),
+        _take("acc", acc, torch.float32, rows), _take("block_table", block_table, torch.int32),
+        _take("seq_lens", seq_lens, torch.int32), _take("new_lens", new_lens, torch.int32, (B,)),
+        _take("kept", kept, torch.int32, (B, hkv, budget)), budget, n_sink, n_recent, B, hkv, D,
+        page, blocks, total, _stream_ptr(stream)))
 
 
 def fa_gather_kv_debug(cache, row_bytes, block_table, b, n_kv_heads, page_size,

@@ -1,0 +1,437 @@
+// fa_evict.cu -- eviction from a KV cache by accumulated attention weight, for
+// sm_103a (GB300).
+//
+// For every sequence longer than the budget and each of its KV heads: keep the
+// first n_sink tokens, the last n_recent, and of the tokens between them the
+// ones with the largest running totals; move the kept rows, in order, to the
+// front of the cache.
+//
+// One thread-block cluster per (sequence, KV head) does both parts in one
+// launch.
+//   Selection: a radix selection of the k-th largest total (11 + 11 + 10 bits
+//   of the order-preserving integer), each CTA counting its share of the
+//   tokens, the counts summed through distributed shared memory; then every
+//   warp emits its tokens' kept indices at the rank that the warps before it
+//   leave.  Ties go to the lowest index.
+//   Move: rows go down in place (a kept row's new index is never above its
+//   old one).  The cluster works in rounds of consecutive kept rows: every CTA
+//   reads its rows into shared memory, a cluster barrier, every CTA writes
+//   them.  The rows that round q overwrites lie below the sources of all later
+//   rounds, so a round's reads need not wait for the writes before it.
+// Bound by HBM: each kept row that changes its place is read and written once.
+#include "fa_common.cuh"
+
+namespace fa {
+namespace ev {
+
+constexpr int THREADS = 512;
+constexpr int WARPS = THREADS / 32;
+constexpr int BINS = 2048;
+constexpr int MAX_CTAS = 8;              // CTAs per cluster
+constexpr int STAGE_BYTES = 96 * 1024;   // rows in flight per CTA: two CTAs per SM
+
+struct Args {
+    char *a[4];          // K, V, K scales, V scales (NULL: none)
+    int row_bytes[4];    // powers of two from 8
+    float *acc;
+    int *new_lens, *kept;
+    int budget, sink, recent;
+    int rows;            // rows staged per CTA and round
+};
+
+// Totals as integers in the same order: NaN counts as -inf, -0 as 0.
+__device__ __forceinline__ unsigned order_key(float x)
+{
+    unsigned b = __float_as_uint(x);
+    if (x != x)
+        b = 0xff800000u;
+    else if (x == 0.f)
+        b = 0u;
+    return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+
+__device__ __forceinline__ long long row_of(const Params &p, int b, int kv, int t)
+{
+    const long long r = tc::tile_row(p, b, kv, t - t % tc::TILE);
+    return r < 0 ? -1 : r + t % tc::TILE;
+}
+
+__device__ __forceinline__ unsigned ld_cluster(uint32_t a)
+{
+    unsigned v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    return v;
+}
+
+template <int N>
+__device__ __forceinline__ void cp(uint32_t dst, const void *src)
+{
+    if constexpr (N == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+
+__global__ void __launch_bounds__(THREADS, 2) evict_kernel(const Params p, const Args x)
+{
+    __shared__ unsigned hist[BINS];
+    __shared__ unsigned cnt[WARPS][2];
+    __shared__ unsigned wsum[WARPS];
+    __shared__ unsigned found[2];
+    extern __shared__ __align__(128) unsigned char stage[];
+
+    const int cs = p.cl_ctas;
+    uint32_t rank = 0;
+    if (cs > 1)
+        asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+    const int unit = blockIdx.x / cs;
+    const int b = unit / p.Hkv, kv = unit % p.Hkv;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    auto sync_all = [&] {
+        if (cs > 1)
+            tc::cluster_sync();
+        else
+            __syncthreads();
+    };
+
+    int lo, n;
+    attended_range(p, b, lo, n, kv == 0 && rank == 0 && tid == 0);
+    int *kept = x.kept + (long long)unit * x.budget;
+    if (kv == 0 && rank == 0 && tid == 0)
+        x.new_lens[b] = min(n, x.budget);
+    if (n <= x.budget) {
+        for (int j = rank * THREADS + tid; j < x.budget; j += cs * THREADS)
+            kept[j] = j < n ? j : -1;
+        return;                                   // the whole cluster
+    }
+
+    // ---- the k-th largest total of the m tokens between sink and recent
+    const int m = n - x.sink - x.recent;
+    const int k = x.budget - x.sink - x.recent;
+    const int gw = rank * WARPS + warp, nw = cs * WARPS;
+    const int w0 = x.sink + static_cast<int>((long long)m * gw / nw);
+    const int w1 = x.sink + static_cast<int>((long long)m * (gw + 1) / nw);
+    auto key_at = [&](int t) -> unsigned {
+        const long long r = row_of(p, b, kv, t);
+        if (r < 0) {
+            flag(FA_STATUS_BAD_BLOCK);
+            return order_key(-INFINITY);
+        }
+        return order_key(__ldcg(x.acc + r));
+    };
+    unsigned thr = 0xffffffffu;                   // keys above thr are kept ...
+    unsigned rem = 0;                             // ... and the first rem equal to it
+    if (k > 0) {
+        thr = 0;
+        rem = k;
+        for (int pass = 0; pass < 3; ++pass) {
+            const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+            const int bits = pass == 2 ? 10 : 11;
+            for (int i = tid; i < BINS; i += THREADS)
+                hist[i] = 0;
+            __syncthreads();
+            for (int t = w0 + lane; t < w1; t += 32) {
+                const unsigned u = key_at(t);
+                if (pass == 0 || ((u ^ thr) >> (shift + bits)) == 0)
+                    atomicAdd(&hist[(u >> shift) & ((1u << bits) - 1)], 1u);
+            }
+            sync_all();
+            constexpr int PER = BINS / THREADS;
+            unsigned c[PER], sum = 0;             // this thread's bins, from the top
+#pragma unroll
+            for (int q = 0; q < PER; ++q) {
+                const int bin = BINS - 1 - (tid * PER + q);
+                c[q] = hist[bin];
+                if (cs > 1) {
+                    const uint32_t a = smem_u32(&hist[bin]);
+                    c[q] = 0;
+                    for (int r = 0; r < cs; ++r)
+                        c[q] += ld_cluster(tc::cl_map(a, r));
+                }
+                sum += c[q];
+            }
+            unsigned incl = sum;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const unsigned y = __shfl_up_sync(0xffffffffu, incl, off);
+                if (lane >= off)
+                    incl += y;
+            }
+            if (lane == 31)
+                wsum[warp] = incl;
+            __syncthreads();
+            unsigned above = incl - sum;
+            for (int i = 0; i < warp; ++i)
+                above += wsum[i];
+#pragma unroll
+            for (int q = 0; q < PER; ++q) {
+                if (above < rem && rem <= above + c[q]) {
+                    found[0] = BINS - 1 - (tid * PER + q);
+                    found[1] = above;
+                }
+                above += c[q];
+            }
+            sync_all();                           // counts read by all before they are cleared
+            thr |= found[0] << shift;
+            rem -= found[1];
+        }
+    }
+    // ---- ranks: what the warps before this one keep
+    unsigned n_gt = 0, n_eq = 0;
+    for (int t0 = w0; t0 < w1; t0 += 32) {
+        const int t = t0 + lane;
+        const unsigned u = t < w1 ? key_at(t) : 0u;
+        n_gt += __popc(__ballot_sync(0xffffffffu, t < w1 && u > thr));
+        n_eq += __popc(__ballot_sync(0xffffffffu, t < w1 && u == thr));
+    }
+    if (lane == 0) {
+        cnt[warp][0] = n_gt;
+        cnt[warp][1] = n_eq;
+    }
+    sync_all();
+    unsigned gt = 0, eq = 0;
+    for (int i = lane; i < gw; i += 32) {
+        const uint32_t a = smem_u32(&cnt[i % WARPS][0]);
+        const uint32_t at = cs > 1 ? tc::cl_map(a, i / WARPS) : a;
+        gt += ld_cluster(at);
+        eq += ld_cluster(at + 4);
+    }
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) {
+        gt += __shfl_xor_sync(0xffffffffu, gt, off);
+        eq += __shfl_xor_sync(0xffffffffu, eq, off);
+    }
+    unsigned at = x.sink + gt + min(eq, rem);
+    for (int t0 = w0; t0 < w1; t0 += 32) {
+        const int t = t0 + lane;
+        const unsigned u = t < w1 ? key_at(t) : 0u;
+        const unsigned eqm = __ballot_sync(0xffffffffu, t < w1 && u == thr);
+        const unsigned below = (1u << lane) - 1u;
+        const bool keep = t < w1 && (u > thr || (u == thr && eq + __popc(eqm & below) < rem));
+        const unsigned km = __ballot_sync(0xffffffffu, keep);
+        const unsigned to = at + __popc(km & below);
+        if (keep && to < static_cast<unsigned>(x.budget))
+            kept[to] = t;
+        at += __popc(km);
+        eq += __popc(eqm);
+    }
+    for (int j = rank * THREADS + tid; j < x.sink; j += cs * THREADS)
+        kept[j] = j;
+    for (int j = rank * THREADS + tid; j < x.recent; j += cs * THREADS)
+        kept[x.budget - x.recent + j] = n - x.recent + j;
+    sync_all();                                   // kept[] is complete
+
+    // ---- move, in rounds of cs * rows kept rows
+    const int R = x.rows;
+    for (int j0 = x.sink; j0 < x.budget; j0 += cs * R) {
+        const int r0 = j0 + rank * R;
+        const int nr = min(R, x.budget - r0);     // <= 0 for the last CTAs of the last round
+        uint32_t off = smem_u32(stage);
+        float av[4];                              // R <= 4 * THREADS
+#pragma unroll
+        for (int a = 0; a < 4; ++a) {
+            if (!x.a[a])
+                continue;
+            const int rb = x.row_bytes[a];
+            const int lg = 31 - __clz(rb >= 16 ? rb / 16 : 1);
+            for (int i = tid; i < (nr > 0 ? nr << lg : 0); i += THREADS) {
+                const int j = r0 + (i >> lg), c = i & ((1 << lg) - 1);
+                const int t = __ldcg(kept + j);
+                const long long src = t == j ? -1 : row_of(p, b, kv, t);
+                if (src < 0)
+                    continue;
+                if (rb >= 16)
+                    cp<16>(off + i * 16, x.a[a] + src * rb + c * 16);
+                else
+                    cp<8>(off + i * 8, x.a[a] + src * rb);
+            }
+            off += R * rb;
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int i = tid + q * THREADS;
+            av[q] = 0.f;
+            if (i < nr) {
+                const long long src = row_of(p, b, kv, __ldcg(kept + r0 + i));
+                if (src >= 0)
+                    av[q] = __ldcg(x.acc + src);
+            }
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        sync_all();                               // every read of the round is done
+        off = 0;
+#pragma unroll
+        for (int a = 0; a < 4; ++a) {
+            if (!x.a[a])
+                continue;
+            const int rb = x.row_bytes[a];
+            const int lg = 31 - __clz(rb >= 16 ? rb / 16 : 1);
+            for (int i = tid; i < (nr > 0 ? nr << lg : 0); i += THREADS) {
+                const int j = r0 + (i >> lg), c = i & ((1 << lg) - 1);
+                const int t = __ldcg(kept + j);
+                if (t == j || row_of(p, b, kv, t) < 0)
+                    continue;
+                const long long dst = row_of(p, b, kv, j);
+                if (dst < 0)
+                    continue;
+                if (rb >= 16)
+                    *reinterpret_cast<uint4 *>(x.a[a] + dst * rb + c * 16) =
+                        *reinterpret_cast<const uint4 *>(stage + off + i * 16);
+                else
+                    *reinterpret_cast<uint2 *>(x.a[a] + dst * rb) =
+                        *reinterpret_cast<const uint2 *>(stage + off + i * 8);
+            }
+            off += R * rb;
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int i = tid + q * THREADS;
+            if (i < nr) {
+                const long long dst = row_of(p, b, kv, r0 + i);
+                if (dst >= 0)
+                    x.acc[dst] = av[q];
+            }
+        }
+        __syncthreads();                          // the stage is free again
+    }
+    // the totals of the rows behind the budget start again from zero
+    for (int t = x.budget + rank * THREADS + tid; t < n; t += cs * THREADS) {
+        const long long r = row_of(p, b, kv, t);
+        if (r >= 0)
+            x.acc[r] = 0.f;
+    }
+}
+
+}  // namespace ev
+
+cudaError_t evict_take_status(unsigned int *v, cudaStream_t st)
+{
+    return take_status(v, st);
+}
+
+}  // namespace fa
+
+using namespace fa;
+
+extern "C" FA_API int fa_evict_kv(void *k_cache, void *v_cache, void *k_scales, void *v_scales,
+                                  float *acc, const int32_t *block_table,
+                                  const int32_t *seq_lens, int32_t *new_lens, int32_t *kept,
+                                  int budget, int n_sink, int n_recent, int batch,
+                                  int n_kv_heads, int head_dim, int page_size,
+                                  int max_blocks_per_seq, int num_blocks, void *stream)
+{
+    const char *name = "fa_evict_kv";
+    g_err[0] = 0;
+    if (!k_cache || !v_cache || !acc || !seq_lens || !new_lens || !kept)
+        return fail(FA_ERR_NULL, "%s: only block_table and the scales may be NULL", name);
+    if (k_scales && !v_scales)
+        return fail(FA_ERR_NULL, "%s: k_scales (a 4-bit cache) without v_scales", name);
+    if (head_dim != 128 && head_dim != 256)
+        return fail(FA_ERR_HEAD_DIM, "%s: head_dim %d not supported (128 or 256)", name, head_dim);
+    if (n_kv_heads <= 0 || n_kv_heads > 4096)
+        return fail(FA_ERR_HEADS, "%s: n_kv_heads %d", name, n_kv_heads);
+    const bool paged = block_table != nullptr;
+    if (batch < 0 || batch > 65535 || max_blocks_per_seq <= 0 ||
+        (paged && (page_size <= 0 || page_size % 16 || num_blocks <= 0)))
+        return fail(FA_ERR_LAYOUT, "%s: bad batch, capacity, page size or block count", name);
+    const long long cap = paged ? (long long)max_blocks_per_seq * page_size
+                                : (long long)max_blocks_per_seq;
+    if (cap > (1ll << 30))
+        return fail(FA_ERR_LAYOUT, "%s: capacity %lld tokens too large", name, cap);
+    if (budget <= 0 || n_sink < 0 || n_recent < 0 || (long long)n_sink + n_recent > budget)
+        return fail(FA_ERR_LAYOUT, "%s: budget %d must be positive and hold n_sink %d and "
+                                   "n_recent %d", name, budget, n_sink, n_recent);
+    if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned16(k_scales) ||
+        !aligned16(v_scales) || !aligned_to(acc, 4) || !aligned_to(seq_lens, 4) ||
+        !aligned_to(new_lens, 4) || !aligned_to(kept, 4) || !aligned_to(block_table, 4))
+        return fail(FA_ERR_ALIGN, "%s: caches and scales must be 16-byte aligned, acc and int32 "
+                                  "arrays 4-byte aligned", name);
+    const size_t kv_rows = (paged ? (size_t)num_blocks * page_size : (size_t)batch * cap) *
+                           n_kv_heads;
+    const int D = head_dim;
+    ev::Args x = {};
+    x.a[0] = static_cast<char *>(k_cache);
+    x.a[1] = static_cast<char *>(v_cache);
+    x.a[2] = static_cast<char *>(k_scales);
+    x.a[3] = static_cast<char *>(v_scales);
+    x.row_bytes[0] = k_scales ? D / 2 : 2 * D;
+    x.row_bytes[1] = k_scales ? D / 2 : v_scales ? D : 2 * D;
+    x.row_bytes[2] = x.row_bytes[3] = D / 16;
+    x.acc = acc;
+    x.new_lens = new_lens;
+    x.kept = kept;
+    x.budget = budget;
+    x.sink = n_sink;
+    x.recent = n_recent;
+    const struct { const void *p; size_t n; } io[] = {
+        {x.a[0], kv_rows * x.row_bytes[0]}, {x.a[1], kv_rows * x.row_bytes[1]},
+        {x.a[2], kv_rows * x.row_bytes[2]}, {x.a[3], kv_rows * x.row_bytes[3]},
+        {acc, kv_rows * 4}, {new_lens, (size_t)batch * 4},
+        {kept, (size_t)batch * n_kv_heads * budget * 4},
+        {seq_lens, (size_t)batch * 4}, {block_table, (size_t)batch * max_blocks_per_seq * 4}};
+    for (int i = 0; i < 9; ++i)
+        for (int j = 0; j < i && j < 7; ++j)
+            if (overlaps(io[i].p, io[i].n, io[j].p, io[j].n))
+                return fail(FA_ERR_ALIAS, "%s: two arrays overlap", name);
+    if (batch == 0)
+        return 0;
+    int sms = 0;
+    if (const int rc = device_sms(&sms))
+        return rc;
+    int total = 0;
+    for (int a = 0; a < 4; ++a)
+        total += x.a[a] ? x.row_bytes[a] : 0;
+    x.rows = ev::STAGE_BYTES / total / 16 * 16;
+    if (x.rows > 4 * ev::THREADS)
+        x.rows = 4 * ev::THREADS;
+    Params p = {};
+    p.bt = block_table;
+    p.seq_lens = seq_lens;
+    p.B = batch;
+    p.Hkv = n_kv_heads;
+    p.page_size = paged ? page_size : 16;
+    p.max_blocks = max_blocks_per_seq;
+    p.num_blocks = num_blocks;
+    p.cap = cap;
+    // the largest cluster that still leaves every unit resident (two CTAs per SM)
+    const long long units = (long long)batch * n_kv_heads;
+    int cs = ev::MAX_CTAS;
+    while (cs > 1 && units * cs > 2ll * sms)
+        cs /= 2;
+    p.cl_ctas = cs;
+    if (units * cs > 0x7fffffffll)
+        return fail(FA_ERR_LAYOUT, "%s: too many rows", name);
+    static std::mutex mu;
+    static bool done[64] = {false};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) {
+        std::lock_guard<std::mutex> lock(mu);
+        if (dev >= 64 || !done[dev]) {
+            e = cudaFuncSetAttribute(ev::evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     ev::STAGE_BYTES);
+            if (e == cudaSuccess && dev < 64)
+                done[dev] = true;
+        }
+    }
+    if (e == cudaSuccess) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(static_cast<unsigned>(units * cs));
+        cfg.blockDim = dim3(ev::THREADS);
+        cfg.dynamicSmemBytes = ev::STAGE_BYTES;
+        cfg.stream = static_cast<cudaStream_t>(stream);
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = cs;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        e = cudaLaunchKernelEx(&cfg, ev::evict_kernel, p, x);
+        if (e == cudaSuccess)
+            e = cudaGetLastError();
+    }
+    if (e != cudaSuccess)
+        return fail(FA_ERR_CUDA, "%s: launch failed: %s", name, cudaGetErrorString(e));
+    return 0;
+}

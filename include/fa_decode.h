@@ -350,6 +350,160 @@ FA_API int fa_append_kv_slots(const float *k_new, const float *v_new, void *k_ca
                               int n_slots, int capacity, int ring, void *stream);
 
 /*
+ * The 4-bit KV cache (both K and V in 4 bits).  A row of head_dim elements is
+ * cut into blocks of 32; block j holds
+ *     s_j = the exact max|x| / 7 rounded to fp16 (nearest even; max|x| is cut
+ *           off at 7 * 65504, so a scale is always finite),
+ *     c   = clamp(round-half-even(x / s_j), -7, 7) of the exact quotient,
+ *           0 when s_j = 0; a NaN counts as 0,
+ * and stands for c * s_j.  Two arrays per cache:
+ *   codes   head_dim / 2 bytes per row.  A row is head_dim / 8 little-endian
+ *           32-bit words of 8 consecutive elements: word o * (head_dim / 32) + j
+ *           (octet o = 0..3 of block j) holds elements 32 j + 8 o + n, n = 0..7,
+ *           as the nibble c + 8 in bits 4 n .. 4 n + 3.
+ *   scales  fp16 [..row..][head_dim / 32].
+ * Rows lie as in fa_decode: paged [num_blocks][n_kv_heads][page_size], or
+ * contiguous [batch][n_kv_heads][capacity] with capacity a multiple of 16.
+ * head_dim is 128 or 256.  Codes and scales are 16-byte aligned.
+ *
+ * fa_append_kv_int4 -- write n_tokens new rows per sequence (one for a decode
+ * step, a chunk for a prompt) into the cache.
+ *
+ * k_new, v_new [batch][n_tokens][n_kv_heads][head_dim] fp32, 16-byte aligned.
+ * positions    int32 [batch] (device): the token index of each sequence's
+ *              first new row; row i goes to positions[b] + i.
+ * n_new        int32 [batch] (device) or NULL: how many of sequence b's
+ *              n_tokens rows are real (a padded batch); the others are not
+ *              stored.  NULL: all of them.
+ * A row whose token lies outside [0, capacity) (every row, when positions[b]
+ * is negative) is not stored and sets FA_STATUS_POS_RANGE; one whose block id
+ * is outside [0, num_blocks) is not stored and sets FA_STATUS_BAD_BLOCK.  No
+ * other byte of the cache changes.  Two rows of one call that name the same
+ * cache row race.  Cache arrays must not overlap each other or the inputs
+ * (FA_ERR_ALIAS).  n_tokens = 0 or batch = 0 is a no-op.
+ */
+FA_API int fa_append_kv_int4(const float *k_new, const float *v_new, void *k_codes,
+                             void *k_scales, void *v_codes, void *v_scales,
+                             const int32_t *block_table, const int32_t *positions,
+                             const int32_t *n_new, int batch, int n_tokens, int n_kv_heads,
+                             int head_dim, int page_size, int max_blocks_per_seq, int num_blocks,
+                             void *stream);
+
+/*
+ * fa_gather_kv_int4 -- the inverse of fa_append_kv_int4: rows positions[b] + i
+ * of the cache as fp16 values (c * s, rounded once), for example the cached
+ * prefix that a prompt's next chunk attends.
+ *
+ * k_out, v_out [batch][n_tokens][n_kv_heads][head_dim] fp16, 16-byte aligned;
+ * they must overlap neither an input nor each other.
+ * n_rows       int32 [batch] (device) or NULL: rows i >= n_rows[b] of the
+ *              output are left as they were.
+ * A row outside the cache, or in an unmapped block, reads as zeros and sets
+ * FA_STATUS_POS_RANGE or FA_STATUS_BAD_BLOCK.
+ */
+FA_API int fa_gather_kv_int4(const void *k_codes, const void *k_scales, const void *v_codes,
+                             const void *v_scales, const int32_t *block_table,
+                             const int32_t *positions, const int32_t *n_rows, void *k_out,
+                             void *v_out, int batch, int n_tokens, int n_kv_heads, int head_dim,
+                             int page_size, int max_blocks_per_seq, int num_blocks, void *stream);
+
+/*
+ * fa_decode_int4 -- decode attention over a 4-bit cache: fa_decode_multi's
+ * rule (n_queries in [1, 256]; 1 is the plain decode step) with K and V the
+ * values that the codes stand for.
+ *
+ * q    [batch][n_queries][n_q_heads][head_dim] fp16.
+ * out  [batch][n_queries][n_q_heads][head_dim] fp16 (fp32 accumulation, one
+ *      rounding), written in full, zero rows for empty ranges.
+ * acc  NULL, or the running totals of fa_decode_weights, to which this call
+ *      adds.
+ * workspace  fa_decode_int4_workspace_size() bytes, 16-byte aligned; contents
+ *      need no initialisation.
+ * Other arguments, device-side status bits, errors, streams and graph capture
+ * as fa_decode.  out, acc, the workspace and the inputs must not overlap.
+ */
+FA_API int fa_decode_int4(const void *q, const void *k_codes, const void *k_scales,
+                          const void *v_codes, const void *v_scales, const int32_t *block_table,
+                          const int32_t *seq_lens, int n_queries, int n_q_heads, int n_kv_heads,
+                          int head_dim, float scale, const int32_t *window, void *out, float *acc,
+                          int batch, int page_size, int max_blocks_per_seq, int num_blocks,
+                          void *workspace, size_t workspace_bytes, void *stream);
+
+/* Scratch bytes for fa_decode_int4, with (with_weights != 0) or without acc.
+ * Host-only; 0 for invalid sizes and for sizes beyond a size_t. */
+FA_API size_t fa_decode_int4_workspace_size(int batch, int n_queries, int n_q_heads,
+                                            int n_kv_heads, int head_dim, int max_kv_len,
+                                            int with_weights, int num_sms);
+
+/*
+ * fa_decode_weights -- fa_decode_multi (n_queries in [1, 256]) that also adds
+ * every key's softmax weight to a running total, the score that fa_evict_kv
+ * keeps tokens by:
+ *
+ *     acc[b][kv][t] += sum over the queries j and the query heads h of KV head
+ *                      kv of softmax weight p[b][j][h][t].
+ *
+ * acc  fp32, one value per cache row, laid out as the cache without its
+ *      head_dim: [num_blocks][n_kv_heads][page_size], or
+ *      [batch][n_kv_heads][capacity].  Rows of keys that no query attends are
+ *      left as they were.  A row starts from 0 when its token is appended:
+ *      the caller clears acc with the pages it hands out (fa_evict_kv clears
+ *      the rows it frees).  Sequences that share a block add to the same rows
+ *      (in no fixed order; rows of one sequence's own get one addition per
+ *      call, so their totals do not depend on timing).
+ * out  fp16 (as fa_decode_int4), not fp32.
+ * workspace  fa_decode_weights_workspace_size() bytes: the split's partials
+ *      and one fp32 score per key and (query, head).
+ * Caches (fp16 K; fp16 or int8 V), other arguments and errors as
+ * fa_decode_multi; acc is 4-byte aligned and overlaps no other array.
+ */
+FA_API int fa_decode_weights(const void *q, const void *k_cache, const void *v_cache,
+                             const void *v_scales, const int32_t *block_table,
+                             const int32_t *seq_lens, int n_queries, int n_q_heads,
+                             int n_kv_heads, int head_dim, float scale, const int32_t *window,
+                             void *out, float *acc, int batch, int page_size,
+                             int max_blocks_per_seq, int num_blocks, void *workspace,
+                             size_t workspace_bytes, void *stream);
+
+/* Scratch bytes for fa_decode_weights (either V type).  Host-only; 0 for
+ * invalid sizes and for sizes beyond a size_t. */
+FA_API size_t fa_decode_weights_workspace_size(int batch, int n_queries, int n_q_heads,
+                                               int n_kv_heads, int head_dim, int max_kv_len,
+                                               int num_sms);
+
+/*
+ * fa_evict_kv -- cut every sequence's cache to `budget` tokens per KV head by
+ * the running totals of fa_decode_weights.
+ *
+ * For a sequence with L_b = seq_lens[b] > budget, each KV head by itself keeps
+ * its first n_sink tokens, its last n_recent, and of the tokens between them
+ * the budget - n_sink - n_recent with the largest totals (ties: the lowest
+ * index; a NaN counts as -infinity).  The kept rows of K, V, the scales and
+ * acc move, in order, to rows 0 .. budget - 1, in place; acc rows budget ..
+ * L_b - 1 become 0; cache rows from budget on are left as they were (with
+ * paged caches their blocks are free again).  K keeps whatever position
+ * encoding its rows were written with.  Shorter sequences do not change.
+ *
+ * k_scales, v_scales  both NULL: fp16 K and V; v_scales alone: fp16 K, int8 V;
+ *            both: the 4-bit cache.
+ * new_lens   int32 [batch]: min(L_b, budget), the lengths to decode with next.
+ * kept       int32 [batch][n_kv_heads][budget]: the old index of every kept
+ *            row; j itself (and -1 from L_b on) for a sequence left alone.
+ * budget > 0; n_sink, n_recent >= 0; n_sink + n_recent <= budget
+ * (else FA_ERR_LAYOUT).  head_dim 128 or 256.
+ * Lengths outside [0, capacity] are clamped and set FA_STATUS_LEN_CLAMPED; a
+ * token in an unmapped block counts as -infinity and is not moved
+ * (FA_STATUS_BAD_BLOCK).  Blocks must not be shared between sequences.  No
+ * two of the arrays may overlap (new_lens is not seq_lens).  All work is one
+ * launch on `stream`, with no workspace.
+ */
+FA_API int fa_evict_kv(void *k_cache, void *v_cache, void *k_scales, void *v_scales, float *acc,
+                       const int32_t *block_table, const int32_t *seq_lens, int32_t *new_lens,
+                       int32_t *kept, int budget, int n_sink, int n_recent, int batch,
+                       int n_kv_heads, int head_dim, int page_size, int max_blocks_per_seq,
+                       int num_blocks, void *stream);
+
+/*
  * fa_gather_kv_debug -- copy sequence b's first n_tokens cache rows, through
  * the same page-address path fa_decode's loader uses, into dense
  * [n_kv_heads][n_tokens][row_bytes] (device).  row_bytes = 2*head_dim for K
