@@ -164,37 +164,50 @@ __global__ void __launch_bounds__(256) gather_kernel(const Params p, const unsig
 // Per 16-key tile and per warp, as in the fp16 kernel,
 //   S[16 keys x 8 columns] = K . Q^T,   O^T[D x 8] += V^T . P^T
 // on mma.sync m16n8k16, with the codes going from shared memory straight into
-// the A fragments: no dequantised tile is ever written.
-//   K: fp16 bits 0x000u and 0x00u0 are the subnormals u 2^-24 and u 2^-20, so
-//      an AND makes two codes into a half2 (the queries of odd elements are
-//      held divided by 16).  The codes' offset of 8 is folded into the
-//      accumulator's first value, -8 sum(q) per block, and each block's sum is
-//      multiplied by the key's scale in fp32.
+// the A fragments: no dequantised tile is ever written.  The fp16 bits 0x000u
+// and 0x00u0 are the subnormals u 2^-24 and u 2^-20, so an AND makes two codes
+// into a half2.
+//   K: the queries of odd elements are held divided by 16, and each block's sum
+//      is multiplied by the key's scale in fp32.  The codes' offset of 8 adds
+//      -8 sum_j s_j sum(q_j) to a score: one tf32 mma per tile, scales by
+//      block sums (in two tf32 parts, 21 bits).
 //   V: the pair of a half2 runs over two keys (the contraction), so the words
-//      of two keys are interleaved by a byte permute; the offset is taken off
-//      exactly in fp16 (1024 + u - 1032, 64 + u - 72), because left in the sum
-//      it would be hundreds of times the result.  A key's scale multiplies its
-//      weight instead of its 32 codes: P s_j is the B operand of block j.
+//      of two keys are interleaved by a byte permute; the accumulators of odd
+//      elements hold 2^-20, the even ones 2^-24.  The offset is taken off tile
+//      by tile with a second mma whose A fragment is the constant -8: 8 more of
+//      them per tile instead of 32 fp16 subtractions, and never hundreds
+//      of times the result in the accumulator, as one correction at the end
+//      would have.  A key's scale multiplies its weight instead of its 32
+//      codes: P s_j is the B operand of block j.
 // P and P s are rounded to fp16 (2^-11 each); everything else is fp32.
 // The running maximum moves only when a score passes it by 8 (log2 units), so
 // weights reach 2^8 and most tiles need no shuffles.  V scales outside
 // [2^-12, 2^7] are carried times 2^-e, a power of two per warp, so that P s
 // stays within fp16 whatever the scales.
-//
-// HBM-bound in bytes (144 B per key and KV head at D = 128, against 512 in
-// fp16) but close to the issue rate: ~280 instructions per tile, and the copy
-// rate leaves a warp scheduler ~390 cycles for it.
-#ifndef FA_I4_NW
-#define FA_I4_NW 4
+// Tiles are copied in batches of up to BT of one unit (cp.async, a ring of
+// batches per warp): the lanes look 32 tiles' cache rows up side by side, so a
+// tile's share of the addressing is a shuffle and three multiply-adds.  They are
+// worked on two at a time.
+#ifndef FA_I4_NW_128
+#define FA_I4_NW_128 4
+#endif
+#ifndef FA_I4_BT_128
+#define FA_I4_BT_128 4
 #endif
 #ifndef FA_I4_STAGES_128
-#define FA_I4_STAGES_128 4
+#define FA_I4_STAGES_128 2
 #endif
 #ifndef FA_I4_CTAS_128
-#define FA_I4_CTAS_128 4
+#define FA_I4_CTAS_128 3
+#endif
+#ifndef FA_I4_NW_256
+#define FA_I4_NW_256 4
+#endif
+#ifndef FA_I4_BT_256
+#define FA_I4_BT_256 2
 #endif
 #ifndef FA_I4_STAGES_256
-#define FA_I4_STAGES_256 4
+#define FA_I4_STAGES_256 3
 #endif
 #ifndef FA_I4_CTAS_256
 #define FA_I4_CTAS_256 2
@@ -202,28 +215,31 @@ __global__ void __launch_bounds__(256) gather_kernel(const Params p, const unsig
 
 template <int D>
 struct Cfg {
-    static constexpr int NW = FA_I4_NW;
+    static constexpr int NW = D == 128 ? FA_I4_NW_128 : FA_I4_NW_256;
+    static constexpr int BT = D == 128 ? FA_I4_BT_128 : FA_I4_BT_256;   // tiles per batch
     static constexpr int STAGES = D == 128 ? FA_I4_STAGES_128 : FA_I4_STAGES_256;
     static constexpr int CTAS_PER_SM = D == 128 ? FA_I4_CTAS_128 : FA_I4_CTAS_256;
     static constexpr int NJ = D / 32;                  // blocks per row
     static constexpr int RB = D / 2;                   // code bytes per row
     static constexpr int SB = D / 16;                  // scale bytes per row
     static constexpr int K_OFF = 0;
-    static constexpr int V_OFF = TILE * RB;
-    static constexpr int KS_OFF = 2 * TILE * RB;
-    static constexpr int VS_OFF = KS_OFF + TILE * SB;
-    static constexpr int STAGE_BYTES = VS_OFF + TILE * SB;
+    static constexpr int V_OFF = BT * TILE * RB;
+    static constexpr int KS_OFF = 2 * BT * TILE * RB;
+    static constexpr int VS_OFF = KS_OFF + BT * TILE * SB;
+    static constexpr int STAGE_BYTES = VS_OFF + BT * TILE * SB;
     static constexpr int SMEM = NW * STAGES * STAGE_BYTES;
+    static_assert(BT % 2 == 0 && BT <= 32, "tiles are worked on in pairs");
+    static_assert(STAGES * BT <= 32, "a bit per tile of the ring");
     static_assert(CTAS_PER_SM * (SMEM + 1024) <= 228 * 1024, "shared memory per SM");
 };
 
 constexpr float NO_MAX = -3e38f;       // running maximum of a column that has no key yet
 constexpr float MAX_SLACK = 8.f;       // log2 units a score may pass the running maximum by
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void *src, int bytes, uint64_t policy)
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src, uint64_t policy)
 {
-    asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst),
-                 "l"(src), "r"(bytes), "l"(policy)
+    asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(dst),
+                 "l"(src), "l"(policy)
                  : "memory");
 }
 __device__ __forceinline__ uint4 lds128(uint32_t a)
@@ -240,6 +256,22 @@ __device__ __forceinline__ uint2 lds64(uint32_t a)
     asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
     return v;
 }
+__device__ __forceinline__ uint32_t lds32(uint32_t a)
+{
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ void sts32(uint32_t a, uint32_t v)
+{
+    asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
+__device__ __forceinline__ float lds_half(uint32_t a)
+{
+    unsigned short v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
+    return __half2float(__ushort_as_half(v));
+}
 __device__ __forceinline__ __half2 as_half2(uint32_t x)
 {
     return *reinterpret_cast<__half2 *>(&x);
@@ -252,24 +284,27 @@ __device__ __forceinline__ float pow2(int e)      // 2^e, e in [-126, 127]
 {
     return __uint_as_float(static_cast<unsigned>(e + 127) << 23);
 }
-// D = A . B + C with C apart from D
-__device__ __forceinline__ void mma_c(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                      uint32_t a3, uint32_t b0, uint32_t b1, float c0, float c1)
+// C = A . B, fp16 operands
+__device__ __forceinline__ void mma_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1)
 {
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
-        "{%4, %5, %6, %7}, {%8, %9}, {%10, %11, %10, %11};"
+        "{%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
-
-// Producer's place: the tile to issue next, as a cache row.  The block id of a
-// page is fetched when the page is entered, an iteration before it is used.
-struct Feed {
-    int ti, off, blk;            // tile index in the sequence, tile in page, page's block
-    const int *bt;               // the sequence's table row
-    long long row0;              // contiguous: the sequence and head's first row
-};
+// C += A . B, tf32 operands (fp32 values of which 10 fraction bits count)
+__device__ __forceinline__ void mma_tf32(float (&d)[4], float a0, float a1, float a2, float a3,
+                                         float b0, float b1)
+{
+    asm volatile(
+        "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, "
+        "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(__float_as_uint(a0)), "r"(__float_as_uint(a1)), "r"(__float_as_uint(a2)),
+          "r"(__float_as_uint(a3)), "r"(__float_as_uint(b0)), "r"(__float_as_uint(b1)));
+}
 
 // Swizzled offset of 16-byte chunk c of code row r: the 8 lanes of every
 // shared-memory phase of the K and V reads fall into different banks.
@@ -317,102 +352,117 @@ __global__ void __launch_bounds__(Cfg<D>::NW * 32, Cfg<D>::CTAS_PER_SM) decode_k
         }
     }
 
+    // ---- producer: the next batch, pw.k .. pw.k + n - 1 of pw's unit.  The lanes
+    // look up the cache rows of 32 tiles side by side (lane x: tile f_k + x), with
+    // the next 32 tiles' block ids already on their way.
+    constexpr int BT = C::BT;
     const int tpp = p.page_size / TILE;          // tiles per page
-    Feed f = {};
-    auto feed_unit = [&] {                       // pw stands in a new unit (or at its start)
-        f.ti = pw.lo / TILE + pw.k;
-        const int kv = pw.j / p.n_hg;
-        if (p.bt) {
-            f.bt = p.bt + (long long)pw.b * p.max_blocks;
-            f.off = f.ti % tpp;
-            f.blk = f.bt[f.ti / tpp];
-        } else {
-            f.row0 = ((long long)pw.b * p.Hkv + kv) * p.cap;
-        }
+    int left = n_my, f_k = 0, f_row = -1, f_blk = 0;
+    unsigned f_have = 0;                         // bit x: tile f_k + x is mapped
+    auto block_of = [&](int k) {                 // block id of tile k of pw's unit
+        const int ti = pw.lo / TILE + k;
+        return k < pw.n ? p.bt[(long long)pw.b * p.max_blocks + (tpp == 1 ? ti : ti / tpp)] : 0;
     };
-    // per-lane copy places: code chunks lane, lane + 32, ... and one scale chunk
-    constexpr int CPR = C::RB / 16;              // code chunks per row
-    constexpr int NCP = TILE * CPR / 32;         // code chunks per lane, K and V each
-    constexpr int NSC = TILE * C::SB / 16;       // scale chunks, K and V each
-    auto issue = [&](int s) -> bool {            // false: the block id is out of range
-        const int kv = pw.j / p.n_hg;
-        long long row;
-        if (p.bt) {
-            if (f.blk < 0 || f.blk >= p.num_blocks) {
-                if (lane == 0)
-                    flag(FA_STATUS_BAD_BLOCK);
-                return false;
-            }
-            row = ((long long)f.blk * p.Hkv + kv) * p.page_size + f.off * TILE;
+    auto window = [&](bool next) {               // rows of tiles pw.k .. pw.k + 31
+        const int kv = pw.j / p.n_hg, k = pw.k + lane, ti = pw.lo / TILE + k;
+        f_k = pw.k;
+        f_row = -1;
+        if (!p.bt) {
+            if (k < pw.n)
+                f_row = static_cast<int>(((long long)pw.b * p.Hkv + kv) * p.cap + ti * TILE);
         } else {
-            row = f.row0 + (long long)f.ti * TILE;
+            const int blk = next ? f_blk : block_of(k);
+            f_blk = block_of(k + 32);
+            if (k < pw.n && blk >= 0 && blk < p.num_blocks)
+                f_row = (blk * p.Hkv + kv) * p.page_size + (tpp == 1 ? 0 : ti % tpp * TILE);
+            else if (lane < left && k < pw.n)    // a tile of this worker's
+                flag(FA_STATUS_BAD_BLOCK);
         }
-        const uint32_t st = ring + s * C::STAGE_BYTES;
-        const int live = pw.hi - f.ti * TILE;    // rows from here on are zero-filled
+        f_have = __ballot_sync(0xffffffffu, f_row >= 0);
+    };
+    constexpr int CPR = C::RB / 16;              // code chunks per row
+    constexpr int NCP = TILE * CPR / 32;         // code chunks per lane and tile, K or V
+    constexpr int NSC = TILE * C::SB / 16;       // scale chunks per tile, K or V
+    const uint32_t d_code = code_off<D>(lane / CPR, lane % CPR);
+    const uint32_t d_scale = (lane >= NSC ? C::VS_OFF : C::KS_OFF) + lane % NSC * 16;
+    const char *k_src = p.k + lane * 16, *v_src = p.v + lane * 16;
+    const char *s_src = (lane >= NSC ? p.vs : p.ks) + lane % NSC * 16;
+    unsigned loaded = 0;                         // BT bits per stage: the tiles it holds
+    int s_put = 0;                               // stage of the next batch
+    auto copy_tile = [&](uint32_t st, int x, int r) {
+        const char *kp = k_src + (long long)r * C::RB;
+        const char *vp = v_src + (long long)r * C::RB;
+        const uint32_t dst = st + d_code + x * TILE * C::RB;
 #pragma unroll
         for (int i = 0; i < NCP; ++i) {
-            const int id = lane + 32 * i, r = id / CPR, c = id % CPR;
-            const int bytes = r < live ? 16 : 0;
-            const long long at = row * C::RB + id * 16;
-            cp16(st + C::K_OFF + code_off<D>(r, c), p.k + at, bytes, policy);
-            cp16(st + C::V_OFF + code_off<D>(r, c), p.v + at, bytes, policy);
+            // at D = 256 every second chunk flips the swizzle's bit 2
+            const uint32_t at = D == 256 && (i & 1) ? (dst ^ 64u) : dst;
+            cp16(at + C::K_OFF + i * 512, kp + i * 512, policy);
+            cp16(at + C::V_OFF + i * 512, vp + i * 512, policy);
         }
-        if (lane < 2 * NSC) {
-            const int c = lane % NSC;
-            const int bytes = min(max(live * C::SB - c * 16, 0), 16);
-            cp16(st + (lane < NSC ? C::KS_OFF : C::VS_OFF) + c * 16,
-                 (lane < NSC ? p.ks : p.vs) + row * C::SB + c * 16, bytes, policy);
-        }
-        return true;
+        if (lane < 2 * NSC)
+            cp16(st + d_scale + x * TILE * C::SB, s_src + (long long)r * C::SB, policy);
     };
-    auto feed_next = [&] {                       // pw to the tile after this one
-        pw.next(p);
-        if (pw.k == 0) {
-            if (pw.b < p.B)
-                feed_unit();
-            return;
-        }
-        ++f.ti;
-        if (p.bt && ++f.off == tpp) {
-            f.off = 0;
-            f.blk = f.bt[f.ti / tpp];
-        }
-    };
-    unsigned ok = 0;                             // bit s: stage s holds a tile
-    auto put = [&](int i) {                      // issue tile i (an empty group past the end)
-        const int s = i % S;
-        if (i < n_my) {
-            ok = issue(s) ? ok | (1u << s) : ok & ~(1u << s);
-            if (i + 1 < n_my)
-                feed_next();
+    auto put = [&] {                             // an empty group past the end
+        if (left > 0) {
+            const int n = min(min(BT, pw.n - pw.k), left);
+            if (pw.k - f_k > 32 - BT)
+                window(pw.k - f_k == 32);
+            const int x0 = pw.k - f_k;
+            const unsigned have = (f_have >> x0) & ((1u << n) - 1u);
+            loaded = (loaded & ~(((1u << BT) - 1u) << (s_put * BT))) | have << (s_put * BT);
+            const uint32_t st = ring + s_put * C::STAGE_BYTES;
+            if (have == (1u << BT) - 1u) {
+#pragma unroll
+                for (int x = 0; x < BT; ++x)
+                    copy_tile(st, x, __shfl_sync(0xffffffffu, f_row, x0 + x));
+            } else {
+#pragma unroll 1
+                for (int x = 0; x < n; ++x)
+                    if ((have >> x) & 1u)
+                        copy_tile(st, x, __shfl_sync(0xffffffffu, f_row, x0 + x));
+            }
+            left -= n;
+            pw.k += n;
+            if (pw.k == pw.n && left > 0) {
+                --pw.k;
+                pw.next(p);
+                window(false);
+            }
+            s_put = s_put + 1 == S ? 0 : s_put + 1;
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
     if (n_my > 0)
-        feed_unit();
+        window(false);
+#pragma unroll 1
     for (int i = 0; i < S - 1; ++i)
-        put(i);
+        put();
 
-    // The unit's queries: column g's elements (n, n+4) of octet t of block j as
-    // half2, odd n divided by 16; and per column pair the block's offset term.
+    // ---- the unit's queries: column g's elements (n, n+4) of octet t of block j
+    // as half2, odd n divided by 16; and column g's offset terms in two tf32 parts
     const int tq = p.tq > 1 ? p.tq : 1;
     uint32_t qb[NJ][4];
-    float c0[NJ], c1[NJ];
-    int nh = 0, clo[2], chi[2], all_lo = 0, all_hi = 0;
+    float ct[NJ / 4][2];             // of block 4i + t
+    int nh = 0, clo[2], chi[2], all_lo = 0, all_hi = 0, base = 0;
     auto load_q = [&] {
+        base = cw.tok();
         const int kv = cw.j / p.n_hg, cg = cw.j % p.n_hg;
         nh = min(GPH, tq * p.G - cg * GPH);
         const tc::Col cq = tc::column(p, kv, cg, g, GPH);
         const uint4 *src = reinterpret_cast<const uint4 *>(
             p.q + (((long long)cw.b * tq + cq.j) * p.Hq + cq.h) * D);
         const __half2 sixteenth = __float2half2_rn(0.0625f);
+        uint4 x[NJ];
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+            x[j] = cq.live ? __ldg(src + j * 4 + t) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
-            const uint4 x = cq.live ? __ldg(src + j * 4 + t) : make_uint4(0u, 0u, 0u, 0u);
-            qb[j][0] = __byte_perm(x.x, x.z, 0x5410);                              // 0, 4
-            qb[j][1] = as_u32(__hmul2(as_half2(__byte_perm(x.x, x.z, 0x7632)), sixteenth));
-            qb[j][2] = __byte_perm(x.y, x.w, 0x5410);                              // 2, 6
-            qb[j][3] = as_u32(__hmul2(as_half2(__byte_perm(x.y, x.w, 0x7632)), sixteenth));
+            qb[j][0] = __byte_perm(x[j].x, x[j].z, 0x5410);                        // 0, 4
+            qb[j][1] = as_u32(__hmul2(as_half2(__byte_perm(x[j].x, x[j].z, 0x7632)), sixteenth));
+            qb[j][2] = __byte_perm(x[j].y, x[j].w, 0x5410);                        // 2, 6
+            qb[j][3] = as_u32(__hmul2(as_half2(__byte_perm(x[j].y, x[j].w, 0x7632)), sixteenth));
             float sum = 0.f;
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
@@ -421,23 +471,27 @@ __global__ void __launch_bounds__(Cfg<D>::NW * 32, Cfg<D>::CTAS_PER_SM) decode_k
             }
             sum += __shfl_xor_sync(0xffffffffu, sum, 1);
             sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-            sum *= -8.f / 16777216.f;
-            c0[j] = __shfl_sync(0xffffffffu, sum, 8 * t);          // column 2t
-            c1[j] = __shfl_sync(0xffffffffu, sum, 8 * t + 4);      // column 2t + 1
+            if (j % 4 == t) {
+                sum *= -8.f * p.c2;                                // log2 units
+                ct[j / 4][0] = __uint_as_float(__float_as_uint(sum) & 0xffffe000u);
+                ct[j / 4][1] = sum - ct[j / 4][0];
+            }
         }
         const tc::Col a = tc::column(p, kv, cg, 2 * t, GPH);
         const tc::Col b = tc::column(p, kv, cg, 2 * t + 1, GPH);
         tc::column_range(p, cw.b, cw.hi, a.live ? a.j : tq - 1, clo[0], chi[0]);
         tc::column_range(p, cw.b, cw.hi, b.live ? b.j : tq - 1, clo[1], chi[1]);
-        int x;
-        tc::column_range(p, cw.b, cw.hi, tq - 1, all_lo, x);   // keys every query attends
-        tc::column_range(p, cw.b, cw.hi, 0, x, all_hi);
+        int x0;
+        tc::column_range(p, cw.b, cw.hi, tq - 1, all_lo, x0);   // keys every query attends
+        tc::column_range(p, cw.b, cw.hi, 0, x0, all_hi);
     };
 
-    float acc[2 * NJ][4];     // [2j + h]: elements 32j + 4g + 2h (0, 1) and + 1 (2, 3); columns 2t, 2t+1
+    // [2j + i]: elements 32j + 4g + 2i (0, 1: columns 2t, 2t+1; times 2^-24) and
+    // + 1 (2, 3; times 2^-20)
+    float acc[2 * NJ][4];
     float mr[2], l[2];
     int e = 0;                // O is held times 2^-e
-    __half vlim = __float2half_rn(0.f);     // V scales above it call for another e
+    __half2 vlim;             // V scales above it call for another e
     auto reset = [&] {
 #pragma unroll
         for (int i = 0; i < 2 * NJ; ++i)
@@ -445,32 +499,60 @@ __global__ void __launch_bounds__(Cfg<D>::NW * 32, Cfg<D>::CTAS_PER_SM) decode_k
         mr[0] = mr[1] = NO_MAX;
         l[0] = l[1] = 0.f;
         e = 0;
-        vlim = __float2half_rn(0.f);
+        vlim = __float2half2_rn(0.f);
     };
     if (n_my > 0)
         load_q();
     reset();
     const float c2 = p.c2 * 16777216.f;
+    // the constant A fragment: -8 2^-24 in even rows, -8 2^-20 in odd ones, each
+    // combined with a zero the compiler does not know (T < 2^60), or it would
+    // build the four registers anew for every mma
+    const uint32_t m8[4] = {0x80088008u ^ static_cast<uint32_t>(T >> 60),
+                            0x80808080u ^ static_cast<uint32_t>(T >> 61),
+                            0x80088008u ^ static_cast<uint32_t>(t1 >> 60),
+                            0x80808080u ^ static_cast<uint32_t>(t1 >> 61)};
+    const uint32_t half_sel = g & 1 ? 0x7632 : 0x5410;
+    // lane's places in a stage: K rows g, V rows 2t, scales
+    uint32_t kc[NJ / 4], vc[2][NJ / 4];
+#pragma unroll
+    for (int q = 0; q < NJ / 4; ++q) {
+        kc[q] = C::K_OFF + code_off<D>(g, D == 128 ? t : 2 * t + q);
+        vc[0][q] = C::V_OFF + code_off<D>(2 * t, D == 128 ? g >> 1 : 2 * (g >> 1) + q);
+        vc[1][q] = C::V_OFF + code_off<D>(2 * t + 1, D == 128 ? g >> 1 : 2 * (g >> 1) + q);
+    }
 
-    for (int i = 0; i < n_my; ++i) {
-        const int s = i % S;
+    int s = 0;
+    for (int i = 0; i < n_my;) {
         asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
-        __syncwarp();                 // tile i has landed; every lane is done with tile i - 1
-        const bool tile_ok = (ok >> s) & 1u;
-        put(i + S - 1);
-        const uint32_t st = ring + s * C::STAGE_BYTES;
-        const int base = cw.tok();
+        __syncwarp();                 // the batch has landed; every lane is done with the last
+        const unsigned have_all = loaded >> (s * BT);
+        const int nb = min(min(BT, cw.n - cw.k), n_my - i);
+        const uint32_t stage = ring + s * C::STAGE_BYTES;
+        s = s + 1 == S ? 0 : s + 1;
+        put();
 
-        if (tile_ok) {
-            // ---- scores: rows are keys g and g + 8, columns 2t and 2t + 1
-            float sc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+        for (int hh = 0; hh < nb; hh += 2) {
+        const uint32_t st = stage + hh * TILE * C::RB;       // codes and scales of this pair
+        const uint32_t ss = stage + hh * TILE * C::SB;
+        const unsigned have = (have_all >> hh) & 3u;
+        // ---- scores of tile h: rows are keys g and g + 8, columns 2t and 2t + 1
+        float sc[2][4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float a4[4], off[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int jj = 0; jj < NJ; jj += 4) {
-                const int ch = D == 128 ? t : 2 * t + jj / 4;
-                const uint4 wa = lds128(st + C::K_OFF + code_off<D>(g, ch));
-                const uint4 wb = lds128(st + C::K_OFF + code_off<D>(g + 8, ch));
-                const uint2 sa = lds64(st + C::KS_OFF + g * C::SB + jj * 2);
-                const uint2 sb = lds64(st + C::KS_OFF + (g + 8) * C::SB + jj * 2);
+                const uint32_t row = st + h * TILE * C::RB;
+                const uint32_t srow = ss + C::KS_OFF + (h * TILE + g) * C::SB + jj * 2;
+                // 8 rows down the swizzle is the same
+                const uint4 wa = lds128(row + kc[jj / 4]);
+                const uint4 wb = lds128(row + kc[jj / 4] + 8 * C::RB);
+                const uint2 sa = lds64(srow);
+                const uint2 sb = lds64(srow + 8 * C::SB);
+                const float ta = lds_half(srow + 2 * t), tb = lds_half(srow + 8 * C::SB + 2 * t);
+                mma_tf32(off, ta, tb, ta, tb, ct[jj / 4][0], ct[jj / 4][1]);
                 const uint32_t a[4] = {wa.x, wa.y, wa.z, wa.w};
                 const uint32_t b[4] = {wb.x, wb.y, wb.z, wb.w};
                 const float2 fa[2] = {__half22float2(as_half2(sa.x)), __half22float2(as_half2(sa.y))};
@@ -479,133 +561,148 @@ __global__ void __launch_bounds__(Cfg<D>::NW * 32, Cfg<D>::CTAS_PER_SM) decode_k
                 for (int q = 0; q < 4; ++q) {
                     const int j = jj + q;
                     float d[4];
-                    mma_c(d, a[q] & 0x000f000fu, b[q] & 0x000f000fu, a[q] & 0x00f000f0u,
-                          b[q] & 0x00f000f0u, qb[j][0], qb[j][1], c0[j], c1[j]);
+                    mma_zero(d, a[q] & 0x000f000fu, b[q] & 0x000f000fu, a[q] & 0x00f000f0u,
+                             b[q] & 0x00f000f0u, qb[j][0], qb[j][1]);
                     const uint32_t ah = a[q] >> 8, bh = b[q] >> 8;
                     tc::mma16816(d, ah & 0x000f000fu, bh & 0x000f000fu, ah & 0x00f000f0u,
                                  bh & 0x00f000f0u, qb[j][2], qb[j][3]);
                     const float ka = q & 1 ? fa[q / 2].y : fa[q / 2].x;
                     const float kb = q & 1 ? fb[q / 2].y : fb[q / 2].x;
-                    sc[0] = fmaf(d[0], ka, sc[0]);
-                    sc[1] = fmaf(d[1], ka, sc[1]);
-                    sc[2] = fmaf(d[2], kb, sc[2]);
-                    sc[3] = fmaf(d[3], kb, sc[3]);
+                    a4[0] = j ? fmaf(d[0], ka, a4[0]) : d[0] * ka;
+                    a4[1] = j ? fmaf(d[1], ka, a4[1]) : d[1] * ka;
+                    a4[2] = j ? fmaf(d[2], kb, a4[2]) : d[2] * kb;
+                    a4[3] = j ? fmaf(d[3], kb, a4[3]) : d[3] * kb;
                 }
-            }
-            // ---- V scales as half2 over the key pairs (2t, 2t+1), (2t+8, 2t+9)
-            __half2 sv[2][NJ];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                uint32_t x[NJ];       // the two keys' scales: NJ / 2 words each
-#pragma unroll
-                for (int q = 0; q < NJ / 4; ++q) {
-                    const uint4 v = lds128(st + C::VS_OFF + (2 * t + 8 * h) * C::SB + q * 16);
-                    x[4 * q] = v.x; x[4 * q + 1] = v.y; x[4 * q + 2] = v.z; x[4 * q + 3] = v.w;
-                }
-#pragma unroll
-                for (int j = 0; j < NJ; ++j)
-                    sv[h][j] = as_half2(__byte_perm(x[j / 2], x[NJ / 2 + j / 2],
-                                                    j & 1 ? 0x7632 : 0x5410));
             }
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-                sc[q] *= c2;                  // log2 units
-            // ---- tile edges, and the ranges of several queries
-            if (base < all_lo || base + TILE > all_hi) {
-                const int ka = base + g, kb = base + g + 8;
-                if (ka < clo[0] || ka >= chi[0])
-                    sc[0] = -INFINITY;
-                if (ka < clo[1] || ka >= chi[1])
-                    sc[1] = -INFINITY;
-                if (kb < clo[0] || kb >= chi[0])
-                    sc[2] = -INFINITY;
-                if (kb < clo[1] || kb >= chi[1])
-                    sc[3] = -INFINITY;
-                // rows before the window hold other data: their scales must not
-                // turn a zero weight into NaN (rows after the end are zero-filled)
-                const int r0 = cw.lo - base;
+                sc[h][q] = fmaf(a4[q], c2, off[q]);          // log2 units
+        }
+        // the pair's V scales, a few words per lane, against the limit
+        constexpr int NVW = 2 * TILE * NJ / 2 / 32;
+        uint32_t vw[NVW];
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
+        for (int q = 0; q < NVW; ++q)
+            vw[q] = lds32(ss + C::VS_OFF + (lane + 32 * q) * 4);
+        // ---- tile edges, and the ranges of several queries
+        const bool edge = base < all_lo || base + 2 * TILE > all_hi || have != 3u;
+        // the pair's keys that are there at all; other rows hold anything
+        auto there = [&](int k) {
+            return k >= cw.lo - base && k < cw.hi - base && ((have >> (k / TILE)) & 1u);
+        };
+        if (edge) {
 #pragma unroll
-                    for (int j = 0; j < NJ; ++j) {
-                        const uint32_t m = (2 * t + 8 * h >= r0 ? 0x0000ffffu : 0u) |
-                                           (2 * t + 8 * h + 1 >= r0 ? 0xffff0000u : 0u);
-                        sv[h][j] = as_half2(as_u32(sv[h][j]) & m);
-                    }
+            for (int h = 0; h < 2; ++h) {
+                const int ka = base + h * TILE + g, kb = ka + 8;
+                const bool un = !((have >> h) & 1u);
+                if (un || ka < clo[0] || ka >= chi[0])
+                    sc[h][0] = -INFINITY;
+                if (un || ka < clo[1] || ka >= chi[1])
+                    sc[h][1] = -INFINITY;
+                if (un || kb < clo[0] || kb >= chi[0])
+                    sc[h][2] = -INFINITY;
+                if (un || kb < clo[1] || kb >= chi[1])
+                    sc[h][3] = -INFINITY;
             }
-            if constexpr (WT)
-                tc::store_scores(p, cw.unit(p), base + g, base + g + 8, 2 * t, nh, sc);
-            // ---- online softmax
-            float d[4] = {sc[0] - mr[0], sc[1] - mr[1], sc[2] - mr[0], sc[3] - mr[1]};
-            __half2 vm = sv[0][0];
+            // other rows must not turn a zero weight into NaN
 #pragma unroll
-            for (int j = 1; j < 2 * NJ; ++j)
-                vm = __hmax2(vm, sv[j / NJ][j % NJ]);
-            const __half vmx = __hmax(__low2half(vm), __high2half(vm));
-            const bool over = fmaxf(fmaxf(d[0], d[1]), fmaxf(d[2], d[3])) > MAX_SLACK;
-            if (__any_sync(0xffffffffu, over || __hgt(vmx, vlim))) {
-                float x0 = fmaxf(sc[0], sc[2]), x1 = fmaxf(sc[1], sc[3]);
-                float vx = __half2float(vmx);
+            for (int q = 0; q < NVW; ++q)
+                if (!there((lane + 32 * q) / (NJ / 2))) {
+                    vw[q] = 0u;
+                    sts32(ss + C::VS_OFF + (lane + 32 * q) * 4, 0u);
+                }
+            __syncwarp();
+        }
+        if constexpr (WT) {
 #pragma unroll
-                for (int mask = 4; mask <= 16; mask <<= 1) {
-                    x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, mask));
-                    x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, mask));
-                }
-                vx = fmaxf(vx, __shfl_xor_sync(0xffffffffu, vx, 1));
-                vx = fmaxf(vx, __shfl_xor_sync(0xffffffffu, vx, 2));
-                const float n0 = fmaxf(mr[0], x0), n1 = fmaxf(mr[1], x1);
-                int en = e;
-                if (vx > __half2float(vlim)) {
-                    // the largest scale so far: carried as it is from 2^-12 to
-                    // 2^7, else brought to [1/2, 1) (at most 2^14 up)
-                    const int ex = static_cast<int>((__float_as_uint(vx) >> 23) & 255u) - 126;
-                    en = (ex >= -11 && ex <= 7) ? 0 : max(ex, -14);
-                    vlim = __float2half_rn(en == 0 ? 128.f : fminf(pow2(en + 2), 65504.f));
-                }
-                const float r0 = ex2(mr[0] - n0) * pow2(e - en);
-                const float r1 = ex2(mr[1] - n1) * pow2(e - en);
+            for (int h = 0; h < 2; ++h)
+                if ((have >> h) & 1u)
+                    tc::store_scores(p, cw.unit(p), base + h * TILE + g, base + h * TILE + g + 8,
+                                     2 * t, nh, sc[h]);
+        }
+        // ---- online softmax
+        __half2 vm = as_half2(vw[0]);
 #pragma unroll
-                for (int ii = 0; ii < 2 * NJ; ++ii) {
-                    acc[ii][0] *= r0;
-                    acc[ii][1] *= r1;
-                    acc[ii][2] *= r0;
-                    acc[ii][3] *= r1;
+        for (int q = 1; q < NVW; ++q)
+            vm = __hmax2(vm, as_half2(vw[q]));
+        const float x0 = fmaxf(fmaxf(sc[0][0], sc[0][2]), fmaxf(sc[1][0], sc[1][2]));
+        const float x1 = fmaxf(fmaxf(sc[0][1], sc[0][3]), fmaxf(sc[1][1], sc[1][3]));
+        const bool over = fmaxf(x0 - mr[0], x1 - mr[1]) > MAX_SLACK || !__hble2(vm, vlim);
+        if (__any_sync(0xffffffffu, over)) {
+            float y0 = x0, y1 = x1;
+            float vx = __half2float(__hmax(__low2half(vm), __high2half(vm)));
+#pragma unroll
+            for (int mask = 1; mask <= 16; mask <<= 1) {
+                if (mask >= 4) {
+                    y0 = fmaxf(y0, __shfl_xor_sync(0xffffffffu, y0, mask));
+                    y1 = fmaxf(y1, __shfl_xor_sync(0xffffffffu, y1, mask));
                 }
-                l[0] *= ex2(mr[0] - n0);
-                l[1] *= ex2(mr[1] - n1);
-                mr[0] = n0;
-                mr[1] = n1;
-                e = en;
-                d[0] = sc[0] - n0;
-                d[1] = sc[1] - n1;
-                d[2] = sc[2] - n0;
-                d[3] = sc[3] - n1;
+                vx = fmaxf(vx, __shfl_xor_sync(0xffffffffu, vx, mask));
             }
-            if (e != 0) {
-                const __half2 f2 = __float2half2_rn(pow2(-e));
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int j = 0; j < NJ; ++j)
-                        sv[h][j] = __hmul2(sv[h][j], f2);
+            const float n0 = fmaxf(mr[0], y0), n1 = fmaxf(mr[1], y1);
+            int en = e;
+            if (vx > __low2float(vlim)) {
+                // the largest scale so far: carried as it is from 2^-12 to
+                // 2^7, else brought to [1/2, 1) (at most 2^14 up)
+                const int ex = static_cast<int>((__float_as_uint(vx) >> 23) & 255u) - 126;
+                en = (ex >= -11 && ex <= 7) ? 0 : max(ex, -14);
+                vlim = __float2half2_rn(en == 0 ? 128.f : fminf(pow2(en + 2), 65504.f));
             }
-            const float p0 = ex2(d[0]), p1 = ex2(d[1]), p2 = ex2(d[2]), p3 = ex2(d[3]);
+            const float a0 = ex2(mr[0] - n0), a1 = ex2(mr[1] - n1);
+            l[0] *= a0;
+            l[1] *= a1;
+            const float r0e = a0 * pow2(e - en), r1e = a1 * pow2(e - en);
+#pragma unroll
+            for (int ii = 0; ii < 2 * NJ; ++ii) {
+                acc[ii][0] *= r0e;
+                acc[ii][1] *= r1e;
+                acc[ii][2] *= r0e;
+                acc[ii][3] *= r1e;
+            }
+            mr[0] = n0;
+            mr[1] = n1;
+            e = en;
+        }
+        if (e != 0) {
+            const __half2 f2 = __float2half2_rn(pow2(-e));
+#pragma unroll
+            for (int q = 0; q < NVW; ++q)
+                sts32(ss + C::VS_OFF + (lane + 32 * q) * 4, as_u32(__hmul2(as_half2(vw[q]), f2)));
+            __syncwarp();
+        }
+        // ---- O^T += V^T . (P s)^T: rows are elements, 4 per block and lane
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const float p0 = ex2(sc[h][0] - mr[0]), p1 = ex2(sc[h][1] - mr[1]);
+            const float p2 = ex2(sc[h][2] - mr[0]), p3 = ex2(sc[h][3] - mr[1]);
             l[0] += p0 + p2;
             l[1] += p1 + p3;
             // P^T as the B operand: keys (2t, 2t+1) and (2t+8, 2t+9), column g
             const __half2 pa = as_half2(tc::movmatrix_t(tc::pack_half2(p0, p1)));
             const __half2 pb = as_half2(tc::movmatrix_t(tc::pack_half2(p2, p3)));
-            // ---- O^T += V^T . (P s)^T: rows are elements, 4 per block and lane
-            const uint32_t half_sel = g & 1 ? 0x7632 : 0x5410;
-            const __half2 b1032 = __float2half2_rn(1032.f), b72 = __float2half2_rn(72.f);
+            // V scales as half2 over the same key pairs
+            __half2 sv[2][NJ];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                uint32_t u[NJ];       // the two keys' scales: NJ / 2 words each
+#pragma unroll
+                for (int q = 0; q < NJ / 4; ++q) {
+                    const uint4 v = lds128(ss + C::VS_OFF + (h * TILE + 2 * t + 8 * x) * C::SB +
+                                           q * 16);
+                    u[4 * q] = v.x; u[4 * q + 1] = v.y; u[4 * q + 2] = v.z; u[4 * q + 3] = v.w;
+                }
+#pragma unroll
+                for (int j = 0; j < NJ; ++j)
+                    sv[x][j] = as_half2(__byte_perm(u[j / 2], u[NJ / 2 + j / 2],
+                                                    j & 1 ? 0x7632 : 0x5410));
+            }
 #pragma unroll
             for (int jj = 0; jj < NJ; jj += 4) {
-                uint32_t v[4][4];
+                const uint32_t row = st + h * TILE * C::RB;
+                uint32_t v[4][4];     // keys 2t, 2t+1, 2t+8, 2t+9
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    const int key = 2 * t + (q & 1) + 8 * (q >> 1);
-                    const int ch = D == 128 ? g >> 1 : 2 * (g >> 1) + jj / 4;
-                    const uint4 x = lds128(st + C::V_OFF + code_off<D>(key, ch));
+                    const uint4 x = lds128(row + vc[q & 1][jj / 4] + (q >> 1) * 8 * C::RB);
                     v[q][0] = x.x; v[q][1] = x.y; v[q][2] = x.z; v[q][3] = x.w;
                 }
 #pragma unroll
@@ -614,22 +711,24 @@ __global__ void __launch_bounds__(Cfg<D>::NW * 32, Cfg<D>::CTAS_PER_SM) decode_k
                     const uint32_t x = __byte_perm(v[0][q], v[1][q], half_sel);
                     const uint32_t y = __byte_perm(v[2][q], v[3][q], half_sel);
                     const uint32_t xh = x >> 8, yh = y >> 8;
-                    auto even = [&](uint32_t z) {
-                        return as_u32(__hsub2(as_half2((z & 0x000f000fu) | 0x64006400u), b1032));
-                    };
-                    auto odd = [&](uint32_t z) {
-                        return as_u32(__hsub2(as_half2((z & 0x00f000f0u) | 0x54005400u), b72));
-                    };
                     const uint32_t s0 = as_u32(__hmul2(pa, sv[0][j]));
                     const uint32_t s1 = as_u32(__hmul2(pb, sv[1][j]));
-                    tc::mma16816(acc[2 * j], even(x), odd(x), even(y), odd(y), s0, s1);
-                    tc::mma16816(acc[2 * j + 1], even(xh), odd(xh), even(yh), odd(yh), s0, s1);
+                    tc::mma16816(acc[2 * j], m8[0], m8[1], m8[2], m8[3], s0, s1);
+                    tc::mma16816(acc[2 * j + 1], m8[0], m8[1], m8[2], m8[3], s0, s1);
+                    tc::mma16816(acc[2 * j], x & 0x000f000fu, x & 0x00f000f0u, y & 0x000f000fu,
+                                 y & 0x00f000f0u, s0, s1);
+                    tc::mma16816(acc[2 * j + 1], xh & 0x000f000fu, xh & 0x00f000f0u,
+                                 yh & 0x000f000fu, yh & 0x00f000f0u, s0, s1);
                 }
             }
         }
 
-        const bool unit_end = cw.k == cw.n - 1;
-        if (unit_end || i + 1 == n_my) {
+        base += 2 * TILE;
+        }   // pairs of the batch
+
+        i += nb;
+        cw.k += nb;
+        if (cw.k == cw.n || i == n_my) {
             // ---- end of this worker's segment of the unit
 #pragma unroll
             for (int mask = 4; mask <= 16; mask <<= 1) {
@@ -639,7 +738,6 @@ __global__ void __launch_bounds__(Cfg<D>::NW * 32, Cfg<D>::CTAS_PER_SM) decode_k
             const long long us = cw.unit_start();
             const bool whole = tc::worker_of(us, T, We) == tc::worker_of(us + cw.n - 1, T, We);
             const int kv = cw.j / p.n_hg, cg = cw.j % p.n_hg;
-            const float up = pow2(e);
             const long long slot = w + cw.unit(p);
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
@@ -647,16 +745,18 @@ __global__ void __launch_bounds__(Cfg<D>::NW * 32, Cfg<D>::CTAS_PER_SM) decode_k
                 if (h >= nh)
                     continue;
                 const float mx = mr[x] == NO_MAX ? -INFINITY : mr[x];
+                // 2^24 and 2^20 as the accumulators hold them; l = 0 only without keys
+                const float up = whole && l[x] > 0.f ? pow2(e + 20) / l[x] : pow2(e + 20);
+                const float up16 = up * 16.f;
                 if (whole) {
                     const tc::Col cc = tc::column(p, kv, cg, h, GPH);
                     const long long r = ((long long)cw.b * tq + cc.j) * p.Hq + cc.h;
-                    const float inv = l[x] > 0.f ? up / l[x] : 0.f;
                     __half *o = reinterpret_cast<__half *>(p.out) + r * D + 4 * g;
 #pragma unroll
                     for (int j = 0; j < NJ; ++j)
                         tc::store4(o + 32 * j,
-                                   make_float4(acc[2 * j][x] * inv, acc[2 * j][x + 2] * inv,
-                                               acc[2 * j + 1][x] * inv, acc[2 * j + 1][x + 2] * inv));
+                                   make_float4(acc[2 * j][x] * up16, acc[2 * j][x + 2] * up,
+                                               acc[2 * j + 1][x] * up16, acc[2 * j + 1][x + 2] * up));
                     if (WT && g == 0)
                         p.lse[r] = l[x] > 0.f ? mx + log2f(l[x]) : -INFINITY;
                 } else {
@@ -664,19 +764,18 @@ __global__ void __launch_bounds__(Cfg<D>::NW * 32, Cfg<D>::CTAS_PER_SM) decode_k
 #pragma unroll
                     for (int j = 0; j < NJ; ++j)
                         tc::store4(o + 32 * j,
-                                   make_float4(acc[2 * j][x] * up, acc[2 * j][x + 2] * up,
-                                               acc[2 * j + 1][x] * up, acc[2 * j + 1][x + 2] * up));
+                                   make_float4(acc[2 * j][x] * up16, acc[2 * j][x + 2] * up,
+                                               acc[2 * j + 1][x] * up16, acc[2 * j + 1][x + 2] * up));
                     if (g == 0)
                         p.ws_ml[slot * p.sh + h] = make_float2(mx, l[x]);
                 }
             }
             reset();
-            if (i + 1 < n_my) {
+            if (i < n_my) {
+                --cw.k;
                 cw.next(p);
                 load_q();
             }
-        } else {
-            cw.next(p);
         }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
@@ -988,6 +1087,8 @@ FA_API int fa_decode_int4(const void *q, const void *k_codes, const void *k_scal
         !aligned_to(acc, 4))
         return fail(FA_ERR_ALIGN, "%s: seq_lens, block_table, window and acc must be 4-byte "
                                   "aligned", name);
+    if (kv_rows >= (1ull << 31))
+        return fail(FA_ERR_LAYOUT, "%s: caches of 2^31 rows or more are not supported", name);
     const size_t q_bytes = (size_t)batch * n_queries * n_q_heads * head_dim * 2;
     const size_t cb = kv_rows * (head_dim / 2), sb = kv_rows * (head_dim / 16);
     const i4::Span outs[] = {{out, q_bytes}, {acc, kv_rows * sizeof(float)}};
