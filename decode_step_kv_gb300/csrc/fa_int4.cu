@@ -557,21 +557,25 @@ __global__ void __launch_bounds__(Cfg<D>::NW * 32, Cfg<D>::CTAS_PER_SM) decode_k
                 const uint32_t b[4] = {wb.x, wb.y, wb.z, wb.w};
                 const float2 fa[2] = {__half22float2(as_half2(sa.x)), __half22float2(as_half2(sa.y))};
                 const float2 fb[2] = {__half22float2(as_half2(sb.x)), __half22float2(as_half2(sb.y))};
+                float d[4][4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    mma_zero(d[q], a[q] & 0x000f000fu, b[q] & 0x000f000fu, a[q] & 0x00f000f0u,
+                             b[q] & 0x00f000f0u, qb[jj + q][0], qb[jj + q][1]);
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    const int j = jj + q;
-                    float d[4];
-                    mma_zero(d, a[q] & 0x000f000fu, b[q] & 0x000f000fu, a[q] & 0x00f000f0u,
-                             b[q] & 0x00f000f0u, qb[j][0], qb[j][1]);
                     const uint32_t ah = a[q] >> 8, bh = b[q] >> 8;
-                    tc::mma16816(d, ah & 0x000f000fu, bh & 0x000f000fu, ah & 0x00f000f0u,
-                                 bh & 0x00f000f0u, qb[j][2], qb[j][3]);
+                    tc::mma16816(d[q], ah & 0x000f000fu, bh & 0x000f000fu, ah & 0x00f000f0u,
+                                 bh & 0x00f000f0u, qb[jj + q][2], qb[jj + q][3]);
+                }
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
                     const float ka = q & 1 ? fa[q / 2].y : fa[q / 2].x;
                     const float kb = q & 1 ? fb[q / 2].y : fb[q / 2].x;
-                    a4[0] = j ? fmaf(d[0], ka, a4[0]) : d[0] * ka;
-                    a4[1] = j ? fmaf(d[1], ka, a4[1]) : d[1] * ka;
-                    a4[2] = j ? fmaf(d[2], kb, a4[2]) : d[2] * kb;
-                    a4[3] = j ? fmaf(d[3], kb, a4[3]) : d[3] * kb;
+                    a4[0] = jj + q ? fmaf(d[q][0], ka, a4[0]) : d[q][0] * ka;
+                    a4[1] = jj + q ? fmaf(d[q][1], ka, a4[1]) : d[q][1] * ka;
+                    a4[2] = jj + q ? fmaf(d[q][2], kb, a4[2]) : d[q][2] * kb;
+                    a4[3] = jj + q ? fmaf(d[q][3], kb, a4[3]) : d[q][3] * kb;
                 }
             }
 #pragma unroll
@@ -705,20 +709,24 @@ __global__ void __launch_bounds__(Cfg<D>::NW * 32, Cfg<D>::CTAS_PER_SM) decode_k
                     const uint4 x = lds128(row + vc[q & 1][jj / 4] + (q >> 1) * 8 * C::RB);
                     v[q][0] = x.x; v[q][1] = x.y; v[q][2] = x.z; v[q][3] = x.w;
                 }
+                uint32_t s0[4], s1[4];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    const int j = jj + q;
+                    s0[q] = as_u32(__hmul2(pa, sv[0][jj + q]));
+                    s1[q] = as_u32(__hmul2(pb, sv[1][jj + q]));
+                }
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                    tc::mma16816(acc[2 * jj + q], m8[0], m8[1], m8[2], m8[3], s0[q / 2], s1[q / 2]);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
                     const uint32_t x = __byte_perm(v[0][q], v[1][q], half_sel);
                     const uint32_t y = __byte_perm(v[2][q], v[3][q], half_sel);
                     const uint32_t xh = x >> 8, yh = y >> 8;
-                    const uint32_t s0 = as_u32(__hmul2(pa, sv[0][j]));
-                    const uint32_t s1 = as_u32(__hmul2(pb, sv[1][j]));
-                    tc::mma16816(acc[2 * j], m8[0], m8[1], m8[2], m8[3], s0, s1);
-                    tc::mma16816(acc[2 * j + 1], m8[0], m8[1], m8[2], m8[3], s0, s1);
-                    tc::mma16816(acc[2 * j], x & 0x000f000fu, x & 0x00f000f0u, y & 0x000f000fu,
-                                 y & 0x00f000f0u, s0, s1);
-                    tc::mma16816(acc[2 * j + 1], xh & 0x000f000fu, xh & 0x00f000f0u,
-                                 yh & 0x000f000fu, yh & 0x00f000f0u, s0, s1);
+                    tc::mma16816(acc[2 * (jj + q)], x & 0x000f000fu, x & 0x00f000f0u,
+                                 y & 0x000f000fu, y & 0x00f000f0u, s0[q], s1[q]);
+                    tc::mma16816(acc[2 * (jj + q) + 1], xh & 0x000f000fu, xh & 0x00f000f0u,
+                                 yh & 0x000f000fu, yh & 0x00f000f0u, s0[q], s1[q]);
                 }
             }
         }
