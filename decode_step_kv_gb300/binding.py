@@ -34,6 +34,8 @@ class FaDecodeError(RuntimeError):
 def load(build_if_missing: bool = True) -> ctypes.CDLL:
     """Load (building first if needed) the CUDA library."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             path = _build.build() if build_if_missing else _build.LIB
@@ -352,20 +354,26 @@ def fa_append_kv(k_new, v_new, k_cache, v_cache, v_scales, block_table, position
     _check(rc)
 
 
-def _take(name, t, dtype, shape=None):
-    """Device pointer (None for None) of a contiguous tensor of `dtype` on the
-    current device, of `shape` where one is given."""
+def _take(name, t, dtype, shape, dev):
+    """Device pointer (None for None) of a contiguous tensor of `dtype` and
+    `shape` (None: any) on device `dev`."""
     if t is None:
         return None
-    if t.dtype != dtype:
+    if (t.dtype is dtype and (shape is None or t.shape == shape) and t.get_device() == dev
+            and t.is_contiguous()):
+        return t.data_ptr()
+    if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+    if t.get_device() != dev:
         raise ValueError(f"{name} must be on the current CUDA device, got {t.device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _device():
+    """The current CUDA device (None without one: no tensor is on it)."""
+    return torch.cuda.current_device() if torch.cuda.is_initialized() else None
 
 
 def _cache_dims(name, k, block_table, batch):
@@ -383,25 +391,29 @@ def _cache_dims(name, k, block_table, batch):
     return k.shape[1], k.shape[2], block_table.shape[1], k.shape[0], tuple(k.shape[:3])
 
 
-def _stream_ptr(stream):
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+def _stream_ptr(stream, dev):
+    return (torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
 
 
-def _bytes(workspace):
-    return 0 if workspace is None else workspace.numel() * workspace.element_size()
+def _workspace(t, dev):
+    """Pointer and bytes of a workspace of any type."""
+    if t is None:
+        return None, 0
+    return _take("workspace", t, t.dtype, None, dev), t.numel() * t.element_size()
 
 
-def _int4_cache(name, k_codes, k_scales, v_codes, v_scales, block_table, batch):
+def _int4_cache(name, k_codes, k_scales, v_codes, v_scales, block_table, batch, dev):
     """Pointers and sizes of a 4-bit cache: (pointers, table, kv heads, page,
     max_blocks, num_blocks, rows, head_dim)."""
     hkv, page, blocks, total, rows = _cache_dims(name, k_codes, block_table, batch)
     half = k_codes.shape[3]
-    ptrs = (_take("k_codes", k_codes, torch.uint8),
-            _take("k_scales", k_scales, torch.float16, (*rows, half // 16)),
-            _take("v_codes", v_codes, torch.uint8, (*rows, half)),
-            _take("v_scales", v_scales, torch.float16, (*rows, half // 16)))
-    return (ptrs, _take("block_table", block_table, torch.int32), hkv, page, blocks, total, rows,
-            2 * half)
+    scales = (*rows, half // 16)
+    ptrs = (_take("k_codes", k_codes, torch.uint8, None, dev),
+            _take("k_scales", k_scales, torch.float16, scales, dev),
+            _take("v_codes", v_codes, torch.uint8, (*rows, half), dev),
+            _take("v_scales", v_scales, torch.float16, scales, dev))
+    return (ptrs, _take("block_table", block_table, torch.int32, None, dev), hkv, page, blocks,
+            total, rows, 2 * half)
 
 
 def fa_append_kv_int4(k_new, v_new, k_codes, k_scales, v_codes, v_scales, block_table, positions,
@@ -412,14 +424,16 @@ def fa_append_kv_int4(k_new, v_new, k_codes, k_scales, v_codes, v_scales, block_
     codes: uint8 [blocks, Hkv, page, D/2] with a block_table, or [B, Hkv, capacity, D/2];
     scales: fp16 [..., D/32] beside them."""
     B, T = k_new.shape[:2]
+    dev = _device()
     c, bt, hkv, page, blocks, total, _, D = _int4_cache("fa_append_kv_int4", k_codes, k_scales,
-                                                        v_codes, v_scales, block_table, B)
+                                                        v_codes, v_scales, block_table, B, dev)
     new = (B, T, hkv, D)
     _check(load().fa_append_kv_int4(
-        _take("k_new", k_new, torch.float32, new), _take("v_new", v_new, torch.float32, new), *c,
-        bt, _take("positions", positions, torch.int32, (B,)),
-        _take("n_new", n_new, torch.int32, (B,)), B, T, hkv, D, page, blocks, total,
-        _stream_ptr(stream)))
+        _take("k_new", k_new, torch.float32, new, dev),
+        _take("v_new", v_new, torch.float32, new, dev), *c, bt,
+        _take("positions", positions, torch.int32, (B,), dev),
+        _take("n_new", n_new, torch.int32, (B,), dev), B, T, hkv, D, page, blocks, total,
+        _stream_ptr(stream, dev)))
 
 
 def fa_gather_kv_int4(k_codes, k_scales, v_codes, v_scales, block_table, positions, k_out, v_out,
@@ -427,22 +441,25 @@ def fa_gather_kv_int4(k_codes, k_scales, v_codes, v_scales, block_table, positio
     """Rows positions[b] + i of a 4-bit cache as fp16 k_out / v_out [B, T, Hkv, D];
     `n_rows` [B] int32: only the first n_rows[b] of them."""
     B, T = k_out.shape[:2]
+    dev = _device()
     c, bt, hkv, page, blocks, total, _, D = _int4_cache("fa_gather_kv_int4", k_codes, k_scales,
-                                                        v_codes, v_scales, block_table, B)
+                                                        v_codes, v_scales, block_table, B, dev)
     to = (B, T, hkv, D)
     _check(load().fa_gather_kv_int4(
-        *c, bt, _take("positions", positions, torch.int32, (B,)),
-        _take("n_rows", n_rows, torch.int32, (B,)), _take("k_out", k_out, torch.float16, to),
-        _take("v_out", v_out, torch.float16, to), B, T, hkv, D, page, blocks, total,
-        _stream_ptr(stream)))
+        *c, bt, _take("positions", positions, torch.int32, (B,), dev),
+        _take("n_rows", n_rows, torch.int32, (B,), dev),
+        _take("k_out", k_out, torch.float16, to, dev),
+        _take("v_out", v_out, torch.float16, to, dev), B, T, hkv, D, page, blocks, total,
+        _stream_ptr(stream, dev)))
 
 
-def _queries(name, q, out, n_q_heads, head_dim):
+def _queries(name, q, out, n_q_heads, head_dim, dev):
     """(batch, queries, q pointer, out pointer) of q and out, [B, Hq, D] or [B, Tq, Hq, D]."""
-    if q.dim() not in (3, 4) or tuple(q.shape[-2:]) != (n_q_heads, head_dim):
+    shape = q.shape
+    if len(shape) not in (3, 4) or shape[-2:] != (n_q_heads, head_dim):
         raise ValueError(f"{name}: q must be [B, Hq, D] or [B, Tq, Hq, D]")
-    return (q.shape[0], 1 if q.dim() == 3 else q.shape[1], _take("q", q, torch.float16),
-            _take("out", out, torch.float16, q.shape))
+    return (shape[0], 1 if len(shape) == 3 else shape[1],
+            _take("q", q, torch.float16, None, dev), _take("out", out, torch.float16, shape, dev))
 
 
 def fa_decode_int4(q, k_codes, k_scales, v_codes, v_scales, block_table, seq_lens, n_q_heads,
@@ -452,15 +469,18 @@ def fa_decode_int4(q, k_codes, k_scales, v_codes, v_scales, block_table, seq_len
     sequence) or [B, Tq, Hq, D] (each sequence's last Tq tokens, causal).  `acc`
     (fp32, one value per cache row) also gets every key's softmax weight added, as in
     ``fa_decode_weights``.  The workspace is ``alloc_workspace_int4``'s."""
-    B, tq, qp, op = _queries("fa_decode_int4", q, out, n_q_heads, head_dim)
+    dev = _device()
+    B, tq, qp, op = _queries("fa_decode_int4", q, out, n_q_heads, head_dim, dev)
     c, bt, hkv, page, blocks, total, rows, D = _int4_cache("fa_decode_int4", k_codes, k_scales,
-                                                           v_codes, v_scales, block_table, B)
+                                                           v_codes, v_scales, block_table, B, dev)
     if hkv != n_kv_heads or D != head_dim:
         raise ValueError(f"fa_decode_int4: the cache holds {hkv} heads of {D}")
+    ws, ws_bytes = _workspace(workspace, dev)
     _check(load().fa_decode_int4(
-        qp, *c, bt, _take("seq_lens", seq_lens, torch.int32, (B,)), tq, n_q_heads, hkv, D, scale,
-        _take("window", window, torch.int32, (B,)), op, _take("acc", acc, torch.float32, rows), B,
-        page, blocks, total, _ptr(workspace), _bytes(workspace), _stream_ptr(stream)))
+        qp, *c, bt, _take("seq_lens", seq_lens, torch.int32, (B,), dev), tq, n_q_heads, hkv, D,
+        scale, _take("window", window, torch.int32, (B,), dev), op,
+        _take("acc", acc, torch.float32, rows, dev), B, page, blocks, total, ws, ws_bytes,
+        _stream_ptr(stream, dev)))
 
 
 def fa_decode_int4_workspace_size(batch, n_queries, n_q_heads, n_kv_heads, head_dim, max_kv_len,
@@ -484,20 +504,23 @@ def fa_decode_weights(q, k_cache, v_cache, v_scales, block_table, seq_lens, n_q_
     adds every key's softmax weight, summed over the queries and the query heads of its
     KV head, to `acc` (fp32, one value per cache row: the cache's shape without D).
     The workspace is ``alloc_workspace_weights``'s."""
+    dev = _device()
     hkv, page, blocks, total, rows = _cache_dims("fa_decode_weights", k_cache, block_table,
                                                  q.shape[0])
-    B, tq, qp, op = _queries("fa_decode_weights", q, out, n_q_heads, head_dim)
+    B, tq, qp, op = _queries("fa_decode_weights", q, out, n_q_heads, head_dim, dev)
     if hkv != n_kv_heads:
         raise ValueError(f"fa_decode_weights: the cache holds {hkv} heads")
     row = (*rows, head_dim)
+    ws, ws_bytes = _workspace(workspace, dev)
     _check(load().fa_decode_weights(
-        qp, _take("k_cache", k_cache, torch.float16, row),
-        _take("v_cache", v_cache, torch.float16 if v_scales is None else torch.int8, row),
-        _take("v_scales", v_scales, torch.float16, (*rows, head_dim // 32)),
-        _take("block_table", block_table, torch.int32),
-        _take("seq_lens", seq_lens, torch.int32, (B,)), tq, n_q_heads, hkv, head_dim, scale,
-        _take("window", window, torch.int32, (B,)), op, _take("acc", acc, torch.float32, rows), B,
-        page, blocks, total, _ptr(workspace), _bytes(workspace), _stream_ptr(stream)))
+        qp, _take("k_cache", k_cache, torch.float16, row, dev),
+        _take("v_cache", v_cache, torch.float16 if v_scales is None else torch.int8, row, dev),
+        _take("v_scales", v_scales, torch.float16, (*rows, head_dim // 32), dev),
+        _take("block_table", block_table, torch.int32, None, dev),
+        _take("seq_lens", seq_lens, torch.int32, (B,), dev), tq, n_q_heads, hkv, head_dim, scale,
+        _take("window", window, torch.int32, (B,), dev), op,
+        _take("acc", acc, torch.float32, rows, dev), B, page, blocks, total, ws, ws_bytes,
+        _stream_ptr(stream, dev)))
 
 
 def fa_decode_weights_workspace_size(batch, n_queries, n_q_heads, n_kv_heads, head_dim, max_kv_len,
@@ -521,20 +544,23 @@ def fa_evict_kv(k_cache, v_cache, acc, block_table, seq_lens, new_lens, *, budge
     order to the front.  fp16 caches; with v_scales, int8 V; with both scales, 4-bit K and V
     (uint8 codes).  Writes new_lens [B] and kept [B, Hkv, budget] (int32)."""
     B = seq_lens.shape[0]
+    dev = _device()
     hkv, page, blocks, total, rows = _cache_dims("fa_evict_kv", k_cache, block_table, B)
     int4 = k_scales is not None
     D = k_cache.shape[3] * (2 if int4 else 1)
     scales = (*rows, D // 32)
+    v_type = torch.uint8 if int4 else torch.float16 if v_scales is None else torch.int8
     _check(load().fa_evict_kv(
-        _take("k_cache", k_cache, torch.uint8 if int4 else torch.float16),
-        _take("v_cache", v_cache, torch.uint8 if int4 else torch.float16 if v_scales is None
-              else torch.int8, k_cache.shape),
-        _take("k_scales", k_scales, torch.float16, scales),
-        _take("v_scales", v_scales, torch.float16, scales),
-        _take("acc", acc, torch.float32, rows), _take("block_table", block_table, torch.int32),
-        _take("seq_lens", seq_lens, torch.int32), _take("new_lens", new_lens, torch.int32, (B,)),
-        _take("kept", kept, torch.int32, (B, hkv, budget)), budget, n_sink, n_recent, B, hkv, D,
-        page, blocks, total, _stream_ptr(stream)))
+        _take("k_cache", k_cache, torch.uint8 if int4 else torch.float16, None, dev),
+        _take("v_cache", v_cache, v_type, k_cache.shape, dev),
+        _take("k_scales", k_scales, torch.float16, scales, dev),
+        _take("v_scales", v_scales, torch.float16, scales, dev),
+        _take("acc", acc, torch.float32, rows, dev),
+        _take("block_table", block_table, torch.int32, None, dev),
+        _take("seq_lens", seq_lens, torch.int32, (B,), dev),
+        _take("new_lens", new_lens, torch.int32, (B,), dev),
+        _take("kept", kept, torch.int32, (B, hkv, budget), dev), budget, n_sink, n_recent, B, hkv,
+        D, page, blocks, total, _stream_ptr(stream, dev)))
 
 
 def fa_gather_kv_debug(cache, row_bytes, block_table, b, n_kv_heads, page_size,

@@ -6,18 +6,22 @@
 // ones with the largest running totals; move the kept rows, in order, to the
 // front of the cache.
 //
-// One thread-block cluster per (sequence, KV head) does both parts in one
-// launch.
+// A thread-block cluster per (sequence, KV head) selects and moves what needs an
+// order; a second kernel moves the rest with every SM (within the first when
+// there is little of it).
 //   Selection: a radix selection of the k-th largest total (11 + 11 + 10 bits
 //   of the order-preserving integer), each CTA counting its share of the
 //   tokens, the counts summed through distributed shared memory; then every
 //   warp emits its tokens' kept indices at the rank that the warps before it
-//   leave.  Ties go to the lowest index.
-//   Move: rows go down in place (a kept row's new index is never above its
-//   old one).  The cluster works in rounds of consecutive kept rows: every CTA
-//   reads its rows into shared memory, a cluster barrier, every CTA writes
-//   them.  The rows that round q overwrites lie below the sources of all later
-//   rounds, so a round's reads need not wait for the writes before it.
+//   leave.  Ties go to the lowest index.  A CTA keeps its share of the totals in
+//   shared memory when it fits (24576 tokens), so they are read once.
+//   Move: rows go down in place (a kept row's new index is never above its old
+//   one).  A write to row j only clobbers a source when token j itself is kept,
+//   so order matters only among the kept tokens below the budget.  Those move
+//   first, in rounds: every CTA of the cluster reads its rows of the round into
+//   shared memory, a cluster barrier, every CTA writes them (what a round
+//   overwrites lies below the sources of all later rounds).  After them, the
+//   kept tokens from the budget on move in any order.
 // Bound by HBM: each kept row that changes its place is read and written once.
 #include "fa_common.cuh"
 
@@ -28,7 +32,10 @@ constexpr int THREADS = 512;
 constexpr int WARPS = THREADS / 32;
 constexpr int BINS = 2048;
 constexpr int MAX_CTAS = 8;              // CTAs per cluster
-constexpr int STAGE_BYTES = 96 * 1024;   // rows in flight per CTA: two CTAs per SM
+constexpr int STAGE_BYTES = 96 * 1024;   // totals, then rows in flight, of a CTA: two CTAs per SM
+constexpr int HELD = STAGE_BYTES / 4;    // totals a CTA holds
+constexpr int ROUND_ROWS = THREADS;      // most rows a CTA stages per round
+constexpr double FUSED_BYTES = 4 << 20;  // rows to move up to which one kernel does it all
 
 struct Args {
     char *a[4];          // K, V, K scales, V scales (NULL: none)
@@ -36,7 +43,9 @@ struct Args {
     float *acc;
     int *new_lens, *kept;
     int budget, sink, recent;
+    int lg_page;         // log2 of page_size, or -1
     int rows;            // rows staged per CTA and round
+    int fused;           // the cluster kernel also moves the rows from the budget on
 };
 
 // Totals as integers in the same order: NaN counts as -inf, -0 as 0.
@@ -50,10 +59,16 @@ __device__ __forceinline__ unsigned order_key(float x)
     return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
-__device__ __forceinline__ long long row_of(const Params &p, int b, int kv, int t)
+// Cache row of token t of (b, kv); -1 for a block id out of range.
+__device__ __forceinline__ long long row_of(const Params &p, const Args &x, int b, int kv, int t)
 {
-    const long long r = tc::tile_row(p, b, kv, t - t % tc::TILE);
-    return r < 0 ? -1 : r + t % tc::TILE;
+    if (!p.bt)
+        return ((long long)b * p.Hkv + kv) * p.cap + t;
+    const int page = x.lg_page >= 0 ? t >> x.lg_page : t / p.page_size;
+    const int blk = __ldg(p.bt + (long long)b * p.max_blocks + page);
+    if (blk < 0 || blk >= p.num_blocks)
+        return -1;
+    return ((long long)blk * p.Hkv + kv) * p.page_size + (t - page * p.page_size);
 }
 
 __device__ __forceinline__ unsigned ld_cluster(uint32_t a)
@@ -61,6 +76,80 @@ __device__ __forceinline__ unsigned ld_cluster(uint32_t a)
     unsigned v;
     asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
     return v;
+}
+
+// Places of up to ROUND_ROWS rows: src -1 where nothing is to be moved.
+struct Places {
+    long long src[ROUND_ROWS], dst[ROUND_ROWS];
+};
+
+// Rows pl.src -> pl.dst of one array, by the whole CTA, in pieces, DEPTH of them in
+// flight per thread.  No source may be another row's destination.
+template <typename Piece, int DEPTH>
+__device__ __forceinline__ void copy_rows(char *base, int rb, const Places &pl, int nr)
+{
+    const int lg = 31 - __clz(rb / static_cast<int>(sizeof(Piece)));
+    const int total = nr << lg;
+    for (int i0 = threadIdx.x; i0 < total; i0 += DEPTH * blockDim.x) {
+        Piece v[DEPTH];
+#pragma unroll
+        for (int q = 0; q < DEPTH; ++q) {
+            const int i = i0 + q * blockDim.x;
+            if (i < total && pl.src[i >> lg] >= 0)
+                v[q] = __ldcs(reinterpret_cast<const Piece *>(base + pl.src[i >> lg] * rb) +
+                              (i & ((1 << lg) - 1)));
+        }
+#pragma unroll
+        for (int q = 0; q < DEPTH; ++q) {
+            const int i = i0 + q * blockDim.x;
+            if (i < total && pl.src[i >> lg] >= 0)
+                reinterpret_cast<Piece *>(base + pl.dst[i >> lg] * rb)[i & ((1 << lg) - 1)] = v[q];
+        }
+    }
+}
+
+// Kept rows r0 .. r0 + nr - 1 whose token lies at or above the budget.
+template <int DEPTH>
+__device__ __forceinline__ void move_far(const Params &p, const Args &x, int b, int kv,
+                                         const int *kept, int r0, int nr, Places &pl)
+{
+    __syncthreads();                              // pl is free
+    if (threadIdx.x < nr) {
+        const int j = r0 + threadIdx.x, t = __ldcg(kept + j);
+        const long long s = t >= x.budget ? row_of(p, x, b, kv, t) : -1;
+        const long long d = s >= 0 ? row_of(p, x, b, kv, j) : -1;
+        pl.src[threadIdx.x] = d >= 0 ? s : -1;
+        pl.dst[threadIdx.x] = d;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int a = 0; a < 4; ++a) {
+        if (!x.a[a])
+            continue;
+        if (x.row_bytes[a] >= 16)
+            copy_rows<uint4, DEPTH>(x.a[a], x.row_bytes[a], pl, nr);
+        else
+            copy_rows<uint2, DEPTH>(x.a[a], x.row_bytes[a], pl, nr);
+    }
+}
+
+constexpr int FAR_THREADS = 256;
+constexpr int FAR_ROWS = 64;             // kept rows per CTA
+__global__ void __launch_bounds__(FAR_THREADS) evict_far_kernel(const Params p, const Args x)
+{
+    __shared__ Places pl;
+    const int chunks = (x.budget + FAR_ROWS - 1) / FAR_ROWS;
+    const int unit = blockIdx.x / chunks;
+    const int b = unit / p.Hkv, kv = unit % p.Hkv;
+    int lo, n;
+    attended_range(p, b, lo, n, false);
+    // every CTA waits: what follows on the stream must find both kernels done
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (n <= x.budget)
+        return;
+    const int r0 = blockIdx.x % chunks * FAR_ROWS;
+    move_far<8>(p, x, b, kv, x.kept + (long long)unit * x.budget, r0, min(FAR_ROWS, x.budget - r0),
+                pl);
 }
 
 template <int N>
@@ -78,7 +167,9 @@ __global__ void __launch_bounds__(THREADS, 2) evict_kernel(const Params p, const
     __shared__ unsigned cnt[WARPS][2];
     __shared__ unsigned wsum[WARPS];
     __shared__ unsigned found[2];
+    __shared__ Places pl;
     extern __shared__ __align__(128) unsigned char stage[];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     const int cs = p.cl_ctas;
     uint32_t rank = 0;
@@ -87,12 +178,6 @@ __global__ void __launch_bounds__(THREADS, 2) evict_kernel(const Params p, const
     const int unit = blockIdx.x / cs;
     const int b = unit / p.Hkv, kv = unit % p.Hkv;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    auto sync_all = [&] {
-        if (cs > 1)
-            tc::cluster_sync();
-        else
-            __syncthreads();
-    };
 
     int lo, n;
     attended_range(p, b, lo, n, kv == 0 && rank == 0 && tid == 0);
@@ -105,20 +190,57 @@ __global__ void __launch_bounds__(THREADS, 2) evict_kernel(const Params p, const
         return;                                   // the whole cluster
     }
 
-    // ---- the k-th largest total of the m tokens between sink and recent
+    // ---- the k-th largest total of the m tokens between sink and recent.  When one
+    // CTA holds them all, every CTA of the cluster selects by itself: that costs
+    // a few more passes over shared memory and saves six cluster barriers.
     const int m = n - x.sink - x.recent;
     const int k = x.budget - x.sink - x.recent;
-    const int gw = rank * WARPS + warp, nw = cs * WARPS;
+    const bool solo = m <= HELD;
+    const int sel = solo ? 1 : cs;                // CTAs that share the selection
+    const int sr = solo ? 0 : rank;
+    auto sync_sel = [&] {
+        if (sel > 1)
+            tc::cluster_sync();
+        else
+            __syncthreads();
+    };
+    auto sync_all = [&] {
+        if (cs > 1)
+            tc::cluster_sync();
+        else
+            __syncthreads();
+    };
+    const int gw = sr * WARPS + warp, nw = sel * WARPS;
     const int w0 = x.sink + static_cast<int>((long long)m * gw / nw);
     const int w1 = x.sink + static_cast<int>((long long)m * (gw + 1) / nw);
-    auto key_at = [&](int t) -> unsigned {
-        const long long r = row_of(p, b, kv, t);
+    auto total_at = [&](int t) -> float {
+        const long long r = row_of(p, x, b, kv, t);
         if (r < 0) {
             flag(FA_STATUS_BAD_BLOCK);
-            return order_key(-INFINITY);
+            return -INFINITY;
         }
-        return order_key(__ldcg(x.acc + r));
+        return __ldcg(x.acc + r);
     };
+    // this CTA's totals in shared memory, at the tokens' offsets from its first
+    const int c0 = x.sink + static_cast<int>((long long)m * (sr * WARPS) / nw);
+    const int c1 = x.sink + static_cast<int>((long long)m * (sr * WARPS + WARPS) / nw);
+    const bool held = c1 - c0 <= HELD;
+    float *tot = reinterpret_cast<float *>(stage);
+    if (held) {
+        constexpr int U = 8;
+        for (int t0 = w0 + lane; t0 < w1; t0 += 32 * U) {
+            float v[U];
+#pragma unroll
+            for (int q = 0; q < U; ++q)
+                v[q] = t0 + 32 * q < w1 ? total_at(t0 + 32 * q) : 0.f;
+#pragma unroll
+            for (int q = 0; q < U; ++q)
+                if (t0 + 32 * q < w1)
+                    tot[t0 + 32 * q - c0] = v[q];
+        }
+        __syncwarp();                             // a warp reads its own tokens only
+    }
+    auto key_at = [&](int t) { return order_key(held ? tot[t - c0] : total_at(t)); };
     unsigned thr = 0xffffffffu;                   // keys above thr are kept ...
     unsigned rem = 0;                             // ... and the first rem equal to it
     if (k > 0) {
@@ -135,17 +257,17 @@ __global__ void __launch_bounds__(THREADS, 2) evict_kernel(const Params p, const
                 if (pass == 0 || ((u ^ thr) >> (shift + bits)) == 0)
                     atomicAdd(&hist[(u >> shift) & ((1u << bits) - 1)], 1u);
             }
-            sync_all();
+            sync_sel();
             constexpr int PER = BINS / THREADS;
             unsigned c[PER], sum = 0;             // this thread's bins, from the top
 #pragma unroll
             for (int q = 0; q < PER; ++q) {
                 const int bin = BINS - 1 - (tid * PER + q);
                 c[q] = hist[bin];
-                if (cs > 1) {
+                if (sel > 1) {
                     const uint32_t a = smem_u32(&hist[bin]);
                     c[q] = 0;
-                    for (int r = 0; r < cs; ++r)
+                    for (int r = 0; r < sel; ++r)
                         c[q] += ld_cluster(tc::cl_map(a, r));
                 }
                 sum += c[q];
@@ -171,7 +293,7 @@ __global__ void __launch_bounds__(THREADS, 2) evict_kernel(const Params p, const
                 }
                 above += c[q];
             }
-            sync_all();                           // counts read by all before they are cleared
+            sync_sel();                           // counts read by all before they are cleared
             thr |= found[0] << shift;
             rem -= found[1];
         }
@@ -188,11 +310,11 @@ __global__ void __launch_bounds__(THREADS, 2) evict_kernel(const Params p, const
         cnt[warp][0] = n_gt;
         cnt[warp][1] = n_eq;
     }
-    sync_all();
+    sync_sel();
     unsigned gt = 0, eq = 0;
     for (int i = lane; i < gw; i += 32) {
         const uint32_t a = smem_u32(&cnt[i % WARPS][0]);
-        const uint32_t at = cs > 1 ? tc::cl_map(a, i / WARPS) : a;
+        const uint32_t at = sel > 1 ? tc::cl_map(a, i / WARPS) : a;
         gt += ld_cluster(at);
         eq += ld_cluster(at + 4);
     }
@@ -211,51 +333,85 @@ __global__ void __launch_bounds__(THREADS, 2) evict_kernel(const Params p, const
         const unsigned km = __ballot_sync(0xffffffffu, keep);
         const unsigned to = at + __popc(km & below);
         if (keep && to < static_cast<unsigned>(x.budget))
-            kept[to] = t;
+            kept[to] = t;                         // solo: the same values by every CTA
         at += __popc(km);
         eq += __popc(eqm);
     }
-    for (int j = rank * THREADS + tid; j < x.sink; j += cs * THREADS)
+    for (int j = sr * THREADS + tid; j < x.sink; j += sel * THREADS)
         kept[j] = j;
-    for (int j = rank * THREADS + tid; j < x.recent; j += cs * THREADS)
+    for (int j = sr * THREADS + tid; j < x.recent; j += sel * THREADS)
         kept[x.budget - x.recent + j] = n - x.recent + j;
-    sync_all();                                   // kept[] is complete
+    sync_sel();                                   // kept[] is complete
 
-    // ---- move, in rounds of cs * rows kept rows
+    // ---- totals, in rounds: all of a round's reads before its writes
+    for (int j0 = x.sink; j0 < x.budget; j0 += cs * 4 * THREADS) {
+        const int r0 = j0 + rank * 4 * THREADS + tid;
+        float v[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int j = r0 + q * THREADS;
+            long long src = -1;
+            if (j < x.budget)
+                src = row_of(p, x, b, kv, __ldcg(kept + j));
+            v[q] = src >= 0 ? __ldcg(x.acc + src) : 0.f;
+        }
+        sync_all();
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int j = r0 + q * THREADS;
+            const long long dst = j < x.budget ? row_of(p, x, b, kv, j) : -1;
+            if (dst >= 0)
+                x.acc[dst] = v[q];
+        }
+    }
+    // the totals of the rows behind the budget start again from zero
+    for (int t = x.budget + rank * THREADS + tid; t < n; t += cs * THREADS) {
+        const long long r = row_of(p, x, b, kv, t);
+        if (r >= 0)
+            x.acc[r] = 0.f;
+    }
+
+    // ---- rows of kept tokens below the budget, in rounds of cs * rows: kept[]
+    // ascends, so they are its first n_near entries
+    int n_near = x.sink;
+    for (int step = x.budget - x.sink; step > 0;) {       // first entry >= budget
+        const int half = step / 2;
+        if (__ldcg(kept + n_near + half) < x.budget) {
+            n_near += half + 1;
+            step -= half + 1;
+        } else {
+            step = half;
+        }
+    }
     const int R = x.rows;
-    for (int j0 = x.sink; j0 < x.budget; j0 += cs * R) {
+    for (int j0 = x.sink; j0 < n_near; j0 += cs * R) {
         const int r0 = j0 + rank * R;
-        const int nr = min(R, x.budget - r0);     // <= 0 for the last CTAs of the last round
+        const int nr = max(min(R, n_near - r0), 0);   // 0 for the last CTAs of the last round
+        if (tid < nr) {
+            const int j = r0 + tid, t = __ldcg(kept + j);
+            const long long s = t == j ? -1 : row_of(p, x, b, kv, t);
+            const long long d = s >= 0 ? row_of(p, x, b, kv, j) : -1;
+            pl.src[tid] = d >= 0 ? s : -1;
+            pl.dst[tid] = d;
+        }
+        __syncthreads();
         uint32_t off = smem_u32(stage);
-        float av[4];                              // R <= 4 * THREADS
 #pragma unroll
         for (int a = 0; a < 4; ++a) {
             if (!x.a[a])
                 continue;
             const int rb = x.row_bytes[a];
             const int lg = 31 - __clz(rb >= 16 ? rb / 16 : 1);
-            for (int i = tid; i < (nr > 0 ? nr << lg : 0); i += THREADS) {
-                const int j = r0 + (i >> lg), c = i & ((1 << lg) - 1);
-                const int t = __ldcg(kept + j);
-                const long long src = t == j ? -1 : row_of(p, b, kv, t);
+            for (int i = tid; i < nr << lg; i += THREADS) {
+                const long long src = pl.src[i >> lg];
                 if (src < 0)
                     continue;
                 if (rb >= 16)
-                    cp<16>(off + i * 16, x.a[a] + src * rb + c * 16);
+                    cp<16>(off + i * 16, x.a[a] + src * rb + (i & ((1 << lg) - 1)) * 16);
                 else
                     cp<8>(off + i * 8, x.a[a] + src * rb);
             }
             off += R * rb;
-        }
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const int i = tid + q * THREADS;
-            av[q] = 0.f;
-            if (i < nr) {
-                const long long src = row_of(p, b, kv, __ldcg(kept + r0 + i));
-                if (src >= 0)
-                    av[q] = __ldcg(x.acc + src);
-            }
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
         sync_all();                               // every read of the round is done
@@ -266,40 +422,26 @@ __global__ void __launch_bounds__(THREADS, 2) evict_kernel(const Params p, const
                 continue;
             const int rb = x.row_bytes[a];
             const int lg = 31 - __clz(rb >= 16 ? rb / 16 : 1);
-            for (int i = tid; i < (nr > 0 ? nr << lg : 0); i += THREADS) {
-                const int j = r0 + (i >> lg), c = i & ((1 << lg) - 1);
-                const int t = __ldcg(kept + j);
-                if (t == j || row_of(p, b, kv, t) < 0)
+            for (int i = tid; i < nr << lg; i += THREADS) {
+                if (pl.src[i >> lg] < 0)
                     continue;
-                const long long dst = row_of(p, b, kv, j);
-                if (dst < 0)
-                    continue;
+                char *dst = x.a[a] + pl.dst[i >> lg] * rb;
                 if (rb >= 16)
-                    *reinterpret_cast<uint4 *>(x.a[a] + dst * rb + c * 16) =
+                    reinterpret_cast<uint4 *>(dst)[i & ((1 << lg) - 1)] =
                         *reinterpret_cast<const uint4 *>(stage + off + i * 16);
                 else
-                    *reinterpret_cast<uint2 *>(x.a[a] + dst * rb) =
+                    *reinterpret_cast<uint2 *>(dst) =
                         *reinterpret_cast<const uint2 *>(stage + off + i * 8);
             }
             off += R * rb;
         }
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const int i = tid + q * THREADS;
-            if (i < nr) {
-                const long long dst = row_of(p, b, kv, r0 + i);
-                if (dst >= 0)
-                    x.acc[dst] = av[q];
-            }
-        }
-        __syncthreads();                          // the stage is free again
+        __syncthreads();                          // the stage and the places are free again
     }
-    // the totals of the rows behind the budget start again from zero
-    for (int t = x.budget + rank * THREADS + tid; t < n; t += cs * THREADS) {
-        const long long r = row_of(p, b, kv, t);
-        if (r >= 0)
-            x.acc[r] = 0.f;
-    }
+    // ---- the others; their places may be sources of the rounds above, all read
+    // before the last round's barrier
+    if (x.fused)
+        for (int r0 = n_near + rank * FAR_ROWS; r0 < x.budget; r0 += cs * FAR_ROWS)
+            move_far<4>(p, x, b, kv, kept, r0, min(FAR_ROWS, x.budget - r0), pl);
 }
 
 }  // namespace ev
@@ -382,8 +524,12 @@ extern "C" FA_API int fa_evict_kv(void *k_cache, void *v_cache, void *k_scales, 
     for (int a = 0; a < 4; ++a)
         total += x.a[a] ? x.row_bytes[a] : 0;
     x.rows = ev::STAGE_BYTES / total / 16 * 16;
-    if (x.rows > 4 * ev::THREADS)
-        x.rows = 4 * ev::THREADS;
+    if (x.rows > ev::ROUND_ROWS)
+        x.rows = ev::ROUND_ROWS;
+    x.lg_page = -1;
+    for (int lg = 4; lg < 31; ++lg)
+        if (paged && page_size == 1 << lg)
+            x.lg_page = lg;
     Params p = {};
     p.bt = block_table;
     p.seq_lens = seq_lens;
@@ -393,13 +539,15 @@ extern "C" FA_API int fa_evict_kv(void *k_cache, void *v_cache, void *k_scales, 
     p.max_blocks = max_blocks_per_seq;
     p.num_blocks = num_blocks;
     p.cap = cap;
-    // the largest cluster that still leaves every unit resident (two CTAs per SM)
     const long long units = (long long)batch * n_kv_heads;
+    x.fused = (double)units * budget * total <= ev::FUSED_BYTES;
+    // the largest cluster that still leaves every unit resident (two CTAs per SM)
     int cs = ev::MAX_CTAS;
     while (cs > 1 && units * cs > 2ll * sms)
         cs /= 2;
     p.cl_ctas = cs;
-    if (units * cs > 0x7fffffffll)
+    const long long far_chunks = (budget + (long long)ev::FAR_ROWS - 1) / ev::FAR_ROWS;
+    if (units * cs > 0x7fffffffll || units * far_chunks > 0x7fffffffll)
         return fail(FA_ERR_LAYOUT, "%s: too many rows", name);
     static std::mutex mu;
     static bool done[64] = {false};
@@ -428,6 +576,20 @@ extern "C" FA_API int fa_evict_kv(void *k_cache, void *v_cache, void *k_scales, 
         cfg.attrs = attr;
         cfg.numAttrs = 1;
         e = cudaLaunchKernelEx(&cfg, ev::evict_kernel, p, x);
+        if (e == cudaSuccess)
+            e = cudaGetLastError();
+    }
+    if (e == cudaSuccess && !x.fused) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(static_cast<unsigned>(units * far_chunks));
+        cfg.blockDim = dim3(ev::FAR_THREADS);
+        cfg.stream = static_cast<cudaStream_t>(stream);
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        e = cudaLaunchKernelEx(&cfg, ev::evict_far_kernel, p, x);
         if (e == cudaSuccess)
             e = cudaGetLastError();
     }

@@ -31,10 +31,13 @@ __device__ __forceinline__ __half block_scale(float amax)
     return __float2half_rn(q);
 }
 
-// rint(x / s) clamped to [-7, 7], of the exact quotient (ties to even): the
-// product with 1/s is at most one off, and x - c*s is exact where it decides.
+// rint(x / s) clamped to [-7, 7], of the exact quotient (ties to even); 0 for a
+// NaN.  The product with 1/s is at most one off, and x - c*s is exact where it
+// decides.
 __device__ __forceinline__ int block_code(float x, float s, float inv)
 {
+    if (x != x)
+        return 0;
     float c = rintf(x * inv);
     c = fminf(fmaxf(c, -7.f), 7.f);
     const float e2 = 2.f * fmaf(-c, s, x);
@@ -44,120 +47,146 @@ __device__ __forceinline__ int block_code(float x, float s, float inv)
     return static_cast<int>(fminf(fmaxf(c, -7.f), 7.f));
 }
 
-// Where the token of row (b, i) of an append or gather lives: cache row of
-// KV head kv, or -1 (flagged when `report`).
-__device__ __forceinline__ long long token_row(const Params &p, int b, long long i, int kv,
+// Where row i of sequence b of an append or gather lives: the cache row of KV head
+// kv, or -1 (flagged when `report`).  lg_page: log2 of the page size, or -1.
+__device__ __forceinline__ long long token_row(const Params &p, int lg_page, int b, int i, int kv,
                                                bool report)
 {
-    const long long t = p.seq_lens[b] + i;                // positions
-    if (p.seq_lens[b] < 0 || t >= p.cap) {
+    const int pos = p.seq_lens[b];                        // positions
+    const long long t = (long long)pos + i;
+    if (pos < 0 || t >= p.cap) {
         if (report)
             flag(FA_STATUS_POS_RANGE);
         return -1;
     }
-    const long long row = tc::tile_row(p, b, kv, static_cast<int>(t / TILE * TILE));
-    if (row < 0) {
+    const int tok = static_cast<int>(t);
+    if (!p.bt)
+        return ((long long)b * p.Hkv + kv) * p.cap + tok;
+    const int page = lg_page >= 0 ? tok >> lg_page : tok / p.page_size;
+    const int blk = p.bt[(long long)b * p.max_blocks + page];
+    if (blk < 0 || blk >= p.num_blocks) {
         if (report)
             flag(FA_STATUS_BAD_BLOCK);
         return -1;
     }
-    return row + t % TILE;
+    return ((long long)blk * p.Hkv + kv) * p.page_size + (tok - page * p.page_size);
 }
 
-// One thread per word (8 elements), 4 neighbouring lanes per block; y = 0
-// writes K, y = 1 writes V.  Reads each element once and writes whole rows;
-// bound by HBM.
-__global__ void __launch_bounds__(256) append_kernel(const Params p, const float *k_new,
-                                                     const float *v_new, unsigned *k_codes,
-                                                     __half *k_scales, unsigned *v_codes,
-                                                     __half *v_scales, const int *n_new, int T,
-                                                     int words, long long total)
+// A call's rows: sequence b = blockIdx.y, K or V = blockIdx.z, and along x one
+// thread per word (8 elements), so 4 neighbouring lanes hold a block.
+struct RowArgs {
+    int T, n_words;       // rows per sequence; words per sequence (T * Hkv * D / 8)
+    int lg_page;
+    const int *count;     // real rows per sequence, or NULL
+};
+
+// Reads each element once and writes whole rows: bound by HBM as long as an
+// element takes few instructions.  Hence the code by one fused multiply-add: with
+// 1.5 * 2^23 + 8 added, the sum's low four bits are the nibble of the rounded
+// x / s; where x - c*s does not confirm it (a tie, a quotient next to one, a NaN,
+// a scale rounded so far down that codes are cut off) the thread takes the exact
+// form.
+template <int D>
+__global__ void __launch_bounds__(256) append_kernel(const Params p, const RowArgs a,
+                                                     const float *k_new, const float *v_new,
+                                                     unsigned *k_codes, __half *k_scales,
+                                                     unsigned *v_codes, __half *v_scales)
 {
-    const long long idx = (long long)blockIdx.x * blockDim.x + threadIdx.x;
-    if (idx >= total)                       // whole groups of 4 lanes: words is a multiple of 4
+    constexpr int W = D / 8, NJ = D / 32;
+    const unsigned idx = blockIdx.x * blockDim.x + threadIdx.x;
+    if (idx >= a.n_words)                   // whole groups of 4 lanes
         return;
-    const int w = static_cast<int>(idx % words);
-    const long long r = idx / words;        // (b, i, kv)
-    const int kv = static_cast<int>(r % p.Hkv);
-    const long long bi = r / p.Hkv;
-    const int b = static_cast<int>(bi / T);
-    const int i = static_cast<int>(bi % T);
-    if (n_new && i >= n_new[b])
+    const int b = blockIdx.y, w = idx % W;
+    const unsigned r = idx / W;             // (i, kv)
+    const int i = r / p.Hkv, kv = r - i * p.Hkv;
+    if (a.count && i >= a.count[b])
         return;
-    const bool isv = blockIdx.y != 0;
-    const long long row = token_row(p, b, i, kv, !isv && w == 0);
-    if (row < 0)
-        return;
-    const float4 *src = reinterpret_cast<const float4 *>((isv ? v_new : k_new) + idx * 8);
+    const bool isv = blockIdx.z != 0;
+    const float4 *src = reinterpret_cast<const float4 *>(
+        (isv ? v_new : k_new) + ((long long)b * a.n_words + idx) * 8);
     float x[8];
     {
-        const float4 a = __ldcs(src), c = __ldcs(src + 1);
-        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-        x[4] = c.x; x[5] = c.y; x[6] = c.z; x[7] = c.w;
+        const float4 y = __ldcs(src), z = __ldcs(src + 1);
+        x[0] = y.x; x[1] = y.y; x[2] = y.z; x[3] = y.w;
+        x[4] = z.x; x[5] = z.y; x[6] = z.z; x[7] = z.w;
     }
+    const long long row = token_row(p, a.lg_page, b, i, kv, !isv && w == 0);
+    if (row < 0)
+        return;
     float amax = 0.f;
 #pragma unroll
-    for (int n = 0; n < 8; ++n) {
-        x[n] = x[n] == x[n] ? fminf(fmaxf(x[n], -X_MAX), X_MAX) : 0.f;
-        amax = fmaxf(amax, fabsf(x[n]));
-    }
+    for (int n = 0; n < 8; ++n)
+        amax = fmaxf(amax, fabsf(x[n]));    // a NaN is passed over
     const unsigned quad = 0xfu << (threadIdx.x & 28);     // the block's 4 lanes took this path
     amax = fmaxf(amax, __shfl_xor_sync(quad, amax, 1));
     amax = fmaxf(amax, __shfl_xor_sync(quad, amax, 2));
-    const __half sh = block_scale(amax);
+    const __half sh = block_scale(fminf(amax, X_MAX));
     const float s = __half2float(sh);
     unsigned word = 0x88888888u;
     if (s > 0.f) {
-        const float inv = 1.f / s;
+        const float inv = __fdividef(1.f, s), hs = 0.5f * s;
+        constexpr float MAGIC = 12582920.f;               // 1.5 * 2^23 + 8
+        bool sure = amax * inv < 7.4f;
         word = 0;
 #pragma unroll
-        for (int n = 0; n < 8; ++n)
-            word |= static_cast<unsigned>(block_code(x[n], s, inv) + 8) << (4 * n);
+        for (int n = 0; n < 8; ++n) {
+            const float v = fmaf(x[n], inv, MAGIC);
+            sure = sure && fabsf(fmaf(MAGIC - v, s, x[n])) < hs;
+            word |= (__float_as_uint(v) & 15u) << (4 * n);
+        }
+        if (!sure) {
+            word = 0;
+#pragma unroll
+            for (int n = 0; n < 8; ++n)
+                word |= static_cast<unsigned>(block_code(x[n], s, inv) + 8) << (4 * n);
+        }
     }
-    const int j = w >> 2, o = w & 3, nj = words >> 2;
-    (isv ? v_codes : k_codes)[row * words + o * nj + j] = word;
+    const int j = w >> 2, o = w & 3;
+    (isv ? v_codes : k_codes)[row * W + o * NJ + j] = word;
     if (o == 0)
-        (isv ? v_scales : k_scales)[row * nj + j] = sh;
+        (isv ? v_scales : k_scales)[row * NJ + j] = sh;
 }
 
 // The inverse: rows back as fp16 values c * s (each product rounded once).  A
-// token outside the cache or in an unmapped block reads as zeros; rows i >=
-// n_rows[b] are left as they were.
-__global__ void __launch_bounds__(256) gather_kernel(const Params p, const unsigned *k_codes,
+// token outside the cache or in an unmapped block reads as zeros; rows behind the
+// count are left as they were.
+template <int D>
+__global__ void __launch_bounds__(256) gather_kernel(const Params p, const RowArgs a,
+                                                     const unsigned *k_codes,
                                                      const __half *k_scales,
                                                      const unsigned *v_codes,
-                                                     const __half *v_scales, const int *n_rows,
-                                                     __half *k_out, __half *v_out, int T,
-                                                     int words, long long total)
+                                                     const __half *v_scales, __half *k_out,
+                                                     __half *v_out)
 {
-    const long long idx = (long long)blockIdx.x * blockDim.x + threadIdx.x;
-    if (idx >= total)
+    constexpr int W = D / 8, NJ = D / 32;
+    const unsigned idx = blockIdx.x * blockDim.x + threadIdx.x;
+    if (idx >= a.n_words)
         return;
-    const int w = static_cast<int>(idx % words);
-    const long long r = idx / words;
-    const int kv = static_cast<int>(r % p.Hkv);
-    const long long bi = r / p.Hkv;
-    const int b = static_cast<int>(bi / T);
-    const int i = static_cast<int>(bi % T);
-    if (n_rows && i >= n_rows[b])
+    const int b = blockIdx.y, w = idx % W;
+    const unsigned r = idx / W;
+    const int i = r / p.Hkv, kv = r - i * p.Hkv;
+    if (a.count && i >= a.count[b])
         return;
-    const bool isv = blockIdx.y != 0;
-    const long long row = token_row(p, b, i, kv, !isv && w == 0);
-    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    const bool isv = blockIdx.z != 0;
+    const long long row = token_row(p, a.lg_page, b, i, kv, !isv && w == 0);
+    uint4 out = make_uint4(0u, 0u, 0u, 0u);
     if (row >= 0) {
-        const int j = w >> 2, o = w & 3, nj = words >> 2;
-        const unsigned word = __ldg((isv ? v_codes : k_codes) + row * words + o * nj + j);
-        const float s = __half2float(__ldg((isv ? v_scales : k_scales) + row * nj + j));
-        unsigned h[4];
+        const int j = w >> 2, o = w & 3;
+        const unsigned word = __ldcs((isv ? v_codes : k_codes) + row * W + o * NJ + j);
+        const __half2 s2 = __half2half2((isv ? v_scales : k_scales)[row * NJ + j]);
+        // elements (n, n+4) as 1024 + u, less 1032 exactly, times the scale
+        const __half2 bias = __float2half2_rn(1032.f);
+        uint32_t h[4];
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
-            const int c0 = static_cast<int>((word >> (8 * n)) & 15u) - 8;
-            const int c1 = static_cast<int>((word >> (8 * n + 4)) & 15u) - 8;
-            h[n] = tc::pack_half2(c0 * s, c1 * s);
+            const uint32_t u = ((word >> (4 * n)) & 0x000f000fu) | 0x64006400u;
+            const __half2 c = __hmul2(__hsub2(*reinterpret_cast<const __half2 *>(&u), bias), s2);
+            h[n] = *reinterpret_cast<const uint32_t *>(&c);
         }
-        v = make_uint4(h[0], h[1], h[2], h[3]);
+        out = make_uint4(__byte_perm(h[0], h[1], 0x5410), __byte_perm(h[2], h[3], 0x5410),
+                         __byte_perm(h[0], h[1], 0x7632), __byte_perm(h[2], h[3], 0x7632));
     }
-    reinterpret_cast<uint4 *>(isv ? v_out : k_out)[idx] = v;
+    reinterpret_cast<uint4 *>(isv ? v_out : k_out)[(long long)b * a.n_words + idx] = out;
 }
 
 // --------------------------------------------------------------- attention
@@ -915,6 +944,28 @@ static int check_rows(const char *name, const Span *outs, int n_outs, const Span
     return 0;
 }
 
+static int log2_of(int page_size)               // -1 when it is not a power of two
+{
+    return page_size & (page_size - 1) ? -1 : __builtin_ctz(page_size);
+}
+
+static bool row_args(int T, int Hkv, int D, int page_size, const int *count, RowArgs *a)
+{
+    const long long words = (long long)T * Hkv * (D / 8);
+    if (words > 0x7fffffffll)
+        return false;
+    a->T = T;
+    a->n_words = static_cast<int>(words);
+    a->lg_page = page_size > 0 ? log2_of(page_size) : -1;
+    a->count = count;
+    return true;
+}
+
+static dim3 row_grid(const RowArgs &a, int batch)
+{
+    return dim3((a.n_words + 255) / 256, batch, 2);
+}
+
 static Params row_params(const int32_t *block_table, const int32_t *positions, int batch,
                          int n_kv_heads, int page_size, int max_blocks, int num_blocks,
                          long long cap)
@@ -978,17 +1029,15 @@ FA_API int fa_append_kv_int4(const float *k_new, const float *v_new, void *k_cod
         return rc;
     if (rows == 0)
         return 0;
-    const int words = head_dim / 8;
-    const long long total = (long long)rows * words;
-    const long long ctas = (total + 255) / 256;
-    if (ctas > 0x7fffffffll)
-        return fail(FA_ERR_LAYOUT, "%s: too many rows", name);
+    i4::RowArgs a = {};
+    if (!i4::row_args(n_tokens, n_kv_heads, head_dim, page_size, n_new, &a))
+        return fail(FA_ERR_LAYOUT, "%s: too many rows per sequence", name);
     const Params p = i4::row_params(block_table, positions, batch, n_kv_heads, page_size,
                                     max_blocks_per_seq, num_blocks, cap);
-    i4::append_kernel<<<dim3((unsigned)ctas, 2), 256, 0, static_cast<cudaStream_t>(stream)>>>(
-        p, k_new, v_new, static_cast<unsigned *>(k_codes), static_cast<__half *>(k_scales),
-        static_cast<unsigned *>(v_codes), static_cast<__half *>(v_scales), n_new, n_tokens, words,
-        total);
+    const auto kernel = head_dim == 128 ? i4::append_kernel<128> : i4::append_kernel<256>;
+    kernel<<<i4::row_grid(a, batch), 256, 0, static_cast<cudaStream_t>(stream)>>>(
+        p, a, k_new, v_new, static_cast<unsigned *>(k_codes), static_cast<__half *>(k_scales),
+        static_cast<unsigned *>(v_codes), static_cast<__half *>(v_scales));
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess)
         return fail(FA_ERR_CUDA, "%s: launch failed: %s", name, cudaGetErrorString(e));
@@ -1028,17 +1077,16 @@ FA_API int fa_gather_kv_int4(const void *k_codes, const void *k_scales, const vo
         return rc;
     if (rows == 0)
         return 0;
-    const int words = head_dim / 8;
-    const long long total = (long long)rows * words;
-    const long long ctas = (total + 255) / 256;
-    if (ctas > 0x7fffffffll)
-        return fail(FA_ERR_LAYOUT, "%s: too many rows", name);
+    i4::RowArgs a = {};
+    if (!i4::row_args(n_tokens, n_kv_heads, head_dim, page_size, n_rows, &a))
+        return fail(FA_ERR_LAYOUT, "%s: too many rows per sequence", name);
     const Params p = i4::row_params(block_table, positions, batch, n_kv_heads, page_size,
                                     max_blocks_per_seq, num_blocks, cap);
-    i4::gather_kernel<<<dim3((unsigned)ctas, 2), 256, 0, static_cast<cudaStream_t>(stream)>>>(
-        p, static_cast<const unsigned *>(k_codes), static_cast<const __half *>(k_scales),
-        static_cast<const unsigned *>(v_codes), static_cast<const __half *>(v_scales), n_rows,
-        static_cast<__half *>(k_out), static_cast<__half *>(v_out), n_tokens, words, total);
+    const auto kernel = head_dim == 128 ? i4::gather_kernel<128> : i4::gather_kernel<256>;
+    kernel<<<i4::row_grid(a, batch), 256, 0, static_cast<cudaStream_t>(stream)>>>(
+        p, a, static_cast<const unsigned *>(k_codes), static_cast<const __half *>(k_scales),
+        static_cast<const unsigned *>(v_codes), static_cast<const __half *>(v_scales),
+        static_cast<__half *>(k_out), static_cast<__half *>(v_out));
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess)
         return fail(FA_ERR_CUDA, "%s: launch failed: %s", name, cudaGetErrorString(e));
