@@ -691,10 +691,10 @@ __device__ __forceinline__ void store4(__half *dst, float4 v)
     *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_half2(v.x, v.y), pack_half2(v.z, v.w));
 }
 
-// OutT: float, or __half for the entry points whose output is fp16.  LSE: also
-// write each row's log2-sum-exp2 (p.lse).
-template <int D, bool BI, typename OutT = float, bool LSE = false>
-__global__ void __launch_bounds__(MERGE_THREADS) fa_stream_merge_kernel(const Params p)
+// One output row, by a CTA of MERGE_THREADS.  OutT: float, or __half for the entry
+// points whose output is fp16.
+template <int D, bool BI, typename OutT>
+__device__ __forceinline__ void merge_row(const Params &p, const long long row)
 {
     constexpr int CH = D / 4;                    // float4 columns
     constexpr int SG = MERGE_THREADS / CH;       // slot groups
@@ -703,7 +703,6 @@ __global__ void __launch_bounds__(MERGE_THREADS) fa_stream_merge_kernel(const Pa
     __shared__ float4 part[SG][CH];
 
     // row = (b * tq + query) * Hq + head; its column x = query * G + head % G
-    const long long row = blockIdx.x;
     const int tq = p.tq > 1 ? p.tq : 1;
     const int b = static_cast<int>(row / ((long long)tq * p.Hq));
     const int qj = static_cast<int>((row / p.Hq) % tq);
@@ -723,14 +722,6 @@ __global__ void __launch_bounds__(MERGE_THREADS) fa_stream_merge_kernel(const Pa
         if (tid < CH)
             store4(reinterpret_cast<OutT *>(p.out) + row * D + 4 * tid,
                    make_float4(0.f, 0.f, 0.f, 0.f));
-        if (LSE && tid == 0)
-            p.lse[row] = -INFINITY;
-    };
-    // a further kernel reads what the split kernel wrote, so with LSE no CTA
-    // ends before the split grid has
-    auto done = [&] {
-        if constexpr (LSE)
-            asm volatile("griddepcontrol.wait;" ::: "memory");
     };
     if constexpr (BI) {
         int lo, hi;
@@ -738,15 +729,12 @@ __global__ void __launch_bounds__(MERGE_THREADS) fa_stream_merge_kernel(const Pa
         n = tiles_in<TILE>(lo, hi);
         if (n == 0) {
             zero_row();
-            done();
             return;
         }
         // batch-invariant plan: the unit's chunks, one slot each
         ns = (n + p.chunk - 1) / p.chunk;
-        if (ns == 1) {
-            done();
+        if (ns == 1)
             return;                               // written by the split kernel
-        }
         asm volatile("griddepcontrol.wait;" ::: "memory");
         sb = u * p.max_chunks;
     } else {
@@ -778,7 +766,6 @@ __global__ void __launch_bounds__(MERGE_THREADS) fa_stream_merge_kernel(const Pa
         }
         if (n == 0) {                             // uniform over the CTA
             zero_row();
-            done();
             return;
         }
         if (!scan_here) {
@@ -794,10 +781,8 @@ __global__ void __launch_bounds__(MERGE_THREADS) fa_stream_merge_kernel(const Pa
         const long long us = sh_P + (long long)j * (n + UNIT_COST) + UNIT_COST;   // first tile
         const int wf = worker_of(us, T, We);
         const int wl = worker_of(us + n - 1, T, We);
-        if (wf == wl) {
-            done();
+        if (wf == wl)
             return;                               // written by the split kernel
-        }
         if (scan_here)
             asm volatile("griddepcontrol.wait;" ::: "memory");
         sb = wf + u;
@@ -905,9 +890,13 @@ __global__ void __launch_bounds__(MERGE_THREADS) fa_stream_merge_kernel(const Pa
         const float inv = L > 0.f ? 1.f / L : 0.f;
         store4(reinterpret_cast<OutT *>(p.out) + row * D + 4 * c,
                make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
-        if (LSE && c == 0)
-            p.lse[row] = L > 0.f ? M + log2f(L) : -INFINITY;
     }
+}
+
+template <int D, bool BI, typename OutT = float>
+__global__ void __launch_bounds__(MERGE_THREADS) fa_stream_merge_kernel(const Params p)
+{
+    merge_row<D, BI, OutT>(p, blockIdx.x);
 }
 
 // Warp-per-row form of the stream-K merge, for steps with many rows (the
@@ -918,15 +907,14 @@ __global__ void __launch_bounds__(MERGE_THREADS) fa_stream_merge_kernel(const Pa
 // the partial O columns stream in.  The fold runs in slot order.
 constexpr int MERGE_ROWS_PER_CTA = 8;
 
-template <int D, typename OutT = float, bool LSE = false>
-__global__ void __launch_bounds__(MERGE_ROWS_PER_CTA * 32) fa_stream_merge_rows_kernel(
-    const Params p)
+template <int D, typename OutT>
+__device__ __forceinline__ void merge_rows(const Params &p, const int cta)
 {
     constexpr int CPL = D / 128;                 // float4 columns per lane
     const int lane = threadIdx.x & 31;
     const int tq = p.tq > 1 ? p.tq : 1;
     const long long rows = (long long)p.B * tq * p.Hq;
-    const long long row = (long long)blockIdx.x * MERGE_ROWS_PER_CTA + (threadIdx.x >> 5);
+    const long long row = (long long)cta * MERGE_ROWS_PER_CTA + (threadIdx.x >> 5);
     if (row >= rows)
         return;
     // row = (b * tq + query) * Hq + head; its column x = query * G + head % G
@@ -957,10 +945,6 @@ __global__ void __launch_bounds__(MERGE_ROWS_PER_CTA * 32) fa_stream_merge_rows_
 #pragma unroll
         for (int c = 0; c < CPL; ++c)
             store4(dst + 4 * (lane + 32 * c), make_float4(0.f, 0.f, 0.f, 0.f));
-        if (LSE && lane == 0)
-            p.lse[row] = -INFINITY;
-        if constexpr (LSE)
-            asm volatile("griddepcontrol.wait;" ::: "memory");
         return;
     }
     if (!scan_here) {
@@ -972,11 +956,8 @@ __global__ void __launch_bounds__(MERGE_ROWS_PER_CTA * 32) fa_stream_merge_rows_
     const long long us = P + (long long)j * (n + UNIT_COST) + UNIT_COST;   // first tile
     const int wf = worker_of(us, T, We);
     const int wl = worker_of(us + n - 1, T, We);
-    if (wf == wl) {
-        if constexpr (LSE)
-            asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (wf == wl)
         return;                                   // written by the split kernel
-    }
     if (scan_here)
         asm volatile("griddepcontrol.wait;" ::: "memory");
     const long long sb = (long long)wf + (long long)b * p.U_b + j;
@@ -1023,67 +1004,178 @@ __global__ void __launch_bounds__(MERGE_ROWS_PER_CTA * 32) fa_stream_merge_rows_
     for (int c = 0; c < CPL; ++c)
         store4(dst + 4 * (lane + 32 * c),
                make_float4(o[c].x * inv, o[c].y * inv, o[c].z * inv, o[c].w * inv));
-    if (LSE && lane == 0)
-        p.lse[row] = L > 0.f ? M + log2f(L) : -INFINITY;
 }
 
-// Recorded weights, the last step: every key of sequence b and KV head kv adds
+template <int D, typename OutT = float>
+__global__ void __launch_bounds__(MERGE_ROWS_PER_CTA * 32) fa_stream_merge_rows_kernel(
+    const Params p)
+{
+    merge_rows<D, OutT>(p, blockIdx.x);
+}
+
+// Recorded weights: every key of sequence b and KV head kv adds
 //     sum over the KV head's (query, head) columns of ex2(score - lse)
 // to its cache row's running total.  The split kernel left the scores (log2
-// units, -inf where a column does not attend the key), the merge the rows'
-// log2-sum-exp2.  A thread per key; one fp32 reduction per key, atomic because
-// two sequences' tables may name the same block (a prefix they share).
-constexpr int WEIGHT_KEYS = 256;      // keys per CTA
-constexpr int WEIGHT_COLS = 512;      // columns' log-sum-exps held at a time
+// units, -inf where a column does not attend the key) and, for units one worker
+// covered, the rows' log2-sum-exp2; of the other units' it is reduced here from
+// their partials' (m, l), so this needs no merged row and runs beside the merge.
+// A CTA takes 1024 keys of one (b, kv) at a time, four per thread, so that their
+// loads overlap.  One fp32 reduction per key, atomic because two sequences'
+// tables may name the same block (a prefix they share).
+constexpr int WEIGHT_THREADS = MERGE_THREADS;
+constexpr int WEIGHT_KPT = 4;                              // keys per thread
+constexpr int WEIGHT_KEYS = WEIGHT_THREADS * WEIGHT_KPT;   // keys per item
+constexpr int WEIGHT_COLS = 512;                           // columns at a time
 
-static __global__ void __launch_bounds__(WEIGHT_KEYS) fa_weights_kernel(const Params p)
+__device__ __forceinline__ void add_weights(const Params &p, const int cta, const int ctas)
 {
-    __shared__ float lse[WEIGHT_COLS];
+    __shared__ __align__(16) float lse[WEIGHT_COLS];
     const int tq = p.tq > 1 ? p.tq : 1;
     const int cols = tq * p.G;
-    const long long chunks = (p.cap16 + WEIGHT_KEYS - 1) / WEIGHT_KEYS;   // per (b, kv)
-    const long long items = chunks * p.B * p.Hkv;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    for (long long it = blockIdx.x; it < items; it += gridDim.x) {
-        const int b = static_cast<int>(it / chunks / p.Hkv);
-        const int kv = static_cast<int>(it / chunks % p.Hkv);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int chunks = static_cast<int>((p.cap16 + WEIGHT_KEYS - 1) / WEIGHT_KEYS);
+    const long long items = (long long)chunks * p.B * p.Hkv;
+    bool waited = false;
+    long long T = 0, P = 0;
+    int have_b = -1, n = 0;
+    for (long long it = cta; it < items; it += ctas) {
+        const int u = static_cast<int>(it / chunks);       // (b, kv)
+        const int b = u / p.Hkv, kv = u % p.Hkv;
         int lo, hi;
         attended_range(p, b, lo, hi, false);
-        const long long t0 = (lo / TILE) * TILE + it % chunks * WEIGHT_KEYS;   // a tile start
+        const long long t0 = (lo / TILE) * TILE + (it - (long long)u * chunks) * WEIGHT_KEYS;
         if (t0 >= hi)
             continue;
-        const int t = static_cast<int>(t0) + threadIdx.x;
-        long long row = -1;
-        if (t >= lo && t < hi) {
-            row = tile_row(p, b, kv, t - t % TILE);
-            if (row >= 0)
-                row += t % TILE;
+        if (b != have_b && p.B <= 32 * SCAN_REG) {         // every warp for itself
+            int b_at;
+            long long P_at;
+            T = flat_scan(p, -1, b_at, P_at, false, nullptr, b, &P, &n);
+            have_b = b;
         }
-        float sum = 0.f;
+        long long row[WEIGHT_KPT];
+#pragma unroll
+        for (int q = 0; q < WEIGHT_KPT; ++q) {
+            const int t = static_cast<int>(t0) + threadIdx.x + q * WEIGHT_THREADS;
+            row[q] = -1;
+            if (t >= lo && t < hi) {
+                row[q] = tile_row(p, b, kv, t - t % TILE);
+                if (row[q] >= 0)
+                    row[q] += t % TILE;
+            }
+        }
+        if (!waited)
+            asm volatile("griddepcontrol.wait;" ::: "memory");
+        waited = true;
+        if (b != have_b) {                                 // published by the split kernel
+            T = p.pref[p.B];
+            P = p.pref[b];
+            n = tiles_in<TILE>(lo, hi);
+            have_b = b;
+        }
+        const int We = workers_for(p, T);
+        float sum[WEIGHT_KPT] = {};
         for (int x0 = 0; x0 < cols; x0 += WEIGHT_COLS) {
             const int nx = min(WEIGHT_COLS, cols - x0);
             __syncthreads();
-            for (int i = threadIdx.x; i < nx; i += WEIGHT_KEYS) {
-                const int x = x0 + i;
-                lse[i] = p.lse[((long long)b * tq + x / p.G) * p.Hq + kv * p.G + x % p.G];
+            // a warp per column: its row's log-sum-exp, +inf where it has no key
+            for (int i = warp; i < nx; i += WEIGHT_THREADS / 32) {
+                const int x = x0 + i, j = kv * p.n_hg + x / p.cpu;
+                const long long us = P + (long long)j * (n + UNIT_COST) + UNIT_COST;
+                const int wf = worker_of(us, T, We), wl = worker_of(us + n - 1, T, We);
+                float v;
+                if (wf == wl) {
+                    v = p.lse[((long long)b * tq + x / p.G) * p.Hq + kv * p.G + x % p.G];
+                } else {
+                    const float2 *ml = p.ws_ml + ((long long)wf + (long long)b * p.U_b + j) * p.sh +
+                                       x % p.cpu;
+                    float M = -INFINITY, L = 0.f;
+                    for (int s = lane; s <= wl - wf; s += 32) {
+                        const float2 y = ml[(long long)s * p.sh];
+                        if (y.x == -INFINITY)
+                            continue;
+                        const float m = fmaxf(M, y.x);
+                        L = L * ex2(M - m) + y.y * ex2(y.x - m);
+                        M = m;
+                    }
+                    float Mw = M;
+#pragma unroll
+                    for (int off = 16; off >= 1; off >>= 1)
+                        Mw = fmaxf(Mw, __shfl_xor_sync(0xffffffffu, Mw, off));
+                    L = M == -INFINITY ? 0.f : L * ex2(M - Mw);
+#pragma unroll
+                    for (int off = 16; off >= 1; off >>= 1)
+                        L += __shfl_xor_sync(0xffffffffu, L, off);
+                    v = L > 0.f ? Mw + log2f(L) : -INFINITY;
+                }
+                if (lane == 0)
+                    lse[i] = v == -INFINITY ? INFINITY : v;
             }
             __syncthreads();
-            if (row < 0)
-                continue;
             for (int i = 0; i < nx; i += p.cpu) {
                 const long long unit = (long long)b * p.U_b + kv * p.n_hg + (x0 + i) / p.cpu;
-                const float *s = p.ws_s + (unit * p.cap16 + t) * p.sh;
-                const int n = min(p.cpu, nx - i);
-                for (int c = 0; c < n; ++c) {
-                    const float v = s[c];
-                    sum += v == -INFINITY ? 0.f : ex2(v - lse[i + c]);
+                const int nc = min(p.cpu, nx - i);
+                const float *s = p.ws_s + (unit * p.cap16 + t0 + threadIdx.x) * p.sh;
+                if (p.sh == 4 || p.sh == 8) {              // whole groups in 16-byte loads
+                    float4 v[WEIGHT_KPT][2];
+#pragma unroll
+                    for (int q = 0; q < WEIGHT_KPT; ++q)
+#pragma unroll
+                        for (int c = 0; c < 2; ++c)
+                            if (row[q] >= 0 && 4 * c < p.sh)
+                                v[q][c] = __ldcs(reinterpret_cast<const float4 *>(
+                                                     s + (long long)q * WEIGHT_THREADS * p.sh) +
+                                                 c);
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        if (4 * c >= p.sh)
+                            continue;
+                        const float4 z = reinterpret_cast<const float4 *>(lse + i)[c];
+#pragma unroll
+                        for (int q = 0; q < WEIGHT_KPT; ++q) {
+                            const float4 y = v[q][c];
+                            if (4 * c < nc)
+                                sum[q] += ex2(y.x - z.x);
+                            if (4 * c + 1 < nc)
+                                sum[q] += ex2(y.y - z.y);
+                            if (4 * c + 2 < nc)
+                                sum[q] += ex2(y.z - z.z);
+                            if (4 * c + 3 < nc)
+                                sum[q] += ex2(y.w - z.w);
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int q = 0; q < WEIGHT_KPT; ++q)
+                        for (int c = 0; c < nc; ++c)
+                            if (row[q] >= 0)
+                                sum[q] += ex2(s[(long long)q * WEIGHT_THREADS * p.sh + c] -
+                                              lse[i + c]);
                 }
             }
         }
-        if (row >= 0)
-            atomicAdd(p.acc + row, sum);
+#pragma unroll
+        for (int q = 0; q < WEIGHT_KPT; ++q)
+            if (row[q] >= 0)
+                atomicAdd(p.acc + row[q], sum[q]);
     }
+    if (!waited)
+        asm volatile("griddepcontrol.wait;" ::: "memory");
 }
+
+// The merge (fp16 output) and the recorded weights in one launch: the first
+// merge_ctas CTAs merge, BY_WARP as fa_stream_merge_rows_kernel.
+template <int D, bool BY_WARP>
+__global__ void __launch_bounds__(MERGE_THREADS) fa_merge_weights_kernel(const Params p,
+                                                                         const int merge_ctas)
+{
+    if (static_cast<int>(blockIdx.x) >= merge_ctas)
+        add_weights(p, blockIdx.x - merge_ctas, gridDim.x - merge_ctas);
+    else if constexpr (BY_WARP)
+        merge_rows<D, __half>(p, blockIdx.x);
+    else
+        merge_row<D, false, __half>(p, blockIdx.x);
+}
+static_assert(MERGE_THREADS == MERGE_ROWS_PER_CTA * 32, "one block size for both merges");
 
 // Scores of the keys ka and kb of a unit's tile (rows g4 and g4 + 8 of the
 // mma tile) for this lane's columns c0 = 2 t4 and c0 + 1, of nh live ones.
@@ -1178,21 +1270,39 @@ static bool weight_space(size_t base, int B, int tq, int Hq, int units, int sh, 
     return true;
 }
 
-static cudaError_t launch_weights(const Params &p, int sms, cudaStream_t st)
+// The merge of an fp16 output, with the recorded weights when p.acc is set; as the
+// fp32 merge, a warp per row from MERGE_WARP_ROWS_PER_SM rows per SM.
+constexpr int MERGE_WARP_ROWS_PER_SM = 4;
+template <int D>
+static cudaError_t launch_merge_half(const Params &p, int sms, cudaStream_t st)
 {
-    const long long chunks = (p.cap16 + tc::WEIGHT_KEYS - 1) / tc::WEIGHT_KEYS;
-    const long long items = chunks * p.B * p.Hkv;
-    const long long most = (long long)sms * 8;       // resident CTAs: 2048 threads per SM
+    const long long rows = (long long)p.B * (p.tq > 1 ? p.tq : 1) * p.Hq;
+    const bool by_warp = rows >= (long long)MERGE_WARP_ROWS_PER_SM * sms;
+    const long long merge = by_warp ? (rows + tc::MERGE_ROWS_PER_CTA - 1) / tc::MERGE_ROWS_PER_CTA
+                                    : rows;
+    long long ctas = merge;
+    if (p.acc) {
+        const long long items = (p.cap16 + tc::WEIGHT_KEYS - 1) / tc::WEIGHT_KEYS * p.B * p.Hkv;
+        const long long most = (long long)sms * 4;
+        ctas += items < most ? items : most;
+    }
+    if (ctas > 0x7fffffffll)
+        return cudaErrorInvalidConfiguration;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(items < most ? items : most));
-    cfg.blockDim = dim3(tc::WEIGHT_KEYS);
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+    cfg.blockDim = dim3(tc::MERGE_THREADS);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, tc::fa_weights_kernel, p);
+    const int m = static_cast<int>(merge);
+    const cudaError_t e =
+        p.acc ? (by_warp ? cudaLaunchKernelEx(&cfg, tc::fa_merge_weights_kernel<D, true>, p, m)
+                         : cudaLaunchKernelEx(&cfg, tc::fa_merge_weights_kernel<D, false>, p, m))
+              : (by_warp ? cudaLaunchKernelEx(&cfg, tc::fa_stream_merge_rows_kernel<D, __half>, p)
+                         : cudaLaunchKernelEx(&cfg, tc::fa_stream_merge_kernel<D, false, __half>, p));
     return e == cudaSuccess ? cudaGetLastError() : e;
 }
 

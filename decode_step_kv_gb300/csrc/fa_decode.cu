@@ -600,7 +600,7 @@ struct Smem {
 // runs.
 constexpr int CL_MAX_CTAS = 8;  // the portable maximum cluster size
 // WT: recorded weights -- the tile's scores go to the workspace for
-// fa_weights_kernel, whole units also write their log-sum-exp, and the output
+// add_weights, whole units also write their log-sum-exp, and the output
 // is fp16.
 template <int D, bool VI8, bool BI, int NG, bool CL = false, bool WT = false>
 __global__ void __launch_bounds__(Cfg<D, VI8, NG>::NW * 32, Cfg<D, VI8, NG>::CTAS_PER_SM)
@@ -2473,15 +2473,8 @@ static int decode_impl(const void *q, const void *k_cache, const void *v_cache,
         attr[0].val.programmaticStreamSerializationAllowed = prof_end ? 0 : 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        if (acc && by_warp)
-            e = D == 128
-                    ? cudaLaunchKernelEx(&cfg, tc::fa_stream_merge_rows_kernel<128, __half, true>, p)
-                    : cudaLaunchKernelEx(&cfg, tc::fa_stream_merge_rows_kernel<256, __half, true>, p);
-        else if (acc)
-            e = D == 128 ? cudaLaunchKernelEx(
-                               &cfg, tc::fa_stream_merge_kernel<128, false, __half, true>, p)
-                         : cudaLaunchKernelEx(
-                               &cfg, tc::fa_stream_merge_kernel<256, false, __half, true>, p);
+        if (acc)
+            e = D == 128 ? launch_merge_half<128>(p, sms, st) : launch_merge_half<256>(p, sms, st);
         else if (by_warp)
             e = D == 128 ? cudaLaunchKernelEx(&cfg, tc::fa_stream_merge_rows_kernel<128>, p)
                          : cudaLaunchKernelEx(&cfg, tc::fa_stream_merge_rows_kernel<256>, p);
@@ -2499,9 +2492,6 @@ static int decode_impl(const void *q, const void *k_cache, const void *v_cache,
     }
     if (e != cudaSuccess)
         return fail(FA_ERR_CUDA, "fa_decode: merge launch failed: %s", cudaGetErrorString(e));
-    if (acc && (e = launch_weights(p, sms, st)) != cudaSuccess)
-        return fail(FA_ERR_CUDA, "fa_decode_weights: weights launch failed: %s",
-                    cudaGetErrorString(e));
     return 0;
 }
 

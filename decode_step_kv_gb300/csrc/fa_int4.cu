@@ -874,25 +874,7 @@ static cudaError_t launch(const Params &p, int ctas, int sms, cudaStream_t st)
     decode_kernel<D, WT><<<ctas, Cfg<D>::NW * 32, Cfg<D>::SMEM, st>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess)
         return e;
-    const long long rows = (long long)p.B * p.tq * p.Hq;
-    const bool by_warp = rows >= 4ll * sms;      // as the fp16 kernel's merge
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(
-        by_warp ? (rows + tc::MERGE_ROWS_PER_CTA - 1) / tc::MERGE_ROWS_PER_CTA : rows));
-    cfg.blockDim = dim3(by_warp ? tc::MERGE_ROWS_PER_CTA * 32 : tc::MERGE_THREADS);
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    e = by_warp ? cudaLaunchKernelEx(&cfg, tc::fa_stream_merge_rows_kernel<D, __half, WT>, p)
-                : cudaLaunchKernelEx(&cfg, tc::fa_stream_merge_kernel<D, false, __half, WT>, p);
-    if (e == cudaSuccess)
-        e = cudaGetLastError();
-    if (WT && e == cudaSuccess)
-        e = launch_weights(p, sms, st);
-    return e;
+    return launch_merge_half<D>(p, sms, st);
 }
 
 // The checks of a cache's layout that append, gather and decode share.
