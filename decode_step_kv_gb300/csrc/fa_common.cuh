@@ -67,6 +67,8 @@ struct Params {
     float *ws_s;      // recorded weights: [B*units][cap16][sh] scores in log2 units
     float *acc;       // recorded weights: the running total of every cache row
     long long cap16;  // recorded weights: capacity rounded up to whole tiles
+    int lg_page;      // recorded weights: log2 of page_size, or -1
+    int w_rounds;     // recorded weights: rounds of WEIGHT_KEYS keys per item
 };
 
 // ------------------------------------------------------------ PTX wrappers
@@ -142,6 +144,13 @@ __device__ __forceinline__ float ex2(float x)
 {
     float y;
     asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ float ex2_ftz(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
 
@@ -1019,12 +1028,14 @@ __global__ void __launch_bounds__(MERGE_ROWS_PER_CTA * 32) fa_stream_merge_rows_
 // units, -inf where a column does not attend the key) and, for units one worker
 // covered, the rows' log2-sum-exp2; of the other units' it is reduced here from
 // their partials' (m, l), so this needs no merged row and runs beside the merge.
-// A CTA takes 1024 keys of one (b, kv) at a time, four per thread, so that their
-// loads overlap.  One fp32 reduction per key, atomic because two sequences'
+// An item is w_rounds * 1024 keys of one (b, kv): its rows' log-sum-exps once, then
+// four keys per thread and round, so that their loads overlap.  (With items of
+// one round and page divisions, 16 sequences of 16384 keys took 41 us instead of
+// their bytes' 8.)  One fp32 reduction per key, atomic because two sequences'
 // tables may name the same block (a prefix they share).
 constexpr int WEIGHT_THREADS = MERGE_THREADS;
 constexpr int WEIGHT_KPT = 4;                              // keys per thread
-constexpr int WEIGHT_KEYS = WEIGHT_THREADS * WEIGHT_KPT;   // keys per item
+constexpr int WEIGHT_KEYS = WEIGHT_THREADS * WEIGHT_KPT;   // keys per round
 constexpr int WEIGHT_COLS = 512;                           // columns at a time
 
 __device__ __forceinline__ void add_weights(const Params &p, const int cta, const int ctas)
@@ -1033,35 +1044,37 @@ __device__ __forceinline__ void add_weights(const Params &p, const int cta, cons
     const int tq = p.tq > 1 ? p.tq : 1;
     const int cols = tq * p.G;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int chunks = static_cast<int>((p.cap16 + WEIGHT_KEYS - 1) / WEIGHT_KEYS);
+    const int item_keys = WEIGHT_KEYS * p.w_rounds;
+    const int chunks = static_cast<int>((p.cap16 + item_keys - 1) / item_keys);
     const long long items = (long long)chunks * p.B * p.Hkv;
     bool waited = false;
     long long T = 0, P = 0;
     int have_b = -1, n = 0;
+    // cache row of token t of (b, kv); -1 for a block id out of range (caches here
+    // have fewer than 2^31 rows)
+    auto row_at = [&](int b, int kv, int t) -> int {
+        if (!p.bt)
+            return (b * p.Hkv + kv) * static_cast<int>(p.cap) + t;
+        const int page = p.lg_page >= 0 ? t >> p.lg_page : t / p.page_size;
+        const int blk = p.bt[(long long)b * p.max_blocks + page];
+        if (blk < 0 || blk >= p.num_blocks)
+            return -1;
+        return (blk * p.Hkv + kv) * p.page_size + (t - page * p.page_size);
+    };
     for (long long it = cta; it < items; it += ctas) {
         const int u = static_cast<int>(it / chunks);       // (b, kv)
-        const int b = u / p.Hkv, kv = u % p.Hkv;
+        const int b = u / p.Hkv, kv = u - b * p.Hkv;
         int lo, hi;
         attended_range(p, b, lo, hi, false);
-        const long long t0 = (lo / TILE) * TILE + (it - (long long)u * chunks) * WEIGHT_KEYS;
+        const long long t0 = (lo / TILE) * TILE + (it - (long long)u * chunks) * item_keys;
         if (t0 >= hi)
             continue;
+        const int end = static_cast<int>(t0 + item_keys < hi ? t0 + item_keys : hi);
         if (b != have_b && p.B <= 32 * SCAN_REG) {         // every warp for itself
             int b_at;
             long long P_at;
             T = flat_scan(p, -1, b_at, P_at, false, nullptr, b, &P, &n);
             have_b = b;
-        }
-        long long row[WEIGHT_KPT];
-#pragma unroll
-        for (int q = 0; q < WEIGHT_KPT; ++q) {
-            const int t = static_cast<int>(t0) + threadIdx.x + q * WEIGHT_THREADS;
-            row[q] = -1;
-            if (t >= lo && t < hi) {
-                row[q] = tile_row(p, b, kv, t - t % TILE);
-                if (row[q] >= 0)
-                    row[q] += t % TILE;
-            }
         }
         if (!waited)
             asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -1073,7 +1086,6 @@ __device__ __forceinline__ void add_weights(const Params &p, const int cta, cons
             have_b = b;
         }
         const int We = workers_for(p, T);
-        float sum[WEIGHT_KPT] = {};
         for (int x0 = 0; x0 < cols; x0 += WEIGHT_COLS) {
             const int nx = min(WEIGHT_COLS, cols - x0);
             __syncthreads();
@@ -1111,52 +1123,57 @@ __device__ __forceinline__ void add_weights(const Params &p, const int cta, cons
                     lse[i] = v == -INFINITY ? INFINITY : v;
             }
             __syncthreads();
-            for (int i = 0; i < nx; i += p.cpu) {
-                const long long unit = (long long)b * p.U_b + kv * p.n_hg + (x0 + i) / p.cpu;
-                const int nc = min(p.cpu, nx - i);
-                const float *s = p.ws_s + (unit * p.cap16 + t0 + threadIdx.x) * p.sh;
-                if (p.sh == 4 || p.sh == 8) {              // whole groups in 16-byte loads
-                    float4 v[WEIGHT_KPT][2];
+            // the scores of column group i of key t: at + i * group + t * sh
+            const long long group = p.cap16 * p.sh;
+            const float *at = p.ws_s + ((long long)b * p.U_b + kv * p.n_hg + x0 / p.cpu) * group;
+            const int ng = (nx + p.cpu - 1) / p.cpu;
+            // (more than WEIGHT_COLS columns add to a key once per pass)
+            for (int tr = static_cast<int>(t0) + threadIdx.x; tr < end; tr += WEIGHT_KEYS) {
+                int row[WEIGHT_KPT];
 #pragma unroll
-                    for (int q = 0; q < WEIGHT_KPT; ++q)
+                for (int q = 0; q < WEIGHT_KPT; ++q) {
+                    const int t = tr + q * WEIGHT_THREADS;
+                    row[q] = t >= lo && t < end ? row_at(b, kv, t) : -1;
+                }
+                float sum[WEIGHT_KPT] = {};
+                if (p.sh % 4 == 0) {                       // 4 or 8: 16-byte loads
+                    const int quads = p.sh / 4;
+                    for (int i = 0; i < ng * quads; ++i) {
+                        const float *s = at + (quads == 1 ? i : i >> 1) * group + (i & (quads - 1)) * 4 +
+                                         (long long)tr * p.sh;
+                        float4 v[WEIGHT_KPT];
 #pragma unroll
-                        for (int c = 0; c < 2; ++c)
-                            if (row[q] >= 0 && 4 * c < p.sh)
-                                v[q][c] = __ldcs(reinterpret_cast<const float4 *>(
-                                                     s + (long long)q * WEIGHT_THREADS * p.sh) +
-                                                 c);
+                        for (int q = 0; q < WEIGHT_KPT; ++q)
+                            if (row[q] >= 0)
+                                v[q] = __ldcs(reinterpret_cast<const float4 *>(
+                                    s + q * WEIGHT_THREADS * p.sh));
+                        // columns past the last hold nothing: +inf weighs them 0
+                        const float4 z = reinterpret_cast<const float4 *>(lse)[i];
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        if (4 * c >= p.sh)
-                            continue;
-                        const float4 z = reinterpret_cast<const float4 *>(lse + i)[c];
-#pragma unroll
-                        for (int q = 0; q < WEIGHT_KPT; ++q) {
-                            const float4 y = v[q][c];
-                            if (4 * c < nc)
-                                sum[q] += ex2(y.x - z.x);
-                            if (4 * c + 1 < nc)
-                                sum[q] += ex2(y.y - z.y);
-                            if (4 * c + 2 < nc)
-                                sum[q] += ex2(y.z - z.z);
-                            if (4 * c + 3 < nc)
-                                sum[q] += ex2(y.w - z.w);
-                        }
+                        for (int q = 0; q < WEIGHT_KPT; ++q)
+                            if (row[q] >= 0) {
+                                float y = ex2_ftz(v[q].x - z.x);
+                                y += 4 * i + 1 < nx ? ex2_ftz(v[q].y - z.y) : 0.f;
+                                y += 4 * i + 2 < nx ? ex2_ftz(v[q].z - z.z) : 0.f;
+                                y += 4 * i + 3 < nx ? ex2_ftz(v[q].w - z.w) : 0.f;
+                                sum[q] += 4 * i < nx ? y : 0.f;
+                            }
                     }
                 } else {
 #pragma unroll
                     for (int q = 0; q < WEIGHT_KPT; ++q)
-                        for (int c = 0; c < nc; ++c)
-                            if (row[q] >= 0)
-                                sum[q] += ex2(s[(long long)q * WEIGHT_THREADS * p.sh + c] -
-                                              lse[i + c]);
+                        if (row[q] >= 0)
+                            for (int x = 0; x < nx; ++x)
+                                sum[q] += ex2_ftz(at[x / p.cpu * group + x % p.cpu +
+                                                     (long long)(tr + q * WEIGHT_THREADS) * p.sh] -
+                                                  lse[x]);
                 }
+#pragma unroll
+                for (int q = 0; q < WEIGHT_KPT; ++q)
+                    if (row[q] >= 0)
+                        atomicAdd(p.acc + row[q], sum[q]);
             }
         }
-#pragma unroll
-        for (int q = 0; q < WEIGHT_KPT; ++q)
-            if (row[q] >= 0)
-                atomicAdd(p.acc + row[q], sum[q]);
     }
     if (!waited)
         asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -1165,7 +1182,7 @@ __device__ __forceinline__ void add_weights(const Params &p, const int cta, cons
 // The merge (fp16 output) and the recorded weights in one launch: the first
 // merge_ctas CTAs merge, BY_WARP as fa_stream_merge_rows_kernel.
 template <int D, bool BY_WARP>
-__global__ void __launch_bounds__(MERGE_THREADS) fa_merge_weights_kernel(const Params p,
+__global__ void __launch_bounds__(MERGE_THREADS, D == 128 ? 4 : 2) fa_merge_weights_kernel(const Params p,
                                                                          const int merge_ctas)
 {
     if (static_cast<int>(blockIdx.x) >= merge_ctas)
@@ -1270,20 +1287,33 @@ static bool weight_space(size_t base, int B, int tq, int Hq, int units, int sh, 
     return true;
 }
 
+static int log2_of(int x)               // -1 when x is not a power of two
+{
+    return x <= 0 || (x & (x - 1)) ? -1 : __builtin_ctz(x);
+}
+
 // The merge of an fp16 output, with the recorded weights when p.acc is set; as the
 // fp32 merge, a warp per row from MERGE_WARP_ROWS_PER_SM rows per SM.
 constexpr int MERGE_WARP_ROWS_PER_SM = 4;
 template <int D>
-static cudaError_t launch_merge_half(const Params &p, int sms, cudaStream_t st)
+static cudaError_t launch_merge_half(const Params &p0, int sms, cudaStream_t st)
 {
+    Params p = p0;
     const long long rows = (long long)p.B * (p.tq > 1 ? p.tq : 1) * p.Hq;
     const bool by_warp = rows >= (long long)MERGE_WARP_ROWS_PER_SM * sms;
     const long long merge = by_warp ? (rows + tc::MERGE_ROWS_PER_CTA - 1) / tc::MERGE_ROWS_PER_CTA
                                     : rows;
     long long ctas = merge;
     if (p.acc) {
-        const long long items = (p.cap16 + tc::WEIGHT_KEYS - 1) / tc::WEIGHT_KEYS * p.B * p.Hkv;
+        // items of up to 8 rounds, while the capacity leaves two for every SM
         const long long most = (long long)sms * 4;
+        const long long rounds = (p.cap16 + tc::WEIGHT_KEYS - 1) / tc::WEIGHT_KEYS;
+        const long long units = (long long)p.B * p.Hkv;
+        p.w_rounds = 8;
+        while (p.w_rounds > 1 && (rounds + p.w_rounds - 1) / p.w_rounds * units < 2ll * sms)
+            p.w_rounds /= 2;
+        p.lg_page = p.bt ? log2_of(p.page_size) : -1;
+        const long long items = (rounds + p.w_rounds - 1) / p.w_rounds * units;
         ctas += items < most ? items : most;
     }
     if (ctas > 0x7fffffffll)

@@ -526,10 +526,7 @@ extern "C" FA_API int fa_evict_kv(void *k_cache, void *v_cache, void *k_scales, 
     x.rows = ev::STAGE_BYTES / total / 16 * 16;
     if (x.rows > ev::ROUND_ROWS)
         x.rows = ev::ROUND_ROWS;
-    x.lg_page = -1;
-    for (int lg = 4; lg < 31; ++lg)
-        if (paged && page_size == 1 << lg)
-            x.lg_page = lg;
+    x.lg_page = log2_of(page_size);
     Params p = {};
     p.bt = block_table;
     p.seq_lens = seq_lens;

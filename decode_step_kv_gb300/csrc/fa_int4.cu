@@ -926,11 +926,6 @@ static int check_rows(const char *name, const Span *outs, int n_outs, const Span
     return 0;
 }
 
-static int log2_of(int page_size)               // -1 when it is not a power of two
-{
-    return page_size & (page_size - 1) ? -1 : __builtin_ctz(page_size);
-}
-
 static bool row_args(int T, int Hkv, int D, int page_size, const int *count, RowArgs *a)
 {
     const long long words = (long long)T * Hkv * (D / 8);
@@ -938,7 +933,7 @@ static bool row_args(int T, int Hkv, int D, int page_size, const int *count, Row
         return false;
     a->T = T;
     a->n_words = static_cast<int>(words);
-    a->lg_page = page_size > 0 ? log2_of(page_size) : -1;
+    a->lg_page = log2_of(page_size);
     a->count = count;
     return true;
 }
