@@ -1126,7 +1126,6 @@ __device__ __forceinline__ void add_weights(const Params &p, const int cta, cons
             // the scores of column group i of key t: at + i * group + t * sh
             const long long group = p.cap16 * p.sh;
             const float *at = p.ws_s + ((long long)b * p.U_b + kv * p.n_hg + x0 / p.cpu) * group;
-            const int ng = (nx + p.cpu - 1) / p.cpu;
             // (more than WEIGHT_COLS columns add to a key once per pass)
             for (int tr = static_cast<int>(t0) + threadIdx.x; tr < end; tr += WEIGHT_KEYS) {
                 int row[WEIGHT_KPT];
@@ -1136,28 +1135,28 @@ __device__ __forceinline__ void add_weights(const Params &p, const int cta, cons
                     row[q] = t >= lo && t < end ? row_at(b, kv, t) : -1;
                 }
                 float sum[WEIGHT_KPT] = {};
-                if (p.sh % 4 == 0) {                       // 4 or 8: 16-byte loads
-                    const int quads = p.sh / 4;
-                    for (int i = 0; i < ng * quads; ++i) {
-                        const float *s = at + (quads == 1 ? i : i >> 1) * group + (i & (quads - 1)) * 4 +
-                                         (long long)tr * p.sh;
+                if (p.sh % 4 == 0) {                       // 16-byte loads
+                    const float *s = at + (long long)tr * p.sh;
+                    for (int x = 0, c = 0; x < nx; x += 4) {
                         float4 v[WEIGHT_KPT];
 #pragma unroll
                         for (int q = 0; q < WEIGHT_KPT; ++q)
                             if (row[q] >= 0)
                                 v[q] = __ldcs(reinterpret_cast<const float4 *>(
-                                    s + q * WEIGHT_THREADS * p.sh));
-                        // columns past the last hold nothing: +inf weighs them 0
-                        const float4 z = reinterpret_cast<const float4 *>(lse)[i];
+                                    s + c + q * WEIGHT_THREADS * p.sh));
+                        const float4 z = *reinterpret_cast<const float4 *>(lse + x);
 #pragma unroll
                         for (int q = 0; q < WEIGHT_KPT; ++q)
                             if (row[q] >= 0) {
-                                float y = ex2_ftz(v[q].x - z.x);
-                                y += 4 * i + 1 < nx ? ex2_ftz(v[q].y - z.y) : 0.f;
-                                y += 4 * i + 2 < nx ? ex2_ftz(v[q].z - z.z) : 0.f;
-                                y += 4 * i + 3 < nx ? ex2_ftz(v[q].w - z.w) : 0.f;
-                                sum[q] += 4 * i < nx ? y : 0.f;
+                                sum[q] += ex2_ftz(v[q].x - z.x);
+                                sum[q] += x + 1 < nx ? ex2_ftz(v[q].y - z.y) : 0.f;
+                                sum[q] += x + 2 < nx ? ex2_ftz(v[q].z - z.z) : 0.f;
+                                sum[q] += x + 3 < nx ? ex2_ftz(v[q].w - z.w) : 0.f;
                             }
+                        if ((c += 4) == p.sh) {            // on to the next column group
+                            c = 0;
+                            s += group;
+                        }
                     }
                 } else {
 #pragma unroll

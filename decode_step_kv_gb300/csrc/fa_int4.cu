@@ -214,8 +214,8 @@ __global__ void __launch_bounds__(256) gather_kernel(const Params p, const RowAr
 // [2^-12, 2^7] are carried times 2^-e, a power of two per warp, so that P s
 // stays within fp16 whatever the scales.
 // Tiles are copied in batches of up to BT of one unit (cp.async, a ring of
-// batches per warp): the lanes look 32 tiles' cache rows up side by side, so a
-// tile's share of the addressing is a shuffle and three multiply-adds.  They are
+// batches per warp); the lanes look their cache rows up side by side, so a tile's
+// share of the addressing is a shuffle and three multiply-adds.  They are
 // worked on two at a time.
 #ifndef FA_I4_NW_128
 #define FA_I4_NW_128 4
@@ -295,6 +295,11 @@ __device__ __forceinline__ void sts32(uint32_t a, uint32_t v)
 {
     asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
 }
+__device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w)
+{
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w)
+                 : "memory");
+}
 __device__ __forceinline__ float lds_half(uint32_t a)
 {
     unsigned short v;
@@ -343,6 +348,50 @@ __device__ __forceinline__ int code_off(int r, int c)
     return D == 128 ? r * 64 + ((c ^ ((r >> 1) & 3)) << 4) : r * 128 + ((c ^ (r & 7)) << 4);
 }
 
+// A producer's cache rows.  The lanes of a warp look up 32 tiles of pw's unit side by
+// side (lane x: tile k + x), with the next 32 tiles' block ids already on their way.
+struct Feed {
+    int tpp;                     // tiles per page
+    int k = 0, row = -1, blk = 0;
+    unsigned have = 0;           // bit x: tile k + x is mapped
+
+    __device__ __forceinline__ Feed(const Params &p) : tpp(p.page_size / TILE) {}
+    __device__ __forceinline__ int block_of(const Params &p, const tc::Walk &pw, int x) const
+    {
+        const int ti = pw.lo / TILE + x;
+        return x < pw.n ? p.bt[(long long)pw.b * p.max_blocks + (tpp == 1 ? ti : ti / tpp)] : 0;
+    }
+    // tiles pw.k .. pw.k + 31; `next`: they follow the window before
+    __device__ __forceinline__ void window(const Params &p, const tc::Walk &pw, int left, bool next)
+    {
+        const int lane = threadIdx.x & 31;
+        const int kv = pw.j / p.n_hg, x = pw.k + lane, ti = pw.lo / TILE + x;
+        k = pw.k;
+        row = -1;
+        if (!p.bt) {
+            if (x < pw.n)
+                row = static_cast<int>(((long long)pw.b * p.Hkv + kv) * p.cap + ti * TILE);
+        } else {
+            const int id = next ? blk : block_of(p, pw, x);
+            blk = block_of(p, pw, x + 32);
+            if (x < pw.n && id >= 0 && id < p.num_blocks)
+                row = (id * p.Hkv + kv) * p.page_size + (tpp == 1 ? 0 : ti % tpp * TILE);
+            else if (lane < left && x < pw.n)    // a tile of this worker's
+                flag(FA_STATUS_BAD_BLOCK);
+        }
+        have = __ballot_sync(0xffffffffu, row >= 0);
+    }
+    // the lane that holds tile pw.k, with the N - 1 tiles after it in the next lanes
+    // (units are walked in steps of N from a window's start)
+    template <int N>
+    __device__ __forceinline__ int at(const Params &p, const tc::Walk &pw, int left)
+    {
+        if (pw.k - k > 32 - N)
+            window(p, pw, left, pw.k - k == 32);
+        return pw.k - k;
+    }
+};
+
 template <int D, bool WT>
 __global__ void __launch_bounds__(Cfg<D>::NW * 32, Cfg<D>::CTAS_PER_SM) decode_kernel(const Params p)
 {
@@ -381,34 +430,10 @@ __global__ void __launch_bounds__(Cfg<D>::NW * 32, Cfg<D>::CTAS_PER_SM) decode_k
         }
     }
 
-    // ---- producer: the next batch, pw.k .. pw.k + n - 1 of pw's unit.  The lanes
-    // look up the cache rows of 32 tiles side by side (lane x: tile f_k + x), with
-    // the next 32 tiles' block ids already on their way.
+    // ---- producer: the next batch, pw.k .. pw.k + n - 1 of pw's unit
     constexpr int BT = C::BT;
-    const int tpp = p.page_size / TILE;          // tiles per page
-    int left = n_my, f_k = 0, f_row = -1, f_blk = 0;
-    unsigned f_have = 0;                         // bit x: tile f_k + x is mapped
-    auto block_of = [&](int k) {                 // block id of tile k of pw's unit
-        const int ti = pw.lo / TILE + k;
-        return k < pw.n ? p.bt[(long long)pw.b * p.max_blocks + (tpp == 1 ? ti : ti / tpp)] : 0;
-    };
-    auto window = [&](bool next) {               // rows of tiles pw.k .. pw.k + 31
-        const int kv = pw.j / p.n_hg, k = pw.k + lane, ti = pw.lo / TILE + k;
-        f_k = pw.k;
-        f_row = -1;
-        if (!p.bt) {
-            if (k < pw.n)
-                f_row = static_cast<int>(((long long)pw.b * p.Hkv + kv) * p.cap + ti * TILE);
-        } else {
-            const int blk = next ? f_blk : block_of(k);
-            f_blk = block_of(k + 32);
-            if (k < pw.n && blk >= 0 && blk < p.num_blocks)
-                f_row = (blk * p.Hkv + kv) * p.page_size + (tpp == 1 ? 0 : ti % tpp * TILE);
-            else if (lane < left && k < pw.n)    // a tile of this worker's
-                flag(FA_STATUS_BAD_BLOCK);
-        }
-        f_have = __ballot_sync(0xffffffffu, f_row >= 0);
-    };
+    int left = n_my;
+    Feed f(p);
     constexpr int CPR = C::RB / 16;              // code chunks per row
     constexpr int NCP = TILE * CPR / 32;         // code chunks per lane and tile, K or V
     constexpr int NSC = TILE * C::SB / 16;       // scale chunks per tile, K or V
@@ -435,35 +460,33 @@ __global__ void __launch_bounds__(Cfg<D>::NW * 32, Cfg<D>::CTAS_PER_SM) decode_k
     auto put = [&] {                             // an empty group past the end
         if (left > 0) {
             const int n = min(min(BT, pw.n - pw.k), left);
-            if (pw.k - f_k > 32 - BT)
-                window(pw.k - f_k == 32);
-            const int x0 = pw.k - f_k;
-            const unsigned have = (f_have >> x0) & ((1u << n) - 1u);
+            const int x0 = f.at<BT>(p, pw, left);
+            const unsigned have = (f.have >> x0) & ((1u << n) - 1u);
             loaded = (loaded & ~(((1u << BT) - 1u) << (s_put * BT))) | have << (s_put * BT);
             const uint32_t st = ring + s_put * C::STAGE_BYTES;
             if (have == (1u << BT) - 1u) {
 #pragma unroll
                 for (int x = 0; x < BT; ++x)
-                    copy_tile(st, x, __shfl_sync(0xffffffffu, f_row, x0 + x));
+                    copy_tile(st, x, __shfl_sync(0xffffffffu, f.row, x0 + x));
             } else {
 #pragma unroll 1
                 for (int x = 0; x < n; ++x)
                     if ((have >> x) & 1u)
-                        copy_tile(st, x, __shfl_sync(0xffffffffu, f_row, x0 + x));
+                        copy_tile(st, x, __shfl_sync(0xffffffffu, f.row, x0 + x));
             }
             left -= n;
             pw.k += n;
             if (pw.k == pw.n && left > 0) {
                 --pw.k;
                 pw.next(p);
-                window(false);
+                f.window(p, pw, left, false);
             }
             s_put = s_put + 1 == S ? 0 : s_put + 1;
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
     if (n_my > 0)
-        window(false);
+        f.window(p, pw, left, false);
 #pragma unroll 1
     for (int i = 0; i < S - 1; ++i)
         put();
@@ -681,7 +704,7 @@ __global__ void __launch_bounds__(Cfg<D>::NW * 32, Cfg<D>::CTAS_PER_SM) decode_k
                 en = (ex >= -11 && ex <= 7) ? 0 : max(ex, -14);
                 vlim = __float2half2_rn(en == 0 ? 128.f : fminf(pow2(en + 2), 65504.f));
             }
-            const float a0 = ex2(mr[0] - n0), a1 = ex2(mr[1] - n1);
+            const float a0 = ex2_ftz(mr[0] - n0), a1 = ex2_ftz(mr[1] - n1);
             l[0] *= a0;
             l[1] *= a1;
             const float r0e = a0 * pow2(e - en), r1e = a1 * pow2(e - en);
@@ -706,8 +729,8 @@ __global__ void __launch_bounds__(Cfg<D>::NW * 32, Cfg<D>::CTAS_PER_SM) decode_k
         // ---- O^T += V^T . (P s)^T: rows are elements, 4 per block and lane
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const float p0 = ex2(sc[h][0] - mr[0]), p1 = ex2(sc[h][1] - mr[1]);
-            const float p2 = ex2(sc[h][2] - mr[0]), p3 = ex2(sc[h][3] - mr[1]);
+            const float p0 = ex2_ftz(sc[h][0] - mr[0]), p1 = ex2_ftz(sc[h][1] - mr[1]);
+            const float p2 = ex2_ftz(sc[h][2] - mr[0]), p3 = ex2_ftz(sc[h][3] - mr[1]);
             l[0] += p0 + p2;
             l[1] += p1 + p3;
             // P^T as the B operand: keys (2t, 2t+1) and (2t+8, 2t+9), column g
@@ -818,9 +841,537 @@ __global__ void __launch_bounds__(Cfg<D>::NW * 32, Cfg<D>::CTAS_PER_SM) decode_k
     asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
+// ------------------------------------------------- attention, many columns
+// More than 16 (query, head) columns per KV head: with 8 columns per warp every
+// group would unpack the codes again, 130 of its ~280 instructions per tile.
+// Here a CTA of four warps unpacks a tile of KT keys once into shared memory as
+// fp16 codes, and its warps share it: CW warps of 16 columns each (the mma's M:
+// S[16 columns x keys] = Q . K^T, whose accumulators are the A operand of
+// O[16 x D] += (P s) . V without a transpose) times KS = 4 / CW slices of the
+// tile's keys.  Scales are used as above, K's in fp32 after each block's mma,
+// V's on the weights.  The fp16 copies hold the code's value itself, so nothing
+// is to be taken off later.
+// Work is split as above with CTAs as workers; a unit has CW * 16 columns.
+// Bound by the mma rate: 32 of them per 16 keys, 16 columns and warp at D = 128.
+template <int D, int CW>
+struct WideCfg {
+    static constexpr int KT = D == 128 ? 64 : 32;      // keys per tile
+    static constexpr int SUB = KT / TILE;              // 16-key subtiles per tile
+    static constexpr int KS = 4 / CW;                  // key slices
+    static constexpr int SK = KT / KS;                 // keys per slice
+    static constexpr int CK = SK < 32 ? SK : 32;       // keys per softmax step
+    static constexpr int COLS = 16 * CW;
+    static constexpr int NJ = D / 32, RB = D / 2, SB = D / 16;
+    static constexpr int RAW_K = 0, RAW_V = KT * RB;   // codes as copied (swizzled rows)
+    static constexpr int SC = 2 * KT * RB;             // two stages of K scales, V scales
+    static constexpr int SC_STAGE = 2 * KT * SB;
+    static constexpr int F16_K = SC + 2 * SC_STAGE;    // codes as fp16, rows of 2 D bytes
+    static constexpr int F16_V = F16_K + KT * D * 2;
+    static constexpr int Q = F16_V + KT * D * 2;       // the unit's queries
+    static constexpr int JOIN_ML = Q + COLS * D * 2;   // slice 1's (m, l) per column
+    static constexpr int SMEM = JOIN_ML + COLS * 8;
+    static constexpr int CTAS_PER_SM = D == 128 ? 3 : 2;
+    static_assert(SK % 16 == 0, "the PV mma takes 16 keys");
+    static_assert(F16_K % 128 == 0 && Q % 128 == 0, "swizzled rows");
+    // slices are joined in the fp16 buffers: 16 columns x D floats per warp
+    static_assert(KS == 1 || CW * 16 * D * 4 <= 2 * KT * D * 2, "join buffer");
+    static_assert(CTAS_PER_SM * (SMEM + 1024) <= 228 * 1024, "shared memory per SM");
+};
+
+// Byte offset of 16-byte chunk c of row r in rows of D fp16 values.
+template <int D>
+__device__ __forceinline__ int f16_off(int r, int c)
+{
+    return r * (2 * D) + ((c ^ (r & 7)) << 4);
+}
+
+template <int D, int CW, bool WT>
+__global__ void __launch_bounds__(128, WideCfg<D, CW>::CTAS_PER_SM) wide_kernel(const Params p)
+{
+    using C = WideCfg<D, CW>;
+    constexpr int NJ = C::NJ, KT = C::KT, SUB = C::SUB, CK = C::CK, NT = CK / 8;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int g = lane >> 2, t = lane & 3;
+    const int cwi = warp % CW, ks = warp / CW;     // this warp's columns and key slice
+    const int w = blockIdx.x;
+    int b_at = -1, We = 0;
+    long long P_at = 0, T = 0, t0 = 0, t1 = 0;
+    if (!tc::stream_range(p, w, T, We, t0, t1, b_at, P_at))
+        return;                                    // the whole CTA: the range is the worker's
+
+    extern __shared__ __align__(128) unsigned char smem[];
+    const uint32_t sm = smem_u32(smem);
+    const uint64_t policy = evict_first_policy();
+
+    tc::Walk cw;
+    cw.init(p, b_at, P_at, t0, tc::UNIT_COST);
+    tc::Walk pw = cw;
+    int n_my = 0;                                  // 16-key tiles in [t0, t1)
+    {
+        tc::Walk e = cw;
+        while (e.pos() < t1) {
+            const long long us = e.unit_start();
+            const long long end = us + e.n < t1 ? us + e.n : t1;
+            n_my += static_cast<int>(end - e.pos());
+            if (us + e.n >= t1)
+                break;
+            e.k = e.n - 1;
+            e.next(p);
+        }
+    }
+    if (n_my == 0)
+        return;
+    // ---- copies: warp x takes subtile x % SUB (at D = 256 its K with warps 0 and 1,
+    // its V with 2 and 3)
+    const int sub = warp % SUB;
+    const bool does_k = warp < SUB, does_v = SUB == 4 || warp >= SUB;
+    constexpr int CPR = C::RB / 16, NCP = TILE * CPR / 32, NSC = TILE * C::SB / 16;
+    int left = n_my;
+    unsigned mapped = 0;                           // SUB bits per stage: its mapped subtiles
+    Feed f(p);
+    uint32_t c_dst[NCP];
+#pragma unroll
+    for (int i = 0; i < NCP; ++i)
+        c_dst[i] = sm + sub * TILE * C::RB + code_off<D>((lane + 32 * i) / CPR, (lane + 32 * i) % CPR);
+    auto copy = [&](int stage) {                   // the next tile of pw's unit
+        const int nb = min(min(SUB, pw.n - pw.k), left);
+        const int x0 = f.at<SUB>(p, pw, left);
+        const unsigned have = (f.have >> x0) & ((1u << nb) - 1u);
+        mapped = (mapped & ~(((1u << SUB) - 1u) << (stage * SUB))) | have << (stage * SUB);
+        const long long row = __shfl_sync(0xffffffffu, f.row, x0 + sub);
+        if ((have >> sub) & 1u) {
+            const char *kp = p.k + row * C::RB + lane * 16, *vp = p.v + row * C::RB + lane * 16;
+#pragma unroll
+            for (int i = 0; i < NCP; ++i) {
+                if (does_k)
+                    cp16(c_dst[i] + C::RAW_K, kp + i * 512, policy);
+                if (does_v)
+                    cp16(c_dst[i] + C::RAW_V, vp + i * 512, policy);
+            }
+            const uint32_t sc = sm + C::SC + stage * C::SC_STAGE + sub * TILE * C::SB;
+            if (does_k && lane < NSC)
+                cp16(sc + lane * 16, p.ks + row * C::SB + lane * 16, policy);
+            if (does_v && lane >= 16 && lane < 16 + NSC)
+                cp16(sc + KT * C::SB + (lane - 16) * 16, p.vs + row * C::SB + (lane - 16) * 16,
+                     policy);
+        }
+        left -= nb;
+        pw.k += nb;
+        if (pw.k == pw.n && left > 0) {
+            --pw.k;
+            pw.next(p);
+            f.window(p, pw, left, false);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    f.window(p, pw, left, false);
+
+    // ---- the unit's queries in shared memory; every 8 elements in the order 0, 4,
+    // 1, 5, 2, 6, 3, 7 that unpacking a word of codes gives
+    const int tq = p.tq > 1 ? p.tq : 1;
+    int nh = 0, clo[2], chi[2], all_lo = 0, all_hi = 0, base = 0;
+    auto load_q = [&] {
+        base = cw.tok();
+        const int kv = cw.j / p.n_hg, cg = cw.j % p.n_hg;
+        nh = min(C::COLS, tq * p.G - cg * C::COLS);
+        for (int i = tid; i < C::COLS * (D / 8); i += 128) {
+            const int r = i / (D / 8), c = i % (D / 8);
+            const tc::Col q = tc::column(p, kv, cg, r, C::COLS);
+            uint4 x = make_uint4(0u, 0u, 0u, 0u);
+            if (q.live)
+                x = __ldg(reinterpret_cast<const uint4 *>(
+                              p.q + (((long long)cw.b * tq + q.j) * p.Hq + q.h) * D) + c);
+            const uint4 y = make_uint4(__byte_perm(x.x, x.z, 0x5410), __byte_perm(x.x, x.z, 0x7632),
+                                       __byte_perm(x.y, x.w, 0x5410), __byte_perm(x.y, x.w, 0x7632));
+            *reinterpret_cast<uint4 *>(smem + C::Q + f16_off<D>(r, c)) = y;
+        }
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const tc::Col c = tc::column(p, kv, cg, cwi * 16 + g + 8 * x, C::COLS);
+            tc::column_range(p, cw.b, cw.hi, c.live ? c.j : tq - 1, clo[x], chi[x]);
+        }
+        int x0;
+        tc::column_range(p, cw.b, cw.hi, tq - 1, all_lo, x0);   // keys every query attends
+        tc::column_range(p, cw.b, cw.hi, 0, x0, all_hi);
+    };
+
+    // [n]: columns g (0, 1) and g + 8 (2, 3), elements 8n + t (0, 2) and 8n + t + 4
+    float acc[D / 8][4];
+    float mr[2], l[2];
+    int e = 0;                // O is held times 2^-e
+    __half2 vlim;             // V scales above it call for another e
+    auto reset = [&] {
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i)
+            acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+        mr[0] = mr[1] = NO_MAX;
+        l[0] = l[1] = 0.f;
+        e = 0;
+        vlim = __float2half2_rn(0.f);
+    };
+    // ---- this lane's places.  Chunk c of row r lies at (c ^ (r & 7)) * 16, so a lane
+    // needs one address per value of c's low three bits; the rest are constants.
+    // Unpacking: two code chunks of one key, K's and V's alike.
+    uint32_t raw_a[2], f16_a[2][2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        const int key = tid % KT, c = tid / KT + x * (128 / KT);
+        const int o = D == 128 ? c : c / 2;         // octet of the chunk's four words
+        raw_a[x] = sm + C::RAW_K + code_off<D>(key, c);
+#pragma unroll
+        for (int z = 0; z < 2; ++z)
+            f16_a[x][z] = sm + C::F16_K + f16_off<D>(key, 4 * z + o) +
+                          (D == 256 ? (c & 1) * 256 : 0);
+    }
+    // ldmatrix: queries (16 rows, two chunks), K (8 rows, four chunks), V (16 rows, two)
+    uint32_t q_a[4], k_a[2], v_a[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+        q_a[x] = sm + C::Q + f16_off<D>(cwi * 16 + (lane & 15), 2 * x + (lane >> 4));
+        v_a[x] = sm + C::F16_V + f16_off<D>(lane & 15, 2 * x + (lane >> 4));
+        k_a[x & 1] = sm + C::F16_K + f16_off<D>(lane & 7, 4 * (x & 1) + (lane >> 3));
+    }
+    copy(0);
+    load_q();
+    reset();
+
+    int stage = 0;
+    for (int i = 0; i < n_my;) {
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        __syncthreads();      // the tile has landed; every warp is done with the one before
+        const int nb = min(min(SUB, cw.n - cw.k), n_my - i);
+        const unsigned have = (mapped >> (stage * SUB)) & ((1u << SUB) - 1u);
+        const uint32_t sc = sm + C::SC + stage * C::SC_STAGE;
+        const bool edge = base < all_lo || base + KT > all_hi || have != (1u << SUB) - 1u;
+        auto there = [&](int k) {                  // key k of the tile is attended by someone
+            return k >= cw.lo - base && k < cw.hi - base && ((have >> (k / TILE)) & 1u);
+        };
+        if (edge) {
+            // other rows must not turn a zero weight into NaN
+            for (int x = tid; x < KT * NJ / 2; x += 128)
+                if (!there(x / (NJ / 2))) {
+                    sts32(sc + x * 4, 0u);
+                    sts32(sc + KT * C::SB + x * 4, 0u);
+                }
+        }
+        // ---- unpack: a word of codes is one 16-byte chunk of fp16 values.  8 lanes
+        // take the same octet of 8 keys, so reads and writes meet no bank twice.
+        {
+            const __half2 b1032 = __float2half2_rn(1032.f), b72 = __float2half2_rn(72.f);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {                   // K, K, V, V
+                const uint4 v = lds128(raw_a[x & 1] + (x >> 1) * (C::RAW_V - C::RAW_K));
+                const uint32_t wds[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const uint32_t a = wds[q], h = wds[q] >> 8;
+                    auto even = [&](uint32_t z) {
+                        return as_u32(__hsub2(as_half2((z & 0x000f000fu) | 0x64006400u), b1032));
+                    };
+                    auto odd = [&](uint32_t z) {
+                        return as_u32(__hsub2(as_half2((z & 0x00f000f0u) | 0x54005400u), b72));
+                    };
+                    sts128(f16_a[x & 1][q & 1] + (x >> 1) * (C::F16_V - C::F16_K) + (q >> 1) * 128,
+                           even(a), odd(a), even(h), odd(h));
+                }
+            }
+        }
+        __syncthreads();
+        i += nb;
+        const bool seg_end = cw.k + nb == cw.n || i == n_my;
+        if (i < n_my)
+            copy(stage ^ 1);
+
+        const int k_lo = ks * C::SK;               // this warp's keys of the tile
+#pragma unroll 1
+        for (int kk = k_lo; kk < k_lo + C::SK && kk < nb * TILE; kk += CK) {
+            // ---- scores: 8 keys per mma, blocks of 32 elements scaled in fp32
+            float sc4[NT][4];
+            float kscale[NT][2][4];
+#pragma unroll
+            for (int jj = 0; jj < NJ; jj += 4) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const uint2 u = lds64(sc + (kk + 8 * n + 2 * t + x) * C::SB + jj * 2);
+                        const float2 f0 = __half22float2(as_half2(u.x));
+                        const float2 f1 = __half22float2(as_half2(u.y));
+                        kscale[n][x][0] = f0.x; kscale[n][x][1] = f0.y;
+                        kscale[n][x][2] = f1.x; kscale[n][x][3] = f1.y;
+                    }
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int j = jj + q;
+                    // A: 16 columns x 32 elements (chunks 4j .. 4j+3)
+                    uint32_t a[2][4];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        tc::ldsm_x4(q_a[(2 * j + h) & 3] + (j >> 1) * 128, a[h][0], a[h][1], a[h][2],
+                                    a[h][3]);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        // B: 8 keys x 32 elements
+                        uint32_t k0, k1, k2, k3;
+                        tc::ldsm_x4(k_a[j & 1] + kk * (2 * D) + n * (16 * D) + (j >> 1) * 128, k0,
+                                    k1, k2, k3);
+                        float d[4];
+                        mma_zero(d, a[0][0], a[0][1], a[0][2], a[0][3], k0, k1);
+                        tc::mma16816(d, a[1][0], a[1][1], a[1][2], a[1][3], k2, k3);
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            sc4[n][x] = j ? fmaf(d[x], kscale[n][x & 1][q], sc4[n][x])
+                                          : d[x] * kscale[n][x & 1][q];
+                    }
+                }
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    sc4[n][x] *= p.c2;                     // log2 units
+            if (edge) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const int kt = kk + 8 * n + 2 * t + (x & 1), k = base + kt;
+                        if (k < clo[x >> 1] || k >= chi[x >> 1] || !((have >> (kt / TILE)) & 1u))
+                            sc4[n][x] = -INFINITY;
+                    }
+            }
+            if constexpr (WT) {
+                // [unit][key][column]: 8 lanes write 8 neighbouring columns
+                const int col = cwi * 16 + g;
+                float *at = p.ws_s + (cw.unit(p) * p.cap16 + base + kk + 2 * t) * p.sh + col;
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    if (!((have >> ((kk + 8 * n) / TILE)) & 1u))
+                        continue;
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        float *a = at + (8 * n + x) * p.sh;
+                        if (col < nh)
+                            a[0] = sc4[n][x];
+                        if (col + 8 < nh)
+                            a[8] = sc4[n][x + 2];
+                    }
+                }
+            }
+            // ---- online softmax (as above: the maximum moves when passed by 8)
+            __half2 vm = __float2half2_rn(0.f);
+            constexpr int NVW = CK * NJ / 2 / 32;
+#pragma unroll
+            for (int q = 0; q < (NVW > 0 ? NVW : 1); ++q)
+                if (NVW > 0 || lane < CK * NJ / 2)
+                    vm = __hmax2(vm, as_half2(lds32(sc + KT * C::SB + kk * C::SB +
+                                                    (lane + 32 * q) * 4)));
+            float x0 = sc4[0][0], x1 = sc4[0][2];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                x0 = fmaxf(x0, fmaxf(sc4[n][0], sc4[n][1]));
+                x1 = fmaxf(x1, fmaxf(sc4[n][2], sc4[n][3]));
+            }
+            const bool over = fmaxf(x0 - mr[0], x1 - mr[1]) > MAX_SLACK || !__hble2(vm, vlim);
+            if (__any_sync(0xffffffffu, over)) {
+                float vx = __half2float(__hmax(__low2half(vm), __high2half(vm)));
+#pragma unroll
+                for (int mask = 1; mask <= 16; mask <<= 1) {
+                    if (mask <= 2) {
+                        x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, mask));
+                        x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, mask));
+                    }
+                    vx = fmaxf(vx, __shfl_xor_sync(0xffffffffu, vx, mask));
+                }
+                const float n0 = fmaxf(mr[0], x0), n1 = fmaxf(mr[1], x1);
+                int en = e;
+                if (vx > __low2float(vlim)) {
+                    const int ex = static_cast<int>((__float_as_uint(vx) >> 23) & 255u) - 126;
+                    en = (ex >= -11 && ex <= 7) ? 0 : max(ex, -14);
+                    vlim = __float2half2_rn(en == 0 ? 128.f : fminf(pow2(en + 2), 65504.f));
+                }
+                const float a0 = ex2_ftz(mr[0] - n0), a1 = ex2_ftz(mr[1] - n1);
+                l[0] *= a0;
+                l[1] *= a1;
+                const float r0 = a0 * pow2(e - en), r1 = a1 * pow2(e - en);
+#pragma unroll
+                for (int ii = 0; ii < D / 8; ++ii) {
+                    acc[ii][0] *= r0;
+                    acc[ii][1] *= r0;
+                    acc[ii][2] *= r1;
+                    acc[ii][3] *= r1;
+                }
+                mr[0] = n0;
+                mr[1] = n1;
+                e = en;
+            }
+            // ---- O += (P s) . V, 16 keys at a time
+#pragma unroll
+            for (int m = 0; m < CK / 16; ++m) {
+                uint32_t pa[4];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float *s = sc4[2 * m + h];
+                    const float p0 = ex2_ftz(s[0] - mr[0]), p1 = ex2_ftz(s[1] - mr[0]);
+                    const float p2 = ex2_ftz(s[2] - mr[1]), p3 = ex2_ftz(s[3] - mr[1]);
+                    l[0] += p0 + p1;
+                    l[1] += p2 + p3;
+                    pa[2 * h] = tc::pack_half2(p0, p1);
+                    pa[2 * h + 1] = tc::pack_half2(p2, p3);
+                }
+                // V scales as half2 over the key pairs (2t, 2t+1) and (2t+8, 2t+9)
+                __half2 sv[2][NJ];
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    uint32_t u[NJ];
+#pragma unroll
+                    for (int q = 0; q < NJ / 4; ++q) {
+                        const uint4 v = lds128(sc + KT * C::SB +
+                                               (kk + 16 * m + 8 * x + 2 * t) * C::SB + q * 16);
+                        u[4 * q] = v.x; u[4 * q + 1] = v.y; u[4 * q + 2] = v.z; u[4 * q + 3] = v.w;
+                    }
+#pragma unroll
+                    for (int j = 0; j < NJ; ++j)
+                        sv[x][j] = as_half2(__byte_perm(u[j / 2], u[NJ / 2 + j / 2],
+                                                        j & 1 ? 0x7632 : 0x5410));
+                }
+                if (e != 0) {
+                    const __half2 f2 = __float2half2_rn(pow2(-e));
+#pragma unroll
+                    for (int x = 0; x < 2; ++x)
+#pragma unroll
+                        for (int j = 0; j < NJ; ++j)
+                            sv[x][j] = __hmul2(sv[x][j], f2);
+                }
+#pragma unroll
+                for (int j = 0; j < NJ; ++j) {
+                    const uint32_t a0 = as_u32(__hmul2(as_half2(pa[0]), sv[0][j]));
+                    const uint32_t a1 = as_u32(__hmul2(as_half2(pa[1]), sv[0][j]));
+                    const uint32_t a2 = as_u32(__hmul2(as_half2(pa[2]), sv[1][j]));
+                    const uint32_t a3 = as_u32(__hmul2(as_half2(pa[3]), sv[1][j]));
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        // B: 16 keys x elements 32j + 16h .. + 15
+                        uint32_t v0, v1, v2, v3;
+                        tc::ldsm_x4_t(v_a[(2 * j + h) & 3] + kk * (2 * D) + m * (32 * D) +
+                                          (j >> 1) * 128,
+                                      v0, v1, v2, v3);
+                        tc::mma16816(acc[4 * j + 2 * h], a0, a1, a2, a3, v0, v1);
+                        tc::mma16816(acc[4 * j + 2 * h + 1], a0, a1, a2, a3, v2, v3);
+                    }
+                }
+            }
+        }
+        stage ^= 1;
+        cw.k += nb;
+        base += nb * TILE;
+        if (!seg_end)
+            continue;
+
+        // ---- end of this worker's segment of the unit
+#pragma unroll
+        for (int mask = 1; mask <= 2; mask <<= 1) {
+            l[0] += __shfl_xor_sync(0xffffffffu, l[0], mask);
+            l[1] += __shfl_xor_sync(0xffffffffu, l[1], mask);
+        }
+        const float up = pow2(e);
+        if constexpr (C::KS == 2) {
+            // slice 1 hands its sums to slice 0 through the fp16 buffers
+            float *join = reinterpret_cast<float *>(smem + C::F16_K) + cwi * (16 * D);
+            float *join_ml = reinterpret_cast<float *>(smem + C::JOIN_ML) + (cwi * 8 + g) * 4;
+            __syncthreads();
+            if (ks == 1) {
+#pragma unroll
+                for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                        join[(n * 4 + x) * 32 + lane] = acc[n][x] * up;
+                if (t == 0) {
+                    join_ml[0] = mr[0];
+                    join_ml[1] = l[0];
+                    join_ml[2] = mr[1];
+                    join_ml[3] = l[1];
+                }
+            }
+            __syncthreads();
+            if (ks == 0) {
+                float f0[2], f1[2];
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const float m1 = join_ml[2 * x], l1 = join_ml[2 * x + 1];
+                    const float m = fmaxf(mr[x], m1);
+                    f0[x] = ex2_ftz(mr[x] - m);
+                    f1[x] = ex2_ftz(m1 - m);
+                    l[x] = l[x] * f0[x] + l1 * f1[x];
+                    mr[x] = m;
+                }
+#pragma unroll
+                for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                        acc[n][x] = acc[n][x] * (up * f0[x >> 1]) +
+                                    join[(n * 4 + x) * 32 + lane] * f1[x >> 1];
+            }
+            // (the next tile's unpacking starts after a barrier)
+        }
+        if (ks == 0) {
+            const float un = C::KS == 2 ? 1.f : up;
+            const long long us = cw.unit_start();
+            const bool whole = tc::worker_of(us, T, We) == tc::worker_of(us + cw.n - 1, T, We);
+            const int kv = cw.j / p.n_hg, cg = cw.j % p.n_hg;
+            const long long slot = w + cw.unit(p);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const int c = cwi * 16 + g + 8 * x;
+                if (c >= nh)
+                    continue;
+                const float mx = mr[x] == NO_MAX ? -INFINITY : mr[x];
+                if (whole) {
+                    const tc::Col cc = tc::column(p, kv, cg, c, C::COLS);
+                    const long long r = ((long long)cw.b * tq + cc.j) * p.Hq + cc.h;
+                    const float inv = l[x] > 0.f ? un / l[x] : 0.f;
+                    __half *o = reinterpret_cast<__half *>(p.out) + r * D + t;
+#pragma unroll
+                    for (int n = 0; n < D / 8; ++n) {
+                        o[8 * n] = __float2half_rn(acc[n][2 * x] * inv);
+                        o[8 * n + 4] = __float2half_rn(acc[n][2 * x + 1] * inv);
+                    }
+                    if (WT && t == 0)
+                        p.lse[r] = l[x] > 0.f ? mx + log2f(l[x]) : -INFINITY;
+                } else {
+                    float *o = p.ws_o + (slot * p.sh + c) * D + t;
+#pragma unroll
+                    for (int n = 0; n < D / 8; ++n) {
+                        o[8 * n] = acc[n][2 * x] * un;
+                        o[8 * n + 4] = acc[n][2 * x + 1] * un;
+                    }
+                    if (t == 0)
+                        p.ws_ml[slot * p.sh + c] = make_float2(mx, l[x]);
+                }
+            }
+        }
+        reset();
+        if (i < n_my) {
+            if (cw.k == cw.n) {
+                --cw.k;
+                cw.next(p);
+            }
+            __syncthreads();                       // every warp is done with the queries
+            load_q();                              // read after the next barriers
+        }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
 // ---------------------------------------------------------------- host side
+// Columns per KV head from which the kernel with a shared unpacked tile is taken: at
+// 16 the two cost the same per key (two groups' unpacking against half-idle warps).
+constexpr int WIDE_MIN_COLS = 17;
+
 struct Plan {
-    int ctas, W, n_hg, units, sh;
+    int ctas, W, n_hg, units, sh, cpu;
     size_t bytes;                // partial slots and prefix
 };
 
@@ -828,12 +1379,19 @@ static Plan make_plan(int B, int tq, int Hq, int Hkv, int D, long long cap, int 
 {
     Plan pl = {};
     const int cols = tq * (Hq / Hkv);
-    pl.n_hg = (cols + GPH - 1) / GPH;
-    pl.sh = cols < GPH ? cols : GPH;
+    pl.cpu = cols < WIDE_MIN_COLS ? GPH : cols <= 32 ? 32 : 64;
+    pl.n_hg = (cols + pl.cpu - 1) / pl.cpu;
+    pl.sh = cols < pl.cpu ? cols : pl.cpu;
     pl.units = Hkv * pl.n_hg;
-    const int nw = D == 128 ? Cfg<128>::NW : Cfg<256>::NW;
-    const int cps = D == 128 ? Cfg<128>::CTAS_PER_SM : Cfg<256>::CTAS_PER_SM;
-    // one persistent wave, capped at a warp per position the capacity allows
+    int nw, cps;                 // workers per CTA, CTAs per SM
+    if (pl.cpu == GPH) {
+        nw = D == 128 ? Cfg<128>::NW : Cfg<256>::NW;
+        cps = D == 128 ? Cfg<128>::CTAS_PER_SM : Cfg<256>::CTAS_PER_SM;
+    } else {
+        nw = 1;
+        cps = D == 128 ? WideCfg<128, 4>::CTAS_PER_SM : WideCfg<256, 4>::CTAS_PER_SM;
+    }
+    // one persistent wave, capped at a worker per position the capacity allows
     const long long most = ((long long)B * pl.units * ((cap + TILE - 1) / TILE + tc::UNIT_COST) +
                             nw - 1) / nw;
     const long long wave = (long long)sms * cps;
@@ -851,11 +1409,13 @@ static bool sizes_ok(int batch, int tq, int Hq, int Hkv, int D)
            Hkv <= 4096 && Hq % Hkv == 0 && Hq / Hkv <= 64 && (D == 128 || D == 256);
 }
 
-template <int D, bool WT>
-static cudaError_t launch(const Params &p, int ctas, int sms, cudaStream_t st)
+// Launches `kernel` after letting it use `smem` bytes of shared memory (once per
+// device).
+template <typename K>
+static cudaError_t launch_split(K kernel, bool (&done)[64], const Params &p, int ctas, int threads,
+                                int smem, cudaStream_t st)
 {
     static std::mutex mu;
-    static bool done[64] = {false};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess)
@@ -863,18 +1423,29 @@ static cudaError_t launch(const Params &p, int ctas, int sms, cudaStream_t st)
     {
         std::lock_guard<std::mutex> lock(mu);
         if (dev >= 64 || !done[dev]) {
-            e = cudaFuncSetAttribute(decode_kernel<D, WT>,
-                                     cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::SMEM);
+            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
             if (e != cudaSuccess)
                 return e;
             if (dev < 64)
                 done[dev] = true;
         }
     }
-    decode_kernel<D, WT><<<ctas, Cfg<D>::NW * 32, Cfg<D>::SMEM, st>>>(p);
-    if ((e = cudaGetLastError()) != cudaSuccess)
-        return e;
-    return launch_merge_half<D>(p, sms, st);
+    kernel<<<ctas, threads, smem, st>>>(p);
+    return cudaGetLastError();
+}
+
+template <int D, bool WT>
+static cudaError_t launch(const Params &p, int ctas, int sms, cudaStream_t st)
+{
+    static bool done[3][64] = {};
+    cudaError_t e;
+    if (p.cpu == GPH)
+        e = launch_split(decode_kernel<D, WT>, done[0], p, ctas, Cfg<D>::NW * 32, Cfg<D>::SMEM, st);
+    else if (p.cpu == 32)
+        e = launch_split(wide_kernel<D, 2, WT>, done[1], p, ctas, 128, WideCfg<D, 2>::SMEM, st);
+    else
+        e = launch_split(wide_kernel<D, 4, WT>, done[2], p, ctas, 128, WideCfg<D, 4>::SMEM, st);
+    return e == cudaSuccess ? launch_merge_half<D>(p, sms, st) : e;
 }
 
 // The checks of a cache's layout that append, gather and decode share.
@@ -1182,7 +1753,7 @@ FA_API int fa_decode_int4(const void *q, const void *k_codes, const void *k_scal
     p.W = pl.W;
     p.U_b = pl.units;
     p.sh = pl.sh;
-    p.cpu = i4::GPH;
+    p.cpu = pl.cpu;
     if (acc) {
         p.acc = acc;
         p.lse = reinterpret_cast<float *>(static_cast<char *>(workspace) + wsp.lse);

@@ -163,6 +163,66 @@ def test_several_queries(D, tq, Hq, Hkv, windowed):
 
 
 @pytest.mark.parametrize("D", [128, 256])
+@pytest.mark.parametrize("tq,Hq,Hkv", [(16, 1, 1), (17, 1, 1), (3, 16, 2), (31, 2, 2), (8, 8, 2), (11, 3, 1),
+                                       (21, 3, 1), (16, 8, 2), (13, 20, 4), (26, 5, 1), (256, 1, 1)])
+def test_many_columns(D, tq, Hq, Hkv):
+    """Around and beyond 16, 32 and 64 (query, head) columns per KV head."""
+    lens = [700, 3, 65, 64, 0, 290]
+    lay = Layout(len(lens), Hkv, 704, True, 16, seed=tq)
+    window = [0, 2, 20, 0, 5, 33] if tq % 2 else None
+    check(lay, Int4Cache(lay, D, lens, seed=Hq), queries(len(lens), tq, Hq, D, tq), lens, Hq, D ** -0.5,
+          window)
+
+
+@pytest.mark.parametrize("D", [128, 256])
+@pytest.mark.parametrize("paged,page", [(False, 16), (True, 16), (True, 80)])
+def test_many_columns_layouts_and_magnitudes(D, paged, page):
+    """Long enough to be split over workers; V from tiny to large along the sequence."""
+    lens = [3000, 1111, 16, 2999]
+    lay = Layout(4, 2, 3040, paged, page, seed=1)
+    ramp = np.ones((*lay.rows, 1))
+    for b, n in enumerate(lens):
+        d = np.ones((2, lay.cap, 1))
+        d[:, :n, 0] = 2.0 ** np.linspace(-20 + 4 * b, 12, n)
+        lay.put(ramp, b, d)
+    cache = Int4Cache(lay, D, lens, seed=2, v_mag=ramp)
+    for tq, Hq in ((5, 8), (12, 8)):
+        check(lay, cache, queries(4, tq, Hq, D, tq, mag=1.5), lens, Hq, D ** -0.5)
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.3, 2.0])
+def test_many_columns_scales(scale):
+    lens = [300, 19]
+    lay = Layout(2, 2, 304, False)
+    check(lay, Int4Cache(lay, 128, lens, seed=8), queries(2, 7, 8, 128, 5), lens, 8, scale)
+
+
+@pytest.mark.parametrize("tq,Hq", [(1, 4), (8, 8), (32, 4)])
+def test_rows_outside_the_ranges_may_hold_anything(tq, Hq):
+    """Rows before the window and in unmapped blocks: NaN scales, out-of-range ids."""
+    lens = [200, 133]
+    lay = Layout(2, 2, 208, True, seed=9)
+    cache = Int4Cache(lay, 128, lens, seed=9)
+    q = queries(2, tq, Hq, 128, 9)
+    window = [40, 17]
+    want, absum, size, _ = attend(q, cache.key, cache.value, lens, lay, 0.1, window)
+    for b, (n, w) in enumerate(zip(lens, window)):
+        first = n - tq + 1 - w                          # the first key any query attends
+        for s in (cache.ks, cache.vs):
+            d = lay.dense(s, b).copy()
+            d[:, :first] = np.nan
+            lay.put(s, b, d)
+        lay.table[b, :first // 16] = 2 ** 30
+        lay.table[b, -(-n // 16):] = -5
+    fa.fa_decode_device_status()
+    acc = torch.zeros(lay.rows, device="cuda")
+    got = run(lay, cache, q, lens, Hq, 0.1, window, acc=acc).cpu().numpy()
+    assert fa.fa_decode_device_status() == 0
+    assert np.all(np.abs(got - want) <= cache.tolerance(want, absum, size))
+    assert abs(float(acc.sum()) - 2 * tq * Hq) < 1e-3
+
+
+@pytest.mark.parametrize("D", [128, 256])
 def test_windows(D):
     lens = [400, 17, 64, 399, 1]
     lay = Layout(5, 2, 400, True, 16, seed=4)
@@ -240,11 +300,12 @@ def test_long_sequences_split_over_the_gpu():
     check(lay, Int4Cache(lay, 128, lens, seed=1), queries(3, 1, 16, 128, 4), lens, 16, 128 ** -0.5)
 
 
-def test_bad_blocks_and_lengths_are_flagged():
+@pytest.mark.parametrize("tq", [1, 9])
+def test_bad_blocks_and_lengths_are_flagged(tq):
     lens = [64, 64]
     lay = Layout(2, 2, 64, True, seed=1)
     cache = Int4Cache(lay, 128, lens, seed=1)
-    q = queries(2, 1, 4, 128, 1)
+    q = queries(2, tq, 4, 128, 1)
     fa.fa_decode_device_status()
     good = run(lay, cache, q, [64, 64], 4, 0.1)
     over = run(lay, cache, q, [10 ** 6, -3], 4, 0.1)
@@ -255,12 +316,13 @@ def test_bad_blocks_and_lengths_are_flagged():
     got = run(lay, cache, q, [64, 64], 4, 0.1, acc=acc)
     assert fa.fa_decode_device_status() == fa.FA_STATUS_BAD_BLOCK
     assert torch.equal(got[0], good[0])
-    keep = np.r_[0:32, 48:64]
-    kb, vb = cache.key(1)[:, keep], cache.value(1)[:, keep]
-    sub = Layout(1, 2, 48, False)
-    want, absum, size, _ = attend(q[1:], lambda b: kb, lambda b: vb, [48], sub, 0.1)
-    assert np.all(np.abs(got[1:].cpu().numpy() - want) <= cache.tolerance(want, absum, size))
-    assert abs(float(acc.sum()) - 2 * 4) < 1e-4     # every (sequence, head) row sums to 1
+    if tq == 1:
+        keep = np.r_[0:32, 48:64]
+        kb, vb = cache.key(1)[:, keep], cache.value(1)[:, keep]
+        sub = Layout(1, 2, 48, False)
+        want, absum, size, _ = attend(q[1:], lambda b: kb, lambda b: vb, [48], sub, 0.1)
+        assert np.all(np.abs(got[1:].cpu().numpy() - want) <= cache.tolerance(want, absum, size))
+    assert abs(float(acc.sum()) - 2 * 4 * tq) < 1e-3     # every (query, head) row sums to 1
 
 
 def test_stream_graph_and_new_lengths():
