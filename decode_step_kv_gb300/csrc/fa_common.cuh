@@ -64,7 +64,8 @@ struct Params {
     int n_slots;
     int cl_ctas;      // cluster plan: CTAs per cluster (1, 2, 4 or 8)
     float *lse;       // recorded weights: [B*tq*Hq] log2-sum-exp2 of each row (-inf: no key)
-    float *ws_s;      // recorded weights: [B*units][cap16][sh] scores in log2 units
+    float *ws_s;      // recorded weights: scores in log2 units, of units of 8 columns
+                      // [B*units][cap16][sh], of wider ones [B*units][cap16/16][sh][16 keys]
     float *acc;       // recorded weights: the running total of every cache row
     long long cap16;  // recorded weights: capacity rounded up to whole tiles
     int lg_page;      // recorded weights: log2 of page_size, or -1
@@ -1043,7 +1044,6 @@ __device__ __forceinline__ void add_weights(const Params &p, const int cta, cons
     __shared__ __align__(16) float lse[WEIGHT_COLS];
     const int tq = p.tq > 1 ? p.tq : 1;
     const int cols = tq * p.G;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int item_keys = WEIGHT_KEYS * p.w_rounds;
     const int chunks = static_cast<int>((p.cap16 + item_keys - 1) / item_keys);
     const long long items = (long long)chunks * p.B * p.Hkv;
@@ -1089,19 +1089,19 @@ __device__ __forceinline__ void add_weights(const Params &p, const int cta, cons
         for (int x0 = 0; x0 < cols; x0 += WEIGHT_COLS) {
             const int nx = min(WEIGHT_COLS, cols - x0);
             __syncthreads();
-            // a warp per column: its row's log-sum-exp, +inf where it has no key
-            for (int i = warp; i < nx; i += WEIGHT_THREADS / 32) {
+            // 32 lanes per column, or 4 when there are many: its row's log-sum-exp, +inf
+            // where it has no key
+            const int lpc = nx > 8 ? 4 : 32;
+            for (int i0 = 0; i0 < nx; i0 += WEIGHT_THREADS / lpc) {
+                const int i = min(i0 + static_cast<int>(threadIdx.x) / lpc, nx - 1);
                 const int x = x0 + i, j = kv * p.n_hg + x / p.cpu;
                 const long long us = P + (long long)j * (n + UNIT_COST) + UNIT_COST;
                 const int wf = worker_of(us, T, We), wl = worker_of(us + n - 1, T, We);
-                float v;
-                if (wf == wl) {
-                    v = p.lse[((long long)b * tq + x / p.G) * p.Hq + kv * p.G + x % p.G];
-                } else {
+                float M = -INFINITY, L = 0.f;
+                if (wf < wl) {
                     const float2 *ml = p.ws_ml + ((long long)wf + (long long)b * p.U_b + j) * p.sh +
                                        x % p.cpu;
-                    float M = -INFINITY, L = 0.f;
-                    for (int s = lane; s <= wl - wf; s += 32) {
+                    for (int s = threadIdx.x % lpc; s <= wl - wf; s += lpc) {
                         const float2 y = ml[(long long)s * p.sh];
                         if (y.x == -INFINITY)
                             continue;
@@ -1109,33 +1109,46 @@ __device__ __forceinline__ void add_weights(const Params &p, const int cta, cons
                         L = L * ex2(M - m) + y.y * ex2(y.x - m);
                         M = m;
                     }
-                    float Mw = M;
-#pragma unroll
-                    for (int off = 16; off >= 1; off >>= 1)
-                        Mw = fmaxf(Mw, __shfl_xor_sync(0xffffffffu, Mw, off));
-                    L = M == -INFINITY ? 0.f : L * ex2(M - Mw);
-#pragma unroll
-                    for (int off = 16; off >= 1; off >>= 1)
-                        L += __shfl_xor_sync(0xffffffffu, L, off);
-                    v = L > 0.f ? Mw + log2f(L) : -INFINITY;
                 }
-                if (lane == 0)
-                    lse[i] = v == -INFINITY ? INFINITY : v;
+                float Mw = M;
+                for (int off = lpc / 2; off >= 1; off >>= 1)
+                    Mw = fmaxf(Mw, __shfl_xor_sync(0xffffffffu, Mw, off));
+                L = M == -INFINITY ? 0.f : L * ex2(M - Mw);
+                for (int off = lpc / 2; off >= 1; off >>= 1)
+                    L += __shfl_xor_sync(0xffffffffu, L, off);
+                float v = L > 0.f ? Mw + log2f(L) : -INFINITY;
+                if (wf == wl)
+                    v = p.lse[((long long)b * tq + x / p.G) * p.Hq + kv * p.G + x % p.G];
+                lse[i] = v == -INFINITY ? INFINITY : v;    // the same value by all its lanes
             }
             __syncthreads();
-            // the scores of column group i of key t: at + i * group + t * sh
-            const long long group = p.cap16 * p.sh;
+            const long long group = p.cap16 * p.sh;        // one column group's scores
             const float *at = p.ws_s + ((long long)b * p.U_b + kv * p.n_hg + x0 / p.cpu) * group;
             // (more than WEIGHT_COLS columns add to a key once per pass)
             for (int tr = static_cast<int>(t0) + threadIdx.x; tr < end; tr += WEIGHT_KEYS) {
                 int row[WEIGHT_KPT];
+                float sum[WEIGHT_KPT] = {};
 #pragma unroll
                 for (int q = 0; q < WEIGHT_KPT; ++q) {
                     const int t = tr + q * WEIGHT_THREADS;
                     row[q] = t >= lo && t < end ? row_at(b, kv, t) : -1;
                 }
-                float sum[WEIGHT_KPT] = {};
-                if (p.sh % 4 == 0) {                       // 16-byte loads
+                if (p.cpu > GPH) {
+                    // key t's scores lie 16 floats from column to column, keys side by side
+                    const float *s = at + (long long)(tr / TILE) * p.sh * TILE + tr % TILE;
+                    for (int i = 0; i < nx; i += p.cpu, s += group) {
+                        const int nc = min(p.cpu, nx - i);
+#pragma unroll 4
+                        for (int c = 0; c < nc; ++c) {
+                            const float z = lse[i + c];
+#pragma unroll
+                            for (int q = 0; q < WEIGHT_KPT; ++q)
+                                if (row[q] >= 0)
+                                    sum[q] += ex2_ftz(__ldcs(s + c * TILE +
+                                                             q * (WEIGHT_THREADS * p.sh)) - z);
+                        }
+                    }
+                } else if (p.sh % 4 == 0) {                // a key's scores in 16-byte loads
                     const float *s = at + (long long)tr * p.sh;
                     for (int x = 0, c = 0; x < nx; x += 4) {
                         float4 v[WEIGHT_KPT];
@@ -1193,8 +1206,8 @@ __global__ void __launch_bounds__(MERGE_THREADS, D == 128 ? 4 : 2) fa_merge_weig
 }
 static_assert(MERGE_THREADS == MERGE_ROWS_PER_CTA * 32, "one block size for both merges");
 
-// Scores of the keys ka and kb of a unit's tile (rows g4 and g4 + 8 of the
-// mma tile) for this lane's columns c0 = 2 t4 and c0 + 1, of nh live ones.
+// Scores of keys ka and kb of a unit of 8 columns for this lane's columns c0 = 2 t4
+// and c0 + 1, of nh live ones.
 __device__ __forceinline__ void store_scores(const Params &p, long long unit, int ka, int kb,
                                              int c0, int nh, const float (&sc)[4])
 {
@@ -1214,7 +1227,6 @@ __device__ __forceinline__ void store_scores(const Params &p, long long unit, in
         b[1] = sc[3];
     }
 }
-
 
 }  // namespace tc
 
@@ -1304,11 +1316,12 @@ static cudaError_t launch_merge_half(const Params &p0, int sms, cudaStream_t st)
                                     : rows;
     long long ctas = merge;
     if (p.acc) {
-        // items of up to 8 rounds, while the capacity leaves two for every SM
+        // items of up to 8 rounds, while the capacity leaves two for every SM; of one
+        // with many columns, whose rounds are long enough
         const long long most = (long long)sms * 4;
         const long long rounds = (p.cap16 + tc::WEIGHT_KEYS - 1) / tc::WEIGHT_KEYS;
         const long long units = (long long)p.B * p.Hkv;
-        p.w_rounds = 8;
+        p.w_rounds = p.cpu > tc::GPH ? 1 : 8;
         while (p.w_rounds > 1 && (rounds + p.w_rounds - 1) / p.w_rounds * units < 2ll * sms)
             p.w_rounds /= 2;
         p.lg_page = p.bt ? log2_of(p.page_size) : -1;

@@ -31,8 +31,9 @@ namespace ev {
 constexpr int THREADS = 512;
 constexpr int WARPS = THREADS / 32;
 constexpr int BINS = 2048;
-constexpr int MAX_CTAS = 8;              // CTAs per cluster
-constexpr int STAGE_BYTES = 96 * 1024;   // totals, then rows in flight, of a CTA: two CTAs per SM
+constexpr int MAX_CTAS = 16;             // CTAs per cluster (8 are portable; fewer if they do not fit)
+// Totals, then rows in flight, of a CTA: two CTAs per SM, or one when there are few units.
+constexpr int STAGE_BYTES = 96 * 1024, STAGE_BYTES_1 = 200 * 1024;
 constexpr int HELD = STAGE_BYTES / 4;    // totals a CTA holds
 constexpr int ROUND_ROWS = THREADS;      // most rows a CTA stages per round
 constexpr double FUSED_BYTES = 4 << 20;  // rows to move up to which one kernel does it all
@@ -83,27 +84,39 @@ struct Places {
     long long src[ROUND_ROWS], dst[ROUND_ROWS];
 };
 
-// Rows pl.src -> pl.dst of one array, by the whole CTA, in pieces, DEPTH of them in
-// flight per thread.  No source may be another row's destination.
+// Rows pl.src -> pl.dst of the arrays first .. first + 1 (K and V, or the scales), by the
+// whole CTA, in pieces, DEPTH of them in flight per thread over both arrays.  No
+// source may be another row's destination.
 template <typename Piece, int DEPTH>
-__device__ __forceinline__ void copy_rows(char *base, int rb, const Places &pl, int nr)
+__device__ __forceinline__ void copy_rows(const Args &x, int first, const Places &pl, int nr)
 {
-    const int lg = 31 - __clz(rb / static_cast<int>(sizeof(Piece)));
-    const int total = nr << lg;
+    char *a0 = x.a[first], *a1 = x.a[first + 1];
+    const int l0 = a0 ? 31 - __clz(x.row_bytes[first] / static_cast<int>(sizeof(Piece))) : 0;
+    const int l1 = a1 ? 31 - __clz(x.row_bytes[first + 1] / static_cast<int>(sizeof(Piece))) : 0;
+    const int n0 = a0 ? nr << l0 : 0, total = n0 + (a1 ? nr << l1 : 0);
+    // piece i: its row (-1: not moved) and its place in the row
+    auto place = [&](int i, const long long *rows, Piece *&at) {
+        const bool second = i >= n0;
+        const int k = second ? i - n0 : i, lg = second ? l1 : l0;
+        const long long r = rows[k >> lg];
+        at = reinterpret_cast<Piece *>(second ? a1 : a0) + (r << lg) + (k & ((1 << lg) - 1));
+        return r >= 0;
+    };
     for (int i0 = threadIdx.x; i0 < total; i0 += DEPTH * blockDim.x) {
         Piece v[DEPTH];
 #pragma unroll
         for (int q = 0; q < DEPTH; ++q) {
             const int i = i0 + q * blockDim.x;
-            if (i < total && pl.src[i >> lg] >= 0)
-                v[q] = __ldcs(reinterpret_cast<const Piece *>(base + pl.src[i >> lg] * rb) +
-                              (i & ((1 << lg) - 1)));
+            Piece *at;
+            if (i < total && place(i, pl.src, at))
+                v[q] = __ldcs(at);
         }
 #pragma unroll
         for (int q = 0; q < DEPTH; ++q) {
             const int i = i0 + q * blockDim.x;
-            if (i < total && pl.src[i >> lg] >= 0)
-                reinterpret_cast<Piece *>(base + pl.dst[i >> lg] * rb)[i & ((1 << lg) - 1)] = v[q];
+            Piece *at;
+            if (i < total && place(i, pl.dst, at))
+                *at = v[q];
         }
     }
 }
@@ -119,23 +132,38 @@ __device__ __forceinline__ void move_far(const Params &p, const Args &x, int b, 
         const long long s = t >= x.budget ? row_of(p, x, b, kv, t) : -1;
         const long long d = s >= 0 ? row_of(p, x, b, kv, j) : -1;
         pl.src[threadIdx.x] = d >= 0 ? s : -1;
-        pl.dst[threadIdx.x] = d;
+        pl.dst[threadIdx.x] = s >= 0 ? d : -1;
     }
     __syncthreads();
-#pragma unroll
-    for (int a = 0; a < 4; ++a) {
-        if (!x.a[a])
-            continue;
-        if (x.row_bytes[a] >= 16)
-            copy_rows<uint4, DEPTH>(x.a[a], x.row_bytes[a], pl, nr);
+    copy_rows<uint4, DEPTH>(x, 0, pl, nr);
+    if (x.a[3]) {
+        if (x.row_bytes[3] >= 16)
+            copy_rows<uint4, DEPTH>(x, 2, pl, nr);
         else
-            copy_rows<uint2, DEPTH>(x.a[a], x.row_bytes[a], pl, nr);
+            copy_rows<uint2, DEPTH>(x, 2, pl, nr);
+    }
+}
+
+// The totals of tokens t0, t0 + step, ... below n start again from zero.
+__device__ __forceinline__ void clear_totals(const Params &p, const Args &x, int b, int kv, int t0,
+                                             int step, int n)
+{
+    constexpr int U = 8;
+    for (; t0 < n; t0 += U * step) {
+        long long r[U];
+#pragma unroll
+        for (int q = 0; q < U; ++q)
+            r[q] = t0 < n - q * step ? row_of(p, x, b, kv, t0 + q * step) : -1;
+#pragma unroll
+        for (int q = 0; q < U; ++q)
+            if (r[q] >= 0)
+                x.acc[r[q]] = 0.f;
     }
 }
 
 constexpr int FAR_THREADS = 256;
 constexpr int FAR_ROWS = 64;             // kept rows per CTA
-__global__ void __launch_bounds__(FAR_THREADS) evict_far_kernel(const Params p, const Args x)
+__global__ void __launch_bounds__(FAR_THREADS, 4) evict_far_kernel(const Params p, const Args x)
 {
     __shared__ Places pl;
     const int chunks = (x.budget + FAR_ROWS - 1) / FAR_ROWS;
@@ -147,7 +175,8 @@ __global__ void __launch_bounds__(FAR_THREADS) evict_far_kernel(const Params p, 
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (n <= x.budget)
         return;
-    const int r0 = blockIdx.x % chunks * FAR_ROWS;
+    const int c = blockIdx.x % chunks, r0 = c * FAR_ROWS;
+    clear_totals(p, x, b, kv, x.budget + c * FAR_THREADS + threadIdx.x, chunks * FAR_THREADS, n);
     move_far<8>(p, x, b, kv, x.kept + (long long)unit * x.budget, r0, min(FAR_ROWS, x.budget - r0),
                 pl);
 }
@@ -227,7 +256,7 @@ __global__ void __launch_bounds__(THREADS, 2) evict_kernel(const Params p, const
     const bool held = c1 - c0 <= HELD;
     float *tot = reinterpret_cast<float *>(stage);
     if (held) {
-        constexpr int U = 8;
+        constexpr int U = 16;
         for (int t0 = w0 + lane; t0 < w1; t0 += 32 * U) {
             float v[U];
 #pragma unroll
@@ -265,10 +294,18 @@ __global__ void __launch_bounds__(THREADS, 2) evict_kernel(const Params p, const
                 const int bin = BINS - 1 - (tid * PER + q);
                 c[q] = hist[bin];
                 if (sel > 1) {
+                    // 8 CTAs' loads in flight at a time
                     const uint32_t a = smem_u32(&hist[bin]);
                     c[q] = 0;
-                    for (int r = 0; r < sel; ++r)
-                        c[q] += ld_cluster(tc::cl_map(a, r));
+                    for (int r0 = 0; r0 < sel; r0 += 8) {
+                        unsigned v[8];
+#pragma unroll
+                        for (int r = 0; r < 8; ++r)
+                            v[r] = r0 + r < sel ? ld_cluster(tc::cl_map(a, r0 + r)) : 0u;
+#pragma unroll
+                        for (int r = 0; r < 8; ++r)
+                            c[q] += v[r];
+                    }
                 }
                 sum += c[q];
             }
@@ -300,12 +337,14 @@ __global__ void __launch_bounds__(THREADS, 2) evict_kernel(const Params p, const
     }
     // ---- ranks: what the warps before this one keep
     unsigned n_gt = 0, n_eq = 0;
-    for (int t0 = w0; t0 < w1; t0 += 32) {
-        const int t = t0 + lane;
-        const unsigned u = t < w1 ? key_at(t) : 0u;
-        n_gt += __popc(__ballot_sync(0xffffffffu, t < w1 && u > thr));
-        n_eq += __popc(__ballot_sync(0xffffffffu, t < w1 && u == thr));
+#pragma unroll 4
+    for (int t = w0 + lane; t < w1; t += 32) {    // per lane, then over the warp
+        const unsigned u = key_at(t);
+        n_gt += u > thr;
+        n_eq += u == thr;
     }
+    n_gt = __reduce_add_sync(0xffffffffu, n_gt);
+    n_eq = __reduce_add_sync(0xffffffffu, n_eq);
     if (lane == 0) {
         cnt[warp][0] = n_gt;
         cnt[warp][1] = n_eq;
@@ -324,6 +363,7 @@ __global__ void __launch_bounds__(THREADS, 2) evict_kernel(const Params p, const
         eq += __shfl_xor_sync(0xffffffffu, eq, off);
     }
     unsigned at = x.sink + gt + min(eq, rem);
+#pragma unroll 4
     for (int t0 = w0; t0 < w1; t0 += 32) {
         const int t = t0 + lane;
         const unsigned u = t < w1 ? key_at(t) : 0u;
@@ -364,24 +404,21 @@ __global__ void __launch_bounds__(THREADS, 2) evict_kernel(const Params p, const
                 x.acc[dst] = v[q];
         }
     }
-    // the totals of the rows behind the budget start again from zero
-    for (int t = x.budget + rank * THREADS + tid; t < n; t += cs * THREADS) {
-        const long long r = row_of(p, x, b, kv, t);
-        if (r >= 0)
-            x.acc[r] = 0.f;
-    }
+    if (x.fused)
+        clear_totals(p, x, b, kv, x.budget + rank * THREADS + tid, cs * THREADS, n);
 
     // ---- rows of kept tokens below the budget, in rounds of cs * rows: kept[]
-    // ascends, so they are its first n_near entries
-    int n_near = x.sink;
-    for (int step = x.budget - x.sink; step > 0;) {       // first entry >= budget
-        const int half = step / 2;
-        if (__ldcg(kept + n_near + half) < x.budget) {
-            n_near += half + 1;
-            step -= half + 1;
-        } else {
-            step = half;
-        }
+    // ascends, so they are its first n_near entries (found 32 probes at a time)
+    int n_near = x.sink, span = x.budget - x.sink;    // the end lies in n_near .. n_near + span
+    while (span > 0) {
+        const int stride = (span + 31) / 32;
+        const int at = n_near + lane * stride;        // below the budget: the end is past it
+        const bool low = lane * stride < span && __ldcg(kept + at) < x.budget;
+        const int lows = __popc(__ballot_sync(0xffffffffu, low));
+        if (lows == 0)
+            break;
+        n_near += (lows - 1) * stride + 1;
+        span = min(stride - 1, x.budget - n_near);
     }
     const int R = x.rows;
     for (int j0 = x.sink; j0 < n_near; j0 += cs * R) {
@@ -442,6 +479,66 @@ __global__ void __launch_bounds__(THREADS, 2) evict_kernel(const Params p, const
     if (x.fused)
         for (int r0 = n_near + rank * FAR_ROWS; r0 < x.budget; r0 += cs * FAR_ROWS)
             move_far<4>(p, x, b, kv, kept, r0, min(FAR_ROWS, x.budget - r0), pl);
+}
+
+// The kernel's shared memory and cluster sizes, allowed once per device.
+static cudaError_t allow_attributes()
+{
+    static std::mutex mu;
+    static bool done[64] = {false};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return e;
+    std::lock_guard<std::mutex> lock(mu);
+    if (dev < 64 && done[dev])
+        return cudaSuccess;
+    e = cudaFuncSetAttribute(evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             STAGE_BYTES_1);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(evict_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess && dev < 64)
+        done[dev] = true;
+    return e;
+}
+
+// Clusters of cs CTAs with `stage` bytes each that the current device holds at once
+// (0 if the query fails), cached per device.
+static int cluster_capacity(int cs, int stage)
+{
+    static std::mutex mu;
+    static int cache[64][2][5];
+    static bool known[64][2][5] = {};
+    int dev = 0;
+    if (allow_attributes() != cudaSuccess || cudaGetDevice(&dev) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    const int si = stage == STAGE_BYTES ? 0 : 1, ci = __builtin_ctz(cs);
+    std::lock_guard<std::mutex> lock(mu);
+    if (dev < 64 && known[dev][si][ci])
+        return cache[dev][si][ci];
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(cs * 64);
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = stage;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = cs;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, evict_kernel, &cfg) != cudaSuccess) {
+        n = 0;
+        cudaGetLastError();
+    }
+    if (dev < 64) {
+        cache[dev][si][ci] = n;
+        known[dev][si][ci] = true;
+    }
+    return n;
 }
 
 }  // namespace ev
@@ -517,15 +614,9 @@ extern "C" FA_API int fa_evict_kv(void *k_cache, void *v_cache, void *k_scales, 
                 return fail(FA_ERR_ALIAS, "%s: two arrays overlap", name);
     if (batch == 0)
         return 0;
-    int sms = 0;
-    if (const int rc = device_sms(&sms))
-        return rc;
     int total = 0;
     for (int a = 0; a < 4; ++a)
         total += x.a[a] ? x.row_bytes[a] : 0;
-    x.rows = ev::STAGE_BYTES / total / 16 * 16;
-    if (x.rows > ev::ROUND_ROWS)
-        x.rows = ev::ROUND_ROWS;
     x.lg_page = log2_of(page_size);
     Params p = {};
     p.bt = block_table;
@@ -538,32 +629,32 @@ extern "C" FA_API int fa_evict_kv(void *k_cache, void *v_cache, void *k_scales, 
     p.cap = cap;
     const long long units = (long long)batch * n_kv_heads;
     x.fused = (double)units * budget * total <= ev::FUSED_BYTES;
-    // the largest cluster that still leaves every unit resident (two CTAs per SM)
-    int cs = ev::MAX_CTAS;
-    while (cs > 1 && units * cs > 2ll * sms)
-        cs /= 2;
+    // The largest cluster for which every unit's is resident at once: with one CTA per
+    // SM and 16 or 8 CTAs, else with two per SM and 8 or fewer.
+    int cs = 0, stage = ev::STAGE_BYTES;
+    for (int c = ev::MAX_CTAS; c >= 8 && !cs; c /= 2)
+        if (units <= ev::cluster_capacity(c, ev::STAGE_BYTES_1)) {
+            cs = c;
+            stage = ev::STAGE_BYTES_1;
+        }
+    for (int c = 8; c >= 2 && !cs; c /= 2)
+        if (units <= ev::cluster_capacity(c, stage))
+            cs = c;
+    if (!cs)
+        cs = 1;
     p.cl_ctas = cs;
+    x.rows = stage / total / 16 * 16;
+    if (x.rows > ev::ROUND_ROWS)
+        x.rows = ev::ROUND_ROWS;
     const long long far_chunks = (budget + (long long)ev::FAR_ROWS - 1) / ev::FAR_ROWS;
     if (units * cs > 0x7fffffffll || units * far_chunks > 0x7fffffffll)
         return fail(FA_ERR_LAYOUT, "%s: too many rows", name);
-    static std::mutex mu;
-    static bool done[64] = {false};
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) {
-        std::lock_guard<std::mutex> lock(mu);
-        if (dev >= 64 || !done[dev]) {
-            e = cudaFuncSetAttribute(ev::evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     ev::STAGE_BYTES);
-            if (e == cudaSuccess && dev < 64)
-                done[dev] = true;
-        }
-    }
+    cudaError_t e = ev::allow_attributes();
     if (e == cudaSuccess) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(static_cast<unsigned>(units * cs));
         cfg.blockDim = dim3(ev::THREADS);
-        cfg.dynamicSmemBytes = ev::STAGE_BYTES;
+        cfg.dynamicSmemBytes = stage;
         cfg.stream = static_cast<cudaStream_t>(stream);
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeClusterDimension;

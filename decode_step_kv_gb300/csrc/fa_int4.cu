@@ -1143,21 +1143,19 @@ __global__ void __launch_bounds__(128, WideCfg<D, CW>::CTAS_PER_SM) wide_kernel(
                     }
             }
             if constexpr (WT) {
-                // [unit][key][column]: 8 lanes write 8 neighbouring columns
+                // of every column, 4 lanes write 8 neighbouring keys
                 const int col = cwi * 16 + g;
-                float *at = p.ws_s + (cw.unit(p) * p.cap16 + base + kk + 2 * t) * p.sh + col;
+                float *at = p.ws_s + ((cw.unit(p) * (p.cap16 / TILE) + (base + kk) / TILE) * p.sh +
+                                      col) * TILE + 2 * t;
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     if (!((have >> ((kk + 8 * n) / TILE)) & 1u))
                         continue;
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        float *a = at + (8 * n + x) * p.sh;
-                        if (col < nh)
-                            a[0] = sc4[n][x];
-                        if (col + 8 < nh)
-                            a[8] = sc4[n][x + 2];
-                    }
+                    float *a = at + (n / 2) * (p.sh * TILE) + (n & 1) * 8;
+                    if (col < nh)
+                        *reinterpret_cast<float2 *>(a) = make_float2(sc4[n][0], sc4[n][1]);
+                    if (col + 8 < nh)
+                        *reinterpret_cast<float2 *>(a + 8 * TILE) = make_float2(sc4[n][2], sc4[n][3]);
                 }
             }
             // ---- online softmax (as above: the maximum moves when passed by 8)
