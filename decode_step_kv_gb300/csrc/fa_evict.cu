@@ -7,8 +7,8 @@
 // front of the cache.
 //
 // A thread-block cluster per (sequence, KV head) selects and moves what needs an
-// order; a second kernel moves the rest with every SM (within the first when
-// there is little of it).
+// order; a second kernel moves the rest with every SM, unless there is little of it
+// or the clusters fill the GPU: then they go on with it themselves.
 //   Selection: a radix selection of the k-th largest total (11 + 11 + 10 bits
 //   of the order-preserving integer), each CTA counting its share of the
 //   tokens, the counts summed through distributed shared memory; then every
@@ -75,7 +75,7 @@ __device__ __forceinline__ long long row_of(const Params &p, const Args &x, int 
 __device__ __forceinline__ unsigned ld_cluster(uint32_t a)
 {
     unsigned v;
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a));
     return v;
 }
 
@@ -197,6 +197,8 @@ __global__ void __launch_bounds__(THREADS, 2) evict_kernel(const Params p, const
     __shared__ unsigned wsum[WARPS];
     __shared__ unsigned found[2];
     __shared__ Places pl;
+    unsigned *part = reinterpret_cast<unsigned *>(pl.src);   // while selecting: this CTA's bin sums
+    static_assert(sizeof(Places) >= BINS / 2 * sizeof(unsigned), "a share of the bins");
     extern __shared__ __align__(128) unsigned char stage[];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
@@ -250,11 +252,12 @@ __global__ void __launch_bounds__(THREADS, 2) evict_kernel(const Params p, const
         }
         return __ldcg(x.acc + r);
     };
-    // this CTA's totals in shared memory, at the tokens' offsets from its first
+    // this CTA's totals, as ordered integers, in shared memory, at the tokens' offsets
+    // from its first
     const int c0 = x.sink + static_cast<int>((long long)m * (sr * WARPS) / nw);
     const int c1 = x.sink + static_cast<int>((long long)m * (sr * WARPS + WARPS) / nw);
     const bool held = c1 - c0 <= HELD;
-    float *tot = reinterpret_cast<float *>(stage);
+    unsigned *tot = reinterpret_cast<unsigned *>(stage);
     if (held) {
         constexpr int U = 16;
         for (int t0 = w0 + lane; t0 < w1; t0 += 32 * U) {
@@ -265,11 +268,11 @@ __global__ void __launch_bounds__(THREADS, 2) evict_kernel(const Params p, const
 #pragma unroll
             for (int q = 0; q < U; ++q)
                 if (t0 + 32 * q < w1)
-                    tot[t0 + 32 * q - c0] = v[q];
+                    tot[t0 + 32 * q - c0] = order_key(v[q]);
         }
         __syncwarp();                             // a warp reads its own tokens only
     }
-    auto key_at = [&](int t) { return order_key(held ? tot[t - c0] : total_at(t)); };
+    auto key_at = [&](int t) { return held ? tot[t - c0] : order_key(total_at(t)); };
     unsigned thr = 0xffffffffu;                   // keys above thr are kept ...
     unsigned rem = 0;                             // ... and the first rem equal to it
     if (k > 0) {
@@ -281,6 +284,7 @@ __global__ void __launch_bounds__(THREADS, 2) evict_kernel(const Params p, const
             for (int i = tid; i < BINS; i += THREADS)
                 hist[i] = 0;
             __syncthreads();
+#pragma unroll 4
             for (int t = w0 + lane; t < w1; t += 32) {
                 const unsigned u = key_at(t);
                 if (pass == 0 || ((u ^ thr) >> (shift + bits)) == 0)
@@ -288,27 +292,37 @@ __global__ void __launch_bounds__(THREADS, 2) evict_kernel(const Params p, const
             }
             sync_sel();
             constexpr int PER = BINS / THREADS;
+            if (sel > 1) {
+                // every CTA adds up its share of the bins over the cluster, then all read
+                // the sums (each reading all bins of all CTAs took 16 us per pass)
+                const int share = BINS / sel, tpb = max(THREADS / share, 1);
+                for (int i = tid / tpb; i < share; i += THREADS / tpb) {
+                    const uint32_t a = smem_u32(&hist[sr * share + i]);
+                    unsigned v = 0;
+                    for (int r0 = tid % tpb; r0 < sel; r0 += 4 * tpb) {
+                        unsigned y[4];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            y[q] = r0 + q * tpb < sel ? ld_cluster(tc::cl_map(a, r0 + q * tpb)) : 0u;
+                        v += y[0] + y[1] + y[2] + y[3];
+                    }
+                    for (int off = tpb / 2; off >= 1; off >>= 1)
+                        v += __shfl_xor_sync(0xffffffffu, v, off);
+                    if (tid % tpb == 0)
+                        part[i] = v;
+                }
+                sync_sel();
+            }
             unsigned c[PER], sum = 0;             // this thread's bins, from the top
 #pragma unroll
             for (int q = 0; q < PER; ++q) {
-                const int bin = BINS - 1 - (tid * PER + q);
-                c[q] = hist[bin];
-                if (sel > 1) {
-                    // 8 CTAs' loads in flight at a time
-                    const uint32_t a = smem_u32(&hist[bin]);
-                    c[q] = 0;
-                    for (int r0 = 0; r0 < sel; r0 += 8) {
-                        unsigned v[8];
-#pragma unroll
-                        for (int r = 0; r < 8; ++r)
-                            v[r] = r0 + r < sel ? ld_cluster(tc::cl_map(a, r0 + r)) : 0u;
-#pragma unroll
-                        for (int r = 0; r < 8; ++r)
-                            c[q] += v[r];
-                    }
-                }
-                sum += c[q];
+                const int bin = BINS - 1 - (tid * PER + q), share = BINS / sel;
+                c[q] = sel > 1 ? ld_cluster(tc::cl_map(smem_u32(&part[bin % share]), bin / share))
+                               : hist[bin];
             }
+#pragma unroll
+            for (int q = 0; q < PER; ++q)
+                sum += c[q];
             unsigned incl = sum;
 #pragma unroll
             for (int off = 1; off < 32; off <<= 1) {
@@ -628,21 +642,29 @@ extern "C" FA_API int fa_evict_kv(void *k_cache, void *v_cache, void *k_scales, 
     p.num_blocks = num_blocks;
     p.cap = cap;
     const long long units = (long long)batch * n_kv_heads;
-    x.fused = (double)units * budget * total <= ev::FUSED_BYTES;
-    // The largest cluster for which every unit's is resident at once: with one CTA per
-    // SM and 16 or 8 CTAs, else with two per SM and 8 or fewer.
-    int cs = 0, stage = ev::STAGE_BYTES;
-    for (int c = ev::MAX_CTAS; c >= 8 && !cs; c /= 2)
-        if (units <= ev::cluster_capacity(c, ev::STAGE_BYTES_1)) {
-            cs = c;
-            stage = ev::STAGE_BYTES_1;
-        }
-    for (int c = 8; c >= 2 && !cs; c /= 2)
-        if (units <= ev::cluster_capacity(c, stage))
-            cs = c;
-    if (!cs)
-        cs = 1;
+    // The largest cluster for which every unit's is resident at once, but none larger
+    // than stages the whole budget in one round (more CTAs only add to the
+    // barriers).  16 CTAs with the smaller stage come before 8 with the larger: the
+    // same rows per round, and twice the CTAs to select with.
+    int cs = 1, stage = ev::STAGE_BYTES;
+    const long long round = ev::STAGE_BYTES / total;
+    int most = ev::MAX_CTAS;
+    while (most > 1 && round * (most / 2) >= budget)
+        most /= 2;
+    for (int c = most; c >= 2 && cs == 1; c /= 2)
+        for (int st : {ev::STAGE_BYTES_1, ev::STAGE_BYTES})
+            if (cs == 1 && (st == ev::STAGE_BYTES || c >= 8) &&
+                units <= ev::cluster_capacity(c, st)) {
+                cs = c;
+                stage = st;
+            }
     p.cl_ctas = cs;
+    // One kernel when there is little to move, or when the clusters fill the GPU anyway:
+    // 32 ragged sequences x 8 heads, 82 us against 93 with the far rows in a second.
+    int sms = 0;
+    if (const int rc = device_sms(&sms))
+        return rc;
+    x.fused = (double)units * budget * total <= ev::FUSED_BYTES || units * cs >= sms;
     x.rows = stage / total / 16 * 16;
     if (x.rows > ev::ROUND_ROWS)
         x.rows = ev::ROUND_ROWS;
