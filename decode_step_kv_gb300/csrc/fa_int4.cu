@@ -234,12 +234,12 @@ __global__ void __launch_bounds__(256) gather_kernel(const Params p, const RowAr
 //      block sums (in two tf32 parts, 21 bits).
 //   V: the pair of a half2 runs over two keys (the contraction), so the words
 //      of two keys are interleaved by a byte permute; the accumulators of odd
-//      elements hold 2^-20, the even ones 2^-24.  The offset is taken off tile
-//      by tile with a second mma whose A fragment is the constant -8: 8 more of
-//      them per tile instead of 32 fp16 subtractions, and never hundreds
-//      of times the result in the accumulator, as one correction at the end
-//      would have.  A key's scale multiplies its weight instead of its 32
-//      codes: P s_j is the B operand of block j.
+//      elements hold 2^-20, the even ones 2^-24.  The offset is taken off in fp16,
+//      exactly (u - 8 at either exponent): left in the sum it would be hundreds of
+//      times the result, and a second mma with a constant -8 as its A fragment kept
+//      the tensor pipe busy longer than it saved instructions (226 us against 214
+//      for 32 x 32768 keys of 8 heads x 128).  A key's scale multiplies its weight
+//      instead of its 32 codes: P s_j is the B operand of block j.
 // P and P s are rounded to fp16 (2^-11 each); everything else is fp32.
 // The running maximum moves only when a score passes it by 8 (log2 units), so
 // weights reach 2^8 and most tiles need no shuffles.  V scales outside
@@ -589,13 +589,6 @@ __global__ void __launch_bounds__(Cfg<D>::NW * 32, Cfg<D>::CTAS_PER_SM) decode_k
         load_q();
     reset();
     const float c2 = p.c2 * 16777216.f;
-    // the constant A fragment: -8 2^-24 in even rows, -8 2^-20 in odd ones, each
-    // combined with a zero the compiler does not know (T < 2^60), or it would
-    // build the four registers anew for every mma
-    const uint32_t m8[4] = {0x80088008u ^ static_cast<uint32_t>(T >> 60),
-                            0x80808080u ^ static_cast<uint32_t>(T >> 61),
-                            0x80088008u ^ static_cast<uint32_t>(t1 >> 60),
-                            0x80808080u ^ static_cast<uint32_t>(t1 >> 61)};
     const uint32_t half_sel = g & 1 ? 0x7632 : 0x5410;
     // lane's places in a stage: K rows g, V rows 2t, scales
     uint32_t kc[NJ / 4], vc[2][NJ / 4];
@@ -799,18 +792,20 @@ __global__ void __launch_bounds__(Cfg<D>::NW * 32, Cfg<D>::CTAS_PER_SM) decode_k
                     s0[q] = as_u32(__hmul2(pa, sv[0][jj + q]));
                     s1[q] = as_u32(__hmul2(pb, sv[1][jj + q]));
                 }
-#pragma unroll
-                for (int q = 0; q < 8; ++q)
-                    tc::mma16816(acc[2 * jj + q], m8[0], m8[1], m8[2], m8[3], s0[q / 2], s1[q / 2]);
+                auto even = [](uint32_t z) {
+                    return as_u32(__hsub2(as_half2(z & 0x000f000fu), as_half2(0x00080008u)));
+                };
+                auto odd = [](uint32_t z) {
+                    return as_u32(__hsub2(as_half2(z & 0x00f000f0u), as_half2(0x00800080u)));
+                };
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     const uint32_t x = __byte_perm(v[0][q], v[1][q], half_sel);
                     const uint32_t y = __byte_perm(v[2][q], v[3][q], half_sel);
                     const uint32_t xh = x >> 8, yh = y >> 8;
-                    tc::mma16816(acc[2 * (jj + q)], x & 0x000f000fu, x & 0x00f000f0u,
-                                 y & 0x000f000fu, y & 0x00f000f0u, s0[q], s1[q]);
-                    tc::mma16816(acc[2 * (jj + q) + 1], xh & 0x000f000fu, xh & 0x00f000f0u,
-                                 yh & 0x000f000fu, yh & 0x00f000f0u, s0[q], s1[q]);
+                    tc::mma16816(acc[2 * (jj + q)], even(x), odd(x), even(y), odd(y), s0[q], s1[q]);
+                    tc::mma16816(acc[2 * (jj + q) + 1], even(xh), odd(xh), even(yh), odd(yh), s0[q],
+                                 s1[q]);
                 }
             }
         }
@@ -1398,7 +1393,10 @@ __global__ void __launch_bounds__(128, WideCfg<D, CW>::CTAS_PER_SM) wide_kernel(
 // ---------------------------------------------------------------- host side
 // Columns per KV head from which the kernel with a shared unpacked tile is taken: at
 // 16 the two cost the same per key (two groups' unpacking against half-idle warps).
-constexpr int WIDE_MIN_COLS = 17;
+#ifndef FA_I4_WIDE_MIN
+#define FA_I4_WIDE_MIN 17
+#endif
+constexpr int WIDE_MIN_COLS = FA_I4_WIDE_MIN;
 
 struct Plan {
     int ctas, W, n_hg, units, sh, cpu;
