@@ -64,7 +64,7 @@ struct Params {
     int n_slots;
     int cl_ctas;      // cluster plan: CTAs per cluster (1, 2, 4 or 8)
     float *lse;       // recorded weights: [B*tq*Hq] log2-sum-exp2 of each row (-inf: no key)
-    float *ws_s;      // recorded weights: scores in log2 units, of units of 8 columns
+    float *ws_s;      // recorded weights: scores in log2 units, of units of up to 16 columns
                       // [B*units][cap16][sh], of wider ones [B*units][cap16/16][sh][16 keys]
     float *acc;       // recorded weights: the running total of every cache row
     long long cap16;  // recorded weights: capacity rounded up to whole tiles
@@ -1133,7 +1133,7 @@ __device__ __forceinline__ void add_weights(const Params &p, const int cta, cons
                     const int t = tr + q * WEIGHT_THREADS;
                     row[q] = t >= lo && t < end ? row_at(b, kv, t) : -1;
                 }
-                if (p.cpu > GPH) {
+                if (p.cpu > 2 * GPH) {
                     // key t's scores lie 16 floats from column to column, keys side by side
                     const float *s = at + (long long)(tr / TILE) * p.sh * TILE + tr % TILE;
                     for (int i = 0; i < nx; i += p.cpu, s += group) {
@@ -1206,16 +1206,16 @@ __global__ void __launch_bounds__(MERGE_THREADS, D == 128 ? 4 : 2) fa_merge_weig
 }
 static_assert(MERGE_THREADS == MERGE_ROWS_PER_CTA * 32, "one block size for both merges");
 
-// Scores of keys ka and kb of a unit of 8 columns for this lane's columns c0 = 2 t4
+// Scores of keys ka and kb of a unit of up to 16 columns for this lane's columns c0 = 2 t4
 // and c0 + 1, of nh live ones.
-__device__ __forceinline__ void store_scores(const Params &p, long long unit, int ka, int kb,
-                                             int c0, int nh, const float (&sc)[4])
+__device__ __forceinline__ void store_scores(float *unit, int sh, int ka, int kb, int c0, int nh,
+                                             const float (&sc)[4])
 {
     if (c0 >= nh)
         return;
-    float *a = p.ws_s + (unit * p.cap16 + ka) * p.sh + c0;
-    float *b = p.ws_s + (unit * p.cap16 + kb) * p.sh + c0;
-    if ((p.sh & 1) == 0 && c0 + 1 < nh) {
+    float *a = unit + (long long)ka * sh + c0;
+    float *b = unit + (long long)kb * sh + c0;
+    if ((sh & 1) == 0 && c0 + 1 < nh) {
         *reinterpret_cast<float2 *>(a) = make_float2(sc[0], sc[1]);
         *reinterpret_cast<float2 *>(b) = make_float2(sc[2], sc[3]);
         return;
@@ -1321,7 +1321,7 @@ static cudaError_t launch_merge_half(const Params &p0, int sms, cudaStream_t st)
         const long long most = (long long)sms * 4;
         const long long rounds = (p.cap16 + tc::WEIGHT_KEYS - 1) / tc::WEIGHT_KEYS;
         const long long units = (long long)p.B * p.Hkv;
-        p.w_rounds = p.cpu > tc::GPH ? 1 : 8;
+        p.w_rounds = p.cpu > 2 * tc::GPH ? 1 : 8;
         while (p.w_rounds > 1 && (rounds + p.w_rounds - 1) / p.w_rounds * units < 2ll * sms)
             p.w_rounds /= 2;
         p.lg_page = p.bt ? log2_of(p.page_size) : -1;

@@ -1028,7 +1028,8 @@ __global__ void __launch_bounds__(Cfg<D, VI8, NG>::NW * 32, Cfg<D, VI8, NG>::CTA
                 sc[2] = (kb >= clo[gi][0] && kb < chi[gi][0]) ? sc[2] * p.c2 : -INFINITY;
                 sc[3] = (kb >= clo[gi][1] && kb < chi[gi][1]) ? sc[3] * p.c2 : -INFINITY;
                 if constexpr (WT)
-                    store_scores(p, cw.unit(p), ka, kb, gi * GPH + 2 * t4, nh, sc4[gi]);
+                    store_scores(p.ws_s + cw.unit(p) * p.cap16 * p.sh, p.sh, ka, kb,
+                                 gi * GPH + 2 * t4, nh, sc4[gi]);
                 // ---- online softmax per column (lanes sharing t4 share them)
                 float x0 = fmaxf(sc[0], sc[2]);
                 float x1 = fmaxf(sc[1], sc[3]);

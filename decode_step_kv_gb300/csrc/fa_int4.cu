@@ -249,37 +249,16 @@ __global__ void __launch_bounds__(256) gather_kernel(const Params p, const RowAr
 // batches per warp); the lanes look their cache rows up side by side, so a tile's
 // share of the addressing is a shuffle and three multiply-adds.  They are
 // worked on two at a time.
-#ifndef FA_I4_NW_128
-#define FA_I4_NW_128 4
-#endif
-#ifndef FA_I4_BT_128
-#define FA_I4_BT_128 4
-#endif
-#ifndef FA_I4_STAGES_128
-#define FA_I4_STAGES_128 2
-#endif
-#ifndef FA_I4_CTAS_128
-#define FA_I4_CTAS_128 3
-#endif
-#ifndef FA_I4_NW_256
-#define FA_I4_NW_256 4
-#endif
-#ifndef FA_I4_BT_256
-#define FA_I4_BT_256 2
-#endif
-#ifndef FA_I4_STAGES_256
-#define FA_I4_STAGES_256 3
-#endif
-#ifndef FA_I4_CTAS_256
-#define FA_I4_CTAS_256 2
-#endif
-
-template <int D>
+// Warps per CTA, tiles per batch, batches in the ring, CTAs per SM: measured best of
+// the configurations whose rings fit (D = 128: 2 CTAs x 3 batches and batches of 2
+// were 4-20% slower on 32 x 32768 keys).  Two column groups per warp (NG = 2, D = 128)
+// take the registers of two CTAs per SM.
+template <int D, int NG>
 struct Cfg {
-    static constexpr int NW = D == 128 ? FA_I4_NW_128 : FA_I4_NW_256;
-    static constexpr int BT = D == 128 ? FA_I4_BT_128 : FA_I4_BT_256;   // tiles per batch
-    static constexpr int STAGES = D == 128 ? FA_I4_STAGES_128 : FA_I4_STAGES_256;
-    static constexpr int CTAS_PER_SM = D == 128 ? FA_I4_CTAS_128 : FA_I4_CTAS_256;
+    static constexpr int NW = 4;
+    static constexpr int BT = D == 128 ? 4 : 2;
+    static constexpr int STAGES = D == 128 && NG == 1 ? 2 : 3;
+    static constexpr int CTAS_PER_SM = D == 128 && NG == 1 ? 3 : 2;
     static constexpr int NJ = D / 32;                  // blocks per row
     static constexpr int RB = D / 2;                   // code bytes per row
     static constexpr int SB = D / 16;                  // scale bytes per row
@@ -424,11 +403,14 @@ struct Feed {
     }
 };
 
-template <int D, bool WT>
-__global__ void __launch_bounds__(Cfg<D>::NW * 32, Cfg<D>::CTAS_PER_SM) decode_kernel(const Params p)
+// NG: groups of 8 columns per warp.  With two, a tile is unpacked once for 16
+// columns (speculative verify).
+template <int D, int NG, bool WT>
+__global__ void __launch_bounds__(Cfg<D, NG>::NW * 32, Cfg<D, NG>::CTAS_PER_SM)
+    decode_kernel(const Params p)
 {
-    using C = Cfg<D>;
-    constexpr int NJ = C::NJ, S = C::STAGES;
+    using C = Cfg<D, NG>;
+    constexpr int NJ = C::NJ, S = C::STAGES, COLS = GPH * NG;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     const int warp = threadIdx.x >> 5;
@@ -526,45 +508,53 @@ __global__ void __launch_bounds__(Cfg<D>::NW * 32, Cfg<D>::CTAS_PER_SM) decode_k
     // ---- the unit's queries: column g's elements (n, n+4) of octet t of block j
     // as half2, odd n divided by 16; and column g's offset terms in two tf32 parts
     const int tq = p.tq > 1 ? p.tq : 1;
-    uint32_t qb[NJ][4];
-    float ct[NJ / 4][2];             // of block 4i + t
-    int nh = 0, clo[2], chi[2], all_lo = 0, all_hi = 0, base = 0;
+    uint32_t qb[NG][NJ][4];
+    float ct[NG][NJ / 4][2];         // of block 4i + t
+    int nh = 0, clo[NG][2], chi[NG][2], all_lo = 0, all_hi = 0, base = 0;
+    float *scores = nullptr;         // WT: the unit's
     auto load_q = [&] {
         base = cw.tok();
+        if constexpr (WT)
+            scores = p.ws_s + cw.unit(p) * p.cap16 * p.sh;
         const int kv = cw.j / p.n_hg, cg = cw.j % p.n_hg;
-        nh = min(GPH, tq * p.G - cg * GPH);
-        const tc::Col cq = tc::column(p, kv, cg, g, GPH);
-        const uint4 *src = reinterpret_cast<const uint4 *>(
-            p.q + (((long long)cw.b * tq + cq.j) * p.Hq + cq.h) * D);
+        nh = min(COLS, tq * p.G - cg * COLS);
         const __half2 sixteenth = __float2half2_rn(0.0625f);
-        uint4 x[NJ];
 #pragma unroll
-        for (int j = 0; j < NJ; ++j)
-            x[j] = cq.live ? __ldg(src + j * 4 + t) : make_uint4(0u, 0u, 0u, 0u);
+        for (int gi = 0; gi < NG; ++gi) {
+            const tc::Col cq = tc::column(p, kv, cg, gi * GPH + g, COLS);
+            const uint4 *src = reinterpret_cast<const uint4 *>(
+                p.q + (((long long)cw.b * tq + cq.j) * p.Hq + cq.h) * D);
+            uint4 x[NJ];
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-            qb[j][0] = __byte_perm(x[j].x, x[j].z, 0x5410);                        // 0, 4
-            qb[j][1] = as_u32(__hmul2(as_half2(__byte_perm(x[j].x, x[j].z, 0x7632)), sixteenth));
-            qb[j][2] = __byte_perm(x[j].y, x[j].w, 0x5410);                        // 2, 6
-            qb[j][3] = as_u32(__hmul2(as_half2(__byte_perm(x[j].y, x[j].w, 0x7632)), sixteenth));
-            float sum = 0.f;
+            for (int j = 0; j < NJ; ++j)
+                x[j] = cq.live ? __ldg(src + j * 4 + t) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-            for (int n = 0; n < 4; ++n) {
-                const float2 v = __half22float2(as_half2(qb[j][n]));
-                sum += (v.x + v.y) * (n & 1 ? 16.f : 1.f);
+            for (int j = 0; j < NJ; ++j) {
+                uint32_t *q = qb[gi][j];
+                q[0] = __byte_perm(x[j].x, x[j].z, 0x5410);                        // 0, 4
+                q[1] = as_u32(__hmul2(as_half2(__byte_perm(x[j].x, x[j].z, 0x7632)), sixteenth));
+                q[2] = __byte_perm(x[j].y, x[j].w, 0x5410);                        // 2, 6
+                q[3] = as_u32(__hmul2(as_half2(__byte_perm(x[j].y, x[j].w, 0x7632)), sixteenth));
+                float sum = 0.f;
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    const float2 v = __half22float2(as_half2(q[n]));
+                    sum += (v.x + v.y) * (n & 1 ? 16.f : 1.f);
+                }
+                sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+                if (j % 4 == t) {
+                    sum *= -8.f * p.c2;                            // log2 units
+                    ct[gi][j / 4][0] = __uint_as_float(__float_as_uint(sum) & 0xffffe000u);
+                    ct[gi][j / 4][1] = sum - ct[gi][j / 4][0];
+                }
             }
-            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-            if (j % 4 == t) {
-                sum *= -8.f * p.c2;                                // log2 units
-                ct[j / 4][0] = __uint_as_float(__float_as_uint(sum) & 0xffffe000u);
-                ct[j / 4][1] = sum - ct[j / 4][0];
+#pragma unroll
+            for (int x1 = 0; x1 < 2; ++x1) {
+                const tc::Col c = tc::column(p, kv, cg, gi * GPH + 2 * t + x1, COLS);
+                tc::column_range(p, cw.b, cw.hi, c.live ? c.j : tq - 1, clo[gi][x1], chi[gi][x1]);
             }
         }
-        const tc::Col a = tc::column(p, kv, cg, 2 * t, GPH);
-        const tc::Col b = tc::column(p, kv, cg, 2 * t + 1, GPH);
-        tc::column_range(p, cw.b, cw.hi, a.live ? a.j : tq - 1, clo[0], chi[0]);
-        tc::column_range(p, cw.b, cw.hi, b.live ? b.j : tq - 1, clo[1], chi[1]);
         int x0;
         tc::column_range(p, cw.b, cw.hi, tq - 1, all_lo, x0);   // keys every query attends
         tc::column_range(p, cw.b, cw.hi, 0, x0, all_hi);
@@ -572,16 +562,19 @@ __global__ void __launch_bounds__(Cfg<D>::NW * 32, Cfg<D>::CTAS_PER_SM) decode_k
 
     // [2j + i]: elements 32j + 4g + 2i (0, 1: columns 2t, 2t+1; times 2^-24) and
     // + 1 (2, 3; times 2^-20)
-    float acc[2 * NJ][4];
-    float mr[2], l[2];
+    float acc[NG][2 * NJ][4];
+    float mr[NG][2], l[NG][2];
     int e = 0;                // O is held times 2^-e
     __half2 vlim;             // V scales above it call for another e
     auto reset = [&] {
 #pragma unroll
-        for (int i = 0; i < 2 * NJ; ++i)
-            acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
-        mr[0] = mr[1] = NO_MAX;
-        l[0] = l[1] = 0.f;
+        for (int gi = 0; gi < NG; ++gi) {
+#pragma unroll
+            for (int i = 0; i < 2 * NJ; ++i)
+                acc[gi][i][0] = acc[gi][i][1] = acc[gi][i][2] = acc[gi][i][3] = 0.f;
+            mr[gi][0] = mr[gi][1] = NO_MAX;
+            l[gi][0] = l[gi][1] = 0.f;
+        }
         e = 0;
         vlim = __float2half2_rn(0.f);
     };
@@ -615,10 +608,13 @@ __global__ void __launch_bounds__(Cfg<D>::NW * 32, Cfg<D>::CTAS_PER_SM) decode_k
         const uint32_t ss = stage + hh * TILE * C::SB;
         const unsigned have = (have_all >> hh) & 3u;
         // ---- scores of tile h: rows are keys g and g + 8, columns 2t and 2t + 1
-        float sc[2][4];
+        float sc[NG][2][4];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            float a4[4], off[4] = {0.f, 0.f, 0.f, 0.f};
+            float a4[NG][4], off[NG][4];
+#pragma unroll
+            for (int gi = 0; gi < NG; ++gi)
+                off[gi][0] = off[gi][1] = off[gi][2] = off[gi][3] = 0.f;
 #pragma unroll
             for (int jj = 0; jj < NJ; jj += 4) {
                 const uint32_t row = st + h * TILE * C::RB;
@@ -629,35 +625,50 @@ __global__ void __launch_bounds__(Cfg<D>::NW * 32, Cfg<D>::CTAS_PER_SM) decode_k
                 const uint2 sa = lds64(srow);
                 const uint2 sb = lds64(srow + 8 * C::SB);
                 const float ta = lds_half(srow + 2 * t), tb = lds_half(srow + 8 * C::SB + 2 * t);
-                mma_tf32(off, ta, tb, ta, tb, ct[jj / 4][0], ct[jj / 4][1]);
+#pragma unroll
+                for (int gi = 0; gi < NG; ++gi)
+                    mma_tf32(off[gi], ta, tb, ta, tb, ct[gi][jj / 4][0], ct[gi][jj / 4][1]);
                 const uint32_t a[4] = {wa.x, wa.y, wa.z, wa.w};
                 const uint32_t b[4] = {wb.x, wb.y, wb.z, wb.w};
                 const float2 fa[2] = {__half22float2(as_half2(sa.x)), __half22float2(as_half2(sa.y))};
                 const float2 fb[2] = {__half22float2(as_half2(sb.x)), __half22float2(as_half2(sb.y))};
-                float d[4][4];
+                float d[NG][4][4];
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
-                    mma_zero(d[q], a[q] & 0x000f000fu, b[q] & 0x000f000fu, a[q] & 0x00f000f0u,
-                             b[q] & 0x00f000f0u, qb[jj + q][0], qb[jj + q][1]);
+#pragma unroll
+                    for (int gi = 0; gi < NG; ++gi)
+                        mma_zero(d[gi][q], a[q] & 0x000f000fu, b[q] & 0x000f000fu,
+                                 a[q] & 0x00f000f0u, b[q] & 0x00f000f0u, qb[gi][jj + q][0],
+                                 qb[gi][jj + q][1]);
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     const uint32_t ah = a[q] >> 8, bh = b[q] >> 8;
-                    tc::mma16816(d[q], ah & 0x000f000fu, bh & 0x000f000fu, ah & 0x00f000f0u,
-                                 bh & 0x00f000f0u, qb[jj + q][2], qb[jj + q][3]);
+#pragma unroll
+                    for (int gi = 0; gi < NG; ++gi)
+                        tc::mma16816(d[gi][q], ah & 0x000f000fu, bh & 0x000f000fu,
+                                     ah & 0x00f000f0u, bh & 0x00f000f0u, qb[gi][jj + q][2],
+                                     qb[gi][jj + q][3]);
                 }
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     const float ka = q & 1 ? fa[q / 2].y : fa[q / 2].x;
                     const float kb = q & 1 ? fb[q / 2].y : fb[q / 2].x;
-                    a4[0] = jj + q ? fmaf(d[q][0], ka, a4[0]) : d[q][0] * ka;
-                    a4[1] = jj + q ? fmaf(d[q][1], ka, a4[1]) : d[q][1] * ka;
-                    a4[2] = jj + q ? fmaf(d[q][2], kb, a4[2]) : d[q][2] * kb;
-                    a4[3] = jj + q ? fmaf(d[q][3], kb, a4[3]) : d[q][3] * kb;
+#pragma unroll
+                    for (int gi = 0; gi < NG; ++gi) {
+                        const float *x = d[gi][q];
+                        float *y = a4[gi];
+                        y[0] = jj + q ? fmaf(x[0], ka, y[0]) : x[0] * ka;
+                        y[1] = jj + q ? fmaf(x[1], ka, y[1]) : x[1] * ka;
+                        y[2] = jj + q ? fmaf(x[2], kb, y[2]) : x[2] * kb;
+                        y[3] = jj + q ? fmaf(x[3], kb, y[3]) : x[3] * kb;
+                    }
                 }
             }
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-                sc[h][q] = fmaf(a4[q], c2, off[q]);          // log2 units
+            for (int gi = 0; gi < NG; ++gi)
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    sc[gi][h][q] = fmaf(a4[gi][q], c2, off[gi][q]);          // log2 units
         }
         // the pair's V scales, a few words per lane, against the limit
         constexpr int NVW = 2 * TILE * NJ / 2 / 32;
@@ -676,14 +687,15 @@ __global__ void __launch_bounds__(Cfg<D>::NW * 32, Cfg<D>::CTAS_PER_SM) decode_k
             for (int h = 0; h < 2; ++h) {
                 const int ka = base + h * TILE + g, kb = ka + 8;
                 const bool un = !((have >> h) & 1u);
-                if (un || ka < clo[0] || ka >= chi[0])
-                    sc[h][0] = -INFINITY;
-                if (un || ka < clo[1] || ka >= chi[1])
-                    sc[h][1] = -INFINITY;
-                if (un || kb < clo[0] || kb >= chi[0])
-                    sc[h][2] = -INFINITY;
-                if (un || kb < clo[1] || kb >= chi[1])
-                    sc[h][3] = -INFINITY;
+#pragma unroll
+                for (int gi = 0; gi < NG; ++gi)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        if (un || ka < clo[gi][x] || ka >= chi[gi][x])
+                            sc[gi][h][x] = -INFINITY;
+                        if (un || kb < clo[gi][x] || kb >= chi[gi][x])
+                            sc[gi][h][2 + x] = -INFINITY;
+                    }
             }
             // other rows must not turn a zero weight into NaN
 #pragma unroll
@@ -698,29 +710,31 @@ __global__ void __launch_bounds__(Cfg<D>::NW * 32, Cfg<D>::CTAS_PER_SM) decode_k
 #pragma unroll
             for (int h = 0; h < 2; ++h)
                 if ((have >> h) & 1u)
-                    tc::store_scores(p, cw.unit(p), base + h * TILE + g, base + h * TILE + g + 8,
-                                     2 * t, nh, sc[h]);
+#pragma unroll
+                    for (int gi = 0; gi < NG; ++gi)
+                        tc::store_scores(scores, p.sh, base + h * TILE + g, base + h * TILE + g + 8,
+                                         gi * GPH + 2 * t, nh, sc[gi][h]);
         }
         // ---- online softmax
         __half2 vm = as_half2(vw[0]);
 #pragma unroll
         for (int q = 1; q < NVW; ++q)
             vm = __hmax2(vm, as_half2(vw[q]));
-        const float x0 = fmaxf(fmaxf(sc[0][0], sc[0][2]), fmaxf(sc[1][0], sc[1][2]));
-        const float x1 = fmaxf(fmaxf(sc[0][1], sc[0][3]), fmaxf(sc[1][1], sc[1][3]));
-        const bool over = fmaxf(x0 - mr[0], x1 - mr[1]) > MAX_SLACK || !__hble2(vm, vlim);
+        float top[NG][2];
+        bool over = !__hble2(vm, vlim);
+#pragma unroll
+        for (int gi = 0; gi < NG; ++gi)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                top[gi][x] = fmaxf(fmaxf(sc[gi][0][x], sc[gi][0][2 + x]),
+                                   fmaxf(sc[gi][1][x], sc[gi][1][2 + x]));
+                over = over || top[gi][x] - mr[gi][x] > MAX_SLACK;
+            }
         if (__any_sync(0xffffffffu, over)) {
-            float y0 = x0, y1 = x1;
             float vx = __half2float(__hmax(__low2half(vm), __high2half(vm)));
 #pragma unroll
-            for (int mask = 1; mask <= 16; mask <<= 1) {
-                if (mask >= 4) {
-                    y0 = fmaxf(y0, __shfl_xor_sync(0xffffffffu, y0, mask));
-                    y1 = fmaxf(y1, __shfl_xor_sync(0xffffffffu, y1, mask));
-                }
+            for (int mask = 1; mask <= 16; mask <<= 1)
                 vx = fmaxf(vx, __shfl_xor_sync(0xffffffffu, vx, mask));
-            }
-            const float n0 = fmaxf(mr[0], y0), n1 = fmaxf(mr[1], y1);
             int en = e;
             if (vx > __low2float(vlim)) {
                 // the largest scale so far: carried as it is from 2^-12 to
@@ -729,19 +743,24 @@ __global__ void __launch_bounds__(Cfg<D>::NW * 32, Cfg<D>::CTAS_PER_SM) decode_k
                 en = (ex >= -11 && ex <= 7) ? 0 : max(ex, -14);
                 vlim = __float2half2_rn(en == 0 ? 128.f : fminf(pow2(en + 2), 65504.f));
             }
-            const float a0 = ex2_ftz(mr[0] - n0), a1 = ex2_ftz(mr[1] - n1);
-            l[0] *= a0;
-            l[1] *= a1;
-            const float r0e = a0 * pow2(e - en), r1e = a1 * pow2(e - en);
 #pragma unroll
-            for (int ii = 0; ii < 2 * NJ; ++ii) {
-                acc[ii][0] *= r0e;
-                acc[ii][1] *= r1e;
-                acc[ii][2] *= r0e;
-                acc[ii][3] *= r1e;
-            }
-            mr[0] = n0;
-            mr[1] = n1;
+            for (int gi = 0; gi < NG; ++gi)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    float y = top[gi][x];
+#pragma unroll
+                    for (int mask = 4; mask <= 16; mask <<= 1)
+                        y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, mask));
+                    y = fmaxf(y, mr[gi][x]);
+                    const float a = ex2_ftz(mr[gi][x] - y), r = a * pow2(e - en);
+                    l[gi][x] *= a;
+                    mr[gi][x] = y;
+#pragma unroll
+                    for (int ii = 0; ii < 2 * NJ; ++ii) {
+                        acc[gi][ii][x] *= r;
+                        acc[gi][ii][2 + x] *= r;
+                    }
+                }
             e = en;
         }
         if (e != 0) {
@@ -754,13 +773,18 @@ __global__ void __launch_bounds__(Cfg<D>::NW * 32, Cfg<D>::CTAS_PER_SM) decode_k
         // ---- O^T += V^T . (P s)^T: rows are elements, 4 per block and lane
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const float p0 = ex2_ftz(sc[h][0] - mr[0]), p1 = ex2_ftz(sc[h][1] - mr[1]);
-            const float p2 = ex2_ftz(sc[h][2] - mr[0]), p3 = ex2_ftz(sc[h][3] - mr[1]);
-            l[0] += p0 + p2;
-            l[1] += p1 + p3;
             // P^T as the B operand: keys (2t, 2t+1) and (2t+8, 2t+9), column g
-            const __half2 pa = as_half2(tc::movmatrix_t(tc::pack_half2(p0, p1)));
-            const __half2 pb = as_half2(tc::movmatrix_t(tc::pack_half2(p2, p3)));
+            __half2 pa[NG], pb[NG];
+#pragma unroll
+            for (int gi = 0; gi < NG; ++gi) {
+                const float *x = sc[gi][h];
+                const float p0 = ex2_ftz(x[0] - mr[gi][0]), p1 = ex2_ftz(x[1] - mr[gi][1]);
+                const float p2 = ex2_ftz(x[2] - mr[gi][0]), p3 = ex2_ftz(x[3] - mr[gi][1]);
+                l[gi][0] += p0 + p2;
+                l[gi][1] += p1 + p3;
+                pa[gi] = as_half2(tc::movmatrix_t(tc::pack_half2(p0, p1)));
+                pb[gi] = as_half2(tc::movmatrix_t(tc::pack_half2(p2, p3)));
+            }
             // V scales as half2 over the same key pairs
             __half2 sv[2][NJ];
 #pragma unroll
@@ -786,12 +810,6 @@ __global__ void __launch_bounds__(Cfg<D>::NW * 32, Cfg<D>::CTAS_PER_SM) decode_k
                     const uint4 x = lds128(row + vc[q & 1][jj / 4] + (q >> 1) * 8 * C::RB);
                     v[q][0] = x.x; v[q][1] = x.y; v[q][2] = x.z; v[q][3] = x.w;
                 }
-                uint32_t s0[4], s1[4];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    s0[q] = as_u32(__hmul2(pa, sv[0][jj + q]));
-                    s1[q] = as_u32(__hmul2(pb, sv[1][jj + q]));
-                }
                 auto even = [](uint32_t z) {
                     return as_u32(__hsub2(as_half2(z & 0x000f000fu), as_half2(0x00080008u)));
                 };
@@ -800,12 +818,19 @@ __global__ void __launch_bounds__(Cfg<D>::NW * 32, Cfg<D>::CTAS_PER_SM) decode_k
                 };
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
+                    const int j = jj + q;
                     const uint32_t x = __byte_perm(v[0][q], v[1][q], half_sel);
                     const uint32_t y = __byte_perm(v[2][q], v[3][q], half_sel);
                     const uint32_t xh = x >> 8, yh = y >> 8;
-                    tc::mma16816(acc[2 * (jj + q)], even(x), odd(x), even(y), odd(y), s0[q], s1[q]);
-                    tc::mma16816(acc[2 * (jj + q) + 1], even(xh), odd(xh), even(yh), odd(yh), s0[q],
-                                 s1[q]);
+                    const uint32_t a[4] = {even(x), odd(x), even(y), odd(y)};
+                    const uint32_t b[4] = {even(xh), odd(xh), even(yh), odd(yh)};
+#pragma unroll
+                    for (int gi = 0; gi < NG; ++gi) {
+                        const uint32_t s0 = as_u32(__hmul2(pa[gi], sv[0][j]));
+                        const uint32_t s1 = as_u32(__hmul2(pb[gi], sv[1][j]));
+                        tc::mma16816(acc[gi][2 * j], a[0], a[1], a[2], a[3], s0, s1);
+                        tc::mma16816(acc[gi][2 * j + 1], b[0], b[1], b[2], b[3], s0, s1);
+                    }
                 }
             }
         }
@@ -817,46 +842,48 @@ __global__ void __launch_bounds__(Cfg<D>::NW * 32, Cfg<D>::CTAS_PER_SM) decode_k
         cw.k += nb;
         if (cw.k == cw.n || i == n_my) {
             // ---- end of this worker's segment of the unit
-#pragma unroll
-            for (int mask = 4; mask <= 16; mask <<= 1) {
-                l[0] += __shfl_xor_sync(0xffffffffu, l[0], mask);
-                l[1] += __shfl_xor_sync(0xffffffffu, l[1], mask);
-            }
             const long long us = cw.unit_start();
             const bool whole = tc::worker_of(us, T, We) == tc::worker_of(us + cw.n - 1, T, We);
             const int kv = cw.j / p.n_hg, cg = cw.j % p.n_hg;
             const long long slot = w + cw.unit(p);
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const int h = 2 * t + x;
-                if (h >= nh)
-                    continue;
-                const float mx = mr[x] == NO_MAX ? -INFINITY : mr[x];
-                // 2^24 and 2^20 as the accumulators hold them; l = 0 only without keys
-                const float up = whole && l[x] > 0.f ? pow2(e + 20) / l[x] : pow2(e + 20);
-                const float up16 = up * 16.f;
-                if (whole) {
-                    const tc::Col cc = tc::column(p, kv, cg, h, GPH);
-                    const long long r = ((long long)cw.b * tq + cc.j) * p.Hq + cc.h;
-                    __half *o = reinterpret_cast<__half *>(p.out) + r * D + 4 * g;
+            for (int gi = 0; gi < NG; ++gi)
 #pragma unroll
-                    for (int j = 0; j < NJ; ++j)
-                        tc::store4(o + 32 * j,
-                                   make_float4(acc[2 * j][x] * up16, acc[2 * j][x + 2] * up,
-                                               acc[2 * j + 1][x] * up16, acc[2 * j + 1][x + 2] * up));
-                    if (WT && g == 0)
-                        p.lse[r] = l[x] > 0.f ? mx + log2f(l[x]) : -INFINITY;
-                } else {
-                    float *o = p.ws_o + (slot * p.sh + h) * D + 4 * g;
+                for (int x = 0; x < 2; ++x) {
+                    float lx = l[gi][x];
 #pragma unroll
-                    for (int j = 0; j < NJ; ++j)
-                        tc::store4(o + 32 * j,
-                                   make_float4(acc[2 * j][x] * up16, acc[2 * j][x + 2] * up,
-                                               acc[2 * j + 1][x] * up16, acc[2 * j + 1][x + 2] * up));
-                    if (g == 0)
-                        p.ws_ml[slot * p.sh + h] = make_float2(mx, l[x]);
+                    for (int mask = 4; mask <= 16; mask <<= 1)
+                        lx += __shfl_xor_sync(0xffffffffu, lx, mask);
+                    const int h = gi * GPH + 2 * t + x;
+                    if (h >= nh)
+                        continue;
+                    const float mx = mr[gi][x] == NO_MAX ? -INFINITY : mr[gi][x];
+                    // 2^24 and 2^20 as the accumulators hold them; l = 0 only without keys
+                    const float up = whole && lx > 0.f ? pow2(e + 20) / lx : pow2(e + 20);
+                    const float up16 = up * 16.f;
+                    auto four = [&](int j) {
+                        return make_float4(acc[gi][2 * j][x] * up16, acc[gi][2 * j][x + 2] * up,
+                                           acc[gi][2 * j + 1][x] * up16,
+                                           acc[gi][2 * j + 1][x + 2] * up);
+                    };
+                    if (whole) {
+                        const tc::Col cc = tc::column(p, kv, cg, h, COLS);
+                        const long long r = ((long long)cw.b * tq + cc.j) * p.Hq + cc.h;
+                        __half *o = reinterpret_cast<__half *>(p.out) + r * D + 4 * g;
+#pragma unroll
+                        for (int j = 0; j < NJ; ++j)
+                            tc::store4(o + 32 * j, four(j));
+                        if (WT && g == 0)
+                            p.lse[r] = lx > 0.f ? mx + log2f(lx) : -INFINITY;
+                    } else {
+                        float *o = p.ws_o + (slot * p.sh + h) * D + 4 * g;
+#pragma unroll
+                        for (int j = 0; j < NJ; ++j)
+                            tc::store4(o + 32 * j, four(j));
+                        if (g == 0)
+                            p.ws_ml[slot * p.sh + h] = make_float2(mx, lx);
+                    }
                 }
-            }
             reset();
             if (i < n_my) {
                 --cw.k;
@@ -869,25 +896,21 @@ __global__ void __launch_bounds__(Cfg<D>::NW * 32, Cfg<D>::CTAS_PER_SM) decode_k
 }
 
 // ------------------------------------------------- attention, many columns
-// More than 16 (query, head) columns per KV head: with 8 columns per warp every
-// group would unpack the codes again, 130 of its ~280 instructions per tile.
-// Here a CTA of four warps unpacks a tile of KT keys once into shared memory as
-// fp16 codes, and its warps share it: CW warps of 16 columns each (the mma's M:
-// S[16 columns x keys] = Q . K^T, whose accumulators are the A operand of
-// O[16 x D] += (P s) . V without a transpose) times KS = 4 / CW slices of the
-// tile's keys.  Scales are used as above, K's in fp32 after each block's mma,
-// V's on the weights.  The fp16 copies hold the code's value itself, so nothing
-// is to be taken off later.
-// Work is split as above with CTAs as workers; a unit has CW * 16 columns.
-// Bound by the mma rate: 32 of them per 16 keys, 16 columns and warp at D = 128.
-template <int D, int CW>
+// 64 (query, head) columns per unit, for calls with many of them: a CTA of four
+// warps unpacks a tile of KT keys once into shared memory as fp16 codes, and its
+// warps share it, 16 columns each (the mma's M: S[16 columns x keys] = Q . K^T,
+// whose accumulators are the A operand of O[16 x D] += (P s) . V without a
+// transpose).  Scales are used as above, K's in fp32 after each block's mma, V's on
+// the weights.  Work is split as above with CTAs as workers.
+// Bound by the instructions between its two barriers per tile; see WIDE_GROUPS for
+// where it wins.  (Deeper prefetch and tiles of 128 keys changed nothing; 32 columns
+// with the keys in two slices lost to the kernel above.)
+template <int D>
 struct WideCfg {
     static constexpr int KT = D == 128 ? 64 : 32;      // keys per tile
     static constexpr int SUB = KT / TILE;              // 16-key subtiles per tile
-    static constexpr int KS = 4 / CW;                  // key slices
-    static constexpr int SK = KT / KS;                 // keys per slice
-    static constexpr int CK = SK < 32 ? SK : 32;       // keys per softmax step
-    static constexpr int COLS = 16 * CW;
+    static constexpr int CK = 32;                      // keys per softmax step
+    static constexpr int COLS = 64;
     static constexpr int NJ = D / 32, RB = D / 2, SB = D / 16;
     static constexpr int RAW_K = 0, RAW_V = KT * RB;   // codes as copied (swizzled rows)
     static constexpr int SC = 2 * KT * RB;             // two stages of K scales, V scales
@@ -895,13 +918,9 @@ struct WideCfg {
     static constexpr int F16_K = SC + 2 * SC_STAGE;    // codes as fp16, rows of 2 D bytes
     static constexpr int F16_V = F16_K + KT * D * 2;
     static constexpr int Q = F16_V + KT * D * 2;       // the unit's queries
-    static constexpr int JOIN_ML = Q + COLS * D * 2;   // slice 1's (m, l) per column
-    static constexpr int SMEM = JOIN_ML + COLS * 8;
+    static constexpr int SMEM = Q + COLS * D * 2;
     static constexpr int CTAS_PER_SM = D == 128 ? 3 : 2;
-    static_assert(SK % 16 == 0, "the PV mma takes 16 keys");
     static_assert(F16_K % 128 == 0 && Q % 128 == 0, "swizzled rows");
-    // slices are joined in the fp16 buffers: 16 columns x D floats per warp
-    static_assert(KS == 1 || CW * 16 * D * 4 <= 2 * KT * D * 2, "join buffer");
     static_assert(CTAS_PER_SM * (SMEM + 1024) <= 228 * 1024, "shared memory per SM");
 };
 
@@ -912,16 +931,16 @@ __device__ __forceinline__ int f16_off(int r, int c)
     return r * (2 * D) + ((c ^ (r & 7)) << 4);
 }
 
-template <int D, int CW, bool WT>
-__global__ void __launch_bounds__(128, WideCfg<D, CW>::CTAS_PER_SM) wide_kernel(const Params p)
+template <int D, bool WT>
+__global__ void __launch_bounds__(128, WideCfg<D>::CTAS_PER_SM) wide_kernel(const Params p)
 {
-    using C = WideCfg<D, CW>;
+    using C = WideCfg<D>;
     constexpr int NJ = C::NJ, KT = C::KT, SUB = C::SUB, CK = C::CK, NT = CK / 8;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, t = lane & 3;
-    const int cwi = warp % CW, ks = warp / CW;     // this warp's columns and key slice
+    const int cwi = warp;                          // this warp's 16 columns
     const int w = blockIdx.x;
     int b_at = -1, We = 0;
     long long P_at = 0, T = 0, t0 = 0, t1 = 0;
@@ -1111,9 +1130,8 @@ __global__ void __launch_bounds__(128, WideCfg<D, CW>::CTAS_PER_SM) wide_kernel(
         if (i < n_my)
             copy(stage ^ 1);
 
-        const int k_lo = ks * C::SK;               // this warp's keys of the tile
 #pragma unroll 1
-        for (int kk = k_lo; kk < k_lo + C::SK && kk < nb * TILE; kk += CK) {
+        for (int kk = 0; kk < nb * TILE; kk += CK) {
             // ---- scores: 8 keys per mma, blocks of 32 elements scaled in fp32
             float sc4[NT][4];
             float kscale[NT][2][4];
@@ -1187,12 +1205,9 @@ __global__ void __launch_bounds__(128, WideCfg<D, CW>::CTAS_PER_SM) wide_kernel(
             }
             // ---- online softmax (as above: the maximum moves when passed by 8)
             __half2 vm = __float2half2_rn(0.f);
-            constexpr int NVW = CK * NJ / 2 / 32;
 #pragma unroll
-            for (int q = 0; q < (NVW > 0 ? NVW : 1); ++q)
-                if (NVW > 0 || lane < CK * NJ / 2)
-                    vm = __hmax2(vm, as_half2(lds32(sc + KT * C::SB + kk * C::SB +
-                                                    (lane + 32 * q) * 4)));
+            for (int q = 0; q < CK * NJ / 2 / 32; ++q)
+                vm = __hmax2(vm, as_half2(lds32(sc + KT * C::SB + kk * C::SB + (lane + 32 * q) * 4)));
             float x0 = sc4[0][0], x1 = sc4[0][2];
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
@@ -1301,48 +1316,8 @@ __global__ void __launch_bounds__(128, WideCfg<D, CW>::CTAS_PER_SM) wide_kernel(
             l[0] += __shfl_xor_sync(0xffffffffu, l[0], mask);
             l[1] += __shfl_xor_sync(0xffffffffu, l[1], mask);
         }
-        const float up = pow2(e);
-        if constexpr (C::KS == 2) {
-            // slice 1 hands its sums to slice 0 through the fp16 buffers
-            float *join = reinterpret_cast<float *>(smem + C::F16_K) + cwi * (16 * D);
-            float *join_ml = reinterpret_cast<float *>(smem + C::JOIN_ML) + (cwi * 8 + g) * 4;
-            __syncthreads();
-            if (ks == 1) {
-#pragma unroll
-                for (int n = 0; n < D / 8; ++n)
-#pragma unroll
-                    for (int x = 0; x < 4; ++x)
-                        join[(n * 4 + x) * 32 + lane] = acc[n][x] * up;
-                if (t == 0) {
-                    join_ml[0] = mr[0];
-                    join_ml[1] = l[0];
-                    join_ml[2] = mr[1];
-                    join_ml[3] = l[1];
-                }
-            }
-            __syncthreads();
-            if (ks == 0) {
-                float f0[2], f1[2];
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const float m1 = join_ml[2 * x], l1 = join_ml[2 * x + 1];
-                    const float m = fmaxf(mr[x], m1);
-                    f0[x] = ex2_ftz(mr[x] - m);
-                    f1[x] = ex2_ftz(m1 - m);
-                    l[x] = l[x] * f0[x] + l1 * f1[x];
-                    mr[x] = m;
-                }
-#pragma unroll
-                for (int n = 0; n < D / 8; ++n)
-#pragma unroll
-                    for (int x = 0; x < 4; ++x)
-                        acc[n][x] = acc[n][x] * (up * f0[x >> 1]) +
-                                    join[(n * 4 + x) * 32 + lane] * f1[x >> 1];
-            }
-            // (the next tile's unpacking starts after a barrier)
-        }
-        if (ks == 0) {
-            const float un = C::KS == 2 ? 1.f : up;
+        const float un = pow2(e);
+        {
             const long long us = cw.unit_start();
             const bool whole = tc::worker_of(us, T, We) == tc::worker_of(us + cw.n - 1, T, We);
             const int kv = cw.j / p.n_hg, cg = cw.j % p.n_hg;
@@ -1391,33 +1366,47 @@ __global__ void __launch_bounds__(128, WideCfg<D, CW>::CTAS_PER_SM) wide_kernel(
 }
 
 // ---------------------------------------------------------------- host side
-// Columns per KV head from which the kernel with a shared unpacked tile is taken: at
-// 16 the two cost the same per key (two groups' unpacking against half-idle warps).
-#ifndef FA_I4_WIDE_MIN
-#define FA_I4_WIDE_MIN 17
-#endif
-constexpr int WIDE_MIN_COLS = FA_I4_WIDE_MIN;
+// Groups of 8 columns from which a unit of 64 columns pays.  Over 16 x 4096 keys of 4
+// heads, D = 128 / 256: a unit takes ~38 / 80 us and a group of 8 ~6.5 / 12.7, so six
+// groups cost what a unit does (64 columns: 58 against 67 us at D = 128, 109
+// against 116 at 256; 72, two units, would lose).
+constexpr int WIDE_GROUPS = 6;
+// Tiles per warp (at full capacity, with units of 8 columns) from which a unit of 16
+// columns is taken at D = 128: fewer, larger units cost parallelism first.  16 columns
+// on 16 sequences x 4 heads: 512 keys (2 tiles) 23 us against 20, 4096 (18) 31 and
+// 31, 32768 (144) 93 against 119.  Not with recorded weights, whose passes over the
+// scores outweigh it (24 columns, 32768 keys: 324 us against 253).
+constexpr double TWO_GROUP_MIN_TILES = 20.0;
 
 struct Plan {
     int ctas, W, n_hg, units, sh, cpu;
     size_t bytes;                // partial slots and prefix
 };
 
-static Plan make_plan(int B, int tq, int Hq, int Hkv, int D, long long cap, int sms)
+static Plan make_plan(int B, int tq, int Hq, int Hkv, int D, long long cap, int sms,
+                      bool weights)
 {
     Plan pl = {};
     const int cols = tq * (Hq / Hkv);
-    pl.cpu = cols < WIDE_MIN_COLS ? GPH : cols <= 32 ? 32 : 64;
+    const int groups = (cols + GPH - 1) / GPH;
+    const double per_warp = (double)B * Hkv * groups * ((cap + TILE - 1) / TILE) /
+                            ((double)sms * Cfg<128, 1>::CTAS_PER_SM * Cfg<128, 1>::NW);
+    pl.cpu = groups > WIDE_GROUPS * ((cols + 63) / 64)                              ? 64
+             : D == 128 && groups > 1 && !weights && per_warp >= TWO_GROUP_MIN_TILES ? 2 * GPH
+                                                                                    : GPH;
     pl.n_hg = (cols + pl.cpu - 1) / pl.cpu;
     pl.sh = cols < pl.cpu ? cols : pl.cpu;
     pl.units = Hkv * pl.n_hg;
     int nw, cps;                 // workers per CTA, CTAs per SM
-    if (pl.cpu == GPH) {
-        nw = D == 128 ? Cfg<128>::NW : Cfg<256>::NW;
-        cps = D == 128 ? Cfg<128>::CTAS_PER_SM : Cfg<256>::CTAS_PER_SM;
-    } else {
+    if (pl.cpu == 64) {
         nw = 1;
-        cps = D == 128 ? WideCfg<128, 4>::CTAS_PER_SM : WideCfg<256, 4>::CTAS_PER_SM;
+        cps = D == 128 ? WideCfg<128>::CTAS_PER_SM : WideCfg<256>::CTAS_PER_SM;
+    } else if (pl.cpu == 16) {
+        nw = Cfg<128, 2>::NW;
+        cps = Cfg<128, 2>::CTAS_PER_SM;
+    } else {
+        nw = D == 128 ? Cfg<128, 1>::NW : Cfg<256, 1>::NW;
+        cps = D == 128 ? Cfg<128, 1>::CTAS_PER_SM : Cfg<256, 1>::CTAS_PER_SM;
     }
     // one persistent wave, capped at a worker per position the capacity allows
     const long long most = ((long long)B * pl.units * ((cap + TILE - 1) / TILE + tc::UNIT_COST) +
@@ -1467,12 +1456,15 @@ static cudaError_t launch(const Params &p, int ctas, int sms, cudaStream_t st)
 {
     static bool done[3][64] = {};
     cudaError_t e;
-    if (p.cpu == GPH)
-        e = launch_split(decode_kernel<D, WT>, done[0], p, ctas, Cfg<D>::NW * 32, Cfg<D>::SMEM, st);
-    else if (p.cpu == 32)
-        e = launch_split(wide_kernel<D, 2, WT>, done[1], p, ctas, 128, WideCfg<D, 2>::SMEM, st);
-    else
-        e = launch_split(wide_kernel<D, 4, WT>, done[2], p, ctas, 128, WideCfg<D, 4>::SMEM, st);
+    if (p.cpu == 64) {
+        e = launch_split(wide_kernel<D, WT>, done[0], p, ctas, 128, WideCfg<D>::SMEM, st);
+    } else if (p.cpu == GPH) {
+        using C = Cfg<D, 1>;
+        e = launch_split(decode_kernel<D, 1, WT>, done[1], p, ctas, C::NW * 32, C::SMEM, st);
+    } else {
+        using C = Cfg<128, 2>;       // the plan gives 16 columns at D = 128, without weights
+        e = launch_split(decode_kernel<128, 2, false>, done[2], p, ctas, C::NW * 32, C::SMEM, st);
+    }
     return e == cudaSuccess ? launch_merge_half<D>(p, sms, st) : e;
 }
 
@@ -1680,7 +1672,7 @@ FA_API size_t fa_decode_int4_workspace_size(int batch, int n_queries, int n_q_he
     if (num_sms <= 0 && device_sms(&num_sms) != 0)
         return 0;
     const i4::Plan pl = i4::make_plan(batch, n_queries, n_q_heads, n_kv_heads, head_dim,
-                                      max_kv_len, num_sms);
+                                      max_kv_len, num_sms, with_weights != 0);
     if (!with_weights)
         return pl.bytes;
     WeightSpace ws;
@@ -1736,7 +1728,8 @@ FA_API int fa_decode_int4(const void *q, const void *k_codes, const void *k_scal
     int sms = 0;
     if ((rc = device_sms(&sms)))
         return rc;
-    const i4::Plan pl = i4::make_plan(batch, n_queries, n_q_heads, n_kv_heads, head_dim, cap, sms);
+    const i4::Plan pl = i4::make_plan(batch, n_queries, n_q_heads, n_kv_heads, head_dim, cap, sms,
+                                      acc != nullptr);
     size_t need = pl.bytes;
     WeightSpace wsp = {};
     if (acc) {

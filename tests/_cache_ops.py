@@ -49,9 +49,11 @@ def dequantize(by, scales):
 # ------------------------------------------------------------------ cache layouts
 class Layout:
     """Where token t of (sequence, head) lives: paged through a shuffled table with
-    spare blocks, or contiguous.  `cap` tokens per sequence."""
+    spare blocks, or contiguous.  `cap` tokens per sequence; `room`: a table with that
+    many tokens of capacity, its entries beyond `cap` unmapped."""
 
-    def __init__(self, batch, hkv, cap, paged, page=16, spare=2, seed=0):
+    def __init__(self, batch, hkv, cap, paged, page=16, spare=2, seed=0, room=0):
+        self.room = room
         self.batch, self.hkv, self.cap, self.page, self.paged = batch, hkv, cap, page, paged
         if paged:
             self.blocks = -(-cap // page)
@@ -92,8 +94,16 @@ class Layout:
                 m[b] = d
         return m
 
+    @property
+    def capacity(self):
+        """Tokens per sequence that the table (or the contiguous cache) has room for."""
+        return max(self.cap, -(-self.room // self.page) * self.page if self.paged else 0)
+
     def table_gpu(self):
-        return None if self.table is None else torch.from_numpy(self.table.copy()).cuda()
+        if self.table is None:
+            return None
+        more = self.capacity // self.page - self.table.shape[1]
+        return torch.from_numpy(np.pad(self.table, ((0, 0), (0, more)), constant_values=-1)).cuda()
 
 
 def ranges(n, tq, window, cap):

@@ -107,7 +107,7 @@ def run(lay, cache, q, lens, Hq, scale, window=None, acc=None, stream=None, ws=N
     B, tq, _, D = q.shape
     out = torch.full(q.shape, float("nan"), dtype=torch.float16, device="cuda")
     if ws is None:
-        ws = fa.alloc_workspace_int4(B, tq, Hq, lay.hkv, D, lay.cap, weights=acc is not None)
+        ws = fa.alloc_workspace_int4(B, tq, Hq, lay.hkv, D, lay.capacity, weights=acc is not None)
         ws.fill_(0xFF)
     fa.fa_decode_int4(cuda(q), *cache.gpu(), lay.table_gpu(), lens_gpu(lens), Hq, lay.hkv, D, scale,
                       None if window is None else lens_gpu(window), out, acc=acc, workspace=ws,
@@ -126,8 +126,9 @@ def check(lay, cache, q, lens, Hq, scale, window=None, weights=True):
         return
     before = np.random.RandomState(9).random_sample(lay.rows).astype(np.float32)
     acc = cuda(before)
-    got2 = run(lay, cache, q, lens, Hq, scale, window, acc=acc)
-    assert np.array_equal(got2.cpu().numpy().astype(np.float64), got)
+    # with acc another plan may serve the call: held to the same derived bound
+    got2 = run(lay, cache, q, lens, Hq, scale, window, acc=acc).cpu().numpy().astype(np.float64)
+    assert (np.abs(got2 - want) - cache.tolerance(want, absum, size)).max() <= 0
     after = acc.cpu().numpy().astype(np.float64)
     cols = q.shape[1] * Hq // lay.hkv
     full = before.astype(np.float64)
@@ -188,6 +189,16 @@ def test_many_columns_layouts_and_magnitudes(D, paged, page):
     cache = Int4Cache(lay, D, lens, seed=2, v_mag=ramp)
     for tq, Hq in ((5, 8), (12, 8)):
         check(lay, cache, queries(4, tq, Hq, D, tq, mag=1.5), lens, Hq, D ** -0.5)
+
+
+@pytest.mark.parametrize("tq,Hq,windowed", [(3, 6, False), (4, 8, True), (5, 16, False), (12, 2, True)])
+def test_two_column_groups(tq, Hq, windowed):
+    """Enough capacity that units of 16 columns are taken (9 to 40 columns, head_dim 128)."""
+    lens = [2000, 17, 0, 999, 40, 16, 64]
+    lay = Layout(7, 2, 2000, True, 16, seed=3, room=1 << 17)
+    cache = Int4Cache(lay, 128, lens, seed=tq)
+    window = [0, 5, 3, 77, 0, 33, 1] if windowed else None
+    check(lay, cache, queries(16, tq, Hq, 128, tq), lens, Hq, 0.1, window)
 
 
 @pytest.mark.parametrize("scale", [0.0, -0.3, 2.0])
