@@ -198,7 +198,7 @@ def test_two_column_groups(tq, Hq, windowed):
     lay = Layout(7, 2, 2000, True, 16, seed=3, room=1 << 17)
     cache = Int4Cache(lay, 128, lens, seed=tq)
     window = [0, 5, 3, 77, 0, 33, 1] if windowed else None
-    check(lay, cache, queries(16, tq, Hq, 128, tq), lens, Hq, 0.1, window)
+    check(lay, cache, queries(7, tq, Hq, 128, tq), lens, Hq, 0.1, window)
 
 
 @pytest.mark.parametrize("scale", [0.0, -0.3, 2.0])
