@@ -405,8 +405,11 @@ __global__ void __launch_bounds__(THREADS, 2) evict_kernel(const Params p, const
         for (int q = 0; q < 4; ++q) {
             const int j = r0 + q * THREADS;
             long long src = -1;
-            if (j < x.budget)
+            if (j < x.budget) {
                 src = row_of(p, x, b, kv, __ldcg(kept + j));
+                if (src < 0)                      // one of the last n_recent
+                    flag(FA_STATUS_BAD_BLOCK);
+            }
             v[q] = src >= 0 ? __ldcg(x.acc + src) : 0.f;
         }
         sync_all();

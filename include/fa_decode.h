@@ -421,6 +421,7 @@ FA_API int fa_gather_kv_int4(const void *k_codes, const void *k_scales, const vo
  *      need no initialisation.
  * Other arguments, device-side status bits, errors, streams and graph capture
  * as fa_decode.  out, acc, the workspace and the inputs must not overlap.
+ * Caches of 2^31 rows or more are refused (FA_ERR_LAYOUT), as by fa_decode.
  */
 FA_API int fa_decode_int4(const void *q, const void *k_codes, const void *k_scales,
                           const void *v_codes, const void *v_scales, const int32_t *block_table,
@@ -493,9 +494,10 @@ FA_API size_t fa_decode_weights_workspace_size(int batch, int n_queries, int n_q
  * (else FA_ERR_LAYOUT).  head_dim 128 or 256.
  * Lengths outside [0, capacity] are clamped and set FA_STATUS_LEN_CLAMPED; a
  * token in an unmapped block counts as -infinity and is not moved
- * (FA_STATUS_BAD_BLOCK).  Blocks must not be shared between sequences.  No
- * two of the arrays may overlap (new_lens is not seq_lens).  All work is one
- * launch on `stream`, with no workspace.
+ * (FA_STATUS_BAD_BLOCK; one of the first n_sink tokens is not read, so it sets
+ * nothing).  Blocks must not be shared between sequences.  No two of the
+ * arrays may overlap (new_lens is not seq_lens).  The work is one or two
+ * kernels on `stream`, with no workspace.
  */
 FA_API int fa_evict_kv(void *k_cache, void *v_cache, void *k_scales, void *v_scales, float *acc,
                        const int32_t *block_table, const int32_t *seq_lens, int32_t *new_lens,

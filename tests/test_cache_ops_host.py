@@ -105,6 +105,21 @@ def test_evict_checks(lib, kw, code):
     assert rc == code, msg
 
 
+@pytest.mark.parametrize("kw", [dict(nblk=1 << 26), dict(bt=None, maxb=1 << 29, hq=4)])
+def test_caches_of_too_many_rows(lib, kw):
+    """Cache rows are counted in 32 bits: 2^31 of them are refused, one block fewer is not."""
+    far = {n: (i + 1) << 44 for i, n in enumerate(("kc", "ks", "vc", "vs", "acc", "ws"))}
+    at = {n: x for n, x in far.items() if DECODE.get(n) is not None}
+    rc, msg = rc_of(lib, "fa_decode_int4", DECODE, {**at, **kw})
+    assert rc == -6 and "2^31 rows" in msg
+    if "nblk" in kw:
+        rc, msg = rc_of(lib, "fa_decode_int4", DECODE, {**at, "nblk": (1 << 26) - 1, "wsb": 0})
+        assert rc in (-4, -8) and "2^31 rows" not in msg, msg       # the workspace, or no device
+    at = {n: x for n, x in far.items() if WEIGHTS.get(n) is not None}
+    rc, msg = rc_of(lib, "fa_decode_weights", WEIGHTS, {**at, **kw})
+    assert rc == -6 and "rows" in msg or rc == -8                   # planned for a device first
+
+
 def test_workspace_sizes():
     plain = binding.fa_decode_int4_workspace_size(4, 1, 8, 2, 128, 1000, False, 152)
     with_weights = binding.fa_decode_int4_workspace_size(4, 1, 8, 2, 128, 1000, True, 152)
