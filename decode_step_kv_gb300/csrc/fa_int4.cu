@@ -22,14 +22,15 @@ constexpr float X_MAX = 7.f * 65504.f;     // beyond it the scale saturates
 
 // The scale of a block whose largest magnitude is amax (<= X_MAX): amax / 7
 // rounded once to fp16.  The rounded product with 1/7 is it whenever amax - 7 h
-// (exact) stays clear of the midpoint, 7/2 units of h's last place away; else the
-// fp32 quotient is truncated with a sticky last bit, so that rounding it sees
-// which side of the midpoint the exact one is on.
+// (exact) stays clear of the midpoint, 7/2 units of h's last place away (of the
+// place below when h is a power of two); else the fp32 quotient is truncated with
+// a sticky last bit, so that rounding it sees which side of the midpoint the exact
+// one is on.
 __device__ __forceinline__ __half block_scale(float amax)
 {
     const __half h = __float2half_rn(amax * (1.f / 7.f));
     const float f = __half2float(h);
-    const float binade = __uint_as_float(__float_as_uint(f) & 0x7f800000u);
+    const float binade = __uint_as_float((max(__float_as_uint(f), 1u) - 1u) & 0x7f800000u);
     if (fabsf(fmaf(-7.f, f, amax)) < binade * (7.f / 2048.f * 0.999f))
         return h;
     float q = __fdiv_rz(amax, 7.f);
@@ -1409,10 +1410,11 @@ static Plan make_plan(int B, int tq, int Hq, int Hkv, int D, long long cap, int 
         cps = D == 128 ? Cfg<128, 1>::CTAS_PER_SM : Cfg<256, 1>::CTAS_PER_SM;
     }
     // one persistent wave, capped at a worker per position the capacity allows
-    const long long most = ((long long)B * pl.units * ((cap + TILE - 1) / TILE + tc::UNIT_COST) +
-                            nw - 1) / nw;
+    const double most = (double)B * pl.units * ((cap + TILE - 1) / TILE + tc::UNIT_COST);
     const long long wave = (long long)sms * cps;
-    pl.ctas = static_cast<int>(most < wave ? (most > 0 ? most : 1) : wave);
+    pl.ctas = static_cast<int>(most < (double)wave * nw ? ((long long)most + nw - 1) / nw : wave);
+    if (pl.ctas == 0)
+        pl.ctas = 1;
     pl.W = pl.ctas * nw;
     const size_t slots = (size_t)pl.W + (size_t)B * pl.units;
     pl.bytes = slots * pl.sh * (D * sizeof(float) + sizeof(float2)) +
@@ -1520,7 +1522,7 @@ static int check_rows(const char *name, const Span *outs, int n_outs, const Span
 static bool row_args(int T, int Hkv, int D, int page_size, const int *count, RowArgs *a)
 {
     const long long half = (long long)T * Hkv * (D / 16);
-    if (half > 0x7fffffffll)
+    if (half > 0x7fffffffll - 255)          // row_grid rounds up to whole CTAs
         return false;
     a->T = T;
     a->n_half = static_cast<int>(half);
