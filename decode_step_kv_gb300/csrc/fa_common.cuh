@@ -1304,14 +1304,16 @@ static int log2_of(int x)               // -1 when x is not a power of two
 }
 
 // The merge of an fp16 output, with the recorded weights when p.acc is set; as the
-// fp32 merge, a warp per row from MERGE_WARP_ROWS_PER_SM rows per SM.
+// fp32 merge, a warp per row from MERGE_WARP_ROWS_PER_SM rows per SM.  Beside the
+// recorded weights from one row per SM, which leaves their items more of the first
+// wave of CTAs (16 sequences of 16384 keys, 512 rows: 206 us with a CTA per row, 203).
 constexpr int MERGE_WARP_ROWS_PER_SM = 4;
 template <int D>
 static cudaError_t launch_merge_half(const Params &p0, int sms, cudaStream_t st)
 {
     Params p = p0;
     const long long rows = (long long)p.B * (p.tq > 1 ? p.tq : 1) * p.Hq;
-    const bool by_warp = rows >= (long long)MERGE_WARP_ROWS_PER_SM * sms;
+    const bool by_warp = rows >= (p.acc ? 1ll : MERGE_WARP_ROWS_PER_SM) * sms;
     const long long merge = by_warp ? (rows + tc::MERGE_ROWS_PER_CTA - 1) / tc::MERGE_ROWS_PER_CTA
                                     : rows;
     long long ctas = merge;
