@@ -16,7 +16,7 @@
 //   leave.  Ties go to the lowest index.  A CTA keeps its share of the totals in
 //   shared memory when it fits (24576 tokens), so they are read once.
 //   Move: rows go down in place (a kept row's new index is never above its old
-//   one).  A write to row j only clobbers a source when token j itself is kept,
+//   one; those before the first dropped token stay).  A write to row j only clobbers a source when token j itself is kept,
 //   so order matters only among the kept tokens below the budget.  Those move
 //   first, in rounds: every CTA of the cluster reads its rows of the round into
 //   shared memory, a cluster barrier, every CTA writes them (what a round
@@ -196,6 +196,7 @@ __global__ void __launch_bounds__(THREADS, 2) evict_kernel(const Params p, const
     __shared__ unsigned cnt[WARPS][2];
     __shared__ unsigned wsum[WARPS];
     __shared__ unsigned found[2];
+    __shared__ unsigned stay[2];             // this CTA's kept tokens: below the budget, at their places
     __shared__ Places pl;
     unsigned *part = reinterpret_cast<unsigned *>(pl.src);   // while selecting: this CTA's bin sums
     static_assert(sizeof(Places) >= BINS / 2 * sizeof(unsigned), "a share of the bins");
@@ -363,6 +364,8 @@ __global__ void __launch_bounds__(THREADS, 2) evict_kernel(const Params p, const
         cnt[warp][0] = n_gt;
         cnt[warp][1] = n_eq;
     }
+    if (tid < 2)
+        stay[tid] = 0;
     sync_sel();
     unsigned gt = 0, eq = 0;
     for (int i = lane; i < gw; i += 32) {
@@ -376,7 +379,7 @@ __global__ void __launch_bounds__(THREADS, 2) evict_kernel(const Params p, const
         gt += __shfl_xor_sync(0xffffffffu, gt, off);
         eq += __shfl_xor_sync(0xffffffffu, eq, off);
     }
-    unsigned at = x.sink + gt + min(eq, rem);
+    unsigned at = x.sink + gt + min(eq, rem), n_low = 0, n_fix = 0;
 #pragma unroll 4
     for (int t0 = w0; t0 < w1; t0 += 32) {
         const int t = t0 + lane;
@@ -388,8 +391,16 @@ __global__ void __launch_bounds__(THREADS, 2) evict_kernel(const Params p, const
         const unsigned to = at + __popc(km & below);
         if (keep && to < static_cast<unsigned>(x.budget))
             kept[to] = t;                         // solo: the same values by every CTA
+        n_low += keep && t < x.budget;
+        n_fix += keep && to == static_cast<unsigned>(t);
         at += __popc(km);
         eq += __popc(eqm);
+    }
+    n_low = __reduce_add_sync(0xffffffffu, n_low);
+    n_fix = __reduce_add_sync(0xffffffffu, n_fix);
+    if (lane == 0) {
+        atomicAdd(&stay[0], n_low);
+        atomicAdd(&stay[1], n_fix);
     }
     for (int j = sr * THREADS + tid; j < x.sink; j += sel * THREADS)
         kept[j] = j;
@@ -397,8 +408,22 @@ __global__ void __launch_bounds__(THREADS, 2) evict_kernel(const Params p, const
         kept[x.budget - x.recent + j] = n - x.recent + j;
     sync_sel();                                   // kept[] is complete
 
-    // ---- totals, in rounds: all of a round's reads before its writes
-    for (int j0 = x.sink; j0 < x.budget; j0 += cs * 4 * THREADS) {
+    // kept[] ascends: its first n_fix entries are at their places, its first n_near
+    // lie below the budget
+    {
+        const uint32_t a = smem_u32(stay);
+        const bool mine = lane < sel;
+        n_low = mine ? ld_cluster(sel > 1 ? tc::cl_map(a, lane) : a) : 0u;
+        n_fix = mine ? ld_cluster((sel > 1 ? tc::cl_map(a, lane) : a) + 4) : 0u;
+        n_low = __reduce_add_sync(0xffffffffu, n_low);
+        n_fix = __reduce_add_sync(0xffffffffu, n_fix);
+    }
+    const int n_still = x.sink + n_fix;
+    const int n_near = x.sink + n_low + min(max(x.budget - (n - x.recent), 0), x.recent);
+
+    // ---- totals that move, in rounds: all of a round's reads before its writes (one
+    // round at least: its barrier keeps the CTAs there until all have read the counts)
+    for (int j0 = min(n_still, x.budget - 1); j0 < x.budget; j0 += cs * 4 * THREADS) {
         const int r0 = j0 + rank * 4 * THREADS + tid;
         float v[4];
 #pragma unroll
@@ -424,26 +449,15 @@ __global__ void __launch_bounds__(THREADS, 2) evict_kernel(const Params p, const
     if (x.fused)
         clear_totals(p, x, b, kv, x.budget + rank * THREADS + tid, cs * THREADS, n);
 
-    // ---- rows of kept tokens below the budget, in rounds of cs * rows: kept[]
-    // ascends, so they are its first n_near entries (found 32 probes at a time)
-    int n_near = x.sink, span = x.budget - x.sink;    // the end lies in n_near .. n_near + span
-    while (span > 0) {
-        const int stride = (span + 31) / 32;
-        const int at = n_near + lane * stride;        // below the budget: the end is past it
-        const bool low = lane * stride < span && __ldcg(kept + at) < x.budget;
-        const int lows = __popc(__ballot_sync(0xffffffffu, low));
-        if (lows == 0)
-            break;
-        n_near += (lows - 1) * stride + 1;
-        span = min(stride - 1, x.budget - n_near);
-    }
+    // ---- rows of kept tokens below the budget that change their place, in rounds of
+    // cs * rows
     const int R = x.rows;
-    for (int j0 = x.sink; j0 < n_near; j0 += cs * R) {
+    for (int j0 = n_still; j0 < n_near; j0 += cs * R) {
         const int r0 = j0 + rank * R;
         const int nr = max(min(R, n_near - r0), 0);   // 0 for the last CTAs of the last round
         if (tid < nr) {
             const int j = r0 + tid, t = __ldcg(kept + j);
-            const long long s = t == j ? -1 : row_of(p, x, b, kv, t);
+            const long long s = row_of(p, x, b, kv, t);
             const long long d = s >= 0 ? row_of(p, x, b, kv, j) : -1;
             pl.src[tid] = d >= 0 ? s : -1;
             pl.dst[tid] = d;
