@@ -507,9 +507,13 @@ __global__ void __launch_bounds__(THREADS, 2) evict_kernel(const Params p, const
     }
     // ---- the others; their places may be sources of the rounds above, all read
     // before the last round's barrier
-    if (x.fused)
-        for (int r0 = n_near + rank * FAR_ROWS; r0 < x.budget; r0 += cs * FAR_ROWS)
-            move_far<4>(p, x, b, kv, kept, r0, min(FAR_ROWS, x.budget - r0), pl);
+    if (x.fused) {
+        // chunks as long as leave every CTA one: their places cost a chain of loads each
+        // (32 ragged sequences, 64 rows at a time: 154 us, 512: 123)
+        const int F = min(max((x.budget - n_near + cs - 1) / cs, FAR_ROWS), ROUND_ROWS);
+        for (int r0 = n_near + rank * F; r0 < x.budget; r0 += cs * F)
+            move_far<4>(p, x, b, kv, kept, r0, min(F, x.budget - r0), pl);
+    }
 }
 
 // The kernel's shared memory and cluster sizes, allowed once per device.
