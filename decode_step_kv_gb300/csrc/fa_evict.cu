@@ -11,10 +11,11 @@
 // or the clusters fill the GPU: then they go on with it themselves.
 //   Selection: a radix selection of the k-th largest total (11 + 11 + 10 bits
 //   of the order-preserving integer), each CTA counting its share of the
-//   tokens, the counts summed through distributed shared memory; then every
+//   tokens, the counts summed through distributed shared memory (one cluster
+//   barrier per pass); then every
 //   warp emits its tokens' kept indices at the rank that the warps before it
 //   leave.  Ties go to the lowest index.  A CTA keeps its share of the totals in
-//   shared memory when it fits (24576 tokens), so they are read once.
+//   shared memory when it fits (23424 tokens), so they are read once.
 //   Move: rows go down in place (a kept row's new index is never above its old
 //   one; those before the first dropped token stay).  A write to row j only clobbers a source when token j itself is kept,
 //   so order matters only among the kept tokens below the budget.  Those move
@@ -34,7 +35,10 @@ constexpr int BINS = 2048;
 constexpr int MAX_CTAS = 16;             // CTAs per cluster (8 are portable; fewer if they do not fit)
 // Totals, then rows in flight, of a CTA: two CTAs per SM, or one when there are few units.
 constexpr int STAGE_BYTES = 96 * 1024, STAGE_BYTES_1 = 200 * 1024;
-constexpr int HELD = STAGE_BYTES / 4;    // totals a CTA holds
+constexpr int GROUPS = 64, GROUP_BINS = BINS / GROUPS;   // bins are summed over a cluster in groups
+static_assert(GROUP_BINS == 32 && GROUPS == 64 && WARPS >= MAX_CTAS, "lanes and warps of the search");
+constexpr int SCRATCH = 2 * GROUPS + THREADS + 32 * WARPS;      // words of it
+constexpr int HELD = STAGE_BYTES / 4 - SCRATCH;                 // totals a CTA holds
 constexpr int ROUND_ROWS = THREADS;      // most rows a CTA stages per round
 constexpr double FUSED_BYTES = 4 << 20;  // rows to move up to which one kernel does it all
 
@@ -190,16 +194,29 @@ __device__ __forceinline__ void cp(uint32_t dst, const void *src)
         asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
 }
 
+// The sum of v over the lanes before this one.
+__device__ __forceinline__ unsigned warp_above(unsigned v)
+{
+    unsigned incl = v;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const unsigned y = __shfl_up_sync(0xffffffffu, incl, off);
+        if (static_cast<int>(threadIdx.x & 31) >= off)
+            incl += y;
+    }
+    return incl - v;
+}
+
 __global__ void __launch_bounds__(THREADS, 2) evict_kernel(const Params p, const Args x)
 {
-    __shared__ unsigned hist[BINS];
+    __shared__ __align__(16) unsigned hist[BINS];
     __shared__ unsigned cnt[WARPS][2];
     __shared__ unsigned wsum[WARPS];
     __shared__ unsigned found[2];
     __shared__ unsigned stay[2];             // this CTA's kept tokens: below the budget, at their places
-    __shared__ Places pl;
-    unsigned *part = reinterpret_cast<unsigned *>(pl.src);   // while selecting: this CTA's bin sums
-    static_assert(sizeof(Places) >= BINS / 2 * sizeof(unsigned), "a share of the bins");
+    __shared__ __align__(16) Places pl;
+    unsigned *hist2 = reinterpret_cast<unsigned *>(&pl);     // while selecting: every second pass's
+    static_assert(sizeof(Places) >= BINS * sizeof(unsigned), "a histogram");
     extern __shared__ __align__(128) unsigned char stage[];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
@@ -258,7 +275,7 @@ __global__ void __launch_bounds__(THREADS, 2) evict_kernel(const Params p, const
     const int c0 = x.sink + static_cast<int>((long long)m * (sr * WARPS) / nw);
     const int c1 = x.sink + static_cast<int>((long long)m * (sr * WARPS + WARPS) / nw);
     const bool held = c1 - c0 <= HELD;
-    unsigned *tot = reinterpret_cast<unsigned *>(stage);
+    unsigned *tot = reinterpret_cast<unsigned *>(stage);          // and the selection's scratch
     if (held) {
         constexpr int U = 16;
         for (int t0 = w0 + lane; t0 < w1; t0 += 32 * U) {
@@ -282,72 +299,88 @@ __global__ void __launch_bounds__(THREADS, 2) evict_kernel(const Params p, const
         for (int pass = 0; pass < 3; ++pass) {
             const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
             const int bits = pass == 2 ? 10 : 11;
+            unsigned *h = pass == 1 && sel > 1 ? hist2 : hist;
             for (int i = tid; i < BINS; i += THREADS)
-                hist[i] = 0;
+                h[i] = 0;
             __syncthreads();
 #pragma unroll 4
             for (int t = w0 + lane; t < w1; t += 32) {
                 const unsigned u = key_at(t);
                 if (pass == 0 || ((u ^ thr) >> (shift + bits)) == 0)
-                    atomicAdd(&hist[(u >> shift) & ((1u << bits) - 1)], 1u);
+                    atomicAdd(&h[(u >> shift) & ((1u << bits) - 1)], 1u);
             }
-            sync_sel();
+            __syncthreads();
             constexpr int PER = BINS / THREADS;
             if (sel > 1) {
-                // every CTA adds up its share of the bins over the cluster, then all read
-                // the sums (each reading all bins of all CTAs took 16 us per pass)
-                const int share = BINS / sel, tpb = max(THREADS / share, 1);
-                for (int i = tid / tpb; i < share; i += THREADS / tpb) {
-                    const uint32_t a = smem_u32(&hist[sr * share + i]);
-                    unsigned v = 0;
-                    for (int r0 = tid % tpb; r0 < sel; r0 += 4 * tpb) {
-                        unsigned y[4];
+                // One cluster barrier per pass: the sums of 64 groups of bins over the
+                // cluster, then of the 32 bins of the group that holds the k-th.  What a
+                // slower CTA still reads is written again only two passes later.
+                unsigned *gsum = tot + HELD + (pass & 1) * GROUPS;
+                unsigned *part = tot + HELD + 2 * GROUPS, *bins = part + THREADS;
+                const uint4 q = *reinterpret_cast<const uint4 *>(h + PER * tid);
+                unsigned v = q.x + q.y + q.z + q.w;
 #pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            y[q] = r0 + q * tpb < sel ? ld_cluster(tc::cl_map(a, r0 + q * tpb)) : 0u;
-                        v += y[0] + y[1] + y[2] + y[3];
+                for (int off = 1; off < GROUP_BINS / PER; off <<= 1)
+                    v += __shfl_xor_sync(0xffffffffu, v, off);
+                if (tid % (GROUP_BINS / PER) == 0)
+                    gsum[tid / (GROUP_BINS / PER)] = v;
+                tc::cluster_sync();
+                const uint32_t ga = smem_u32(gsum + tid % GROUPS);
+                v = 0;
+                for (int r = tid / GROUPS; r < sel; r += THREADS / GROUPS)
+                    v += ld_cluster(tc::cl_map(ga, r));
+                part[tid] = v;
+                __syncthreads();
+                // every warp: lane l has the groups 2l and 2l + 1 from the top
+                unsigned g0 = 0, g1 = 0;
+#pragma unroll
+                for (int r = 0; r < THREADS / GROUPS; ++r) {
+                    g0 += part[r * GROUPS + GROUPS - 1 - 2 * lane];
+                    g1 += part[r * GROUPS + GROUPS - 2 - 2 * lane];
+                }
+                unsigned above = warp_above(g0 + g1);
+                const bool in0 = above < rem && rem <= above + g0;
+                const bool in1 = above + g0 < rem && rem <= above + g0 + g1;
+                int src = __ffs(__ballot_sync(0xffffffffu, in0 || in1)) - 1;
+                const int group = __shfl_sync(0xffffffffu, GROUPS - 1 - 2 * lane - (in1 ? 1 : 0), src);
+                rem -= __shfl_sync(0xffffffffu, above + (in1 ? g0 : 0u), src);
+                // warp r fetches CTA r's bins; every warp: lane l has bin l from the top
+                if (warp < sel)
+                    bins[warp * 32 + lane] = ld_cluster(
+                        tc::cl_map(smem_u32(h + group * GROUP_BINS + lane), warp));
+                __syncthreads();
+                v = 0;
+                for (int r = 0; r < sel; ++r)
+                    v += bins[r * 32 + 31 - lane];
+                above = warp_above(v);
+                src = __ffs(__ballot_sync(0xffffffffu, above < rem && rem <= above + v)) - 1;
+                rem -= __shfl_sync(0xffffffffu, above, src);
+                thr |= static_cast<unsigned>(group * GROUP_BINS + 31 - src) << shift;
+            } else {
+                unsigned c[PER], sum = 0;         // this thread's bins, from the top
+#pragma unroll
+                for (int q = 0; q < PER; ++q) {
+                    c[q] = h[BINS - 1 - (tid * PER + q)];
+                    sum += c[q];
+                }
+                unsigned above = warp_above(sum);
+                if (lane == 31)
+                    wsum[warp] = above + sum;
+                __syncthreads();
+                for (int i = 0; i < warp; ++i)
+                    above += wsum[i];
+#pragma unroll
+                for (int q = 0; q < PER; ++q) {
+                    if (above < rem && rem <= above + c[q]) {
+                        found[0] = BINS - 1 - (tid * PER + q);
+                        found[1] = above;
                     }
-                    for (int off = tpb / 2; off >= 1; off >>= 1)
-                        v += __shfl_xor_sync(0xffffffffu, v, off);
-                    if (tid % tpb == 0)
-                        part[i] = v;
+                    above += c[q];
                 }
-                sync_sel();
+                __syncthreads();                  // the bins are read before they are cleared
+                thr |= found[0] << shift;
+                rem -= found[1];
             }
-            unsigned c[PER], sum = 0;             // this thread's bins, from the top
-#pragma unroll
-            for (int q = 0; q < PER; ++q) {
-                const int bin = BINS - 1 - (tid * PER + q), share = BINS / sel;
-                c[q] = sel > 1 ? ld_cluster(tc::cl_map(smem_u32(&part[bin % share]), bin / share))
-                               : hist[bin];
-            }
-#pragma unroll
-            for (int q = 0; q < PER; ++q)
-                sum += c[q];
-            unsigned incl = sum;
-#pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const unsigned y = __shfl_up_sync(0xffffffffu, incl, off);
-                if (lane >= off)
-                    incl += y;
-            }
-            if (lane == 31)
-                wsum[warp] = incl;
-            __syncthreads();
-            unsigned above = incl - sum;
-            for (int i = 0; i < warp; ++i)
-                above += wsum[i];
-#pragma unroll
-            for (int q = 0; q < PER; ++q) {
-                if (above < rem && rem <= above + c[q]) {
-                    found[0] = BINS - 1 - (tid * PER + q);
-                    found[1] = above;
-                }
-                above += c[q];
-            }
-            sync_sel();                           // counts read by all before they are cleared
-            thr |= found[0] << shift;
-            rem -= found[1];
         }
     }
     // ---- ranks: what the warps before this one keep

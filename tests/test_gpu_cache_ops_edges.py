@@ -161,6 +161,30 @@ def test_evict_of_everything_but_one_in_two_kernels(kind):
     ev.check_evict(kind, lay, 256, [40011, 20001], 20000, 4, 100, ev.totals(lay, 5, "odd"))
 
 
+@pytest.mark.parametrize("how", ["heavy", "ties", "odd"])
+@pytest.mark.parametrize("n,budget", [(50000, 9000), (26000, 3000), (24001, 1300), (30001, 500)])
+def test_evict_selects_from_more_tokens_than_a_cta_holds(n, budget, how):
+    """Selection by clusters of 16, 8, 2 and 1 CTAs."""
+    lay = Layout(1, 3, n, True, 64, seed=1)
+    ev.check_evict("int4", lay, 128, [n], budget, 5, 60, ev.totals(lay, n, how))
+
+
+def test_evict_again_after_more_steps():
+    """Most kept tokens at their places already: an eviction of what an eviction left and new tokens."""
+    lay = Layout(2, 2, 1504, True, seed=8)
+    r = np.random.RandomState(4)
+    acc = np.zeros(lay.rows, dtype=np.float32)
+    for b in range(2):
+        a = np.concatenate([r.random_sample((2, 1000)) + 1, r.random_sample((2, 504))], axis=1)
+        a[:, 700 + 100 * b] = 0                             # the first dropped token
+        lay.put(acc, b, a.astype(np.float32))
+    ev.check_evict("int8v", lay, 128, [1500, 1100], 1000, 4, 50, acc)
+    ev.check_evict("fp16", lay, 128, [1500, 1100], 1000, 0, 0, acc)
+    for b in range(2):
+        lay.put(acc, b, np.broadcast_to(-np.arange(1504, dtype=np.float32), (2, 1504)))
+    ev.check_evict("fp16", lay, 128, [1500, 1001], 1000, 0, 0, acc)      # the first 1000 stay
+
+
 def test_evict_contiguous_cache_of_odd_capacity():
     lay = Layout(3, 3, 307, False, seed=1)
     ev.check_evict("int8v", lay, 128, [307, 33, 301], 32, 3, 5, ev.totals(lay, 5))
