@@ -106,8 +106,8 @@ __device__ __forceinline__ void row_place(const Params &p, const RowArgs &a, uns
 // 1.5 * 2^23 + 8 added, the sum's low four bits are the nibble of the rounded
 // x / s; where x - c*s does not confirm it (a tie, a quotient next to one, a NaN,
 // a scale rounded so far down that codes are cut off) the thread takes the exact
-// form.  (One word per thread and a division per scale: 274 instructions per 8
-// elements and 38 us for 2 x 16384 rows of 8 heads x 128, against 23 for the bytes.)
+// form.  2 x 16384 rows of 8 heads x 128: 33 us, 23 for the bytes, with the ALU busy
+// 56% of the time.  (One word per thread and a division per scale: 38 us.)
 template <int D>
 __global__ void __launch_bounds__(256) append_kernel(const Params p, const RowArgs a,
                                                      const float *k_new, const float *v_new,
@@ -171,8 +171,9 @@ __global__ void __launch_bounds__(256) append_kernel(const Params p, const RowAr
         (isv ? v_scales : k_scales)[row * NJ + j] = sh;
 }
 
-// The inverse: rows back as fp16 values c * s (each product rounded once).  A
-// token outside the cache or in an unmapped block reads as zeros; rows behind the
+// The inverse: rows back as fp16 values c * s (each product rounded once).  Bound by
+// the latency of its two short reads per thread: 16384 rows of 8 heads x 128 in 20
+// us, 13 for the bytes.  A token outside the cache or in an unmapped block reads as zeros; rows behind the
 // count are left as they were.
 template <int D>
 __global__ void __launch_bounds__(256) gather_kernel(const Params p, const RowArgs a,
