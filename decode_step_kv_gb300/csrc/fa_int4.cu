@@ -407,7 +407,10 @@ struct Feed {
 
 // NG: groups of 8 columns per warp.  With two, a tile is unpacked once for 16
 // columns (speculative verify).
-template <int D, int NG, bool WT>
+// CL, the plan of small steps: one thread-block cluster of p.cl_ctas CTAs per unit,
+// its warps sharing the unit's tiles evenly and folding their partials through
+// distributed shared memory, which saves the merge kernel.
+template <int D, int NG, bool WT, bool CL>
 __global__ void __launch_bounds__(Cfg<D, NG>::NW * 32, Cfg<D, NG>::CTAS_PER_SM)
     decode_kernel(const Params p)
 {
@@ -422,7 +425,10 @@ __global__ void __launch_bounds__(Cfg<D, NG>::NW * 32, Cfg<D, NG>::CTAS_PER_SM)
     const int w = blockIdx.x * C::NW + warp;
     int b_at = -1, We = 0;
     long long P_at = 0, T = 0, t0 = 0, t1 = 0;
-    if (!tc::stream_range(p, w, T, We, t0, t1, b_at, P_at))
+    uint32_t rank = 0;               // in the cluster
+    if constexpr (CL)
+        asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+    else if (!tc::stream_range(p, w, T, We, t0, t1, b_at, P_at))
         return;
 
     extern __shared__ __align__(128) unsigned char smem[];
@@ -430,10 +436,22 @@ __global__ void __launch_bounds__(Cfg<D, NG>::NW * 32, Cfg<D, NG>::CTAS_PER_SM)
     const uint64_t policy = evict_first_policy();
 
     tc::Walk pw;
-    pw.init(p, b_at, P_at, t0, tc::UNIT_COST);
-    tc::Walk cw = pw;
     int n_my = 0;                    // tiles in [t0, t1)
-    {
+    if constexpr (CL) {
+        const int unit = blockIdx.x / p.cl_ctas, R = p.cl_ctas * C::NW, r = rank * C::NW + warp;
+        pw.b = unit / p.U_b;
+        pw.j = unit % p.U_b;
+        pw.c = 0;
+        pw.P = 0;
+        attended_range(p, pw.b, pw.lo, pw.hi, pw.j == 0 && r == 0);
+        pw.n = tiles_in<TILE>(pw.lo, pw.hi);
+        pw.k = static_cast<int>((long long)pw.n * r / R);
+        n_my = static_cast<int>((long long)pw.n * (r + 1) / R) - pw.k;
+    } else {
+        pw.init(p, b_at, P_at, t0, tc::UNIT_COST);
+    }
+    tc::Walk cw = pw;
+    if constexpr (!CL) {
         tc::Walk e = pw;
         while (e.pos() < t1) {
             const long long us = e.unit_start();
@@ -842,6 +860,8 @@ __global__ void __launch_bounds__(Cfg<D, NG>::NW * 32, Cfg<D, NG>::CTAS_PER_SM)
 
         i += nb;
         cw.k += nb;
+        if constexpr (CL)
+            continue;                // one segment, folded below
         if (cw.k == cw.n || i == n_my) {
             // ---- end of this worker's segment of the unit
             const long long us = cw.unit_start();
@@ -895,6 +915,66 @@ __global__ void __launch_bounds__(Cfg<D, NG>::NW * 32, Cfg<D, NG>::CTAS_PER_SM)
         }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
+    if constexpr (CL) {
+        // ---- the unit's partials: of every warp (m, l) of 8 columns, then O [8][D], in
+        // its ring; folded by all threads of the cluster, 32 elements of a column per warp
+        __syncwarp();
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            float lx = l[0][x];
+#pragma unroll
+            for (int mask = 4; mask <= 16; mask <<= 1)
+                lx += __shfl_xor_sync(0xffffffffu, lx, mask);
+            const int h = 2 * t + x;
+            const uint32_t o = ring + 64 + (h * D + 4 * g) * 4;
+            const float up = pow2(e + 20), up16 = up * 16.f;
+            if (g == 0) {
+                sts32(ring + h * 8, __float_as_uint(mr[0][x] == NO_MAX ? -INFINITY : mr[0][x]));
+                sts32(ring + h * 8 + 4, __float_as_uint(lx));
+            }
+#pragma unroll
+            for (int j = 0; j < NJ; ++j)
+                sts128(o + j * 128, __float_as_uint(acc[0][2 * j][x] * up16),
+                       __float_as_uint(acc[0][2 * j][x + 2] * up),
+                       __float_as_uint(acc[0][2 * j + 1][x] * up16),
+                       __float_as_uint(acc[0][2 * j + 1][x + 2] * up));
+        }
+        tc::cluster_sync();
+        const int R = p.cl_ctas * C::NW, kv = pw.j / p.n_hg, cg = pw.j % p.n_hg;
+        const int live = min(GPH, tq * p.G - cg * GPH);
+        const uint32_t rings = smem_u32(smem);
+        for (int i = rank * C::NW + warp; i < live * (D / 32); i += R) {
+            const int h = i / (D / 32), d = i % (D / 32) * 32 + lane;
+            // lane r has warp r's (m, l)
+            const uint32_t mine = tc::cl_map(rings + lane % C::NW * (S * C::STAGE_BYTES), lane / C::NW);
+            const float2 ml = lane < R ? tc::cl_ld2(mine + h * 8) : make_float2(-INFINITY, 0.f);
+            float M = ml.x;
+#pragma unroll
+            for (int mask = 16; mask >= 1; mask >>= 1)
+                M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, mask));
+            const float a = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
+            float L = a * ml.y;
+#pragma unroll
+            for (int mask = 16; mask >= 1; mask >>= 1)
+                L += __shfl_xor_sync(0xffffffffu, L, mask);
+            float sum = 0.f;
+#pragma unroll 8
+            for (int r = 0; r < R; ++r) {
+                const uint32_t at = tc::cl_map(rings + r % C::NW * (S * C::STAGE_BYTES), r / C::NW);
+                float y;
+                asm volatile("ld.shared::cluster.f32 %0, [%1];"
+                             : "=f"(y)
+                             : "r"(at + 64 + (h * D + d) * 4)
+                             : "memory");
+                const float ar = __shfl_sync(0xffffffffu, a, r);
+                sum = ar > 0.f ? fmaf(y, ar, sum) : sum;
+            }
+            const tc::Col cc = tc::column(p, kv, cg, h, GPH);
+            reinterpret_cast<__half *>(p.out)[(((long long)pw.b * tq + cc.j) * p.Hq + cc.h) * D + d] =
+                __float2half_rn(L == 0.f ? 0.f : sum / L);
+        }
+        tc::cluster_sync();          // no CTA leaves while its partials are read
+    }
 }
 
 // ------------------------------------------------- attention, many columns
@@ -1380,7 +1460,22 @@ constexpr int WIDE_GROUPS = 6;
 // scores outweigh it (24 columns, 32768 keys: 324 us against 253).
 constexpr double TWO_GROUP_MIN_TILES = 20.0;
 
+// The plan of small steps: a cluster of up to 8 CTAs per unit while every cluster is
+// resident at once and a warp has at most so many tiles (at full capacity).  us with
+// clusters against the split and merge, 4 query heads per KV head:
+//                          1 x 2 heads       1 x 8        4 x 8        8 x 8
+//   D = 128,  512 keys     7.0 /  8.0     7.6 /  8.4   7.2 /  9.5   8.0 / 10.9
+//            2048          7.4 / 10.9     8.0 / 11.7   9.3 / 12.3  12.1 / 14.2
+//            8192         11.9 / 18.3    12.1 / 15.4  17.5 / 18.9  28.5 / 25.1
+//   D = 256, 2048          9.7 / 12.5    10.1 / 14.0  13.2 / 14.4  18.5 / 19.1
+//            8192         16.4 / 22.6    16.6 / 17.5  26.5 / 24.4  44.5 / 36.9
+// Equal lengths; the split also balances ragged ones, so the limit is half of where
+// it breaks even.
+constexpr int CL_MAX_CTAS = 8;
+constexpr int CL_MAX_TILES_128 = 16, CL_MAX_TILES_256 = 8;      // per warp
+
 struct Plan {
+    int cl_ctas;                 // the plan of small steps: CTAs per cluster; else 0
     int ctas, W, n_hg, units, sh, cpu;
     size_t bytes;                // partial slots and prefix
 };
@@ -1417,6 +1512,12 @@ static Plan make_plan(int B, int tq, int Hq, int Hkv, int D, long long cap, int 
     if (pl.ctas == 0)
         pl.ctas = 1;
     pl.W = pl.ctas * nw;
+    const long long units = (long long)B * pl.units, tiles = (cap + TILE - 1) / TILE;
+    const int most_tiles = D == 128 ? CL_MAX_TILES_128 : CL_MAX_TILES_256;
+    if (pl.cpu == GPH && !weights)
+        for (int c = CL_MAX_CTAS; c >= 2 && !pl.cl_ctas; c /= 2)
+            if (units * c <= sms && tiles <= (long long)most_tiles * c * nw)
+                pl.cl_ctas = c;
     const size_t slots = (size_t)pl.W + (size_t)B * pl.units;
     pl.bytes = slots * pl.sh * (D * sizeof(float) + sizeof(float2)) +
                (size_t)(B + 1) * sizeof(long long);
@@ -1433,7 +1534,7 @@ static bool sizes_ok(int batch, int tq, int Hq, int Hkv, int D)
 // device).
 template <typename K>
 static cudaError_t launch_split(K kernel, bool (&done)[64], const Params &p, int ctas, int threads,
-                                int smem, cudaStream_t st)
+                                int smem, cudaStream_t st, int cluster = 1)
 {
     static std::mutex mu;
     int dev = 0;
@@ -1450,23 +1551,44 @@ static cudaError_t launch_split(K kernel, bool (&done)[64], const Params &p, int
                 done[dev] = true;
         }
     }
-    kernel<<<ctas, threads, smem, st>>>(p);
-    return cudaGetLastError();
+    if (cluster == 1) {
+        kernel<<<ctas, threads, smem, st>>>(p);
+        return cudaGetLastError();
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = cluster;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, kernel, p);
+    return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
 template <int D, bool WT>
 static cudaError_t launch(const Params &p, int ctas, int sms, cudaStream_t st)
 {
-    static bool done[3][64] = {};
+    static bool done[4][64] = {};
     cudaError_t e;
     if (p.cpu == 64) {
         e = launch_split(wide_kernel<D, WT>, done[0], p, ctas, 128, WideCfg<D>::SMEM, st);
+    } else if (p.cl_ctas) {              // the plan gives clusters without weights
+        using C = Cfg<D, 1>;
+        return launch_split(decode_kernel<D, 1, false, true>, done[3], p, p.B * p.U_b * p.cl_ctas,
+                            C::NW * 32, C::SMEM, st, p.cl_ctas);
     } else if (p.cpu == GPH) {
         using C = Cfg<D, 1>;
-        e = launch_split(decode_kernel<D, 1, WT>, done[1], p, ctas, C::NW * 32, C::SMEM, st);
+        e = launch_split(decode_kernel<D, 1, WT, false>, done[1], p, ctas, C::NW * 32, C::SMEM, st);
     } else {
         using C = Cfg<128, 2>;       // the plan gives 16 columns at D = 128, without weights
-        e = launch_split(decode_kernel<128, 2, false>, done[2], p, ctas, C::NW * 32, C::SMEM, st);
+        e = launch_split(decode_kernel<128, 2, false, false>, done[2], p, ctas, C::NW * 32, C::SMEM,
+                         st);
     }
     return e == cudaSuccess ? launch_merge_half<D>(p, sms, st) : e;
 }
@@ -1779,6 +1901,7 @@ FA_API int fa_decode_int4(const void *q, const void *k_codes, const void *k_scal
     p.U_b = pl.units;
     p.sh = pl.sh;
     p.cpu = pl.cpu;
+    p.cl_ctas = pl.cl_ctas;
     if (acc) {
         p.acc = acc;
         p.lse = reinterpret_cast<float *>(static_cast<char *>(workspace) + wsp.lse);

@@ -298,6 +298,44 @@ def test_peaked_scores():
     check(lay, cache, queries(1, 1, 4, 128, 2, mag=6.0), lens, 4, 0.5)
 
 
+@pytest.mark.parametrize("D", [128, 256])
+@pytest.mark.parametrize("B,Hkv", [(1, 1), (3, 6), (19, 1), (37, 2), (38, 2), (39, 2)])
+@pytest.mark.parametrize("G,tq,windowed", [(1, 1, False), (4, 1, True), (3, 3, True)])
+def test_small_steps(D, B, Hkv, G, tq, windowed):
+    """Clusters of 8, 4 and 2 CTAs per unit, and the first step too large for them; column groups."""
+    lens = [(97 * b) % 130 if b else 128 for b in range(B)]
+    lay = Layout(B, Hkv, 128, B % 2 == 1, 32, seed=B)
+    window = [(b % 4) * 25 for b in range(B)] if windowed else None
+    check(lay, Int4Cache(lay, D, lens, seed=G), queries(B, tq, G * Hkv, D, 1), lens, G * Hkv, D ** -0.5,
+          window, weights=False)
+
+
+@pytest.mark.parametrize("D,cap", [(128, 8192), (128, 8208), (256, 4096), (256, 4112)])
+def test_cluster_and_split_plan_border(D, cap):
+    lens = [cap, 1, cap - 1500]
+    lay = Layout(3, 2, cap, True)
+    check(lay, Int4Cache(lay, D, lens, seed=1), queries(3, 1, 8, D, 4), lens, 8, D ** -0.5, weights=False)
+
+
+def test_small_step_in_a_graph():
+    lens = [200, 0, 77]
+    lay = Layout(3, 2, 208, False, seed=3)
+    cache = Int4Cache(lay, 256, [208] * 3, seed=3)
+    q = queries(3, 2, 8, 256, 3)
+    dev, qd, ln, out = cache.gpu(), cuda(q), lens_gpu(lens), torch.empty((3, 2, 8, 256), dtype=torch.float16,
+                                                                         device="cuda")
+    ws = fa.alloc_workspace_int4(3, 2, 8, 2, 256, lay.cap)
+    want = {n: run(lay, cache, q, [n, 0, 77], 8, 0.1) for n in (200, 3, 208)}
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        fa.fa_decode_int4(qd, *dev, None, ln, 8, 2, 256, 0.1, None, out, workspace=ws)
+    for n in (200, 3, 208):
+        ln.copy_(lens_gpu([n, 0, 77]))
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[n]) and torch.all(out[1] == 0)
+
+
 @pytest.mark.parametrize("B", [33, 140, 300])
 def test_many_sequences(B):
     lens = [(37 * b) % 70 for b in range(B)]
@@ -324,9 +362,11 @@ def test_bad_blocks_and_lengths_are_flagged(tq):
     assert torch.equal(good[0], over[0]) and torch.all(over[1] == 0)
     lay.table[1, 2] = -1                            # tokens 32..47 of sequence 1 are unmapped
     acc = torch.zeros(lay.rows, device="cuda")
-    got = run(lay, cache, q, [64, 64], 4, 0.1, acc=acc)
+    got = run(lay, cache, q, [64, 64], 4, 0.1)
     assert fa.fa_decode_device_status() == fa.FA_STATUS_BAD_BLOCK
     assert torch.equal(got[0], good[0])
+    run(lay, cache, q, [64, 64], 4, 0.1, acc=acc)        # another plan may serve it
+    assert fa.fa_decode_device_status() == fa.FA_STATUS_BAD_BLOCK
     if tq == 1:
         keep = np.r_[0:32, 48:64]
         kb, vb = cache.key(1)[:, keep], cache.value(1)[:, keep]
@@ -342,13 +382,15 @@ def test_stream_graph_and_new_lengths():
     lay = Layout(2, 2, 208, True, seed=3)
     cache = Int4Cache(lay, 128, [208, 208], seed=3)
     q = queries(2, 1, 8, 128, 3)
-    want = {n: run(lay, cache, q, [n, 77], 8, 0.1) for n in (200, 5, 208)}
+    alone = run(lay, cache, q, lens, 8, 0.1)
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
     with torch.cuda.stream(side):
         got = run(lay, cache, q, lens, 8, 0.1)
     side.synchronize()
-    assert torch.equal(got, want[200])
+    assert torch.equal(got, alone)
+    want = {n: run(lay, cache, q, [n, 77], 8, 0.1, acc=torch.zeros(lay.rows, device="cuda"))
+            for n in (200, 5, 208)}
     dev = cache.gpu()
     qd, table, ln = cuda(q), lay.table_gpu(), lens_gpu(lens)
     out = torch.empty_like(qd)
