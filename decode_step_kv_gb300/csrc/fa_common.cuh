@@ -1039,6 +1039,19 @@ constexpr int WEIGHT_KPT = 4;                              // keys per thread
 constexpr int WEIGHT_KEYS = WEIGHT_THREADS * WEIGHT_KPT;   // keys per round
 constexpr int WEIGHT_COLS = 512;                           // columns at a time
 
+// Cache row of token t of (b, kv); -1 for a block id out of range (caches here have
+// fewer than 2^31 rows).
+__device__ __forceinline__ int weight_row(const Params &p, int b, int kv, int t)
+{
+    if (!p.bt)
+        return (b * p.Hkv + kv) * static_cast<int>(p.cap) + t;
+    const int page = p.lg_page >= 0 ? t >> p.lg_page : t / p.page_size;
+    const int blk = p.bt[(long long)b * p.max_blocks + page];
+    if (blk < 0 || blk >= p.num_blocks)
+        return -1;
+    return (blk * p.Hkv + kv) * p.page_size + (t - page * p.page_size);
+}
+
 __device__ __forceinline__ void add_weights(const Params &p, const int cta, const int ctas)
 {
     __shared__ __align__(16) float lse[WEIGHT_COLS];
@@ -1050,17 +1063,6 @@ __device__ __forceinline__ void add_weights(const Params &p, const int cta, cons
     bool waited = false;
     long long T = 0, P = 0;
     int have_b = -1, n = 0;
-    // cache row of token t of (b, kv); -1 for a block id out of range (caches here
-    // have fewer than 2^31 rows)
-    auto row_at = [&](int b, int kv, int t) -> int {
-        if (!p.bt)
-            return (b * p.Hkv + kv) * static_cast<int>(p.cap) + t;
-        const int page = p.lg_page >= 0 ? t >> p.lg_page : t / p.page_size;
-        const int blk = p.bt[(long long)b * p.max_blocks + page];
-        if (blk < 0 || blk >= p.num_blocks)
-            return -1;
-        return (blk * p.Hkv + kv) * p.page_size + (t - page * p.page_size);
-    };
     for (long long it = cta; it < items; it += ctas) {
         const int u = static_cast<int>(it / chunks);       // (b, kv)
         const int b = u / p.Hkv, kv = u - b * p.Hkv;
@@ -1131,7 +1133,7 @@ __device__ __forceinline__ void add_weights(const Params &p, const int cta, cons
 #pragma unroll
                 for (int q = 0; q < WEIGHT_KPT; ++q) {
                     const int t = tr + q * WEIGHT_THREADS;
-                    row[q] = t >= lo && t < end ? row_at(b, kv, t) : -1;
+                    row[q] = t >= lo && t < end ? weight_row(p, b, kv, t) : -1;
                 }
                 if (p.cpu > 2 * GPH) {
                     // key t's scores lie 16 floats from column to column, keys side by side
@@ -1189,6 +1191,53 @@ __device__ __forceinline__ void add_weights(const Params &p, const int cta, cons
     }
     if (!waited)
         asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// The same in the cluster plan, whose warps have their own keys' scores at hand (`unit`:
+// the scores of the unit's row of columns; tokens t0 .. t1 - 1 are this warp's) and the
+// partials (m, l) of every warp r and column c: ml(r, c).
+template <typename Ml>
+__device__ __forceinline__ void add_cluster_weights(const Params &p, int b, int kv, int t0, int t1,
+                                                    int nh, const float *unit, int R, Ml ml)
+{
+    const int lane = threadIdx.x & 31;
+    float lse[GPH];
+#pragma unroll
+    for (int c = 0; c < GPH; ++c) {
+        lse[c] = INFINITY;
+        if (c >= nh)
+            continue;
+        float M = -INFINITY, L = 0.f;
+        for (int r = lane; r < R; r += 32) {
+            const float2 y = ml(r, c);
+            if (y.x == -INFINITY)
+                continue;
+            const float m = fmaxf(M, y.x);
+            L = L * ex2(M - m) + y.y * ex2(y.x - m);
+            M = m;
+        }
+        float Mw = M;
+#pragma unroll
+        for (int off = 16; off >= 1; off >>= 1)
+            Mw = fmaxf(Mw, __shfl_xor_sync(0xffffffffu, Mw, off));
+        L = M == -INFINITY ? 0.f : L * ex2(M - Mw);
+#pragma unroll
+        for (int off = 16; off >= 1; off >>= 1)
+            L += __shfl_xor_sync(0xffffffffu, L, off);
+        if (L > 0.f)
+            lse[c] = Mw + log2f(L);
+    }
+    for (int t = t0 + lane; t < t1; t += 32) {
+        const int row = weight_row(p, b, kv, t);
+        if (row < 0)
+            continue;
+        float sum = 0.f;
+#pragma unroll
+        for (int c = 0; c < GPH; ++c)
+            if (c < nh)
+                sum += ex2_ftz(unit[(long long)t * p.sh + c] - lse[c]);
+        atomicAdd(p.acc + row, sum);
+    }
 }
 
 // The merge (fp16 output) and the recorded weights in one launch: the first
@@ -1326,7 +1375,6 @@ static cudaError_t launch_merge_half(const Params &p0, int sms, cudaStream_t st)
         p.w_rounds = p.cpu > 2 * tc::GPH ? 1 : 8;
         while (p.w_rounds > 1 && (rounds + p.w_rounds - 1) / p.w_rounds * units < 2ll * sms)
             p.w_rounds /= 2;
-        p.lg_page = p.bt ? log2_of(p.page_size) : -1;
         const long long items = (rounds + p.w_rounds - 1) / p.w_rounds * units;
         ctas += items < most ? items : most;
     }

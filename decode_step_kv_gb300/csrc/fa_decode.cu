@@ -600,8 +600,8 @@ struct Smem {
 // runs.
 constexpr int CL_MAX_CTAS = 8;  // the portable maximum cluster size
 // WT: recorded weights -- the tile's scores go to the workspace for
-// add_weights, whole units also write their log-sum-exp, and the output
-// is fp16.
+// add_weights (in the cluster plan each warp adds its own keys' after the fold),
+// whole units also write their log-sum-exp, and the output is fp16.
 template <int D, bool VI8, bool BI, int NG, bool CL = false, bool WT = false>
 __global__ void __launch_bounds__(Cfg<D, VI8, NG>::NW * 32, Cfg<D, VI8, NG>::CTAS_PER_SM)
     fa_stream_mma_kernel(const Params p, const __grid_constant__ CUtensorMap tmK,
@@ -1304,12 +1304,29 @@ __global__ void __launch_bounds__(Cfg<D, VI8, NG>::NW * 32, Cfg<D, VI8, NG>::CTA
                 fold(i0, std::integral_constant<int, 4>());
             const float inv = Lsum > 0.f ? 1.f / Lsum : 0.f;
             const Col cq = column(p, cl_j / p.n_hg, cl_j % p.n_hg, c, CPU);
-            float4 *dst = reinterpret_cast<float4 *>(
-                p.out + (((long long)b_at * tq + cq.j) * p.Hq + cq.h) * D + lane * EPL2);
+            using OutT = typename std::conditional<WT, __half, float>::type;
+            OutT *dst = reinterpret_cast<OutT *>(p.out) +
+                        (((long long)b_at * tq + cq.j) * p.Hq + cq.h) * D + lane * EPL2;
 #pragma unroll
             for (int e = 0; e < EPL2; e += 4)
-                dst[e / 4] = make_float4(o[e] * inv, o[e + 1] * inv, o[e + 2] * inv,
-                                         o[e + 3] * inv);
+                store4(dst + e, make_float4(o[e] * inv, o[e + 1] * inv, o[e + 2] * inv,
+                                            o[e + 3] * inv));
+        }
+        if constexpr (WT) {
+            // the plan gives one column group per KV head
+            if (n_my > 0 && i_fail < 0) {
+                int lo, hi;
+                attended_range(p, b_at, lo, hi, false);
+                const int first = lo / TILE + static_cast<int>(t0);
+                add_cluster_weights(p, b_at, cl_j, max(lo, first * TILE),
+                                    min(hi, (first + n_my) * TILE), nh,
+                                    p.ws_s + ((long long)b_at * p.U_b + cl_j) * p.cap16 * p.sh, R,
+                                    [&](int r, int c) {
+                                        return cl_ld2(cl_map(base + (r % C::NW) * C::WARP_BYTES +
+                                                                 (CPU * D + 2 * c) * 4,
+                                                             r / C::NW));
+                                    });
+            }
         }
         // no CTA leaves while another may still read its shared memory
         __syncwarp();
@@ -1802,7 +1819,7 @@ static cudaError_t launch_mma(const Params &p, const CUtensorMap &tmK, const CUt
 // Clusters of `cs` CTAs of the cluster-plan kernel that fit on the current
 // device at once (cudaOccupancyMaxActiveClusters; 0 if the query fails),
 // cached per device and cluster size.
-template <int D, bool VI8>
+template <int D, bool VI8, bool WT = false>
 static int cluster_capacity(int cs)
 {
     static std::mutex mu;
@@ -1817,7 +1834,7 @@ static int cluster_capacity(int cs)
         return cache[dev][ci];
     const int smem = tc::Smem<D, VI8, 1>::BYTES;
     int n = 0;
-    if (cudaFuncSetAttribute(tc::fa_stream_mma_kernel<D, VI8, false, 1, true>,
+    if (cudaFuncSetAttribute(tc::fa_stream_mma_kernel<D, VI8, false, 1, true, WT>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, smem) == cudaSuccess) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(cs * 64);
@@ -1830,7 +1847,7 @@ static int cluster_capacity(int cs)
         attr[0].val.clusterDim.z = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        if (cudaOccupancyMaxActiveClusters(&n, tc::fa_stream_mma_kernel<D, VI8, false, 1, true>,
+        if (cudaOccupancyMaxActiveClusters(&n, tc::fa_stream_mma_kernel<D, VI8, false, 1, true, WT>,
                                            &cfg) != cudaSuccess) {
             n = 0;
             cudaGetLastError();   // clear the error this refused query left (and only then)
@@ -1845,7 +1862,7 @@ static int cluster_capacity(int cs)
     return n;
 }
 
-template <int D, bool VI8>
+template <int D, bool VI8, bool WT = false>
 static cudaError_t launch_cluster(const Params &p, const CUtensorMap &tmK, const CUtensorMap &tmV,
                                   int units, cudaStream_t st)
 {
@@ -1861,7 +1878,7 @@ static cudaError_t launch_cluster(const Params &p, const CUtensorMap &tmK, const
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, tc::fa_stream_mma_kernel<D, VI8, false, 1, true>, p,
+    cudaError_t e = cudaLaunchKernelEx(&cfg, tc::fa_stream_mma_kernel<D, VI8, false, 1, true, WT>, p,
                                        tmK, tmV);
     return e == cudaSuccess ? cudaGetLastError() : e;
 }
@@ -2348,6 +2365,7 @@ static int decode_impl(const void *q, const void *k_cache, const void *v_cache,
         p.lse = reinterpret_cast<float *>(static_cast<char *>(workspace) + wsp.lse);
         p.ws_s = reinterpret_cast<float *>(static_cast<char *>(workspace) + wsp.scores);
         p.cap16 = (cap + 15) / 16 * 16;
+        p.lg_page = paged ? log2_of(page_size) : -1;
     }
 
     cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -2359,7 +2377,8 @@ static int decode_impl(const void *q, const void *k_cache, const void *v_cache,
     // unit's cluster fits on the GPU at once and a warp gets at most
     // FA_CL_MAX_TPW_<head_dim> tiles (FA_DECODE_PLAN=streamk turns it off).
     int cluster_ctas = 0;
-    if (pl.path == Path::Mma && pl.chunk == 0 && pl.cpu == tc::GPH && !acc) {
+    if (pl.path == Path::Mma && pl.chunk == 0 && pl.cpu == tc::GPH &&
+        !(acc && pl.n_hg > 1)) {         // one addition per key and call
         const char *pe = getenv("FA_DECODE_PLAN");
         const long long units_all = (long long)batch * pl.units;
         const long long unit_tiles = ((ring ? cap + 16 : cap) + tc::TILE - 1) / tc::TILE;
@@ -2369,10 +2388,15 @@ static int decode_impl(const void *q, const void *k_cache, const void *v_cache,
         for (int cs = tc::CL_MAX_CTAS; cs >= 1 && !(pe && !strcmp(pe, "streamk")); cs /= 2) {
             if ((unit_tiles + (long long)cs * nw - 1) / ((long long)cs * nw) > max_tpw)
                 break;                       // smaller clusters give each warp more
-            const int fit = D == 128 ? (vi8 ? cluster_capacity<128, true>(cs)
-                                            : cluster_capacity<128, false>(cs))
-                                     : (vi8 ? cluster_capacity<256, true>(cs)
-                                            : cluster_capacity<256, false>(cs));
+            const int fit =
+                acc ? (D == 128 ? (vi8 ? cluster_capacity<128, true, true>(cs)
+                                       : cluster_capacity<128, false, true>(cs))
+                                : (vi8 ? cluster_capacity<256, true, true>(cs)
+                                       : cluster_capacity<256, false, true>(cs)))
+                    : (D == 128 ? (vi8 ? cluster_capacity<128, true>(cs)
+                                       : cluster_capacity<128, false>(cs))
+                                : (vi8 ? cluster_capacity<256, true>(cs)
+                                       : cluster_capacity<256, false>(cs)));
             if (units_all <= fit) {
                 cluster_ctas = cs;
                 break;
@@ -2399,10 +2423,16 @@ static int decode_impl(const void *q, const void *k_cache, const void *v_cache,
             else if (const int rv = encode_kv_map(&tmV, v_cache, kv_rows_total, D))
                 return rv;
             const int units_all = batch * pl.units;
-            e = D == 128 ? (vi8 ? launch_cluster<128, true>(p, tmK, tmV, units_all, st)
-                                : launch_cluster<128, false>(p, tmK, tmV, units_all, st))
-                         : (vi8 ? launch_cluster<256, true>(p, tmK, tmV, units_all, st)
-                                : launch_cluster<256, false>(p, tmK, tmV, units_all, st));
+            if (acc)
+                e = D == 128 ? (vi8 ? launch_cluster<128, true, true>(p, tmK, tmV, units_all, st)
+                                    : launch_cluster<128, false, true>(p, tmK, tmV, units_all, st))
+                             : (vi8 ? launch_cluster<256, true, true>(p, tmK, tmV, units_all, st)
+                                    : launch_cluster<256, false, true>(p, tmK, tmV, units_all, st));
+            else
+                e = D == 128 ? (vi8 ? launch_cluster<128, true>(p, tmK, tmV, units_all, st)
+                                    : launch_cluster<128, false>(p, tmK, tmV, units_all, st))
+                             : (vi8 ? launch_cluster<256, true>(p, tmK, tmV, units_all, st)
+                                    : launch_cluster<256, false>(p, tmK, tmV, units_all, st));
             if (e != cudaSuccess)
                 return fail(FA_ERR_CUDA, "fa_decode: cluster launch failed: %s",
                             cudaGetErrorString(e));

@@ -973,6 +973,16 @@ __global__ void __launch_bounds__(Cfg<D, NG>::NW * 32, Cfg<D, NG>::CTAS_PER_SM)
             reinterpret_cast<__half *>(p.out)[(((long long)pw.b * tq + cc.j) * p.Hq + cc.h) * D + d] =
                 __float2half_rn(L == 0.f ? 0.f : sum / L);
         }
+        if constexpr (WT)            // the plan gives one column group per KV head
+            if (n_my > 0) {
+                const int first = pw.lo / TILE + static_cast<int>((long long)pw.n * (rank * C::NW + warp) / R);
+                tc::add_cluster_weights(
+                    p, pw.b, pw.j, max(pw.lo, first * TILE), min(pw.hi, (first + n_my) * TILE), live,
+                    p.ws_s + cw.unit(p) * p.cap16 * p.sh, R, [&](int r, int c) {
+                        return tc::cl_ld2(tc::cl_map(rings + r % C::NW * (S * C::STAGE_BYTES),
+                                                     r / C::NW) + c * 8);
+                    });
+            }
         tc::cluster_sync();          // no CTA leaves while its partials are read
     }
 }
@@ -1514,7 +1524,7 @@ static Plan make_plan(int B, int tq, int Hq, int Hkv, int D, long long cap, int 
     pl.W = pl.ctas * nw;
     const long long units = (long long)B * pl.units, tiles = (cap + TILE - 1) / TILE;
     const int most_tiles = D == 128 ? CL_MAX_TILES_128 : CL_MAX_TILES_256;
-    if (pl.cpu == GPH && !weights)
+    if (pl.cpu == GPH && !(weights && groups > 1))       // one addition per key and call
         for (int c = CL_MAX_CTAS; c >= 2 && !pl.cl_ctas; c /= 2)
             if (units * c <= sms && tiles <= (long long)most_tiles * c * nw)
                 pl.cl_ctas = c;
@@ -1578,9 +1588,9 @@ static cudaError_t launch(const Params &p, int ctas, int sms, cudaStream_t st)
     cudaError_t e;
     if (p.cpu == 64) {
         e = launch_split(wide_kernel<D, WT>, done[0], p, ctas, 128, WideCfg<D>::SMEM, st);
-    } else if (p.cl_ctas) {              // the plan gives clusters without weights
+    } else if (p.cl_ctas) {
         using C = Cfg<D, 1>;
-        return launch_split(decode_kernel<D, 1, false, true>, done[3], p, p.B * p.U_b * p.cl_ctas,
+        return launch_split(decode_kernel<D, 1, WT, true>, done[3], p, p.B * p.U_b * p.cl_ctas,
                             C::NW * 32, C::SMEM, st, p.cl_ctas);
     } else if (p.cpu == GPH) {
         using C = Cfg<D, 1>;
@@ -1907,6 +1917,7 @@ FA_API int fa_decode_int4(const void *q, const void *k_codes, const void *k_scal
         p.lse = reinterpret_cast<float *>(static_cast<char *>(workspace) + wsp.lse);
         p.ws_s = reinterpret_cast<float *>(static_cast<char *>(workspace) + wsp.scores);
         p.cap16 = (cap + 15) / 16 * 16;
+        p.lg_page = block_table ? log2_of(page_size) : -1;
     }
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const cudaError_t e =
