@@ -450,8 +450,9 @@ FA_API size_t fa_decode_int4_workspace_size(int batch, int n_queries, int n_q_he
  *      left as they were.  A row starts from 0 when its token is appended:
  *      the caller clears acc with the pages it hands out (fa_evict_kv clears
  *      the rows it frees).  Sequences that share a block add to the same rows
- *      (in no fixed order; rows of one sequence's own get one addition per
- *      call, so their totals do not depend on timing).
+ *      (in no fixed order; rows of one sequence's own get one addition per 512
+ *      columns and call, in a fixed order, so their totals do not depend on
+ *      timing).
  * out  fp16 (as fa_decode_int4), not fp32.
  * workspace  fa_decode_weights_workspace_size() bytes: the split's partials
  *      and one fp32 score per key and (query, head).
