@@ -373,22 +373,25 @@ def _take(name, t, dtype, shape, dev):
 
 def _device():
     """The current CUDA device (None without one: no tensor is on it)."""
-    return torch.cuda.current_device() if torch.cuda.is_initialized() else None
+    return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else None
 
 
 def _cache_dims(name, k, block_table, batch):
-    """(kv heads, page_size, max_blocks_per_seq, num_blocks, row shape) of a cache
-    [num_blocks, Hkv, page, ...] (paged) or [batch, Hkv, capacity, ...]."""
-    if k.dim() != 4:
+    """(kv heads, page_size, max_blocks_per_seq, num_blocks, row shape, row elements) of a
+    cache [num_blocks, Hkv, page, ...] (paged) or [batch, Hkv, capacity, ...]."""
+    shape = k.shape
+    if len(shape) != 4:
         raise ValueError(f"{name}: caches are [blocks or batch, kv heads, page or capacity, row]")
+    n, hkv, page, width = shape
     if block_table is None:
-        if k.shape[0] != batch:
-            raise ValueError(f"{name}: a contiguous cache holds {k.shape[0]} sequences, "
+        if n != batch:
+            raise ValueError(f"{name}: a contiguous cache holds {n} sequences, "
                              f"the call has {batch}")
-        return k.shape[1], 16, k.shape[2], 0, tuple(k.shape[:3])
-    if block_table.dim() != 2 or block_table.shape[0] != batch:
+        return hkv, 16, page, 0, (n, hkv, page), width
+    table = block_table.shape
+    if len(table) != 2 or table[0] != batch:
         raise ValueError(f"{name}: block_table must be [batch, max_blocks_per_seq]")
-    return k.shape[1], k.shape[2], block_table.shape[1], k.shape[0], tuple(k.shape[:3])
+    return hkv, page, table[1], n, (n, hkv, page), width
 
 
 def _stream_ptr(stream, dev):
@@ -405,8 +408,7 @@ def _workspace(t, dev):
 def _int4_cache(name, k_codes, k_scales, v_codes, v_scales, block_table, batch, dev):
     """Pointers and sizes of a 4-bit cache: (pointers, table, kv heads, page,
     max_blocks, num_blocks, rows, head_dim)."""
-    hkv, page, blocks, total, rows = _cache_dims(name, k_codes, block_table, batch)
-    half = k_codes.shape[3]
+    hkv, page, blocks, total, rows, half = _cache_dims(name, k_codes, block_table, batch)
     scales = (*rows, half // 16)
     ptrs = (_take("k_codes", k_codes, torch.uint8, None, dev),
             _take("k_scales", k_scales, torch.float16, scales, dev),
@@ -423,7 +425,8 @@ def fa_append_kv_int4(k_new, v_new, k_codes, k_scales, v_codes, v_scales, block_
 
     codes: uint8 [blocks, Hkv, page, D/2] with a block_table, or [B, Hkv, capacity, D/2];
     scales: fp16 [..., D/32] beside them."""
-    B, T = k_new.shape[:2]
+    shape = k_new.shape
+    B, T = shape[0], shape[1]
     dev = _device()
     c, bt, hkv, page, blocks, total, _, D = _int4_cache("fa_append_kv_int4", k_codes, k_scales,
                                                         v_codes, v_scales, block_table, B, dev)
@@ -440,7 +443,8 @@ def fa_gather_kv_int4(k_codes, k_scales, v_codes, v_scales, block_table, positio
                       *, n_rows=None, stream=None):
     """Rows positions[b] + i of a 4-bit cache as fp16 k_out / v_out [B, T, Hkv, D];
     `n_rows` [B] int32: only the first n_rows[b] of them."""
-    B, T = k_out.shape[:2]
+    shape = k_out.shape
+    B, T = shape[0], shape[1]
     dev = _device()
     c, bt, hkv, page, blocks, total, _, D = _int4_cache("fa_gather_kv_int4", k_codes, k_scales,
                                                         v_codes, v_scales, block_table, B, dev)
@@ -456,9 +460,10 @@ def fa_gather_kv_int4(k_codes, k_scales, v_codes, v_scales, block_table, positio
 def _queries(name, q, out, n_q_heads, head_dim, dev):
     """(batch, queries, q pointer, out pointer) of q and out, [B, Hq, D] or [B, Tq, Hq, D]."""
     shape = q.shape
-    if len(shape) not in (3, 4) or shape[-2:] != (n_q_heads, head_dim):
+    n = len(shape)
+    if (n != 3 and n != 4) or shape[n - 2] != n_q_heads or shape[n - 1] != head_dim:
         raise ValueError(f"{name}: q must be [B, Hq, D] or [B, Tq, Hq, D]")
-    return (shape[0], 1 if len(shape) == 3 else shape[1],
+    return (shape[0], 1 if n == 3 else shape[1],
             _take("q", q, torch.float16, None, dev), _take("out", out, torch.float16, shape, dev))
 
 
@@ -505,8 +510,8 @@ def fa_decode_weights(q, k_cache, v_cache, v_scales, block_table, seq_lens, n_q_
     KV head, to `acc` (fp32, one value per cache row: the cache's shape without D).
     The workspace is ``alloc_workspace_weights``'s."""
     dev = _device()
-    hkv, page, blocks, total, rows = _cache_dims("fa_decode_weights", k_cache, block_table,
-                                                 q.shape[0])
+    hkv, page, blocks, total, rows, _ = _cache_dims("fa_decode_weights", k_cache, block_table,
+                                                    q.shape[0])
     B, tq, qp, op = _queries("fa_decode_weights", q, out, n_q_heads, head_dim, dev)
     if hkv != n_kv_heads:
         raise ValueError(f"fa_decode_weights: the cache holds {hkv} heads")
@@ -545,9 +550,9 @@ def fa_evict_kv(k_cache, v_cache, acc, block_table, seq_lens, new_lens, *, budge
     (uint8 codes).  Writes new_lens [B] and kept [B, Hkv, budget] (int32)."""
     B = seq_lens.shape[0]
     dev = _device()
-    hkv, page, blocks, total, rows = _cache_dims("fa_evict_kv", k_cache, block_table, B)
+    hkv, page, blocks, total, rows, width = _cache_dims("fa_evict_kv", k_cache, block_table, B)
     int4 = k_scales is not None
-    D = k_cache.shape[3] * (2 if int4 else 1)
+    D = width * (2 if int4 else 1)
     scales = (*rows, D // 32)
     v_type = torch.uint8 if int4 else torch.float16 if v_scales is None else torch.int8
     _check(load().fa_evict_kv(
