@@ -242,11 +242,16 @@ __global__ void __launch_bounds__(256) gather_kernel(const Params p, const RowAr
 //      the tensor pipe busy longer than it saved instructions (226 us against 214
 //      for 32 x 32768 keys of 8 heads x 128).  A key's scale multiplies its weight
 //      instead of its 32 codes: P s_j is the B operand of block j.
-// P and P s are rounded to fp16 (2^-11 each); everything else is fp32.
-// The running maximum moves only when a score passes it by 8 (log2 units), so
-// weights reach 2^8 and most tiles need no shuffles.  V scales outside
-// [2^-12, 2^7] are carried times 2^-e, a power of two per warp, so that P s
-// stays within fp16 whatever the scales.
+// P and P s are rounded to fp16, by 2^-11 of their value where that is a normal fp16;
+// everything else is fp32.  Both are kept as high in fp16's range as they may go, because the
+// keys behind a dominant one (an attention sink) have weights of 2^-10 to 2^-20 and scales of any
+// size, and their sum still counts:
+//   P is taken against a reference 2^P_SHIFT below the largest score, which moves only when a
+//      score passes that maximum by MAX_SLACK (log2 units), so most tiles need no shuffles: P
+//      reaches 2^14, and is a normal fp16 from 2^-24 of the largest weight on.
+//   The V scales of block j are carried times 2^-e_j, which brings the largest so far to
+//      [1/2, 1) and lets it grow to 2, so that P s stays below 2^16 and is a normal fp16 while
+//      weight times scale is at least 2^-24 of their largest values.
 // Tiles are copied in batches of up to BT of one unit (cp.async, a ring of
 // batches per warp); the lanes look their cache rows up side by side, so a tile's
 // share of the addressing is a shuffle and three multiply-adds.  They are
@@ -275,8 +280,9 @@ struct Cfg {
     static_assert(CTAS_PER_SM * (SMEM + 1024) <= 228 * 1024, "shared memory per SM");
 };
 
-constexpr float NO_MAX = -3e38f;       // running maximum of a column that has no key yet
-constexpr float MAX_SLACK = 8.f;       // log2 units a score may pass the running maximum by
+constexpr float NO_MAX = -3e38f;       // reference of a column that has no key yet
+constexpr float P_SHIFT = 10.f;        // log2 units from the reference up to the running maximum
+constexpr float MAX_SLACK = 4.f;       // ... a score may pass that maximum by
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void *src, uint64_t policy)
 {
@@ -331,6 +337,62 @@ __device__ __forceinline__ float pow2(int e)      // 2^e, e in [-126, 127]
 {
     return __uint_as_float(static_cast<unsigned>(e + 127) << 23);
 }
+__device__ __forceinline__ float inv_pow2(float x)       // 1 / x of a power of two
+{
+    return __uint_as_float((254u << 23) - __float_as_uint(x));
+}
+
+// The V scales' powers of two.  Lane `lane` keeps those of the two blocks that its scale words
+// hold (words lane, lane + 32, ... of rows of NJ / 2 words: blocks 2 (lane % (NJ / 2)) and the
+// next), the same in every lane of these blocks.
+template <int NJ>
+struct Carry {
+    __half2 f;       // 2^-e: the scales are used times this
+    __half2 limit;   // a scale above it calls for another
+    __device__ __forceinline__ void reset()
+    {
+        f = __float2half2_rn(1.f);
+        limit = __float2half2_rn(0.f);
+    }
+    // 2^-e for a largest scale of x > 0: x * 2^-e in [1/2, 1), or less from 2^-14 down
+    static __device__ __forceinline__ float factor(float x)
+    {
+        const int ex = static_cast<int>((__float_as_uint(x) >> 23) & 255u) - 126;
+        return pow2(-min(max(ex, -14), 16));
+    }
+    // vm: the largest of this lane's words.  Takes the new powers and gives each block's
+    // rescale(j, new / old), by all lanes.
+    template <typename F>
+    __device__ __forceinline__ void grow(__half2 vm, F rescale)
+    {
+#pragma unroll
+        for (int mask = NJ / 2; mask <= 16; mask <<= 1)
+            vm = __hmax2(vm, as_half2(__shfl_xor_sync(0xffffffffu, as_u32(vm), mask)));
+        const float2 x = __half22float2(vm), lim = __half22float2(limit);
+        const float2 old = __half22float2(f);
+        float2 to = old, top = lim;
+        if (x.x > lim.x) {
+            to.x = factor(x.x);
+            top.x = fminf(2.f * inv_pow2(to.x), 65504.f);
+        }
+        if (x.y > lim.y) {
+            to.y = factor(x.y);
+            top.y = fminf(2.f * inv_pow2(to.y), 65504.f);
+        }
+        f = __floats2half2_rn(to.x, to.y);
+        limit = __floats2half2_rn(top.x, top.y);
+        const float r0 = to.x * inv_pow2(old.x), r1 = to.y * inv_pow2(old.y);
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+            rescale(j, __shfl_sync(0xffffffffu, j & 1 ? r1 : r0, j / 2));
+    }
+    // 2^e of block j, by all lanes
+    __device__ __forceinline__ float undo(int j) const
+    {
+        const float2 x = __half22float2(f);
+        return inv_pow2(__shfl_sync(0xffffffffu, j & 1 ? x.y : x.x, j / 2));
+    }
+};
 // C = A . B, fp16 operands
 __device__ __forceinline__ void mma_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1)
@@ -583,9 +645,8 @@ __global__ void __launch_bounds__(Cfg<D, NG>::NW * 32, Cfg<D, NG>::CTAS_PER_SM)
     // [2j + i]: elements 32j + 4g + 2i (0, 1: columns 2t, 2t+1; times 2^-24) and
     // + 1 (2, 3; times 2^-20)
     float acc[NG][2 * NJ][4];
-    float mr[NG][2], l[NG][2];
-    int e = 0;                // O is held times 2^-e
-    __half2 vlim;             // V scales above it call for another e
+    float mr[NG][2], l[NG][2];       // reference (the running maximum less P_SHIFT), sum of P
+    Carry<NJ> cv;                    // block j of O is held times 2^-e_j
     auto reset = [&] {
 #pragma unroll
         for (int gi = 0; gi < NG; ++gi) {
@@ -595,8 +656,7 @@ __global__ void __launch_bounds__(Cfg<D, NG>::NW * 32, Cfg<D, NG>::CTAS_PER_SM)
             mr[gi][0] = mr[gi][1] = NO_MAX;
             l[gi][0] = l[gi][1] = 0.f;
         }
-        e = 0;
-        vlim = __float2half2_rn(0.f);
+        cv.reset();
     };
     if (n_my > 0)
         load_q();
@@ -720,11 +780,8 @@ __global__ void __launch_bounds__(Cfg<D, NG>::NW * 32, Cfg<D, NG>::CTAS_PER_SM)
             // other rows must not turn a zero weight into NaN
 #pragma unroll
             for (int q = 0; q < NVW; ++q)
-                if (!there((lane + 32 * q) / (NJ / 2))) {
+                if (!there((lane + 32 * q) / (NJ / 2)))
                     vw[q] = 0u;
-                    sts32(ss + C::VS_OFF + (lane + 32 * q) * 4, 0u);
-                }
-            __syncwarp();
         }
         if constexpr (WT) {
 #pragma unroll
@@ -741,28 +798,29 @@ __global__ void __launch_bounds__(Cfg<D, NG>::NW * 32, Cfg<D, NG>::CTAS_PER_SM)
         for (int q = 1; q < NVW; ++q)
             vm = __hmax2(vm, as_half2(vw[q]));
         float top[NG][2];
-        bool over = !__hble2(vm, vlim);
+        const bool big = !__hble2(vm, cv.limit);
+        bool over = big;
 #pragma unroll
         for (int gi = 0; gi < NG; ++gi)
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 top[gi][x] = fmaxf(fmaxf(sc[gi][0][x], sc[gi][0][2 + x]),
                                    fmaxf(sc[gi][1][x], sc[gi][1][2 + x]));
-                over = over || top[gi][x] - mr[gi][x] > MAX_SLACK;
+                over = over || top[gi][x] - mr[gi][x] > P_SHIFT + MAX_SLACK;
             }
         if (__any_sync(0xffffffffu, over)) {
-            float vx = __half2float(__hmax(__low2half(vm), __high2half(vm)));
+            if (__any_sync(0xffffffffu, big))
+                cv.grow(vm, [&](int j, float r) {
 #pragma unroll
-            for (int mask = 1; mask <= 16; mask <<= 1)
-                vx = fmaxf(vx, __shfl_xor_sync(0xffffffffu, vx, mask));
-            int en = e;
-            if (vx > __low2float(vlim)) {
-                // the largest scale so far: carried as it is from 2^-12 to
-                // 2^7, else brought to [1/2, 1) (at most 2^14 up)
-                const int ex = static_cast<int>((__float_as_uint(vx) >> 23) & 255u) - 126;
-                en = (ex >= -11 && ex <= 7) ? 0 : max(ex, -14);
-                vlim = __float2half2_rn(en == 0 ? 128.f : fminf(pow2(en + 2), 65504.f));
-            }
+                    for (int gi = 0; gi < NG; ++gi)
+#pragma unroll
+                        for (int ii = 2 * j; ii < 2 * j + 2; ++ii) {
+                            acc[gi][ii][0] *= r;
+                            acc[gi][ii][1] *= r;
+                            acc[gi][ii][2] *= r;
+                            acc[gi][ii][3] *= r;
+                        }
+                });
 #pragma unroll
             for (int gi = 0; gi < NG; ++gi)
 #pragma unroll
@@ -771,25 +829,21 @@ __global__ void __launch_bounds__(Cfg<D, NG>::NW * 32, Cfg<D, NG>::CTAS_PER_SM)
 #pragma unroll
                     for (int mask = 4; mask <= 16; mask <<= 1)
                         y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, mask));
-                    y = fmaxf(y, mr[gi][x]);
-                    const float a = ex2_ftz(mr[gi][x] - y), r = a * pow2(e - en);
+                    y = fmaxf(y - P_SHIFT, mr[gi][x]);
+                    const float a = ex2_ftz(mr[gi][x] - y);
                     l[gi][x] *= a;
                     mr[gi][x] = y;
 #pragma unroll
                     for (int ii = 0; ii < 2 * NJ; ++ii) {
-                        acc[gi][ii][x] *= r;
-                        acc[gi][ii][2 + x] *= r;
+                        acc[gi][ii][x] *= a;
+                        acc[gi][ii][2 + x] *= a;
                     }
                 }
-            e = en;
         }
-        if (e != 0) {
-            const __half2 f2 = __float2half2_rn(pow2(-e));
 #pragma unroll
-            for (int q = 0; q < NVW; ++q)
-                sts32(ss + C::VS_OFF + (lane + 32 * q) * 4, as_u32(__hmul2(as_half2(vw[q]), f2)));
-            __syncwarp();
-        }
+        for (int q = 0; q < NVW; ++q)
+            sts32(ss + C::VS_OFF + (lane + 32 * q) * 4, as_u32(__hmul2(as_half2(vw[q]), cv.f)));
+        __syncwarp();
         // ---- O^T += V^T . (P s)^T: rows are elements, 4 per block and lane
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -868,6 +922,10 @@ __global__ void __launch_bounds__(Cfg<D, NG>::NW * 32, Cfg<D, NG>::CTAS_PER_SM)
             const bool whole = tc::worker_of(us, T, We) == tc::worker_of(us + cw.n - 1, T, We);
             const int kv = cw.j / p.n_hg, cg = cw.j % p.n_hg;
             const long long slot = w + cw.unit(p);
+            float un[NJ];
+#pragma unroll
+            for (int j = 0; j < NJ; ++j)
+                un[j] = cv.undo(j);
 #pragma unroll
             for (int gi = 0; gi < NG; ++gi)
 #pragma unroll
@@ -881,9 +939,9 @@ __global__ void __launch_bounds__(Cfg<D, NG>::NW * 32, Cfg<D, NG>::CTAS_PER_SM)
                         continue;
                     const float mx = mr[gi][x] == NO_MAX ? -INFINITY : mr[gi][x];
                     // 2^24 and 2^20 as the accumulators hold them; l = 0 only without keys
-                    const float up = whole && lx > 0.f ? pow2(e + 20) / lx : pow2(e + 20);
-                    const float up16 = up * 16.f;
+                    const float up0 = whole && lx > 0.f ? pow2(20) / lx : pow2(20);
                     auto four = [&](int j) {
+                        const float up = up0 * un[j], up16 = up * 16.f;
                         return make_float4(acc[gi][2 * j][x] * up16, acc[gi][2 * j][x + 2] * up,
                                            acc[gi][2 * j + 1][x] * up16,
                                            acc[gi][2 * j + 1][x + 2] * up);
@@ -919,6 +977,10 @@ __global__ void __launch_bounds__(Cfg<D, NG>::NW * 32, Cfg<D, NG>::CTAS_PER_SM)
         // ---- the unit's partials: of every warp (m, l) of 8 columns, then O [8][D], in
         // its ring; folded by all threads of the cluster, 32 elements of a column per warp
         __syncwarp();
+        float un[NJ];
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+            un[j] = cv.undo(j) * pow2(20);
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
             float lx = l[0][x];
@@ -927,17 +989,16 @@ __global__ void __launch_bounds__(Cfg<D, NG>::NW * 32, Cfg<D, NG>::CTAS_PER_SM)
                 lx += __shfl_xor_sync(0xffffffffu, lx, mask);
             const int h = 2 * t + x;
             const uint32_t o = ring + 64 + (h * D + 4 * g) * 4;
-            const float up = pow2(e + 20), up16 = up * 16.f;
             if (g == 0) {
                 sts32(ring + h * 8, __float_as_uint(mr[0][x] == NO_MAX ? -INFINITY : mr[0][x]));
                 sts32(ring + h * 8 + 4, __float_as_uint(lx));
             }
 #pragma unroll
             for (int j = 0; j < NJ; ++j)
-                sts128(o + j * 128, __float_as_uint(acc[0][2 * j][x] * up16),
-                       __float_as_uint(acc[0][2 * j][x + 2] * up),
-                       __float_as_uint(acc[0][2 * j + 1][x] * up16),
-                       __float_as_uint(acc[0][2 * j + 1][x + 2] * up));
+                sts128(o + j * 128, __float_as_uint(acc[0][2 * j][x] * (16.f * un[j])),
+                       __float_as_uint(acc[0][2 * j][x + 2] * un[j]),
+                       __float_as_uint(acc[0][2 * j + 1][x] * (16.f * un[j])),
+                       __float_as_uint(acc[0][2 * j + 1][x + 2] * un[j]));
         }
         tc::cluster_sync();
         const int R = p.cl_ctas * C::NW, kv = pw.j / p.n_hg, cg = pw.j % p.n_hg;
@@ -1010,9 +1071,11 @@ struct WideCfg {
     static constexpr int F16_K = SC + 2 * SC_STAGE;    // codes as fp16, rows of 2 D bytes
     static constexpr int F16_V = F16_K + KT * D * 2;
     static constexpr int Q = F16_V + KT * D * 2;       // the unit's queries
-    static constexpr int SMEM = Q + COLS * D * 2;
+    static constexpr int VS = Q + COLS * D * 2;        // the tile's V scales as they are used
+    static constexpr int SMEM = VS + KT * SB;
     static constexpr int CTAS_PER_SM = D == 128 ? 3 : 2;
     static_assert(F16_K % 128 == 0 && Q % 128 == 0, "swizzled rows");
+    static_assert(KT * SB / 4 == 128, "a word of V scales per thread");
     static_assert(CTAS_PER_SM * (SMEM + 1024) <= 228 * 1024, "shared memory per SM");
 };
 
@@ -1138,16 +1201,14 @@ __global__ void __launch_bounds__(128, WideCfg<D>::CTAS_PER_SM) wide_kernel(cons
     // [n]: columns g (0, 1) and g + 8 (2, 3), elements 8n + t (0, 2) and 8n + t + 4
     float acc[D / 8][4];
     float mr[2], l[2];
-    int e = 0;                // O is held times 2^-e
-    __half2 vlim;             // V scales above it call for another e
+    Carry<NJ> cv;             // as above; every warp sees the same scales and keeps the same powers
     auto reset = [&] {
 #pragma unroll
         for (int i = 0; i < D / 8; ++i)
             acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
         mr[0] = mr[1] = NO_MAX;
         l[0] = l[1] = 0.f;
-        e = 0;
-        vlim = __float2half2_rn(0.f);
+        cv.reset();
     };
     // ---- this lane's places.  Chunk c of row r lies at (c ^ (r & 7)) * 16, so a lane
     // needs one address per value of c's low three bits; the rest are constants.
@@ -1186,13 +1247,35 @@ __global__ void __launch_bounds__(128, WideCfg<D>::CTAS_PER_SM) wide_kernel(cons
         auto there = [&](int k) {                  // key k of the tile is attended by someone
             return k >= cw.lo - base && k < cw.hi - base && ((have >> (k / TILE)) & 1u);
         };
-        if (edge) {
-            // other rows must not turn a zero weight into NaN
-            for (int x = tid; x < KT * NJ / 2; x += 128)
-                if (!there(x / (NJ / 2))) {
-                    sts32(sc + x * 4, 0u);
-                    sts32(sc + KT * C::SB + x * 4, 0u);
+        {
+            // V scales: every warp looks at all of them, a thread writes one word as it is used
+            constexpr int NVW = KT * NJ / 2 / 32;
+            uint32_t mine = 0;
+            __half2 vm = __float2half2_rn(0.f);
+#pragma unroll
+            for (int q = 0; q < NVW; ++q) {
+                const int x = lane + 32 * q;
+                uint32_t v = lds32(sc + KT * C::SB + x * 4);
+                // other rows must not turn a zero weight into NaN
+                if (edge && !there(x / (NJ / 2))) {
+                    v = 0u;
+                    if (q == warp)
+                        sts32(sc + x * 4, 0u);               // their K scales
                 }
+                vm = __hmax2(vm, as_half2(v));
+                mine = q == warp ? v : mine;
+            }
+            if (__any_sync(0xffffffffu, !__hble2(vm, cv.limit)))
+                cv.grow(vm, [&](int j, float r) {
+#pragma unroll
+                    for (int ii = 4 * j; ii < 4 * j + 4; ++ii) {
+                        acc[ii][0] *= r;
+                        acc[ii][1] *= r;
+                        acc[ii][2] *= r;
+                        acc[ii][3] *= r;
+                    }
+                });
+            sts32(sm + C::VS + tid * 4, as_u32(__hmul2(as_half2(mine), cv.f)));
         }
         // ---- unpack: a word of codes is one 16-byte chunk of fp16 values.  8 lanes
         // take the same octet of 8 keys, so reads and writes meet no bank twice.
@@ -1295,49 +1378,33 @@ __global__ void __launch_bounds__(128, WideCfg<D>::CTAS_PER_SM) wide_kernel(cons
                         *reinterpret_cast<float2 *>(a + 8 * TILE) = make_float2(sc4[n][2], sc4[n][3]);
                 }
             }
-            // ---- online softmax (as above: the maximum moves when passed by 8)
-            __half2 vm = __float2half2_rn(0.f);
-#pragma unroll
-            for (int q = 0; q < CK * NJ / 2 / 32; ++q)
-                vm = __hmax2(vm, as_half2(lds32(sc + KT * C::SB + kk * C::SB + (lane + 32 * q) * 4)));
+            // ---- online softmax (as above)
             float x0 = sc4[0][0], x1 = sc4[0][2];
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 x0 = fmaxf(x0, fmaxf(sc4[n][0], sc4[n][1]));
                 x1 = fmaxf(x1, fmaxf(sc4[n][2], sc4[n][3]));
             }
-            const bool over = fmaxf(x0 - mr[0], x1 - mr[1]) > MAX_SLACK || !__hble2(vm, vlim);
+            const bool over = fmaxf(x0 - mr[0], x1 - mr[1]) > P_SHIFT + MAX_SLACK;
             if (__any_sync(0xffffffffu, over)) {
-                float vx = __half2float(__hmax(__low2half(vm), __high2half(vm)));
 #pragma unroll
-                for (int mask = 1; mask <= 16; mask <<= 1) {
-                    if (mask <= 2) {
-                        x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, mask));
-                        x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, mask));
-                    }
-                    vx = fmaxf(vx, __shfl_xor_sync(0xffffffffu, vx, mask));
+                for (int mask = 1; mask <= 2; mask <<= 1) {
+                    x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, mask));
+                    x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, mask));
                 }
-                const float n0 = fmaxf(mr[0], x0), n1 = fmaxf(mr[1], x1);
-                int en = e;
-                if (vx > __low2float(vlim)) {
-                    const int ex = static_cast<int>((__float_as_uint(vx) >> 23) & 255u) - 126;
-                    en = (ex >= -11 && ex <= 7) ? 0 : max(ex, -14);
-                    vlim = __float2half2_rn(en == 0 ? 128.f : fminf(pow2(en + 2), 65504.f));
-                }
+                const float n0 = fmaxf(mr[0], x0 - P_SHIFT), n1 = fmaxf(mr[1], x1 - P_SHIFT);
                 const float a0 = ex2_ftz(mr[0] - n0), a1 = ex2_ftz(mr[1] - n1);
                 l[0] *= a0;
                 l[1] *= a1;
-                const float r0 = a0 * pow2(e - en), r1 = a1 * pow2(e - en);
 #pragma unroll
                 for (int ii = 0; ii < D / 8; ++ii) {
-                    acc[ii][0] *= r0;
-                    acc[ii][1] *= r0;
-                    acc[ii][2] *= r1;
-                    acc[ii][3] *= r1;
+                    acc[ii][0] *= a0;
+                    acc[ii][1] *= a0;
+                    acc[ii][2] *= a1;
+                    acc[ii][3] *= a1;
                 }
                 mr[0] = n0;
                 mr[1] = n1;
-                e = en;
             }
             // ---- O += (P s) . V, 16 keys at a time
 #pragma unroll
@@ -1360,7 +1427,7 @@ __global__ void __launch_bounds__(128, WideCfg<D>::CTAS_PER_SM) wide_kernel(cons
                     uint32_t u[NJ];
 #pragma unroll
                     for (int q = 0; q < NJ / 4; ++q) {
-                        const uint4 v = lds128(sc + KT * C::SB +
+                        const uint4 v = lds128(sm + C::VS +
                                                (kk + 16 * m + 8 * x + 2 * t) * C::SB + q * 16);
                         u[4 * q] = v.x; u[4 * q + 1] = v.y; u[4 * q + 2] = v.z; u[4 * q + 3] = v.w;
                     }
@@ -1368,14 +1435,6 @@ __global__ void __launch_bounds__(128, WideCfg<D>::CTAS_PER_SM) wide_kernel(cons
                     for (int j = 0; j < NJ; ++j)
                         sv[x][j] = as_half2(__byte_perm(u[j / 2], u[NJ / 2 + j / 2],
                                                         j & 1 ? 0x7632 : 0x5410));
-                }
-                if (e != 0) {
-                    const __half2 f2 = __float2half2_rn(pow2(-e));
-#pragma unroll
-                    for (int x = 0; x < 2; ++x)
-#pragma unroll
-                        for (int j = 0; j < NJ; ++j)
-                            sv[x][j] = __hmul2(sv[x][j], f2);
                 }
 #pragma unroll
                 for (int j = 0; j < NJ; ++j) {
@@ -1408,7 +1467,10 @@ __global__ void __launch_bounds__(128, WideCfg<D>::CTAS_PER_SM) wide_kernel(cons
             l[0] += __shfl_xor_sync(0xffffffffu, l[0], mask);
             l[1] += __shfl_xor_sync(0xffffffffu, l[1], mask);
         }
-        const float un = pow2(e);
+        float un[NJ];
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+            un[j] = cv.undo(j);
         {
             const long long us = cw.unit_start();
             const bool whole = tc::worker_of(us, T, We) == tc::worker_of(us + cw.n - 1, T, We);
@@ -1423,12 +1485,12 @@ __global__ void __launch_bounds__(128, WideCfg<D>::CTAS_PER_SM) wide_kernel(cons
                 if (whole) {
                     const tc::Col cc = tc::column(p, kv, cg, c, C::COLS);
                     const long long r = ((long long)cw.b * tq + cc.j) * p.Hq + cc.h;
-                    const float inv = l[x] > 0.f ? un / l[x] : 0.f;
+                    const float inv = l[x] > 0.f ? 1.f / l[x] : 0.f;
                     __half *o = reinterpret_cast<__half *>(p.out) + r * D + t;
 #pragma unroll
                     for (int n = 0; n < D / 8; ++n) {
-                        o[8 * n] = __float2half_rn(acc[n][2 * x] * inv);
-                        o[8 * n + 4] = __float2half_rn(acc[n][2 * x + 1] * inv);
+                        o[8 * n] = __float2half_rn(acc[n][2 * x] * (inv * un[n / 4]));
+                        o[8 * n + 4] = __float2half_rn(acc[n][2 * x + 1] * (inv * un[n / 4]));
                     }
                     if (WT && t == 0)
                         p.lse[r] = l[x] > 0.f ? mx + log2f(l[x]) : -INFINITY;
@@ -1436,8 +1498,8 @@ __global__ void __launch_bounds__(128, WideCfg<D>::CTAS_PER_SM) wide_kernel(cons
                     float *o = p.ws_o + (slot * p.sh + c) * D + t;
 #pragma unroll
                     for (int n = 0; n < D / 8; ++n) {
-                        o[8 * n] = acc[n][2 * x] * un;
-                        o[8 * n + 4] = acc[n][2 * x + 1] * un;
+                        o[8 * n] = acc[n][2 * x] * un[n / 4];
+                        o[8 * n + 4] = acc[n][2 * x + 1] * un[n / 4];
                     }
                     if (t == 0)
                         p.ws_ml[slot * p.sh + c] = make_float2(mx, l[x]);
