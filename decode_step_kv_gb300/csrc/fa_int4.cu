@@ -230,10 +230,12 @@ __global__ void __launch_bounds__(256) gather_kernel(const Params p, const RowAr
 // the A fragments: no dequantised tile is ever written.  The fp16 bits 0x000u
 // and 0x00u0 are the subnormals u 2^-24 and u 2^-20, so an AND makes two codes
 // into a half2.
-//   K: the queries of odd elements are held divided by 16, and each block's sum
-//      is multiplied by the key's scale in fp32.  The codes' offset of 8 adds
-//      -8 sum_j s_j sum(q_j) to a score: one tf32 mma per tile, scales by
-//      block sums (in two tf32 parts, 21 bits).
+//   K: the queries of even elements are held times 16, and each block's sum is multiplied
+//      by the key's scale in fp32.  (In a column with an even element of 4096 or more, those of
+//      odd elements are held divided by 16 instead: exactly, but for 2^-33 of the largest.)
+//      The codes' offset of 8 adds -8 sum_j s_j sum(q_j) to a score: one tf32 mma per tile,
+//      scales by block sums (in two tf32 parts, 21 bits: 2^-21 of the offset, which is at most
+//      a few times the sum of the score's absolute terms).
 //   V: the pair of a half2 runs over two keys (the contraction), so the words
 //      of two keys are interleaved by a byte permute; the accumulators of odd
 //      elements hold 2^-20, the even ones 2^-24.  The offset is taken off in fp16,
@@ -588,49 +590,70 @@ __global__ void __launch_bounds__(Cfg<D, NG>::NW * 32, Cfg<D, NG>::CTAS_PER_SM)
         put();
 
     // ---- the unit's queries: column g's elements (n, n+4) of octet t of block j
-    // as half2, odd n divided by 16; and column g's offset terms in two tf32 parts
+    // as half2, odd n a 16th of even ones; and column g's offset terms in two tf32 parts
     const int tq = p.tq > 1 ? p.tq : 1;
     uint32_t qb[NG][NJ][4];
     float ct[NG][NJ / 4][2];         // of block 4i + t
     int nh = 0, clo[NG][2], chi[NG][2], all_lo = 0, all_hi = 0, base = 0;
     float *scores = nullptr;         // WT: the unit's
+    float c2[NG][2];                 // a sum's log2 units: columns 2t, 2t + 1
     auto load_q = [&] {
         base = cw.tok();
         if constexpr (WT)
             scores = p.ws_s + cw.unit(p) * p.cap16 * p.sh;
         const int kv = cw.j / p.n_hg, cg = cw.j % p.n_hg;
         nh = min(COLS, tq * p.G - cg * COLS);
-        const __half2 sixteenth = __float2half2_rn(0.0625f);
 #pragma unroll
         for (int gi = 0; gi < NG; ++gi) {
             const tc::Col cq = tc::column(p, kv, cg, gi * GPH + g, COLS);
             const uint4 *src = reinterpret_cast<const uint4 *>(
                 p.q + (((long long)cw.b * tq + cq.j) * p.Hq + cq.h) * D);
-            uint4 x[NJ];
+            // even elements times 16 / down, odd ones over down; whether every block's sum is
+            // finite
+            auto hold = [&](auto any, const bool low) {
+                constexpr bool ANY = decltype(any)::value;       // a column may be held low
+                const float down = ANY && low ? 16.f : 1.f;
+                const __half2 even = __float2half2_rn(ANY && low ? 1.f : 16.f);
+                const __half2 odd = __float2half2_rn(ANY && low ? 0.0625f : 1.f);
+                uint4 x[NJ];
 #pragma unroll
-            for (int j = 0; j < NJ; ++j)
-                x[j] = cq.live ? __ldg(src + j * 4 + t) : make_uint4(0u, 0u, 0u, 0u);
+                for (int j = 0; j < NJ; ++j)
+                    x[j] = cq.live ? __ldg(src + j * 4 + t) : make_uint4(0u, 0u, 0u, 0u);
+                bool finite = true;
 #pragma unroll
-            for (int j = 0; j < NJ; ++j) {
-                uint32_t *q = qb[gi][j];
-                q[0] = __byte_perm(x[j].x, x[j].z, 0x5410);                        // 0, 4
-                q[1] = as_u32(__hmul2(as_half2(__byte_perm(x[j].x, x[j].z, 0x7632)), sixteenth));
-                q[2] = __byte_perm(x[j].y, x[j].w, 0x5410);                        // 2, 6
-                q[3] = as_u32(__hmul2(as_half2(__byte_perm(x[j].y, x[j].w, 0x7632)), sixteenth));
-                float sum = 0.f;
+                for (int j = 0; j < NJ; ++j) {
+                    uint32_t *q = qb[gi][j];
+                    q[0] = as_u32(__hmul2(as_half2(__byte_perm(x[j].x, x[j].z, 0x5410)), even));
+                    q[1] = __byte_perm(x[j].x, x[j].z, 0x7632);                        // 1, 5
+                    q[2] = as_u32(__hmul2(as_half2(__byte_perm(x[j].y, x[j].w, 0x5410)), even));
+                    q[3] = __byte_perm(x[j].y, x[j].w, 0x7632);                        // 3, 7
+                    if constexpr (ANY) {
+                        q[1] = as_u32(__hmul2(as_half2(q[1]), odd));
+                        q[3] = as_u32(__hmul2(as_half2(q[3]), odd));
+                    }
+                    float sum = 0.f;
 #pragma unroll
-                for (int n = 0; n < 4; ++n) {
-                    const float2 v = __half22float2(as_half2(q[n]));
-                    sum += (v.x + v.y) * (n & 1 ? 16.f : 1.f);
+                    for (int n = 0; n < 4; ++n) {
+                        const float2 v = __half22float2(as_half2(q[n]));
+                        sum += (v.x + v.y) * (n & 1 ? 16.f : 1.f);
+                    }
+                    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+                    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+                    finite = finite && fabsf(sum) < INFINITY;
+                    if (j % 4 == t) {
+                        sum *= -0.5f * down * p.c2;                    // log2 units
+                        ct[gi][j / 4][0] = __uint_as_float(__float_as_uint(sum) & 0xffffe000u);
+                        ct[gi][j / 4][1] = sum - ct[gi][j / 4][0];
+                    }
                 }
-                sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-                sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-                if (j % 4 == t) {
-                    sum *= -8.f * p.c2;                            // log2 units
-                    ct[gi][j / 4][0] = __uint_as_float(__float_as_uint(sum) & 0xffffe000u);
-                    ct[gi][j / 4][1] = sum - ct[gi][j / 4][0];
-                }
-            }
+                return finite;
+            };
+            const bool low = !hold(std::false_type(), false);    // of all four lanes of a column
+            const unsigned lows = __ballot_sync(0xffffffffu, low);
+            if (lows)
+                hold(std::true_type(), low);
+            c2[gi][0] = p.c2 * ((lows >> (8 * t)) & 1u ? 16777216.f : 1048576.f);
+            c2[gi][1] = p.c2 * ((lows >> (8 * t + 4)) & 1u ? 16777216.f : 1048576.f);
 #pragma unroll
             for (int x1 = 0; x1 < 2; ++x1) {
                 const tc::Col c = tc::column(p, kv, cg, gi * GPH + 2 * t + x1, COLS);
@@ -661,7 +684,6 @@ __global__ void __launch_bounds__(Cfg<D, NG>::NW * 32, Cfg<D, NG>::CTAS_PER_SM)
     if (n_my > 0)
         load_q();
     reset();
-    const float c2 = p.c2 * 16777216.f;
     const uint32_t half_sel = g & 1 ? 0x7632 : 0x5410;
     // lane's places in a stage: K rows g, V rows 2t, scales
     uint32_t kc[NJ / 4], vc[2][NJ / 4];
@@ -748,7 +770,7 @@ __global__ void __launch_bounds__(Cfg<D, NG>::NW * 32, Cfg<D, NG>::CTAS_PER_SM)
             for (int gi = 0; gi < NG; ++gi)
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
-                    sc[gi][h][q] = fmaf(a4[gi][q], c2, off[gi][q]);          // log2 units
+                    sc[gi][h][q] = fmaf(a4[gi][q], c2[gi][q & 1], off[gi][q]);   // log2 units
         }
         // the pair's V scales, a few words per lane, against the limit
         constexpr int NVW = 2 * TILE * NJ / 2 / 32;

@@ -119,6 +119,17 @@ def test_sink_with_recorded_weights(D, tq, batch, n):
 
 
 @pytest.mark.parametrize("D,tq,batch,n", PLANS)
+def test_small_queries_and_large_keys(D, tq, batch, n):
+    """Queries mostly below 2^-10, scores of N(0, 3): no query element loses bits."""
+    r = np.random.RandomState(3)
+    k = r.standard_normal((2, n, D)) * 3 * 2.0 ** 13
+    v = r.standard_normal((2, n, D))
+    q = torch.from_numpy((r.standard_normal((batch, tq, 8, D)) * 2.0 ** -13).astype(np.float16)).cuda()
+    c = Shared(2, n, k.astype(np.float32), v.astype(np.float32), batch)
+    relative_check(c, q, D ** -0.5, c.decode(q, D ** -0.5))
+
+
+@pytest.mark.parametrize("D,tq,batch,n", PLANS)
 def test_a_query_of_nan_gives_nan(D, tq, batch, n):
     """Its own row only, in every plan.  (The others may move their references at other keys, so
     each may be off by its two roundings of 2^-11, twice over, on either side.)"""
@@ -134,3 +145,20 @@ def test_a_query_of_nan_gives_nan(D, tq, batch, n):
     assert torch.all(torch.isnan(got[bad]))
     diff = (got[~bad].double() - clean[~bad].double()).norm(dim=-1)
     assert torch.all(diff <= 2 * 5 * 2.0 ** -11 * clean[~bad].double().norm(dim=-1))
+
+
+def test_large_and_small_queries_side_by_side():
+    """Each column has its own factor: heads of queries of 2^13 beside heads of 2^-13."""
+    r = np.random.RandomState(5)
+    D, n = 128, 2048
+    mag = np.where(np.arange(8) % 2, 2.0 ** 13, 2.0 ** -13).reshape(1, 1, 8, 1)
+    k = r.standard_normal((2, n, D)) * 2.0 ** 13 * 3
+    k[1] *= 2.0 ** -26
+    v = r.standard_normal((2, n, D))
+    c = Shared(2, n, k.astype(np.float32), v.astype(np.float32), 2)
+    q = torch.from_numpy((np.clip(r.standard_normal((2, 1, 8, D)), -4, 4) * mag).astype(np.float16)).cuda()
+    got = c.decode(q, D ** -0.5)
+    for head, keep in ((0, 0), (1, 1)):              # rows whose scores are of N(0, 3)
+        sub = Shared(1, n, k[head:head + 1].astype(np.float32), v[head:head + 1].astype(np.float32), 2)
+        at = slice(4 * head + keep, 4 * head + 4, 2)
+        relative_check(sub, q[:, :, at].contiguous(), D ** -0.5, got[:, :, at].contiguous())
