@@ -153,16 +153,18 @@ __device__ __forceinline__ void move_far(const Params &p, const Args &x, int b, 
     }
 }
 
-// The totals of tokens t0, t0 + step, ... below n start again from zero.
-__device__ __forceinline__ void clear_totals(const Params &p, const Args &x, int b, int kv, int t0,
-                                             int step, int n)
+// The totals of tokens t0, t0 + step, ... below n start again from zero.  Int holds n + 8
+// steps: the second kernel's step is four times the budget, the first one's at most 8192.
+template <typename Int>
+__device__ __forceinline__ void clear_totals(const Params &p, const Args &x, int b, int kv, Int t0,
+                                             Int step, int n)
 {
     constexpr int U = 8;
     for (; t0 < n; t0 += U * step) {
         long long r[U];
 #pragma unroll
         for (int q = 0; q < U; ++q)
-            r[q] = t0 < n - q * step ? row_of(p, x, b, kv, t0 + q * step) : -1;
+            r[q] = t0 < n - q * step ? row_of(p, x, b, kv, static_cast<int>(t0 + q * step)) : -1;
 #pragma unroll
         for (int q = 0; q < U; ++q)
             if (r[q] >= 0)
@@ -185,7 +187,8 @@ __global__ void __launch_bounds__(FAR_THREADS, 4) evict_far_kernel(const Params 
     if (n <= x.budget)
         return;
     const int c = blockIdx.x % chunks, r0 = c * FAR_ROWS;
-    clear_totals(p, x, b, kv, x.budget + c * FAR_THREADS + threadIdx.x, chunks * FAR_THREADS, n);
+    clear_totals<long long>(p, x, b, kv, x.budget + (long long)c * FAR_THREADS + threadIdx.x,
+                            (long long)chunks * FAR_THREADS, n);
     move_far<8>(p, x, b, kv, x.kept + (long long)unit * x.budget, r0, min(FAR_ROWS, x.budget - r0),
                 pl);
 }
@@ -239,8 +242,8 @@ __global__ void __launch_bounds__(THREADS, 2) evict_kernel(const Params p, const
     if (kv == 0 && rank == 0 && tid == 0)
         x.new_lens[b] = min(n, x.budget);
     if (n <= x.budget) {
-        for (int j = rank * THREADS + tid; j < x.budget; j += cs * THREADS)
-            kept[j] = j < n ? j : -1;
+        for (long long j = rank * THREADS + tid; j < x.budget; j += cs * THREADS)
+            kept[j] = j < n ? static_cast<int>(j) : -1;
         return;                                   // the whole cluster
     }
 
@@ -485,7 +488,7 @@ __global__ void __launch_bounds__(THREADS, 2) evict_kernel(const Params p, const
         }
     }
     if (x.fused)
-        clear_totals(p, x, b, kv, x.budget + rank * THREADS + tid, cs * THREADS, n);
+        clear_totals<int>(p, x, b, kv, x.budget + rank * THREADS + tid, cs * THREADS, n);
 
     // ---- rows of kept tokens below the budget that change their place, in rounds of
     // cs * rows
@@ -723,12 +726,15 @@ extern "C" FA_API int fa_evict_kv(void *k_cache, void *v_cache, void *k_scales, 
     int sms = 0;
     if (const int rc = device_sms(&sms))
         return rc;
-    x.fused = (double)units * budget * total <= ev::FUSED_BYTES || units * cs >= sms;
+    // (A budget that no sequence can exceed moves nothing: the second kernel may rely on
+    // budgets of less than 2^30.)
+    x.fused = budget >= cap || (double)units * budget * total <= ev::FUSED_BYTES ||
+              units * cs >= sms;
     x.rows = stage / total / 16 * 16;
     if (x.rows > ev::ROUND_ROWS)
         x.rows = ev::ROUND_ROWS;
     const long long far_chunks = (budget + (long long)ev::FAR_ROWS - 1) / ev::FAR_ROWS;
-    if (units * cs > 0x7fffffffll || units * far_chunks > 0x7fffffffll)
+    if (units * cs > 0x7fffffffll || (!x.fused && units * far_chunks > 0x7fffffffll))
         return fail(FA_ERR_LAYOUT, "%s: too many rows", name);
     cudaError_t e = ev::allow_attributes();
     if (e == cudaSuccess) {
