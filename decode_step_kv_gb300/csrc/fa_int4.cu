@@ -1574,17 +1574,24 @@ struct Plan {
     size_t bytes;                // partial slots and prefix
 };
 
+static bool two_groups_pay(int B, int Hkv, int D, int groups, long long cap, int sms)
+{
+    const double per_warp = (double)B * Hkv * groups * ((cap + TILE - 1) / TILE) /
+                            ((double)sms * Cfg<128, 1>::CTAS_PER_SM * Cfg<128, 1>::NW);
+    return D == 128 && groups > 1 && per_warp >= TWO_GROUP_MIN_TILES;
+}
+
+// cpu: the columns per unit; 0: what the rules above give.
 static Plan make_plan(int B, int tq, int Hq, int Hkv, int D, long long cap, int sms,
-                      bool weights)
+                      bool weights, int cpu = 0)
 {
     Plan pl = {};
     const int cols = tq * (Hq / Hkv);
     const int groups = (cols + GPH - 1) / GPH;
-    const double per_warp = (double)B * Hkv * groups * ((cap + TILE - 1) / TILE) /
-                            ((double)sms * Cfg<128, 1>::CTAS_PER_SM * Cfg<128, 1>::NW);
-    pl.cpu = groups > WIDE_GROUPS * ((cols + 63) / 64)                              ? 64
-             : D == 128 && groups > 1 && !weights && per_warp >= TWO_GROUP_MIN_TILES ? 2 * GPH
-                                                                                    : GPH;
+    pl.cpu = cpu                                                               ? cpu
+             : groups > WIDE_GROUPS * ((cols + 63) / 64)                       ? 64
+             : !weights && two_groups_pay(B, Hkv, D, groups, cap, sms)         ? 2 * GPH
+                                                                               : GPH;
     pl.n_hg = (cols + pl.cpu - 1) / pl.cpu;
     pl.sh = cols < pl.cpu ? cols : pl.cpu;
     pl.units = Hkv * pl.n_hg;
@@ -1616,6 +1623,24 @@ static Plan make_plan(int B, int tq, int Hq, int Hkv, int D, long long cap, int 
     pl.bytes = slots * pl.sh * (D * sizeof(float) + sizeof(float2)) +
                (size_t)(B + 1) * sizeof(long long);
     return pl;
+}
+
+// Bytes of partial slots and prefix that serve these sizes and any smaller batch, number of
+// queries or capacity, whose units may be of another width with more slots: the largest over
+// the widths that one of them may take (each width's bytes grow with every size).
+static size_t plan_bytes(int B, int tq, int Hq, int Hkv, int D, long long cap, int sms)
+{
+    const int cols = tq * (Hq / Hkv), groups = (cols + GPH - 1) / GPH;
+    size_t n = make_plan(B, tq, Hq, Hkv, D, cap, sms, false, GPH).bytes;
+    if (two_groups_pay(B, Hkv, D, groups, cap, sms)) {
+        const size_t m = make_plan(B, tq, Hq, Hkv, D, cap, sms, false, 2 * GPH).bytes;
+        n = m > n ? m : n;
+    }
+    if (groups > WIDE_GROUPS) {
+        const size_t m = make_plan(B, tq, Hq, Hkv, D, cap, sms, false, 64).bytes;
+        n = m > n ? m : n;
+    }
+    return n;
 }
 
 static bool sizes_ok(int batch, int tq, int Hq, int Hkv, int D)
@@ -1890,12 +1915,15 @@ FA_API size_t fa_decode_int4_workspace_size(int batch, int n_queries, int n_q_he
         return 0;
     if (num_sms <= 0 && device_sms(&num_sms) != 0)
         return 0;
-    const i4::Plan pl = i4::make_plan(batch, n_queries, n_q_heads, n_kv_heads, head_dim,
-                                      max_kv_len, num_sms, with_weights != 0);
+    const size_t bytes = i4::plan_bytes(batch, n_queries, n_q_heads, n_kv_heads, head_dim,
+                                        max_kv_len, num_sms);
     if (!with_weights)
-        return pl.bytes;
+        return bytes;
+    // (the scores of a plan with weights grow with every size)
+    const i4::Plan pl = i4::make_plan(batch, n_queries, n_q_heads, n_kv_heads, head_dim,
+                                      max_kv_len, num_sms, true);
     WeightSpace ws;
-    return weight_space(pl.bytes, batch, n_queries, n_q_heads, pl.units, pl.sh, max_kv_len, &ws)
+    return weight_space(bytes, batch, n_queries, n_q_heads, pl.units, pl.sh, max_kv_len, &ws)
                ? ws.total
                : 0;
 }

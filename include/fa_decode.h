@@ -430,7 +430,9 @@ FA_API int fa_decode_int4(const void *q, const void *k_codes, const void *k_scal
                           int batch, int page_size, int max_blocks_per_seq, int num_blocks,
                           void *workspace, size_t workspace_bytes, void *stream);
 
-/* Scratch bytes for fa_decode_int4, with (with_weights != 0) or without acc.
+/* Scratch bytes for fa_decode_int4, with (with_weights != 0) or without acc:
+ * enough for any call with these heads and head_dim whose batch, n_queries and
+ * capacity are no larger, and with weights for those without acc too.
  * Host-only; 0 for invalid sizes and for sizes beyond a size_t. */
 FA_API size_t fa_decode_int4_workspace_size(int batch, int n_queries, int n_q_heads,
                                             int n_kv_heads, int head_dim, int max_kv_len,
