@@ -2210,8 +2210,6 @@ static int decode_impl(const void *q, const void *k_cache, const void *v_cache,
                        const int32_t *slot_ids, int n_slots, float *acc)
 {
     g_err[0] = 0;
-    if (!q || !k_cache || !v_cache || !seq_lens || !out)
-        return fail(FA_ERR_NULL, "fa_decode: q, k_cache, v_cache, seq_lens and out are required");
     if (head_dim != 128 && head_dim != 256)
         return fail(FA_ERR_HEAD_DIM, "fa_decode: head_dim %d not supported (128 or 256)", head_dim);
     if (n_q_heads <= 0 || n_kv_heads <= 0 || n_q_heads % n_kv_heads ||
@@ -2222,6 +2220,10 @@ static int decode_impl(const void *q, const void *k_cache, const void *v_cache,
     if (batch < 0 || batch > 65535 || max_blocks_per_seq <= 0 || n_kv_heads > 4096)
         return fail(FA_ERR_LAYOUT, "fa_decode: bad batch %d, max_blocks_per_seq %d or kv heads %d",
                     batch, max_blocks_per_seq, n_kv_heads);
+    if (batch == 0)                          // a no-op: empty arrays may have no pointer
+        return 0;
+    if (!q || !k_cache || !v_cache || !seq_lens || !out)
+        return fail(FA_ERR_NULL, "fa_decode: q, k_cache, v_cache, seq_lens and out are required");
     const bool paged = block_table != nullptr;
     const bool vi8 = v_scales != nullptr;
     long long cap;
@@ -2281,8 +2283,6 @@ static int decode_impl(const void *q, const void *k_cache, const void *v_cache,
             if (overlaps(acc, acc_bytes, x.p, x.n))
                 return fail(FA_ERR_ALIAS, "fa_decode_weights: acc overlaps out or an input");
     }
-    if (batch == 0)
-        return 0;
     const long long kv_rows_total = paged ? (long long)num_blocks * n_kv_heads * page_size
                                           : slots * n_kv_heads * cap;
     int sms = 0;
@@ -2535,7 +2535,7 @@ FA_API int fa_decode_weights(const void *q, const void *k_cache, const void *v_c
                              size_t workspace_bytes, void *stream)
 {
     g_err[0] = 0;
-    if (!acc)
+    if (!acc && batch != 0)
         return fail(FA_ERR_NULL, "fa_decode_weights: acc is required");
     if (n_queries <= 0 || n_queries > 256)
         return fail(FA_ERR_LAYOUT, "fa_decode_weights: n_queries %d must be in [1, 256]",

@@ -637,25 +637,29 @@ extern "C" FA_API int fa_evict_kv(void *k_cache, void *v_cache, void *k_scales, 
 {
     const char *name = "fa_evict_kv";
     g_err[0] = 0;
-    if (!k_cache || !v_cache || !acc || !seq_lens || !new_lens || !kept)
-        return fail(FA_ERR_NULL, "%s: only block_table and the scales may be NULL", name);
-    if (k_scales && !v_scales)
-        return fail(FA_ERR_NULL, "%s: k_scales (a 4-bit cache) without v_scales", name);
     if (head_dim != 128 && head_dim != 256)
         return fail(FA_ERR_HEAD_DIM, "%s: head_dim %d not supported (128 or 256)", name, head_dim);
     if (n_kv_heads <= 0 || n_kv_heads > 4096)
         return fail(FA_ERR_HEADS, "%s: n_kv_heads %d", name, n_kv_heads);
+    if (batch < 0 || batch > 65535)
+        return fail(FA_ERR_LAYOUT, "%s: bad batch %d", name, batch);
+    if (budget <= 0 || n_sink < 0 || n_recent < 0 || (long long)n_sink + n_recent > budget)
+        return fail(FA_ERR_LAYOUT, "%s: budget %d must be positive and hold n_sink %d and "
+                                   "n_recent %d", name, budget, n_sink, n_recent);
+    if (batch == 0)                          // a no-op: empty arrays may have no pointer
+        return 0;
+    if (!k_cache || !v_cache || !acc || !seq_lens || !new_lens || !kept)
+        return fail(FA_ERR_NULL, "%s: only block_table and the scales may be NULL", name);
+    if (k_scales && !v_scales)
+        return fail(FA_ERR_NULL, "%s: k_scales (a 4-bit cache) without v_scales", name);
     const bool paged = block_table != nullptr;
-    if (batch < 0 || batch > 65535 || max_blocks_per_seq <= 0 ||
+    if (max_blocks_per_seq <= 0 ||
         (paged && (page_size <= 0 || page_size % 16 || num_blocks <= 0)))
-        return fail(FA_ERR_LAYOUT, "%s: bad batch, capacity, page size or block count", name);
+        return fail(FA_ERR_LAYOUT, "%s: bad capacity, page size or block count", name);
     const long long cap = paged ? (long long)max_blocks_per_seq * page_size
                                 : (long long)max_blocks_per_seq;
     if (cap > (1ll << 30))
         return fail(FA_ERR_LAYOUT, "%s: capacity %lld tokens too large", name, cap);
-    if (budget <= 0 || n_sink < 0 || n_recent < 0 || (long long)n_sink + n_recent > budget)
-        return fail(FA_ERR_LAYOUT, "%s: budget %d must be positive and hold n_sink %d and "
-                                   "n_recent %d", name, budget, n_sink, n_recent);
     if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned16(k_scales) ||
         !aligned16(v_scales) || !aligned_to(acc, 4) || !aligned_to(seq_lens, 4) ||
         !aligned_to(new_lens, 4) || !aligned_to(kept, 4) || !aligned_to(block_table, 4))
@@ -688,8 +692,6 @@ extern "C" FA_API int fa_evict_kv(void *k_cache, void *v_cache, void *k_scales, 
         for (int j = 0; j < i && j < 7; ++j)
             if (overlaps(io[i].p, io[i].n, io[j].p, io[j].n))
                 return fail(FA_ERR_ALIAS, "%s: two arrays overlap", name);
-    if (batch == 0)
-        return 0;
     int total = 0;
     for (int a = 0; a < 4; ++a)
         total += x.a[a] ? x.row_bytes[a] : 0;

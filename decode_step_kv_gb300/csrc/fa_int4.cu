@@ -1712,18 +1712,26 @@ static cudaError_t launch(const Params &p, int ctas, int sms, cudaStream_t st)
     return e == cudaSuccess ? launch_merge_half<D>(p, sms, st) : e;
 }
 
-// The checks of a cache's layout that append, gather and decode share.
-static int check_cache(const char *name, int head_dim, int n_kv_heads, bool paged, int batch,
-                       int page_size, int max_blocks, int num_blocks, long long *cap,
-                       size_t *kv_rows)
+// Whether a call has anything to do: 0 (a no-op, whatever its pointers: empty arrays may have
+// none), an error of its sizes, or NOT_EMPTY.
+constexpr int NOT_EMPTY = 1;
+static int check_empty(const char *name, int head_dim, int n_kv_heads, int batch, int n_tokens)
 {
     if (head_dim != 128 && head_dim != 256)
         return fail(FA_ERR_HEAD_DIM, "%s: head_dim %d not supported (128 or 256)", name, head_dim);
     if (n_kv_heads <= 0 || n_kv_heads > 4096)
         return fail(FA_ERR_HEADS, "%s: n_kv_heads %d", name, n_kv_heads);
-    if (batch < 0 || batch > 65535 || max_blocks <= 0)
-        return fail(FA_ERR_LAYOUT, "%s: bad batch %d or max_blocks_per_seq %d", name, batch,
-                    max_blocks);
+    if (batch < 0 || batch > 65535 || n_tokens < 0)
+        return fail(FA_ERR_LAYOUT, "%s: bad batch %d or n_tokens %d", name, batch, n_tokens);
+    return batch == 0 || n_tokens == 0 ? 0 : NOT_EMPTY;
+}
+
+// The checks of a cache's layout that append, gather and decode share.
+static int check_cache(const char *name, int n_kv_heads, bool paged, int batch, int page_size,
+                       int max_blocks, int num_blocks, long long *cap, size_t *kv_rows)
+{
+    if (max_blocks <= 0)
+        return fail(FA_ERR_LAYOUT, "%s: bad max_blocks_per_seq %d", name, max_blocks);
     if (paged) {
         if (page_size <= 0 || page_size % 16 || num_blocks <= 0)
             return fail(FA_ERR_LAYOUT, "%s: page_size %d must be a positive multiple of 16 and "
@@ -1817,16 +1825,17 @@ FA_API int fa_append_kv_int4(const float *k_new, const float *v_new, void *k_cod
 {
     const char *name = "fa_append_kv_int4";
     g_err[0] = 0;
-    if (!k_new || !v_new || !k_codes || !k_scales || !v_codes || !v_scales || !positions)
-        return fail(FA_ERR_NULL, "%s: only block_table and n_new may be NULL", name);
     long long cap;
     size_t kv_rows;
-    int rc = i4::check_cache(name, head_dim, n_kv_heads, block_table != nullptr, batch, page_size,
-                             max_blocks_per_seq, num_blocks, &cap, &kv_rows);
+    int rc = i4::check_empty(name, head_dim, n_kv_heads, batch, n_tokens);
+    if (rc != i4::NOT_EMPTY)
+        return rc;
+    if (!k_new || !v_new || !k_codes || !k_scales || !v_codes || !v_scales || !positions)
+        return fail(FA_ERR_NULL, "%s: only block_table and n_new may be NULL", name);
+    rc = i4::check_cache(name, n_kv_heads, block_table != nullptr, batch, page_size,
+                         max_blocks_per_seq, num_blocks, &cap, &kv_rows);
     if (rc)
         return rc;
-    if (n_tokens < 0)
-        return fail(FA_ERR_LAYOUT, "%s: n_tokens %d", name, n_tokens);
     if (!aligned16(k_new) || !aligned16(v_new) || !aligned16(k_codes) || !aligned16(v_codes) ||
         !aligned16(k_scales) || !aligned16(v_scales) || !aligned_to(positions, 4) ||
         !aligned_to(block_table, 4) || !aligned_to(n_new, 4))
@@ -1840,8 +1849,6 @@ FA_API int fa_append_kv_int4(const float *k_new, const float *v_new, void *k_cod
                             {block_table, (size_t)batch * max_blocks_per_seq * 4}};
     if ((rc = i4::check_rows(name, outs, 4, ins, 5)))
         return rc;
-    if (rows == 0)
-        return 0;
     i4::RowArgs a = {};
     if (!i4::row_args(n_tokens, n_kv_heads, head_dim, page_size, n_new, &a))
         return fail(FA_ERR_LAYOUT, "%s: too many rows per sequence", name);
@@ -1865,16 +1872,17 @@ FA_API int fa_gather_kv_int4(const void *k_codes, const void *k_scales, const vo
 {
     const char *name = "fa_gather_kv_int4";
     g_err[0] = 0;
-    if (!k_codes || !k_scales || !v_codes || !v_scales || !positions || !k_out || !v_out)
-        return fail(FA_ERR_NULL, "%s: only block_table and n_rows may be NULL", name);
     long long cap;
     size_t kv_rows;
-    int rc = i4::check_cache(name, head_dim, n_kv_heads, block_table != nullptr, batch, page_size,
-                             max_blocks_per_seq, num_blocks, &cap, &kv_rows);
+    int rc = i4::check_empty(name, head_dim, n_kv_heads, batch, n_tokens);
+    if (rc != i4::NOT_EMPTY)
+        return rc;
+    if (!k_codes || !k_scales || !v_codes || !v_scales || !positions || !k_out || !v_out)
+        return fail(FA_ERR_NULL, "%s: only block_table and n_rows may be NULL", name);
+    rc = i4::check_cache(name, n_kv_heads, block_table != nullptr, batch, page_size,
+                         max_blocks_per_seq, num_blocks, &cap, &kv_rows);
     if (rc)
         return rc;
-    if (n_tokens < 0)
-        return fail(FA_ERR_LAYOUT, "%s: n_tokens %d", name, n_tokens);
     if (!aligned16(k_out) || !aligned16(v_out) || !aligned16(k_codes) || !aligned16(v_codes) ||
         !aligned16(k_scales) || !aligned16(v_scales) || !aligned_to(positions, 4) ||
         !aligned_to(block_table, 4) || !aligned_to(n_rows, 4))
@@ -1888,8 +1896,6 @@ FA_API int fa_gather_kv_int4(const void *k_codes, const void *k_scales, const vo
                             {block_table, (size_t)batch * max_blocks_per_seq * 4}};
     if ((rc = i4::check_rows(name, outs, 2, ins, 7)))
         return rc;
-    if (rows == 0)
-        return 0;
     i4::RowArgs a = {};
     if (!i4::row_args(n_tokens, n_kv_heads, head_dim, page_size, n_rows, &a))
         return fail(FA_ERR_LAYOUT, "%s: too many rows per sequence", name);
@@ -1937,12 +1943,15 @@ FA_API int fa_decode_int4(const void *q, const void *k_codes, const void *k_scal
 {
     const char *name = "fa_decode_int4";
     g_err[0] = 0;
-    if (!q || !k_codes || !k_scales || !v_codes || !v_scales || !seq_lens || !out)
-        return fail(FA_ERR_NULL, "%s: only block_table, window and acc may be NULL", name);
     long long cap;
     size_t kv_rows;
-    int rc = i4::check_cache(name, head_dim, n_kv_heads, block_table != nullptr, batch, page_size,
-                             max_blocks_per_seq, num_blocks, &cap, &kv_rows);
+    int rc = i4::check_empty(name, head_dim, n_kv_heads, batch, 1);
+    if (rc != i4::NOT_EMPTY)
+        return rc;
+    if (!q || !k_codes || !k_scales || !v_codes || !v_scales || !seq_lens || !out)
+        return fail(FA_ERR_NULL, "%s: only block_table, window and acc may be NULL", name);
+    rc = i4::check_cache(name, n_kv_heads, block_table != nullptr, batch, page_size,
+                         max_blocks_per_seq, num_blocks, &cap, &kv_rows);
     if (rc)
         return rc;
     if (n_q_heads <= 0 || n_q_heads % n_kv_heads || n_q_heads / n_kv_heads > 64)
@@ -1970,8 +1979,6 @@ FA_API int fa_decode_int4(const void *q, const void *k_codes, const void *k_scal
                             {block_table, (size_t)batch * max_blocks_per_seq * 4}};
     if ((rc = i4::check_rows(name, outs, 2, ins, 8)))
         return rc;
-    if (batch == 0)
-        return 0;
     int sms = 0;
     if ((rc = device_sms(&sms)))
         return rc;

@@ -499,8 +499,8 @@ FA_API size_t fa_decode_weights_workspace_size(int batch, int n_queries, int n_q
  * token in an unmapped block counts as -infinity and is not moved
  * (FA_STATUS_BAD_BLOCK; one of the first n_sink tokens is not read, so it sets
  * nothing).  Blocks must not be shared between sequences.  No two of the
- * arrays may overlap (new_lens is not seq_lens).  The work is one or two
- * kernels on `stream`, with no workspace.
+ * arrays may overlap (new_lens is not seq_lens).  batch = 0 is a no-op.  The
+ * work is one or two kernels on `stream`, with no workspace.
  */
 FA_API int fa_evict_kv(void *k_cache, void *v_cache, void *k_scales, void *v_scales, float *acc,
                        const int32_t *block_table, const int32_t *seq_lens, int32_t *new_lens,
