@@ -155,6 +155,15 @@ __device__ __forceinline__ float ex2_ftz(float x)
     return y;
 }
 
+// Of a kernel launched while the one before it may still run: waits until that one has
+// finished and its writes can be read.  Every CTA of such a kernel gets here before it ends,
+// those without anything to read too: what follows on the stream waits for this kernel alone,
+// and must find both done.
+__device__ __forceinline__ void wait_for_previous()
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 __device__ __forceinline__ void flag(unsigned bit)
 {
     atomicOr(&g_status, bit);
@@ -745,7 +754,7 @@ __device__ __forceinline__ void merge_row(const Params &p, const long long row)
         ns = (n + p.chunk - 1) / p.chunk;
         if (ns == 1)
             return;                               // written by the split kernel
-        asm volatile("griddepcontrol.wait;" ::: "memory");
+        wait_for_previous();
         sb = u * p.max_chunks;
     } else {
         // T, and the flattened start and tiles of sequence b: one warp's
@@ -779,7 +788,7 @@ __device__ __forceinline__ void merge_row(const Params &p, const long long row)
             return;
         }
         if (!scan_here) {
-            asm volatile("griddepcontrol.wait;" ::: "memory");
+            wait_for_previous();
             if (tid == 0) {
                 sh_T = p.pref[p.B];
                 sh_P = p.pref[b];
@@ -794,7 +803,7 @@ __device__ __forceinline__ void merge_row(const Params &p, const long long row)
         if (wf == wl)
             return;                               // written by the split kernel
         if (scan_here)
-            asm volatile("griddepcontrol.wait;" ::: "memory");
+            wait_for_previous();
         sb = wf + u;
         ns = wl - wf + 1;
     }
@@ -907,6 +916,7 @@ template <int D, bool BI, typename OutT = float>
 __global__ void __launch_bounds__(MERGE_THREADS) fa_stream_merge_kernel(const Params p)
 {
     merge_row<D, BI, OutT>(p, blockIdx.x);
+    wait_for_previous();             // rows that the split kernel wrote, and empty ones
 }
 
 // Warp-per-row form of the stream-K merge, for steps with many rows (the
@@ -958,7 +968,7 @@ __device__ __forceinline__ void merge_rows(const Params &p, const int cta)
         return;
     }
     if (!scan_here) {
-        asm volatile("griddepcontrol.wait;" ::: "memory");
+        wait_for_previous();
         T = p.pref[p.B];
         P = p.pref[b];
     }
@@ -969,7 +979,7 @@ __device__ __forceinline__ void merge_rows(const Params &p, const int cta)
     if (wf == wl)
         return;                                   // written by the split kernel
     if (scan_here)
-        asm volatile("griddepcontrol.wait;" ::: "memory");
+        wait_for_previous();
     const long long sb = (long long)wf + (long long)b * p.U_b + j;
     const int ns = wl - wf + 1;
     const float2 *ml = p.ws_ml + sb * p.sh + hh;
@@ -1021,6 +1031,7 @@ __global__ void __launch_bounds__(MERGE_ROWS_PER_CTA * 32) fa_stream_merge_rows_
     const Params p)
 {
     merge_rows<D, OutT>(p, blockIdx.x);
+    wait_for_previous();             // as above
 }
 
 // Recorded weights: every key of sequence b and KV head kv adds
@@ -1079,7 +1090,7 @@ __device__ __forceinline__ void add_weights(const Params &p, const int cta, cons
             have_b = b;
         }
         if (!waited)
-            asm volatile("griddepcontrol.wait;" ::: "memory");
+            wait_for_previous();
         waited = true;
         if (b != have_b) {                                 // published by the split kernel
             T = p.pref[p.B];
@@ -1189,8 +1200,6 @@ __device__ __forceinline__ void add_weights(const Params &p, const int cta, cons
             }
         }
     }
-    if (!waited)
-        asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // The same in the cluster plan, whose warps have their own keys' scores at hand (`unit`:
@@ -1252,6 +1261,7 @@ __global__ void __launch_bounds__(MERGE_THREADS, D == 128 ? 4 : 2) fa_merge_weig
         merge_rows<D, __half>(p, blockIdx.x);
     else
         merge_row<D, false, __half>(p, blockIdx.x);
+    wait_for_previous();             // as above
 }
 static_assert(MERGE_THREADS == MERGE_ROWS_PER_CTA * 32, "one block size for both merges");
 

@@ -1346,15 +1346,13 @@ __global__ void __launch_bounds__(D / 4) fa_merge_kernel(const Params p)
     attended_range(p, b, lo, hi, false);
     const int nt = hi > lo ? (hi - 1) / p.tile - lo / p.tile + 1 : 0;
     const int ns = (nt + p.tps - 1) / p.tps;
-    if (ns == 1)
-        return;                                   // the split kernel wrote this row
     float4 *dst = reinterpret_cast<float4 *>(p.out + row * D) + threadIdx.x;
-    if (ns == 0) {
+    if (ns == 0)
         *dst = make_float4(0.f, 0.f, 0.f, 0.f);
-        return;
-    }
     // launched programmatically: wait here until the split grid's partials are visible
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    wait_for_previous();
+    if (ns <= 1)
+        return;                                   // an empty row, or one the split kernel wrote
     const float2 *ml = p.ws_ml + row * p.max_splits;
     const float4 *po = reinterpret_cast<const float4 *>(p.ws_o + row * p.max_splits * D) +
                        threadIdx.x;

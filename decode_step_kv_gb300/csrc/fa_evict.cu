@@ -182,8 +182,7 @@ __global__ void __launch_bounds__(FAR_THREADS, 4) evict_far_kernel(const Params 
     const int b = unit / p.Hkv, kv = unit % p.Hkv;
     int lo, n;
     attended_range(p, b, lo, n, false);
-    // every CTA waits: what follows on the stream must find both kernels done
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    wait_for_previous();
     if (n <= x.budget)
         return;
     const int c = blockIdx.x % chunks, r0 = c * FAR_ROWS;
