@@ -62,22 +62,32 @@ def parse_args():
 def recorded_traffic(kernel, workload):
     """DRAM bytes per launch of `kernel` on `workload` from the committed ncu
     summary, or None when that summary was taken on a different kernel source
-    (the counters then no longer describe the code being timed)."""
+    (the counters then no longer describe the code being timed): the hash of
+    fa_decode.cu and, on lines "<name> sha256:", of each file beside it that it
+    includes."""
     import hashlib
+    import re
     path = os.path.join(ROOT, "profiles", f"{kernel}_{workload}.md")
     src = os.path.join(ROOT, "decode_step_kv_gb300", "csrc", "fa_decode.cu")
+
+    def sha(file):
+        with open(file, "rb") as f:
+            return hashlib.sha256(f.read()).hexdigest()
+
     try:
         text = open(path).read()
-        sha = hashlib.sha256(open(src, "rb").read()).hexdigest()
+        want = {"source": sha(src)}
+        for name in re.findall(r'^\s*#include\s+"([^"/]+)"', open(src).read(), re.M):
+            file = os.path.join(os.path.dirname(src), name)
+            if os.path.exists(file):
+                want[name] = sha(file)
     except OSError:
         return None
-    recorded_sha = recorded = None
-    for line in text.splitlines():
-        if "source sha256:" in line:
-            recorded_sha = line.split("source sha256:")[1].split()[0].strip()
-        if "traffic_bytes_per_launch:" in line:
-            recorded = int(line.split("traffic_bytes_per_launch:")[1].split()[0])
-    return recorded if recorded_sha == sha else None
+    for name, digest in want.items():
+        if re.search(rf"{re.escape(name)} sha256:\s*{digest}", text) is None:
+            return None
+    recorded = re.findall(r"traffic_bytes_per_launch:\s*(\d+)", text)
+    return int(recorded[-1]) if recorded else None
 
 
 def measured_peaks():
