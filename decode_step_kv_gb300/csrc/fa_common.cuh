@@ -748,13 +748,13 @@ __device__ __forceinline__ void merge_row(const Params &p, const long long row)
         n = tiles_in<TILE>(lo, hi);
         if (n == 0) {
             zero_row();
-            return;
+            return wait_for_previous();
         }
         // batch-invariant plan: the unit's chunks, one slot each
         ns = (n + p.chunk - 1) / p.chunk;
+        wait_for_previous();
         if (ns == 1)
             return;                               // written by the split kernel
-        wait_for_previous();
         sb = u * p.max_chunks;
     } else {
         // T, and the flattened start and tiles of sequence b: one warp's
@@ -785,7 +785,7 @@ __device__ __forceinline__ void merge_row(const Params &p, const long long row)
         }
         if (n == 0) {                             // uniform over the CTA
             zero_row();
-            return;
+            return wait_for_previous();
         }
         if (!scan_here) {
             wait_for_previous();
@@ -800,10 +800,10 @@ __device__ __forceinline__ void merge_row(const Params &p, const long long row)
         const long long us = sh_P + (long long)j * (n + UNIT_COST) + UNIT_COST;   // first tile
         const int wf = worker_of(us, T, We);
         const int wl = worker_of(us + n - 1, T, We);
-        if (wf == wl)
-            return;                               // written by the split kernel
         if (scan_here)
             wait_for_previous();
+        if (wf == wl)
+            return;                               // written by the split kernel
         sb = wf + u;
         ns = wl - wf + 1;
     }
@@ -916,7 +916,6 @@ template <int D, bool BI, typename OutT = float>
 __global__ void __launch_bounds__(MERGE_THREADS) fa_stream_merge_kernel(const Params p)
 {
     merge_row<D, BI, OutT>(p, blockIdx.x);
-    wait_for_previous();             // rows that the split kernel wrote, and empty ones
 }
 
 // Warp-per-row form of the stream-K merge, for steps with many rows (the
@@ -936,7 +935,7 @@ __device__ __forceinline__ void merge_rows(const Params &p, const int cta)
     const long long rows = (long long)p.B * tq * p.Hq;
     const long long row = (long long)cta * MERGE_ROWS_PER_CTA + (threadIdx.x >> 5);
     if (row >= rows)
-        return;
+        return wait_for_previous();
     // row = (b * tq + query) * Hq + head; its column x = query * G + head % G
     const int b = static_cast<int>(row / ((long long)tq * p.Hq));
     const int qj = static_cast<int>((row / p.Hq) % tq);
@@ -965,7 +964,7 @@ __device__ __forceinline__ void merge_rows(const Params &p, const int cta)
 #pragma unroll
         for (int c = 0; c < CPL; ++c)
             store4(dst + 4 * (lane + 32 * c), make_float4(0.f, 0.f, 0.f, 0.f));
-        return;
+        return wait_for_previous();
     }
     if (!scan_here) {
         wait_for_previous();
@@ -976,10 +975,10 @@ __device__ __forceinline__ void merge_rows(const Params &p, const int cta)
     const long long us = P + (long long)j * (n + UNIT_COST) + UNIT_COST;   // first tile
     const int wf = worker_of(us, T, We);
     const int wl = worker_of(us + n - 1, T, We);
-    if (wf == wl)
-        return;                                   // written by the split kernel
     if (scan_here)
         wait_for_previous();
+    if (wf == wl)
+        return;                                   // written by the split kernel
     const long long sb = (long long)wf + (long long)b * p.U_b + j;
     const int ns = wl - wf + 1;
     const float2 *ml = p.ws_ml + sb * p.sh + hh;
@@ -1031,7 +1030,6 @@ __global__ void __launch_bounds__(MERGE_ROWS_PER_CTA * 32) fa_stream_merge_rows_
     const Params p)
 {
     merge_rows<D, OutT>(p, blockIdx.x);
-    wait_for_previous();             // as above
 }
 
 // Recorded weights: every key of sequence b and KV head kv adds
@@ -1200,6 +1198,8 @@ __device__ __forceinline__ void add_weights(const Params &p, const int cta, cons
             }
         }
     }
+    if (!waited)
+        wait_for_previous();
 }
 
 // The same in the cluster plan, whose warps have their own keys' scores at hand (`unit`:
@@ -1261,7 +1261,6 @@ __global__ void __launch_bounds__(MERGE_THREADS, D == 128 ? 4 : 2) fa_merge_weig
         merge_rows<D, __half>(p, blockIdx.x);
     else
         merge_row<D, false, __half>(p, blockIdx.x);
-    wait_for_previous();             // as above
 }
 static_assert(MERGE_THREADS == MERGE_ROWS_PER_CTA * 32, "one block size for both merges");
 
