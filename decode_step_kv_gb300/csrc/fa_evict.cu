@@ -17,18 +17,20 @@
 //   leave.  Ties go to the lowest index.  A CTA keeps its share of the totals in
 //   shared memory when it fits (23424 tokens), so they are read once.
 //   Move: rows go down in place (a kept row's new index is never above its old
-//   one; those before the first dropped token stay).  A write to row j only clobbers a source when token j itself is kept,
-//   so order matters only among the kept tokens below the budget.  Those move
-//   first, in rounds: every CTA of the cluster reads its rows of the round into
+//   one; those before the first dropped token stay).  A write to row j only
+//   clobbers a source when token j itself is kept, so order matters only among
+//   the kept tokens below the budget.  Those move first, in rounds: every CTA of the cluster reads its rows of the round into
 //   shared memory, a cluster barrier, every CTA writes them (what a round
 //   overwrites lies below the sources of all later rounds).  After them, the
 //   kept tokens from the budget on move in any order.
-// A first eviction is bound by HBM in its second half (each kept row that changes its
-// place is read and written once, in pieces of a row) and by latency in its first: 32
-// sequences of 1024 to 8192 tokens x 8 heads x 128 (fp16) cut to 2048 take 121 us, of
-// which ~18 select, against 68 for the bytes; one of 131072 x 8 heads x 256 cut to
-// 16384 takes 101, of which ~30 select, against 40.  A later one, with most kept
-// tokens at their places, takes 49 and 67.
+// Bound by latency: of selecting (~18 us in the first case below, ~30 in the second), of the
+// rounds' barriers, and of rows of 256 or 512 bytes read and written once from scattered
+// places (DRAM 44% busy in the first case's kernel, 57% in the second's second one).  GPU time,
+// cold L2, fp16, against the bytes of the totals and of the rows that change their place:
+//   32 sequences of 1024 to 8192 tokens x 8 heads x 128, cut to 2048       119 us     67
+//   32 of 2304 (cut again 256 tokens later)                                115 us     80
+//   one of 131072 x 8 heads x 256, cut to 16384                             97 us     40
+//   one of 16640 (again 256 later: 96% of the moved rows in order)          89 us     16
 #include "fa_common.cuh"
 
 namespace fa {
@@ -549,7 +551,7 @@ __global__ void __launch_bounds__(THREADS, 2) evict_kernel(const Params p, const
     // before the last round's barrier
     if (x.fused) {
         // chunks as long as leave every CTA one: their places cost a chain of loads each
-        // (32 ragged sequences, 64 rows at a time: 154 us, 512: 123)
+        // (32 ragged sequences, 64 rows at a time: a quarter slower)
         const int F = min(max((x.budget - n_near + cs - 1) / cs, FAR_ROWS), ROUND_ROWS);
         for (int r0 = n_near + rank * F; r0 < x.budget; r0 += cs * F)
             move_far<4>(p, x, b, kv, kept, r0, min(F, x.budget - r0), pl);
@@ -723,7 +725,7 @@ extern "C" FA_API int fa_evict_kv(void *k_cache, void *v_cache, void *k_scales, 
             }
     p.cl_ctas = cs;
     // One kernel when there is little to move, or when the clusters fill the GPU anyway:
-    // 32 ragged sequences x 8 heads, 125 us against 137 with the far rows in a second.
+    // 32 ragged sequences x 8 heads, a tenth slower with the far rows in a second.
     int sms = 0;
     if (const int rc = device_sms(&sms))
         return rc;

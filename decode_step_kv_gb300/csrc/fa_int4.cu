@@ -101,13 +101,13 @@ __device__ __forceinline__ void row_place(const Params &p, const RowArgs &a, uns
     kv = r - i * p.Hkv;
 }
 
-// Reads each element once and writes whole rows: bound by HBM as long as an
-// element takes few instructions.  Hence the code by one fused multiply-add: with
-// 1.5 * 2^23 + 8 added, the sum's low four bits are the nibble of the rounded
-// x / s; where x - c*s does not confirm it (a tie, a quotient next to one, a NaN,
-// a scale rounded so far down that codes are cut off) the thread takes the exact
-// form.  2 x 16384 rows of 8 heads x 128: 33 us, 23 for the bytes, with the ALU busy
-// 56% of the time.  (One word per thread and a division per scale: 38 us.)
+// Reads each element once and writes whole rows, in few instructions per element: the
+// code comes from one fused multiply-add: with 1.5 * 2^23 + 8 added, the sum's low four
+// bits are the nibble of the rounded x / s; where x - c*s does not confirm it (a tie, a
+// quotient next to one, a NaN, a scale rounded so far down that codes are cut off) the
+// thread takes the exact form.  2 x 16384 rows of 8 heads x 128: 33 us, 23 for the bytes;
+// nothing is full (DRAM 52%, ALU 56%, issue 64%), the loads of 16 bytes that lie 64 apart
+// wait longest.  (One word per thread and a division per scale: 38 us.)
 template <int D>
 __global__ void __launch_bounds__(256) append_kernel(const Params p, const RowArgs a,
                                                      const float *k_new, const float *v_new,
@@ -254,14 +254,19 @@ __global__ void __launch_bounds__(256) gather_kernel(const Params p, const RowAr
 //   The V scales of block j are carried times 2^-e_j, which brings the largest so far to
 //      [1/2, 1) and lets it grow to 2, so that P s stays below 2^16 and is a normal fp16 while
 //      weight times scale is at least 2^-24 of their largest values.
+// So the result is off by 3.0-3.8e-4 of its norm, 2.1e-4 of them its own rounding, also behind a
+// sink that takes half the weight (32768 keys, V of 0.02: 3.1e-4; with weights up to 2^8 and
+// the scales as they are it was 2.9e-2, with V of 0.1 5.6e-3).  P in two fp16 parts would take
+// off one of the two roundings and cost 5% (226 us against 214 for 32 x 32768 keys).
 // Tiles are copied in batches of up to BT of one unit (cp.async, a ring of
 // batches per warp); the lanes look their cache rows up side by side, so a tile's
 // share of the addressing is a shuffle and three multiply-adds.  They are
 // worked on two at a time.
 // Warps per CTA, tiles per batch, batches in the ring, CTAs per SM: measured best of
-// the configurations whose rings fit (D = 128: 2 CTAs x 3 batches and batches of 2
-// were 4-20% slower on 32 x 32768 keys).  Two column groups per warp (NG = 2, D = 128)
-// take the registers of two CTAs per SM.
+// the configurations whose rings fit, at D = 128 on 32 x 32768 keys (213 us): 2 CTAs x 3
+// batches took 226-238 then, 4 CTAs of 128 registers x batches of 2 267-289, one CTA of 14
+// warps 308; the tile loop unrolled by two 219 and more.  Two column groups per warp (NG = 2,
+// D = 128) take the registers of two CTAs per SM.
 template <int D, int NG>
 struct Cfg {
     static constexpr int NW = 4;
@@ -1542,15 +1547,15 @@ __global__ void __launch_bounds__(128, WideCfg<D>::CTAS_PER_SM) wide_kernel(cons
 }
 
 // ---------------------------------------------------------------- host side
-// Groups of 8 columns from which a unit of 64 columns pays.  Over 16 x 4096 keys of 4
-// heads, D = 128 / 256: a unit takes ~38 / 80 us and a group of 8 ~6.5 / 12.7, so six
-// groups cost what a unit does (64 columns: 58 against 67 us at D = 128, 109
-// against 116 at 256; 72, two units, would lose).
+// Groups of 8 columns beyond which a unit of 64 columns is taken.  16 x 4096 keys of 4 heads,
+// us with units of 64 columns against units of 8: 56 columns 51.9 / 51.7 at D = 128 and 103 /
+// 99 at 256, 64 columns 53.0 / 51.9 and 105 / 112: seven or eight groups cost what a unit does;
+// 72 columns, two units, would lose.
 constexpr int WIDE_GROUPS = 6;
 // Tiles per warp (at full capacity, with units of 8 columns) from which a unit of 16
 // columns is taken at D = 128: fewer, larger units cost parallelism first.  16 columns
-// on 16 sequences x 4 heads: 512 keys (2 tiles) 23 us against 20, 4096 (18) 31 and
-// 31, 32768 (144) 93 against 119.  Not with recorded weights, whose passes over the
+// on 16 sequences x 4 heads: 512 keys (2 tiles) 17.3 us against 14.7, 4096 (18) 25.2 and
+// 26.6, 32768 (144) 87 against 114.  Not with recorded weights, whose passes over the
 // scores outweigh it (24 columns, 32768 keys: 324 us against 253).
 constexpr double TWO_GROUP_MIN_TILES = 20.0;
 
@@ -1558,11 +1563,11 @@ constexpr double TWO_GROUP_MIN_TILES = 20.0;
 // resident at once and a warp has at most so many tiles (at full capacity).  us with
 // clusters against the split and merge, 4 query heads per KV head:
 //                          1 x 2 heads       1 x 8        4 x 8        8 x 8
-//   D = 128,  512 keys     7.0 /  8.0     7.6 /  8.4   7.2 /  9.5   8.0 / 10.9
-//            2048          7.4 / 10.9     8.0 / 11.7   9.3 / 12.3  12.1 / 14.2
-//            8192         11.9 / 18.3    12.1 / 15.4  17.5 / 18.9  28.5 / 25.1
-//   D = 256, 2048          9.7 / 12.5    10.1 / 14.0  13.2 / 14.4  18.5 / 19.1
-//            8192         16.4 / 22.6    16.6 / 17.5  26.5 / 24.4  44.5 / 36.9
+//   D = 128,  512 keys     7.1 /  8.0     7.2 /  8.1   7.0 /  9.1   7.8 / 10.3
+//            2048          7.8 / 10.5     7.8 / 11.1   9.2 / 11.9  11.9 / 13.1
+//            8192         11.8 / 18.3    11.9 / 14.9  17.1 / 16.7  28.2 / 23.8
+//   D = 256, 2048          9.9 / 12.4     9.9 / 13.6  12.8 / 13.7  17.8 / 16.9
+//            8192         16.3 / 22.4    16.4 / 16.5  25.8 / 22.5  44.4 / 36.4
 // Equal lengths; the split also balances ragged ones, so the limit is half of where
 // it breaks even.
 constexpr int CL_MAX_CTAS = 8;

@@ -93,7 +93,7 @@ def sink_case(D, tq, batch, n, spread, hkv=2, group=4, seed=0):
             torch.from_numpy(q.astype(np.float16)).cuda(), scale)
 
 
-@pytest.mark.parametrize("sigma", [1.0, 0.02, 1e-3])
+@pytest.mark.parametrize("sigma", [2e4, 1.0, 0.02, 1e-3, 3e-5])
 @pytest.mark.parametrize("D,tq,batch,n", PLANS)
 def test_sink_before_many_keys(D, tq, batch, n, sigma):
     c, q, scale = sink_case(D, tq, batch, n, sigma)
