@@ -15,7 +15,10 @@ from .binding import (FaDecodeError, fa_append_kv, fa_append_kv_ring, fa_decode_
                       fa_quantize_v_int8, load,
                       fa_append_kv_int4, fa_gather_kv_int4, fa_decode_int4,
                       fa_decode_int4_workspace_size, alloc_workspace_int4, fa_decode_weights,
-                      fa_decode_weights_workspace_size, alloc_workspace_weights, fa_evict_kv)
+                      fa_decode_weights_workspace_size, alloc_workspace_weights, fa_evict_kv,
+                      fa_decode_sinks, fa_decode_sinks_workspace_size, alloc_workspace_sinks,
+                      fa_prefill, fa_prefill_workspace_size, alloc_workspace_prefill,
+                      fa_rope_table, fa_rope, fa_rope_append_kv)
 
 __all__ = ["fa_decode", "fa_decode_batch_invariant", "fa_decode_batch_invariant_workspace_size",
            "fa_decode_multi_batch_invariant", "fa_decode_multi_batch_invariant_workspace_size",
@@ -24,4 +27,7 @@ __all__ = ["fa_decode", "fa_decode_batch_invariant", "fa_decode_batch_invariant_
            "fa_decode_device_status", "fa_decode_profile_next", "alloc_workspace", "FaDecodeError", "load",
            "fa_append_kv_int4", "fa_gather_kv_int4", "fa_decode_int4",
            "fa_decode_int4_workspace_size", "alloc_workspace_int4", "fa_decode_weights",
-           "fa_decode_weights_workspace_size", "alloc_workspace_weights", "fa_evict_kv"]
+           "fa_decode_weights_workspace_size", "alloc_workspace_weights", "fa_evict_kv",
+           "fa_decode_sinks", "fa_decode_sinks_workspace_size", "alloc_workspace_sinks",
+           "fa_prefill", "fa_prefill_workspace_size", "alloc_workspace_prefill",
+           "fa_rope_table", "fa_rope", "fa_rope_append_kv"]

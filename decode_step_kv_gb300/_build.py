@@ -12,7 +12,8 @@ import subprocess
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
-SRCS = [os.path.join(CSRC, f) for f in ("fa_decode.cu", "fa_int4.cu", "fa_evict.cu")]
+SRCS = [os.path.join(CSRC, f) for f in ("fa_decode.cu", "fa_int4.cu", "fa_evict.cu",
+                                         "fa_rope.cu", "fa_prefill.cu")]
 HDRS = [os.path.join(ROOT, "include", "fa_decode.h"), os.path.join(CSRC, "fa_common.cuh")]
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libfa_decode.so")

@@ -104,6 +104,26 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
             lib.fa_evict_kv.argtypes = [P, P, P, P, P, P, P, P, P, i32, i32, i32, i32, i32, i32,
                                         i32, i32, i32, P]
             lib.fa_evict_kv.restype = i32
+            lib.fa_decode_sinks.argtypes = [P, P, P, P, P, P, i32, i32, i32, i32, f32, P, i32, P,
+                                            i32, i32, i32, i32, P, sz, P]
+            lib.fa_decode_sinks.restype = i32
+            lib.fa_decode_sinks_workspace_size.argtypes = [i32] * 7
+            lib.fa_decode_sinks_workspace_size.restype = sz
+            lib.fa_prefill.argtypes = [P, P, P, P, P, P, P, i32, i32, i32, f32, P, i32, P, i32,
+                                       i32, i32, i32, i32, P, sz, P]
+            lib.fa_prefill.restype = i32
+            lib.fa_prefill_workspace_size.argtypes = [i32] * 7
+            lib.fa_prefill_workspace_size.restype = sz
+            lib.fa_rope_freqs.argtypes = [i32, ctypes.c_double, i32, ctypes.c_double,
+                                          ctypes.c_double, P, P]
+            lib.fa_rope_freqs.restype = i32
+            lib.fa_rope.argtypes = [P, i32, P, i32, P, f32, P, P, i32, i32, f32, i64, i32, i32,
+                                    i64, i64, P]
+            lib.fa_rope.restype = i32
+            lib.fa_rope_append_kv.argtypes = [P, P, P, i32, i64, i64, i64, P, P, f32, P, i32, i32,
+                                              f32, P, P, P, P, P, P, P, P, i32, i32, i32, i32,
+                                              i32, i32, i32, i32, P]
+            lib.fa_rope_append_kv.restype = i32
             lib.fa_gather_kv_debug.argtypes = [P, i32, P, i32, i32, i32, i32, i32, i32, P, P]
             lib.fa_gather_kv_debug.restype = i32
             lib.fa_decode_device_status.argtypes = [ctypes.POINTER(ctypes.c_uint), P]
@@ -566,6 +586,182 @@ def fa_evict_kv(k_cache, v_cache, acc, block_table, seq_lens, new_lens, *, budge
         _take("new_lens", new_lens, torch.int32, (B,), dev),
         _take("kept", kept, torch.int32, (B, hkv, budget), dev), budget, n_sink, n_recent, B, hkv,
         D, page, blocks, total, _stream_ptr(stream, dev)))
+
+
+def _fp16_cache(name, k_cache, v_cache, v_scales, block_table, n_kv_heads, head_dim, batch, dev):
+    """Pointers (K, V, V's scales, table) and sizes (page, max_blocks, num_blocks) of a cache of
+    fp16 K and fp16 or int8 V."""
+    hkv, page, blocks, total, rows, _ = _cache_dims(name, k_cache, block_table, batch)
+    if hkv != n_kv_heads:
+        raise ValueError(f"{name}: the cache holds {hkv} heads")
+    row = (*rows, head_dim)
+    return ((_take("k_cache", k_cache, torch.float16, row, dev),
+             _take("v_cache", v_cache, torch.float16 if v_scales is None else torch.int8, row, dev),
+             _take("v_scales", v_scales, torch.float16, (*rows, head_dim // 32), dev)),
+            _take("block_table", block_table, torch.int32, None, dev), page, blocks, total)
+
+
+def fa_decode_sinks(q, k_cache, v_cache, v_scales, block_table, seq_lens, n_q_heads, n_kv_heads,
+                    head_dim, scale, window, out, *, n_sink, workspace=None, stream=None):
+    """Decode attention (q, out fp16 [B, Hq, D] or [B, Tq, Hq, D]) where each query sees the
+    last `window[b]` keys up to itself and the first `n_sink`.  The workspace is
+    ``alloc_workspace_sinks``'s."""
+    dev = _device()
+    B, tq, qp, op = _queries("fa_decode_sinks", q, out, n_q_heads, head_dim, dev)
+    c, bt, page, blocks, total = _fp16_cache("fa_decode_sinks", k_cache, v_cache, v_scales,
+                                             block_table, n_kv_heads, head_dim, B, dev)
+    ws, ws_bytes = _workspace(workspace, dev)
+    _check(load().fa_decode_sinks(
+        qp, *c, bt, _take("seq_lens", seq_lens, torch.int32, (B,), dev), tq, n_q_heads, n_kv_heads,
+        head_dim, scale, _take("window", window, torch.int32, (B,), dev), n_sink, op, B, page,
+        blocks, total, ws, ws_bytes, _stream_ptr(stream, dev)))
+
+
+def fa_decode_sinks_workspace_size(batch, n_queries, n_q_heads, n_kv_heads, head_dim, max_kv_len,
+                                   num_sms=0) -> int:
+    return int(load().fa_decode_sinks_workspace_size(batch, n_queries, n_q_heads, n_kv_heads,
+                                                     head_dim, max_kv_len, num_sms))
+
+
+def alloc_workspace_sinks(batch, n_queries, n_q_heads, n_kv_heads, head_dim, max_kv_len, *,
+                          device="cuda"):
+    """Device scratch for fa_decode_sinks."""
+    n = fa_decode_sinks_workspace_size(batch, n_queries, n_q_heads, n_kv_heads, head_dim,
+                                       max_kv_len)
+    return torch.empty(max(n, 16), dtype=torch.uint8, device=device)
+
+
+def fa_prefill(q, k_cache, v_cache, v_scales, block_table, starts, seq_lens, n_q_heads, n_kv_heads,
+               head_dim, scale, window, out, *, n_sink=0, workspace=None, stream=None):
+    """Causal attention of a chunk of new tokens per sequence over its cache: q, out fp16
+    [N, Hq, D], sequence b's rows starts[b] .. starts[b + 1] - 1 (starts None: one each), the
+    last of them at position seq_lens[b] - 1.  The new tokens' K and V are in the cache
+    already.  `window` and `n_sink` as in ``fa_decode_sinks``; v_scales must be None.  The
+    workspace is ``alloc_workspace_prefill``'s."""
+    dev = _device()
+    B = seq_lens.shape[0]
+    if len(q.shape) != 3 or q.shape[1] != n_q_heads or q.shape[2] != head_dim:
+        raise ValueError("fa_prefill: q must be [N, Hq, D]")
+    N = q.shape[0]
+    c, bt, page, blocks, total = _fp16_cache("fa_prefill", k_cache, v_cache, v_scales,
+                                             block_table, n_kv_heads, head_dim, B, dev)
+    ws, ws_bytes = _workspace(workspace, dev)
+    _check(load().fa_prefill(
+        _take("q", q, torch.float16, None, dev), *c, bt,
+        _take("starts", starts, torch.int32, (B + 1,), dev),
+        _take("seq_lens", seq_lens, torch.int32, (B,), dev), n_q_heads, n_kv_heads, head_dim,
+        scale, _take("window", window, torch.int32, (B,), dev), n_sink,
+        _take("out", out, torch.float16, q.shape, dev), B, N, page, blocks, total, ws, ws_bytes,
+        _stream_ptr(stream, dev)))
+
+
+def fa_prefill_workspace_size(batch, n_tokens, n_q_heads, n_kv_heads, head_dim, max_kv_len,
+                              num_sms=0) -> int:
+    return int(load().fa_prefill_workspace_size(batch, n_tokens, n_q_heads, n_kv_heads, head_dim,
+                                                max_kv_len, num_sms))
+
+
+def alloc_workspace_prefill(batch, n_tokens, n_q_heads, n_kv_heads, head_dim, max_kv_len, *,
+                            device="cuda"):
+    """Device scratch for fa_prefill."""
+    n = fa_prefill_workspace_size(batch, n_tokens, n_q_heads, n_kv_heads, head_dim, max_kv_len)
+    return torch.empty(max(n, 16), dtype=torch.uint8, device=device)
+
+
+_DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+_SCALINGS = {None: 0, "linear": 1, "ntk": 2, "yarn": 3}
+
+
+def fa_rope_table(rot_dim, base=10000.0, *, scaling=None, factor=1.0, original_len=0, device="cuda"):
+    """(table, magnitude) of a rotary embedding for ``fa_rope`` and ``fa_rope_append_kv``, made
+    once per model.  `scaling`: None, "linear", "ntk" or "yarn" (with the original context
+    length).  The table is int64 [rot_dim / 2] on `device`: turns per position, 2^64 to a turn."""
+    if scaling not in _SCALINGS:
+        raise ValueError(f"fa_rope_table: unknown scaling {scaling!r}")
+    freqs = (ctypes.c_uint64 * max(1, int(rot_dim) // 2))()
+    magnitude = ctypes.c_float(0.0)
+    _check(load().fa_rope_freqs(rot_dim, base, _SCALINGS[scaling], factor, original_len, freqs,
+                                ctypes.byref(magnitude)))
+    table = torch.frombuffer(bytearray(freqs), dtype=torch.int64)
+    return table.to(device), magnitude.value
+
+
+def _heads(name, t, dtype, dev, n=None, heads=None, head_dim=None):
+    """(pointer, token stride, N, H, D) of a tensor [N, H, D] whose tokens' rows may lie apart."""
+    if len(t.shape) != 3:
+        raise ValueError(f"{name} must be [tokens, heads, head_dim]")
+    N, H, D = t.shape
+    if (n is not None and N != n) or (heads is not None and H != heads) or \
+            (head_dim is not None and D != head_dim):
+        raise ValueError(f"{name} must have shape {(n, heads, head_dim)}, got {tuple(t.shape)}")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on the current CUDA device, got {t.device}")
+    if N and ((H > 1 and t.stride(1) != D) or t.stride(2) != 1):
+        raise ValueError(f"{name}: a token's heads must be contiguous")
+    return t.data_ptr(), t.stride(0) if N > 1 else H * D, N, H, D
+
+
+def _dtype(name, t):
+    if t.dtype not in _DTYPES:
+        raise ValueError(f"{name} must be fp32, fp16 or bf16, got {t.dtype}")
+    return _DTYPES[t.dtype]
+
+
+def _table(freqs, dev):
+    """(pointer, rot_dim) of a table of ``fa_rope_table``; None: no rotation."""
+    if freqs is None:
+        return None, 0
+    return _take("freqs", freqs, torch.int64, (freqs.numel(),), dev), 2 * freqs.numel()
+
+
+def fa_rope(x, positions, freqs, out, *, weight=None, eps=1e-6, interleaved=False, magnitude=1.0,
+            stream=None):
+    """RMS norm of every head (with `weight` [D]) and rotation to `positions` (int32 [N]) of x
+    [N, H, D] (fp32, fp16 or bf16; token rows may lie apart) into out [N, H, D] of any of these
+    types, or x itself.  `freqs`, `magnitude`: ``fa_rope_table``'s (freqs None: norm only)."""
+    dev = _device()
+    kind, out_kind = _dtype("x", x), _dtype("out", out)
+    xp, xs, N, H, D = _heads("x", x, x.dtype, dev)
+    op, os, *_ = _heads("out", out, out.dtype, dev, N, H, D)
+    fp, rot = _table(freqs, dev)
+    _check(load().fa_rope(
+        xp, kind, op, out_kind, _take("weight", weight, x.dtype, (D,), dev), eps,
+        _take("positions", positions, torch.int32, (N,), dev), fp, rot, int(interleaved),
+        magnitude, N, H, D, xs, os, _stream_ptr(stream, dev)))
+
+
+def fa_rope_append_kv(q, k, v, q_out, k_cache, v_cache, v_scales, block_table, starts, positions,
+                      freqs, *, q_weight=None, k_weight=None, eps=1e-6, interleaved=False,
+                      magnitude=1.0, rope_positions=None, stream=None):
+    """From a projection to attention in one pass: q [N, Hq, D] and k [N, Hkv, D] (fp32, fp16 or
+    bf16; token rows may lie apart) normed (`q_weight`, `k_weight` [D]) and rotated, q into q_out
+    (fp16 [N, Hq, D]; both None: no queries), k and v into the cache.  Sequence b's tokens are
+    rows starts[b] .. starts[b + 1] - 1 (starts None: one each), its first at cache index
+    positions[b], rotated to rope_positions[b] where that differs.  `freqs`, `magnitude`:
+    ``fa_rope_table``'s."""
+    dev = _device()
+    kind = _dtype("k", k)
+    B = positions.shape[0]
+    kp, ks, N, hkv, D = _heads("k", k, k.dtype, dev)
+    vp, vs, *_ = _heads("v", v, k.dtype, dev, N, hkv, D)
+    qp, qs, hq, qo = None, 0, 0, None
+    if q is not None:
+        qp, qs, _, hq, _ = _heads("q", q, k.dtype, dev, N, None, D)
+        if q_out is None:
+            raise ValueError("fa_rope_append_kv: q_out is required with q")
+        qo = _take("q_out", q_out, torch.float16, (N, hq, D), dev)
+    c, bt, page, blocks, total = _fp16_cache("fa_rope_append_kv", k_cache, v_cache, v_scales,
+                                             block_table, hkv, D, B, dev)
+    fp, rot = _table(freqs, dev)
+    _check(load().fa_rope_append_kv(
+        qp, kp, vp, kind, qs, ks, vs, _take("q_weight", q_weight, k.dtype, (D,), dev),
+        _take("k_weight", k_weight, k.dtype, (D,), dev), eps, fp, rot, int(interleaved),
+        magnitude, qo, *c, bt, _take("starts", starts, torch.int32, (B + 1,), dev),
+        _take("positions", positions, torch.int32, (B,), dev),
+        _take("rope_positions", rope_positions, torch.int32, (B,), dev), B, N, hq, hkv, D, page,
+        blocks, total, _stream_ptr(stream, dev)))
 
 
 def fa_gather_kv_debug(cache, row_bytes, block_table, b, n_kv_heads, page_size,

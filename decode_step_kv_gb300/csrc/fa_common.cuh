@@ -70,6 +70,7 @@ struct Params {
     long long cap16;  // recorded weights: capacity rounded up to whole tiles
     int lg_page;      // recorded weights: log2 of page_size, or -1
     int w_rounds;     // recorded weights: rounds of WEIGHT_KEYS keys per item
+    int sink;         // decode with sinks: first tokens that stay visible behind a window
 };
 
 // ------------------------------------------------------------ PTX wrappers
@@ -210,6 +211,25 @@ template <int TILE>
 __device__ __forceinline__ int tiles_in(int lo, int hi)
 {
     return hi > lo ? (hi - 1) / TILE - lo / TILE + 1 : 0;
+}
+
+// Decode with sinks: a unit's tiles are the ones that hold a sink and lie before
+// the attended range's first tile, then the range's own; a query attends the keys
+// below p.sink beside its window.  Tiles before the range:
+template <int TILE>
+__device__ __forceinline__ int sink_tiles(const Params &p, int lo)
+{
+    return min((p.sink + TILE - 1) / TILE, lo / TILE);
+}
+// A unit's tiles; with SK those of the sinks too (none when p.sink is 0).
+template <int TILE, bool SK>
+__device__ __forceinline__ int range_tiles(const Params &p, int lo, int hi)
+{
+    const int n = tiles_in<TILE>(lo, hi);
+    if constexpr (SK)
+        return n > 0 ? n + sink_tiles<TILE>(p, lo) : 0;
+    else
+        return n;
 }
 
 // Byte offset of token `tok` (a tile start) of (b, kv) in a cache whose rows
@@ -375,15 +395,19 @@ __device__ __forceinline__ long long seq_span(const Params &p, int n)
     return n > 0 ? (long long)(n + UNIT_COST) * p.U_b : 0;
 }
 
-struct Walk {
+template <bool SK>
+struct WalkOf {
     int b, j, k, n, lo, hi;   // sequence, unit in sequence, tile in unit, tiles per unit
     int c;                    // empty positions before each unit's tiles
+    int ns;                   // SK: the unit's first tiles that hold sinks
     long long P;              // flattened position of sequence b's first unit
 
     __device__ __forceinline__ void load(const Params &p)
     {
         attended_range(p, b, lo, hi, false);
-        n = tiles_in<TILE>(lo, hi);
+        n = range_tiles<TILE, SK>(p, lo, hi);
+        if constexpr (SK)
+            ns = sink_tiles<TILE>(p, lo);
     }
     // position at the first tile at or after flattened position t of
     // sequence b_ (whose first unit starts at P_)
@@ -416,7 +440,13 @@ struct Walk {
             load(p);
         } while (n == 0);
     }
-    __device__ __forceinline__ int tok() const { return (lo / TILE + k) * TILE; }
+    __device__ __forceinline__ int tok() const
+    {
+        if constexpr (SK)
+            return (k < ns ? k : lo / TILE + k - ns) * TILE;
+        else
+            return (lo / TILE + k) * TILE;
+    }
     __device__ __forceinline__ long long unit(const Params &p) const
     {
         return (long long)b * p.U_b + j;
@@ -428,12 +458,14 @@ struct Walk {
     }
     __device__ __forceinline__ long long pos() const { return unit_start() + k; }
 };
+using Walk = WalkOf<false>;
 
 // Warp-cooperative scan over the sequences: T = the flattened positions of
 // the step (tiles plus UNIT_COST per unit); when target >= 0 also the
 // sequence holding position `target` and that sequence's first position;
 // when want >= 0 also sequence want's first position and tile count.
 // Every lane returns the same values.
+template <bool SK = false>
 __device__ __forceinline__ long long flat_scan(const Params &p, long long target, int &b_at,
                                                long long &P_at, bool report = false,
                                                long long *pref = nullptr, int want = -1,
@@ -451,7 +483,7 @@ __device__ __forceinline__ long long flat_scan(const Params &p, long long target
         if (b < p.B) {
             int lo, hi;
             attended_range(p, b, lo, hi, report);
-            nt = tiles_in<TILE>(lo, hi);
+            nt = range_tiles<TILE, SK>(p, lo, hi);
             c = seq_span(p, nt);
         }
         long long x = c;
@@ -577,6 +609,7 @@ __device__ __forceinline__ int worker_of(long long t, long long T, int We)
 // Stream-K plan: worker w's flattened positions [t0, t1), with T and We of the
 // step and the sequence holding t0 (b_at) and its first position (P_at).
 // Warp-cooperative; false when the worker has nothing to do.
+template <bool SK = false>
 __device__ __forceinline__ bool stream_range(const Params &p, int w, long long &T, int &We,
                                              long long &t0, long long &t1, int &b_at,
                                              long long &P_at)
@@ -599,7 +632,7 @@ __device__ __forceinline__ bool stream_range(const Params &p, int w, long long &
             if (b < p.B) {
                 int lo, hi;
                 attended_range(p, b, lo, hi, w == 0);   // worker 0 reports clamped lengths
-                c[i] = seq_span(p, tiles_in<TILE>(lo, hi));
+                c[i] = seq_span(p, range_tiles<TILE, SK>(p, lo, hi));
             }
             x[i] = c[i];
 #pragma unroll
@@ -633,7 +666,7 @@ __device__ __forceinline__ bool stream_range(const Params &p, int w, long long &
         }
     } else {
         // worker 0 also publishes each sequence's flattened start for the merge
-        T = flat_scan(p, -1, b_at, P_at, w == 0, w == 0 ? p.pref : nullptr);
+        T = flat_scan<SK>(p, -1, b_at, P_at, w == 0, w == 0 ? p.pref : nullptr);
         if (T == 0)
             return false;
         We = workers_for(p, T);
@@ -641,7 +674,7 @@ __device__ __forceinline__ bool stream_range(const Params &p, int w, long long &
             return false;
         t0 = range_start(w, T, We);
         t1 = range_start(w + 1, T, We);
-        flat_scan(p, t0, b_at, P_at);
+        flat_scan<SK>(p, t0, b_at, P_at);
     }
     return true;
 }
@@ -769,7 +802,8 @@ __device__ __forceinline__ void merge_row(const Params &p, const long long row)
             if (wid == 0) {
                 int b_at, nb = 0;
                 long long P_at, Pb = 0;
-                const long long T = flat_scan(p, -1, b_at, P_at, false, nullptr, b, &Pb, &nb);
+                const long long T =
+                    flat_scan<true>(p, -1, b_at, P_at, false, nullptr, b, &Pb, &nb);
                 if (lane == 0) {
                     sh_T = T;
                     sh_P = Pb;
@@ -781,7 +815,7 @@ __device__ __forceinline__ void merge_row(const Params &p, const long long row)
         } else {
             int lo, hi;
             attended_range(p, b, lo, hi, false);
-            n = tiles_in<TILE>(lo, hi);
+            n = range_tiles<TILE, true>(p, lo, hi);
         }
         if (n == 0) {                             // uniform over the CTA
             zero_row();
@@ -954,11 +988,11 @@ __device__ __forceinline__ void merge_rows(const Params &p, const int cta)
     if (scan_here) {
         int b_at;
         long long P_at;
-        T = flat_scan(p, -1, b_at, P_at, false, nullptr, b, &P, &n);
+        T = flat_scan<true>(p, -1, b_at, P_at, false, nullptr, b, &P, &n);
     } else {
         int lo, hi;
         attended_range(p, b, lo, hi, false);
-        n = tiles_in<TILE>(lo, hi);
+        n = range_tiles<TILE, true>(p, lo, hi);
     }
     if (n == 0) {
 #pragma unroll
@@ -1315,6 +1349,23 @@ static cudaError_t take_status(unsigned int *v, cudaStream_t st)
 // the other translation units' take_status
 cudaError_t int4_take_status(unsigned int *v, cudaStream_t st);
 cudaError_t evict_take_status(unsigned int *v, cudaStream_t st);
+cudaError_t rope_take_status(unsigned int *v, cudaStream_t st);
+cudaError_t prefill_take_status(unsigned int *v, cudaStream_t st);
+
+// cuTensorMapEncodeTiled through the runtime's driver entry point (no -lcuda).
+[[maybe_unused]] static PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder()
+{
+    [[maybe_unused]] static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000,
+                                             cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            f = nullptr;
+        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+    }();
+    return fn;
+}
 
 static int device_sms(int *out)
 {

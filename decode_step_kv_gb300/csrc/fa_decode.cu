@@ -602,7 +602,8 @@ constexpr int CL_MAX_CTAS = 8;  // the portable maximum cluster size
 // WT: recorded weights -- the tile's scores go to the workspace for
 // add_weights (in the cluster plan each warp adds its own keys' after the fold),
 // whole units also write their log-sum-exp, and the output is fp16.
-template <int D, bool VI8, bool BI, int NG, bool CL = false, bool WT = false>
+// SK: the first p.sink tokens stay visible behind the window; the output is fp16.
+template <int D, bool VI8, bool BI, int NG, bool CL = false, bool WT = false, bool SK = false>
 __global__ void __launch_bounds__(Cfg<D, VI8, NG>::NW * 32, Cfg<D, VI8, NG>::CTAS_PER_SM)
     fa_stream_mma_kernel(const Params p, const __grid_constant__ CUtensorMap tmK,
                          const __grid_constant__ CUtensorMap tmV)
@@ -640,7 +641,7 @@ __global__ void __launch_bounds__(Cfg<D, VI8, NG>::NW * 32, Cfg<D, VI8, NG>::CTA
         cl_j = u % p.U_b;
         int lo, hi;
         attended_range(p, b_at, lo, hi, blockIdx.x % cs == 0 && threadIdx.x == 0);
-        cl_n = tiles_in<TILE>(lo, hi);
+        cl_n = range_tiles<TILE, SK>(p, lo, hi);
         const int R = cs * C::NW;
         const int r = (blockIdx.x % cs) * C::NW + warp;
         t0 = (long long)r * cl_n / R;
@@ -667,7 +668,7 @@ __global__ void __launch_bounds__(Cfg<D, VI8, NG>::NW * 32, Cfg<D, VI8, NG>::CTA
         } else {
             t1 = T;
         }
-    } else if (!stream_range(p, w, T, We, t0, t1, b_at, P_at)) {
+    } else if (!stream_range<SK>(p, w, T, We, t0, t1, b_at, P_at)) {
         return;
     }
     // [t0, t1): this worker's flattened positions; its tiles are the ones in
@@ -691,6 +692,7 @@ __global__ void __launch_bounds__(Cfg<D, VI8, NG>::NW * 32, Cfg<D, VI8, NG>::CTA
     __syncwarp();
 
     const uint64_t policy = evict_first_policy();
+    using Walk = WalkOf<SK>;
     Walk pw;                          // producer position (lane 0 issues)
     if (!CL || t1 > t0)
         pw.init(p, b_at, P_at, t0, (BI || CL) ? 0 : UNIT_COST);
@@ -700,6 +702,8 @@ __global__ void __launch_bounds__(Cfg<D, VI8, NG>::NW * 32, Cfg<D, VI8, NG>::CTA
         pw.k = pw.n = pw.c = 0;
         pw.lo = pw.hi = 0;
         pw.P = 0;
+        if constexpr (SK)
+            pw.ns = 0;
     }
     Walk cw = pw;                     // consumer position
 
@@ -852,6 +856,9 @@ __global__ void __launch_bounds__(Cfg<D, VI8, NG>::NW * 32, Cfg<D, VI8, NG>::CTA
         const int base = cw.tok();
         const int r0 = max(cw.lo - base, 0);
         const int r1 = min(cw.hi - base, TILE);
+        // attended tile rows: [r0, r1), and with sinks those below rs
+        const int rs = SK ? p.sink - base : 0;
+        auto row_live = [&](int row) { return row < r1 && (row >= r0 || (SK && row < rs)); };
         const bool block_ok = tile_row(p, cw.b, kv, base) >= 0;
         const uint32_t sK = ring + s * C::STAGE_BYTES;
         const uint32_t sV = VI8 ? (FA_I8_INPLACE ? sK : cvt) : sK + C::T_BYTES;
@@ -872,7 +879,7 @@ __global__ void __launch_bounds__(Cfg<D, VI8, NG>::NW * 32, Cfg<D, VI8, NG>::CTA
                     constexpr int NIT = TILE * CPR / 32;  // chunks per lane
                     constexpr int BAT = NIT < 4 ? NIT : 4;
                     const int row = lane % TILE;
-                    const bool live = row >= r0 && row < r1;
+                    const bool live = row_live(row);
 #pragma unroll
                     for (int k0 = 0; k0 < NIT; k0 += BAT) {
                         uint32_t w[BAT][4];
@@ -921,7 +928,7 @@ __global__ void __launch_bounds__(Cfg<D, VI8, NG>::NW * 32, Cfg<D, VI8, NG>::CTA
                         const int row = q % TILE;
                         const int cc = (q / TILE + row) % CPR;
                         uint32_t o[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
-                        if (row >= r0 && row < r1) {
+                        if (row_live(row)) {
                             uint32_t w0, w1, w2, w3;
                             unsigned short sb;
                             asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
@@ -953,12 +960,12 @@ __global__ void __launch_bounds__(Cfg<D, VI8, NG>::NW * 32, Cfg<D, VI8, NG>::CTA
             if constexpr (VI8) {
                 if constexpr (!FA_I8_INPLACE)
                     dequant_v();
-            } else if (r0 != 0 || r1 != TILE) {
+            } else if ((SK ? r0 > 0 && rs < min(r0, TILE) : r0 != 0) || r1 != TILE) {
                 // keys outside [r0, r1) hold other tokens' data: zero their V
                 // rows (a 128-byte row segment per box) so 0-weights stay 0
                 for (int ii = lane; ii < TILE * C::BOXES * 8; ii += 32) {
                     const int row = ii / (C::BOXES * 8);
-                    if (row < r0 || row >= r1) {
+                    if (!row_live(row)) {
                         const int rem = ii % (C::BOXES * 8);
                         const uint32_t a = sV + (rem >> 3) * C::BOX_BYTES + row * 128 +
                                            (rem & 7) * 16;
@@ -1023,10 +1030,13 @@ __global__ void __launch_bounds__(Cfg<D, VI8, NG>::NW * 32, Cfg<D, VI8, NG>::CTA
                 float *sc = sc4[gi];
                 // keys outside each column's own range (tile edges, and with
                 // several queries the causal and window limits) weigh nothing
-                sc[0] = (ka >= clo[gi][0] && ka < chi[gi][0]) ? sc[0] * p.c2 : -INFINITY;
-                sc[1] = (ka >= clo[gi][1] && ka < chi[gi][1]) ? sc[1] * p.c2 : -INFINITY;
-                sc[2] = (kb >= clo[gi][0] && kb < chi[gi][0]) ? sc[2] * p.c2 : -INFINITY;
-                sc[3] = (kb >= clo[gi][1] && kb < chi[gi][1]) ? sc[3] * p.c2 : -INFINITY;
+                auto sees = [&](int key, int c) {
+                    return (key >= clo[gi][c] || (SK && key < p.sink)) && key < chi[gi][c];
+                };
+                sc[0] = sees(ka, 0) ? sc[0] * p.c2 : -INFINITY;
+                sc[1] = sees(ka, 1) ? sc[1] * p.c2 : -INFINITY;
+                sc[2] = sees(kb, 0) ? sc[2] * p.c2 : -INFINITY;
+                sc[3] = sees(kb, 1) ? sc[3] * p.c2 : -INFINITY;
                 if constexpr (WT)
                     store_scores(p.ws_s + cw.unit(p) * p.cap16 * p.sh, p.sh, ka, kb,
                                  gi * GPH + 2 * t4, nh, sc4[gi]);
@@ -1149,7 +1159,7 @@ __global__ void __launch_bounds__(Cfg<D, VI8, NG>::NW * 32, Cfg<D, VI8, NG>::CTA
                     // the whole unit was ours: normalised output
                     const float i0 = l[gi][0] > 0.f ? 1.f / l[gi][0] : 0.f;
                     const float i1 = l[gi][1] > 0.f ? 1.f / l[gi][1] : 0.f;
-                    using OutT = typename std::conditional<WT, __half, float>::type;
+                    using OutT = typename std::conditional<WT || SK, __half, float>::type;
                     const long long w0 = ((long long)cw.b * tq + c0.j) * p.Hq + c0.h;
                     const long long w1 = ((long long)cw.b * tq + c1.j) * p.Hq + c1.h;
                     OutT *o0 = reinterpret_cast<OutT *>(p.out) + w0 * D;
@@ -1304,7 +1314,7 @@ __global__ void __launch_bounds__(Cfg<D, VI8, NG>::NW * 32, Cfg<D, VI8, NG>::CTA
                 fold(i0, std::integral_constant<int, 4>());
             const float inv = Lsum > 0.f ? 1.f / Lsum : 0.f;
             const Col cq = column(p, cl_j / p.n_hg, cl_j % p.n_hg, c, CPU);
-            using OutT = typename std::conditional<WT, __half, float>::type;
+            using OutT = typename std::conditional<WT || SK, __half, float>::type;
             OutT *dst = reinterpret_cast<OutT *>(p.out) +
                         (((long long)b_at * tq + cq.j) * p.Hq + cq.h) * D + lane * EPL2;
 #pragma unroll
@@ -1740,21 +1750,6 @@ static cudaError_t dispatch_gp(const Params &p, int gp, dim3 grid, cudaStream_t 
     }
 }
 
-// cuTensorMapEncodeTiled through the runtime's driver entry point (no -lcuda).
-static PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder()
-{
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-        void *f = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000,
-                                             cudaEnableDefault, &q) != cudaSuccess ||
-            q != cudaDriverEntryPointSuccess)
-            f = nullptr;
-        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-    }();
-    return fn;
-}
-
 // A K or V cache viewed as a 2-D fp16 tensor [rows][D], loaded in boxes of
 // 16 rows x 64 columns with the 128-byte swizzle.
 static int encode_kv_map(CUtensorMap *map, const void *base, long long rows, int D)
@@ -1775,7 +1770,7 @@ static int encode_kv_map(CUtensorMap *map, const void *base, long long rows, int
     return 0;
 }
 
-template <int D, bool VI8, bool BI, int NG = 1, bool WT = false>
+template <int D, bool VI8, bool BI, int NG = 1, bool WT = false, bool SK = false>
 static cudaError_t launch_mma(const Params &p, const CUtensorMap &tmK, const CUtensorMap &tmV,
                               dim3 grid, cudaStream_t st)
 {
@@ -1789,7 +1784,7 @@ static cudaError_t launch_mma(const Params &p, const CUtensorMap &tmK, const CUt
     {
         std::lock_guard<std::mutex> lock(mu);
         if (dev >= 64 || !done[dev]) {
-            e = cudaFuncSetAttribute(tc::fa_stream_mma_kernel<D, VI8, BI, NG, false, WT>,
+            e = cudaFuncSetAttribute(tc::fa_stream_mma_kernel<D, VI8, BI, NG, false, WT, SK>,
                                      cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
             if (e != cudaSuccess)
                 return e;
@@ -1797,7 +1792,7 @@ static cudaError_t launch_mma(const Params &p, const CUtensorMap &tmK, const CUt
                 done[dev] = true;
         }
     }
-    tc::fa_stream_mma_kernel<D, VI8, BI, NG, false, WT>
+    tc::fa_stream_mma_kernel<D, VI8, BI, NG, false, WT, SK>
         <<<grid, tc::Cfg<D, VI8, NG>::NW * 32, smem, st>>>(p, tmK, tmV);
     return cudaGetLastError();
 }
@@ -1817,7 +1812,7 @@ static cudaError_t launch_mma(const Params &p, const CUtensorMap &tmK, const CUt
 // Clusters of `cs` CTAs of the cluster-plan kernel that fit on the current
 // device at once (cudaOccupancyMaxActiveClusters; 0 if the query fails),
 // cached per device and cluster size.
-template <int D, bool VI8, bool WT = false>
+template <int D, bool VI8, bool WT = false, bool SK = false>
 static int cluster_capacity(int cs)
 {
     static std::mutex mu;
@@ -1832,7 +1827,7 @@ static int cluster_capacity(int cs)
         return cache[dev][ci];
     const int smem = tc::Smem<D, VI8, 1>::BYTES;
     int n = 0;
-    if (cudaFuncSetAttribute(tc::fa_stream_mma_kernel<D, VI8, false, 1, true, WT>,
+    if (cudaFuncSetAttribute(tc::fa_stream_mma_kernel<D, VI8, false, 1, true, WT, SK>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, smem) == cudaSuccess) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(cs * 64);
@@ -1845,7 +1840,7 @@ static int cluster_capacity(int cs)
         attr[0].val.clusterDim.z = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        if (cudaOccupancyMaxActiveClusters(&n, tc::fa_stream_mma_kernel<D, VI8, false, 1, true, WT>,
+        if (cudaOccupancyMaxActiveClusters(&n, tc::fa_stream_mma_kernel<D, VI8, false, 1, true, WT, SK>,
                                            &cfg) != cudaSuccess) {
             n = 0;
             cudaGetLastError();   // clear the error this refused query left (and only then)
@@ -1860,7 +1855,7 @@ static int cluster_capacity(int cs)
     return n;
 }
 
-template <int D, bool VI8, bool WT = false>
+template <int D, bool VI8, bool WT = false, bool SK = false>
 static cudaError_t launch_cluster(const Params &p, const CUtensorMap &tmK, const CUtensorMap &tmV,
                                   int units, cudaStream_t st)
 {
@@ -1876,7 +1871,7 @@ static cudaError_t launch_cluster(const Params &p, const CUtensorMap &tmK, const
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, tc::fa_stream_mma_kernel<D, VI8, false, 1, true, WT>, p,
+    cudaError_t e = cudaLaunchKernelEx(&cfg, tc::fa_stream_mma_kernel<D, VI8, false, 1, true, WT, SK>, p,
                                        tmK, tmV);
     return e == cudaSuccess ? cudaGetLastError() : e;
 }
@@ -1991,7 +1986,7 @@ static int decode_impl(const void *q, const void *k_cache, const void *v_cache,
                        int max_blocks_per_seq, int num_blocks, void *workspace,
                        size_t workspace_bytes, void *stream, bool ring, int tq,
                        int chunk = 0, const int32_t *slot_ids = nullptr, int n_slots = 0,
-                       float *acc = nullptr);
+                       float *acc = nullptr, int sink = -1);
 
 FA_API int fa_decode(const void *q, const void *k_cache, const void *v_cache,
                      const void *v_scales, const int32_t *block_table,
@@ -2187,7 +2182,7 @@ static int call_plan(int batch, int n_q_heads, int n_kv_heads, int D, long long 
         if (tq > 1 || chunk > 0 || weights)
             return fail(FA_ERR_LAYOUT, "fa_decode: caches of 2^31 rows or more are not "
                                        "supported with several queries, batch-invariant "
-                                       "splits or recorded weights");
+                                       "splits, recorded weights or sinks");
         path = Path::Simt;
     }
     if (tq > 1 || chunk > 0 || weights)
@@ -2205,8 +2200,10 @@ static int decode_impl(const void *q, const void *k_cache, const void *v_cache,
                        float scale, const int32_t *window, void *out, int batch, int page_size,
                        int max_blocks_per_seq, int num_blocks, void *workspace,
                        size_t workspace_bytes, void *stream, bool ring, int tq, int chunk,
-                       const int32_t *slot_ids, int n_slots, float *acc)
+                       const int32_t *slot_ids, int n_slots, float *acc, int sink)
 {
+    const bool sinks = sink >= 0;
+    const bool half_out = acc || sinks;
     g_err[0] = 0;
     if (head_dim != 128 && head_dim != 256)
         return fail(FA_ERR_HEAD_DIM, "fa_decode: head_dim %d not supported (128 or 256)", head_dim);
@@ -2256,7 +2253,7 @@ static int decode_impl(const void *q, const void *k_cache, const void *v_cache,
     const long long slots = slot_ids ? (long long)n_slots : (long long)batch;
     // aliasing: out against every input range we can size
     const size_t out_bytes = (size_t)batch * tq * n_q_heads * D *
-                             (acc ? sizeof(__half) : sizeof(float));
+                             (half_out ? sizeof(__half) : sizeof(float));
     const size_t rows = paged ? (size_t)num_blocks * page_size : (size_t)slots * cap;
     const size_t kv_rows = rows * n_kv_heads;
     if (overlaps(out, out_bytes, q, (size_t)batch * tq * n_q_heads * D * 2) ||
@@ -2287,7 +2284,7 @@ static int decode_impl(const void *q, const void *k_cache, const void *v_cache,
     Plan pl;
     size_t need = 0;
     int rc = call_plan(batch, n_q_heads, n_kv_heads, D, cap, vi8, ring, tq, chunk,
-                       kv_rows_total, &sms, &pl, &need, acc != nullptr);
+                       kv_rows_total, &sms, &pl, &need, half_out);
     if (rc)
         return rc;
     WeightSpace wsp = {};
@@ -2358,6 +2355,7 @@ static int decode_impl(const void *q, const void *k_cache, const void *v_cache,
     p.cpu = pl.cpu;
     p.slot = slot_ids;
     p.n_slots = static_cast<int>(slots);
+    p.sink = sinks ? sink : 0;
     if (acc) {
         p.acc = acc;
         p.lse = reinterpret_cast<float *>(static_cast<char *>(workspace) + wsp.lse);
@@ -2387,7 +2385,11 @@ static int decode_impl(const void *q, const void *k_cache, const void *v_cache,
             if ((unit_tiles + (long long)cs * nw - 1) / ((long long)cs * nw) > max_tpw)
                 break;                       // smaller clusters give each warp more
             const int fit =
-                acc ? (D == 128 ? (vi8 ? cluster_capacity<128, true, true>(cs)
+                sinks ? (D == 128 ? (vi8 ? cluster_capacity<128, true, false, true>(cs)
+                                         : cluster_capacity<128, false, false, true>(cs))
+                                  : (vi8 ? cluster_capacity<256, true, false, true>(cs)
+                                         : cluster_capacity<256, false, false, true>(cs)))
+                : acc ? (D == 128 ? (vi8 ? cluster_capacity<128, true, true>(cs)
                                        : cluster_capacity<128, false, true>(cs))
                                 : (vi8 ? cluster_capacity<256, true, true>(cs)
                                        : cluster_capacity<256, false, true>(cs)))
@@ -2421,7 +2423,13 @@ static int decode_impl(const void *q, const void *k_cache, const void *v_cache,
             else if (const int rv = encode_kv_map(&tmV, v_cache, kv_rows_total, D))
                 return rv;
             const int units_all = batch * pl.units;
-            if (acc)
+            if (sinks)
+                e = D == 128
+                        ? (vi8 ? launch_cluster<128, true, false, true>(p, tmK, tmV, units_all, st)
+                               : launch_cluster<128, false, false, true>(p, tmK, tmV, units_all, st))
+                        : (vi8 ? launch_cluster<256, true, false, true>(p, tmK, tmV, units_all, st)
+                               : launch_cluster<256, false, false, true>(p, tmK, tmV, units_all, st));
+            else if (acc)
                 e = D == 128 ? (vi8 ? launch_cluster<128, true, true>(p, tmK, tmV, units_all, st)
                                     : launch_cluster<128, false, true>(p, tmK, tmV, units_all, st))
                              : (vi8 ? launch_cluster<256, true, true>(p, tmK, tmV, units_all, st)
@@ -2440,7 +2448,10 @@ static int decode_impl(const void *q, const void *k_cache, const void *v_cache,
         }
         if (vi8) {
             tmV = tmK;   // unused: int8 V arrives by plain bulk copies
-            if (acc)
+            if (sinks)
+                e = D == 128 ? launch_mma<128, true, false, 1, false, true>(p, tmK, tmV, grid, st)
+                             : launch_mma<256, true, false, 1, false, true>(p, tmK, tmV, grid, st);
+            else if (acc)
                 e = D == 128 ? launch_mma<128, true, false, 1, true>(p, tmK, tmV, grid, st)
                              : launch_mma<256, true, false, 1, true>(p, tmK, tmV, grid, st);
             else if (pl.chunk > 0)
@@ -2456,7 +2467,10 @@ static int decode_impl(const void *q, const void *k_cache, const void *v_cache,
             const int rv = encode_kv_map(&tmV, v_cache, kv_rows_total, D);
             if (rv)
                 return rv;
-            if (acc)
+            if (sinks)
+                e = D == 128 ? launch_mma<128, false, false, 1, false, true>(p, tmK, tmV, grid, st)
+                             : launch_mma<256, false, false, 1, false, true>(p, tmK, tmV, grid, st);
+            else if (acc)
                 e = D == 128 ? launch_mma<128, false, false, 1, true>(p, tmK, tmV, grid, st)
                              : launch_mma<256, false, false, 1, true>(p, tmK, tmV, grid, st);
             else if (pl.chunk > 0)
@@ -2502,7 +2516,7 @@ static int decode_impl(const void *q, const void *k_cache, const void *v_cache,
         attr[0].val.programmaticStreamSerializationAllowed = prof_end ? 0 : 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        if (acc)
+        if (half_out)
             e = D == 128 ? launch_merge_half<128>(p, sms, st) : launch_merge_half<256>(p, sms, st);
         else if (by_warp)
             e = D == 128 ? cudaLaunchKernelEx(&cfg, tc::fa_stream_merge_rows_kernel<128>, p)
@@ -2562,6 +2576,43 @@ FA_API size_t fa_decode_weights_workspace_size(int batch, int n_queries, int n_q
                           n_q_heads, pl.units, pl.sh, max_kv_len, &w))
             return 0;
         need = w.total > need ? w.total : need;
+    }
+    return need;
+}
+
+FA_API int fa_decode_sinks(const void *q, const void *k_cache, const void *v_cache,
+                           const void *v_scales, const int32_t *block_table,
+                           const int32_t *seq_lens, int n_queries, int n_q_heads, int n_kv_heads,
+                           int head_dim, float scale, const int32_t *window, int n_sink, void *out,
+                           int batch, int page_size, int max_blocks_per_seq, int num_blocks,
+                           void *workspace, size_t workspace_bytes, void *stream)
+{
+    g_err[0] = 0;
+    if (n_queries <= 0 || n_queries > 256)
+        return fail(FA_ERR_LAYOUT, "fa_decode_sinks: n_queries %d must be in [1, 256]", n_queries);
+    if (n_sink < 0 || n_sink > (1 << 30))
+        return fail(FA_ERR_LAYOUT, "fa_decode_sinks: n_sink %d must be in [0, 2^30]", n_sink);
+    return decode_impl(q, k_cache, v_cache, v_scales, block_table, seq_lens, n_q_heads,
+                       n_kv_heads, head_dim, scale, window, out, batch, page_size,
+                       max_blocks_per_seq, num_blocks, workspace, workspace_bytes, stream, false,
+                       n_queries, 0, nullptr, 0, nullptr, n_sink);
+}
+
+FA_API size_t fa_decode_sinks_workspace_size(int batch, int n_queries, int n_q_heads,
+                                             int n_kv_heads, int head_dim, int max_kv_len,
+                                             int num_sms)
+{
+    if (n_queries <= 0 || n_queries > 256 || batch <= 0 || n_q_heads <= 0 || n_kv_heads <= 0 ||
+        n_q_heads % n_kv_heads || (head_dim != 128 && head_dim != 256) || max_kv_len < 0)
+        return 0;
+    if (num_sms <= 0 && device_sms(&num_sms) != 0)
+        return 0;
+    size_t need = 0;
+    for (bool vi8 : {false, true}) {
+        const Plan pl = make_plan(Path::Mma, batch, n_q_heads, n_kv_heads, head_dim, max_kv_len,
+                                  num_sms, vi8, n_queries, 0, true);
+        const size_t n = plan_workspace(pl, batch, n_q_heads, head_dim);
+        need = n > need ? n : need;
     }
     return need;
 }
@@ -2835,17 +2886,21 @@ FA_API int fa_decode_device_status(unsigned int *status, void *stream)
     if (!status)
         return fail(FA_ERR_NULL, "fa_decode_device_status: null pointer");
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    unsigned int v = 0, v_int4 = 0, v_evict = 0;
+    unsigned int v = 0, v_int4 = 0, v_evict = 0, v_rope = 0, v_prefill = 0;
     cudaError_t e = take_status(&v, st);
     if (e == cudaSuccess)
         e = int4_take_status(&v_int4, st);
     if (e == cudaSuccess)
         e = evict_take_status(&v_evict, st);
     if (e == cudaSuccess)
+        e = rope_take_status(&v_rope, st);
+    if (e == cudaSuccess)
+        e = prefill_take_status(&v_prefill, st);
+    if (e == cudaSuccess)
         e = cudaStreamSynchronize(st);
     if (e != cudaSuccess)
         return fail(FA_ERR_CUDA, "fa_decode_device_status: %s", cudaGetErrorString(e));
-    *status = v | v_int4 | v_evict;
+    *status = v | v_int4 | v_evict | v_rope | v_prefill;
     return 0;
 }
 

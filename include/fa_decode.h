@@ -509,6 +509,175 @@ FA_API int fa_evict_kv(void *k_cache, void *v_cache, void *k_scales, void *v_sca
                        int num_blocks, void *stream);
 
 /*
+ * fa_decode_sinks -- decode attention with a sliding window and sinks: a query
+ * at position t attends, of the keys up to itself, the last window[b] and the
+ * first n_sink (the whole range when window[b] is 0, as in fa_decode).  The
+ * last n_queries tokens of each sequence are the queries, as in
+ * fa_decode_multi (n_queries in [1, 256]; 1 is the plain step).
+ *
+ * q       [batch][n_queries][n_q_heads][head_dim] fp16.
+ * out     the same shape, fp16 (fp32 accumulation, one rounding), written in
+ *         full, zero rows for empty ranges.
+ * n_sink  in [0, 2^30]; 0 leaves the window alone.
+ * workspace  fa_decode_sinks_workspace_size() bytes, 16-byte aligned.
+ * Only pages that hold a sink or a key of some query's window are read; the
+ * others may be unmapped.  Caches (fp16 K; fp16 or int8 V; paged or
+ * contiguous, below 2^31 rows), other arguments, streams, graph capture,
+ * status bits and errors as fa_decode_multi.
+ */
+FA_API int fa_decode_sinks(const void *q, const void *k_cache, const void *v_cache,
+                           const void *v_scales, const int32_t *block_table,
+                           const int32_t *seq_lens, int n_queries, int n_q_heads, int n_kv_heads,
+                           int head_dim, float scale, const int32_t *window, int n_sink, void *out,
+                           int batch, int page_size, int max_blocks_per_seq, int num_blocks,
+                           void *workspace, size_t workspace_bytes, void *stream);
+
+/* Scratch bytes for fa_decode_sinks (either V type).  Host-only; 0 for invalid
+ * sizes. */
+FA_API size_t fa_decode_sinks_workspace_size(int batch, int n_queries, int n_q_heads,
+                                             int n_kv_heads, int head_dim, int max_kv_len,
+                                             int num_sms);
+
+/*
+ * fa_prefill -- attention of a chunk of new tokens per sequence (a prompt, the
+ * next part of one, or a single token) over its cache, causal.  The new tokens
+ * are each sequence's last and are in the cache already.
+ *
+ * q       [n_tokens][n_q_heads][head_dim] fp16: the sequences' new tokens one
+ *         after another.
+ * starts  int32 [batch + 1] (device), not decreasing, within [0, n_tokens]:
+ *         sequence b's new tokens are rows starts[b] .. starts[b + 1] - 1 of q
+ *         and out.  Rows of no sequence are neither read nor written.  NULL:
+ *         one token per sequence (n_tokens == batch).
+ * seq_lens  int32 [batch]: tokens in each cache, the new ones included.  Row i
+ *         of sequence b's n_b sits at position seq_lens[b] - n_b + i and
+ *         attends the keys up to itself; with a window[b] > 0 the last
+ *         window[b] of them and the first n_sink.  A row at a negative
+ *         position gets zeros.
+ * v_scales  must be NULL: int8 V is refused (FA_ERR_LAYOUT).
+ * out     [n_tokens][n_q_heads][head_dim] fp16 (fp32 accumulation, one
+ *         rounding).
+ * workspace  fa_prefill_workspace_size() bytes, 16-byte aligned; contents need
+ *         no initialisation.  Calls that may overlap on the GPU must not share
+ *         one.
+ * K rows in range may hold anything where a row's mask hides them; V rows that
+ * some row of a sequence's chunk sees must be finite (a weight of 0 times an
+ * infinity is a NaN in the rows beside it).  V rows that none sees, and pages
+ * that hold no key of any row, may hold anything, the latter be unmapped.
+ * Caches (fp16, paged or contiguous, below 2^31 rows), block_table, sizes,
+ * status bits, streams, graph capture and errors as fa_decode; a tile of keys
+ * in an unmapped block is skipped.  batch = 0 or n_tokens = 0 is a no-op.
+ */
+FA_API int fa_prefill(const void *q, const void *k_cache, const void *v_cache,
+                      const void *v_scales, const int32_t *block_table, const int32_t *starts,
+                      const int32_t *seq_lens, int n_q_heads, int n_kv_heads, int head_dim,
+                      float scale, const int32_t *window, int n_sink, void *out, int batch,
+                      int n_tokens, int page_size, int max_blocks_per_seq, int num_blocks,
+                      void *workspace, size_t workspace_bytes, void *stream);
+
+/* Scratch bytes for fa_prefill.  Host-only; 0 for invalid sizes. */
+FA_API size_t fa_prefill_workspace_size(int batch, int n_tokens, int n_q_heads, int n_kv_heads,
+                                        int head_dim, int max_kv_len, int num_sms);
+
+/* Element types of fa_rope and fa_rope_append_kv. */
+#define FA_DTYPE_F32 0
+#define FA_DTYPE_F16 1
+#define FA_DTYPE_BF16 2
+
+/* Scalings of rotary positions for long contexts (fa_rope_freqs). */
+#define FA_ROPE_NONE 0
+#define FA_ROPE_LINEAR 1   /* every rate divided by factor */
+#define FA_ROPE_NTK 2      /* base * factor^(rot_dim / (rot_dim - 2)) */
+#define FA_ROPE_YARN 3     /* by parts: slow pairs divided by factor, fast ones kept */
+
+/*
+ * fa_rope_freqs -- the table of a rotary embedding, computed once per model on
+ * the host.  Pair j of rot_dim / 2 turns by base^(-2 j / rot_dim) radians per
+ * position, scaled for long contexts:
+ *   FA_ROPE_LINEAR  divided by factor (position interpolation);
+ *   FA_ROPE_NTK     with base * factor^(rot_dim / (rot_dim - 2));
+ *   FA_ROPE_YARN    pairs that turn more than 32 times in original_len
+ *                   positions keep their rate, those that turn less than once
+ *                   are divided by factor, a linear ramp in j between them.
+ * freqs      HOST array of rot_dim / 2: turns per position as a fraction of
+ *            2^64.  Copy it to the device for fa_rope.  Own rates: entry =
+ *            radians / (2 pi) * 2^64, modulo 2^64.
+ * magnitude  HOST: the factor on cos and sin, 0.1 ln(factor) + 1 for
+ *            FA_ROPE_YARN, else 1.
+ * base > 1 and factor >= 1, and original_len >= 1 for FA_ROPE_YARN (ignored
+ * otherwise), else FA_ERR_SCALE; rot_dim even, else FA_ERR_LAYOUT.
+ */
+FA_API int fa_rope_freqs(int rot_dim, double base, int scaling, double factor, double original_len,
+                         uint64_t *freqs, float *magnitude);
+
+/*
+ * fa_rope -- rotary positions of one array of heads, with each head's RMS norm
+ * before them: queries or keys on their way to attention, or keys on their way
+ * to fa_append_kv, its ring and slot forms and fa_append_kv_int4 (as fp32).
+ *
+ *     y = x * rsqrt(mean(x^2) + eps) * weight     (weight NULL: y = x)
+ *     (y_a, y_b) -> magnitude * (y_a cos - y_b sin, y_a sin + y_b cos)
+ *
+ * for pair j < rot_dim / 2: elements (j, j + rot_dim / 2), or (2 j, 2 j + 1)
+ * when interleaved; elements from rot_dim on are only normed.  fp32 inside,
+ * one rounding at the end.
+ *
+ * x          [n_tokens][n_heads][head_dim] of dtype (FA_DTYPE_*), token rows
+ *            x_stride elements apart; out the same of out_dtype, out_stride
+ *            apart.  out may be x itself (same type and stride); no other
+ *            overlap (FA_ERR_ALIAS).
+ * weight     [head_dim] of dtype, or NULL.
+ * positions  int32 [n_tokens] (device); any value; may be NULL when rot_dim
+ *            is 0.
+ * freqs      [rot_dim / 2] (device) of fa_rope_freqs, 8-byte aligned.
+ * rot_dim    a multiple of 16 in [0, head_dim]; 0 only norms.
+ * head_dim 128 or 256.  x, out, weight and every token row are 16-byte
+ * aligned (else FA_ERR_ALIGN).  n_tokens = 0 is a no-op.
+ */
+FA_API int fa_rope(const void *x, int dtype, void *out, int out_dtype, const void *weight,
+                   float eps, const int32_t *positions, const uint64_t *freqs, int rot_dim,
+                   int interleaved, float magnitude, long long n_tokens, int n_heads, int head_dim,
+                   long long x_stride, long long out_stride, void *stream);
+
+/*
+ * fa_rope_append_kv -- everything between a projection and attention, in one
+ * pass: q and k normed (with their weights) and rotated as by fa_rope, q
+ * handed on as fp16, k and v written to the cache.
+ *
+ * q, k, v    [n_tokens][heads][head_dim] of dtype, token rows q_stride,
+ *            k_stride, v_stride elements apart (the three parts of one
+ *            projection's output, for example).  n_q_heads = 0: no queries.
+ * starts     int32 [batch + 1] (device) as fa_prefill's: sequence b's new
+ *            tokens are rows starts[b] .. starts[b + 1] - 1.  Rows of no
+ *            sequence are left alone.  NULL: one token per sequence.
+ * positions  int32 [batch] (device): the cache token index of each sequence's
+ *            first new row; row i goes to positions[b] + i.
+ * rope_positions  int32 [batch] (device): the position that the first new row
+ *            is rotated to, where it is not its cache index (a cache cut by
+ *            fa_evict_kv keeps its rows' positions); NULL: positions.
+ * q_out      [n_tokens][n_q_heads][head_dim] fp16, contiguous.
+ * caches     fp16 K; V fp16 (v_scales NULL: rounded to nearest even) or int8
+ *            with the codec of fa_quantize_v_int8, in fa_decode's layouts,
+ *            paged or contiguous.
+ * A row outside the cache (every row, when positions[b] is negative) is not
+ * stored and sets FA_STATUS_POS_RANGE; one in an unmapped block is not stored
+ * and sets FA_STATUS_BAD_BLOCK; its q is rotated all the same.  No other byte
+ * of the cache changes.  Two rows of one call that name the same cache row
+ * race.  Outputs must overlap neither an input nor each other (FA_ERR_ALIAS).
+ * Alignments as fa_rope; the caches and q_out 16-byte.  n_tokens = 0 or
+ * batch = 0 is a no-op.
+ */
+FA_API int fa_rope_append_kv(const void *q, const void *k, const void *v, int dtype,
+                             long long q_stride, long long k_stride, long long v_stride,
+                             const void *q_weight, const void *k_weight, float eps,
+                             const uint64_t *freqs, int rot_dim, int interleaved, float magnitude,
+                             void *q_out, void *k_cache, void *v_cache, void *v_scales,
+                             const int32_t *block_table, const int32_t *starts,
+                             const int32_t *positions, const int32_t *rope_positions, int batch,
+                             int n_tokens, int n_q_heads, int n_kv_heads, int head_dim,
+                             int page_size, int max_blocks_per_seq, int num_blocks, void *stream);
+
+/*
  * fa_gather_kv_debug -- copy sequence b's first n_tokens cache rows, through
  * the same page-address path fa_decode's loader uses, into dense
  * [n_kv_heads][n_tokens][row_bytes] (device).  row_bytes = 2*head_dim for K
