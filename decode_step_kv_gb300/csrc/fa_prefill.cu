@@ -2,82 +2,1021 @@
 // cache: row (token i of sequence b, query head h) at position
 // at = L_b - n_b + i sees the keys t <= at and, with a window W, of those the
 // last W and the first n_sink.
+//
+//     O = sum_t 2^(c2 q.k_t - m) v_t / sum_t 2^(c2 q.k_t - m),  c2 = scale log2(e)
+//
+// Rows.  The G query heads of a KV head share its keys, so a tile of 128 rows
+// holds floor(128 / G) tokens with their G heads; a unit of work is one KV head
+// of one row tile (two tiles of 128 rows at head_dim 128, one at 256) and walks
+// the keys its rows see in tiles of 128.
+//
+// Matrix products.  S = Q K^T and O += P V are tcgen05 products of 128 x 128 x
+// 16 steps: Q, K and V from shared memory (TMA, 128-byte swizzle), S and O in
+// TMEM, P written over S in TMEM as fp16.  One softmax thread owns a row: its
+// running maximum and sum never leave it.  O is rescaled only when a row's
+// maximum has grown by more than 2^8 (P then stays below 2^8 in fp16), so the
+// usual tile does not touch O.
+//
+// What bounds it: at 128 rows of one KV head a key tile costs 2 x 128 x 128 x
+// 128 x 2 operations for 64 KB of K and V, 512 + 512 tensor cycles, so whole
+// prompts are bound by the tensor pipe and chunks of few rows by HBM.  With two
+// row tiles (head_dim 128) the products of one run while the other's softmax
+// does; with one, S is double-buffered and the next tile's Q K^T runs meanwhile.
+//
+// Work over the GPU.  A one-CTA kernel lists the units' tiles as positions of
+// one axis (as the decode plan: UNIT_COST positions per unit beside its tiles),
+// every CTA takes an equal stretch of it, and a unit that a stretch cuts leaves
+// fp32 partials that a merge kernel joins in a fixed order.
 #include "fa_common.cuh"
 
 namespace fa {
 namespace prefill {
 
-struct Args {
-    Params cache;            // paging: bt, Hkv, page_size, max_blocks, num_blocks, cap, B, seq_lens
-    const __half *q;
-    const __half *k, *v;
-    const int *starts, *window;
-    __half *out;
-    int tokens, hq, group, sink;
-    float c2;                // scale * log2(e)
+constexpr int BM = 128;             // rows of a stream
+constexpr int BN = 128;             // keys of a tile
+constexpr int STAGES = 5;           // ring of K / V parts of 128 keys x 128 dims
+constexpr int STAGE_BYTES = 32768;
+constexpr int SLAB = 16384;         // 128 rows x 64 columns
+constexpr int UNIT_COST = 2;        // positions charged for a unit's start
+constexpr int MIN_POS = 4;          // fewest positions a CTA is given
+constexpr int BITS = 8;             // key tiles whose unmapped groups are remembered
+
+template <int D>
+struct Cfg {
+    static constexpr int NS = D == 128 ? 2 : 1;             // streams of 128 rows
+    static constexpr int DS = D / 128;                      // ring stages per K or V tile
+    static constexpr int THREADS = 128 + 128 * NS;
+    static constexpr int Q_BYTES = NS * BM * D * 2;
+    static constexpr int BAR_OFF = Q_BYTES + STAGES * STAGE_BYTES;
+    static constexpr int SMEM = BAR_OFF + 512 + 1024;       // alignment slack
+    static constexpr int ROWS = NS * BM;                    // of a partial slot
+    static constexpr size_t SLOT_BYTES = (size_t)ROWS * D * sizeof(float);
 };
 
-// A warp per (token, query head) row, a key at a time.
-template <int D>
-__global__ void __launch_bounds__(256) rows_kernel(const Args p)
+// A row tile of a sequence.
+struct Ent {
+    int b, tok;                     // sequence; first row of q
+    int ntok, at;                   // tokens; position of the first
+    int lo, hi;                     // keys [lo, hi) some row's window holds
+    int n, ns, kt0;                 // key tiles; those before kt0 that hold sinks; first of [lo, hi)
+    int window;
+    int pad[2];
+};
+
+struct Args {
+    Params cache;                   // paging: bt, Hkv, page_size, max_blocks, num_blocks, cap, B, seq_lens
+    const int *starts, *window;
+    __half *out;
+    int tokens, hq, group, tpt, sink;
+    int lg_br;                      // log2 of the rows of a K / V box
+    int oob_row;                    // a cache row beyond the tensor: reads as zeros
+    float c2;
+    uint32_t idesc_qk;
+    int W;                          // CTAs of the main kernel
+    int max_ents;
+    // workspace
+    Ent *ents;
+    long long *pos;                 // [max_ents + 1] first position of each entry
+    int *ebase;                     // [B + 1] first entry of each sequence
+    int4 *split;                    // [W] the unit that CTA w leaves to its successors: entry, kv, CTAs
+    float *part;                    // [2 W] slots of [D / 4][ROWS] float4
+    float2 *ml;                     // [2 W][ROWS]
+};
+
+// ------------------------------------------------------------ the plan
+// Row tiles of every sequence and the positions of their units, by one CTA.
+constexpr int PLAN_THREADS = 1024;
+
+__device__ __forceinline__ long long block_scan(long long x, long long *sh, long long &total)
 {
-    constexpr int E = D / 32;
-    const int lane = threadIdx.x & 31;
-    const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-    if (row >= (long long)p.tokens * p.hq)
+    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+    long long s = x;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, s, off);
+        if (lane >= off)
+            s += y;
+    }
+    if (lane == 31)
+        sh[wid] = s;
+    __syncthreads();
+    if (wid == 0) {
+        long long v = sh[lane];
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, v, off);
+            if (lane >= off)
+                v += y;
+        }
+        sh[lane] = v;
+    }
+    __syncthreads();
+    const long long before = wid ? sh[wid - 1] : 0;
+    total = sh[31];
+    __syncthreads();
+    return before + s - x;
+}
+
+__global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const Args p, int per)
+{
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    __shared__ long long sh[32];
+    const int B = p.cache.B;
+    auto rows_of = [&](int b, int &first) {         // a sequence's rows, within q whatever starts says
+        first = p.starts ? min(max(p.starts[b], 0), p.tokens) : b;
+        const int end = p.starts ? min(max(p.starts[b + 1], first), p.tokens) : b + 1;
+        return end - first;
+    };
+    long long run = 0, total;
+    for (int b0 = 0; b0 < B; b0 += PLAN_THREADS) {
+        const int b = b0 + threadIdx.x;
+        int first;
+        const long long n = b < B ? (rows_of(b, first) + per - 1) / per : 0;
+        const long long at = block_scan(n, sh, total);
+        if (b < B)
+            p.ebase[b] = static_cast<int>(min(run + at, (long long)p.max_ents));
+        run += total;
+    }
+    const int E = static_cast<int>(min(run, (long long)p.max_ents));
+    if (threadIdx.x == 0)
+        p.ebase[B] = E;
+    __syncthreads();
+    run = 0;
+    for (int e0 = 0; e0 < E; e0 += PLAN_THREADS) {
+        const int e = e0 + threadIdx.x;
+        long long span = 0;
+        if (e < E) {
+            int lo = 0, hi = B;                     // ebase[lo] <= e < ebase[hi]
+            while (hi - lo > 1) {
+                const int m = (lo + hi) >> 1;
+                if (p.ebase[m] <= e)
+                    lo = m;
+                else
+                    hi = m;
+            }
+            const int b = lo, rt = e - p.ebase[b];
+            int first;
+            const int nb = rows_of(b, first);
+            long long len = p.cache.seq_lens[b];
+            if (len < 0 || len > p.cache.cap) {
+                flag(FA_STATUS_LEN_CLAMPED);
+                len = len < 0 ? 0 : p.cache.cap;
+            }
+            Ent x = {};
+            x.b = b;
+            x.tok = first + rt * per;
+            x.ntok = min(per, nb - rt * per);
+            x.at = static_cast<int>(len) - nb + rt * per;
+            x.window = p.window ? max(p.window[b], 0) : 0;
+            x.hi = max(x.at + x.ntok, 0);
+            const int at0 = max(x.at, 0);
+            x.lo = x.window > 0 && at0 >= x.window ? at0 - x.window + 1 : 0;
+            x.kt0 = x.lo / BN;
+            x.ns = x.hi > 0 ? min((p.sink + BN - 1) / BN, x.kt0) : 0;
+            x.n = x.hi > 0 ? x.ns + (x.hi - 1) / BN - x.kt0 + 1 : 0;
+            p.ents[e] = x;
+            span = (long long)p.cache.Hkv * (x.n + UNIT_COST);
+        }
+        const long long at = block_scan(span, sh, total);
+        if (e < E)
+            p.pos[e] = run + at;
+        run += total;
+    }
+    if (threadIdx.x == 0)
+        p.pos[E] = run;
+}
+
+// ------------------------------------------------------------ a CTA's stretch
+__device__ __forceinline__ int ctas_for(const Args &p, long long T)
+{
+    const long long w = T / MIN_POS;
+    return w < 1 ? 1 : static_cast<int>(w < p.W ? w : p.W);
+}
+
+struct Piece {
+    Ent x;
+    int e, kv, k0, k1;              // key tiles [k0, k1) of unit (e, kv)
+    int slot;                       // partial slot, -1: the whole unit
+    bool first_part;                // a partial from the unit's first tile
+    long long last;                 // position of the unit's last tile
+    __device__ __forceinline__ int key_tile(int k) const { return k < x.ns ? k : x.kt0 + k - x.ns; }
+};
+
+// The pieces of positions [t0, t1), in order.
+struct Pieces {
+    int e, kv, E, w;
+    long long t0, t1, us;           // us: position of the current unit's first tile
+    Ent x;
+    __device__ __forceinline__ void start(const Args &p, int e_, int w_, long long t0_, long long t1_)
+    {
+        e = e_;
+        w = w_;
+        t0 = t0_;
+        t1 = t1_;
+        E = p.ebase[p.cache.B];
+        x = p.ents[e];
+        const long long off = t0 - p.pos[e];
+        kv = static_cast<int>(off / (x.n + UNIT_COST));
+        us = p.pos[e] + (long long)kv * (x.n + UNIT_COST) + UNIT_COST;
+    }
+    __device__ __forceinline__ bool next(const Args &p, Piece &q)
+    {
+        while (e < E && us - UNIT_COST < t1) {
+            const long long k0 = t0 > us ? t0 - us : 0, k1 = t1 - us < x.n ? t1 - us : x.n;
+            const bool empty = x.n == 0 && us - UNIT_COST >= t0;   // zero rows
+            const bool some = empty || k1 > k0;
+            if (some) {
+                q.x = x;
+                q.e = e;
+                q.kv = kv;
+                q.k0 = static_cast<int>(k0);
+                q.k1 = empty ? 0 : static_cast<int>(k1);
+                const bool whole = k0 == 0 && q.k1 == x.n;
+                q.slot = whole ? -1 : (k0 > 0 ? 2 * w : 2 * w + 1);
+                q.first_part = !whole && k0 == 0;
+                q.last = us + x.n - 1;
+            }
+            us += x.n + UNIT_COST;
+            if (++kv == p.cache.Hkv) {
+                kv = 0;
+                if (++e < E)
+                    x = p.ents[e];
+                us = e < E ? p.pos[e] + UNIT_COST : us;
+            }
+            if (some)
+                return true;
+        }
+        return false;
+    }
+};
+
+// ------------------------------------------------------------ tcgen05 wrappers
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, int x, int y, int z,
+                                            uint32_t bar)
+{
+    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+                 " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+                 "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+                 : "memory");
+}
+
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
+                 " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+                 "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+                 : "memory");
+}
+
+__device__ __forceinline__ void mbar_arrive(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// Arrives on bar when the products issued so far by this thread are done.
+__device__ __forceinline__ void mma_commit(uint32_t bar)
+{
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+                 : "memory");
+}
+
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// A matrix in shared memory under the 128-byte swizzle.  K-major (Q, K): rows of
+// 128 bytes, 8-row groups 1024 bytes apart.  MN-major (V): a row is 64 columns of
+// one key, 8-key groups 1024 bytes apart, the next 64 columns a slab further.
+__device__ __forceinline__ uint64_t mat_desc(uint32_t addr, uint32_t lbo)
+{
+    return (uint64_t)((addr >> 4) & 0x3fff) | (uint64_t)(lbo >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
+           1ull << 46 | 2ull << 61;
+}
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+                 "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+                 : "memory");
+}
+
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+                 "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+                 : "memory");
+}
+
+#define FA_R8(r, i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), "=r"(r[i + 4]), "=r"(r[i + 5]), \
+                    "=r"(r[i + 6]), "=r"(r[i + 7])
+#define FA_W8(r, i) "r"(r[i]), "r"(r[i + 1]), "r"(r[i + 2]), "r"(r[i + 3]), "r"(r[i + 4]), "r"(r[i + 5]), \
+                    "r"(r[i + 6]), "r"(r[i + 7])
+
+// 32 columns of this warp's 32 TMEM lanes, one lane per thread.
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t *r)
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+                 "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, "
+                 "%28, %29, %30, %31}, [%32];"
+                 : FA_R8(r, 0), FA_R8(r, 8), FA_R8(r, 16), FA_R8(r, 24)
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t *r)
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+                 "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, "
+                 "%28, %29, %30, %31, %32};" ::"r"(addr),
+                 FA_W8(r, 0), FA_W8(r, 8), FA_W8(r, 16), FA_W8(r, 24)
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *r)
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+                 "%11, %12, %13, %14, %15, %16};" ::"r"(addr),
+                 FA_W8(r, 0), FA_W8(r, 8)
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// ------------------------------------------------------------ the main kernel
+// Warp 0 loads, warp 1 issues the products, warps 4-7 (and 8-11) own the rows of
+// stream 0 (and 1).  A piece whose tokens fill both streams runs them in turn
+// ("paired"); one with a single stream of rows alternates two S buffers instead.
+// The two forms have barriers of their own, so that a stream-1 warp that sits a
+// piece out misses none of its phases.
+struct Bars {
+    uint64_t full[STAGES], empty[STAGES];
+    uint64_t q_full, q_empty;
+    uint64_t s_pair[2], p_pair[2];      // S ready, P ready: of stream s
+    uint64_t s_one[2], p_one[2];        // S ready, P ready: of buffer j % 2
+    uint64_t pv_one;                    // single stream: a P V done
+    uint64_t o_full[2], o_empty[2];     // the unit's O complete; read out
+    uint64_t end;
+    uint32_t tmem;
+    uint32_t bits[BITS];                // per key tile: groups in unmapped blocks
+    int e0;
+};
+
+template <int D>
+__global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
+    attend_kernel(const Args p, const __grid_constant__ CUtensorMap tmQ,
+                  const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV)
+{
+    using C = Cfg<D>;
+    constexpr int NS = C::NS, DS = C::DS;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char *smem = reinterpret_cast<unsigned char *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    Bars &bars = *reinterpret_cast<Bars *>(smem + C::BAR_OFF);
+    static_assert(sizeof(Bars) <= 512, "barriers fit their space");
+    const uint32_t sQ = smem_u32(smem), ring = sQ + C::Q_BYTES;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int w = blockIdx.x;
+
+    if (warp == 0 && lane == 0) {
+        for (int i = 0; i < STAGES; ++i) {
+            mbar_init(smem_u32(&bars.full[i]), 1);
+            mbar_init(smem_u32(&bars.empty[i]), 1);
+        }
+        mbar_init(smem_u32(&bars.q_full), 1);
+        mbar_init(smem_u32(&bars.q_empty), 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&bars.s_pair[i]), 1);
+            mbar_init(smem_u32(&bars.p_pair[i]), 4);
+            mbar_init(smem_u32(&bars.s_one[i]), 1);
+            mbar_init(smem_u32(&bars.p_one[i]), 4);
+            mbar_init(smem_u32(&bars.o_full[i]), 1);
+            mbar_init(smem_u32(&bars.o_empty[i]), 4);
+        }
+        mbar_init(smem_u32(&bars.pv_one), 1);
+        mbar_init(smem_u32(&bars.end), 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmQ)) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmK)) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmV)) : "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                         smem_u32(&bars.tmem))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        fence_before();
+    }
+    wait_for_previous();
+    const int E = p.ebase[p.cache.B];
+    const long long T = E > 0 ? p.pos[E] : 0;
+    const int We = T > 0 ? ctas_for(p, T) : 0;
+    const bool working = w < We;
+    const long long t0 = working ? T * w / We : 0, t1 = working ? T * (w + 1) / We : 0;
+    if (warp == 0 && working) {
+        // the entry that holds position t0, 32 ways at a time
+        int lo = 0, hi = E;                         // pos[lo] <= t0 < pos[hi]
+        while (hi - lo > 1) {
+            const int step = (hi - lo + 31) / 32;
+            const int at = min(lo + step * lane, hi);
+            const unsigned le = __ballot_sync(0xffffffffu, at < hi && p.pos[at] <= t0);
+            const int last = 31 - __clz(le);
+            hi = min(lo + step * (last + 1), hi);
+            lo = lo + step * last;
+        }
+        if (lane == 0)
+            bars.e0 = lo;
+    }
+    if (threadIdx.x == 0)
+        p.split[w] = make_int4(-1, 0, 0, 0);
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = bars.tmem;
+    constexpr uint32_t O_COL = 256;
+
+    Pieces walk;
+    Piece pc;
+    bool ok = working;
+    if (working)
+        walk.start(p, bars.e0, w, t0, t1);
+    auto wait = [&](uint64_t &bar, uint32_t count) {      // the bar's phase number `count`
+        if (mbar_wait_warp(smem_u32(&bar), count & 1))
+            return true;
+        if (lane == 0)
+            flag(FA_STATUS_WAIT_TIMEOUT);
+        return false;
+    };
+    auto paired = [&](const Piece &q) { return NS == 2 && q.x.ntok > p.tpt; };
+
+    if (warp == 0) {
+        // ---------------------------------------------------------- loads
+        uint32_t it = 0, qn = 0, tiles = 0;     // stages filled, Q tiles loaded, key tiles so far
+        const int br = 1 << p.lg_br, groups = BN >> p.lg_br;
+        // one part (128 dims) of a K or V tile: the rows of its groups, from the lanes
+        auto part = [&](const CUtensorMap *map, int row, int ds) {
+            const uint32_t s = it % STAGES;
+            if (it >= STAGES && !wait(bars.empty[s], it / STAGES - 1))
+                return false;
+            const uint32_t bar = smem_u32(&bars.full[s]), dst = ring + s * STAGE_BYTES;
+            if (lane == 0)
+                mbar_expect_tx(bar, STAGE_BYTES);
+            __syncwarp();
+            if (lane < groups) {
+                tma_load(dst + lane * br * 128, map, ds * 128, row, bar);
+                tma_load(dst + SLAB + lane * br * 128, map, ds * 128 + 64, row, bar);
+            }
+            ++it;
+            return true;
+        };
+        while (ok && walk.next(p, pc)) {
+            const int n = pc.k1 - pc.k0;
+            if (n == 0)
+                continue;
+            // the cache row of this lane's group of key tile k; oob_row for groups no row sees
+            // and, reported, for unmapped blocks
+            auto rows = [&](int k, bool report) {
+                const int t = pc.key_tile(k) * BN + lane * br;
+                int row = p.oob_row;
+                bool bad = false;
+                if (lane < groups && t < pc.x.hi && (t + br > pc.x.lo || t < p.sink)) {
+                    const long long r = tc::tile_row(p.cache, pc.x.b, pc.kv, t);
+                    bad = r < 0;
+                    row = bad ? p.oob_row : static_cast<int>(r);
+                }
+                if (report) {
+                    const unsigned bits = __ballot_sync(0xffffffffu, bad);
+                    if (lane == 0) {
+                        if (bits)
+                            flag(FA_STATUS_BAD_BLOCK);
+                        bars.bits[tiles % BITS] = bits;
+                    }
+                    ++tiles;
+                    __syncwarp();
+                }
+                return row;
+            };
+            int prev = 0;                       // rows of the tile before: its V
+            for (int j = 0; ok && j <= n; ++j) {
+                int row = 0;
+                if (j < n) {
+                    row = rows(pc.k0 + j, true);
+                    for (int ds = 0; ok && ds < DS; ++ds)
+                        ok = part(&tmK, row, ds);
+                }
+                if (ok && j == 0) {
+                    const bool two = paired(pc);
+                    if (qn > 0)
+                        ok = wait(bars.q_empty, qn - 1);
+                    if (ok && lane == 0) {
+                        const uint32_t bar = smem_u32(&bars.q_full);
+                        const int box = p.group * p.tpt * 128;
+                        mbar_expect_tx(bar, (two ? 2 : 1) * (D / 64) * box);
+                        for (int s = 0; s < (two ? 2 : 1); ++s)
+                            for (int c = 0; c < D / 64; ++c)
+                                tma_load_3d(sQ + s * BM * D * 2 + c * SLAB, &tmQ, c * 64,
+                                            pc.kv * p.group, pc.x.tok + s * p.tpt, bar);
+                    }
+                    ++qn;
+                    __syncwarp();
+                }
+                if (ok && j > 0)
+                    for (int ds = 0; ok && ds < DS; ++ds)
+                        ok = part(&tmV, prev, ds);
+                prev = row;
+            }
+        }
+        // no copy is left in flight when the CTA ends
+        for (uint32_t i = it > STAGES ? it - STAGES : 0; i < it; ++i)
+            mbar_wait_warp(smem_u32(&bars.full[i % STAGES]), i / STAGES & 1);
+        if (qn > 0)
+            mbar_wait_warp(smem_u32(&bars.q_full), (qn - 1) & 1);
+    } else if (warp == 1) {
+        // ---------------------------------------------------------- products
+        uint32_t it = 0, qn = 0, pair_n = 0, on[2] = {0, 0}, one_n[2] = {0, 0};
+        constexpr uint32_t idesc_pv = 1u << 4 | 1u << 16 | (128u >> 3) << 17 | (128u >> 4) << 24;
+        // S buffer <- Q of stream s . K^T, from the stages at `at`
+        auto qk = [&](int s, int buf, uint32_t at) {
+            if (lane == 0) {
+#pragma unroll
+                for (int ds = 0; ds < DS; ++ds) {
+                    const uint32_t k = ring + (at + ds) % STAGES * STAGE_BYTES;
+                    const uint32_t q = sQ + s * BM * D * 2 + ds * 2 * SLAB;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const uint32_t off = (i / 4) * SLAB + (i % 4) * 32;
+                        mma_ss(tmem + buf * 128, mat_desc(q + off, 16), mat_desc(k + off, 16), p.idesc_qk,
+                               ds > 0 || i > 0);
+                    }
+                }
+            }
+        };
+        // O of stream s (+)= P in buffer buf . V
+        auto pv = [&](int s, int buf, uint32_t at, bool add) {
+            if (lane == 0) {
+#pragma unroll
+                for (int ds = 0; ds < DS; ++ds) {
+                    const uint32_t v = ring + (at + ds) % STAGES * STAGE_BYTES;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        mma_ts(tmem + O_COL + (s + ds) * 128, tmem + buf * 128 + i * 8,
+                               mat_desc(v + i * 2048, SLAB), idesc_pv, add || i > 0);
+                }
+            }
+        };
+        auto arrived = [&](uint32_t at) {           // the DS stages from `at` hold their part
+            for (int ds = 0; ds < DS; ++ds)
+                if (!wait(bars.full[(at + ds) % STAGES], (at + ds) / STAGES))
+                    return false;
+            return true;
+        };
+        auto release = [&](uint32_t at) {
+            if (lane == 0)
+                for (int ds = 0; ds < DS; ++ds)
+                    mma_commit(smem_u32(&bars.empty[(at + ds) % STAGES]));
+        };
+        auto commit = [&](uint64_t &bar) {
+            if (lane == 0)
+                mma_commit(smem_u32(&bar));
+        };
+        // V rows of key tile k that no row sees may hold anything: zero them, so that a
+        // weight of 0 leaves nothing
+        auto clean = [&](int k, uint32_t at) {
+            const int kb = pc.key_tile(k) * BN, hi = pc.x.hi - kb, lo = pc.x.lo - kb, sk = p.sink - kb;
+            if (hi >= BN && (lo <= 0 || sk >= min(lo, BN)))
+                return;
+            for (int i = lane; i < BN * 8; i += 32) {
+                const int r = i >> 3;
+                if (r < hi && (r >= lo || r < sk))
+                    continue;
+                for (int ds = 0; ds < DS; ++ds)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+                        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(
+                                         ring + (at + ds) % STAGES * STAGE_BYTES + c * SLAB + i * 16),
+                                     "r"(0)
+                                     : "memory");
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+        };
+        while (ok && walk.next(p, pc)) {
+            const int n = pc.k1 - pc.k0;
+            if (n == 0)
+                continue;
+            const bool two = paired(pc);
+            ok = wait(bars.q_full, qn);
+            ++qn;
+            if (NS == 2 && two) {
+                uint32_t at_v = 0;
+                for (int j = 0; ok && j <= n; ++j) {
+                    // stages in order: K0, K1, V0, K2, V1, ...
+                    const uint32_t at_k = it;
+                    if (j < n) {
+                        ok = arrived(at_k);
+                        it += DS;
+                    }
+                    if (ok && j > 0) {
+                        at_v = it;
+                        ok = arrived(at_v);
+                        it += DS;
+                        if (ok)
+                            clean(pc.k0 + j - 1, at_v);
+                    }
+                    for (int s = 0; ok && s < 2; ++s) {
+                        if (j > 0) {
+                            ok = wait(bars.p_pair[s], pair_n + j - 1);
+                            if (ok && j == 1 && on[s] > 0)
+                                ok = wait(bars.o_empty[s], on[s] - 1);
+                            if (!ok)
+                                break;
+                            fence_after();
+                            pv(s, s, at_v, j > 1);
+                        }
+                        if (j < n) {
+                            qk(s, s, at_k);
+                            commit(bars.s_pair[s]);
+                        } else {
+                            commit(bars.o_full[s]);
+                            ++on[s];
+                        }
+                    }
+                    if (ok) {
+                        if (j > 0)
+                            release(at_v);
+                        if (j < n)
+                            release(at_k);
+                        if (j == n - 1)
+                            commit(bars.q_empty);
+                    }
+                }
+                pair_n += n;
+            } else {
+                for (int j = 0; ok && j <= n; ++j) {
+                    if (j < n) {
+                        ok = arrived(it);
+                        if (ok) {
+                            qk(0, j & 1, it);
+                            commit(bars.s_one[j & 1]);
+                            release(it);
+                            if (j == n - 1)
+                                commit(bars.q_empty);
+                        }
+                        it += DS;
+                    }
+                    if (ok && j > 0) {
+                        const int i = j - 1;
+                        ok = arrived(it);
+                        if (ok)
+                            clean(pc.k0 + i, it);
+                        if (ok)
+                            ok = wait(bars.p_one[i & 1], one_n[i & 1] + i / 2);
+                        if (ok && i == 0 && on[0] > 0)
+                            ok = wait(bars.o_empty[0], on[0] - 1);
+                        if (ok) {
+                            fence_after();
+                            pv(0, i & 1, it, i > 0);
+                            commit(bars.pv_one);
+                            release(it);
+                        }
+                        it += DS;
+                    }
+                }
+                one_n[0] += (n + 1) / 2;
+                one_n[1] += n / 2;
+                if (ok) {
+                    commit(bars.o_full[0]);
+                    ++on[0];
+                }
+            }
+        }
+        // no product is left running when the TMEM goes back
+        commit(bars.end);
+        mbar_wait_warp(smem_u32(&bars.end), 0);
+    } else if (warp >= 4) {
+        // ---------------------------------------------------------- softmax
+        const int s = (warp - 4) >> 2;              // stream
+        const int r = threadIdx.x & 127;            // row of the stream
+        const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);
+        uint32_t tiles = 0, pair_n = 0, on = 0, one_n[2] = {0, 0}, pv_n = 0;
+        while (ok && walk.next(p, pc)) {
+            const int n = pc.k1 - pc.k0;
+            const bool two = paired(pc);
+            const int i_tok = s * p.tpt + r / p.group;
+            const bool live = r < p.tpt * p.group && i_tok < pc.x.ntok;
+            const int at = pc.x.at + i_tok;
+            float m = -INFINITY, l = 0.f;
+            if (s == 0 || two) {
+                // positions of this stream's first and last row
+                const int at_lo = pc.x.at + s * p.tpt;
+                const int at_hi = pc.x.at + min((s + 1) * p.tpt, pc.x.ntok) - 1;
+                for (int j = 0; ok && j < n; ++j) {
+                    const int buf = two ? s : j & 1;
+                    ok = two ? wait(bars.s_pair[s], pair_n + j) : wait(bars.s_one[buf], one_n[buf] + j / 2);
+                    if (!ok)
+                        break;
+                    fence_after();
+                    const int kb = pc.key_tile(pc.k0 + j) * BN;
+                    const uint32_t bits = *reinterpret_cast<volatile uint32_t *>(&bars.bits[(tiles + j) % BITS]);
+                    const bool edge = kb + BN - 1 > at_lo || bits ||
+                                      (pc.x.window > 0 && kb <= at_hi - pc.x.window && kb + BN > p.sink);
+                    const int hi = at - kb, lo = pc.x.window > 0 ? hi - pc.x.window + 1 : -1;
+                    const int sk = p.sink - kb;
+                    // S goes by twice, 32 columns at a time (the next ones on their way
+                    // meanwhile): once for the maximum, once for the weights.  Held in
+                    // registers in between, 128 values beside the walk's state spill
+                    auto passes = [&](auto use) {
+                        uint32_t x[2][32];
+                        tmem_ld32(lanes + buf * 128, x[0]);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            if (c < 3)
+                                tmem_ld32(lanes + buf * 128 + (c + 1) * 32, x[(c + 1) & 1]);
+                            if (edge) {
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) {
+                                    const int t = c * 32 + i;
+                                    if (t > hi || (t < lo && t >= sk) || (bits >> (t >> p.lg_br) & 1))
+                                        x[c & 1][i] = 0xff800000u;      // -infinity
+                                }
+                            }
+                            use(c, x[c & 1]);
+                            if (c < 3)
+                                tmem_ld_wait();
+                        }
+                    };
+                    float top = -INFINITY;
+                    passes([&](int, const uint32_t (&x)[32]) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            top = fmaxf(top, __uint_as_float(x[i]));
+                    });
+                    top *= p.c2;
+                    const bool grow = top > m + 8.f;        // also from -infinity
+                    if (__any_sync(0xffffffffu, grow)) {
+                        const float m1 = fmaxf(m, top);
+                        const float a = ex2(m - (m1 == -INFINITY ? 0.f : m1));
+                        m = m1;
+                        l *= a;
+                        if (j > 0) {
+                            // the P V before must have landed (paired: it came before this S)
+                            if (!two) {
+                                ok = wait(bars.pv_one, pv_n + j - 1);
+                                if (!ok)
+                                    break;
+                                fence_after();
+                            }
+#pragma unroll
+                            for (int c = 0; c < D / 32; ++c) {
+                                uint32_t o[32];
+                                const uint32_t col = lanes + O_COL + s * 128 + c * 32;
+                                tmem_ld32(col, o);
+                                tmem_ld_wait();
+#pragma unroll
+                                for (int i = 0; i < 32; ++i)
+                                    o[i] = __float_as_uint(__uint_as_float(o[i]) * a);
+                                tmem_st32(col, o);
+                            }
+                        }
+                    }
+                    const float ref = m == -INFINITY ? 0.f : m;
+                    float sum = 0.f;
+                    passes([&](int c, const uint32_t (&x)[32]) {
+                        uint32_t h[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const float a = ex2_ftz(fmaf(__uint_as_float(x[2 * i]), p.c2, -ref));
+                            const float b = ex2_ftz(fmaf(__uint_as_float(x[2 * i + 1]), p.c2, -ref));
+                            sum += a + b;
+                            h[i] = tc::pack_half2(a, b);
+                        }
+                        // over columns of S that have gone by
+                        tmem_st16(lanes + buf * 128 + c * 16, h);
+                    });
+                    l += sum;
+                    tmem_st_wait();
+                    fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(smem_u32(two ? &bars.p_pair[s] : &bars.p_one[buf]));
+                }
+                if (ok && n > 0) {
+                    ok = wait(bars.o_full[s], on);
+                    ++on;
+                }
+                if (!ok)
+                    break;
+                fence_after();
+                // ---- the unit's rows, or this piece's partial of them
+                const float inv = l > 0.f ? 1.f / l : 0.f;
+                __half *dst = p.out + ((long long)(pc.x.tok + i_tok) * p.hq + pc.kv * p.group + r % p.group) * D;
+                float4 *part = reinterpret_cast<float4 *>(p.part) + (size_t)max(pc.slot, 0) * (D / 4) * C::ROWS +
+                               s * BM + r;
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t o[32];
+                    if (n > 0) {
+                        tmem_ld32(lanes + O_COL + s * 128 + c * 32, o);
+                        tmem_ld_wait();
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            o[i] = 0;
+                    }
+                    if (!live)
+                        continue;
+                    if (pc.slot >= 0) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            part[(size_t)(c * 8 + i) * C::ROWS] =
+                                make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
+                                            __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            uint32_t h[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                h[e] = tc::pack_half2(__uint_as_float(o[8 * i + 2 * e]) * inv,
+                                                      __uint_as_float(o[8 * i + 2 * e + 1]) * inv);
+                            *reinterpret_cast<uint4 *>(dst + c * 32 + i * 8) = make_uint4(h[0], h[1], h[2], h[3]);
+                        }
+                    }
+                }
+                if (pc.slot >= 0 && live)
+                    p.ml[(size_t)pc.slot * C::ROWS + s * BM + r] = make_float2(m, l);
+                if (n > 0) {
+                    fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(smem_u32(&bars.o_empty[s]));
+                }
+                if (pc.first_part && s == 0 && r == 0)
+                    p.split[w] = make_int4(pc.e, pc.kv,
+                                           static_cast<int>(((pc.last + 1) * We - 1) / T) - w + 1, 0);
+            }
+            tiles += n;
+            if (two) {
+                pair_n += n;
+            } else {
+                one_n[0] += (n + 1) / 2;
+                one_n[1] += n / 2;
+                pv_n += n;
+            }
+        }
+    }
+    __syncthreads();
+    if (warp == 1) {
+        fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    }
+}
+
+// ------------------------------------------------------------ the merge
+// CTA (y, w): 16 columns of 256 / (D / 16)... of the unit that CTA w of the main
+// kernel began and left to the next ones: their partials in order, weighed by
+// 2^(m - M).
+template <int D>
+__global__ void __launch_bounds__(256) merge_kernel(const Args p)
+{
+    using C = Cfg<D>;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    wait_for_previous();
+    const int w = blockIdx.y;
+    const int4 u = p.split[w];
+    if (u.x < 0)
         return;
-    const int n = static_cast<int>(row / p.hq), h = static_cast<int>(row % p.hq);
-    int b = 0;
-    if (p.starts) {
-        if (n < p.starts[0] || n >= p.starts[p.cache.B])
-            return;
-        while (p.starts[b + 1] <= n)
-            ++b;
-    } else {
-        b = n;
-    }
-    const int first = p.starts ? p.starts[b] : b, count = p.starts ? p.starts[b + 1] - first : 1;
-    long long len = p.cache.seq_lens[b];
-    if (len < 0 || len > p.cache.cap) {
-        flag(FA_STATUS_LEN_CLAMPED);
-        len = len < 0 ? 0 : p.cache.cap;
-    }
-    const int at = static_cast<int>(len) - count + n - first;
-    const int w = p.window ? p.window[b] : 0;
-    float q[E], o[E] = {}, m = -INFINITY, l = 0.f;
+    const Ent x = p.ents[u.x];
+    const int idx = blockIdx.x * 256 + threadIdx.x;
+    const int row = idx % C::ROWS, c16 = idx / C::ROWS;
+    const int s = row / BM, r = row % BM;
+    const int i_tok = s * p.tpt + r / p.group;
+    if (r >= p.tpt * p.group || i_tok >= x.ntok)
+        return;
+    auto slot = [&](int i) { return (size_t)(i == 0 ? 2 * w + 1 : 2 * (w + i)); };
+    float M = -INFINITY;
+    for (int i = 0; i < u.z; ++i)
+        M = fmaxf(M, p.ml[slot(i) * C::ROWS + row].x);
+    float4 o[4] = {};
+    float L = 0.f;
+    for (int i = 0; i < u.z; ++i) {
+        const float2 v = p.ml[slot(i) * C::ROWS + row];
+        const float a = v.x == -INFINITY ? 0.f : ex2(v.x - M);
+        L = fmaf(v.y, a, L);
+        const float4 *src = reinterpret_cast<const float4 *>(p.part) + slot(i) * (D / 4) * C::ROWS +
+                            (size_t)c16 * 4 * C::ROWS + row;
 #pragma unroll
-    for (int e = 0; e < E; ++e)
-        q[e] = __half2float(p.q[row * D + lane + 32 * e]);
-    for (int t = 0; t <= at; ++t) {
-        if (w > 0 && t <= at - w && t >= p.sink) {
-            t = at - w;
-            continue;
+        for (int c = 0; c < 4; ++c) {
+            const float4 y = src[(size_t)c * C::ROWS];
+            o[c].x = fmaf(y.x, a, o[c].x);
+            o[c].y = fmaf(y.y, a, o[c].y);
+            o[c].z = fmaf(y.z, a, o[c].z);
+            o[c].w = fmaf(y.w, a, o[c].w);
         }
-        const long long r = row_offset(p.cache, b, h / p.group, t, 1);
-        if (r < 0) {
-            flag(FA_STATUS_BAD_BLOCK);
-            continue;
-        }
-        float s = 0.f;
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-            s = fmaf(q[e], __half2float(p.k[r * D + lane + 32 * e]), s);
-#pragma unroll
-        for (int x = 16; x >= 1; x >>= 1)
-            s += __shfl_xor_sync(0xffffffffu, s, x);
-        s *= p.c2;
-        const float top = fmaxf(m, s), ref = top == -INFINITY ? 0.f : top;
-        const float a = ex2(m - ref), x = ex2(s - ref);
-        m = top;
-        l = l * a + x;
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-            o[e] = o[e] * a + x * __half2float(p.v[r * D + lane + 32 * e]);
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = L > 0.f ? 1.f / L : 0.f;
+    __half *dst = p.out + ((long long)(x.tok + i_tok) * p.hq + u.y * p.group + r % p.group) * D + c16 * 16;
 #pragma unroll
-    for (int e = 0; e < E; ++e)
-        p.out[row * D + lane + 32 * e] = __float2half_rn(o[e] * inv);
+    for (int c = 0; c < 2; ++c)
+        *reinterpret_cast<uint4 *>(dst + 8 * c) =
+            make_uint4(tc::pack_half2(o[2 * c].x * inv, o[2 * c].y * inv),
+                       tc::pack_half2(o[2 * c].z * inv, o[2 * c].w * inv),
+                       tc::pack_half2(o[2 * c + 1].x * inv, o[2 * c + 1].y * inv),
+                       tc::pack_half2(o[2 * c + 1].z * inv, o[2 * c + 1].w * inv));
+}
+
+// Sizes of a call and the layout of its workspace.
+struct Space {
+    int tpt, per, max_ents, W;
+    size_t ents, pos, ebase, split, ml, part, total;    // offsets, and the bytes in all
+};
+
+static Space space_of(int batch, int n_tokens, int hq, int hkv, int D, long long cap, int sms)
+{
+    Space s = {};
+    const int ns = D == 128 ? Cfg<128>::NS : Cfg<256>::NS;
+    const int rows = D == 128 ? Cfg<128>::ROWS : Cfg<256>::ROWS;
+    const size_t slot = D == 128 ? Cfg<128>::SLOT_BYTES : Cfg<256>::SLOT_BYTES;
+    s.tpt = BM / (hq / hkv);
+    s.per = ns * s.tpt;
+    s.max_ents = n_tokens / s.per + (batch < n_tokens ? batch : n_tokens);
+    const double most = (double)s.max_ents * hkv * ((cap + BN - 1) / BN + UNIT_COST) / MIN_POS;
+    s.W = most < 1 ? 1 : most < sms ? static_cast<int>(most) : sms;
+    size_t at = 0;
+    auto take = [&](size_t n) {
+        const size_t here = at;
+        at += (n + 127) / 128 * 128;
+        return here;
+    };
+    s.ents = take((size_t)s.max_ents * sizeof(Ent));
+    s.pos = take(((size_t)s.max_ents + 1) * sizeof(long long));
+    s.ebase = take(((size_t)batch + 1) * sizeof(int));
+    s.split = take((size_t)s.W * sizeof(int4));
+    s.ml = take((size_t)2 * s.W * rows * sizeof(float2));
+    s.part = take((size_t)2 * s.W * slot);
+    s.total = at;
+    return s;
+}
+
+// [rows][D] of fp16 in boxes of `br` rows x 64 columns, 128-byte swizzle; q as
+// [tokens][heads][D] in boxes of tpt tokens x G heads x 64 columns.
+static int encode_map(CUtensorMap *map, const void *base, int rank, const cuuint64_t *dims,
+                      const cuuint64_t *strides, const cuuint32_t *box)
+{
+    auto enc = tensor_map_encoder();
+    if (!enc)
+        return fail(FA_ERR_CUDA, "fa_prefill: cuTensorMapEncodeTiled unavailable");
+    const cuuint32_t estr[3] = {1, 1, 1};
+    const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, rank, const_cast<void *>(base), dims,
+                           strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS)
+        return fail(FA_ERR_CUDA, "fa_prefill: cuTensorMapEncodeTiled failed (%d)", (int)r);
+    return 0;
+}
+
+template <int D>
+static cudaError_t launch(const Args &p, const CUtensorMap &tmQ, const CUtensorMap &tmK,
+                          const CUtensorMap &tmV, int per, cudaStream_t st)
+{
+    using C = Cfg<D>;
+    static std::mutex mu;
+    static bool done[64] = {false};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return e;
+    {
+        std::lock_guard<std::mutex> lock(mu);
+        if (dev >= 64 || !done[dev]) {
+            e = cudaFuncSetAttribute(attend_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+            if (e != cudaSuccess)
+                return e;
+            if (dev < 64)
+                done[dev] = true;
+        }
+    }
+    plan_kernel<<<1, PLAN_THREADS, 0, st>>>(p, per);
+    e = cudaGetLastError();
+    if (e != cudaSuccess)
+        return e;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cfg.gridDim = dim3(p.W);
+    cfg.blockDim = dim3(C::THREADS);
+    cfg.dynamicSmemBytes = C::SMEM;
+    e = cudaLaunchKernelEx(&cfg, attend_kernel<D>, p, tmQ, tmK, tmV);
+    if (e != cudaSuccess)
+        return e;
+    cfg.gridDim = dim3(C::ROWS * (D / 16) / 256, p.W);
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = 0;
+    e = cudaLaunchKernelEx(&cfg, merge_kernel<D>, p);
+    return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
 }  // namespace prefill
@@ -103,7 +1042,7 @@ FA_API size_t fa_prefill_workspace_size(int batch, int n_tokens, int n_q_heads, 
         return 0;
     if (num_sms <= 0 && device_sms(&num_sms) != 0)
         return 0;
-    return 16;
+    return space_of(batch, n_tokens, n_q_heads, n_kv_heads, head_dim, max_kv_len, num_sms).total;
 }
 
 FA_API int fa_prefill(const void *q, const void *k_cache, const void *v_cache,
@@ -150,10 +1089,11 @@ FA_API int fa_prefill(const void *q, const void *k_cache, const void *v_cache,
         !aligned_to(window, 4) || !aligned_to(starts, 4))
         return fail(FA_ERR_ALIGN, "fa_prefill: q, caches, out and workspace must be 16-byte, int32 "
                                   "arrays 4-byte aligned");
-    const size_t need = fa_prefill_workspace_size(batch, n_tokens, n_q_heads, n_kv_heads, D,
-                                                  static_cast<int>(cap), 0);
-    if (!need)
-        return fail(FA_ERR_WORKSPACE, "fa_prefill: no workspace size for these sizes");
+    int sms = 0;
+    if (const int rc = device_sms(&sms))
+        return rc;
+    const Space sp = space_of(batch, n_tokens, n_q_heads, n_kv_heads, D, cap, sms);
+    const size_t need = sp.total;
     if (!workspace || workspace_bytes < need)
         return fail(FA_ERR_WORKSPACE, "fa_prefill: workspace %zu bytes, need %zu", workspace_bytes,
                     need);
@@ -176,26 +1116,49 @@ FA_API int fa_prefill(const void *q, const void *k_cache, const void *v_cache,
     p.cache.max_blocks = max_blocks_per_seq;
     p.cache.num_blocks = num_blocks;
     p.cache.cap = cap;
-    p.q = static_cast<const __half *>(q);
-    p.k = static_cast<const __half *>(k_cache);
-    p.v = static_cast<const __half *>(v_cache);
     p.starts = starts;
     p.window = window;
     p.out = static_cast<__half *>(out);
     p.tokens = n_tokens;
     p.hq = n_q_heads;
     p.group = n_q_heads / n_kv_heads;
+    p.tpt = sp.tpt;
     p.sink = n_sink;
-    p.c2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
-    const long long ctas = ((long long)n_tokens * n_q_heads + 7) / 8;
-    if (ctas > 0x7fffffffll)
-        return fail(FA_ERR_LAYOUT, "fa_prefill: too many rows");
+    // boxes of as many rows as always lie together: the largest power of two in a page
+    const int br = paged ? (page_size & -page_size) < BN ? (page_size & -page_size) : BN : 64;
+    p.lg_br = log2_of(br);
+    p.oob_row = static_cast<int>(rows);
+    // a negative scale: the product negates Q; the running maximum wants c2 > 0, and 0
+    // weighs every key alike, as this does
+    const double c2 = fabs(static_cast<double>(scale)) * 1.4426950408889634;
+    p.c2 = c2 < 1e-37 ? 1e-37f : static_cast<float>(c2);
+    p.idesc_qk = 1u << 4 | (scale < 0.f ? 1u << 13 : 0u) | (BN >> 3) << 17 | (BM >> 4) << 24;
+    p.W = sp.W;
+    p.max_ents = sp.max_ents;
+    char *ws = static_cast<char *>(workspace);
+    p.ents = reinterpret_cast<Ent *>(ws + sp.ents);
+    p.pos = reinterpret_cast<long long *>(ws + sp.pos);
+    p.ebase = reinterpret_cast<int *>(ws + sp.ebase);
+    p.split = reinterpret_cast<int4 *>(ws + sp.split);
+    p.ml = reinterpret_cast<float2 *>(ws + sp.ml);
+    p.part = reinterpret_cast<float *>(ws + sp.part);
+    CUtensorMap tmQ, tmK, tmV;
+    const cuuint64_t qd[3] = {(cuuint64_t)D, (cuuint64_t)n_q_heads, (cuuint64_t)n_tokens};
+    const cuuint64_t qs[2] = {(cuuint64_t)D * 2, (cuuint64_t)n_q_heads * D * 2};
+    const cuuint32_t qb[3] = {64, (cuuint32_t)p.group, (cuuint32_t)p.tpt};
+    const cuuint64_t kd[2] = {(cuuint64_t)D, (cuuint64_t)rows};
+    const cuuint64_t ks[1] = {(cuuint64_t)D * 2};
+    const cuuint32_t kb[2] = {64, (cuuint32_t)br};
+    int rc = encode_map(&tmQ, q, 3, qd, qs, qb);
+    if (!rc)
+        rc = encode_map(&tmK, k_cache, 2, kd, ks, kb);
+    if (!rc)
+        rc = encode_map(&tmV, v_cache, 2, kd, ks, kb);
+    if (rc)
+        return rc;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (D == 128)
-        rows_kernel<128><<<(unsigned)ctas, 256, 0, st>>>(p);
-    else
-        rows_kernel<256><<<(unsigned)ctas, 256, 0, st>>>(p);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = D == 128 ? launch<128>(p, tmQ, tmK, tmV, sp.per, st)
+                                   : launch<256>(p, tmQ, tmK, tmV, sp.per, st);
     if (e != cudaSuccess)
         return fail(FA_ERR_CUDA, "fa_prefill: launch failed: %s", cudaGetErrorString(e));
     return 0;

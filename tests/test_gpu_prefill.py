@@ -110,6 +110,11 @@ def test_windows_and_sinks(D, window, sink):
                 window=[window, 0, window], sink=sink)
 
 
+@pytest.mark.parametrize("scale", [-0.09, 1e-20, 0.5])
+def test_scale_of_any_sign(scale):
+    run_prefill(Layout(2, 2, 200, True, page=16, seed=6), [200, 90], [40, 90], 8, 128, scale=scale)
+
+
 def test_far_pages_may_be_unmapped():
     """Pages behind a window that hold no sink are not looked up; those beyond the length neither."""
     lay = Layout(2, 1, 900, True, page=16, seed=8)
