@@ -198,52 +198,43 @@ struct Piece {
     int e, kv, k0, k1;              // key tiles [k0, k1) of unit (e, kv)
     int slot;                       // partial slot, -1: the whole unit
     bool first_part;                // a partial from the unit's first tile
-    long long last;                 // position of the unit's last tile
+    int last;                       // the unit's last tile, counted from the stretch's first position
     __device__ __forceinline__ int key_tile(int k) const { return k < x.ns ? k : x.kt0 + k - x.ns; }
 };
 
-// The pieces of positions [t0, t1), in order.
+// The pieces of a stretch of `len` positions, in order.
 struct Pieces {
-    int e, kv, E, w;
-    long long t0, t1, us;           // us: position of the current unit's first tile
-    Ent x;
-    __device__ __forceinline__ void start(const Args &p, int e_, int w_, long long t0_, long long t1_)
+    int e, kv, us, len;             // us: the current unit's first tile, counted from the stretch's start
+    __device__ __forceinline__ void start(const Args &p, int e_, long long t0, long long t1)
     {
         e = e_;
-        w = w_;
-        t0 = t0_;
-        t1 = t1_;
-        E = p.ebase[p.cache.B];
-        x = p.ents[e];
+        const int unit = p.ents[e].n + UNIT_COST;
         const long long off = t0 - p.pos[e];
-        kv = static_cast<int>(off / (x.n + UNIT_COST));
-        us = p.pos[e] + (long long)kv * (x.n + UNIT_COST) + UNIT_COST;
+        kv = static_cast<int>(off / unit);
+        us = static_cast<int>(kv * (long long)unit + UNIT_COST - off);
+        len = static_cast<int>(t1 - t0);
     }
     __device__ __forceinline__ bool next(const Args &p, Piece &q)
     {
-        while (e < E && us - UNIT_COST < t1) {
-            const long long k0 = t0 > us ? t0 - us : 0, k1 = t1 - us < x.n ? t1 - us : x.n;
-            const bool empty = x.n == 0 && us - UNIT_COST >= t0;   // zero rows
-            const bool some = empty || k1 > k0;
-            if (some) {
-                q.x = x;
-                q.e = e;
-                q.kv = kv;
-                q.k0 = static_cast<int>(k0);
-                q.k1 = empty ? 0 : static_cast<int>(k1);
-                const bool whole = k0 == 0 && q.k1 == x.n;
-                q.slot = whole ? -1 : (k0 > 0 ? 2 * w : 2 * w + 1);
-                q.first_part = !whole && k0 == 0;
-                q.last = us + x.n - 1;
-            }
-            us += x.n + UNIT_COST;
+        while (us - UNIT_COST < len) {      // the last unit ends where the last stretch does
+            if (e != q.e)               // kept over its KV heads
+                q.x = p.ents[e];
+            const int n = q.x.n;
+            const bool empty = n == 0 && us >= UNIT_COST;       // zero rows
+            q.k0 = empty ? 0 : max(-us, 0);
+            q.k1 = empty ? 0 : min(len - us, n);
+            q.e = e;
+            q.kv = kv;
+            const bool whole = q.k0 == 0 && q.k1 == n;
+            q.slot = whole ? -1 : 2 * static_cast<int>(blockIdx.x) + (q.k0 == 0);
+            q.first_part = !whole && q.k0 == 0;
+            q.last = us + n - 1;
+            us += n + UNIT_COST;
             if (++kv == p.cache.Hkv) {
                 kv = 0;
-                if (++e < E)
-                    x = p.ents[e];
-                us = e < E ? p.pos[e] + UNIT_COST : us;
+                ++e;
             }
-            if (some)
+            if (empty || q.k1 > q.k0)
                 return true;
         }
         return false;
@@ -274,37 +265,50 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar)
 }
 
 // Arrives on bar when the products issued so far by this thread are done.
-__device__ __forceinline__ void mma_commit(uint32_t bar)
+__device__ __forceinline__ void mma_commit(uint32_t lead, uint32_t bar)
 {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+                 "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+                 "r"(lead)
                  : "memory");
 }
 
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
-// A matrix in shared memory under the 128-byte swizzle.  K-major (Q, K): rows of
-// 128 bytes, 8-row groups 1024 bytes apart.  MN-major (V): a row is 64 columns of
-// one key, 8-key groups 1024 bytes apart, the next 64 columns a slab further.
-__device__ __forceinline__ uint64_t mat_desc(uint32_t addr, uint32_t lbo)
+// A matrix in shared memory under the 128-byte swizzle, version 1.  K-major (Q, K):
+// rows of 128 bytes, 8-row groups 1024 bytes apart.  MN-major (V): a row is 64
+// columns of one key, 8-key groups 1024 bytes apart, the next 64 columns a slab
+// further.  The high word is the same for all; the low one is the address (in
+// units of 16 bytes) and the slab distance, so a step adds to it.
+constexpr uint32_t DESC_HI = 1024 >> 4 | 1u << 14 | 2u << 29;
+constexpr uint32_t DESC_V = (SLAB >> 4) << 16;
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr) { return addr >> 4; }
+
+// `lead` is set in one lane; the others run along, so that the warp never
+// diverges around the products and their operands stay in uniform registers.
+__device__ __forceinline__ uint32_t elect()
 {
-    return (uint64_t)((addr >> 4) & 0x3fff) | (uint64_t)(lbo >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
-           1ull << 46 | 2ull << 61;
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r;
 }
 
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add)
+__device__ __forceinline__ void mma_ss(uint32_t lead, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool add)
 {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-                 "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+    asm volatile("{\n\t.reg .pred p, q;\n\t.reg .b64 da, db;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+                 "setp.ne.u32 q, %5, 0;\n\tmov.b64 da, {%1, %6};\n\tmov.b64 db, {%2, %6};\n\t"
+                 "@q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+                 "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)add), "r"(lead), "r"(DESC_HI)
                  : "memory");
 }
 
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add)
+__device__ __forceinline__ void mma_ts(uint32_t lead, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool add)
 {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-                 "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+    asm volatile("{\n\t.reg .pred p, q;\n\t.reg .b64 db;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+                 "setp.ne.u32 q, %5, 0;\n\tmov.b64 db, {%2, %6};\n\t"
+                 "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d),
+                 "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)add), "r"(lead), "r"(DESC_HI)
                  : "memory");
 }
 
@@ -338,8 +342,37 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *r)
                  FA_W8(r, 0), FA_W8(r, 8)
                  : "memory");
 }
+// Two 32-bit floats in one register pair: one instruction for both.
+__device__ __forceinline__ uint64_t pair2(float a, float b)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void split2(uint64_t v, float &a, float &b)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
 __device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// The low n bits, n of any sign and size.
+__device__ __forceinline__ uint32_t below(int n)
+{
+    return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
+}
 
 // ------------------------------------------------------------ the main kernel
 // Warp 0 loads, warp 1 issues the products, warps 4-7 (and 8-11) own the rows of
@@ -374,7 +407,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
     Bars &bars = *reinterpret_cast<Bars *>(smem + C::BAR_OFF);
     static_assert(sizeof(Bars) <= 512, "barriers fit their space");
     const uint32_t sQ = smem_u32(smem), ring = sQ + C::Q_BYTES;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int w = blockIdx.x;
 
     if (warp == 0 && lane == 0) {
@@ -435,9 +468,10 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
 
     Pieces walk;
     Piece pc;
+    pc.e = -1;
     bool ok = working;
     if (working)
-        walk.start(p, bars.e0, w, t0, t1);
+        walk.start(p, bars.e0, t0, t1);
     auto wait = [&](uint64_t &bar, uint32_t count) {      // the bar's phase number `count`
         if (mbar_wait_warp(smem_u32(&bar), count & 1))
             return true;
@@ -533,33 +567,30 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         // ---------------------------------------------------------- products
         uint32_t it = 0, qn = 0, pair_n = 0, on[2] = {0, 0}, one_n[2] = {0, 0};
         constexpr uint32_t idesc_pv = 1u << 4 | 1u << 16 | (128u >> 3) << 17 | (128u >> 4) << 24;
+        const uint32_t lead = elect();
+        const uint32_t q_lo = desc_lo(sQ), ring_lo = desc_lo(ring);
         // S buffer <- Q of stream s . K^T, from the stages at `at`
         auto qk = [&](int s, int buf, uint32_t at) {
-            if (lane == 0) {
 #pragma unroll
-                for (int ds = 0; ds < DS; ++ds) {
-                    const uint32_t k = ring + (at + ds) % STAGES * STAGE_BYTES;
-                    const uint32_t q = sQ + s * BM * D * 2 + ds * 2 * SLAB;
+            for (int ds = 0; ds < DS; ++ds) {
+                const uint32_t k = ring_lo + (at + ds) % STAGES * (STAGE_BYTES >> 4);
+                const uint32_t q = q_lo + s * (BM * D * 2 >> 4) + ds * (2 * SLAB >> 4);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const uint32_t off = (i / 4) * SLAB + (i % 4) * 32;
-                        mma_ss(tmem + buf * 128, mat_desc(q + off, 16), mat_desc(k + off, 16), p.idesc_qk,
-                               ds > 0 || i > 0);
-                    }
+                for (int i = 0; i < 8; ++i) {
+                    const uint32_t off = ((i / 4) * SLAB + (i % 4) * 32) >> 4;
+                    mma_ss(lead, tmem + buf * 128, q + off, k + off, p.idesc_qk, ds > 0 || i > 0);
                 }
             }
         };
         // O of stream s (+)= P in buffer buf . V
         auto pv = [&](int s, int buf, uint32_t at, bool add) {
-            if (lane == 0) {
 #pragma unroll
-                for (int ds = 0; ds < DS; ++ds) {
-                    const uint32_t v = ring + (at + ds) % STAGES * STAGE_BYTES;
+            for (int ds = 0; ds < DS; ++ds) {
+                const uint32_t v = ring_lo + DESC_V + (at + ds) % STAGES * (STAGE_BYTES >> 4);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        mma_ts(tmem + O_COL + (s + ds) * 128, tmem + buf * 128 + i * 8,
-                               mat_desc(v + i * 2048, SLAB), idesc_pv, add || i > 0);
-                }
+                for (int i = 0; i < 8; ++i)
+                    mma_ts(lead, tmem + O_COL + (s + ds) * 128, tmem + buf * 128 + i * 8, v + i * (2048 >> 4),
+                           idesc_pv, add || i > 0);
             }
         };
         auto arrived = [&](uint32_t at) {           // the DS stages from `at` hold their part
@@ -569,13 +600,11 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
             return true;
         };
         auto release = [&](uint32_t at) {
-            if (lane == 0)
-                for (int ds = 0; ds < DS; ++ds)
-                    mma_commit(smem_u32(&bars.empty[(at + ds) % STAGES]));
+            for (int ds = 0; ds < DS; ++ds)
+                mma_commit(lead, smem_u32(&bars.empty[(at + ds) % STAGES]));
         };
         auto commit = [&](uint64_t &bar) {
-            if (lane == 0)
-                mma_commit(smem_u32(&bar));
+            mma_commit(lead, smem_u32(&bar));
         };
         // V rows of key tile k that no row sees may hold anything: zero them, so that a
         // weight of 0 leaves nothing
@@ -599,10 +628,10 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
             __syncwarp();
         };
         while (ok && walk.next(p, pc)) {
-            const int n = pc.k1 - pc.k0;
+            const int n = __shfl_sync(0xffffffffu, pc.k1 - pc.k0, 0);
             if (n == 0)
                 continue;
-            const bool two = paired(pc);
+            const bool two = __shfl_sync(0xffffffffu, paired(pc), 0);
             ok = wait(bars.q_full, qn);
             ++qn;
             if (NS == 2 && two) {
@@ -732,24 +761,30 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                             if (c < 3)
                                 tmem_ld32(lanes + buf * 128 + (c + 1) * 32, x[(c + 1) & 1]);
                             if (edge) {
+                                // a bit per column that the row sees
+                                uint32_t see = below(hi + 1 - c * 32) &
+                                               (~below(lo - c * 32) | below(sk - c * 32));
+                                if (bits)
+                                    for (int t = 0; t < 32; t += 16)
+                                        if (bits >> ((c * 32 + t) >> p.lg_br) & 1)
+                                            see &= ~(0xffffu << t);
 #pragma unroll
-                                for (int i = 0; i < 32; ++i) {
-                                    const int t = c * 32 + i;
-                                    if (t > hi || (t < lo && t >= sk) || (bits >> (t >> p.lg_br) & 1))
+                                for (int i = 0; i < 32; ++i)
+                                    if (!(see >> i & 1))
                                         x[c & 1][i] = 0xff800000u;      // -infinity
-                                }
                             }
                             use(c, x[c & 1]);
                             if (c < 3)
                                 tmem_ld_wait();
                         }
                     };
-                    float top = -INFINITY;
+                    float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
                     passes([&](int, const uint32_t (&x)[32]) {
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
-                            top = fmaxf(top, __uint_as_float(x[i]));
+                            tops[i & 3] = fmaxf(tops[i & 3], __uint_as_float(x[i]));
                     });
+                    float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
                     top *= p.c2;
                     const bool grow = top > m + 8.f;        // also from -infinity
                     if (__any_sync(0xffffffffu, grow)) {
@@ -779,20 +814,28 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                         }
                     }
                     const float ref = m == -INFINITY ? 0.f : m;
-                    float sum = 0.f;
+                    const uint64_t c22 = pair2(p.c2, p.c2), ref2 = pair2(-ref, -ref);
+                    uint64_t sums[4] = {0, 0, 0, 0};
                     passes([&](int c, const uint32_t (&x)[32]) {
                         uint32_t h[16];
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
-                            const float a = ex2_ftz(fmaf(__uint_as_float(x[2 * i]), p.c2, -ref));
-                            const float b = ex2_ftz(fmaf(__uint_as_float(x[2 * i + 1]), p.c2, -ref));
-                            sum += a + b;
+                            float a, b;
+                            split2(fma2(pair2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), c22,
+                                        ref2), a, b);
+                            a = ex2_ftz(a);
+                            b = ex2_ftz(b);
+                            sums[i & 3] = add2(sums[i & 3], pair2(a, b));
                             h[i] = tc::pack_half2(a, b);
                         }
                         // over columns of S that have gone by
                         tmem_st16(lanes + buf * 128 + c * 16, h);
                     });
-                    l += sum;
+                    {
+                        float a, b;
+                        split2(add2(add2(sums[0], sums[1]), add2(sums[2], sums[3])), a, b);
+                        l += a + b;
+                    }
                     tmem_st_wait();
                     fence_before();
                     __syncwarp();
@@ -852,7 +895,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                 }
                 if (pc.first_part && s == 0 && r == 0)
                     p.split[w] = make_int4(pc.e, pc.kv,
-                                           static_cast<int>(((pc.last + 1) * We - 1) / T) - w + 1, 0);
+                                           static_cast<int>(((t0 + pc.last + 1) * We - 1) / T) - w + 1, 0);
             }
             tiles += n;
             if (two) {
