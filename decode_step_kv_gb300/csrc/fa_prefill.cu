@@ -342,6 +342,12 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *r)
                  FA_W8(r, 0), FA_W8(r, 8)
                  : "memory");
 }
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
 // Two 32-bit floats in one register pair: one instruction for both.
 __device__ __forceinline__ uint64_t pair2(float a, float b)
 {
@@ -481,6 +487,9 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
     };
     auto paired = [&](const Piece &q) { return NS == 2 && q.x.ntok > p.tpt; };
 
+    if (warp < 4) {
+    if constexpr (NS == 2)
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == 0) {
         // ---------------------------------------------------------- loads
         uint32_t it = 0, qn = 0, tiles = 0;     // stages filled, Q tiles loaded, key tiles so far
@@ -720,7 +729,10 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         // no product is left running when the TMEM goes back
         commit(bars.end);
         mbar_wait_warp(smem_u32(&bars.end), 0);
-    } else if (warp >= 4) {
+    }
+    } else {
+        if constexpr (NS == 2)
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
         // ---------------------------------------------------------- softmax
         const int s = (warp - 4) >> 2;              // stream
         const int r = threadIdx.x & 127;            // row of the stream
@@ -749,41 +761,30 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                                       (pc.x.window > 0 && kb <= at_hi - pc.x.window && kb + BN > p.sink);
                     const int hi = at - kb, lo = pc.x.window > 0 ? hi - pc.x.window + 1 : -1;
                     const int sk = p.sink - kb;
-                    // S goes by twice, 32 columns at a time (the next ones on their way
-                    // meanwhile): once for the maximum, once for the weights.  Held in
-                    // registers in between, 128 values beside the walk's state spill
-                    auto passes = [&](auto use) {
-                        uint32_t x[2][32];
-                        tmem_ld32(lanes + buf * 128, x[0]);
-                        tmem_ld_wait();
+                    uint32_t x[128];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        tmem_ld32(lanes + buf * 128 + c * 32, x + c * 32);
+                    tmem_ld_wait();
+                    if (edge) {
 #pragma unroll
                         for (int c = 0; c < 4; ++c) {
-                            if (c < 3)
-                                tmem_ld32(lanes + buf * 128 + (c + 1) * 32, x[(c + 1) & 1]);
-                            if (edge) {
-                                // a bit per column that the row sees
-                                uint32_t see = below(hi + 1 - c * 32) &
-                                               (~below(lo - c * 32) | below(sk - c * 32));
-                                if (bits)
-                                    for (int t = 0; t < 32; t += 16)
-                                        if (bits >> ((c * 32 + t) >> p.lg_br) & 1)
-                                            see &= ~(0xffffu << t);
+                            // a bit per column that the row sees
+                            uint32_t see = below(hi + 1 - c * 32) & (~below(lo - c * 32) | below(sk - c * 32));
+                            if (bits)
+                                for (int t = 0; t < 32; t += 16)
+                                    if (bits >> ((c * 32 + t) >> p.lg_br) & 1)
+                                        see &= ~(0xffffu << t);
 #pragma unroll
-                                for (int i = 0; i < 32; ++i)
-                                    if (!(see >> i & 1))
-                                        x[c & 1][i] = 0xff800000u;      // -infinity
-                            }
-                            use(c, x[c & 1]);
-                            if (c < 3)
-                                tmem_ld_wait();
+                            for (int i = 0; i < 32; ++i)
+                                if (!(see >> i & 1))
+                                    x[c * 32 + i] = 0xff800000u;        // -infinity
                         }
-                    };
-                    float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                    passes([&](int, const uint32_t (&x)[32]) {
+                    }
+                    float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};   // chains of their own
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            tops[i & 3] = fmaxf(tops[i & 3], __uint_as_float(x[i]));
-                    });
+                    for (int i = 0; i < 128; i += 2)
+                        tops[i / 2 & 3] = max3(tops[i / 2 & 3], __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
                     float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
                     top *= p.c2;
                     const bool grow = top > m + 8.f;        // also from -infinity
@@ -816,21 +817,21 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                     const float ref = m == -INFINITY ? 0.f : m;
                     const uint64_t c22 = pair2(p.c2, p.c2), ref2 = pair2(-ref, -ref);
                     uint64_t sums[4] = {0, 0, 0, 0};
-                    passes([&](int c, const uint32_t (&x)[32]) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
                         uint32_t h[16];
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
                             float a, b;
-                            split2(fma2(pair2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), c22,
-                                        ref2), a, b);
+                            split2(fma2(pair2(__uint_as_float(x[c * 32 + 2 * i]),
+                                              __uint_as_float(x[c * 32 + 2 * i + 1])), c22, ref2), a, b);
                             a = ex2_ftz(a);
                             b = ex2_ftz(b);
                             sums[i & 3] = add2(sums[i & 3], pair2(a, b));
                             h[i] = tc::pack_half2(a, b);
                         }
-                        // over columns of S that have gone by
                         tmem_st16(lanes + buf * 128 + c * 16, h);
-                    });
+                    }
                     {
                         float a, b;
                         split2(add2(add2(sums[0], sums[1]), add2(sums[2], sums[3])), a, b);
