@@ -45,6 +45,7 @@ template <int D>
 struct Cfg {
     static constexpr int NS = D == 128 ? 2 : 1;             // streams of 128 rows
     static constexpr int DS = D / 128;                      // ring stages per K or V tile
+    static constexpr int SW = D == 128 ? 64 : 128;          // keys of an S buffer
     static constexpr int THREADS = 128 + 128 * NS;
     static constexpr int Q_BYTES = NS * BM * D * 2;
     static constexpr int BAR_OFF = Q_BYTES + STAGES * STAGE_BYTES;
@@ -380,22 +381,41 @@ __device__ __forceinline__ uint32_t below(int n)
     return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
 }
 
+// V rows of key tile k that no row sees may hold anything: zero them, so that a
+// weight of 0 leaves nothing.  `part` is the tile's 128 dims in shared memory.
+__device__ __forceinline__ void clean(const Args &p, const Piece &pc, int k, uint32_t part, int lane)
+{
+    const int kb = pc.key_tile(k) * BN, hi = pc.x.hi - kb, lo = pc.x.lo - kb, sk = p.sink - kb;
+    if (hi >= BN && (lo <= 0 || sk >= min(lo, BN)))
+        return;
+    for (int i = lane; i < BN * 8; i += 32) {
+        const int r = i >> 3;
+        if (r < hi && (r >= lo || r < sk))
+            continue;
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(part + c * SLAB + i * 16), "r"(0)
+                         : "memory");
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+}
+
 // ------------------------------------------------------------ the main kernel
-// Warp 0 loads, warp 1 issues the products, warps 4-7 (and 8-11) own the rows of
-// stream 0 (and 1).  A piece whose tokens fill both streams runs them in turn
-// ("paired"); one with a single stream of rows alternates two S buffers instead.
-// The two forms have barriers of their own, so that a stream-1 warp that sits a
-// piece out misses none of its phases.
+// Warp 0 loads, warps 1 and 3 issue the products of streams 0 and 1, warps 4-7 and
+// 8-11 own their rows.  Every stream has two S buffers of SW keys, so that its
+// products run ahead of its softmax: Q K^T of part i + 2 of the keys follows P V of
+// part i, whose columns it takes over.  A piece whose tokens fill one stream leaves
+// the other out: it waits for none of its barriers.
 struct Bars {
     uint64_t full[STAGES], empty[STAGES];
     uint64_t q_full, q_empty;
-    uint64_t s_pair[2], p_pair[2];      // S ready, P ready: of stream s
-    uint64_t s_one[2], p_one[2];        // S ready, P ready: of buffer j % 2
-    uint64_t pv_one;                    // single stream: a P V done
-    uint64_t o_full[2], o_empty[2];     // the unit's O complete; read out
+    uint64_t s_full[2][2], p_full[2][2];    // S, P of [stream][buffer]
+    uint64_t pv[2];                         // a P V of the stream done
+    uint64_t o_full[2], o_empty[2];         // the unit's O complete; read out
     uint64_t end;
     uint32_t tmem;
-    uint32_t bits[BITS];                // per key tile: groups in unmapped blocks
+    uint32_t bits[BITS];                    // per key tile: groups in unmapped blocks
     int e0;
 };
 
@@ -405,7 +425,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                   const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV)
 {
     using C = Cfg<D>;
-    constexpr int NS = C::NS, DS = C::DS;
+    constexpr int NS = C::NS, DS = C::DS, SW = C::SW, PARTS = BN / SW;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     extern __shared__ unsigned char smem_raw[];
     unsigned char *smem = reinterpret_cast<unsigned char *>(
@@ -419,20 +439,20 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
     if (warp == 0 && lane == 0) {
         for (int i = 0; i < STAGES; ++i) {
             mbar_init(smem_u32(&bars.full[i]), 1);
-            mbar_init(smem_u32(&bars.empty[i]), 1);
+            mbar_init(smem_u32(&bars.empty[i]), NS);
         }
         mbar_init(smem_u32(&bars.q_full), 1);
-        mbar_init(smem_u32(&bars.q_empty), 1);
+        mbar_init(smem_u32(&bars.q_empty), NS);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_u32(&bars.s_pair[i]), 1);
-            mbar_init(smem_u32(&bars.p_pair[i]), 4);
-            mbar_init(smem_u32(&bars.s_one[i]), 1);
-            mbar_init(smem_u32(&bars.p_one[i]), 4);
+            for (int b = 0; b < 2; ++b) {
+                mbar_init(smem_u32(&bars.s_full[i][b]), 1);
+                mbar_init(smem_u32(&bars.p_full[i][b]), 4);
+            }
+            mbar_init(smem_u32(&bars.pv[i]), 1);
             mbar_init(smem_u32(&bars.o_full[i]), 1);
             mbar_init(smem_u32(&bars.o_empty[i]), 4);
         }
-        mbar_init(smem_u32(&bars.pv_one), 1);
-        mbar_init(smem_u32(&bars.end), 1);
+        mbar_init(smem_u32(&bars.end), NS);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmQ)) : "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmK)) : "memory");
@@ -487,84 +507,86 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
     };
     auto paired = [&](const Piece &q) { return NS == 2 && q.x.ntok > p.tpt; };
 
-    if (warp < 4) {
-    if constexpr (NS == 2)
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    // key tiles that Q K^T runs ahead of P V by
+    constexpr int LEAD = 2 / PARTS;
     if (warp == 0) {
         // ---------------------------------------------------------- loads
         uint32_t it = 0, qn = 0, tiles = 0;     // stages filled, Q tiles loaded, key tiles so far
         const int br = 1 << p.lg_br, groups = BN >> p.lg_br;
-        // one part (128 dims) of a K or V tile: the rows of its groups, from the lanes
-        auto part = [&](const CUtensorMap *map, int row, int ds) {
-            const uint32_t s = it % STAGES;
-            if (it >= STAGES && !wait(bars.empty[s], it / STAGES - 1))
-                return false;
-            const uint32_t bar = smem_u32(&bars.full[s]), dst = ring + s * STAGE_BYTES;
-            if (lane == 0)
-                mbar_expect_tx(bar, STAGE_BYTES);
-            __syncwarp();
-            if (lane < groups) {
-                tma_load(dst + lane * br * 128, map, ds * 128, row, bar);
-                tma_load(dst + SLAB + lane * br * 128, map, ds * 128 + 64, row, bar);
+        const int g = lane % groups, slab = lane / groups;      // a lane per group of rows and 64 dims
+        // a K or V tile: DS stages of 128 dims
+        auto tile = [&](const CUtensorMap *map, int row) {
+#pragma unroll
+            for (int ds = 0; ds < DS; ++ds) {
+                const uint32_t s = it % STAGES;
+                if (it >= STAGES && !wait(bars.empty[s], it / STAGES - 1))
+                    return false;
+                const uint32_t bar = smem_u32(&bars.full[s]), dst = ring + s * STAGE_BYTES;
+                if (lane == 0)
+                    mbar_expect_tx(bar, STAGE_BYTES);
+                __syncwarp();
+                if (slab < 2)
+                    tma_load(dst + slab * SLAB + g * br * 128, map, ds * 128 + slab * 64, row, bar);
+                ++it;
             }
-            ++it;
             return true;
         };
         while (ok && walk.next(p, pc)) {
             const int n = pc.k1 - pc.k0;
             if (n == 0)
                 continue;
-            // the cache row of this lane's group of key tile k; oob_row for groups no row sees
-            // and, reported, for unmapped blocks
-            auto rows = [&](int k, bool report) {
-                const int t = pc.key_tile(k) * BN + lane * br;
+            // the cache row of this lane's group of key tile k; oob_row for groups no row sees,
+            // and, with a bit set, for unmapped blocks
+            auto rows = [&](int j, uint32_t &bits) {
                 int row = p.oob_row;
                 bool bad = false;
-                if (lane < groups && t < pc.x.hi && (t + br > pc.x.lo || t < p.sink)) {
+                const int t = j < n ? pc.key_tile(pc.k0 + j) * BN + g * br : pc.x.hi;
+                if (t < pc.x.hi && (t + br > pc.x.lo || t < p.sink)) {
                     const long long r = tc::tile_row(p.cache, pc.x.b, pc.kv, t);
                     bad = r < 0;
                     row = bad ? p.oob_row : static_cast<int>(r);
                 }
-                if (report) {
-                    const unsigned bits = __ballot_sync(0xffffffffu, bad);
-                    if (lane == 0) {
-                        if (bits)
-                            flag(FA_STATUS_BAD_BLOCK);
-                        bars.bits[tiles % BITS] = bits;
-                    }
-                    ++tiles;
-                    __syncwarp();
-                }
+                bits = __ballot_sync(0xffffffffu, bad && slab == 0);
                 return row;
             };
-            int prev = 0;                       // rows of the tile before: its V
-            for (int j = 0; ok && j <= n; ++j) {
-                int row = 0;
-                if (j < n) {
-                    row = rows(pc.k0 + j, true);
-                    for (int ds = 0; ok && ds < DS; ++ds)
-                        ok = part(&tmK, row, ds);
+            auto k_tile = [&](int row, uint32_t bits) {
+                if (lane == 0) {
+                    if (bits)
+                        flag(FA_STATUS_BAD_BLOCK);
+                    bars.bits[tiles % BITS] = bits;
                 }
-                if (ok && j == 0) {
-                    const bool two = paired(pc);
-                    if (qn > 0)
-                        ok = wait(bars.q_empty, qn - 1);
-                    if (ok && lane == 0) {
-                        const uint32_t bar = smem_u32(&bars.q_full);
-                        const int box = p.group * p.tpt * 128;
-                        mbar_expect_tx(bar, (two ? 2 : 1) * (D / 64) * box);
-                        for (int s = 0; s < (two ? 2 : 1); ++s)
-                            for (int c = 0; c < D / 64; ++c)
-                                tma_load_3d(sQ + s * BM * D * 2 + c * SLAB, &tmQ, c * 64,
-                                            pc.kv * p.group, pc.x.tok + s * p.tpt, bar);
-                    }
-                    ++qn;
-                    __syncwarp();
-                }
-                if (ok && j > 0)
-                    for (int ds = 0; ok && ds < DS; ++ds)
-                        ok = part(&tmV, prev, ds);
-                prev = row;
+                ++tiles;
+                return tile(&tmK, row);
+            };
+            // in the order of their products: K0 (K1), then V(j), K(j + LEAD)
+            uint32_t bits0, bits1, bits2;
+            int row0 = rows(0, bits0), row1 = rows(1, bits1), row2;
+            ok = k_tile(row0, bits0);
+            if (ok && qn > 0)
+                ok = wait(bars.q_empty, qn - 1);
+            if (!ok)
+                break;
+            if (lane == 0) {
+                const uint32_t bar = smem_u32(&bars.q_full);
+                const int box = p.group * p.tpt * 128, streams = paired(pc) ? 2 : 1;
+                mbar_expect_tx(bar, streams * (D / 64) * box);
+                for (int s = 0; s < streams; ++s)
+                    for (int c = 0; c < D / 64; ++c)
+                        tma_load_3d(sQ + s * BM * D * 2 + c * SLAB, &tmQ, c * 64, pc.kv * p.group,
+                                    pc.x.tok + s * p.tpt, bar);
+            }
+            ++qn;
+            __syncwarp();
+            if (LEAD == 2 && n > 1)
+                ok = k_tile(row1, bits1);
+            for (int j = 0; ok && j < n; ++j) {
+                row2 = rows(j + 2, bits2);          // looked up while the ring is full
+                ok = tile(&tmV, row0);
+                if (ok && j + LEAD < n)
+                    ok = LEAD == 1 ? k_tile(row1, bits1) : k_tile(row2, bits2);
+                row0 = row1;
+                row1 = row2;
+                bits1 = bits2;
             }
         }
         // no copy is left in flight when the CTA ends
@@ -572,245 +594,242 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
             mbar_wait_warp(smem_u32(&bars.full[i % STAGES]), i / STAGES & 1);
         if (qn > 0)
             mbar_wait_warp(smem_u32(&bars.q_full), (qn - 1) & 1);
-    } else if (warp == 1) {
-        // ---------------------------------------------------------- products
-        uint32_t it = 0, qn = 0, pair_n = 0, on[2] = {0, 0}, one_n[2] = {0, 0};
+    } else if (warp == 1 || (NS == 2 && warp == 3)) {
+        // ------------------------------------- products: a warp per stream
+        // Each waits for every stage in turn and gives every stage back, also of
+        // the pieces it sits out, so that neither loses count of the phases.
+        const int s = warp >> 1;
+        uint32_t stage = 0, phase = 0, qn = 0, on = 0, used[2] = {0, 0};
         constexpr uint32_t idesc_pv = 1u << 4 | 1u << 16 | (128u >> 3) << 17 | (128u >> 4) << 24;
         const uint32_t lead = elect();
-        const uint32_t q_lo = desc_lo(sQ), ring_lo = desc_lo(ring);
-        // S buffer <- Q of stream s . K^T, from the stages at `at`
-        auto qk = [&](int s, int buf, uint32_t at) {
-#pragma unroll
-            for (int ds = 0; ds < DS; ++ds) {
-                const uint32_t k = ring_lo + (at + ds) % STAGES * (STAGE_BYTES >> 4);
-                const uint32_t q = q_lo + s * (BM * D * 2 >> 4) + ds * (2 * SLAB >> 4);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const uint32_t off = ((i / 4) * SLAB + (i % 4) * 32) >> 4;
-                    mma_ss(lead, tmem + buf * 128, q + off, k + off, p.idesc_qk, ds > 0 || i > 0);
-                }
+        const uint32_t q_lo = desc_lo(sQ) + s * (BM * D * 2 >> 4), ring_lo = desc_lo(ring);
+        const uint32_t s_col = tmem + s * 128, o_col = tmem + O_COL + s * 128;
+        bool mine = true;
+        auto full = [&](uint32_t st, uint32_t ph) {     // stage st has arrived
+            if (mbar_wait_warp(smem_u32(&bars.full[st]), ph))
+                return true;
+            if (lane == 0)
+                flag(FA_STATUS_WAIT_TIMEOUT);
+            return false;
+        };
+        auto advance = [&] {
+            if (++stage == STAGES) {
+                stage = 0;
+                phase ^= 1;
             }
         };
-        // O of stream s (+)= P in buffer buf . V
-        auto pv = [&](int s, int buf, uint32_t at, bool add) {
+        auto release = [&](uint32_t st) {               // refilled when the products are done
+            mma_commit(lead, smem_u32(&bars.empty[st]));
+        };
+        // S of buffer b <- Q K^T: dims 128 ds .. of the keys from row 64 * half of stage st
+        auto qk = [&](int b, int half, int ds, uint32_t st) {
+            if (!mine)
+                return;
+            const uint32_t k = ring_lo + st * (STAGE_BYTES >> 4) + half * (64 * 128 >> 4);
+            const uint32_t q = q_lo + ds * (2 * SLAB >> 4);
 #pragma unroll
-            for (int ds = 0; ds < DS; ++ds) {
-                const uint32_t v = ring_lo + DESC_V + (at + ds) % STAGES * (STAGE_BYTES >> 4);
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    mma_ts(lead, tmem + O_COL + (s + ds) * 128, tmem + buf * 128 + i * 8, v + i * (2048 >> 4),
-                           idesc_pv, add || i > 0);
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t off = ((i / 4) * SLAB + (i % 4) * 32) >> 4;
+                mma_ss(lead, s_col + b * SW, q + off, k + off, p.idesc_qk, ds > 0 || i > 0);
             }
         };
-        auto arrived = [&](uint32_t at) {           // the DS stages from `at` hold their part
-            for (int ds = 0; ds < DS; ++ds)
-                if (!wait(bars.full[(at + ds) % STAGES], (at + ds) / STAGES))
-                    return false;
-            return true;
-        };
-        auto release = [&](uint32_t at) {
-            for (int ds = 0; ds < DS; ++ds)
-                mma_commit(lead, smem_u32(&bars.empty[(at + ds) % STAGES]));
+        // O's columns 128 ds .. (+)= P of buffer b . the keys from row 64 * half of stage st
+        auto pv = [&](int b, int half, int ds, uint32_t st, bool add) {
+            if (!mine)
+                return;
+            const uint32_t v = ring_lo + DESC_V + st * (STAGE_BYTES >> 4) + half * (64 * 128 >> 4);
+#pragma unroll
+            for (int i = 0; i < SW / 16; ++i)
+                mma_ts(lead, o_col + ds * 128, s_col + b * SW + i * 8, v + i * (2048 >> 4), idesc_pv, add || i > 0);
         };
         auto commit = [&](uint64_t &bar) {
-            mma_commit(lead, smem_u32(&bar));
+            if (mine)
+                mma_commit(lead, smem_u32(&bar));
         };
-        // V rows of key tile k that no row sees may hold anything: zero them, so that a
-        // weight of 0 leaves nothing
-        auto clean = [&](int k, uint32_t at) {
-            const int kb = pc.key_tile(k) * BN, hi = pc.x.hi - kb, lo = pc.x.lo - kb, sk = p.sink - kb;
-            if (hi >= BN && (lo <= 0 || sk >= min(lo, BN)))
-                return;
-            for (int i = lane; i < BN * 8; i += 32) {
-                const int r = i >> 3;
-                if (r < hi && (r >= lo || r < sk))
-                    continue;
-                for (int ds = 0; ds < DS; ++ds)
-#pragma unroll
-                    for (int c = 0; c < 2; ++c)
-                        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(
-                                         ring + (at + ds) % STAGES * STAGE_BYTES + c * SLAB + i * 16),
-                                     "r"(0)
-                                     : "memory");
-            }
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
+        // P of part i is there (and, first, O has been read out)
+        auto p_ready = [&](int i) {
+            if (!mine)
+                return true;
+            if (!wait(bars.p_full[s][i & 1], used[i & 1] + i / 2) ||
+                (i == 0 && on > 0 && !wait(bars.o_empty[s], on - 1)))
+                return false;
+            fence_after();
+            return true;
+        };
+        auto dirty = [&](int k) {       // only a range's ends hold keys that no row sees
+            return mine && (k == pc.x.n - 1 || k == pc.x.ns || k == pc.x.ns - 1);
         };
         while (ok && walk.next(p, pc)) {
             const int n = __shfl_sync(0xffffffffu, pc.k1 - pc.k0, 0);
             if (n == 0)
                 continue;
-            const bool two = __shfl_sync(0xffffffffu, paired(pc), 0);
+            mine = s == 0 || __shfl_sync(0xffffffffu, paired(pc), 0);
             ok = wait(bars.q_full, qn);
             ++qn;
-            if (NS == 2 && two) {
-                uint32_t at_v = 0;
-                for (int j = 0; ok && j <= n; ++j) {
-                    // stages in order: K0, K1, V0, K2, V1, ...
-                    const uint32_t at_k = it;
-                    if (j < n) {
-                        ok = arrived(at_k);
-                        it += DS;
+            if constexpr (PARTS == 2) {
+                // parts 2 j and 2 j + 1 are the halves of tile j
+                ok = ok && full(stage, phase);
+                if (ok) {
+                    for (int b = 0; b < 2; ++b) {
+                        qk(b, b, 0, stage);
+                        commit(bars.s_full[s][b]);
                     }
-                    if (ok && j > 0) {
-                        at_v = it;
-                        ok = arrived(at_v);
-                        it += DS;
-                        if (ok)
-                            clean(pc.k0 + j - 1, at_v);
+                    release(stage);
+                    if (n == 1)
+                        mma_commit(lead, smem_u32(&bars.q_empty));
+                    advance();
+                }
+                for (int j = 0; ok && j < n; ++j) {
+                    const uint32_t v = stage, vp = phase;
+                    advance();
+                    const uint32_t k = stage, kp = phase;
+                    ok = full(v, vp);
+                    if (ok && dirty(pc.k0 + j))
+                        clean(p, pc, pc.k0 + j, ring + v * STAGE_BYTES, lane);
+                    for (int b = 0; ok && b < 2; ++b) {
+                        ok = p_ready(2 * j + b);
+                        if (!ok)
+                            break;
+                        pv(b, b, 0, v, 2 * j + b > 0);
+                        commit(bars.pv[s]);
+                        if (b == 1)
+                            release(v);
+                        if (j + 1 < n) {
+                            if (b == 0)
+                                ok = full(k, kp);
+                            if (ok) {
+                                qk(b, b, 0, k);
+                                commit(bars.s_full[s][b]);
+                            }
+                        }
                     }
-                    for (int s = 0; ok && s < 2; ++s) {
-                        if (j > 0) {
-                            ok = wait(bars.p_pair[s], pair_n + j - 1);
-                            if (ok && j == 1 && on[s] > 0)
-                                ok = wait(bars.o_empty[s], on[s] - 1);
-                            if (!ok)
-                                break;
-                            fence_after();
-                            pv(s, s, at_v, j > 1);
-                        }
-                        if (j < n) {
-                            qk(s, s, at_k);
-                            commit(bars.s_pair[s]);
-                        } else {
-                            commit(bars.o_full[s]);
-                            ++on[s];
-                        }
+                    if (ok && j + 1 < n) {
+                        release(k);
+                        advance();
+                        if (j + 2 == n)
+                            mma_commit(lead, smem_u32(&bars.q_empty));
+                    }
+                }
+            } else {
+                auto k_tile = [&](int j) {
+                    for (int ds = 0; ds < DS; ++ds) {
+                        if (!full(stage, phase))
+                            return false;
+                        qk(j & 1, 0, ds, stage);
+                        release(stage);
+                        advance();
+                    }
+                    commit(bars.s_full[s][j & 1]);
+                    if (j == n - 1)
+                        mma_commit(lead, smem_u32(&bars.q_empty));
+                    return true;
+                };
+                ok = ok && k_tile(0) && (n == 1 || k_tile(1));
+                for (int j = 0; ok && j < n; ++j) {
+                    for (int ds = 0; ok && ds < DS; ++ds) {
+                        ok = full(stage, phase);
+                        if (ok && dirty(pc.k0 + j))
+                            clean(p, pc, pc.k0 + j, ring + stage * STAGE_BYTES, lane);
+                        if (ok && ds == 0)
+                            ok = p_ready(j);
+                        if (!ok)
+                            break;
+                        pv(j & 1, 0, ds, stage, j > 0);
+                        release(stage);
+                        advance();
                     }
                     if (ok) {
-                        if (j > 0)
-                            release(at_v);
-                        if (j < n)
-                            release(at_k);
-                        if (j == n - 1)
-                            commit(bars.q_empty);
+                        commit(bars.pv[s]);
+                        if (j + 2 < n)
+                            ok = k_tile(j + 2);
                     }
                 }
-                pair_n += n;
-            } else {
-                for (int j = 0; ok && j <= n; ++j) {
-                    if (j < n) {
-                        ok = arrived(it);
-                        if (ok) {
-                            qk(0, j & 1, it);
-                            commit(bars.s_one[j & 1]);
-                            release(it);
-                            if (j == n - 1)
-                                commit(bars.q_empty);
-                        }
-                        it += DS;
-                    }
-                    if (ok && j > 0) {
-                        const int i = j - 1;
-                        ok = arrived(it);
-                        if (ok)
-                            clean(pc.k0 + i, it);
-                        if (ok)
-                            ok = wait(bars.p_one[i & 1], one_n[i & 1] + i / 2);
-                        if (ok && i == 0 && on[0] > 0)
-                            ok = wait(bars.o_empty[0], on[0] - 1);
-                        if (ok) {
-                            fence_after();
-                            pv(0, i & 1, it, i > 0);
-                            commit(bars.pv_one);
-                            release(it);
-                        }
-                        it += DS;
-                    }
-                }
-                one_n[0] += (n + 1) / 2;
-                one_n[1] += n / 2;
-                if (ok) {
-                    commit(bars.o_full[0]);
-                    ++on[0];
-                }
+            }
+            if (ok && mine) {
+                commit(bars.o_full[s]);
+                ++on;
+                used[0] += (n * PARTS + 1) / 2;
+                used[1] += n * PARTS / 2;
             }
         }
         // no product is left running when the TMEM goes back
-        commit(bars.end);
+        mma_commit(lead, smem_u32(&bars.end));
         mbar_wait_warp(smem_u32(&bars.end), 0);
-    }
-    } else {
-        if constexpr (NS == 2)
-            asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    } else if (warp >= 4) {
         // ---------------------------------------------------------- softmax
         const int s = (warp - 4) >> 2;              // stream
         const int r = threadIdx.x & 127;            // row of the stream
         const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);
-        uint32_t tiles = 0, pair_n = 0, on = 0, one_n[2] = {0, 0}, pv_n = 0;
+        const uint32_t s_col = lanes + s * 128, o_col = lanes + O_COL + s * 128;
+        uint32_t tiles = 0, on = 0, pv_n = 0, used[2] = {0, 0};
         while (ok && walk.next(p, pc)) {
-            const int n = pc.k1 - pc.k0;
-            const bool two = paired(pc);
-            const int i_tok = s * p.tpt + r / p.group;
-            const bool live = r < p.tpt * p.group && i_tok < pc.x.ntok;
-            const int at = pc.x.at + i_tok;
-            float m = -INFINITY, l = 0.f;
-            if (s == 0 || two) {
+            const int n = pc.k1 - pc.k0, m_parts = n * PARTS;
+            if (s == 0 || paired(pc)) {
+                const int i_tok = s * p.tpt + r / p.group;
+                const int at = pc.x.at + i_tok;
                 // positions of this stream's first and last row
                 const int at_lo = pc.x.at + s * p.tpt;
                 const int at_hi = pc.x.at + min((s + 1) * p.tpt, pc.x.ntok) - 1;
-                for (int j = 0; ok && j < n; ++j) {
-                    const int buf = two ? s : j & 1;
-                    ok = two ? wait(bars.s_pair[s], pair_n + j) : wait(bars.s_one[buf], one_n[buf] + j / 2);
+                float m = -INFINITY, l = 0.f;
+                for (int i = 0; ok && i < m_parts; ++i) {
+                    const int b = i & 1, half = PARTS == 2 ? b : 0;
+                    ok = wait(bars.s_full[s][b], used[b] + i / 2);
                     if (!ok)
                         break;
                     fence_after();
-                    const int kb = pc.key_tile(pc.k0 + j) * BN;
-                    const uint32_t bits = *reinterpret_cast<volatile uint32_t *>(&bars.bits[(tiles + j) % BITS]);
-                    const bool edge = kb + BN - 1 > at_lo || bits ||
-                                      (pc.x.window > 0 && kb <= at_hi - pc.x.window && kb + BN > p.sink);
-                    const int hi = at - kb, lo = pc.x.window > 0 ? hi - pc.x.window + 1 : -1;
-                    const int sk = p.sink - kb;
-                    uint32_t x[128];
+                    const int kb = pc.key_tile(pc.k0 + i / PARTS) * BN + half * SW;
+                    const uint32_t bits =
+                        *reinterpret_cast<volatile uint32_t *>(&bars.bits[(tiles + i / PARTS) % BITS]);
+                    const bool edge = kb + SW - 1 > at_lo || bits ||
+                                      (pc.x.window > 0 && kb <= at_hi - pc.x.window && kb + SW > p.sink);
+                    uint32_t x[SW];
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        tmem_ld32(lanes + buf * 128 + c * 32, x + c * 32);
+                    for (int c = 0; c < SW / 32; ++c)
+                        tmem_ld32(s_col + b * SW + c * 32, x + c * 32);
                     tmem_ld_wait();
                     if (edge) {
+                        const int hi = at - kb, lo = pc.x.window > 0 ? hi - pc.x.window + 1 : -1;
+                        const int sk = p.sink - kb;
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) {
+                        for (int c = 0; c < SW / 32; ++c) {
                             // a bit per column that the row sees
                             uint32_t see = below(hi + 1 - c * 32) & (~below(lo - c * 32) | below(sk - c * 32));
                             if (bits)
                                 for (int t = 0; t < 32; t += 16)
-                                    if (bits >> ((c * 32 + t) >> p.lg_br) & 1)
+                                    if (bits >> ((half * SW + c * 32 + t) >> p.lg_br) & 1)
                                         see &= ~(0xffffu << t);
 #pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                if (!(see >> i & 1))
-                                    x[c * 32 + i] = 0xff800000u;        // -infinity
+                            for (int e = 0; e < 32; ++e)
+                                if (!(see >> e & 1))
+                                    x[c * 32 + e] = 0xff800000u;        // -infinity
                         }
                     }
                     float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};   // chains of their own
 #pragma unroll
-                    for (int i = 0; i < 128; i += 2)
-                        tops[i / 2 & 3] = max3(tops[i / 2 & 3], __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
-                    float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
-                    top *= p.c2;
+                    for (int e = 0; e < SW; e += 2)
+                        tops[e / 2 & 3] = max3(tops[e / 2 & 3], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+                    const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * p.c2;
                     const bool grow = top > m + 8.f;        // also from -infinity
                     if (__any_sync(0xffffffffu, grow)) {
                         const float m1 = fmaxf(m, top);
                         const float a = ex2(m - (m1 == -INFINITY ? 0.f : m1));
                         m = m1;
                         l *= a;
-                        if (j > 0) {
-                            // the P V before must have landed (paired: it came before this S)
-                            if (!two) {
-                                ok = wait(bars.pv_one, pv_n + j - 1);
-                                if (!ok)
-                                    break;
-                                fence_after();
-                            }
-#pragma unroll
+                        if (i > 0) {
+                            // the P V before must have landed
+                            ok = wait(bars.pv[s], pv_n + i - 1);
+                            if (!ok)
+                                break;
+                            fence_after();
+#pragma unroll 1
                             for (int c = 0; c < D / 32; ++c) {
                                 uint32_t o[32];
-                                const uint32_t col = lanes + O_COL + s * 128 + c * 32;
-                                tmem_ld32(col, o);
+                                tmem_ld32(o_col + c * 32, o);
                                 tmem_ld_wait();
 #pragma unroll
-                                for (int i = 0; i < 32; ++i)
-                                    o[i] = __float_as_uint(__uint_as_float(o[i]) * a);
-                                tmem_st32(col, o);
+                                for (int e = 0; e < 32; ++e)
+                                    o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
+                                tmem_st32(o_col + c * 32, o);
                             }
                         }
                     }
@@ -818,30 +837,30 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                     const uint64_t c22 = pair2(p.c2, p.c2), ref2 = pair2(-ref, -ref);
                     uint64_t sums[4] = {0, 0, 0, 0};
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
+                    for (int c = 0; c < SW / 32; ++c) {
                         uint32_t h[16];
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            float a, b;
-                            split2(fma2(pair2(__uint_as_float(x[c * 32 + 2 * i]),
-                                              __uint_as_float(x[c * 32 + 2 * i + 1])), c22, ref2), a, b);
+                        for (int e = 0; e < 16; ++e) {
+                            float a, d;
+                            split2(fma2(pair2(__uint_as_float(x[c * 32 + 2 * e]),
+                                              __uint_as_float(x[c * 32 + 2 * e + 1])), c22, ref2), a, d);
                             a = ex2_ftz(a);
-                            b = ex2_ftz(b);
-                            sums[i & 3] = add2(sums[i & 3], pair2(a, b));
-                            h[i] = tc::pack_half2(a, b);
+                            d = ex2_ftz(d);
+                            sums[e & 3] = add2(sums[e & 3], pair2(a, d));
+                            h[e] = tc::pack_half2(a, d);
                         }
-                        tmem_st16(lanes + buf * 128 + c * 16, h);
-                    }
-                    {
-                        float a, b;
-                        split2(add2(add2(sums[0], sums[1]), add2(sums[2], sums[3])), a, b);
-                        l += a + b;
+                        tmem_st16(s_col + b * SW + c * 16, h);
                     }
                     tmem_st_wait();
                     fence_before();
                     __syncwarp();
                     if (lane == 0)
-                        mbar_arrive(smem_u32(two ? &bars.p_pair[s] : &bars.p_one[buf]));
+                        mbar_arrive(smem_u32(&bars.p_full[s][b]));
+                    {
+                        float a, d;
+                        split2(add2(add2(sums[0], sums[1]), add2(sums[2], sums[3])), a, d);
+                        l += a + d;
+                    }
                 }
                 if (ok && n > 0) {
                     ok = wait(bars.o_full[s], on);
@@ -851,6 +870,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                     break;
                 fence_after();
                 // ---- the unit's rows, or this piece's partial of them
+                const bool live = r < p.tpt * p.group && i_tok < pc.x.ntok;
                 const float inv = l > 0.f ? 1.f / l : 0.f;
                 __half *dst = p.out + ((long long)(pc.x.tok + i_tok) * p.hq + pc.kv * p.group + r % p.group) * D;
                 float4 *part = reinterpret_cast<float4 *>(p.part) + (size_t)max(pc.slot, 0) * (D / 4) * C::ROWS +
@@ -859,30 +879,30 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                 for (int c = 0; c < D / 32; ++c) {
                     uint32_t o[32];
                     if (n > 0) {
-                        tmem_ld32(lanes + O_COL + s * 128 + c * 32, o);
+                        tmem_ld32(o_col + c * 32, o);
                         tmem_ld_wait();
                     } else {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            o[i] = 0;
+                        for (int e = 0; e < 32; ++e)
+                            o[e] = 0;
                     }
                     if (!live)
                         continue;
                     if (pc.slot >= 0) {
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            part[(size_t)(c * 8 + i) * C::ROWS] =
-                                make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
-                                            __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
+                        for (int e = 0; e < 8; ++e)
+                            part[(size_t)(c * 8 + e) * C::ROWS] =
+                                make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
+                                            __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
                     } else {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
+                        for (int e = 0; e < 4; ++e) {
                             uint32_t h[4];
 #pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                h[e] = tc::pack_half2(__uint_as_float(o[8 * i + 2 * e]) * inv,
-                                                      __uint_as_float(o[8 * i + 2 * e + 1]) * inv);
-                            *reinterpret_cast<uint4 *>(dst + c * 32 + i * 8) = make_uint4(h[0], h[1], h[2], h[3]);
+                            for (int k = 0; k < 4; ++k)
+                                h[k] = tc::pack_half2(__uint_as_float(o[8 * e + 2 * k]) * inv,
+                                                      __uint_as_float(o[8 * e + 2 * k + 1]) * inv);
+                            *reinterpret_cast<uint4 *>(dst + c * 32 + e * 8) = make_uint4(h[0], h[1], h[2], h[3]);
                         }
                     }
                 }
@@ -897,15 +917,11 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                 if (pc.first_part && s == 0 && r == 0)
                     p.split[w] = make_int4(pc.e, pc.kv,
                                            static_cast<int>(((t0 + pc.last + 1) * We - 1) / T) - w + 1, 0);
+                used[0] += (m_parts + 1) / 2;
+                used[1] += m_parts / 2;
+                pv_n += m_parts;
             }
             tiles += n;
-            if (two) {
-                pair_n += n;
-            } else {
-                one_n[0] += (n + 1) / 2;
-                one_n[1] += n / 2;
-                pv_n += n;
-            }
         }
     }
     __syncthreads();
@@ -1176,7 +1192,8 @@ FA_API int fa_prefill(const void *q, const void *k_cache, const void *v_cache,
     // weighs every key alike, as this does
     const double c2 = fabs(static_cast<double>(scale)) * 1.4426950408889634;
     p.c2 = c2 < 1e-37 ? 1e-37f : static_cast<float>(c2);
-    p.idesc_qk = 1u << 4 | (scale < 0.f ? 1u << 13 : 0u) | (BN >> 3) << 17 | (BM >> 4) << 24;
+    const uint32_t sw = D == 128 ? Cfg<128>::SW : Cfg<256>::SW;
+    p.idesc_qk = 1u << 4 | (scale < 0.f ? 1u << 13 : 0u) | (sw >> 3) << 17 | (BM >> 4) << 24;
     p.W = sp.W;
     p.max_ents = sp.max_ents;
     char *ws = static_cast<char *>(workspace);
