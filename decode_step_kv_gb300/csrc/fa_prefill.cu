@@ -526,7 +526,8 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                     mbar_expect_tx(bar, STAGE_BYTES);
                 __syncwarp();
                 if (slab < 2)
-                    tma_load(dst + slab * SLAB + g * br * 128, map, ds * 128 + slab * 64, row, bar);
+                    tma_load(dst + slab * SLAB + g * br * 128, map, ds * 128 + slab * 64, row < 0 ? p.oob_row : row,
+                             bar);
                 ++it;
             }
             return true;
@@ -535,21 +536,16 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
             const int n = pc.k1 - pc.k0;
             if (n == 0)
                 continue;
-            // the cache row of this lane's group of key tile k; oob_row for groups no row sees,
-            // and, with a bit set, for unmapped blocks
-            auto rows = [&](int j, uint32_t &bits) {
-                int row = p.oob_row;
-                bool bad = false;
+            // the cache row of this lane's group of key tile j; oob_row for groups no row sees,
+            // -1 for an unmapped block
+            auto rows = [&](int j) {
                 const int t = j < n ? pc.key_tile(pc.k0 + j) * BN + g * br : pc.x.hi;
-                if (t < pc.x.hi && (t + br > pc.x.lo || t < p.sink)) {
-                    const long long r = tc::tile_row(p.cache, pc.x.b, pc.kv, t);
-                    bad = r < 0;
-                    row = bad ? p.oob_row : static_cast<int>(r);
-                }
-                bits = __ballot_sync(0xffffffffu, bad && slab == 0);
-                return row;
+                return t < pc.x.hi && (t + br > pc.x.lo || t < p.sink)
+                           ? static_cast<int>(tc::tile_row(p.cache, pc.x.b, pc.kv, t))
+                           : p.oob_row;
             };
-            auto k_tile = [&](int row, uint32_t bits) {
+            auto k_tile = [&](int row) {
+                const uint32_t bits = __ballot_sync(0xffffffffu, row < 0 && slab == 0);
                 if (lane == 0) {
                     if (bits)
                         flag(FA_STATUS_BAD_BLOCK);
@@ -559,9 +555,8 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                 return tile(&tmK, row);
             };
             // in the order of their products: K0 (K1), then V(j), K(j + LEAD)
-            uint32_t bits0, bits1, bits2;
-            int row0 = rows(0, bits0), row1 = rows(1, bits1), row2;
-            ok = k_tile(row0, bits0);
+            int row0 = rows(0), row1 = rows(1);
+            ok = k_tile(row0);
             if (ok && qn > 0)
                 ok = wait(bars.q_empty, qn - 1);
             if (!ok)
@@ -578,15 +573,14 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
             ++qn;
             __syncwarp();
             if (LEAD == 2 && n > 1)
-                ok = k_tile(row1, bits1);
+                ok = k_tile(row1);
             for (int j = 0; ok && j < n; ++j) {
-                row2 = rows(j + 2, bits2);          // looked up while the ring is full
+                const int row2 = rows(j + 2);       // looked up a tile before its copies (LEAD 1)
                 ok = tile(&tmV, row0);
                 if (ok && j + LEAD < n)
-                    ok = LEAD == 1 ? k_tile(row1, bits1) : k_tile(row2, bits2);
+                    ok = k_tile(LEAD == 1 ? row1 : row2);
                 row0 = row1;
                 row1 = row2;
-                bits1 = bits2;
             }
         }
         // no copy is left in flight when the CTA ends
@@ -777,15 +771,15 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                     if (!ok)
                         break;
                     fence_after();
+                    uint32_t x[SW];
+#pragma unroll
+                    for (int c = 0; c < SW / 32; ++c)
+                        tmem_ld32(s_col + b * SW + c * 32, x + c * 32);
                     const int kb = pc.key_tile(pc.k0 + i / PARTS) * BN + half * SW;
                     const uint32_t bits =
                         *reinterpret_cast<volatile uint32_t *>(&bars.bits[(tiles + i / PARTS) % BITS]);
                     const bool edge = kb + SW - 1 > at_lo || bits ||
                                       (pc.x.window > 0 && kb <= at_hi - pc.x.window && kb + SW > p.sink);
-                    uint32_t x[SW];
-#pragma unroll
-                    for (int c = 0; c < SW / 32; ++c)
-                        tmem_ld32(s_col + b * SW + c * 32, x + c * 32);
                     tmem_ld_wait();
                     if (edge) {
                         const int hi = at - kb, lo = pc.x.window > 0 ? hi - pc.x.window + 1 : -1;
@@ -838,16 +832,21 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                     uint64_t sums[4] = {0, 0, 0, 0};
 #pragma unroll
                     for (int c = 0; c < SW / 32; ++c) {
+                        // a step for all 32 before the next: a dozen exponentials in flight
                         uint32_t h[16];
+                        float w[32];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            split2(fma2(pair2(__uint_as_float(x[c * 32 + 2 * e]),
+                                              __uint_as_float(x[c * 32 + 2 * e + 1])), c22, ref2),
+                                   w[2 * e], w[2 * e + 1]);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            w[e] = ex2_ftz(w[e]);
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
-                            float a, d;
-                            split2(fma2(pair2(__uint_as_float(x[c * 32 + 2 * e]),
-                                              __uint_as_float(x[c * 32 + 2 * e + 1])), c22, ref2), a, d);
-                            a = ex2_ftz(a);
-                            d = ex2_ftz(d);
-                            sums[e & 3] = add2(sums[e & 3], pair2(a, d));
-                            h[e] = tc::pack_half2(a, d);
+                            h[e] = tc::pack_half2(w[2 * e], w[2 * e + 1]);
+                            sums[e & 3] = add2(sums[e & 3], pair2(w[2 * e], w[2 * e + 1]));
                         }
                         tmem_st16(s_col + b * SW + c * 16, h);
                     }
