@@ -54,7 +54,7 @@ struct Cfg {
     static constexpr size_t SLOT_BYTES = (size_t)ROWS * D * sizeof(float);
 };
 
-// A row tile of a sequence.
+// A row tile of a sequence: the rows of a CTA, or of a cluster of two.
 struct Ent {
     int b, tok;                     // sequence; first row of q
     int ntok, at;                   // tokens; position of the first
@@ -73,15 +73,15 @@ struct Args {
     int oob_row;                    // a cache row beyond the tensor: reads as zeros
     float c2;
     uint32_t idesc_qk;
-    int W;                          // CTAs of the main kernel
+    int W;                          // CTAs (clusters) of the main kernel
     int max_ents;
     // workspace
     Ent *ents;
     long long *pos;                 // [max_ents + 1] first position of each entry
     int *ebase;                     // [B + 1] first entry of each sequence
-    int4 *split;                    // [W] the unit that CTA w leaves to its successors: entry, kv, CTAs
-    float *part;                    // [2 W] slots of [D / 4][ROWS] float4
-    float2 *ml;                     // [2 W][ROWS]
+    int4 *split;                    // [CTAs] the unit that a CTA leaves to its successors: entry, kv, parts
+    float *part;                    // [2 CTAs] slots of [D / 4][ROWS] float4
+    float2 *ml;                     // [2 CTAs][ROWS]
 };
 
 // ------------------------------------------------------------ the plan
@@ -196,6 +196,7 @@ __device__ __forceinline__ int ctas_for(const Args &p, long long T)
 
 struct Piece {
     Ent x;
+    int tok, ntok, at;              // this CTA's share of the row tile: as in Ent
     int e, kv, k0, k1;              // key tiles [k0, k1) of unit (e, kv)
     int slot;                       // partial slot, -1: the whole unit
     bool first_part;                // a partial from the unit's first tile
@@ -206,9 +207,12 @@ struct Piece {
 // The pieces of a stretch of `len` positions, in order.
 struct Pieces {
     int e, kv, us, len;             // us: the current unit's first tile, counted from the stretch's start
-    __device__ __forceinline__ void start(const Args &p, int e_, long long t0, long long t1)
+    int skip, most;                 // tokens of the row tile before this CTA's, and its most
+    __device__ __forceinline__ void start(const Args &p, int e_, long long t0, long long t1, int skip_, int most_)
     {
         e = e_;
+        skip = skip_;
+        most = most_;
         const int unit = p.ents[e].n + UNIT_COST;
         const long long off = t0 - p.pos[e];
         kv = static_cast<int>(off / unit);
@@ -218,8 +222,12 @@ struct Pieces {
     __device__ __forceinline__ bool next(const Args &p, Piece &q)
     {
         while (us - UNIT_COST < len) {      // the last unit ends where the last stretch does
-            if (e != q.e)               // kept over its KV heads
+            if (e != q.e) {             // kept over its KV heads
                 q.x = p.ents[e];
+                q.tok = q.x.tok + skip;
+                q.at = q.x.at + skip;
+                q.ntok = min(max(q.x.ntok - skip, 0), most);
+            }
             const int n = q.x.n;
             const bool empty = n == 0 && us >= UNIT_COST;       // zero rows
             q.k0 = empty ? 0 : max(-us, 0);
@@ -265,12 +273,31 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar)
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
+// The same box into both CTAs of the cluster, each at the same place and barrier.
+__device__ __forceinline__ void tma_load_both(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
+                 ".multicast::cluster [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
+                 "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "h"((unsigned short)3)
+                 : "memory");
+}
+
 // Arrives on bar when the products issued so far by this thread are done.
 __device__ __forceinline__ void mma_commit(uint32_t lead, uint32_t bar)
 {
     asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
                  "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
                  "r"(lead)
+                 : "memory");
+}
+
+// The same on the barrier at this place in both CTAs of the cluster.
+__device__ __forceinline__ void mma_commit_both(uint32_t lead, uint32_t bar)
+{
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+                 "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+                 " [%0], %2;\n\t}" ::"r"(bar),
+                 "r"(lead), "h"((unsigned short)3)
                  : "memory");
 }
 
@@ -284,7 +311,8 @@ __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::aft
 // units of 16 bytes) and the slab distance, so a step adds to it.
 constexpr uint32_t DESC_HI = 1024 >> 4 | 1u << 14 | 2u << 29;
 constexpr uint32_t DESC_V = (SLAB >> 4) << 16;
-__device__ __forceinline__ uint32_t desc_lo(uint32_t addr) { return addr >> 4; }
+// (an address in a cluster carries its CTA's number above the 18 bits of the offset)
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr) { return addr >> 4 & 0x3fff; }
 
 // `lead` is set in one lane; the others run along, so that the warp never
 // diverges around the products and their operands stay in uniform registers.
@@ -405,8 +433,14 @@ __device__ __forceinline__ void clean(const Args &p, const Piece &pc, int k, uin
 // Warp 0 loads, warps 1 and 3 issue the products of streams 0 and 1, warps 4-7 and
 // 8-11 own their rows.  Every stream has two S buffers of SW keys, so that its
 // products run ahead of its softmax: Q K^T of part i + 2 of the keys follows P V of
-// part i, whose columns it takes over.  A piece whose tokens fill one stream leaves
-// the other out: it waits for none of its barriers.
+// part i, whose columns it takes over.  A piece whose tokens do not reach a stream
+// leaves it out: it waits for none of its barriers.
+//
+// CL = 2: a cluster of two CTAs takes two row tiles of one KV head side by side.
+// Each loads half of every K and V tile into both, so that L2 is read once for
+// both: at head_dim 256 a CTA's 128 rows take 128 KB per 2048 tensor cycles, which
+// L2 does not deliver to every SM at once.  The two share the stages' barriers and
+// nothing else.
 struct Bars {
     uint64_t full[STAGES], empty[STAGES];
     uint64_t q_full, q_empty;
@@ -419,7 +453,7 @@ struct Bars {
     int e0;
 };
 
-template <int D>
+template <int D, int CL>
 __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
     attend_kernel(const Args p, const __grid_constant__ CUtensorMap tmQ,
                   const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV)
@@ -434,12 +468,12 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
     static_assert(sizeof(Bars) <= 512, "barriers fit their space");
     const uint32_t sQ = smem_u32(smem), ring = sQ + C::Q_BYTES;
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-    const int w = blockIdx.x;
+    const int w = blockIdx.x / CL, rank = blockIdx.x % CL;   // a cluster's CTAs follow one another
 
     if (warp == 0 && lane == 0) {
         for (int i = 0; i < STAGES; ++i) {
             mbar_init(smem_u32(&bars.full[i]), 1);
-            mbar_init(smem_u32(&bars.empty[i]), NS);
+            mbar_init(smem_u32(&bars.empty[i]), CL * NS);
         }
         mbar_init(smem_u32(&bars.q_full), 1);
         mbar_init(smem_u32(&bars.q_empty), NS);
@@ -486,8 +520,12 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
             bars.e0 = lo;
     }
     if (threadIdx.x == 0)
-        p.split[w] = make_int4(-1, 0, 0, 0);
-    __syncthreads();
+        p.split[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    __syncwarp();
+    if constexpr (CL == 2)
+        tc::cluster_sync();         // the other CTA's barriers are there
+    else
+        __syncthreads();
     fence_after();
     const uint32_t tmem = bars.tmem;
     constexpr uint32_t O_COL = 256;
@@ -497,7 +535,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
     pc.e = -1;
     bool ok = working;
     if (working)
-        walk.start(p, bars.e0, t0, t1);
+        walk.start(p, bars.e0, t0, t1, rank * NS * p.tpt, NS * p.tpt);
     auto wait = [&](uint64_t &bar, uint32_t count) {      // the bar's phase number `count`
         if (mbar_wait_warp(smem_u32(&bar), count & 1))
             return true;
@@ -505,7 +543,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
             flag(FA_STATUS_WAIT_TIMEOUT);
         return false;
     };
-    auto paired = [&](const Piece &q) { return NS == 2 && q.x.ntok > p.tpt; };
+    auto takes = [&](int s) { return pc.ntok > s * p.tpt; };     // the piece has rows of stream s
 
     // key tiles that Q K^T runs ahead of P V by
     constexpr int LEAD = 2 / PARTS;
@@ -525,9 +563,14 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                 if (lane == 0)
                     mbar_expect_tx(bar, STAGE_BYTES);
                 __syncwarp();
-                if (slab < 2)
-                    tma_load(dst + slab * SLAB + g * br * 128, map, ds * 128 + slab * 64, row < 0 ? p.oob_row : row,
-                             bar);
+                const int y = row < 0 ? p.oob_row : row;
+                if constexpr (CL == 2) {
+                    if (slab < 2 && g * 2 / groups == rank)
+                        tma_load_both(dst + slab * SLAB + g * br * 128, map, ds * 128 + slab * 64, y, bar);
+                } else {
+                    if (slab < 2)
+                        tma_load(dst + slab * SLAB + g * br * 128, map, ds * 128 + slab * 64, y, bar);
+                }
                 ++it;
             }
             return true;
@@ -563,12 +606,12 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                 break;
             if (lane == 0) {
                 const uint32_t bar = smem_u32(&bars.q_full);
-                const int box = p.group * p.tpt * 128, streams = paired(pc) ? 2 : 1;
+                const int box = p.group * p.tpt * 128, streams = takes(0) + (NS == 2 && takes(1));
                 mbar_expect_tx(bar, streams * (D / 64) * box);
                 for (int s = 0; s < streams; ++s)
                     for (int c = 0; c < D / 64; ++c)
                         tma_load_3d(sQ + s * BM * D * 2 + c * SLAB, &tmQ, c * 64, pc.kv * p.group,
-                                    pc.x.tok + s * p.tpt, bar);
+                                    pc.tok + s * p.tpt, bar);
             }
             ++qn;
             __syncwarp();
@@ -583,9 +626,12 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                 row1 = row2;
             }
         }
-        // no copy is left in flight when the CTA ends
-        for (uint32_t i = it > STAGES ? it - STAGES : 0; i < it; ++i)
+        // no copy is left in flight when the CTA ends, nor an arrival of the other CTA's
+        for (uint32_t i = it > STAGES ? it - STAGES : 0; i < it; ++i) {
             mbar_wait_warp(smem_u32(&bars.full[i % STAGES]), i / STAGES & 1);
+            if (CL == 2)
+                mbar_wait_warp(smem_u32(&bars.empty[i % STAGES]), i / STAGES & 1);
+        }
         if (qn > 0)
             mbar_wait_warp(smem_u32(&bars.q_full), (qn - 1) & 1);
     } else if (warp == 1 || (NS == 2 && warp == 3)) {
@@ -613,7 +659,10 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
             }
         };
         auto release = [&](uint32_t st) {               // refilled when the products are done
-            mma_commit(lead, smem_u32(&bars.empty[st]));
+            if constexpr (CL == 2)
+                mma_commit_both(lead, smem_u32(&bars.empty[st]));
+            else
+                mma_commit(lead, smem_u32(&bars.empty[st]));
         };
         // S of buffer b <- Q K^T: dims 128 ds .. of the keys from row 64 * half of stage st
         auto qk = [&](int b, int half, int ds, uint32_t st) {
@@ -657,7 +706,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
             const int n = __shfl_sync(0xffffffffu, pc.k1 - pc.k0, 0);
             if (n == 0)
                 continue;
-            mine = s == 0 || __shfl_sync(0xffffffffu, paired(pc), 0);
+            mine = __shfl_sync(0xffffffffu, takes(s), 0);
             ok = wait(bars.q_full, qn);
             ++qn;
             if constexpr (PARTS == 2) {
@@ -758,12 +807,12 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         uint32_t tiles = 0, on = 0, pv_n = 0, used[2] = {0, 0};
         while (ok && walk.next(p, pc)) {
             const int n = pc.k1 - pc.k0, m_parts = n * PARTS;
-            if (s == 0 || paired(pc)) {
+            if (takes(s)) {
                 const int i_tok = s * p.tpt + r / p.group;
-                const int at = pc.x.at + i_tok;
+                const int at = pc.at + i_tok;
                 // positions of this stream's first and last row
-                const int at_lo = pc.x.at + s * p.tpt;
-                const int at_hi = pc.x.at + min((s + 1) * p.tpt, pc.x.ntok) - 1;
+                const int at_lo = pc.at + s * p.tpt;
+                const int at_hi = pc.at + min((s + 1) * p.tpt, pc.ntok) - 1;
                 float m = -INFINITY, l = 0.f;
                 for (int i = 0; ok && i < m_parts; ++i) {
                     const int b = i & 1, half = PARTS == 2 ? b : 0;
@@ -869,9 +918,9 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                     break;
                 fence_after();
                 // ---- the unit's rows, or this piece's partial of them
-                const bool live = r < p.tpt * p.group && i_tok < pc.x.ntok;
+                const bool live = r < p.tpt * p.group && i_tok < pc.ntok;
                 const float inv = l > 0.f ? 1.f / l : 0.f;
-                __half *dst = p.out + ((long long)(pc.x.tok + i_tok) * p.hq + pc.kv * p.group + r % p.group) * D;
+                __half *dst = p.out + ((long long)(pc.tok + i_tok) * p.hq + pc.kv * p.group + r % p.group) * D;
                 float4 *part = reinterpret_cast<float4 *>(p.part) + (size_t)max(pc.slot, 0) * (D / 4) * C::ROWS +
                                s * BM + r;
 #pragma unroll
@@ -914,7 +963,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                         mbar_arrive(smem_u32(&bars.o_empty[s]));
                 }
                 if (pc.first_part && s == 0 && r == 0)
-                    p.split[w] = make_int4(pc.e, pc.kv,
+                    p.split[blockIdx.x] = make_int4(pc.e, pc.kv,
                                            static_cast<int>(((t0 + pc.last + 1) * We - 1) / T) - w + 1, 0);
                 used[0] += (m_parts + 1) / 2;
                 used[1] += m_parts / 2;
@@ -928,13 +977,14 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
     }
+    if constexpr (CL == 2)
+        tc::cluster_sync();         // neither CTA leaves while the other may still reach it
 }
 
 // ------------------------------------------------------------ the merge
-// CTA (y, w): 16 columns of 256 / (D / 16)... of the unit that CTA w of the main
-// kernel began and left to the next ones: their partials in order, weighed by
-// 2^(m - M).
-template <int D>
+// CTA (x, w): 256 of the (row, 16 columns) of the unit that CTA w of the main kernel
+// began and left to the next ones: their partials in order, weighed by 2^(m - M).
+template <int D, int CL>
 __global__ void __launch_bounds__(256) merge_kernel(const Args p)
 {
     using C = Cfg<D>;
@@ -948,10 +998,10 @@ __global__ void __launch_bounds__(256) merge_kernel(const Args p)
     const int idx = blockIdx.x * 256 + threadIdx.x;
     const int row = idx % C::ROWS, c16 = idx / C::ROWS;
     const int s = row / BM, r = row % BM;
-    const int i_tok = s * p.tpt + r / p.group;
+    const int i_tok = (w % CL * C::NS + s) * p.tpt + r / p.group;
     if (r >= p.tpt * p.group || i_tok >= x.ntok)
         return;
-    auto slot = [&](int i) { return (size_t)(i == 0 ? 2 * w + 1 : 2 * (w + i)); };
+    auto slot = [&](int i) { return (size_t)(i == 0 ? 2 * w + 1 : 2 * (w + CL * i)); };
     float M = -INFINITY;
     for (int i = 0; i < u.z; ++i)
         M = fmaxf(M, p.ml[slot(i) * C::ROWS + row].x);
@@ -985,21 +1035,23 @@ __global__ void __launch_bounds__(256) merge_kernel(const Args p)
 
 // Sizes of a call and the layout of its workspace.
 struct Space {
-    int tpt, per, max_ents, W;
+    int cl, tpt, per, max_ents, W;
     size_t ents, pos, ebase, split, ml, part, total;    // offsets, and the bytes in all
 };
 
-static Space space_of(int batch, int n_tokens, int hq, int hkv, int D, long long cap, int sms)
+static Space space_of(int cl, int batch, int n_tokens, int hq, int hkv, int D, long long cap, int sms)
 {
     Space s = {};
+    s.cl = cl;
     const int ns = D == 128 ? Cfg<128>::NS : Cfg<256>::NS;
     const int rows = D == 128 ? Cfg<128>::ROWS : Cfg<256>::ROWS;
     const size_t slot = D == 128 ? Cfg<128>::SLOT_BYTES : Cfg<256>::SLOT_BYTES;
     s.tpt = BM / (hq / hkv);
-    s.per = ns * s.tpt;
+    s.per = cl * ns * s.tpt;
     s.max_ents = n_tokens / s.per + (batch < n_tokens ? batch : n_tokens);
     const double most = (double)s.max_ents * hkv * ((cap + BN - 1) / BN + UNIT_COST) / MIN_POS;
-    s.W = most < 1 ? 1 : most < sms ? static_cast<int>(most) : sms;
+    const int room = sms / cl > 0 ? sms / cl : 1;
+    s.W = most < 1 ? 1 : most < room ? static_cast<int>(most) : room;
     size_t at = 0;
     auto take = [&](size_t n) {
         const size_t here = at;
@@ -1009,11 +1061,26 @@ static Space space_of(int batch, int n_tokens, int hq, int hkv, int D, long long
     s.ents = take((size_t)s.max_ents * sizeof(Ent));
     s.pos = take(((size_t)s.max_ents + 1) * sizeof(long long));
     s.ebase = take(((size_t)batch + 1) * sizeof(int));
-    s.split = take((size_t)s.W * sizeof(int4));
-    s.ml = take((size_t)2 * s.W * rows * sizeof(float2));
-    s.part = take((size_t)2 * s.W * slot);
+    s.split = take((size_t)s.W * cl * sizeof(int4));
+    s.ml = take((size_t)2 * s.W * cl * rows * sizeof(float2));
+    s.part = take((size_t)2 * s.W * cl * slot);
     s.total = at;
     return s;
+}
+
+// CTAs per cluster: two where the sequences' rows fill a cluster's on average.
+static int cluster_of(int batch, int n_tokens, int hq, int hkv, int D)
+{
+    const int rows = 2 * (D == 128 ? Cfg<128>::ROWS : Cfg<256>::ROWS);
+    return (long long)n_tokens * (hq / hkv) >= (long long)batch * rows ? 2 : 1;
+}
+
+// Enough for the call's own form and, with smaller sizes, for either.
+static size_t space_need(int batch, int n_tokens, int hq, int hkv, int D, long long cap, int sms)
+{
+    const size_t a = space_of(1, batch, n_tokens, hq, hkv, D, cap, sms).total;
+    const size_t b = space_of(2, batch, n_tokens, hq, hkv, D, cap, sms).total;
+    return a > b ? a : b;
 }
 
 // [rows][D] of fp16 in boxes of `br` rows x 64 columns, 128-byte swizzle; q as
@@ -1033,7 +1100,7 @@ static int encode_map(CUtensorMap *map, const void *base, int rank, const cuuint
     return 0;
 }
 
-template <int D>
+template <int D, int CL>
 static cudaError_t launch(const Args &p, const CUtensorMap &tmQ, const CUtensorMap &tmK,
                           const CUtensorMap &tmV, int per, cudaStream_t st)
 {
@@ -1047,7 +1114,7 @@ static cudaError_t launch(const Args &p, const CUtensorMap &tmQ, const CUtensorM
     {
         std::lock_guard<std::mutex> lock(mu);
         if (dev >= 64 || !done[dev]) {
-            e = cudaFuncSetAttribute(attend_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+            e = cudaFuncSetAttribute(attend_kernel<D, CL>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
             if (e != cudaSuccess)
                 return e;
             if (dev < 64)
@@ -1059,22 +1126,27 @@ static cudaError_t launch(const Args &p, const CUtensorMap &tmQ, const CUtensorM
     if (e != cudaSuccess)
         return e;
     cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = CL;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cfg.stream = st;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    cfg.gridDim = dim3(p.W);
+    cfg.numAttrs = CL == 2 ? 2 : 1;
+    cfg.gridDim = dim3(p.W * CL);
     cfg.blockDim = dim3(C::THREADS);
     cfg.dynamicSmemBytes = C::SMEM;
-    e = cudaLaunchKernelEx(&cfg, attend_kernel<D>, p, tmQ, tmK, tmV);
+    e = cudaLaunchKernelEx(&cfg, attend_kernel<D, CL>, p, tmQ, tmK, tmV);
     if (e != cudaSuccess)
         return e;
-    cfg.gridDim = dim3(C::ROWS * (D / 16) / 256, p.W);
+    cfg.numAttrs = 1;
+    cfg.gridDim = dim3(C::ROWS * (D / 16) / 256, p.W * CL);
     cfg.blockDim = dim3(256);
     cfg.dynamicSmemBytes = 0;
-    e = cudaLaunchKernelEx(&cfg, merge_kernel<D>, p);
+    e = cudaLaunchKernelEx(&cfg, merge_kernel<D, CL>, p);
     return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
@@ -1101,7 +1173,7 @@ FA_API size_t fa_prefill_workspace_size(int batch, int n_tokens, int n_q_heads, 
         return 0;
     if (num_sms <= 0 && device_sms(&num_sms) != 0)
         return 0;
-    return space_of(batch, n_tokens, n_q_heads, n_kv_heads, head_dim, max_kv_len, num_sms).total;
+    return space_need(batch, n_tokens, n_q_heads, n_kv_heads, head_dim, max_kv_len, num_sms);
 }
 
 FA_API int fa_prefill(const void *q, const void *k_cache, const void *v_cache,
@@ -1151,7 +1223,8 @@ FA_API int fa_prefill(const void *q, const void *k_cache, const void *v_cache,
     int sms = 0;
     if (const int rc = device_sms(&sms))
         return rc;
-    const Space sp = space_of(batch, n_tokens, n_q_heads, n_kv_heads, D, cap, sms);
+    const int cl = cluster_of(batch, n_tokens, n_q_heads, n_kv_heads, D);
+    const Space sp = space_of(cl, batch, n_tokens, n_q_heads, n_kv_heads, D, cap, sms);
     const size_t need = sp.total;
     if (!workspace || workspace_bytes < need)
         return fail(FA_ERR_WORKSPACE, "fa_prefill: workspace %zu bytes, need %zu", workspace_bytes,
@@ -1183,8 +1256,9 @@ FA_API int fa_prefill(const void *q, const void *k_cache, const void *v_cache,
     p.group = n_q_heads / n_kv_heads;
     p.tpt = sp.tpt;
     p.sink = n_sink;
-    // boxes of as many rows as always lie together: the largest power of two in a page
-    const int br = paged ? (page_size & -page_size) < BN ? (page_size & -page_size) : BN : 64;
+    // boxes of as many rows as always lie together, the largest power of two in a page; at most
+    // half a tile, which is what a CTA of a cluster loads
+    const int br = paged && (page_size & -page_size) < 64 ? (page_size & -page_size) : 64;
     p.lg_br = log2_of(br);
     p.oob_row = static_cast<int>(rows);
     // a negative scale: the product negates Q; the running maximum wants c2 > 0, and 0
@@ -1217,8 +1291,10 @@ FA_API int fa_prefill(const void *q, const void *k_cache, const void *v_cache,
     if (rc)
         return rc;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = D == 128 ? launch<128>(p, tmQ, tmK, tmV, sp.per, st)
-                                   : launch<256>(p, tmQ, tmK, tmV, sp.per, st);
+    const cudaError_t e = cl == 2 ? (D == 128 ? launch<128, 2>(p, tmQ, tmK, tmV, sp.per, st)
+                                              : launch<256, 2>(p, tmQ, tmK, tmV, sp.per, st))
+                                  : (D == 128 ? launch<128, 1>(p, tmQ, tmK, tmV, sp.per, st)
+                                              : launch<256, 1>(p, tmQ, tmK, tmV, sp.per, st));
     if (e != cudaSuccess)
         return fail(FA_ERR_CUDA, "fa_prefill: launch failed: %s", cudaGetErrorString(e));
     return 0;

@@ -93,6 +93,17 @@ def test_lengths(D, new, lens):
     run_prefill(Layout(len(new), 2, max(lens), True, page=16, seed=1), lens, new, 8, D, seed=3)
 
 
+@pytest.mark.parametrize("D", [128, 256])
+@pytest.mark.parametrize("hq,hkv", [(8, 1), (10, 2)])
+@pytest.mark.parametrize("new,lens,window,sink", [
+    ([600], [600], [0], 0), ([1100], [1700], [0], 0), ([513, 1, 700, 0], [513, 300, 701, 9], [0, 0, 0, 0], 0),
+    ([650, 1000], [900, 1000], [100, 300], 5), ([900, 300], [500, 2000], [0, 0], 0)])
+def test_clusters(D, hq, hkv, new, lens, window, sink):
+    """Chunks long enough for two CTAs side by side on one KV head, ends in the first or the second."""
+    run_prefill(Layout(len(new), hkv, max(lens), True, page=16, seed=12), lens, new, hq, D,
+                window=window if any(window) else None, sink=sink, seed=4)
+
+
 @pytest.mark.parametrize("page", [16, 32, 48, 64, 128, 256])
 def test_pages(page):
     run_prefill(Layout(2, 2, 400, True, page=page, seed=5), [400, 333], [150, 20], 8, 128)
