@@ -549,29 +549,35 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
     constexpr int LEAD = 2 / PARTS;
     if (warp == 0) {
         // ---------------------------------------------------------- loads
-        uint32_t it = 0, qn = 0, tiles = 0;     // stages filled, Q tiles loaded, key tiles so far
+        uint32_t stage = 0, phase = 1, it = 0, qn = 0, tiles = 0;   // (stages filled, Q tiles, key tiles)
         const int br = 1 << p.lg_br, groups = BN >> p.lg_br;
         const int g = lane % groups, slab = lane / groups;      // a lane per group of rows and 64 dims
+        const bool copies = slab < 2 && (CL == 1 || g * 2 / groups == rank);
+        const uint32_t to = ring + slab * SLAB + g * br * 128;
         // a K or V tile: DS stages of 128 dims
         auto tile = [&](const CUtensorMap *map, int row) {
+            const int y = row < 0 ? p.oob_row : row;
 #pragma unroll
             for (int ds = 0; ds < DS; ++ds) {
-                const uint32_t s = it % STAGES;
-                if (it >= STAGES && !wait(bars.empty[s], it / STAGES - 1))
+                // (the first round of stages: the phase before a barrier's first counts as done)
+                if (!wait(bars.empty[stage], phase))
                     return false;
-                const uint32_t bar = smem_u32(&bars.full[s]), dst = ring + s * STAGE_BYTES;
+                const uint32_t bar = smem_u32(&bars.full[stage]);
                 if (lane == 0)
                     mbar_expect_tx(bar, STAGE_BYTES);
                 __syncwarp();
-                const int y = row < 0 ? p.oob_row : row;
-                if constexpr (CL == 2) {
-                    if (slab < 2 && g * 2 / groups == rank)
-                        tma_load_both(dst + slab * SLAB + g * br * 128, map, ds * 128 + slab * 64, y, bar);
-                } else {
-                    if (slab < 2)
-                        tma_load(dst + slab * SLAB + g * br * 128, map, ds * 128 + slab * 64, y, bar);
+                if (copies) {
+                    const uint32_t dst = to + stage * STAGE_BYTES;
+                    if constexpr (CL == 2)
+                        tma_load_both(dst, map, ds * 128 + slab * 64, y, bar);
+                    else
+                        tma_load(dst, map, ds * 128 + slab * 64, y, bar);
                 }
                 ++it;
+                if (++stage == STAGES) {
+                    stage = 0;
+                    phase ^= 1;
+                }
             }
             return true;
         };
@@ -579,13 +585,29 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
             const int n = pc.k1 - pc.k0;
             if (n == 0)
                 continue;
-            // the cache row of this lane's group of key tile j; oob_row for groups no row sees,
-            // -1 for an unmapped block
-            auto rows = [&](int j) {
+            // This lane's group of key tile j lies in block `look(j)` of the table, which is read
+            // a tile before it is needed; its cache row is row_of(j, block): oob_row for groups
+            // that no row sees, -1 for an unmapped block
+            auto token = [&](int j) {
                 const int t = j < n ? pc.key_tile(pc.k0 + j) * BN + g * br : pc.x.hi;
-                return t < pc.x.hi && (t + br > pc.x.lo || t < p.sink)
-                           ? static_cast<int>(tc::tile_row(p.cache, pc.x.b, pc.kv, t))
-                           : p.oob_row;
+                return t < pc.x.hi && (t + br > pc.x.lo || t < p.sink) ? t : -1;
+            };
+            auto look = [&](int j) {
+                const int t = token(j);
+                return p.cache.bt && t >= 0
+                           ? p.cache.bt[(long long)pc.x.b * p.cache.max_blocks + t / p.cache.page_size]
+                           : 0;
+            };
+            auto row_of = [&](int j, int block) {
+                const int t = token(j);
+                if (t < 0)
+                    return p.oob_row;
+                if (!p.cache.bt)
+                    return static_cast<int>(((long long)pc.x.b * p.cache.Hkv + pc.kv) * p.cache.cap + t);
+                if (block < 0 || block >= p.cache.num_blocks)
+                    return -1;
+                return static_cast<int>(((long long)block * p.cache.Hkv + pc.kv) * p.cache.page_size +
+                                        t % p.cache.page_size);
             };
             auto k_tile = [&](int row) {
                 const uint32_t bits = __ballot_sync(0xffffffffu, row < 0 && slab == 0);
@@ -598,7 +620,9 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                 return tile(&tmK, row);
             };
             // in the order of their products: K0 (K1), then V(j), K(j + LEAD)
-            int row0 = rows(0), row1 = rows(1);
+            const int block0 = look(0), block1 = look(1);
+            int ahead = look(2);
+            int row0 = row_of(0, block0), row1 = row_of(1, block1);
             ok = k_tile(row0);
             if (ok && qn > 0)
                 ok = wait(bars.q_empty, qn - 1);
@@ -618,7 +642,8 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
             if (LEAD == 2 && n > 1)
                 ok = k_tile(row1);
             for (int j = 0; ok && j < n; ++j) {
-                const int row2 = rows(j + 2);       // looked up a tile before its copies (LEAD 1)
+                const int row2 = row_of(j + 2, ahead);
+                ahead = look(j + 3);
                 ok = tile(&tmV, row0);
                 if (ok && j + LEAD < n)
                     ok = k_tile(LEAD == 1 ? row1 : row2);
