@@ -27,6 +27,7 @@ namespace fa {
 namespace rope {
 
 constexpr int THREADS = 256;
+constexpr int ROWS = 2;             // rows of a thread in flight together
 
 struct Turn {                       // the rotation, the same for every row of a call
     const unsigned long long *freqs;    // [rot_dim / 2] turns per position, 2^64 = one turn
@@ -36,29 +37,44 @@ struct Turn {                       // the rotation, the same for every row of a
     float eps;
 };
 
+// 8 consecutive elements as they lie in memory, and as floats.
 template <typename T>
-__device__ __forceinline__ void load8(const T *src, float (&x)[8])
-{
-    if constexpr (sizeof(T) == 4) {
-        const float4 a = *reinterpret_cast<const float4 *>(src);
-        const float4 b = reinterpret_cast<const float4 *>(src)[1];
-        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-        x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-    } else {
-        const uint4 v = *reinterpret_cast<const uint4 *>(src);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+struct Raw {
+    uint4 v[sizeof(T) / 2];
+    __device__ __forceinline__ void load(const T *src)
+    {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float2 f;
-            if constexpr (std::is_same<T, __half>::value)
-                f = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
-            else
-                f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w[i]));
-            x[2 * i] = f.x;
-            x[2 * i + 1] = f.y;
+        for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i)
+            v[i] = reinterpret_cast<const uint4 *>(src)[i];
+    }
+    __device__ __forceinline__ void zero()
+    {
+#pragma unroll
+        for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i)
+            v[i] = make_uint4(0u, 0u, 0u, 0u);
+    }
+    __device__ __forceinline__ void get(float (&x)[8]) const
+    {
+#pragma unroll
+        for (int k = 0; k < static_cast<int>(sizeof(T) / 2); ++k) {
+            const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if constexpr (sizeof(T) == 4) {
+                    x[4 * k + i] = __uint_as_float(w[i]);
+                } else {
+                    float2 f;
+                    if constexpr (std::is_same<T, __half>::value)
+                        f = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
+                    else
+                        f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w[i]));
+                    x[2 * i] = f.x;
+                    x[2 * i + 1] = f.y;
+                }
+            }
         }
     }
-}
+};
 
 template <typename T>
 __device__ __forceinline__ void store8(T *dst, const float (&x)[8])
@@ -119,12 +135,12 @@ struct Angles {
     }
 };
 
-// One row's chunks x, y normed (w, v: the weight's) and turned, in place.  Every
-// lane of the row's D / 16 takes part.
-template <int D, bool NORM>
+// One row's chunks x, y normed and turned, in place.  w, v: the weight's chunks; a row
+// with `plain` set has none and is only turned.  Every lane of the row's D / 16 takes part.
+template <int D, bool NORM, typename In>
 __device__ __forceinline__ void norm_turn(const Turn &t, const Chunks<D> &at, const Angles &g,
-                                          float (&x)[8], float (&y)[8], const float (&w)[8],
-                                          const float (&v)[8])
+                                          float (&x)[8], float (&y)[8], const Raw<In> &w, const Raw<In> &v,
+                                          bool plain, bool still = false)
 {
     if constexpr (NORM) {
         float s = 0.f;
@@ -134,14 +150,19 @@ __device__ __forceinline__ void norm_turn(const Turn &t, const Chunks<D> &at, co
 #pragma unroll
         for (int m = D / 32; m >= 1; m >>= 1)
             s += __shfl_xor_sync(0xffffffffu, s, m);
-        const float r = rsqrtf(s * (1.f / D) + t.eps);
+        if (!plain) {
+            const float r = rsqrtf(s * (1.f / D) + t.eps);
+            float a[8], b[8];
+            w.get(a);
+            v.get(b);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            x[i] *= r * w[i];
-            y[i] *= r * v[i];
+            for (int i = 0; i < 8; ++i) {
+                x[i] *= r * a[i];
+                y[i] *= r * b[i];
+            }
         }
     }
-    if (!at.turned)
+    if (!at.turned || still)
         return;
     if (t.inter) {
 #pragma unroll
@@ -188,24 +209,34 @@ __global__ void __launch_bounds__(THREADS) rope_kernel(const RopeArgs p)
     Angles g;
     if (live)
         g.set(p.turn, c, p.turn.rot ? p.positions[n] : 0);
-    float w[8], v[8];
+    Raw<In> w, v;
     if constexpr (NORM) {
-        load8(static_cast<const In *>(p.w) + at.a, w);
-        load8(static_cast<const In *>(p.w) + at.b, v);
+        w.load(static_cast<const In *>(p.w) + at.a);
+        v.load(static_cast<const In *>(p.w) + at.b);
     }
-    for (int i = 0; i < p.per; ++i) {       // the same count in every lane: the norm's shuffles
-        const int h = h0 + i;
-        float x[8] = {}, y[8] = {};
-        if (h < h1) {
-            const In *src = static_cast<const In *>(p.x) + n * p.x_stride + (long long)h * D;
-            load8(src + at.a, x);
-            load8(src + at.b, y);
+    const In *src = static_cast<const In *>(p.x) + n * p.x_stride;
+    Out *dst = static_cast<Out *>(p.out) + n * p.out_stride;
+    for (int i = 0; i < p.per; i += ROWS) {     // the same count in every lane: the norm's shuffles
+        Raw<In> a[ROWS], b[ROWS];
+#pragma unroll
+        for (int k = 0; k < ROWS; ++k) {
+            a[k].zero();
+            b[k].zero();
+            if (h0 + i + k < h1) {
+                a[k].load(src + (h0 + i + k) * D + at.a);
+                b[k].load(src + (h0 + i + k) * D + at.b);
+            }
         }
-        norm_turn<D, NORM>(p.turn, at, g, x, y, w, v);
-        if (h < h1) {
-            Out *dst = static_cast<Out *>(p.out) + n * p.out_stride + (long long)h * D;
-            store8(dst + at.a, x);
-            store8(dst + at.b, y);
+#pragma unroll
+        for (int k = 0; k < ROWS; ++k) {
+            float x[8], y[8];
+            a[k].get(x);
+            b[k].get(y);
+            norm_turn<D, NORM, In>(p.turn, at, g, x, y, w, v, false);
+            if (h0 + i + k < h1) {
+                store8(dst + (h0 + i + k) * D + at.a, x);
+                store8(dst + (h0 + i + k) * D + at.b, y);
+            }
         }
     }
 }
@@ -282,13 +313,12 @@ __device__ __forceinline__ void quantize16(const float (&x)[8], const float (&y)
 
 // A group of D / 16 threads takes `per` consecutive rows of one token, whose rows
 // are its query heads, then its key heads, then its value heads.
-template <int D, typename In>
+template <int D, typename In, bool NORM, bool VI8>
 __global__ void __launch_bounds__(THREADS) rope_append_kernel(const AppendArgs p)
 {
     constexpr int L = D / 16;
     const int c = threadIdx.x % L;
-    const int hkv = p.cache.Hkv;
-    const int rows = p.hq + 2 * hkv;
+    const int hkv = p.cache.Hkv, keys = p.hq + hkv, rows = keys + hkv;
     const long long group = (long long)blockIdx.x * (THREADS / L) + threadIdx.x / L;
     const int parts = (rows + p.per - 1) / p.per;
     const long long n = group / parts;
@@ -298,84 +328,82 @@ __global__ void __launch_bounds__(THREADS) rope_append_kernel(const AppendArgs p
     const Chunks<D> at(p.turn, c);
     Angles g;
     long long cache_row = -1;       // of KV head 0; heads are `step` rows apart
-    long long step = 0;
+    int step = 0;
     if (b >= 0) {
         const int i = static_cast<int>(n) - (p.starts ? __ldg(p.starts + b) : b);
-        const long long t = (long long)p.positions[b] + i;
-        if (r0 < p.hq + hkv && p.turn.rot)
+        const int first_at = p.positions[b];
+        const long long t = (long long)first_at + i;
+        if (r0 < keys && p.turn.rot)
             g.set(p.turn, c, p.rope_pos ? p.rope_pos[b] + i : static_cast<int>(t));
         if (r1 > p.hq) {
             const bool first = c == 0 && r0 <= p.hq;    // one report per token
-            if (t < 0 || t >= p.cache.cap || p.positions[b] < 0) {
+            if (t >= p.cache.cap || first_at < 0) {
                 if (first)
                     flag(FA_STATUS_POS_RANGE);
             } else {
-                const long long row = row_offset(p.cache, b, 0, static_cast<int>(t), 1);
-                if (row < 0 && first)
+                cache_row = row_offset(p.cache, b, 0, static_cast<int>(t), 1);
+                if (cache_row < 0 && first)
                     flag(FA_STATUS_BAD_BLOCK);
-                cache_row = row;
-                step = p.cache.bt ? p.cache.page_size : p.cache.cap;
+                step = p.cache.bt ? p.cache.page_size : static_cast<int>(p.cache.cap);
             }
         }
     }
-    for (int i = 0; i < p.per; ++i) {       // the same count in every lane: the shuffles
-        const int r = r0 + i;
-        const bool is_q = r < p.hq, is_k = !is_q && r < p.hq + hkv;
-        const int h = is_q ? r : is_k ? r - p.hq : r - p.hq - hkv;
-        const bool live = r < r1;
-        // a value's 16 elements are consecutive
-        const int ca = is_q || is_k ? at.a : 16 * c, cb = is_q || is_k ? at.b : 16 * c + 8;
-        float x[8] = {}, y[8] = {}, w[8] = {}, v[8] = {};
-        const void *weight = is_q ? p.qw : is_k ? p.kw : nullptr;
-        if (live) {
-            const In *src = static_cast<const In *>(is_q ? p.q : is_k ? p.k : p.v) +
-                            n * (is_q ? p.q_stride : is_k ? p.k_stride : p.v_stride) +
-                            (long long)h * D;
-            load8(src + ca, x);
-            load8(src + cb, y);
-            if (weight) {
-                load8(static_cast<const In *>(weight) + ca, w);
-                load8(static_cast<const In *>(weight) + cb, v);
-            }
-        }
-        if (__any_sync(0xffffffffu, weight != nullptr)) {
-            float u[8], z[8];
+    const In *const q = static_cast<const In *>(p.q) + n * p.q_stride;
+    const In *const k = static_cast<const In *>(p.k) + n * p.k_stride - (long long)p.hq * D;
+    const In *const v = static_cast<const In *>(p.v) + n * p.v_stride - (long long)keys * D;
+    for (int i = 0; i < p.per; i += ROWS) {     // the same count in every lane: the shuffles
+        Raw<In> ra[ROWS], rb[ROWS];
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                u[j] = x[j], z[j] = y[j];
-            norm_turn<D, true>(p.turn, at, g, u, z, w, v);
-            if (weight) {
+        for (int u = 0; u < ROWS; ++u) {
+            const int r = r0 + i + u;
+            ra[u].zero();
+            rb[u].zero();
+            if (r < r1) {
+                // a value's 16 elements are consecutive
+                const In *src = (r < p.hq ? q : r < keys ? k : v) + r * D;
+                ra[u].load(src + (r < keys ? at.a : 16 * c));
+                rb[u].load(src + (r < keys ? at.b : 16 * c + 8));
+            }
+        }
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    x[j] = u[j], y[j] = z[j];
+        for (int u = 0; u < ROWS; ++u) {
+            const int r = r0 + i + u;
+            const bool is_q = r < p.hq, is_v = r >= keys, live = r < r1;
+            float x[8], y[8];
+            ra[u].get(x);
+            rb[u].get(y);
+            Raw<In> w, z;
+            bool plain = true;
+            if constexpr (NORM) {
+                const void *weight = is_q ? p.qw : is_v ? nullptr : p.kw;
+                plain = !weight;
+                w.zero();
+                z.zero();
+                if (weight && live) {
+                    w.load(static_cast<const In *>(weight) + at.a);
+                    z.load(static_cast<const In *>(weight) + at.b);
+                }
             }
-        }
-        if (!weight && (is_q || is_k))
-            norm_turn<D, false>(p.turn, at, g, x, y, w, v);
-        if (p.v_scales && __any_sync(0xffffffffu, live && !is_q && !is_k)) {
-            uint4 codes;
-            __half s;
-            quantize16(x, y, codes, s);
-            if (live && !is_q && !is_k && cache_row >= 0) {
-                const long long row = cache_row + (long long)h * step;
-                *reinterpret_cast<uint4 *>(static_cast<int8_t *>(p.v_cache) + row * D + 16 * c) = codes;
-                if (c % 2 == 0)
-                    p.v_scales[row * (D / 32) + c / 2] = s;
+            norm_turn<D, NORM, In>(p.turn, at, g, x, y, w, z, plain, is_v);
+            const long long row = cache_row + (long long)(r - (is_v ? keys : p.hq)) * step;
+            if constexpr (VI8) {
+                if (__any_sync(0xffffffffu, live && is_v)) {
+                    uint4 codes;
+                    __half scale;
+                    quantize16(x, y, codes, scale);
+                    if (live && is_v && cache_row >= 0) {
+                        *reinterpret_cast<uint4 *>(static_cast<int8_t *>(p.v_cache) + row * D + 16 * c) = codes;
+                        if (c % 2 == 0)
+                            p.v_scales[row * (D / 32) + c / 2] = scale;
+                    }
+                }
             }
-            if (!is_q && !is_k)
-                continue;
-        }
-        if (!live)
-            continue;
-        if (is_q) {
-            __half *dst = p.q_out + (n * p.hq + h) * D;
-            store8(dst + ca, x);
-            store8(dst + cb, y);
-        } else if (cache_row >= 0) {
-            __half *dst = (is_k ? p.k_cache : static_cast<__half *>(p.v_cache)) +
-                          (cache_row + (long long)h * step) * D;
-            store8(dst + ca, x);
-            store8(dst + cb, y);
+            if (live && (is_q || (cache_row >= 0 && !(VI8 && is_v)))) {
+                __half *dst = is_q ? p.q_out + (n * p.hq + r) * D
+                                   : (is_v ? static_cast<__half *>(p.v_cache) : p.k_cache) + row * D;
+                store8(dst + (is_v ? 16 * c : at.a), x);
+                store8(dst + (is_v ? 16 * c + 8 : at.b), y);
+            }
         }
     }
 }
@@ -437,15 +465,29 @@ static cudaError_t launch_rope(const RopeArgs &p, int dtype, int out_dtype, unsi
     }
 }
 
+template <int D, typename In>
+static cudaError_t launch_append(const AppendArgs &p, unsigned ctas, cudaStream_t st)
+{
+    const bool norm = p.qw || p.kw;
+    if (norm && p.v_scales)
+        rope_append_kernel<D, In, true, true><<<ctas, THREADS, 0, st>>>(p);
+    else if (norm)
+        rope_append_kernel<D, In, true, false><<<ctas, THREADS, 0, st>>>(p);
+    else if (p.v_scales)
+        rope_append_kernel<D, In, false, true><<<ctas, THREADS, 0, st>>>(p);
+    else
+        rope_append_kernel<D, In, false, false><<<ctas, THREADS, 0, st>>>(p);
+    return cudaGetLastError();
+}
+
 template <int D>
 static cudaError_t launch_append(const AppendArgs &p, int dtype, unsigned ctas, cudaStream_t st)
 {
     switch (dtype) {
-    case FA_DTYPE_F32: rope_append_kernel<D, float><<<ctas, THREADS, 0, st>>>(p); break;
-    case FA_DTYPE_F16: rope_append_kernel<D, __half><<<ctas, THREADS, 0, st>>>(p); break;
-    default: rope_append_kernel<D, __nv_bfloat16><<<ctas, THREADS, 0, st>>>(p); break;
+    case FA_DTYPE_F32: return launch_append<D, float>(p, ctas, st);
+    case FA_DTYPE_F16: return launch_append<D, __half>(p, ctas, st);
+    default: return launch_append<D, __nv_bfloat16>(p, ctas, st);
     }
-    return cudaGetLastError();
 }
 
 // The checks that both calls share; 0 or an error already reported.
