@@ -862,6 +862,17 @@ __global__ void __launch_bounds__(Cfg<D, VI8, NG>::NW * 32, Cfg<D, VI8, NG>::CTA
         const bool block_ok = tile_row(p, cw.b, kv, base) >= 0;
         const uint32_t sK = ring + s * C::STAGE_BYTES;
         const uint32_t sV = VI8 ? (FA_I8_INPLACE ? sK : cvt) : sK + C::T_BYTES;
+        // With sinks an int8 scale is split into a power of two, which multiplies the code
+        // exactly, and a factor that multiplies the weight (in [1, 2); a subnormal scale's
+        // is an integer below 1024): one rounding of weight * factor instead of one of the
+        // weight and one of code * scale
+        constexpr bool SPLIT = SK && VI8;
+        auto v_scale = [&](unsigned short bits) -> __half {
+            if constexpr (SPLIT)
+                return __ushort_as_half(static_cast<unsigned short>(bits & 0x7c00 ? bits & 0xfc00 : (bits & 0x8000) | 1));
+            else
+                return __ushort_as_half(bits);
+        };
 
         // int8 V: dequantise the tile into an fp16 tile at sV (same swizzled
         // layout as a TMA-loaded one); keys outside [r0, r1) become zero rows
@@ -902,7 +913,7 @@ __global__ void __launch_bounds__(Cfg<D, VI8, NG>::NW * 32, Cfg<D, VI8, NG>::CTA
                             const int cc = ((lane + 32 * (k0 + j)) / TILE + row) % CPR;
                             uint32_t o[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
                             if (live) {
-                                const __half2 s2 = __half2half2(__ushort_as_half(sb[j]));
+                                const __half2 s2 = __half2half2(v_scale(sb[j]));
                                 dequant4(w[j][0], s2, o[0], o[1]);
                                 dequant4(w[j][1], s2, o[2], o[3]);
                                 dequant4(w[j][2], s2, o[4], o[5]);
@@ -937,7 +948,7 @@ __global__ void __launch_bounds__(Cfg<D, VI8, NG>::NW * 32, Cfg<D, VI8, NG>::CTA
                             asm volatile("ld.shared.u16 %0, [%1];"
                                          : "=h"(sb)
                                          : "r"(sc + (row * (D / 32) + cc / 2) * 2));
-                            const __half2 s2 = __half2half2(__ushort_as_half(sb));
+                            const __half2 s2 = __half2half2(v_scale(sb));
                             dequant4(w0, s2, o[0], o[1]);
                             dequant4(w1, s2, o[2], o[3]);
                             dequant4(w2, s2, o[4], o[5]);
@@ -1025,6 +1036,7 @@ __global__ void __launch_bounds__(Cfg<D, VI8, NG>::NW * 32, Cfg<D, VI8, NG>::CTA
             }
             const int ka = base + g4, kb = base + g4 + 8;
             uint32_t pb0[NG], pb1[NG];
+            float pw[SPLIT ? NG : 1][4];        // SPLIT: the weights before their factors
 #pragma unroll
             for (int gi = 0; gi < NG; ++gi) {
                 float *sc = sc4[gi];
@@ -1075,8 +1087,12 @@ __global__ void __launch_bounds__(Cfg<D, VI8, NG>::NW * 32, Cfg<D, VI8, NG>::CTA
                 l[gi][0] += p0 + p2;
                 l[gi][1] += p1 + p3;
                 // ---- P^T as the PV B operand (keys x columns), via movmatrix
-                pb0[gi] = movmatrix_t(pack_half2(p0, p1));
-                pb1[gi] = movmatrix_t(pack_half2(p2, p3));
+                if constexpr (SPLIT) {
+                    pw[gi][0] = p0, pw[gi][1] = p1, pw[gi][2] = p2, pw[gi][3] = p3;
+                } else {
+                    pb0[gi] = movmatrix_t(pack_half2(p0, p1));
+                    pb1[gi] = movmatrix_t(pack_half2(p2, p3));
+                }
             }
             // ---- O^T += V^T . P^T  (rows: head_dim; cols: columns); the V
             // fragments serve every group
@@ -1087,6 +1103,24 @@ __global__ void __launch_bounds__(Cfg<D, VI8, NG>::NW * 32, Cfg<D, VI8, NG>::CTA
                 for (int mt = 0; mt < KS; ++mt) {
                     uint32_t a0, a1, a2, a3;
                     ldsm_x4_t(swz(sV, vrow, mt * 2 + (mi & 1)), a0, a1, a2, a3);
+                    if constexpr (SPLIT) {
+                        if (mt % 2 == 0) {      // a block of 32 elements: keys g4 and g4 + 8
+                            const uint32_t at = sK + C::T_BYTES + C::V8_BYTES + (g4 * (D / 32) + mt / 2) * 2;
+                            auto factor = [&](uint32_t addr) {
+                                unsigned short s;
+                                asm volatile("ld.shared.u16 %0, [%1];" : "=h"(s) : "r"(addr));
+                                return s & 0x7c00 ? __half2float(__ushort_as_half(static_cast<unsigned short>(
+                                                        (s & 0x3ff) | 0x3c00)))
+                                                  : static_cast<float>(s & 0x3ff);
+                            };
+                            const float f0 = factor(at), f1 = factor(at + 8 * (D / 32) * 2);
+#pragma unroll
+                            for (int gi = 0; gi < NG; ++gi) {
+                                pb0[gi] = movmatrix_t(pack_half2(pw[gi][0] * f0, pw[gi][1] * f0));
+                                pb1[gi] = movmatrix_t(pack_half2(pw[gi][2] * f1, pw[gi][3] * f1));
+                            }
+                        }
+                    }
 #pragma unroll
                     for (int gi = 0; gi < NG; ++gi)
                         mma16816(acc[gi][mt], a0, a1, a2, a3, pb0[gi], pb1[gi]);
@@ -2172,20 +2206,20 @@ FA_API int fa_decode_slots(const void *q, const void *k_cache, const void *v_cac
 // per-column query ranges of several queries and the chunk plan.
 static int call_plan(int batch, int n_q_heads, int n_kv_heads, int D, long long cap, bool vi8,
                      bool ring, int tq, int chunk, long long kv_rows_total, int *sms, Plan *pl,
-                     size_t *need, bool weights = false)
+                     size_t *need, bool weights = false, bool sinks = false)
 {
     const int rc = device_sms(sms);
     if (rc)
         return rc;
     Path path = choose_path();
     if (kv_rows_total >= (1ll << 31)) {
-        if (tq > 1 || chunk > 0 || weights)
+        if (tq > 1 || chunk > 0 || weights || sinks)
             return fail(FA_ERR_LAYOUT, "fa_decode: caches of 2^31 rows or more are not "
                                        "supported with several queries, batch-invariant "
                                        "splits, recorded weights or sinks");
         path = Path::Simt;
     }
-    if (tq > 1 || chunk > 0 || weights)
+    if (tq > 1 || chunk > 0 || weights || sinks)
         path = Path::Mma;
     // a ring's attended range (the last cap tokens) can straddle one more tile
     *pl = make_plan(path, batch, n_q_heads, n_kv_heads, D, ring ? cap + 16 : cap, *sms, vi8, tq,
@@ -2284,7 +2318,7 @@ static int decode_impl(const void *q, const void *k_cache, const void *v_cache,
     Plan pl;
     size_t need = 0;
     int rc = call_plan(batch, n_q_heads, n_kv_heads, D, cap, vi8, ring, tq, chunk,
-                       kv_rows_total, &sms, &pl, &need, half_out);
+                       kv_rows_total, &sms, &pl, &need, acc != nullptr, sinks);
     if (rc)
         return rc;
     WeightSpace wsp = {};
@@ -2448,7 +2482,10 @@ static int decode_impl(const void *q, const void *k_cache, const void *v_cache,
         }
         if (vi8) {
             tmV = tmK;   // unused: int8 V arrives by plain bulk copies
-            if (sinks)
+            if (sinks && pl.cpu > tc::GPH)
+                e = D == 128 ? launch_mma<128, true, false, 2, false, true>(p, tmK, tmV, grid, st)
+                             : launch_mma<256, true, false, 2, false, true>(p, tmK, tmV, grid, st);
+            else if (sinks)
                 e = D == 128 ? launch_mma<128, true, false, 1, false, true>(p, tmK, tmV, grid, st)
                              : launch_mma<256, true, false, 1, false, true>(p, tmK, tmV, grid, st);
             else if (acc)
@@ -2467,7 +2504,10 @@ static int decode_impl(const void *q, const void *k_cache, const void *v_cache,
             const int rv = encode_kv_map(&tmV, v_cache, kv_rows_total, D);
             if (rv)
                 return rv;
-            if (sinks)
+            if (sinks && pl.cpu > tc::GPH)
+                e = D == 128 ? launch_mma<128, false, false, 2, false, true>(p, tmK, tmV, grid, st)
+                             : launch_mma<256, false, false, 2, false, true>(p, tmK, tmV, grid, st);
+            else if (sinks)
                 e = D == 128 ? launch_mma<128, false, false, 1, false, true>(p, tmK, tmV, grid, st)
                              : launch_mma<256, false, false, 1, false, true>(p, tmK, tmV, grid, st);
             else if (acc)
@@ -2610,7 +2650,7 @@ FA_API size_t fa_decode_sinks_workspace_size(int batch, int n_queries, int n_q_h
     size_t need = 0;
     for (bool vi8 : {false, true}) {
         const Plan pl = make_plan(Path::Mma, batch, n_q_heads, n_kv_heads, head_dim, max_kv_len,
-                                  num_sms, vi8, n_queries, 0, true);
+                                  num_sms, vi8, n_queries);
         const size_t n = plan_workspace(pl, batch, n_q_heads, head_dim);
         need = n > need ? n : need;
     }

@@ -27,7 +27,7 @@ namespace fa {
 namespace rope {
 
 constexpr int THREADS = 256;
-constexpr int ROWS = 2;             // rows of a thread in flight together
+constexpr int ROWS = 2;             // rows of a thread in flight together (append)
 
 struct Turn {                       // the rotation, the same for every row of a call
     const unsigned long long *freqs;    // [rot_dim / 2] turns per position, 2^64 = one turn
@@ -97,37 +97,46 @@ __device__ __forceinline__ void store8(T *dst, const float (&x)[8])
     }
 }
 
-// What thread c of a row's D / 16 holds: elements a .. a + 7 and b .. b + 7.
+// What thread c of a row's D / 16 holds: elements a .. a + 7 and b .. b + 7, both 16 bytes
+// (of a 16-bit type) from its neighbours', so that a warp reads and writes whole lines.
 template <int D>
 struct Chunks {
     int a, b;
-    bool turned;
+    bool turned, turned_b;          // (of two halves: one is the other's partner)
     __device__ __forceinline__ Chunks(const Turn &t, int c)
     {
-        turned = c < t.rot / 16;
-        if (t.inter || !turned) {       // 16 elements in a row
-            a = 16 * c;
-            b = a + 8;
-        } else {                        // pairs 8 c .. 8 c + 7 of the two halves
+        const int pairs = t.rot / 16;
+        if (t.inter) {                  // pairs lie within 8 elements
             a = 8 * c;
-            b = a + t.rot / 2;
+            b = a + D / 2;
+            turned = a < t.rot;
+            turned_b = b < t.rot;
+        } else {
+            turned = turned_b = c < pairs;
+            a = turned ? 8 * c : t.rot + 8 * (c - pairs);
+            b = a + (turned ? t.rot : D - t.rot) / 2;
         }
     }
 };
 
-// Sines and cosines of pairs 8 c .. 8 c + 7 at position pos.
+// Sines and cosines of the thread's pairs at position pos: 8 c .. 8 c + 7 of two halves, or
+// interleaved a / 2 .. a / 2 + 3 and b / 2 .. b / 2 + 3.
 struct Angles {
     float cs[8], sn[8];
-    __device__ __forceinline__ void set(const Turn &t, int c, int pos)
+    template <int D>
+    __device__ __forceinline__ void set(const Turn &t, const Chunks<D> &at, int pos)
     {
-        if (c >= t.rot / 16)
+        if (!at.turned)
             return;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const unsigned long long f = __ldg(t.freqs + 8 * c + i);
-            const unsigned long long at = (unsigned long long)(long long)pos * f;
+            if (i >= 4 && !at.turned_b)
+                return;
+            const int j = !t.inter ? at.a + i : i < 4 ? at.a / 2 + i : at.b / 2 + i - 4;
+            const unsigned long long f = __ldg(t.freqs + j);
+            const unsigned long long turn = (unsigned long long)(long long)pos * f;
             // a signed fraction of a half turn, in [-1, 1)
-            const float x = static_cast<float>(static_cast<int>(at >> 32)) * 0x1p-31f;
+            const float x = static_cast<float>(static_cast<int>(turn >> 32)) * 0x1p-31f;
             sincospif(x, &sn[i], &cs[i]);
             sn[i] *= t.magnitude;
             cs[i] *= t.magnitude;
@@ -143,10 +152,16 @@ __device__ __forceinline__ void norm_turn(const Turn &t, const Chunks<D> &at, co
                                           bool plain, bool still = false)
 {
     if constexpr (NORM) {
-        float s = 0.f;
+        uint64_t q[2] = {0, 0};
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            s = fmaf(x[i], x[i], fmaf(y[i], y[i], s));
+        for (int i = 0; i < 8; i += 2) {
+            const uint64_t a = pair2(x[i], x[i + 1]), b = pair2(y[i], y[i + 1]);
+            q[0] = fma2(a, a, q[0]);
+            q[1] = fma2(b, b, q[1]);
+        }
+        float s, s1;
+        split2(add2(q[0], q[1]), s, s1);
+        s += s1;
 #pragma unroll
         for (int m = D / 32; m >= 1; m >>= 1)
             s += __shfl_xor_sync(0xffffffffu, s, m);
@@ -155,10 +170,11 @@ __device__ __forceinline__ void norm_turn(const Turn &t, const Chunks<D> &at, co
             float a[8], b[8];
             w.get(a);
             v.get(b);
+            const uint64_t r2 = pair2(r, r);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                x[i] *= r * a[i];
-                y[i] *= r * b[i];
+            for (int i = 0; i < 8; i += 2) {
+                split2(mul2(pair2(x[i], x[i + 1]), mul2(r2, pair2(a[i], a[i + 1]))), x[i], x[i + 1]);
+                split2(mul2(pair2(y[i], y[i + 1]), mul2(r2, pair2(b[i], b[i + 1]))), y[i], y[i + 1]);
             }
         }
     }
@@ -167,18 +183,25 @@ __device__ __forceinline__ void norm_turn(const Turn &t, const Chunks<D> &at, co
     if (t.inter) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const float a = x[2 * i], b = x[2 * i + 1], c = y[2 * i], d = y[2 * i + 1];
+            const float a = x[2 * i], b = x[2 * i + 1];
             x[2 * i] = a * g.cs[i] - b * g.sn[i];
             x[2 * i + 1] = a * g.sn[i] + b * g.cs[i];
-            y[2 * i] = c * g.cs[i + 4] - d * g.sn[i + 4];
-            y[2 * i + 1] = c * g.sn[i + 4] + d * g.cs[i + 4];
+        }
+        if (at.turned_b) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float a = y[2 * i], b = y[2 * i + 1];
+                y[2 * i] = a * g.cs[i + 4] - b * g.sn[i + 4];
+                y[2 * i + 1] = a * g.sn[i + 4] + b * g.cs[i + 4];
+            }
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float a = x[i], b = y[i];
-            x[i] = a * g.cs[i] - b * g.sn[i];
-            y[i] = a * g.sn[i] + b * g.cs[i];
+        for (int i = 0; i < 8; i += 2) {
+            const uint64_t a = pair2(x[i], x[i + 1]), b = pair2(y[i], y[i + 1]);
+            const uint64_t c = pair2(g.cs[i], g.cs[i + 1]), d = pair2(g.sn[i], g.sn[i + 1]);
+            split2(sub2(mul2(a, c), mul2(b, d)), x[i], x[i + 1]);
+            split2(fma2(a, d, mul2(b, c)), y[i], y[i + 1]);
         }
     }
 }
@@ -195,7 +218,7 @@ struct RopeArgs {
 
 // A group of D / 16 threads takes `per` consecutive heads of one token.
 template <int D, typename In, typename Out, bool NORM>
-__global__ void __launch_bounds__(THREADS) rope_kernel(const RopeArgs p)
+__global__ void __launch_bounds__(THREADS, 4) rope_kernel(const RopeArgs p)
 {
     constexpr int L = D / 16;
     const int c = threadIdx.x % L;
@@ -208,7 +231,7 @@ __global__ void __launch_bounds__(THREADS) rope_kernel(const RopeArgs p)
     const Chunks<D> at(p.turn, c);
     Angles g;
     if (live)
-        g.set(p.turn, c, p.turn.rot ? p.positions[n] : 0);
+        g.set(p.turn, at, p.turn.rot ? p.positions[n] : 0);
     Raw<In> w, v;
     if constexpr (NORM) {
         w.load(static_cast<const In *>(p.w) + at.a);
@@ -216,27 +239,21 @@ __global__ void __launch_bounds__(THREADS) rope_kernel(const RopeArgs p)
     }
     const In *src = static_cast<const In *>(p.x) + n * p.x_stride;
     Out *dst = static_cast<Out *>(p.out) + n * p.out_stride;
-    for (int i = 0; i < p.per; i += ROWS) {     // the same count in every lane: the norm's shuffles
-        Raw<In> a[ROWS], b[ROWS];
-#pragma unroll
-        for (int k = 0; k < ROWS; ++k) {
-            a[k].zero();
-            b[k].zero();
-            if (h0 + i + k < h1) {
-                a[k].load(src + (h0 + i + k) * D + at.a);
-                b[k].load(src + (h0 + i + k) * D + at.b);
-            }
+    for (int h = h0; h < h0 + p.per; ++h) {     // the same count in every lane: the norm's shuffles
+        Raw<In> a, b;
+        a.zero();
+        b.zero();
+        if (h < h1) {
+            a.load(src + h * D + at.a);
+            b.load(src + h * D + at.b);
         }
-#pragma unroll
-        for (int k = 0; k < ROWS; ++k) {
-            float x[8], y[8];
-            a[k].get(x);
-            b[k].get(y);
-            norm_turn<D, NORM, In>(p.turn, at, g, x, y, w, v, false);
-            if (h0 + i + k < h1) {
-                store8(dst + (h0 + i + k) * D + at.a, x);
-                store8(dst + (h0 + i + k) * D + at.b, y);
-            }
+        float x[8], y[8];
+        a.get(x);
+        b.get(y);
+        norm_turn<D, NORM, In>(p.turn, at, g, x, y, w, v, false);
+        if (h < h1) {
+            store8(dst + h * D + at.a, x);
+            store8(dst + h * D + at.b, y);
         }
     }
 }
@@ -272,49 +289,44 @@ __device__ __forceinline__ int sequence_of(const int *starts, int B, int n)
     return lo;
 }
 
-// 32 consecutive elements, 16 in each of two neighbouring lanes, as int8 codes and
+// 32 consecutive elements, 8 in each of four neighbouring lanes, as int8 codes and
 // one fp16 scale: s = fp16(max|x| / 127) of the exact quotient, code = the exact
 // quotient x / s rounded half to even.  The 32-bit quotient of an element lies on
 // the wrong side of a tie only when it equals the tie k + 1/2 itself; then the sign
 // of x - (k + 1/2) s, exact in one fma (a product of 9 by 11 bits), decides.
-__device__ __forceinline__ void quantize16(const float (&x)[8], const float (&y)[8], uint4 &codes,
-                                           __half &scale)
+__device__ __forceinline__ uint2 quantize8(const float (&x)[8], __half &scale)
 {
     float top = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-        top = fmaxf(top, fmaxf(fabsf(x[i]), fabsf(y[i])));
+        top = fmaxf(top, fabsf(x[i]));
     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
     scale = __double2half(static_cast<double>(top) / 127.0);
     const float s = __half2float(scale);
-    uint32_t w[4];
+    uint32_t w[2] = {0, 0};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        w[j] = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float z = j < 2 ? x[4 * j + i] : y[4 * (j - 2) + i];
-            float r = 0.f;
-            if (s != 0.f) {
-                const float t = __fdiv_rn(z, s);
-                r = rintf(t);
-                const float tie = floorf(t) + 0.5f;
-                if (t == tie) {
-                    const float e = fmaf(-tie, s, z);
-                    r = e > 0.f ? tie + 0.5f : e < 0.f ? tie - 0.5f : r;
-                }
-                r = fminf(fmaxf(r, -127.f), 127.f);
+    for (int i = 0; i < 8; ++i) {
+        float r = 0.f;
+        if (s != 0.f) {
+            const float t = __fdiv_rn(x[i], s);
+            r = rintf(t);
+            const float tie = floorf(t) + 0.5f;
+            if (t == tie) {
+                const float e = fmaf(-tie, s, x[i]);
+                r = e > 0.f ? tie + 0.5f : e < 0.f ? tie - 0.5f : r;
             }
-            w[j] |= (static_cast<uint32_t>(static_cast<int>(r)) & 0xffu) << (8 * i);
+            r = fminf(fmaxf(r, -127.f), 127.f);
         }
+        w[i / 4] |= (static_cast<uint32_t>(static_cast<int>(r)) & 0xffu) << (8 * (i % 4));
     }
-    codes = make_uint4(w[0], w[1], w[2], w[3]);
+    return make_uint2(w[0], w[1]);
 }
 
 // A group of D / 16 threads takes `per` consecutive rows of one token, whose rows
 // are its query heads, then its key heads, then its value heads.
 template <int D, typename In, bool NORM, bool VI8>
-__global__ void __launch_bounds__(THREADS) rope_append_kernel(const AppendArgs p)
+__global__ void __launch_bounds__(THREADS, 3) rope_append_kernel(const AppendArgs p)
 {
     constexpr int L = D / 16;
     const int c = threadIdx.x % L;
@@ -334,7 +346,7 @@ __global__ void __launch_bounds__(THREADS) rope_append_kernel(const AppendArgs p
         const int first_at = p.positions[b];
         const long long t = (long long)first_at + i;
         if (r0 < keys && p.turn.rot)
-            g.set(p.turn, c, p.rope_pos ? p.rope_pos[b] + i : static_cast<int>(t));
+            g.set(p.turn, at, p.rope_pos ? p.rope_pos[b] + i : static_cast<int>(t));
         if (r1 > p.hq) {
             const bool first = c == 0 && r0 <= p.hq;    // one report per token
             if (t >= p.cache.cap || first_at < 0) {
@@ -359,10 +371,9 @@ __global__ void __launch_bounds__(THREADS) rope_append_kernel(const AppendArgs p
             ra[u].zero();
             rb[u].zero();
             if (r < r1) {
-                // a value's 16 elements are consecutive
                 const In *src = (r < p.hq ? q : r < keys ? k : v) + r * D;
-                ra[u].load(src + (r < keys ? at.a : 16 * c));
-                rb[u].load(src + (r < keys ? at.b : 16 * c + 8));
+                ra[u].load(src + (r < keys ? at.a : 8 * c));
+                rb[u].load(src + (r < keys ? at.b : 8 * c + D / 2));
             }
         }
 #pragma unroll
@@ -388,21 +399,24 @@ __global__ void __launch_bounds__(THREADS) rope_append_kernel(const AppendArgs p
             const long long row = cache_row + (long long)(r - (is_v ? keys : p.hq)) * step;
             if constexpr (VI8) {
                 if (__any_sync(0xffffffffu, live && is_v)) {
-                    uint4 codes;
-                    __half scale;
-                    quantize16(x, y, codes, scale);
+                    __half s0, s1;
+                    const uint2 c0 = quantize8(x, s0), c1 = quantize8(y, s1);
                     if (live && is_v && cache_row >= 0) {
-                        *reinterpret_cast<uint4 *>(static_cast<int8_t *>(p.v_cache) + row * D + 16 * c) = codes;
-                        if (c % 2 == 0)
-                            p.v_scales[row * (D / 32) + c / 2] = scale;
+                        int8_t *dst = static_cast<int8_t *>(p.v_cache) + row * D + 8 * c;
+                        *reinterpret_cast<uint2 *>(dst) = c0;
+                        *reinterpret_cast<uint2 *>(dst + D / 2) = c1;
+                        if (c % 4 == 0) {
+                            p.v_scales[row * (D / 32) + c / 4] = s0;
+                            p.v_scales[row * (D / 32) + D / 64 + c / 4] = s1;
+                        }
                     }
                 }
             }
             if (live && (is_q || (cache_row >= 0 && !(VI8 && is_v)))) {
                 __half *dst = is_q ? p.q_out + (n * p.hq + r) * D
                                    : (is_v ? static_cast<__half *>(p.v_cache) : p.k_cache) + row * D;
-                store8(dst + (is_v ? 16 * c : at.a), x);
-                store8(dst + (is_v ? 16 * c + 8 : at.b), y);
+                store8(dst + (is_v ? 8 * c : at.a), x);
+                store8(dst + (is_v ? 8 * c + D / 2 : at.b), y);
             }
         }
     }
