@@ -37,7 +37,7 @@ constexpr int BN = 128;             // keys of a tile
 constexpr int STAGES = 5;           // ring of K / V parts of 128 keys x 128 dims
 constexpr int STAGE_BYTES = 32768;
 constexpr int SLAB = 16384;         // 128 rows x 64 columns
-constexpr int UNIT_COST = 2;        // positions charged for a unit's start
+constexpr int UNIT_COST = 3;        // positions charged for a unit's start
 constexpr int MIN_POS = 4;          // fewest positions a CTA is given
 constexpr int BITS = 8;             // key tiles whose unmapped groups are remembered
 
