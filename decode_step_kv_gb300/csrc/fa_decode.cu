@@ -863,13 +863,13 @@ __global__ void __launch_bounds__(Cfg<D, VI8, NG>::NW * 32, Cfg<D, VI8, NG>::CTA
         const uint32_t sK = ring + s * C::STAGE_BYTES;
         const uint32_t sV = VI8 ? (FA_I8_INPLACE ? sK : cvt) : sK + C::T_BYTES;
         // With sinks an int8 scale is split into a power of two, which multiplies the code
-        // exactly, and a factor that multiplies the weight (in [1, 2); a subnormal scale's
-        // is an integer below 1024): one rounding of weight * factor instead of one of the
-        // weight and one of code * scale
+        // exactly, and a factor in [1, 2) that multiplies the weight: one rounding of
+        // weight * factor instead of one of the weight and one of code * scale
         constexpr bool SPLIT = SK && VI8;
         auto v_scale = [&](unsigned short bits) -> __half {
             if constexpr (SPLIT)
-                return __ushort_as_half(static_cast<unsigned short>(bits & 0x7c00 ? bits & 0xfc00 : (bits & 0x8000) | 1));
+                return __float2half_rn(__uint_as_float(
+                    __float_as_uint(__half2float(__ushort_as_half(bits))) & 0xff800000u));
             else
                 return __ushort_as_half(bits);
         };
@@ -1082,8 +1082,12 @@ __global__ void __launch_bounds__(Cfg<D, VI8, NG>::NW * 32, Cfg<D, VI8, NG>::CTA
                     m[gi][0] = n0;
                     m[gi][1] = n1;
                 }
-                const float p0 = ex2(sc[0] - r0m), p1 = ex2(sc[1] - r1m);
-                const float p2 = ex2(sc[2] - r0m), p3 = ex2(sc[3] - r1m);
+                // With sinks the weights (and their sum and O with them) are taken 2^10 times
+                // as large: a sink often takes most of the weight, and the keys behind it,
+                // 2^-10 to 2^-20 of it each, keep their bits in fp16
+                constexpr float UP = SK ? 10.f : 0.f;
+                const float p0 = ex2(sc[0] - (r0m - UP)), p1 = ex2(sc[1] - (r1m - UP));
+                const float p2 = ex2(sc[2] - (r0m - UP)), p3 = ex2(sc[3] - (r1m - UP));
                 l[gi][0] += p0 + p2;
                 l[gi][1] += p1 + p3;
                 // ---- P^T as the PV B operand (keys x columns), via movmatrix
@@ -1109,9 +1113,8 @@ __global__ void __launch_bounds__(Cfg<D, VI8, NG>::NW * 32, Cfg<D, VI8, NG>::CTA
                             auto factor = [&](uint32_t addr) {
                                 unsigned short s;
                                 asm volatile("ld.shared.u16 %0, [%1];" : "=h"(s) : "r"(addr));
-                                return s & 0x7c00 ? __half2float(__ushort_as_half(static_cast<unsigned short>(
-                                                        (s & 0x3ff) | 0x3c00)))
-                                                  : static_cast<float>(s & 0x3ff);
+                                return __uint_as_float(
+                                    (__float_as_uint(__half2float(__ushort_as_half(s))) & 0x7fffffu) | 0x3f800000u);
                             };
                             const float f0 = factor(at), f1 = factor(at + 8 * (D / 32) * 2);
 #pragma unroll

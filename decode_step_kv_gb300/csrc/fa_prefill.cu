@@ -14,8 +14,7 @@
 // 16 steps: Q, K and V from shared memory (TMA, 128-byte swizzle), S and O in
 // TMEM, P written over S in TMEM as fp16.  One softmax thread owns a row: its
 // running maximum and sum never leave it.  O is rescaled only when a row's
-// maximum has grown by more than 2^8 (P then stays below 2^8 in fp16), so the
-// usual tile does not touch O.
+// maximum has grown by more than 2^5, so the usual tile does not touch O.
 //
 // What bounds it: at 128 rows of one KV head a key tile costs 2 x 128 x 128 x
 // 128 x 2 operations for 64 KB of K and V, 512 + 512 tensor cycles, so whole
@@ -40,6 +39,10 @@ constexpr int SLAB = 16384;         // 128 rows x 64 columns
 constexpr int UNIT_COST = 3;        // positions charged for a unit's start
 constexpr int MIN_POS = 4;          // fewest positions a CTA is given
 constexpr int BITS = 8;             // key tiles whose unmapped groups are remembered
+// Weights are taken 2^UP above the reference's 1, so that the keys behind a dominant one
+// (2^-10 to 2^-20 of it each: an attention sink's companions) keep their bits in fp16, and
+// the reference follows a row's maximum when that has outgrown it by 2^GROW: P < 2^15.
+constexpr float UP = 10.f, GROW = 5.f;
 
 template <int D>
 struct Cfg {
@@ -200,13 +203,14 @@ struct Piece {
     int e, kv, k0, k1;              // key tiles [k0, k1) of unit (e, kv)
     int slot;                       // partial slot, -1: the whole unit
     bool first_part;                // a partial from the unit's first tile
-    int last;                       // the unit's last tile, counted from the stretch's first position
+    long long last;                 // the unit's last tile, counted from the stretch's first position
     __device__ __forceinline__ int key_tile(int k) const { return k < x.ns ? k : x.kt0 + k - x.ns; }
 };
 
 // The pieces of a stretch of `len` positions, in order.
 struct Pieces {
-    int e, kv, us, len;             // us: the current unit's first tile, counted from the stretch's start
+    int e, kv;
+    long long us, len;              // us: the current unit's first tile, counted from the stretch's start
     int skip, most;                 // tokens of the row tile before this CTA's, and its most
     __device__ __forceinline__ void start(const Args &p, int e_, long long t0, long long t1, int skip_, int most_)
     {
@@ -216,8 +220,8 @@ struct Pieces {
         const int unit = p.ents[e].n + UNIT_COST;
         const long long off = t0 - p.pos[e];
         kv = static_cast<int>(off / unit);
-        us = static_cast<int>(kv * (long long)unit + UNIT_COST - off);
-        len = static_cast<int>(t1 - t0);
+        us = kv * (long long)unit + UNIT_COST - off;
+        len = t1 - t0;
     }
     __device__ __forceinline__ bool next(const Args &p, Piece &q)
     {
@@ -230,8 +234,8 @@ struct Pieces {
             }
             const int n = q.x.n;
             const bool empty = n == 0 && us >= UNIT_COST;       // zero rows
-            q.k0 = empty ? 0 : max(-us, 0);
-            q.k1 = empty ? 0 : min(len - us, n);
+            q.k0 = empty || us > 0 ? 0 : static_cast<int>(-us);
+            q.k1 = empty ? 0 : len - us < n ? static_cast<int>(len - us) : n;
             q.e = e;
             q.kv = kv;
             const bool whole = q.k0 == 0 && q.k1 == n;
@@ -854,7 +858,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                     for (int e = 0; e < SW; e += 2)
                         tops[e / 2 & 3] = max3(tops[e / 2 & 3], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
                     const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * p.c2;
-                    const bool grow = top > m + 8.f;        // also from -infinity
+                    const bool grow = top > m + GROW;       // also from -infinity
                     if (__any_sync(0xffffffffu, grow)) {
                         const float m1 = fmaxf(m, top);
                         const float a = ex2(m - (m1 == -INFINITY ? 0.f : m1));
@@ -878,7 +882,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                             }
                         }
                     }
-                    const float ref = m == -INFINITY ? 0.f : m;
+                    const float ref = m == -INFINITY ? 0.f : m - UP;
                     const uint64_t c22 = pair2(p.c2, p.c2), ref2 = pair2(-ref, -ref);
                     uint64_t sums[4] = {0, 0, 0, 0};
 #pragma unroll

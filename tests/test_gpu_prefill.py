@@ -277,6 +277,86 @@ def test_captured_replayed_with_other_lengths_and_repeatable():
         assert bool((out[st[2]:] == 9.0).all())
 
 
+def dominated(L, D, hkv, rng):
+    """Keys whose first takes about half of every query's weight, the others an even share."""
+    k = rng.randn(1, hkv, L, D) * 0.02
+    k[:, :, 0, 0] = np.log(L) / 4.0
+    k[:, :, 1:, 0] = 0.0
+    return k.astype(np.float16), rng.randn(1, hkv, L, D).astype(np.float16)
+
+
+def dominated_error(got, q, at, k, v, scale, hkv):
+    want, _ = attend_rows(q, at, k[0].astype(np.float64), v, scale, 0, 0, hkv)
+    # the first key's part is the same value for all: what is left is the others' weights
+    return np.linalg.norm(got - want) / np.linalg.norm(want)
+
+
+@pytest.mark.parametrize("L", [4096, 32768])
+@pytest.mark.parametrize("vscale", [1.0, 0.02])
+def test_keys_behind_a_dominant_one(L, vscale):
+    """Weights of 2^-13 to 2^-16 behind a key that takes half of all keep fp16's 11 bits: the error of
+    independent roundings (2^-11 / sqrt(3) each at most, of the weights and of the output) stays below
+    5e-4 of the output's norm; weights rounded as subnormals (steps of 2^-24) would give 1e-3 and more."""
+    D, hq, hkv, n = 128, 4, 1, 20
+    rng = np.random.RandomState(3)
+    k, v = dominated(L, D, hkv, rng)
+    v = (v * vscale).astype(np.float16)
+    v[:, :, 0] = 0
+    q = rng.randn(n, hq, D).astype(np.float16)
+    q[..., 0] = 4.0
+    dev = [torch.from_numpy(x).cuda() for x in (q, k, v)]
+    out = torch.empty(n, hq, D, dtype=torch.float16, device="cuda")
+    ws = fa.alloc_workspace_prefill(1, n, hq, hkv, D, L)
+    fa.fa_prefill(*dev, None, None, ints([0, n]), ints([L]), hq, hkv, D, 1.0, None, out, workspace=ws)
+    err = dominated_error(f64(out), q.astype(np.float64), np.arange(L - n, L), k, v[0].astype(np.float64), 1.0, hkv)
+    floor = np.sqrt(out.numel()) * 2.0 ** -25 / np.linalg.norm(f64(out))     # subnormal outputs' own rounding
+    assert err <= 5e-4 + floor, (err, floor)
+
+
+@pytest.mark.parametrize("L", [4096, 32768])
+@pytest.mark.parametrize("int8", [False, True])
+def test_sinks_keep_the_keys_behind_them(L, int8):
+    D, hq, hkv = 128, 4, 1
+    rng = np.random.RandomState(3)
+    k, v = dominated(L, D, hkv, rng)
+    v[:, :, 0] = 0
+    s = None
+    val = v.astype(np.float64)
+    if int8:
+        s = (np.abs(v.astype(np.float64).reshape(1, hkv, L, D // 32, 32)).max(-1) / 127).astype(np.float16)
+        codes = np.where(s[..., None] > 0, np.rint(v.astype(np.float64).reshape(1, hkv, L, D // 32, 32) /
+                                                   np.maximum(s[..., None].astype(np.float64), 1e-30)), 0)
+        v = np.clip(codes, -127, 127).reshape(1, hkv, L, D).astype(np.int8)
+        val = values(v, s)
+    q = rng.randn(1, hq, D).astype(np.float16)
+    q[..., 0] = 4.0
+    out = torch.empty(1, hq, D, dtype=torch.float16, device="cuda")
+    fa.fa_decode_sinks(*(torch.from_numpy(x).cuda() for x in (q, k, v)), None if s is None else
+                       torch.from_numpy(s).cuda(), None, ints([L]), hq, hkv, D, 1.0, None, out, n_sink=4,
+                       workspace=fa.alloc_workspace_sinks(1, 1, hq, hkv, D, L))
+    err = dominated_error(f64(out), q.astype(np.float64), [L - 1], k, val[0], 1.0, hkv)
+    floor = np.sqrt(out.numel()) * 2.0 ** -25 / np.linalg.norm(f64(out))
+    assert err <= 5e-4 + floor, (err, floor)
+
+
+@pytest.mark.parametrize("scale", [2.0 ** -24, 3 * 2.0 ** -24, 2.0 ** -14, 500.0])
+def test_sinks_int8_scales_of_any_size(scale):
+    """Subnormal and large scales: code * scale itself, whatever its split."""
+    D, hq, hkv, L = 128, 4, 1, 64
+    rng = np.random.RandomState(5)
+    k = rng.randn(1, hkv, L, D).astype(np.float16)
+    v = rng.randint(-127, 128, (1, hkv, L, D)).astype(np.int8)
+    s = np.full((1, hkv, L, D // 32), scale, dtype=np.float16)
+    s[:, :, ::3] = 0
+    q = rng.randn(1, hq, D).astype(np.float16)
+    out = torch.empty(1, hq, D, dtype=torch.float16, device="cuda")
+    fa.fa_decode_sinks(*(torch.from_numpy(x).cuda() for x in (q, k, v, s)), None, ints([L]), hq, hkv, D, 0.1, None,
+                       out, n_sink=4, workspace=fa.alloc_workspace_sinks(1, 1, hq, hkv, D, L))
+    val = values(v, s)[0]
+    want, size = attend_rows(q.astype(np.float64), [L - 1], k[0].astype(np.float64), val, 0.1, 0, 0, hkv)
+    assert (np.abs(f64(out) - want) <= attend_tolerance(size, L, 127 * scale)).all()
+
+
 # ------------------------------------------------------------------ decode with sinks
 @pytest.mark.parametrize("D", [128, 256])
 @pytest.mark.parametrize("int8", [False, True])
