@@ -38,6 +38,12 @@ constexpr int STAGE_BYTES = 32768;
 constexpr int SLAB = 16384;         // 128 rows x 64 columns
 constexpr int UNIT_COST = 3;        // positions charged for a unit's start
 constexpr int MIN_POS = 4;          // fewest positions a CTA is given
+// Few and short units (at most this many positions on average, their start included) go to
+// a CTA each, more of them where they take most CTAs anyway: a merge of split units costs
+// what two or three tiles in a row do.  64 tokens over 512 keys, 2 units of 4 tiles: 17.1 us
+// whole, 18.4 split; over 1024 keys 23.1 and 19.5; 16 single tokens over 1000 keys, 128
+// units of 8 tiles: 20.6 and 23.8
+constexpr int WHOLE = 8, WHOLE_BUSY = 11;
 constexpr int BITS = 8;             // key tiles whose unmapped groups are remembered
 // Weights are taken 2^UP above the reference's 1, so that the keys behind a dominant one
 // (2^-10 to 2^-20 of it each: an attention sink's companions) keep their bits in fp16, and
@@ -483,9 +489,16 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
     wait_for_previous();
     const int E = p.ebase[p.cache.B];
     const long long T = E > 0 ? p.pos[E] : 0;
-    const int We = T > 0 ? ctas_for(p, T) : 0;
+    const long long units = (long long)E * p.cache.Hkv;
+    const bool whole = units <= p.W && T <= units * (2 * units > p.W ? WHOLE_BUSY : WHOLE);
+    const int We = T > 0 ? whole ? static_cast<int>(units) : ctas_for(p, T) : 0;
     const bool working = w < We;
-    const long long t0 = working ? T * w / We : 0, t1 = working ? T * (w + 1) / We : 0;
+    auto unit_at = [&](int u) {
+        const int e = u / p.cache.Hkv;
+        return e < E ? p.pos[e] + (long long)(u % p.cache.Hkv) * (p.ents[e].n + UNIT_COST) : T;
+    };
+    const long long t0 = !working ? 0 : whole ? unit_at(w) : T * w / We;
+    const long long t1 = !working ? 0 : whole ? unit_at(w + 1) : T * (w + 1) / We;
     if (warp == 0 && working) {
         // the entry that holds position t0, 32 ways at a time
         int lo = 0, hi = E;                         // pos[lo] <= t0 < pos[hi]
