@@ -2651,12 +2651,13 @@ FA_API size_t fa_decode_sinks_workspace_size(int batch, int n_queries, int n_q_h
     if (num_sms <= 0 && device_sms(&num_sms) != 0)
         return 0;
     size_t need = 0;
-    for (bool vi8 : {false, true}) {
-        const Plan pl = make_plan(Path::Mma, batch, n_q_heads, n_kv_heads, head_dim, max_kv_len,
-                                  num_sms, vi8, n_queries);
-        const size_t n = plan_workspace(pl, batch, n_q_heads, head_dim);
-        need = n > need ? n : need;
-    }
+    for (bool vi8 : {false, true})
+        for (bool narrow : {false, true}) {      // a smaller step may take units of 8 columns
+            const Plan pl = make_plan(Path::Mma, batch, n_q_heads, n_kv_heads, head_dim, max_kv_len,
+                                      num_sms, vi8, n_queries, 0, narrow);
+            const size_t n = plan_workspace(pl, batch, n_q_heads, head_dim);
+            need = n > need ? n : need;
+        }
     return need;
 }
 

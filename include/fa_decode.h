@@ -532,8 +532,9 @@ FA_API int fa_decode_sinks(const void *q, const void *k_cache, const void *v_cac
                            int batch, int page_size, int max_blocks_per_seq, int num_blocks,
                            void *workspace, size_t workspace_bytes, void *stream);
 
-/* Scratch bytes for fa_decode_sinks (either V type).  Host-only; 0 for invalid
- * sizes. */
+/* Scratch bytes for fa_decode_sinks (either V type), enough for any call with
+ * these heads and head_dim whose batch, n_queries and capacity are no larger.
+ * Host-only; 0 for invalid sizes. */
 FA_API size_t fa_decode_sinks_workspace_size(int batch, int n_queries, int n_q_heads,
                                              int n_kv_heads, int head_dim, int max_kv_len,
                                              int num_sms);
@@ -575,7 +576,10 @@ FA_API int fa_prefill(const void *q, const void *k_cache, const void *v_cache,
                       int n_tokens, int page_size, int max_blocks_per_seq, int num_blocks,
                       void *workspace, size_t workspace_bytes, void *stream);
 
-/* Scratch bytes for fa_prefill.  Host-only; 0 for invalid sizes. */
+/* Scratch bytes for fa_prefill, enough for any call with these heads and
+ * head_dim whose batch, n_tokens and capacity are no larger (about 40 MB from
+ * a few units of work per SM on: fp32 partials of two units per SM).
+ * Host-only; 0 for invalid sizes. */
 FA_API size_t fa_prefill_workspace_size(int batch, int n_tokens, int n_q_heads, int n_kv_heads,
                                         int head_dim, int max_kv_len, int num_sms);
 

@@ -489,3 +489,98 @@ def test_prompt_in_chunks_then_decode(D, window, sink):
         assert float((whole[b].float() - parts[b].float()).abs().max()) <= 2 * (2.0 ** -10 + 2.0 ** -14) * 5
         assert float((whole[b][-1].float() - one[b].float()).abs().max()) <= 2 * (2.0 ** -10 + 2.0 ** -14) * 5
     assert bool((one == two).all())
+
+
+def test_offsets_beyond_32_bits():
+    """A pool of more than 4 GiB per array, its last blocks in use: append, prefill and decode with sinks."""
+    D, hq, hkv, page, n = 128, 4, 2, 16, 200
+    total = (5 << 30) // (hkv * page * D * 2)
+    kc, vc = (torch.zeros(total, hkv, page, D, dtype=torch.float16, device="cuda") for _ in range(2))
+    assert kc.numel() * 2 > 1 << 32
+    blocks = -(-n // page)
+    table = (total - 1 - torch.arange(blocks, dtype=torch.int32, device="cuda")).view(1, -1).contiguous()
+    x = torch.randn(n, hq + 2 * hkv, D, generator=torch.Generator(device="cuda").manual_seed(1), device="cuda").half()
+    q = torch.empty(n, hq, D, dtype=torch.float16, device="cuda")
+    starts = ints([0, n])
+    fa.fa_rope_append_kv(x[:, :hq], x[:, hq:hq + hkv], x[:, hq + hkv:], q, kc, vc, None, table, starts, ints([0]), None)
+    out = torch.empty_like(q)
+    fa.fa_prefill(q, kc, vc, None, table, starts, ints([n]), hq, hkv, D, 0.1, None, out,
+                  workspace=fa.alloc_workspace_prefill(1, n, hq, hkv, D, blocks * page))
+    one = torch.empty(1, hq, D, dtype=torch.float16, device="cuda")
+    fa.fa_decode_sinks(q[-1:].contiguous(), kc, vc, None, table, ints([n]), hq, hkv, D, 0.1, ints([50]), one, n_sink=3,
+                       workspace=fa.alloc_workspace_sinks(1, 1, hq, hkv, D, blocks * page))
+    k, v = (f64(x[:, a:a + hkv]).transpose(1, 0, 2) for a in (hq, hq + hkv))
+    want, size = attend_rows(f64(q), np.arange(n), k, v, 0.1, 0, 0, hkv)
+    assert (np.abs(f64(out) - want) <= attend_tolerance(size, n, 5.0)).all()
+    want, size = attend_rows(f64(q[-1:]), [n - 1], k, v, 0.1, 50, 3, hkv)
+    assert (np.abs(f64(one) - want) <= attend_tolerance(size, n, 5.0)).all()
+
+
+def test_two_streams_and_a_reader_right_behind():
+    """Two chunks at once, each with its own workspace, each read by what follows it on its stream."""
+    D, hq, hkv, L, n = 128, 16, 4, 5000, 150
+    rng = np.random.RandomState(2)
+    lay = Layout(1, hkv, L, False)
+    data, want = [], []
+    for i in range(2):
+        k, v = (rng.randn(*lay.rows, D).astype(np.float16) for _ in range(2))
+        q = rng.randn(n, hq, D).astype(np.float16)
+        w, size = attend_rows(q.astype(np.float64), np.arange(L - n, L), k[0].astype(np.float64), v[0].astype(np.float64),
+                              D ** -0.5, 0, 0, hkv)
+        want.append((w, attend_tolerance(size, L, 5.0)))
+        data.append([torch.from_numpy(a).cuda() for a in (q, k, v)] +
+                    [torch.empty(n, hq, D, dtype=torch.float16, device="cuda"),
+                     fa.alloc_workspace_prefill(1, n, hq, hkv, D, L)])
+    starts, lens = ints([0, n]), ints([L])
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(4):
+        for i, s in enumerate(streams):
+            q, k, v, out, ws = data[i]
+            with torch.cuda.stream(s):
+                out.fill_(9.0)
+                fa.fa_prefill(q, k, v, None, None, starts, lens, hq, hkv, D, D ** -0.5, None, out, workspace=ws)
+                got[i].append(out.clone())
+    torch.cuda.synchronize()
+    for i in range(2):
+        for out in got[i]:
+            assert (np.abs(f64(out) - want[i][0]) <= want[i][1]).all()
+            assert bool((out == got[i][0]).all())
+
+
+def test_workspaces_of_exact_size_are_enough():
+    """Every byte behind the workspace's end stays."""
+    for B, n, L, hq, hkv, D in ((1, 1, 16, 1, 1, 128), (3, 700, 900, 8, 1, 256), (2, 40, 3000, 8, 2, 128)):
+        size = fa.fa_prefill_workspace_size(B, B * n, hq, hkv, D, L)
+        buf = torch.full((size + 4096,), 77, dtype=torch.uint8, device="cuda")
+        q = torch.randn(B * n, hq, D, device="cuda").half()
+        k, v = (torch.randn(B, hkv, L, D, device="cuda").half() for _ in range(2))
+        out = torch.empty_like(q)
+        fa.fa_prefill(q, k, v, None, None, ints([n * i for i in range(B + 1)]), ints([L] * B), hq, hkv, D, 0.1, None,
+                      out, workspace=buf[:size])
+        assert bool((buf[size:] == 77).all()) and bool(torch.isfinite(out).all())
+
+
+def test_refusals_of_tensors():
+    q = torch.zeros(4, 8, 128, dtype=torch.float16, device="cuda")
+    k = torch.zeros(1, 2, 64, 128, dtype=torch.float16, device="cuda")
+    ws = fa.alloc_workspace_prefill(1, 4, 8, 2, 128, 64)
+    good = dict(q=q, k=k, v=k.clone(), vs=None, starts=ints([0, 4]), lens=ints([4]), out=torch.empty_like(q), ws=ws)
+
+    def call(**kw):
+        a = {**good, **kw}
+        fa.fa_prefill(a["q"], a["k"], a["v"], a["vs"], None, a["starts"], a["lens"], 8, 2, 128, 0.1, None, a["out"],
+                      workspace=a["ws"])
+
+    call()
+    for kw in (dict(q=q.float()), dict(k=k.float()), dict(starts=ints([0, 4, 5])), dict(lens=torch.tensor([4])),
+               dict(out=torch.empty(4, 8, 64, dtype=torch.float16, device="cuda")), dict(q=q.transpose(0, 1)),
+               dict(starts=torch.tensor([0, 4], device="cuda"))):
+        with pytest.raises(ValueError):
+            call(**kw)
+    for kw, code in ((dict(ws=None), -4), (dict(ws=ws[:1000]), -4), (dict(out=q), -7)):
+        with pytest.raises(fa.FaDecodeError) as e:
+            call(**kw)
+        assert e.value.code == code
+    torch.cuda.synchronize()

@@ -135,3 +135,15 @@ def test_workspace_sizes():
         assert f(1, 1, 8, 2, 64, 100, 152) == 0
         assert f(1, 1, 8, 2, 128, -1, 152) == 0
         assert 0 < f(2, 7, 8, 2, 128, 5000, 152) < 1 << 30
+
+
+@pytest.mark.parametrize("D", [128, 256])
+@pytest.mark.parametrize("size", [fa.fa_prefill_workspace_size, fa.fa_decode_sinks_workspace_size])
+def test_workspace_serves_smaller_calls(D, size):
+    rng = np.random.RandomState(1)
+    for _ in range(300):
+        hkv = int(rng.choice([1, 2, 8]))
+        hq = hkv * int(rng.choice([1, 3, 4, 8]))
+        most = [int(2 ** rng.uniform(0, x)) for x in (8, 8, 16)]
+        less = [int(rng.randint(1, m + 1)) for m in most]
+        assert size(less[0], less[1], hq, hkv, D, less[2], 152) <= size(most[0], most[1], hq, hkv, D, most[2], 152)
