@@ -16,15 +16,21 @@
 // running maximum and sum never leave it.  O is rescaled only when a row's
 // maximum has grown by more than 2^5, so the usual tile does not touch O.
 //
-// What bounds it: at 128 rows of one KV head a key tile costs 2 x 128 x 128 x
-// 128 x 2 operations for 64 KB of K and V, 512 + 512 tensor cycles, so whole
-// prompts are bound by the tensor pipe and chunks of few rows by HBM.  With two
-// row tiles (head_dim 128) the products of one run while the other's softmax
-// does; with one, S is double-buffered and the next tile's Q K^T runs meanwhile.
+// What bounds it: 128 keys cost a row tile 4 x 128 x 128 x D operations, at D = 128
+// 1024 tensor cycles, so whole prompts are bound by the products and the softmax
+// (64 exponentials per 64 keys and thread at four cycles a warp, and as much again
+// around them), chunks of few rows by K and V.  Each stream has two S buffers, so
+// that its products run ahead of its softmax.  At D = 128 these hold 64 keys: a
+// 128 x 64 x 16 step takes 52-76 cycles where a 128 x 128 x 16 one takes 64, but TMEM
+// has no room for two of 128 keys beside O, and one buffer a stream, whose Q K^T
+// waits for its P V, took 1943 us for a prompt of 16384 tokens (32 / 8 heads) against
+// 1657.  As it stands: 1525-1600 us (1.38-1.44 PFLOP/s of the 1.91 that a library
+// product reaches; the power cap holds the clocks at 1.65-1.75 GHz), 512 tokens over
+// 131072 keys 751-781 us, 4 prompts of 1K-8K at D = 256 767-786 us.
 //
-// Work over the GPU.  A one-CTA kernel lists the units' tiles as positions of
-// one axis (as the decode plan: UNIT_COST positions per unit beside its tiles),
-// every CTA takes an equal stretch of it, and a unit that a stretch cuts leaves
+// Work over the GPU.  A one-CTA kernel lists the units' tiles as positions of one
+// axis (as the decode plan: UNIT_COST positions per unit beside its tiles), every
+// CTA or cluster takes an equal stretch of it, and a unit that a stretch cuts leaves
 // fp32 partials that a merge kernel joins in a fixed order.
 #include "fa_common.cuh"
 
@@ -36,7 +42,9 @@ constexpr int BN = 128;             // keys of a tile
 constexpr int STAGES = 5;           // ring of K / V parts of 128 keys x 128 dims
 constexpr int STAGE_BYTES = 32768;
 constexpr int SLAB = 16384;         // 128 rows x 64 columns
-constexpr int UNIT_COST = 3;        // positions charged for a unit's start
+// Positions charged for a unit's start (its Q, the pipeline's filling, its epilogue).  1, 2, 3,
+// 4: the 16384-token prompt, 13 units per CTA, 1694, 1602, 1525, 1531 us; others within 2%
+constexpr int UNIT_COST = 3;
 constexpr int MIN_POS = 4;          // fewest positions a CTA is given
 // Few and short units (at most this many positions on average, their start included) go to
 // a CTA each, more of them where they take most CTAs anyway: a merge of split units costs
@@ -424,10 +432,11 @@ __device__ __forceinline__ void clean(const Args &p, const Piece &pc, int k, uin
 // leaves it out: it waits for none of its barriers.
 //
 // CL = 2: a cluster of two CTAs takes two row tiles of one KV head side by side.
-// Each loads half of every K and V tile into both, so that L2 is read once for
-// both: at head_dim 256 a CTA's 128 rows take 128 KB per 2048 tensor cycles, which
-// L2 does not deliver to every SM at once.  The two share the stages' barriers and
-// nothing else.
+// Each loads half of every K and V tile into both, so that L2 is read, and boxes are
+// issued, once for both: at head_dim 256 a CTA's 128 rows take 128 KB per 2048
+// tensor cycles, which L2 does not deliver to every SM at once (897 -> 771 us for 4
+// prompts), and 16-token pages make 16 boxes of a tile (512 tokens over 131072 keys
+// 867 -> 751 us).  The two share the stages' barriers and nothing else.
 struct Bars {
     uint64_t full[STAGES], empty[STAGES];
     uint64_t q_full, q_empty;

@@ -14,11 +14,13 @@
 // no 64-bit floating point, whose rate on this GPU is 1/60 of the 32-bit one.
 // Its top 32 bits go to sincospif.
 //
-// What bounds it: HBM.  A row of D elements is held by D / 16 threads, 16
-// elements each in two chunks of 8 that hold whole pairs, so that a rotation
-// needs no exchange; the norm takes log2(D / 16) shuffles.  A thread's 8 pairs
-// are the same ones in every head, so its sines and cosines are computed once
-// for all the rows of a token that it takes.
+// What bounds it: HBM, then latency.  A row of D elements is held by D / 16 threads,
+// 16 elements each in two chunks of 8 that hold whole pairs, so that a rotation
+// needs no exchange; the norm takes log2(D / 16) shuffles.  A thread's 8 pairs are
+// the same ones in every head, so its sines and cosines are computed once for all
+// the rows of a token that it takes.  Measured: 5 prompts of 1K-5K tokens, 64 + 16
+// heads x 128 in bf16, 617 MB, 123 us (5.0 TB/s); 8 x 2048 tokens of 16 heads x 256 in
+// bf16, 268 MB, 55.6 us (4.8 TB/s); 64 single tokens 5 and 7 us on the GPU.
 #include <cuda_bf16.h>
 
 #include "fa_common.cuh"
@@ -27,7 +29,11 @@ namespace fa {
 namespace rope {
 
 constexpr int THREADS = 256;
-constexpr int ROWS = 2;             // rows of a thread in flight together (append)
+// Rows of a thread in flight together in the append kernel, which is held to 80 registers
+// (three CTAs per SM): 123 us for the 5 prompts above; one row 149, two rows at the 106
+// registers they would take 150.  The rotation alone keeps one row at 64 registers, four
+// CTAs: 55.6 us against 59.4-63.7 with two rows at two and three CTAs.
+constexpr int ROWS = 2;
 
 struct Turn {                       // the rotation, the same for every row of a call
     const unsigned long long *freqs;    // [rot_dim / 2] turns per position, 2^64 = one turn
