@@ -591,13 +591,16 @@ def fa_evict_kv(k_cache, v_cache, acc, block_table, seq_lens, new_lens, *, budge
 def _fp16_cache(name, k_cache, v_cache, v_scales, block_table, n_kv_heads, head_dim, batch, dev):
     """Pointers (K, V, V's scales, table) and sizes (page, max_blocks, num_blocks) of a cache of
     fp16 K and fp16 or int8 V."""
-    hkv, page, blocks, total, rows, _ = _cache_dims(name, k_cache, block_table, batch)
-    if hkv != n_kv_heads:
-        raise ValueError(f"{name}: the cache holds {hkv} heads")
-    row = (*rows, head_dim)
-    return ((_take("k_cache", k_cache, torch.float16, row, dev),
-             _take("v_cache", v_cache, torch.float16 if v_scales is None else torch.int8, row, dev),
-             _take("v_scales", v_scales, torch.float16, (*rows, head_dim // 32), dev)),
+    hkv, page, blocks, total, rows, width = _cache_dims(name, k_cache, block_table, batch)
+    if hkv != n_kv_heads or width != head_dim:
+        raise ValueError(f"{name}: the cache holds {hkv} heads of {width}")
+    shape = k_cache.shape
+    if v_scales is None:
+        v, vs = _take("v_cache", v_cache, torch.float16, shape, dev), None
+    else:
+        v = _take("v_cache", v_cache, torch.int8, shape, dev)
+        vs = _take("v_scales", v_scales, torch.float16, (*rows, head_dim // 32), dev)
+    return ((_take("k_cache", k_cache, torch.float16, None, dev), v, vs),
             _take("block_table", block_table, torch.int32, None, dev), page, blocks, total)
 
 
@@ -686,34 +689,40 @@ def fa_rope_table(rot_dim, base=10000.0, *, scaling=None, factor=1.0, original_l
     return table.to(device), magnitude.value
 
 
-def _heads(name, t, dtype, dev, n=None, heads=None, head_dim=None):
-    """(pointer, token stride, N, H, D) of a tensor [N, H, D] whose tokens' rows may lie apart."""
-    if len(t.shape) != 3:
+def _heads(name, t, dtype, dev, want=None):
+    """(pointer, token stride, shape) of a tensor [N, H, D] whose tokens' rows may lie apart;
+    `want`: the shape it must have."""
+    shape = t.shape
+    if (len(shape) == 3 and t.dtype is dtype and t.get_device() == dev
+            and (want is None or shape == want)):
+        N, H, D = shape
+        s0, s1, s2 = t.stride()
+        if (s2 == 1 and (s1 == D or H == 1)) or N == 0:
+            return t.data_ptr(), s0 if N > 1 else H * D, shape
+    if len(shape) != 3:
         raise ValueError(f"{name} must be [tokens, heads, head_dim]")
-    N, H, D = t.shape
-    if (n is not None and N != n) or (heads is not None and H != heads) or \
-            (head_dim is not None and D != head_dim):
-        raise ValueError(f"{name} must have shape {(n, heads, head_dim)}, got {tuple(t.shape)}")
+    if want is not None and shape != want:
+        raise ValueError(f"{name} must have shape {tuple(want)}, got {tuple(shape)}")
     if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if t.get_device() != dev:
         raise ValueError(f"{name} must be on the current CUDA device, got {t.device}")
-    if N and ((H > 1 and t.stride(1) != D) or t.stride(2) != 1):
-        raise ValueError(f"{name}: a token's heads must be contiguous")
-    return t.data_ptr(), t.stride(0) if N > 1 else H * D, N, H, D
+    raise ValueError(f"{name}: a token's heads must be contiguous")
 
 
 def _dtype(name, t):
-    if t.dtype not in _DTYPES:
+    kind = _DTYPES.get(t.dtype)
+    if kind is None:
         raise ValueError(f"{name} must be fp32, fp16 or bf16, got {t.dtype}")
-    return _DTYPES[t.dtype]
+    return kind
 
 
 def _table(freqs, dev):
     """(pointer, rot_dim) of a table of ``fa_rope_table``; None: no rotation."""
     if freqs is None:
         return None, 0
-    return _take("freqs", freqs, torch.int64, (freqs.numel(),), dev), 2 * freqs.numel()
+    n = freqs.numel()
+    return _take("freqs", freqs, torch.int64, (n,), dev), 2 * n
 
 
 def fa_rope(x, positions, freqs, out, *, weight=None, eps=1e-6, interleaved=False, magnitude=1.0,
@@ -723,8 +732,9 @@ def fa_rope(x, positions, freqs, out, *, weight=None, eps=1e-6, interleaved=Fals
     types, or x itself.  `freqs`, `magnitude`: ``fa_rope_table``'s (freqs None: norm only)."""
     dev = _device()
     kind, out_kind = _dtype("x", x), _dtype("out", out)
-    xp, xs, N, H, D = _heads("x", x, x.dtype, dev)
-    op, os, *_ = _heads("out", out, out.dtype, dev, N, H, D)
+    xp, xs, shape = _heads("x", x, x.dtype, dev)
+    op, os, _ = _heads("out", out, out.dtype, dev, shape)
+    N, H, D = shape
     fp, rot = _table(freqs, dev)
     _check(load().fa_rope(
         xp, kind, op, out_kind, _take("weight", weight, x.dtype, (D,), dev), eps,
@@ -744,20 +754,25 @@ def fa_rope_append_kv(q, k, v, q_out, k_cache, v_cache, v_scales, block_table, s
     dev = _device()
     kind = _dtype("k", k)
     B = positions.shape[0]
-    kp, ks, N, hkv, D = _heads("k", k, k.dtype, dev)
-    vp, vs, *_ = _heads("v", v, k.dtype, dev, N, hkv, D)
+    dtype = k.dtype
+    kp, ks, shape = _heads("k", k, dtype, dev)
+    vp, vs, _ = _heads("v", v, dtype, dev, shape)
+    N, hkv, D = shape
     qp, qs, hq, qo = None, 0, 0, None
     if q is not None:
-        qp, qs, _, hq, _ = _heads("q", q, k.dtype, dev, N, None, D)
+        qp, qs, shape = _heads("q", q, dtype, dev)
+        hq = shape[1]
+        if shape[0] != N or shape[2] != D:
+            raise ValueError(f"q must have shape {(N, hq, D)}, got {tuple(shape)}")
         if q_out is None:
             raise ValueError("fa_rope_append_kv: q_out is required with q")
-        qo = _take("q_out", q_out, torch.float16, (N, hq, D), dev)
+        qo = _take("q_out", q_out, torch.float16, shape, dev)
     c, bt, page, blocks, total = _fp16_cache("fa_rope_append_kv", k_cache, v_cache, v_scales,
                                              block_table, hkv, D, B, dev)
     fp, rot = _table(freqs, dev)
     _check(load().fa_rope_append_kv(
-        qp, kp, vp, kind, qs, ks, vs, _take("q_weight", q_weight, k.dtype, (D,), dev),
-        _take("k_weight", k_weight, k.dtype, (D,), dev), eps, fp, rot, int(interleaved),
+        qp, kp, vp, kind, qs, ks, vs, _take("q_weight", q_weight, dtype, (D,), dev),
+        _take("k_weight", k_weight, dtype, (D,), dev), eps, fp, rot, int(interleaved),
         magnitude, qo, *c, bt, _take("starts", starts, torch.int32, (B + 1,), dev),
         _take("positions", positions, torch.int32, (B,), dev),
         _take("rope_positions", rope_positions, torch.int32, (B,), dev), B, N, hq, hkv, D, page,

@@ -259,3 +259,34 @@ def test_append_in_a_graph_on_another_stream():
         check(q_out, want, size, F16)
         for b in range(B):
             assert (lay.dense(vc.cpu().numpy(), b)[:, b + shift] == x[b, hq + hkv:].cpu().numpy()).all()
+
+
+def test_refusals_of_tensors():
+    D, hq, hkv, N = 128, 4, 2, 3
+    x = draw((N, hq + 2 * hkv, D), F16, 1).cuda()
+    kc, vc = (torch.zeros(N, hkv, 16, D, dtype=F16, device="cuda") for _ in range(2))
+    table, _ = fa.fa_rope_table(D)
+    at = torch.zeros(N, dtype=torch.int32, device="cuda")
+    good = dict(q=x[:, :hq], k=x[:, hq:hq + hkv], v=x[:, hq + hkv:], qo=torch.empty(N, hq, D, dtype=F16, device="cuda"),
+                kc=kc, vc=vc, at=at, table=table, w=None)
+
+    def call(**kw):
+        a = {**good, **kw}
+        fa.fa_rope_append_kv(a["q"], a["k"], a["v"], a["qo"], a["kc"], a["vc"], None, None, None, a["at"], a["table"],
+                             q_weight=a["w"])
+
+    call()
+    for kw in (dict(q=x[:2, :hq]), dict(q=x[:, :hq].float()), dict(k=x[:, hq:hq + hkv].transpose(1, 2)),
+               dict(v=x[:, hq:hq + 1]), dict(qo=None), dict(qo=torch.empty(N, hq, D, device="cuda")), dict(kc=kc[:2]),
+               dict(vc=vc.float()), dict(at=at.long()), dict(table=table.float()), dict(w=table),
+               dict(k=x[:, ::2][:, :hkv]), dict(v=x[:, hq + hkv:].cpu()), dict(q=x[0])):
+        with pytest.raises(ValueError):
+            call(**kw)
+    out = torch.empty(N, hq, D, dtype=F16, device="cuda")
+    for a, b in ((x[:, :hq], out[:2]), (x[:, :hq].int(), out), (x[:, :hq].cpu(), out)):
+        with pytest.raises(ValueError):
+            fa.fa_rope(a, at, table, b)
+    with pytest.raises(fa.FaDecodeError) as e:
+        fa.fa_rope(x[:, :hq], at, table, x[:, 1:hq + 1])       # a shifted overlap
+    assert e.value.code == -7
+    torch.cuda.synchronize()
