@@ -639,7 +639,7 @@ def fa_prefill(q, k_cache, v_cache, v_scales, block_table, starts, seq_lens, n_q
     """Causal attention of a chunk of new tokens per sequence over its cache: q, out fp16
     [N, Hq, D], sequence b's rows starts[b] .. starts[b + 1] - 1 (starts None: one each), the
     last of them at position seq_lens[b] - 1.  The new tokens' K and V are in the cache
-    already.  `window` and `n_sink` as in ``fa_decode_sinks``; v_scales must be None.  The
+    already.  `window` and `n_sink` as in ``fa_decode_sinks``; with v_scales, int8 V.  The
     workspace is ``alloc_workspace_prefill``'s."""
     dev = _device()
     B = seq_lens.shape[0]

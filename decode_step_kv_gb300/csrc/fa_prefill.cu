@@ -58,17 +58,28 @@ constexpr int BITS = 8;             // key tiles whose unmapped groups are remem
 // the reference follows a row's maximum when that has outgrown it by 2^GROW: P < 2^15.
 constexpr float UP = 10.f, GROW = 5.f;
 
-template <int D>
+// VI8: int8 V.  Its tiles arrive raw and are turned into fp16 stages by a warpgroup of
+// their own, in a ring of four whose odd (at D = 256 last two) stages only V uses, so
+// that every stage has one producer.  8192-token prompt, 32 / 8 heads x 128: 493 us
+// against 406 with fp16 V; 4 x 4096 tokens, 16 / 8 heads x 256, 671 against 451 (the
+// ring then holds one K tile).
+constexpr int RAW_BYTES = BN * 128;
+template <int D, bool VI8 = false>
 struct Cfg {
     static constexpr int NS = D == 128 ? 2 : 1;             // streams of 128 rows
     static constexpr int DS = D / 128;                      // ring stages per K or V tile
     static constexpr int SW = D == 128 ? 64 : 128;          // keys of an S buffer
-    static constexpr int THREADS = 128 + 128 * NS;
+    static constexpr int STG = VI8 ? 4 : STAGES;
+    static constexpr int THREADS = 128 + 128 * NS + (VI8 ? 128 : 0);
     static constexpr int Q_BYTES = NS * BM * D * 2;
-    static constexpr int BAR_OFF = Q_BYTES + STAGES * STAGE_BYTES;
-    static constexpr int SMEM = BAR_OFF + 512 + 1024;       // alignment slack
+    static constexpr int RAW_OFF = Q_BYTES + STG * STAGE_BYTES;
+    static constexpr int BAR_OFF = RAW_OFF + (VI8 ? 2 * RAW_BYTES : 0);
+    static constexpr int SMEM = BAR_OFF + 512 + 1024;       // barriers, alignment slack
     static constexpr int ROWS = NS * BM;                    // of a partial slot
     static constexpr size_t SLOT_BYTES = (size_t)ROWS * D * sizeof(float);
+    // registers of the warps around (VI8; 65536 in all) and of the rows' warps
+    static constexpr int FEW = D == 128 ? 80 : 96, MANY = D == 128 ? 168 : 240;
+    __host__ __device__ static constexpr bool v_stage(int i) { return VI8 && (D == 128 ? i % 2 == 1 : i >= 2); }
 };
 
 // A row tile of a sequence: the rows of a CTA, or of a cluster of two.
@@ -84,6 +95,7 @@ struct Ent {
 struct Args {
     Params cache;                   // paging: bt, Hkv, page_size, max_blocks, num_blocks, cap, B, seq_lens
     const int *starts, *window;
+    const __half *v_scales;         // int8 V
     __half *out;
     int tokens, hq, group, tpt, sink;
     int lg_br;                      // log2 of the rows of a K / V box
@@ -443,19 +455,20 @@ struct Bars {
     uint64_t s_full[2][2], p_full[2][2];    // S, P of [stream][buffer]
     uint64_t pv[2];                         // a P V of the stream done
     uint64_t o_full[2], o_empty[2];         // the unit's O complete; read out
+    uint64_t raw_full[2], raw_empty[2];     // int8 V: a raw part has arrived, has been read
     uint64_t end;
     uint32_t tmem;
     uint32_t bits[BITS];                    // per key tile: groups in unmapped blocks
     int e0;
 };
 
-template <int D, int CL>
-__global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
+template <int D, int CL, bool VI8>
+__global__ void __launch_bounds__(Cfg<D, VI8>::THREADS, 1)
     attend_kernel(const Args p, const __grid_constant__ CUtensorMap tmQ,
                   const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV)
 {
-    using C = Cfg<D>;
-    constexpr int NS = C::NS, DS = C::DS, SW = C::SW, PARTS = BN / SW;
+    using C = Cfg<D, VI8>;
+    constexpr int NS = C::NS, DS = C::DS, SW = C::SW, PARTS = BN / SW, STG = C::STG;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     extern __shared__ unsigned char smem_raw[];
     unsigned char *smem = reinterpret_cast<unsigned char *>(
@@ -467,9 +480,10 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
     const int w = blockIdx.x / CL, rank = blockIdx.x % CL;   // a cluster's CTAs follow one another
 
     if (warp == 0 && lane == 0) {
-        for (int i = 0; i < STAGES; ++i) {
-            mbar_init(smem_u32(&bars.full[i]), 1);
-            mbar_init(smem_u32(&bars.empty[i]), CL * NS);
+        for (int i = 0; i < STG; ++i) {
+            // (an int8 V stage is filled by four warps, for this CTA alone)
+            mbar_init(smem_u32(&bars.full[i]), C::v_stage(i) ? 4 : 1);
+            mbar_init(smem_u32(&bars.empty[i]), C::v_stage(i) ? NS : CL * NS);
         }
         mbar_init(smem_u32(&bars.q_full), 1);
         mbar_init(smem_u32(&bars.q_empty), NS);
@@ -481,6 +495,8 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
             mbar_init(smem_u32(&bars.pv[i]), 1);
             mbar_init(smem_u32(&bars.o_full[i]), 1);
             mbar_init(smem_u32(&bars.o_empty[i]), 4);
+            mbar_init(smem_u32(&bars.raw_full[i]), 1);
+            mbar_init(smem_u32(&bars.raw_empty[i]), 4);
         }
         mbar_init(smem_u32(&bars.end), NS);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -550,9 +566,15 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
 
     // key tiles that Q K^T runs ahead of P V by
     constexpr int LEAD = 2 / PARTS;
+    // VI8 moves registers from the other warps to the rows'; each role's code lies behind
+    // its own setmaxnreg, by which the compiler allots its registers
+    if (warp < 4) {
+    if constexpr (VI8)
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::FEW));
     if (warp == 0) {
         // ---------------------------------------------------------- loads
         uint32_t stage = 0, phase = 1, it = 0, qn = 0, tiles = 0;   // (stages filled, Q tiles, key tiles)
+        uint32_t raw = 0;                                           // VI8: raw parts
         const int br = 1 << p.lg_br, groups = BN >> p.lg_br;
         const int g = lane % groups, slab = lane / groups;      // a lane per group of rows and 64 dims
         const bool copies = slab < 2 && (CL == 1 || g * 2 / groups == rank);
@@ -562,6 +584,11 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
             const int y = row < 0 ? p.oob_row : row;
 #pragma unroll
             for (int ds = 0; ds < DS; ++ds) {
+                if constexpr (VI8) {
+                    // K's stages: 0 and 2 in turn, or 0 and 1 for the two parts
+                    stage = DS == 1 ? it % 2 * 2 : ds;
+                    phase = (DS == 1 ? it / 2 : it / DS) + 1;
+                }
                 // (the first round of stages: the phase before a barrier's first counts as done)
                 if (!wait(bars.empty[stage], phase))
                     return false;
@@ -577,10 +604,28 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                         tma_load(dst, map, ds * 128 + slab * 64, y, bar);
                 }
                 ++it;
-                if (++stage == STAGES) {
+                if (!VI8 && ++stage == STG) {
                     stage = 0;
                     phase ^= 1;
                 }
+            }
+            return true;
+        };
+        // VI8: a V tile's raw parts, each CTA its own
+        auto raw_tile = [&](int row) {
+            const int y = row < 0 ? p.oob_row : row;
+#pragma unroll
+            for (int ds = 0; ds < DS; ++ds) {
+                const uint32_t b = raw % 2;
+                if (!wait(bars.raw_empty[b], raw / 2 + 1))
+                    return false;
+                const uint32_t bar = smem_u32(&bars.raw_full[b]);
+                if (lane == 0)
+                    mbar_expect_tx(bar, RAW_BYTES);
+                __syncwarp();
+                if (slab == 0)
+                    tma_load(sQ + C::RAW_OFF + b * RAW_BYTES + g * br * 128, &tmV, ds * 128, y, bar);
+                ++raw;
             }
             return true;
         };
@@ -647,7 +692,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
             for (int j = 0; ok && j < n; ++j) {
                 const int row2 = row_of(j + 2, ahead);
                 ahead = look(j + 3);
-                ok = tile(&tmV, row0);
+                ok = VI8 ? raw_tile(row0) : tile(&tmV, row0);
                 if (ok && j + LEAD < n)
                     ok = k_tile(LEAD == 1 ? row1 : row2);
                 row0 = row1;
@@ -655,11 +700,16 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
             }
         }
         // no copy is left in flight when the CTA ends, nor an arrival of the other CTA's
-        for (uint32_t i = it > STAGES ? it - STAGES : 0; i < it; ++i) {
-            mbar_wait_warp(smem_u32(&bars.full[i % STAGES]), i / STAGES & 1);
+        constexpr uint32_t LAST = VI8 ? 2 : STG;    // fills that may still be on their way
+        for (uint32_t i = it > LAST ? it - LAST : 0; i < it; ++i) {
+            const uint32_t st = !VI8 ? i % STG : DS == 1 ? i % 2 * 2 : i % 2;
+            const uint32_t ph = (!VI8 ? i / STG : i / 2) & 1;
+            mbar_wait_warp(smem_u32(&bars.full[st]), ph);
             if (CL == 2)
-                mbar_wait_warp(smem_u32(&bars.empty[i % STAGES]), i / STAGES & 1);
+                mbar_wait_warp(smem_u32(&bars.empty[st]), ph);
         }
+        for (uint32_t i = raw > 2 ? raw - 2 : 0; i < raw; ++i)
+            mbar_wait_warp(smem_u32(&bars.raw_full[i % 2]), i / 2 & 1);
         if (qn > 0)
             mbar_wait_warp(smem_u32(&bars.q_full), (qn - 1) & 1);
     } else if (warp == 1 || (NS == 2 && warp == 3)) {
@@ -681,13 +731,14 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
             return false;
         };
         auto advance = [&] {
-            if (++stage == STAGES) {
+            if (++stage == STG) {
                 stage = 0;
                 phase ^= 1;
             }
         };
+        uint32_t done = 0;                              // VI8 with two parts: tiles before the piece
         auto release = [&](uint32_t st) {               // refilled when the products are done
-            if constexpr (CL == 2)
+            if (CL == 2 && !C::v_stage(st))
                 mma_commit_both(lead, smem_u32(&bars.empty[st]));
             else
                 mma_commit(lead, smem_u32(&bars.empty[st]));
@@ -755,7 +806,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                     advance();
                     const uint32_t k = stage, kp = phase;
                     ok = full(v, vp);
-                    if (ok && dirty(pc.k0 + j))
+                    if (!VI8 && ok && dirty(pc.k0 + j))
                         clean(p, pc, pc.k0 + j, ring + v * STAGE_BYTES, lane);
                     for (int b = 0; ok && b < 2; ++b) {
                         ok = p_ready(2 * j + b);
@@ -784,11 +835,13 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
             } else {
                 auto k_tile = [&](int j) {
                     for (int ds = 0; ds < DS; ++ds) {
-                        if (!full(stage, phase))
+                        const uint32_t st = VI8 ? ds : stage;
+                        if (!full(st, VI8 ? done + j & 1 : phase))
                             return false;
-                        qk(j & 1, 0, ds, stage);
-                        release(stage);
-                        advance();
+                        qk(j & 1, 0, ds, st);
+                        release(st);
+                        if (!VI8)
+                            advance();
                     }
                     commit(bars.s_full[s][j & 1]);
                     if (j == n - 1)
@@ -798,16 +851,18 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                 ok = ok && k_tile(0) && (n == 1 || k_tile(1));
                 for (int j = 0; ok && j < n; ++j) {
                     for (int ds = 0; ok && ds < DS; ++ds) {
-                        ok = full(stage, phase);
-                        if (ok && dirty(pc.k0 + j))
-                            clean(p, pc, pc.k0 + j, ring + stage * STAGE_BYTES, lane);
+                        const uint32_t st = VI8 ? 2 + ds : stage;
+                        ok = full(st, VI8 ? done + j & 1 : phase);
+                        if (!VI8 && ok && dirty(pc.k0 + j))
+                            clean(p, pc, pc.k0 + j, ring + st * STAGE_BYTES, lane);
                         if (ok && ds == 0)
                             ok = p_ready(j);
                         if (!ok)
                             break;
-                        pv(j & 1, 0, ds, stage, j > 0);
-                        release(stage);
-                        advance();
+                        pv(j & 1, 0, ds, st, j > 0);
+                        release(st);
+                        if (!VI8)
+                            advance();
                     }
                     if (ok) {
                         commit(bars.pv[s]);
@@ -816,6 +871,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                     }
                 }
             }
+            done += n;
             if (ok && mine) {
                 commit(bars.o_full[s]);
                 ++on;
@@ -826,7 +882,10 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         // no product is left running when the TMEM goes back
         mma_commit(lead, smem_u32(&bars.end));
         mbar_wait_warp(smem_u32(&bars.end), 0);
-    } else if (warp >= 4) {
+    }
+    } else if (warp < 4 + 4 * NS) {
+        if constexpr (VI8)
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::MANY));
         // ---------------------------------------------------------- softmax
         const int s = (warp - 4) >> 2;              // stream
         const int r = threadIdx.x & 127;            // row of the stream
@@ -999,6 +1058,82 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
             }
             tiles += n;
         }
+    } else if constexpr (VI8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::FEW));
+        // ---------------------------------------------------------- int8 V
+        // A thread per row of a tile: its codes times its scales, rounded to fp16, into
+        // the swizzled stage; zeros for rows that no row of q sees or whose block is
+        // unmapped.  The lanes' 16-byte chunks are rotated by the row, so that both the
+        // reads and the writes of eight lanes fall into different banks.
+        const int r = threadIdx.x & 127;
+        uint32_t raw = 0, tiles = 0;
+        while (ok && walk.next(p, pc)) {
+            const int n = pc.k1 - pc.k0;
+            // the scales of this thread's row of key tile j, on their way a tile early
+            auto look = [&](int j, uint2 (&sc)[DS]) {
+                const int t = j < n ? pc.key_tile(pc.k0 + j) * BN + r : pc.x.hi;
+                long long row = -1;
+                if (t < pc.x.hi && (t >= pc.x.lo || t < p.sink))
+                    row = tc::tile_row(p.cache, pc.x.b, pc.kv, t);
+#pragma unroll
+                for (int ds = 0; ds < DS; ++ds)
+                    sc[ds] = row < 0 ? make_uint2(0u, 0u)
+                                     : __ldg(reinterpret_cast<const uint2 *>(p.v_scales + row * (D / 32)) + ds);
+                return row >= 0;
+            };
+            uint2 next[DS];
+            bool next_live = look(0, next);
+            for (int j = 0; ok && j < n; ++j) {
+                uint2 sc[DS];
+                const bool live = next_live;
+#pragma unroll
+                for (int ds = 0; ds < DS; ++ds)
+                    sc[ds] = next[ds];
+                next_live = look(j + 1, next);
+#pragma unroll
+                for (int ds = 0; ds < DS; ++ds) {
+                    const uint32_t b = raw % 2, st = DS == 1 ? 1 + tiles % 2 * 2 : 2 + ds;
+                    ok = ok && wait(bars.raw_full[b], raw / 2) &&
+                         wait(bars.empty[st], (DS == 1 ? tiles / 2 : tiles) + 1);
+                    if (!ok)
+                        break;
+                    const uint32_t src = sQ + C::RAW_OFF + b * RAW_BYTES + r * 128;
+                    const uint32_t dst = ring + st * STAGE_BYTES + r * 128;
+#pragma unroll 4
+                    for (int i = 0; i < 8; ++i) {
+                        const int c = (i + r) & 7;
+                        uint32_t w[4], o[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+                        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                                     : "r"(src + c * 16));
+                        if (live) {
+                            const uint32_t two = c & 4 ? sc[ds].y : sc[ds].x;
+                            const __half2 s2 = __half2half2(
+                                __ushort_as_half(static_cast<unsigned short>(c & 2 ? two >> 16 : two)));
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                tc::dequant4(w[k], s2, o[2 * k], o[2 * k + 1]);
+                        }
+                        const uint32_t to = dst + (c >> 2) * SLAB;
+                        const int q = 2 * c & 7;
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+                            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                             to + (((q + k) ^ (r & 7)) * 16)),
+                                         "r"(o[4 * k]), "r"(o[4 * k + 1]), "r"(o[4 * k + 2]), "r"(o[4 * k + 3])
+                                         : "memory");
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(smem_u32(&bars.full[st]));
+                        mbar_arrive(smem_u32(&bars.raw_empty[b]));
+                    }
+                    ++raw;
+                }
+                ++tiles;
+            }
+        }
     }
     __syncthreads();
     if (warp == 1) {
@@ -1112,27 +1247,29 @@ static size_t space_need(int batch, int n_tokens, int hq, int hkv, int D, long l
 }
 
 // [rows][D] of fp16 in boxes of `br` rows x 64 columns, 128-byte swizzle; q as
-// [tokens][heads][D] in boxes of tpt tokens x G heads x 64 columns.
+// [tokens][heads][D] in boxes of tpt tokens x G heads x 64 columns; bytes: int8 V in
+// boxes of `br` rows x 128 columns as they lie.
 static int encode_map(CUtensorMap *map, const void *base, int rank, const cuuint64_t *dims,
-                      const cuuint64_t *strides, const cuuint32_t *box)
+                      const cuuint64_t *strides, const cuuint32_t *box, bool bytes = false)
 {
     auto enc = tensor_map_encoder();
     if (!enc)
         return fail(FA_ERR_CUDA, "fa_prefill: cuTensorMapEncodeTiled unavailable");
     const cuuint32_t estr[3] = {1, 1, 1};
-    const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, rank, const_cast<void *>(base), dims,
-                           strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+    const CUresult r = enc(map, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, rank,
+                           const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                           bytes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS)
         return fail(FA_ERR_CUDA, "fa_prefill: cuTensorMapEncodeTiled failed (%d)", (int)r);
     return 0;
 }
 
-template <int D, int CL>
+template <int D, int CL, bool VI8>
 static cudaError_t launch(const Args &p, const CUtensorMap &tmQ, const CUtensorMap &tmK,
                           const CUtensorMap &tmV, int per, cudaStream_t st)
 {
-    using C = Cfg<D>;
+    using C = Cfg<D, VI8>;
     static std::mutex mu;
     static bool done[64] = {false};
     int dev = 0;
@@ -1142,7 +1279,7 @@ static cudaError_t launch(const Args &p, const CUtensorMap &tmQ, const CUtensorM
     {
         std::lock_guard<std::mutex> lock(mu);
         if (dev >= 64 || !done[dev]) {
-            e = cudaFuncSetAttribute(attend_kernel<D, CL>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+            e = cudaFuncSetAttribute(attend_kernel<D, CL, VI8>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
             if (e != cudaSuccess)
                 return e;
             if (dev < 64)
@@ -1167,7 +1304,7 @@ static cudaError_t launch(const Args &p, const CUtensorMap &tmQ, const CUtensorM
     cfg.gridDim = dim3(p.W * CL);
     cfg.blockDim = dim3(C::THREADS);
     cfg.dynamicSmemBytes = C::SMEM;
-    e = cudaLaunchKernelEx(&cfg, attend_kernel<D, CL>, p, tmQ, tmK, tmV);
+    e = cudaLaunchKernelEx(&cfg, attend_kernel<D, CL, VI8>, p, tmQ, tmK, tmV);
     if (e != cudaSuccess)
         return e;
     cfg.numAttrs = 1;
@@ -1230,9 +1367,6 @@ FA_API int fa_prefill(const void *q, const void *k_cache, const void *v_cache,
     if (!starts && n_tokens != batch)
         return fail(FA_ERR_LAYOUT, "fa_prefill: without starts every sequence has one token "
                                    "(n_tokens %d, batch %d)", n_tokens, batch);
-    if (v_scales)
-        return fail(FA_ERR_LAYOUT, "fa_prefill: int8 V is not supported (fa_decode_multi takes up "
-                                   "to 256 queries over it)");
     const long long cap = paged ? (long long)max_blocks_per_seq * page_size : max_blocks_per_seq;
     if (cap > (1ll << 30))
         return fail(FA_ERR_LAYOUT, "fa_prefill: capacity %lld tokens too large", cap);
@@ -1243,7 +1377,8 @@ FA_API int fa_prefill(const void *q, const void *k_cache, const void *v_cache,
         return 0;
     if (!q || !k_cache || !v_cache || !seq_lens || !out)
         return fail(FA_ERR_NULL, "fa_prefill: q, k_cache, v_cache, seq_lens and out are required");
-    if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out) ||
+    const bool vi8 = v_scales != nullptr;
+    if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(v_scales) || !aligned16(out) ||
         !aligned16(workspace) || !aligned_to(seq_lens, 4) || !aligned_to(block_table, 4) ||
         !aligned_to(window, 4) || !aligned_to(starts, 4))
         return fail(FA_ERR_ALIGN, "fa_prefill: q, caches, out and workspace must be 16-byte, int32 "
@@ -1259,7 +1394,8 @@ FA_API int fa_prefill(const void *q, const void *k_cache, const void *v_cache,
                     need);
     const size_t qn = (size_t)n_tokens * n_q_heads * D * 2;
     const struct { const void *p; size_t n; } in[] = {
-        {q, qn}, {k_cache, rows * D * 2}, {v_cache, rows * D * 2}, {seq_lens, (size_t)batch * 4},
+        {q, qn}, {k_cache, rows * D * 2}, {v_cache, rows * D * (vi8 ? 1 : 2)},
+        {v_scales, rows * (D / 32) * 2}, {seq_lens, (size_t)batch * 4},
         {starts, ((size_t)batch + 1) * 4}, {block_table, (size_t)batch * max_blocks_per_seq * 4},
         {window, (size_t)batch * 4}};
     for (const auto &x : in)
@@ -1278,6 +1414,7 @@ FA_API int fa_prefill(const void *q, const void *k_cache, const void *v_cache,
     p.cache.cap = cap;
     p.starts = starts;
     p.window = window;
+    p.v_scales = static_cast<const __half *>(v_scales);
     p.out = static_cast<__half *>(out);
     p.tokens = n_tokens;
     p.hq = n_q_heads;
@@ -1314,15 +1451,21 @@ FA_API int fa_prefill(const void *q, const void *k_cache, const void *v_cache,
     int rc = encode_map(&tmQ, q, 3, qd, qs, qb);
     if (!rc)
         rc = encode_map(&tmK, k_cache, 2, kd, ks, kb);
+    const cuuint64_t vs[1] = {(cuuint64_t)D};
+    const cuuint32_t vb[2] = {128, (cuuint32_t)br};
     if (!rc)
-        rc = encode_map(&tmV, v_cache, 2, kd, ks, kb);
+        rc = vi8 ? encode_map(&tmV, v_cache, 2, kd, vs, vb, true) : encode_map(&tmV, v_cache, 2, kd, ks, kb);
     if (rc)
         return rc;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = cl == 2 ? (D == 128 ? launch<128, 2>(p, tmQ, tmK, tmV, sp.per, st)
-                                              : launch<256, 2>(p, tmQ, tmK, tmV, sp.per, st))
-                                  : (D == 128 ? launch<128, 1>(p, tmQ, tmK, tmV, sp.per, st)
-                                              : launch<256, 1>(p, tmQ, tmK, tmV, sp.per, st));
+    auto go = [&](auto int8) {
+        constexpr bool I = decltype(int8)::value;
+        return cl == 2 ? (D == 128 ? launch<128, 2, I>(p, tmQ, tmK, tmV, sp.per, st)
+                                   : launch<256, 2, I>(p, tmQ, tmK, tmV, sp.per, st))
+                       : (D == 128 ? launch<128, 1, I>(p, tmQ, tmK, tmV, sp.per, st)
+                                   : launch<256, 1, I>(p, tmQ, tmK, tmV, sp.per, st));
+    };
+    const cudaError_t e = vi8 ? go(std::true_type()) : go(std::false_type());
     if (e != cudaSuccess)
         return fail(FA_ERR_CUDA, "fa_prefill: launch failed: %s", cudaGetErrorString(e));
     return 0;

@@ -555,7 +555,7 @@ FA_API size_t fa_decode_sinks_workspace_size(int batch, int n_queries, int n_q_h
  *         attends the keys up to itself; with a window[b] > 0 the last
  *         window[b] of them and the first n_sink.  A row at a negative
  *         position gets zeros.
- * v_scales  must be NULL: int8 V is refused (FA_ERR_LAYOUT).
+ * v_scales  NULL (fp16 V) or the scales of int8 V, as fa_decode's.
  * out     [n_tokens][n_q_heads][head_dim] fp16 (fp32 accumulation, one
  *         rounding).
  * workspace  fa_prefill_workspace_size() bytes, 16-byte aligned; contents need
@@ -565,9 +565,10 @@ FA_API size_t fa_decode_sinks_workspace_size(int batch, int n_queries, int n_q_h
  * some row of a sequence's chunk sees must be finite (a weight of 0 times an
  * infinity is a NaN in the rows beside it).  V rows that none sees, and pages
  * that hold no key of any row, may hold anything, the latter be unmapped.
- * Caches (fp16, paged or contiguous, below 2^31 rows), block_table, sizes,
- * status bits, streams, graph capture and errors as fa_decode; a tile of keys
- * in an unmapped block is skipped.  batch = 0 or n_tokens = 0 is a no-op.
+ * Caches (fp16 K; fp16 or int8 V; paged or contiguous, below 2^31 rows),
+ * block_table, sizes, status bits, streams, graph capture and errors as
+ * fa_decode; keys in an unmapped block are skipped.  batch = 0 or n_tokens = 0
+ * is a no-op.
  */
 FA_API int fa_prefill(const void *q, const void *k_cache, const void *v_cache,
                       const void *v_scales, const int32_t *block_table, const int32_t *starts,

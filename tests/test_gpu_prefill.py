@@ -44,10 +44,12 @@ def values(v, s):
     return v.astype(np.float64) if s is None else v * np.repeat(s.astype(np.float64), 32, axis=-1)
 
 
-def run_prefill(lay, lens, new, hq, D, window=None, sink=0, seed=0, scale=None, starts=None, tokens=None, table=None):
+def run_prefill(lay, lens, new, hq, D, window=None, sink=0, seed=0, scale=None, starts=None, tokens=None, table=None,
+                int8=False):
     B = lay.batch
     w = window or [0] * B
-    k, v, _ = caches(lay, lens, new, w, sink, D, seed)
+    k, v, s = caches(lay, lens, new, w, sink, D, seed, int8=int8)
+    val = values(v, s)
     if starts is None:
         starts = np.concatenate([[0], np.cumsum(new)]).tolist()
     N = tokens or starts[-1]
@@ -55,8 +57,8 @@ def run_prefill(lay, lens, new, hq, D, window=None, sink=0, seed=0, scale=None, 
     out = torch.full((N, hq, D), 9.0, dtype=torch.float16, device="cuda")
     ws = fa.alloc_workspace_prefill(B, N, hq, lay.hkv, D, lay.capacity)
     ws.fill_(255)                                      # a NaN wherever it is read unwritten
-    fa.fa_prefill(torch.from_numpy(q).cuda(), torch.from_numpy(k).cuda(), torch.from_numpy(v).cuda(), None,
-                  lay.table_gpu() if table is None else torch.from_numpy(table).cuda(), ints(starts), ints(lens), hq,
+    fa.fa_prefill(torch.from_numpy(q).cuda(), torch.from_numpy(k).cuda(), torch.from_numpy(v).cuda(),
+                  None if s is None else torch.from_numpy(s).cuda(), lay.table_gpu() if table is None else torch.from_numpy(table).cuda(), ints(starts), ints(lens), hq,
                   lay.hkv, D, scale or D ** -0.5,
                   ints(window) if window else None, out, n_sink=sink, workspace=ws)
     got = f64(out)
@@ -66,9 +68,10 @@ def run_prefill(lay, lens, new, hq, D, window=None, sink=0, seed=0, scale=None, 
         rest[rows] = False
         at = np.arange(lens[b] - n, lens[b])
         kk = lay.dense(k, b).astype(np.float64)
-        vv = lay.dense(v, b).astype(np.float64)
+        vv = lay.dense(val, b)
         want, size = attend_rows(q[rows].astype(np.float64), at, kk, vv, scale or D ** -0.5, w[b], sink, lay.hkv)
-        tol = attend_tolerance(size, max(lens[b], 1), 5.0)
+        # int8 V: one more rounding, of code * scale to fp16
+        tol = attend_tolerance(size, max(lens[b], 1), 5.0) + (2.0 ** -11 * size if int8 else 0)
         err = np.abs(got[rows] - want)
         assert np.isfinite(got[rows]).all(), b
         assert (err <= tol).all(), (b, (err / tol).max(), np.argwhere(err > tol)[:4].tolist())
@@ -107,6 +110,18 @@ def test_clusters(D, hq, hkv, new, lens, window, sink):
 @pytest.mark.parametrize("page", [16, 32, 48, 64, 128, 256])
 def test_pages(page):
     run_prefill(Layout(2, 2, 400, True, page=page, seed=5), [400, 333], [150, 20], 8, 128)
+
+
+@pytest.mark.parametrize("D", [128, 256])
+@pytest.mark.parametrize("hq,hkv,new,lens,window,sink,page", [
+    (8, 2, [1], [1], [0], 0, 16), (8, 2, [70, 1, 129], [300, 1, 129], [0] * 3, 0, 16),
+    (3, 1, [257, 0, 40], [700, 3, 41], [0] * 3, 0, 48), (8, 1, [700, 300], [900, 2000], [0, 0], 0, 16),
+    (8, 1, [650, 1000], [900, 1000], [100, 300], 5, 64), (4, 2, [20, 90, 200], [700, 90, 513], [129, 0, 129], 40, 16),
+    (16, 1, [9], [9001], [0], 0, 16), (4, 4, [64, 3], [40, 2], [0, 0], 0, 0), (8, 1, [600], [777], [0], 0, 0)])
+def test_int8_v(D, hq, hkv, new, lens, window, sink, page):
+    """V in codes and scales: paged (page > 0) or contiguous, one CTA per row tile or clusters of two."""
+    run_prefill(Layout(len(new), hkv, max(lens), page > 0, page=page or 16, seed=13), lens, new, hq, D,
+                window=window if any(window) else None, sink=sink, seed=5, int8=True)
 
 
 @pytest.mark.parametrize("cap", [200, 333, 1])

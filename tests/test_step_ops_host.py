@@ -102,7 +102,7 @@ def prefill(**kw):
 @pytest.mark.parametrize("kw,want", [
     (dict(d=64), -2), (dict(hq=7), -3), (dict(hq=130), -3), (dict(hkv=0), -3), (dict(scale=float("nan")), -5),
     (dict(B=-1), -6), (dict(B=65536), -6), (dict(n=-1), -6), (dict(page=8), -6), (dict(total=0), -6),
-    (dict(blocks=0), -6), (dict(sink=-1), -6), (dict(st=None), -6), (dict(vsc=at(9)), -6), (dict(total=1 << 26), -6),
+    (dict(blocks=0), -6), (dict(sink=-1), -6), (dict(st=None), -6), (dict(vsc=at(9, 8)), -9), (dict(total=1 << 26), -6),
     (dict(bt=None, blocks=(1 << 30) + 1), -6), (dict(q=None), -1), (dict(lens=None), -1), (dict(out=None), -1),
     (dict(q=at(0, 8)), -9), (dict(window=at(8, 2)), -9), (dict(st=at(4, 1)), -9), (dict(ws=at(7, 8)), -9),
     (dict(B=0, q=None), 0), (dict(n=0, q=None, out=None), 0)])
