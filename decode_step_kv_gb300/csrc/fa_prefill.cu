@@ -941,9 +941,10 @@ __global__ void __launch_bounds__(Cfg<D, VI8>::THREADS, 1)
                     const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * p.c2;
                     const bool grow = top > m + GROW;       // also from -infinity
                     if (__any_sync(0xffffffffu, grow)) {
-                        const float m1 = fmaxf(m, top);
-                        const float a = ex2(m - (m1 == -INFINITY ? 0.f : m1));
-                        m = m1;
+                        // a row's reference follows its own scores alone: its bits depend neither on
+                        // its neighbours nor on the rows behind the last token, which hold anything
+                        const float a = grow ? ex2(m - top) : 1.f;
+                        m = grow ? top : m;
                         l *= a;
                         if (i > 0) {
                             // the P V before must have landed

@@ -599,3 +599,23 @@ def test_refusals_of_tensors():
             call(**kw)
         assert e.value.code == code
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("D", [128, 256])
+@pytest.mark.parametrize("hq,n", [(5, 355), (3, 41), (8, 700)])
+def test_bits_do_not_depend_on_what_lies_beside(D, hq, n):
+    """A row tile's last rows hold tokens of others, or nothing: the rows beside them keep their bits."""
+    rng = np.random.RandomState(6)
+    L = n + 200
+    k, v = (torch.from_numpy(rng.randn(1, 1, L, D).astype(np.float16)).cuda() for _ in range(2))
+    q = torch.from_numpy(rng.randn(n + 130, hq, D).astype(np.float16)).cuda()
+    ws = fa.alloc_workspace_prefill(1, n + 130, hq, 1, D, L)
+    got = []
+    for fill in (0.0, 300.0, float("nan"), float("inf"), 0.0):
+        q[n:] = fill
+        out = torch.full_like(q, 9.0)
+        fa.fa_prefill(q, k, v, None, None, ints([0, n]), ints([L]), hq, 1, D, D ** -0.5, None, out, workspace=ws)
+        got.append(out)
+        assert bool((out[n:] == 9.0).all())
+    for x in got[1:]:
+        assert bool((x == got[0]).all())
