@@ -32,6 +32,8 @@
 // axis (as the decode plan: UNIT_COST positions per unit beside its tiles), every
 // CTA or cluster takes an equal stretch of it, and a unit that a stretch cuts leaves
 // fp32 partials that a merge kernel joins in a fixed order.
+#include <cfloat>
+
 #include "fa_common.cuh"
 
 namespace fa {
@@ -57,6 +59,9 @@ constexpr int BITS = 8;             // key tiles whose unmapped groups are remem
 // (2^-10 to 2^-20 of it each: an attention sink's companions) keep their bits in fp16, and
 // the reference follows a row's maximum when that has outgrown it by 2^GROW: P < 2^15.
 constexpr float UP = 10.f, GROW = 5.f;
+// A score in log2 units beyond FAR (its steps in 32 bits are 2^-7 there, and 2^4 at 2^27) is taken as a
+// difference from the row's largest before it meets c2 and UP, which would be rounded to its steps.
+constexpr float FAR = 65536.f;
 
 // VI8: int8 V.  Its tiles arrive raw and are turned into fp16 stages by a warpgroup of
 // their own, in a ring of four whose odd (at D = 256 last two) stages only V uses, so
@@ -409,6 +414,15 @@ __device__ __forceinline__ float max3(float a, float b, float c)
 }
 __device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// The factor on weights whose reference moves from score a to score b >= a (q . k, before c2).
+// The weights of scores that are not far are taken against the rounded product of reference and c2,
+// so that their factor is that of the products.
+__device__ __forceinline__ float rescale(float a, float b, float c2)
+{
+    const float y = __fmul_rn(b, c2);
+    return ex2(fabsf(y) > FAR ? (a - b) * c2 : __fmul_rn(a, c2) - y);
+}
 
 // The low n bits, n of any sign and size.
 __device__ __forceinline__ uint32_t below(int n)
@@ -900,7 +914,8 @@ __global__ void __launch_bounds__(Cfg<D, VI8>::THREADS, 1)
                 // positions of this stream's first and last row
                 const int at_lo = pc.at + s * p.tpt;
                 const int at_hi = pc.at + min((s + 1) * p.tpt, pc.ntok) - 1;
-                float m = -INFINITY, l = 0.f;
+                float m = -INFINITY, l = 0.f;       // reference (a score before c2), sum of the weights
+                bool far = false;                   // some row of the warp has one beyond FAR
                 for (int i = 0; ok && i < m_parts; ++i) {
                     const int b = i & 1, half = PARTS == 2 ? b : 0;
                     ok = wait(bars.s_full[s][b], used[b] + i / 2);
@@ -917,17 +932,21 @@ __global__ void __launch_bounds__(Cfg<D, VI8>::THREADS, 1)
                     const bool edge = kb + SW - 1 > at_lo || bits ||
                                       (pc.x.window > 0 && kb <= at_hi - pc.x.window && kb + SW > p.sink);
                     tmem_ld_wait();
-                    if (edge) {
+                    // a bit per column of 32 that the row sees
+                    auto seen = [&](int c) {
                         const int hi = at - kb, lo = pc.x.window > 0 ? hi - pc.x.window + 1 : -1;
                         const int sk = p.sink - kb;
+                        uint32_t see = below(hi + 1 - c * 32) & (~below(lo - c * 32) | below(sk - c * 32));
+                        if (bits)
+                            for (int t = 0; t < 32; t += 16)
+                                if (bits >> ((half * SW + c * 32 + t) >> p.lg_br) & 1)
+                                    see &= ~(0xffffu << t);
+                        return see;
+                    };
+                    if (edge) {
 #pragma unroll
                         for (int c = 0; c < SW / 32; ++c) {
-                            // a bit per column that the row sees
-                            uint32_t see = below(hi + 1 - c * 32) & (~below(lo - c * 32) | below(sk - c * 32));
-                            if (bits)
-                                for (int t = 0; t < 32; t += 16)
-                                    if (bits >> ((half * SW + c * 32 + t) >> p.lg_br) & 1)
-                                        see &= ~(0xffffu << t);
+                            const uint32_t see = seen(c);
 #pragma unroll
                             for (int e = 0; e < 32; ++e)
                                 if (!(see >> e & 1))
@@ -938,14 +957,15 @@ __global__ void __launch_bounds__(Cfg<D, VI8>::THREADS, 1)
 #pragma unroll
                     for (int e = 0; e < SW; e += 2)
                         tops[e / 2 & 3] = max3(tops[e / 2 & 3], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
-                    const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * p.c2;
-                    const bool grow = top > m + GROW;       // also from -infinity
+                    const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+                    const bool grow = (top - m) * p.c2 > GROW;      // also from -infinity
                     if (__any_sync(0xffffffffu, grow)) {
                         // a row's reference follows its own scores alone: its bits depend neither on
                         // its neighbours nor on the rows behind the last token, which hold anything
-                        const float a = grow ? ex2(m - top) : 1.f;
+                        const float a = grow ? rescale(m, top, p.c2) : 1.f;
                         m = grow ? top : m;
                         l *= a;
+                        far = __any_sync(0xffffffffu, m != -INFINITY && fabsf(m * p.c2) > FAR);
                         if (i > 0) {
                             // the P V before must have landed
                             ok = wait(bars.pv[s], pv_n + i - 1);
@@ -964,28 +984,52 @@ __global__ void __launch_bounds__(Cfg<D, VI8>::THREADS, 1)
                             }
                         }
                     }
-                    const float ref = m == -INFINITY ? 0.f : m - UP;
+                    const float ref = m == -INFINITY ? 0.f : __fmul_rn(m, p.c2) - UP;
                     const uint64_t c22 = pair2(p.c2, p.c2), ref2 = pair2(-ref, -ref);
                     uint64_t sums[4] = {0, 0, 0, 0};
+                    if (far) {                  // (uniform over the warp; the scores are read again)
+                        const bool mine = m != -INFINITY && fabsf(m * p.c2) > FAR;
+                        const float from = mine ? m : 0.f, up = mine ? UP : -ref;
+#pragma unroll 1
+                        for (int c = 0; c < SW / 32; ++c) {
+                            uint32_t y[32], h[16];
+                            tmem_ld32(s_col + b * SW + c * 32, y);
+                            const uint32_t see = seen(c);
+                            tmem_ld_wait();
 #pragma unroll
-                    for (int c = 0; c < SW / 32; ++c) {
-                        // a step for all 32 before the next: a dozen exponentials in flight
-                        uint32_t h[16];
-                        float w[32];
+                            for (int e = 0; e < 16; ++e) {
+                                float w[2];
 #pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            split2(fma2(pair2(__uint_as_float(x[c * 32 + 2 * e]),
-                                              __uint_as_float(x[c * 32 + 2 * e + 1])), c22, ref2),
-                                   w[2 * e], w[2 * e + 1]);
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            w[e] = ex2_ftz(w[e]);
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            h[e] = tc::pack_half2(w[2 * e], w[2 * e + 1]);
-                            sums[e & 3] = add2(sums[e & 3], pair2(w[2 * e], w[2 * e + 1]));
+                                for (int k = 0; k < 2; ++k)
+                                    w[k] = see >> (2 * e + k) & 1
+                                               ? ex2_ftz(fmaf(__uint_as_float(y[2 * e + k]) - from, p.c2, up))
+                                               : 0.f;
+                                h[e] = tc::pack_half2(w[0], w[1]);
+                                sums[e & 3] = add2(sums[e & 3], pair2(w[0], w[1]));
+                            }
+                            tmem_st16(s_col + b * SW + c * 16, h);
                         }
-                        tmem_st16(s_col + b * SW + c * 16, h);
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < SW / 32; ++c) {
+                            // a step for all 32 before the next: a dozen exponentials in flight
+                            uint32_t h[16];
+                            float w[32];
+#pragma unroll
+                            for (int e = 0; e < 16; ++e)
+                                split2(fma2(pair2(__uint_as_float(x[c * 32 + 2 * e]),
+                                                  __uint_as_float(x[c * 32 + 2 * e + 1])), c22, ref2),
+                                       w[2 * e], w[2 * e + 1]);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                w[e] = ex2_ftz(w[e]);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) {
+                                h[e] = tc::pack_half2(w[2 * e], w[2 * e + 1]);
+                                sums[e & 3] = add2(sums[e & 3], pair2(w[2 * e], w[2 * e + 1]));
+                            }
+                            tmem_st16(s_col + b * SW + c * 16, h);
+                        }
                     }
                     tmem_st_wait();
                     fence_before();
@@ -1147,7 +1191,7 @@ __global__ void __launch_bounds__(Cfg<D, VI8>::THREADS, 1)
 
 // ------------------------------------------------------------ the merge
 // CTA (x, w): 256 of the (row, 16 columns) of the unit that CTA w of the main kernel
-// began and left to the next ones: their partials in order, weighed by 2^(m - M).
+// began and left to the next ones: their partials in order, weighed by 2^(c2 (m - M)).
 template <int D, int CL>
 __global__ void __launch_bounds__(256) merge_kernel(const Args p)
 {
@@ -1173,7 +1217,7 @@ __global__ void __launch_bounds__(256) merge_kernel(const Args p)
     float L = 0.f;
     for (int i = 0; i < u.z; ++i) {
         const float2 v = p.ml[slot(i) * C::ROWS + row];
-        const float a = v.x == -INFINITY ? 0.f : ex2(v.x - M);
+        const float a = v.x == -INFINITY ? 0.f : rescale(v.x, M, p.c2);
         L = fmaf(v.y, a, L);
         const float4 *src = reinterpret_cast<const float4 *>(p.part) + slot(i) * (D / 4) * C::ROWS +
                             (size_t)c16 * 4 * C::ROWS + row;
@@ -1430,7 +1474,7 @@ FA_API int fa_prefill(const void *q, const void *k_cache, const void *v_cache,
     // a negative scale: the product negates Q; the running maximum wants c2 > 0, and 0
     // weighs every key alike, as this does
     const double c2 = fabs(static_cast<double>(scale)) * 1.4426950408889634;
-    p.c2 = c2 < 1e-37 ? 1e-37f : static_cast<float>(c2);
+    p.c2 = static_cast<float>(fmin(fmax(c2, 1e-37), static_cast<double>(FLT_MAX)));
     const uint32_t sw = D == 128 ? Cfg<128>::SW : Cfg<256>::SW;
     p.idesc_qk = 1u << 4 | (scale < 0.f ? 1u << 13 : 0u) | (sw >> 3) << 17 | (BM >> 4) << 24;
     p.W = sp.W;
