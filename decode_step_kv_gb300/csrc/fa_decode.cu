@@ -1084,10 +1084,13 @@ __global__ void __launch_bounds__(Cfg<D, VI8, NG>::NW * 32, Cfg<D, VI8, NG>::CTA
                 }
                 // With sinks the weights (and their sum and O with them) are taken 2^10 times
                 // as large: a sink often takes most of the weight, and the keys behind it,
-                // 2^-10 to 2^-20 of it each, keep their bits in fp16
+                // 2^-10 to 2^-20 of it each, keep their bits in fp16.  The shift is added to the
+                // difference, which is small and exact where it counts: beside a score of 2^27 it
+                // would be rounded to 2^4, and the weight to 2^16, an infinity in fp16
                 constexpr float UP = SK ? 10.f : 0.f;
-                const float p0 = ex2(sc[0] - (r0m - UP)), p1 = ex2(sc[1] - (r1m - UP));
-                const float p2 = ex2(sc[2] - (r0m - UP)), p3 = ex2(sc[3] - (r1m - UP));
+                auto weight = [](float x, float top) { return SK ? ex2((x - top) + UP) : ex2(x - top); };
+                const float p0 = weight(sc[0], r0m), p1 = weight(sc[1], r1m);
+                const float p2 = weight(sc[2], r0m), p3 = weight(sc[3], r1m);
                 l[gi][0] += p0 + p2;
                 l[gi][1] += p1 + p3;
                 // ---- P^T as the PV B operand (keys x columns), via movmatrix

@@ -87,3 +87,18 @@ def test_prefill(e, D, codes, order, sign, n, L):
                   workspace=fa.alloc_workspace_prefill(1, n, HKV * G, HKV, D, L))
     check(out, val, lev, range(L - n, L))
     assert binding.fa_decode_device_status() == 0
+
+
+@pytest.mark.parametrize("e", SIZES)
+@pytest.mark.parametrize("D,codes", [(128, False), (256, False), (128, True), (256, True)])
+@pytest.mark.parametrize("order,sign", [("flat", 1), ("flat", -1), ("up", 1), ("down", 1), ("mixed", -1)])
+@pytest.mark.parametrize("tq,L", [(1, 704), (3, 704), (1, 6000)])
+def test_sinks(e, D, codes, order, sign, tq, L):
+    q, k, lev = inputs(D, tq, L, e, order, sign)
+    v, s, val = values(L, D, codes)
+    out = torch.zeros(1, tq, HKV * G, D, dtype=torch.float16, device="cuda")
+    qd, kd, vd, sd = gpu(q[None], k[None], v[None], None if s is None else s[None])
+    fa.fa_decode_sinks(qd, kd, vd, sd, None, ints([L]), HKV * G, HKV, D, sign * D ** -0.5, ints([400]), out, n_sink=5,
+                       workspace=fa.alloc_workspace_sinks(1, tq, HKV * G, HKV, D, L))
+    check(out[0], val, lev, range(L - tq, L), 400, 5)
+    assert binding.fa_decode_device_status() == 0
