@@ -291,6 +291,14 @@ constexpr float NO_MAX = -3e38f;       // reference of a column that has no key 
 constexpr float P_SHIFT = 10.f;        // log2 units from the reference up to the running maximum
 constexpr float MAX_SLACK = 4.f;       // ... a score may pass that maximum by
 
+// The reference for scores up to `top`, at least `mr`.  Beside a score of 2^27 a step of 32 bits is
+// 2^4, and P_SHIFT below it would be rounded to 16 below: P of 2^16, an infinity in fp16.
+__device__ __forceinline__ float reference(float top, float mr)
+{
+    const float y = top - P_SHIFT;
+    return fmaxf(top - y > P_SHIFT + MAX_SLACK ? top : y, mr);
+}
+
 __device__ __forceinline__ void cp16(uint32_t dst, const void *src, uint64_t policy)
 {
     asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(dst),
@@ -856,7 +864,7 @@ __global__ void __launch_bounds__(Cfg<D, NG>::NW * 32, Cfg<D, NG>::CTAS_PER_SM)
 #pragma unroll
                     for (int mask = 4; mask <= 16; mask <<= 1)
                         y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, mask));
-                    y = fmaxf(y - P_SHIFT, mr[gi][x]);
+                    y = reference(y, mr[gi][x]);
                     const float a = ex2_ftz(mr[gi][x] - y);
                     l[gi][x] *= a;
                     mr[gi][x] = y;
@@ -1419,7 +1427,7 @@ __global__ void __launch_bounds__(128, WideCfg<D>::CTAS_PER_SM) wide_kernel(cons
                     x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, mask));
                     x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, mask));
                 }
-                const float n0 = fmaxf(mr[0], x0 - P_SHIFT), n1 = fmaxf(mr[1], x1 - P_SHIFT);
+                const float n0 = reference(x0, mr[0]), n1 = reference(x1, mr[1]);
                 const float a0 = ex2_ftz(mr[0] - n0), a1 = ex2_ftz(mr[1] - n1);
                 l[0] *= a0;
                 l[1] *= a1;

@@ -10,6 +10,7 @@ import torch
 
 import decode_step_kv_gb300 as fa
 from decode_step_kv_gb300 import binding
+from _cache_ops import dequantize, pack, quantize
 from _step_ops import f64
 
 pytestmark = pytest.mark.gpu
@@ -101,4 +102,22 @@ def test_sinks(e, D, codes, order, sign, tq, L):
     fa.fa_decode_sinks(qd, kd, vd, sd, None, ints([L]), HKV * G, HKV, D, sign * D ** -0.5, ints([400]), out, n_sink=5,
                        workspace=fa.alloc_workspace_sinks(1, tq, HKV * G, HKV, D, L))
     check(out[0], val, lev, range(L - tq, L), 400, 5)
+    assert binding.fa_decode_device_status() == 0
+
+
+@pytest.mark.parametrize("e", SIZES)
+@pytest.mark.parametrize("D", [128, 256])
+@pytest.mark.parametrize("order,sign", [("flat", 1), ("flat", -1), ("up", 1), ("down", 1), ("mixed", -1)])
+@pytest.mark.parametrize("tq,L", [(1, 704), (4, 704), (16, 704), (1, 6000), (16, 6000)])
+def test_int4(e, D, order, sign, tq, L):
+    """4-bit caches.  A level's keys have the same codes and scale; levels differ by their scales."""
+    q, k, lev = inputs(D, tq, L, e, order, sign)
+    v, _, _ = values(L, D, False)
+    (kc, ks), (vc, vs) = (quantize(x.astype(np.float64)) for x in (k, v))
+    kc, vc = pack(kc), pack(vc)
+    out = torch.zeros(1, tq, HKV * G, D, dtype=torch.float16, device="cuda")
+    qd, *caches = gpu(q[None], kc[None], ks[None], vc[None], vs[None])
+    fa.fa_decode_int4(qd, *caches, None, ints([L]), HKV * G, HKV, D, sign * D ** -0.5, None, out,
+                      workspace=fa.alloc_workspace_int4(1, tq, HKV * G, HKV, D, L))
+    check(out[0], dequantize(vc, vs), lev, range(L - tq, L))
     assert binding.fa_decode_device_status() == 0
