@@ -24,14 +24,20 @@
 // 128 x 64 x 16 step takes 52-76 cycles where a 128 x 128 x 16 one takes 64, but TMEM
 // has no room for two of 128 keys beside O, and one buffer a stream, whose Q K^T
 // waits for its P V, took 1943 us for a prompt of 16384 tokens (32 / 8 heads) against
-// 1657.  As it stands: 1525-1600 us (1.38-1.44 PFLOP/s of the 1.91 that a library
+// 1657.  As it stands: 1557-1577 us (1.39-1.41 PFLOP/s of the 1.91 that a library
 // product reaches; the power cap holds the clocks at 1.65-1.75 GHz), 512 tokens over
-// 131072 keys 751-781 us, 4 prompts of 1K-8K at D = 256 767-786 us.
+// 131072 keys 823-843 us, 4 prompts of 1K-8K at D = 256 895-917 us.
+//
+// Every CTA fetches its own K and V tiles.  At D = 256 its 128 rows take 128 KB per
+// 2048 tensor cycles, which L2 does not deliver to every SM at once.  A load into two
+// CTAs of a cluster halves that (4 prompts at D = 256 710 us, 512 tokens over 131072
+// keys 765), but it must stay off memory that another GPU serves, which a pointer does
+// not tell, and the library is the same for every rank of a run on several GPUs.
 //
 // Work over the GPU.  A one-CTA kernel lists the units' tiles as positions of one
 // axis (as the decode plan: UNIT_COST positions per unit beside its tiles), every
-// CTA or cluster takes an equal stretch of it, and a unit that a stretch cuts leaves
-// fp32 partials that a merge kernel joins in a fixed order.
+// CTA takes an equal stretch of it, and a unit that a stretch cuts leaves fp32
+// partials that a merge kernel joins in a fixed order.
 #include <cfloat>
 
 #include "fa_common.cuh"
@@ -65,9 +71,11 @@ constexpr float FAR = 65536.f;
 
 // VI8: int8 V.  Its tiles arrive raw and are turned into fp16 stages by a warpgroup of
 // their own, in a ring of four whose odd (at D = 256 last two) stages only V uses, so
-// that every stage has one producer.  8192-token prompt, 32 / 8 heads x 128: 493 us
-// against 406 with fp16 V; 4 x 4096 tokens, 16 / 8 heads x 256, 671 against 451 (the
-// ring then holds one K tile).
+// that every stage has one producer.  Code times scale is rounded to fp16, as fa_decode
+// rounds it: a factor per 32 dims cannot ride on the weight, which one product takes
+// against all dims.  8192-token prompt, 32 / 8 heads x 128: 510 us against
+// 407 with fp16 V; 4 x 4096 tokens, 16 / 8 heads x 256, 925 against 604 (the ring then
+// holds one K tile).  These kernels spill: 152 bytes at D = 128, 156 at D = 256.
 constexpr int RAW_BYTES = BN * 128;
 template <int D, bool VI8 = false>
 struct Cfg {
@@ -87,7 +95,7 @@ struct Cfg {
     __host__ __device__ static constexpr bool v_stage(int i) { return VI8 && (D == 128 ? i % 2 == 1 : i >= 2); }
 };
 
-// A row tile of a sequence: the rows of a CTA, or of a cluster of two.
+// A row tile of a sequence.
 struct Ent {
     int b, tok;                     // sequence; first row of q
     int ntok, at;                   // tokens; position of the first
@@ -107,15 +115,15 @@ struct Args {
     int oob_row;                    // a cache row beyond the tensor: reads as zeros
     float c2;
     uint32_t idesc_qk;
-    int W;                          // CTAs (clusters) of the main kernel
+    int W;                          // CTAs of the main kernel
     int max_ents;
     // workspace
     Ent *ents;
     long long *pos;                 // [max_ents + 1] first position of each entry
     int *ebase;                     // [B + 1] first entry of each sequence
-    int4 *split;                    // [CTAs] the unit that a CTA leaves to its successors: entry, kv, parts
-    float *part;                    // [2 CTAs] slots of [D / 4][ROWS] float4
-    float2 *ml;                     // [2 CTAs][ROWS]
+    int4 *split;                    // [W] the unit that a CTA leaves to its successors: entry, kv, parts
+    float *part;                    // [2 W] slots of [D / 4][ROWS] float4
+    float2 *ml;                     // [2 W][ROWS]
 };
 
 // ------------------------------------------------------------ the plan
@@ -230,7 +238,6 @@ __device__ __forceinline__ int ctas_for(const Args &p, long long T)
 
 struct Piece {
     Ent x;
-    int tok, ntok, at;              // this CTA's share of the row tile: as in Ent
     int e, kv, k0, k1;              // key tiles [k0, k1) of unit (e, kv)
     int slot;                       // partial slot, -1: the whole unit
     bool first_part;                // a partial from the unit's first tile
@@ -242,12 +249,9 @@ struct Piece {
 struct Pieces {
     int e, kv;
     long long us, len;              // us: the current unit's first tile, counted from the stretch's start
-    int skip, most;                 // tokens of the row tile before this CTA's, and its most
-    __device__ __forceinline__ void start(const Args &p, int e_, long long t0, long long t1, int skip_, int most_)
+    __device__ __forceinline__ void start(const Args &p, int e_, long long t0, long long t1)
     {
         e = e_;
-        skip = skip_;
-        most = most_;
         const int unit = p.ents[e].n + UNIT_COST;
         const long long off = t0 - p.pos[e];
         kv = static_cast<int>(off / unit);
@@ -257,12 +261,8 @@ struct Pieces {
     __device__ __forceinline__ bool next(const Args &p, Piece &q)
     {
         while (us - UNIT_COST < len) {      // the last unit ends where the last stretch does
-            if (e != q.e) {             // kept over its KV heads
+            if (e != q.e)               // kept over its KV heads
                 q.x = p.ents[e];
-                q.tok = q.x.tok + skip;
-                q.at = q.x.at + skip;
-                q.ntok = min(max(q.x.ntok - skip, 0), most);
-            }
             const int n = q.x.n;
             const bool empty = n == 0 && us >= UNIT_COST;       // zero rows
             q.k0 = empty || us > 0 ? 0 : static_cast<int>(-us);
@@ -308,31 +308,12 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar)
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-// The same box into both CTAs of the cluster, each at the same place and barrier.
-__device__ __forceinline__ void tma_load_both(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar)
-{
-    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
-                 ".multicast::cluster [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
-                 "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "h"((unsigned short)3)
-                 : "memory");
-}
-
 // Arrives on bar when the products issued so far by this thread are done.
 __device__ __forceinline__ void mma_commit(uint32_t lead, uint32_t bar)
 {
     asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
                  "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
                  "r"(lead)
-                 : "memory");
-}
-
-// The same on the barrier at this place in both CTAs of the cluster.
-__device__ __forceinline__ void mma_commit_both(uint32_t lead, uint32_t bar)
-{
-    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
-                 "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
-                 " [%0], %2;\n\t}" ::"r"(bar),
-                 "r"(lead), "h"((unsigned short)3)
                  : "memory");
 }
 
@@ -346,8 +327,7 @@ __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::aft
 // units of 16 bytes) and the slab distance, so a step adds to it.
 constexpr uint32_t DESC_HI = 1024 >> 4 | 1u << 14 | 2u << 29;
 constexpr uint32_t DESC_V = (SLAB >> 4) << 16;
-// (an address in a cluster carries its CTA's number above the 18 bits of the offset)
-__device__ __forceinline__ uint32_t desc_lo(uint32_t addr) { return addr >> 4 & 0x3fff; }
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr) { return addr >> 4; }
 
 // `lead` is set in one lane; the others run along, so that the warp never
 // diverges around the products and their operands stay in uniform registers.
@@ -456,13 +436,6 @@ __device__ __forceinline__ void clean(const Args &p, const Piece &pc, int k, uin
 // products run ahead of its softmax: Q K^T of part i + 2 of the keys follows P V of
 // part i, whose columns it takes over.  A piece whose tokens do not reach a stream
 // leaves it out: it waits for none of its barriers.
-//
-// CL = 2: a cluster of two CTAs takes two row tiles of one KV head side by side.
-// Each loads half of every K and V tile into both, so that L2 is read, and boxes are
-// issued, once for both: at head_dim 256 a CTA's 128 rows take 128 KB per 2048
-// tensor cycles, which L2 does not deliver to every SM at once (897 -> 771 us for 4
-// prompts), and 16-token pages make 16 boxes of a tile (512 tokens over 131072 keys
-// 867 -> 751 us).  The two share the stages' barriers and nothing else.
 struct Bars {
     uint64_t full[STAGES], empty[STAGES];
     uint64_t q_full, q_empty;
@@ -476,7 +449,7 @@ struct Bars {
     int e0;
 };
 
-template <int D, int CL, bool VI8>
+template <int D, bool VI8>
 __global__ void __launch_bounds__(Cfg<D, VI8>::THREADS, 1)
     attend_kernel(const Args p, const __grid_constant__ CUtensorMap tmQ,
                   const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV)
@@ -491,13 +464,13 @@ __global__ void __launch_bounds__(Cfg<D, VI8>::THREADS, 1)
     static_assert(sizeof(Bars) <= 512, "barriers fit their space");
     const uint32_t sQ = smem_u32(smem), ring = sQ + C::Q_BYTES;
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-    const int w = blockIdx.x / CL, rank = blockIdx.x % CL;   // a cluster's CTAs follow one another
+    const int w = blockIdx.x;
 
     if (warp == 0 && lane == 0) {
         for (int i = 0; i < STG; ++i) {
-            // (an int8 V stage is filled by four warps, for this CTA alone)
+            // (an int8 V stage is filled by four warps)
             mbar_init(smem_u32(&bars.full[i]), C::v_stage(i) ? 4 : 1);
-            mbar_init(smem_u32(&bars.empty[i]), C::v_stage(i) ? NS : CL * NS);
+            mbar_init(smem_u32(&bars.empty[i]), NS);
         }
         mbar_init(smem_u32(&bars.q_full), 1);
         mbar_init(smem_u32(&bars.q_empty), NS);
@@ -553,12 +526,8 @@ __global__ void __launch_bounds__(Cfg<D, VI8>::THREADS, 1)
             bars.e0 = lo;
     }
     if (threadIdx.x == 0)
-        p.split[blockIdx.x] = make_int4(-1, 0, 0, 0);
-    __syncwarp();
-    if constexpr (CL == 2)
-        tc::cluster_sync();         // the other CTA's barriers are there
-    else
-        __syncthreads();
+        p.split[w] = make_int4(-1, 0, 0, 0);
+    __syncthreads();
     fence_after();
     const uint32_t tmem = bars.tmem;
     constexpr uint32_t O_COL = 256;
@@ -568,7 +537,7 @@ __global__ void __launch_bounds__(Cfg<D, VI8>::THREADS, 1)
     pc.e = -1;
     bool ok = working;
     if (working)
-        walk.start(p, bars.e0, t0, t1, rank * NS * p.tpt, NS * p.tpt);
+        walk.start(p, bars.e0, t0, t1);
     auto wait = [&](uint64_t &bar, uint32_t count) {      // the bar's phase number `count`
         if (mbar_wait_warp(smem_u32(&bar), count & 1))
             return true;
@@ -576,14 +545,14 @@ __global__ void __launch_bounds__(Cfg<D, VI8>::THREADS, 1)
             flag(FA_STATUS_WAIT_TIMEOUT);
         return false;
     };
-    auto takes = [&](int s) { return pc.ntok > s * p.tpt; };     // the piece has rows of stream s
+    // the piece has rows of stream s (of the first it always has)
+    auto takes = [&](int s) { return NS == 1 || s == 0 || pc.x.ntok > p.tpt; };
 
     // key tiles that Q K^T runs ahead of P V by
     constexpr int LEAD = 2 / PARTS;
-    // VI8 moves registers from the other warps to the rows'; each role's code lies behind
-    // its own setmaxnreg, by which the compiler allots its registers
-    if (warp < 4) {
-    if constexpr (VI8)
+    // VI8 moves registers from the other warps to the rows'.  (8192-token prompt 511 us; 560 with
+    // the roles of the first four warps in a branch of their own behind their setmaxnreg.)
+    if (VI8 && warp < 4)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::FEW));
     if (warp == 0) {
         // ---------------------------------------------------------- loads
@@ -591,7 +560,6 @@ __global__ void __launch_bounds__(Cfg<D, VI8>::THREADS, 1)
         uint32_t raw = 0;                                           // VI8: raw parts
         const int br = 1 << p.lg_br, groups = BN >> p.lg_br;
         const int g = lane % groups, slab = lane / groups;      // a lane per group of rows and 64 dims
-        const bool copies = slab < 2 && (CL == 1 || g * 2 / groups == rank);
         const uint32_t to = ring + slab * SLAB + g * br * 128;
         // a K or V tile: DS stages of 128 dims
         auto tile = [&](const CUtensorMap *map, int row) {
@@ -610,13 +578,8 @@ __global__ void __launch_bounds__(Cfg<D, VI8>::THREADS, 1)
                 if (lane == 0)
                     mbar_expect_tx(bar, STAGE_BYTES);
                 __syncwarp();
-                if (copies) {
-                    const uint32_t dst = to + stage * STAGE_BYTES;
-                    if constexpr (CL == 2)
-                        tma_load_both(dst, map, ds * 128 + slab * 64, y, bar);
-                    else
-                        tma_load(dst, map, ds * 128 + slab * 64, y, bar);
-                }
+                if (slab < 2)
+                    tma_load(to + stage * STAGE_BYTES, map, ds * 128 + slab * 64, y, bar);
                 ++it;
                 if (!VI8 && ++stage == STG) {
                     stage = 0;
@@ -625,7 +588,7 @@ __global__ void __launch_bounds__(Cfg<D, VI8>::THREADS, 1)
             }
             return true;
         };
-        // VI8: a V tile's raw parts, each CTA its own
+        // VI8: a V tile's raw parts
         auto raw_tile = [&](int row) {
             const int y = row < 0 ? p.oob_row : row;
 #pragma unroll
@@ -692,12 +655,12 @@ __global__ void __launch_bounds__(Cfg<D, VI8>::THREADS, 1)
                 break;
             if (lane == 0) {
                 const uint32_t bar = smem_u32(&bars.q_full);
-                const int box = p.group * p.tpt * 128, streams = takes(0) + (NS == 2 && takes(1));
+                const int box = p.group * p.tpt * 128, streams = NS == 2 && takes(1) ? 2 : 1;
                 mbar_expect_tx(bar, streams * (D / 64) * box);
                 for (int s = 0; s < streams; ++s)
                     for (int c = 0; c < D / 64; ++c)
                         tma_load_3d(sQ + s * BM * D * 2 + c * SLAB, &tmQ, c * 64, pc.kv * p.group,
-                                    pc.tok + s * p.tpt, bar);
+                                    pc.x.tok + s * p.tpt, bar);
             }
             ++qn;
             __syncwarp();
@@ -713,14 +676,12 @@ __global__ void __launch_bounds__(Cfg<D, VI8>::THREADS, 1)
                 row1 = row2;
             }
         }
-        // no copy is left in flight when the CTA ends, nor an arrival of the other CTA's
+        // no copy is left in flight when the CTA ends
         constexpr uint32_t LAST = VI8 ? 2 : STG;    // fills that may still be on their way
         for (uint32_t i = it > LAST ? it - LAST : 0; i < it; ++i) {
             const uint32_t st = !VI8 ? i % STG : DS == 1 ? i % 2 * 2 : i % 2;
             const uint32_t ph = (!VI8 ? i / STG : i / 2) & 1;
             mbar_wait_warp(smem_u32(&bars.full[st]), ph);
-            if (CL == 2)
-                mbar_wait_warp(smem_u32(&bars.empty[st]), ph);
         }
         for (uint32_t i = raw > 2 ? raw - 2 : 0; i < raw; ++i)
             mbar_wait_warp(smem_u32(&bars.raw_full[i % 2]), i / 2 & 1);
@@ -752,10 +713,7 @@ __global__ void __launch_bounds__(Cfg<D, VI8>::THREADS, 1)
         };
         uint32_t done = 0;                              // VI8 with two parts: tiles before the piece
         auto release = [&](uint32_t st) {               // refilled when the products are done
-            if (CL == 2 && !C::v_stage(st))
-                mma_commit_both(lead, smem_u32(&bars.empty[st]));
-            else
-                mma_commit(lead, smem_u32(&bars.empty[st]));
+            mma_commit(lead, smem_u32(&bars.empty[st]));
         };
         // S of buffer b <- Q K^T: dims 128 ds .. of the keys from row 64 * half of stage st
         auto qk = [&](int b, int half, int ds, uint32_t st) {
@@ -799,7 +757,7 @@ __global__ void __launch_bounds__(Cfg<D, VI8>::THREADS, 1)
             const int n = __shfl_sync(0xffffffffu, pc.k1 - pc.k0, 0);
             if (n == 0)
                 continue;
-            mine = __shfl_sync(0xffffffffu, takes(s), 0);
+            mine = NS == 1 || __shfl_sync(0xffffffffu, takes(s), 0);
             ok = wait(bars.q_full, qn);
             ++qn;
             if constexpr (PARTS == 2) {
@@ -896,8 +854,7 @@ __global__ void __launch_bounds__(Cfg<D, VI8>::THREADS, 1)
         // no product is left running when the TMEM goes back
         mma_commit(lead, smem_u32(&bars.end));
         mbar_wait_warp(smem_u32(&bars.end), 0);
-    }
-    } else if (warp < 4 + 4 * NS) {
+    } else if (warp >= 4 && (!VI8 || warp < 4 + 4 * NS)) {
         if constexpr (VI8)
             asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::MANY));
         // ---------------------------------------------------------- softmax
@@ -910,10 +867,10 @@ __global__ void __launch_bounds__(Cfg<D, VI8>::THREADS, 1)
             const int n = pc.k1 - pc.k0, m_parts = n * PARTS;
             if (takes(s)) {
                 const int i_tok = s * p.tpt + r / p.group;
-                const int at = pc.at + i_tok;
+                const int at = pc.x.at + i_tok;
                 // positions of this stream's first and last row
-                const int at_lo = pc.at + s * p.tpt;
-                const int at_hi = pc.at + min((s + 1) * p.tpt, pc.ntok) - 1;
+                const int at_lo = pc.x.at + s * p.tpt;
+                const int at_hi = pc.x.at + min((s + 1) * p.tpt, pc.x.ntok) - 1;
                 float m = -INFINITY, l = 0.f;       // reference (a score before c2), sum of the weights
                 bool far = false;                   // some row of the warp has one beyond FAR
                 for (int i = 0; ok && i < m_parts; ++i) {
@@ -1050,9 +1007,9 @@ __global__ void __launch_bounds__(Cfg<D, VI8>::THREADS, 1)
                     break;
                 fence_after();
                 // ---- the unit's rows, or this piece's partial of them
-                const bool live = r < p.tpt * p.group && i_tok < pc.ntok;
+                const bool live = r < p.tpt * p.group && i_tok < pc.x.ntok;
                 const float inv = l > 0.f ? 1.f / l : 0.f;
-                __half *dst = p.out + ((long long)(pc.tok + i_tok) * p.hq + pc.kv * p.group + r % p.group) * D;
+                __half *dst = p.out + ((long long)(pc.x.tok + i_tok) * p.hq + pc.kv * p.group + r % p.group) * D;
                 float4 *part = reinterpret_cast<float4 *>(p.part) + (size_t)max(pc.slot, 0) * (D / 4) * C::ROWS +
                                s * BM + r;
 #pragma unroll
@@ -1095,7 +1052,7 @@ __global__ void __launch_bounds__(Cfg<D, VI8>::THREADS, 1)
                         mbar_arrive(smem_u32(&bars.o_empty[s]));
                 }
                 if (pc.first_part && s == 0 && r == 0)
-                    p.split[blockIdx.x] = make_int4(pc.e, pc.kv,
+                    p.split[w] = make_int4(pc.e, pc.kv,
                                            static_cast<int>(((t0 + pc.last + 1) * We - 1) / T) - w + 1, 0);
                 used[0] += (m_parts + 1) / 2;
                 used[1] += m_parts / 2;
@@ -1103,7 +1060,7 @@ __global__ void __launch_bounds__(Cfg<D, VI8>::THREADS, 1)
             }
             tiles += n;
         }
-    } else if constexpr (VI8) {
+    } else if (VI8 && warp >= 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::FEW));
         // ---------------------------------------------------------- int8 V
         // A thread per row of a tile: its codes times its scales, rounded to fp16, into
@@ -1185,14 +1142,12 @@ __global__ void __launch_bounds__(Cfg<D, VI8>::THREADS, 1)
         fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
     }
-    if constexpr (CL == 2)
-        tc::cluster_sync();         // neither CTA leaves while the other may still reach it
 }
 
 // ------------------------------------------------------------ the merge
 // CTA (x, w): 256 of the (row, 16 columns) of the unit that CTA w of the main kernel
 // began and left to the next ones: their partials in order, weighed by 2^(c2 (m - M)).
-template <int D, int CL>
+template <int D>
 __global__ void __launch_bounds__(256) merge_kernel(const Args p)
 {
     using C = Cfg<D>;
@@ -1206,10 +1161,10 @@ __global__ void __launch_bounds__(256) merge_kernel(const Args p)
     const int idx = blockIdx.x * 256 + threadIdx.x;
     const int row = idx % C::ROWS, c16 = idx / C::ROWS;
     const int s = row / BM, r = row % BM;
-    const int i_tok = (w % CL * C::NS + s) * p.tpt + r / p.group;
+    const int i_tok = s * p.tpt + r / p.group;
     if (r >= p.tpt * p.group || i_tok >= x.ntok)
         return;
-    auto slot = [&](int i) { return (size_t)(i == 0 ? 2 * w + 1 : 2 * (w + CL * i)); };
+    auto slot = [&](int i) { return (size_t)(i == 0 ? 2 * w + 1 : 2 * (w + i)); };
     float M = -INFINITY;
     for (int i = 0; i < u.z; ++i)
         M = fmaxf(M, p.ml[slot(i) * C::ROWS + row].x);
@@ -1243,23 +1198,21 @@ __global__ void __launch_bounds__(256) merge_kernel(const Args p)
 
 // Sizes of a call and the layout of its workspace.
 struct Space {
-    int cl, tpt, per, max_ents, W;
+    int tpt, per, max_ents, W;
     size_t ents, pos, ebase, split, ml, part, total;    // offsets, and the bytes in all
 };
 
-static Space space_of(int cl, int batch, int n_tokens, int hq, int hkv, int D, long long cap, int sms)
+static Space space_of(int batch, int n_tokens, int hq, int hkv, int D, long long cap, int sms)
 {
     Space s = {};
-    s.cl = cl;
     const int ns = D == 128 ? Cfg<128>::NS : Cfg<256>::NS;
     const int rows = D == 128 ? Cfg<128>::ROWS : Cfg<256>::ROWS;
     const size_t slot = D == 128 ? Cfg<128>::SLOT_BYTES : Cfg<256>::SLOT_BYTES;
     s.tpt = BM / (hq / hkv);
-    s.per = cl * ns * s.tpt;
+    s.per = ns * s.tpt;
     s.max_ents = n_tokens / s.per + (batch < n_tokens ? batch : n_tokens);
     const double most = (double)s.max_ents * hkv * ((cap + BN - 1) / BN + UNIT_COST) / MIN_POS;
-    const int room = sms / cl > 0 ? sms / cl : 1;
-    s.W = most < 1 ? 1 : most < room ? static_cast<int>(most) : room;
+    s.W = most < 1 ? 1 : most < sms ? static_cast<int>(most) : sms;
     size_t at = 0;
     auto take = [&](size_t n) {
         const size_t here = at;
@@ -1269,26 +1222,11 @@ static Space space_of(int cl, int batch, int n_tokens, int hq, int hkv, int D, l
     s.ents = take((size_t)s.max_ents * sizeof(Ent));
     s.pos = take(((size_t)s.max_ents + 1) * sizeof(long long));
     s.ebase = take(((size_t)batch + 1) * sizeof(int));
-    s.split = take((size_t)s.W * cl * sizeof(int4));
-    s.ml = take((size_t)2 * s.W * cl * rows * sizeof(float2));
-    s.part = take((size_t)2 * s.W * cl * slot);
+    s.split = take((size_t)s.W * sizeof(int4));
+    s.ml = take((size_t)2 * s.W * rows * sizeof(float2));
+    s.part = take((size_t)2 * s.W * slot);
     s.total = at;
     return s;
-}
-
-// CTAs per cluster: two where the sequences' rows fill a cluster's on average.
-static int cluster_of(int batch, int n_tokens, int hq, int hkv, int D)
-{
-    const int rows = 2 * (D == 128 ? Cfg<128>::ROWS : Cfg<256>::ROWS);
-    return (long long)n_tokens * (hq / hkv) >= (long long)batch * rows ? 2 : 1;
-}
-
-// Enough for the call's own form and, with smaller sizes, for either.
-static size_t space_need(int batch, int n_tokens, int hq, int hkv, int D, long long cap, int sms)
-{
-    const size_t a = space_of(1, batch, n_tokens, hq, hkv, D, cap, sms).total;
-    const size_t b = space_of(2, batch, n_tokens, hq, hkv, D, cap, sms).total;
-    return a > b ? a : b;
 }
 
 // [rows][D] of fp16 in boxes of `br` rows x 64 columns, 128-byte swizzle; q as
@@ -1310,7 +1248,7 @@ static int encode_map(CUtensorMap *map, const void *base, int rank, const cuuint
     return 0;
 }
 
-template <int D, int CL, bool VI8>
+template <int D, bool VI8>
 static cudaError_t launch(const Args &p, const CUtensorMap &tmQ, const CUtensorMap &tmK,
                           const CUtensorMap &tmV, int per, cudaStream_t st)
 {
@@ -1324,7 +1262,7 @@ static cudaError_t launch(const Args &p, const CUtensorMap &tmQ, const CUtensorM
     {
         std::lock_guard<std::mutex> lock(mu);
         if (dev >= 64 || !done[dev]) {
-            e = cudaFuncSetAttribute(attend_kernel<D, CL, VI8>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+            e = cudaFuncSetAttribute(attend_kernel<D, VI8>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
             if (e != cudaSuccess)
                 return e;
             if (dev < 64)
@@ -1336,27 +1274,22 @@ static cudaError_t launch(const Args &p, const CUtensorMap &tmQ, const CUtensorM
     if (e != cudaSuccess)
         return e;
     cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[2];
+    cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = CL;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
     cfg.stream = st;
     cfg.attrs = attr;
-    cfg.numAttrs = CL == 2 ? 2 : 1;
-    cfg.gridDim = dim3(p.W * CL);
+    cfg.numAttrs = 1;
+    cfg.gridDim = dim3(p.W);
     cfg.blockDim = dim3(C::THREADS);
     cfg.dynamicSmemBytes = C::SMEM;
-    e = cudaLaunchKernelEx(&cfg, attend_kernel<D, CL, VI8>, p, tmQ, tmK, tmV);
+    e = cudaLaunchKernelEx(&cfg, attend_kernel<D, VI8>, p, tmQ, tmK, tmV);
     if (e != cudaSuccess)
         return e;
-    cfg.numAttrs = 1;
-    cfg.gridDim = dim3(C::ROWS * (D / 16) / 256, p.W * CL);
+    cfg.gridDim = dim3(C::ROWS * (D / 16) / 256, p.W);
     cfg.blockDim = dim3(256);
     cfg.dynamicSmemBytes = 0;
-    e = cudaLaunchKernelEx(&cfg, merge_kernel<D, CL>, p);
+    e = cudaLaunchKernelEx(&cfg, merge_kernel<D>, p);
     return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
@@ -1383,7 +1316,7 @@ FA_API size_t fa_prefill_workspace_size(int batch, int n_tokens, int n_q_heads, 
         return 0;
     if (num_sms <= 0 && device_sms(&num_sms) != 0)
         return 0;
-    return space_need(batch, n_tokens, n_q_heads, n_kv_heads, head_dim, max_kv_len, num_sms);
+    return space_of(batch, n_tokens, n_q_heads, n_kv_heads, head_dim, max_kv_len, num_sms).total;
 }
 
 FA_API int fa_prefill(const void *q, const void *k_cache, const void *v_cache,
@@ -1431,8 +1364,7 @@ FA_API int fa_prefill(const void *q, const void *k_cache, const void *v_cache,
     int sms = 0;
     if (const int rc = device_sms(&sms))
         return rc;
-    const int cl = cluster_of(batch, n_tokens, n_q_heads, n_kv_heads, D);
-    const Space sp = space_of(cl, batch, n_tokens, n_q_heads, n_kv_heads, D, cap, sms);
+    const Space sp = space_of(batch, n_tokens, n_q_heads, n_kv_heads, D, cap, sms);
     const size_t need = sp.total;
     if (!workspace || workspace_bytes < need)
         return fail(FA_ERR_WORKSPACE, "fa_prefill: workspace %zu bytes, need %zu", workspace_bytes,
@@ -1467,7 +1399,7 @@ FA_API int fa_prefill(const void *q, const void *k_cache, const void *v_cache,
     p.tpt = sp.tpt;
     p.sink = n_sink;
     // boxes of as many rows as always lie together, the largest power of two in a page; at most
-    // half a tile, which is what a CTA of a cluster loads
+    // half a tile, so that half of a tile that no row sees is not read
     const int br = paged && (page_size & -page_size) < 64 ? (page_size & -page_size) : 64;
     p.lg_br = log2_of(br);
     p.oob_row = static_cast<int>(rows);
@@ -1505,10 +1437,7 @@ FA_API int fa_prefill(const void *q, const void *k_cache, const void *v_cache,
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     auto go = [&](auto int8) {
         constexpr bool I = decltype(int8)::value;
-        return cl == 2 ? (D == 128 ? launch<128, 2, I>(p, tmQ, tmK, tmV, sp.per, st)
-                                   : launch<256, 2, I>(p, tmQ, tmK, tmV, sp.per, st))
-                       : (D == 128 ? launch<128, 1, I>(p, tmQ, tmK, tmV, sp.per, st)
-                                   : launch<256, 1, I>(p, tmQ, tmK, tmV, sp.per, st));
+        return D == 128 ? launch<128, I>(p, tmQ, tmK, tmV, sp.per, st) : launch<256, I>(p, tmQ, tmK, tmV, sp.per, st);
     };
     const cudaError_t e = vi8 ? go(std::true_type()) : go(std::false_type());
     if (e != cudaSuccess)
