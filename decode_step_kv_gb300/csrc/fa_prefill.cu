@@ -24,9 +24,9 @@
 // 128 x 64 x 16 step takes 52-76 cycles where a 128 x 128 x 16 one takes 64, but TMEM
 // has no room for two of 128 keys beside O, and one buffer a stream, whose Q K^T
 // waits for its P V, took 1943 us for a prompt of 16384 tokens (32 / 8 heads) against
-// 1657.  As it stands: 1557-1577 us (1.39-1.41 PFLOP/s of the 1.91 that a library
+// 1657.  As it stands: 1526-1570 us (1.40-1.44 PFLOP/s of the 1.91 that a library
 // product reaches; the power cap holds the clocks at 1.65-1.75 GHz), 512 tokens over
-// 131072 keys 823-843 us, 4 prompts of 1K-8K at D = 256 895-917 us.
+// 131072 keys 827-839 us, 4 prompts of 1K-8K at D = 256 913-930 us.
 //
 // Every CTA fetches its own K and V tiles.  At D = 256 its 128 rows take 128 KB per
 // 2048 tensor cycles, which L2 does not deliver to every SM at once.  A load into two
@@ -69,13 +69,19 @@ constexpr float UP = 10.f, GROW = 5.f;
 // difference from the row's largest before it meets c2 and UP, which would be rounded to its steps.
 constexpr float FAR = 65536.f;
 
+// The most key tiles of a piece.  The tensor cores' 32-bit sums drop what an addition leaves below
+// their last bit: a sum of one sign loses 4e-9 of itself (6e-9 at D = 256) with every key, 5e-3 over
+// 2^20 keys.  So O is begun anew with every piece and added to what came before in fp32: a piece of
+// 16384 keys loses 2^-13 at most.  512 tokens over 131072 keys, up to 7 cuts per CTA, 818 -> 830 us.
+constexpr int SPAN = 128;
+
 // VI8: int8 V.  Its tiles arrive raw and are turned into fp16 stages by a warpgroup of
 // their own, in a ring of four whose odd (at D = 256 last two) stages only V uses, so
 // that every stage has one producer.  Code times scale is rounded to fp16, as fa_decode
 // rounds it: a factor per 32 dims cannot ride on the weight, which one product takes
-// against all dims.  8192-token prompt, 32 / 8 heads x 128: 510 us against
-// 407 with fp16 V; 4 x 4096 tokens, 16 / 8 heads x 256, 925 against 604 (the ring then
-// holds one K tile).  These kernels spill: 152 bytes at D = 128, 156 at D = 256.
+// against all dims.  8192-token prompt, 32 / 8 heads x 128: 505 us against 440 with
+// fp16 V; 4 x 4096 tokens, 16 / 8 heads x 256, 969 against 621 (the ring then holds one
+// K tile).  These kernels spill: 164 bytes at D = 128, 168 at D = 256.
 constexpr int RAW_BYTES = BN * 128;
 template <int D, bool VI8 = false>
 struct Cfg {
@@ -241,6 +247,7 @@ struct Piece {
     int e, kv, k0, k1;              // key tiles [k0, k1) of unit (e, kv)
     int slot;                       // partial slot, -1: the whole unit
     bool first_part;                // a partial from the unit's first tile
+    bool begins, ends;              // the first, the last piece of the unit's tiles in this stretch
     long long last;                 // the unit's last tile, counted from the stretch's first position
     __device__ __forceinline__ int key_tile(int k) const { return k < x.ns ? k : x.kt0 + k - x.ns; }
 };
@@ -248,10 +255,12 @@ struct Piece {
 // The pieces of a stretch of `len` positions, in order.
 struct Pieces {
     int e, kv;
+    int done;                       // tiles of the current unit before the next piece, 0: at its first
     long long us, len;              // us: the current unit's first tile, counted from the stretch's start
     __device__ __forceinline__ void start(const Args &p, int e_, long long t0, long long t1)
     {
         e = e_;
+        done = 0;
         const int unit = p.ents[e].n + UNIT_COST;
         const long long off = t0 - p.pos[e];
         kv = static_cast<int>(off / unit);
@@ -273,6 +282,14 @@ struct Pieces {
             q.slot = whole ? -1 : 2 * static_cast<int>(blockIdx.x) + (q.k0 == 0);
             q.first_part = !whole && q.k0 == 0;
             q.last = us + n - 1;
+            q.begins = done == 0;
+            q.k0 = q.begins ? q.k0 : done;
+            q.ends = q.k1 - q.k0 <= SPAN;
+            if (!q.ends) {
+                done = q.k1 = q.k0 + SPAN;
+                return true;
+            }
+            done = 0;
             us += n + UNIT_COST;
             if (++kv == p.cache.Hkv) {
                 kv = 0;
@@ -863,16 +880,22 @@ __global__ void __launch_bounds__(Cfg<D, VI8>::THREADS, 1)
         const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);
         const uint32_t s_col = lanes + s * 128, o_col = lanes + O_COL + s * 128;
         uint32_t tiles = 0, on = 0, pv_n = 0, used[2] = {0, 0};
+        float m, l;                     // a unit's reference (a score before c2), sum of its weights
+        float kept;                     // the reference of O in the slot
+        bool far;                       // some row of the warp has one beyond FAR
         while (ok && walk.next(p, pc)) {
             const int n = pc.k1 - pc.k0, m_parts = n * PARTS;
+            if (pc.begins) {
+                m = kept = -INFINITY;
+                l = 0.f;
+                far = false;
+            }
             if (takes(s)) {
                 const int i_tok = s * p.tpt + r / p.group;
                 const int at = pc.x.at + i_tok;
                 // positions of this stream's first and last row
                 const int at_lo = pc.x.at + s * p.tpt;
                 const int at_hi = pc.x.at + min((s + 1) * p.tpt, pc.x.ntok) - 1;
-                float m = -INFINITY, l = 0.f;       // reference (a score before c2), sum of the weights
-                bool far = false;                   // some row of the warp has one beyond FAR
                 for (int i = 0; ok && i < m_parts; ++i) {
                     const int b = i & 1, half = PARTS == 2 ? b : 0;
                     ok = wait(bars.s_full[s][b], used[b] + i / 2);
@@ -1010,8 +1033,11 @@ __global__ void __launch_bounds__(Cfg<D, VI8>::THREADS, 1)
                 const bool live = r < p.tpt * p.group && i_tok < pc.x.ntok;
                 const float inv = l > 0.f ? 1.f / l : 0.f;
                 __half *dst = p.out + ((long long)(pc.x.tok + i_tok) * p.hq + pc.kv * p.group + r % p.group) * D;
-                float4 *part = reinterpret_cast<float4 *>(p.part) + (size_t)max(pc.slot, 0) * (D / 4) * C::ROWS +
-                               s * BM + r;
+                // (a whole unit may take the slot of the CTA's last piece, which comes after it)
+                float4 *part = reinterpret_cast<float4 *>(p.part) +
+                               (size_t)(pc.slot >= 0 ? pc.slot : 2 * w + 1) * (D / 4) * C::ROWS + s * BM + r;
+                const float f = kept == -INFINITY ? 0.f : rescale(kept, m, p.c2);
+                kept = m;
 #pragma unroll
                 for (int c = 0; c < D / 32; ++c) {
                     uint32_t o[32];
@@ -1025,7 +1051,17 @@ __global__ void __launch_bounds__(Cfg<D, VI8>::THREADS, 1)
                     }
                     if (!live)
                         continue;
-                    if (pc.slot >= 0) {
+                    if (!pc.begins) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const float4 was = part[(size_t)(c * 8 + e) * C::ROWS];
+                            o[4 * e] = __float_as_uint(fmaf(was.x, f, __uint_as_float(o[4 * e])));
+                            o[4 * e + 1] = __float_as_uint(fmaf(was.y, f, __uint_as_float(o[4 * e + 1])));
+                            o[4 * e + 2] = __float_as_uint(fmaf(was.z, f, __uint_as_float(o[4 * e + 2])));
+                            o[4 * e + 3] = __float_as_uint(fmaf(was.w, f, __uint_as_float(o[4 * e + 3])));
+                        }
+                    }
+                    if (pc.slot >= 0 || !pc.ends) {
 #pragma unroll
                         for (int e = 0; e < 8; ++e)
                             part[(size_t)(c * 8 + e) * C::ROWS] =
