@@ -10,9 +10,11 @@
 //
 // Angles.  A rate is held as a 64-bit fraction of a turn, f = rate / 2 pi *
 // 2^64, so pos * f mod 2^64 is the angle's fraction of a turn at any 32-bit
-// position, off by at most pos * 2^-65 turns: two integer multiplications and
-// no 64-bit floating point, whose rate on this GPU is 1/60 of the 32-bit one.
-// Its top 32 bits go to sincospif.
+// position: two integer multiplications, which add no error, and no 64-bit floating
+// point, whose rate on this GPU is 1/60 of the 32-bit one.  The rates themselves come
+// from 64-bit floats on the host, off by under 2^-55 turns each, so an angle by
+// pos * 2^-55 (2^-35 turns at position 2^20, 2^-24 at 2^31).  Its top 32 bits go to
+// sincospif.
 //
 // What bounds it: HBM, then latency.  A row of D elements is held by D / 16 threads,
 // 16 elements each in two chunks of 8 that hold whole pairs, so that a rotation
@@ -32,7 +34,9 @@ constexpr int THREADS = 256;
 // Rows of a thread in flight together in the append kernel, which is held to 80 registers
 // (three CTAs per SM): 123 us for the 5 prompts above; one row 149, two rows at the 106
 // registers they would take 150.  The rotation alone keeps one row at 64 registers, four
-// CTAs: 55.6 us against 59.4-63.7 with two rows at two and three CTAs.
+// CTAs: 55.6 us against 59.4-63.7 with two rows at two and three CTAs.  Both limits spill: the
+// rotation with norm 14 bytes (bf16) and 24 (fp32), the append with norm from fp32 104, with
+// int8 V 8-116 in all kinds but fp16 with norm at D = 256.
 constexpr int ROWS = 2;
 
 struct Turn {                       // the rotation, the same for every row of a call

@@ -518,7 +518,9 @@ FA_API int fa_evict_kv(void *k_cache, void *v_cache, void *k_scales, void *v_sca
  * q       [batch][n_queries][n_q_heads][head_dim] fp16.
  * out     the same shape, fp16 (fp32 accumulation, one rounding), written in
  *         full, zero rows for empty ranges.
- * n_sink  in [0, 2^30]; 0 leaves the window alone.
+ * n_sink  in [0, 2^30]; 0 leaves the window alone.  The sinks' K rows are read
+ *         as they are: they keep the positions they were rotated to and are
+ *         not numbered anew inside the window.
  * workspace  fa_decode_sinks_workspace_size() bytes, 16-byte aligned.
  * Only pages that hold a sink or a key of some query's window are read; the
  * others may be unmapped.  Caches (fp16 K; fp16 or int8 V; paged or
@@ -605,8 +607,8 @@ FA_API size_t fa_prefill_workspace_size(int batch, int n_tokens, int n_q_heads, 
  *                   positions keep their rate, those that turn less than once
  *                   are divided by factor, a linear ramp in j between them.
  * freqs      HOST array of rot_dim / 2: turns per position as a fraction of
- *            2^64.  Copy it to the device for fa_rope.  Own rates: entry =
- *            radians / (2 pi) * 2^64, modulo 2^64.
+ *            2^64, each within 2^-55 turns.  Copy it to the device for
+ *            fa_rope.  Own rates: entry = radians / (2 pi) * 2^64, modulo 2^64.
  * magnitude  HOST: the factor on cos and sin, 0.1 ln(factor) + 1 for
  *            FA_ROPE_YARN, else 1.
  * base > 1 and factor >= 1, and original_len >= 1 for FA_ROPE_YARN (ignored
