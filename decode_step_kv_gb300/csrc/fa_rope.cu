@@ -12,8 +12,8 @@
 // 2^64, so pos * f mod 2^64 is the angle's fraction of a turn at any 32-bit
 // position: two integer multiplications, which add no error, and no 64-bit floating
 // point, whose rate on this GPU is 1/60 of the 32-bit one.  The rates themselves come
-// from 64-bit floats on the host, off by under 2^-55 turns each, so an angle by
-// pos * 2^-55 (2^-35 turns at position 2^20, 2^-24 at 2^31).  Its top 32 bits go to
+// from 64-bit floats on the host, off by under 2^-54 turns each, so an angle by
+// pos * 2^-54 (2^-34 turns at position 2^20, 2^-23 at 2^31).  Its top 32 bits go to
 // sincospif.
 //
 // What bounds it: HBM, then latency.  A row of D elements is held by D / 16 threads,

@@ -607,7 +607,7 @@ FA_API size_t fa_prefill_workspace_size(int batch, int n_tokens, int n_q_heads, 
  *                   positions keep their rate, those that turn less than once
  *                   are divided by factor, a linear ramp in j between them.
  * freqs      HOST array of rot_dim / 2: turns per position as a fraction of
- *            2^64, each within 2^-55 turns.  Copy it to the device for
+ *            2^64, each within 2^-54 turns.  Copy it to the device for
  *            fa_rope.  Own rates: entry = radians / (2 pi) * 2^64, modulo 2^64.
  * magnitude  HOST: the factor on cos and sin, 0.1 ln(factor) + 1 for
  *            FA_ROPE_YARN, else 1.
