@@ -29,10 +29,11 @@
 // 131072 keys 827-839 us, 4 prompts of 1K-8K at D = 256 913-930 us.
 //
 // Every CTA fetches its own K and V tiles.  At D = 256 its 128 rows take 128 KB per
-// 2048 tensor cycles, which L2 does not deliver to every SM at once.  A load into two
-// CTAs of a cluster halves that (4 prompts at D = 256 710 us, 512 tokens over 131072
-// keys 765), but it must stay off memory that another GPU serves, which a pointer does
-// not tell, and the library is the same for every rank of a run on several GPUs.
+// 2048 tensor cycles and the ring has room for 160 KB on their way: the loads' latency
+// bounds it (tensor pipe 45% busy, L2 and DRAM 34%).  A load into two CTAs of a cluster
+// halves what is fetched (4 prompts at D = 256 710 us, 512 tokens over 131072 keys 765),
+// but it must stay off memory that another GPU serves, which a pointer does not tell,
+// and the library is the same for every rank of a run on several GPUs.
 //
 // Work over the GPU.  A one-CTA kernel lists the units' tiles as positions of one
 // axis (as the decode plan: UNIT_COST positions per unit beside its tiles), every
@@ -72,7 +73,7 @@ constexpr float FAR = 65536.f;
 // The most key tiles of a piece.  The tensor cores' 32-bit sums drop what an addition leaves below
 // their last bit: a sum of one sign loses 4e-9 of itself (6e-9 at D = 256) with every key, 5e-3 over
 // 2^20 keys.  So O is begun anew with every piece and added to what came before in fp32: a piece of
-// 16384 keys loses 2^-13 at most.  512 tokens over 131072 keys, up to 7 cuts per CTA, 818 -> 830 us.
+// 16384 keys loses 2^-13 at most.  512 tokens over 131072 keys, three cuts per CTA, 818 -> 830 us.
 constexpr int SPAN = 128;
 
 // VI8: int8 V.  Its tiles arrive raw and are turned into fp16 stages by a warpgroup of
