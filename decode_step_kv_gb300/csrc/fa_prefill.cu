@@ -31,7 +31,7 @@
 // Every CTA fetches its own K and V tiles.  At D = 256 its 128 rows take 128 KB per
 // 2048 tensor cycles and the ring has room for 160 KB on their way: the loads' latency
 // bounds it (tensor pipe 45% busy, L2 and DRAM 34%).  A load into two CTAs of a cluster
-// halves what is fetched (4 prompts at D = 256 710 us, 512 tokens over 131072 keys 765),
+// halves what is fetched (4 prompts at D = 256 704 us, 512 tokens over 131072 keys 760),
 // but it must stay off memory that another GPU serves, which a pointer does not tell,
 // and the library is the same for every rank of a run on several GPUs.
 //
@@ -80,8 +80,8 @@ constexpr int SPAN = 128;
 // their own, in a ring of four whose odd (at D = 256 last two) stages only V uses, so
 // that every stage has one producer.  Code times scale is rounded to fp16, as fa_decode
 // rounds it: a factor per 32 dims cannot ride on the weight, which one product takes
-// against all dims.  8192-token prompt, 32 / 8 heads x 128: 505 us against 440 with
-// fp16 V; 4 x 4096 tokens, 16 / 8 heads x 256, 969 against 621 (the ring then holds one
+// against all dims.  8192-token prompt, 32 / 8 heads x 128: 500 us against 406 with
+// fp16 V; 4 x 4096 tokens, 16 / 8 heads x 256, 970 against 627 (the ring then holds one
 // K tile).  These kernels spill: 164 bytes at D = 128, 168 at D = 256.
 constexpr int RAW_BYTES = BN * 128;
 template <int D, bool VI8 = false>
